@@ -21,6 +21,7 @@ STATUS = {-1: "MFS_E_ARG", -2: "MFS_E_SLOT", -3: "MFS_E_TOKEN", -4: "MFS_E_RANGE
           -6: "MFS_E_CUDA", -7: "MFS_E_DEVICE", -8: "MFS_E_NOMEM"}
 MFS_DTYPE_F32, MFS_DTYPE_BF16 = 0, 1
 MFS_MAX_SLOTS = 64
+MFS_ROPE = {None: 0, "interleaved": 1, "half": 2}
 
 
 class MfsError(RuntimeError):
@@ -38,6 +39,13 @@ class mfs_config(ctypes.Structure):
         ("weight_dtype", ctypes.c_int), ("kv_dtype", ctypes.c_int), ("max_slots", ctypes.c_int)]
 
 
+class mfs_paged_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("table_width", ctypes.c_int),
+                ("table_stride", ctypes.c_longlong)] + [(n, ctypes.c_int) for n in (
+                    "n_pages", "page_size", "n_kv_heads", "head_dim", "dtype")] + [
+                        (n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "row_stride")]
+
+
 def _load_library():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -45,6 +53,7 @@ def _load_library():
                           "(or python full_duplex_speech_frame_gb300/build.py)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, ci, i32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
+    ll, pkv = ctypes.c_longlong, ctypes.POINTER(mfs_paged_kv)
     sig = {
         "mfs_create": (ci, [ctypes.POINTER(mfs_config), vp, ctypes.POINTER(vp)]),
         "mfs_destroy": (None, [vp]),
@@ -71,6 +80,11 @@ def _load_library():
         "mfs_phase_times": (ci, [vp, vp, ci]),
         "mfs_argmax_rows_noalloc": (ci, [vp, ci, ci, ctypes.c_longlong, vp, vp]),
         "mfs_rvq_encode": (ci, [vp, vp, ci, ci, vp, ci, vp, vp]),
+        "mfs_sample_rows": (ci, [vp, ci, ci, ci, ll, vp, vp, vp, vp, vp, vp, vp]),
+        "mfs_kv_append": (ci, [pkv, ci, ci, vp, vp, vp, ll, ci, vp, ll, vp, ll, vp, ll, vp, ll, ci, ctypes.c_double, vp]),
+        "mfs_paged_attention_workspace": (ctypes.c_size_t, [pkv, ci]),
+        "mfs_paged_attention": (ci, [pkv, ci, vp, vp, ll, ci, vp, ll, ctypes.c_float, ci, vp, ctypes.c_size_t, vp]),
+        "mfs_prompt_attention": (ci, [ci, ci, ci, vp, vp, ll, ci, vp, ll, vp, ll, ci, ci, vp, ll, ctypes.c_float, ci, vp]),
         "mfs_slot_state_bytes": (ctypes.c_size_t, [vp]),
         "mfs_export_slot": (ci, [vp, ci, vp, ctypes.c_size_t]),
         "mfs_import_slot": (ci, [vp, ci, vp, ctypes.c_size_t]),
@@ -361,3 +375,152 @@ def mfs_rvq_encode(z_sem, z_ac, codebooks, codes, stream=None) -> None:
     rc = _lib.mfs_rvq_encode(z_sem.data_ptr(), z_ac.data_ptr(), T, D, codebooks.data_ptr(), codebooks.shape[1],
                              codes.data_ptr(), st)
     _check(None, rc)
+
+
+# ------------------------------------------------- operators on device tensors
+
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise MfsError(-1, message)
+
+
+def _dtype_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return MFS_DTYPE_BF16
+    _need(t.dtype == torch.float32, f"dtype {t.dtype}: need float32 or bfloat16")
+    return MFS_DTYPE_F32
+
+
+def _array(t, what: str, n: int, dtype, device):
+    """Data pointer of a contiguous 1-D CUDA tensor of at least n elements (None: null)."""
+    if t is None:
+        return None
+    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] >= n and t.device == device and (n <= 1 or t.stride(0) == 1),
+          f"{what}: need a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, what: str, n: int, heads: int, head_dim: int, like):
+    """(data pointer, token stride) of a [tokens, heads, head_dim] tensor whose heads are dense."""
+    _need(t.dim() == 3 and t.dtype == like.dtype and t.device == like.device and t.shape[0] == n and t.shape[1] == heads and
+          t.shape[2] == head_dim and t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim),
+          f"{what}: need {like.dtype} [{n}, {heads}, {head_dim}] with dense heads on {like.device}")
+    return t.data_ptr(), t.stride(0) if n > 1 else heads * head_dim
+
+
+def _enqueue(device, stream, name: str, *args) -> None:
+    """Call a library function (its last argument: the stream) with `device` current."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(_lib, name)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(_lib, name)(*args, stream)
+    if rc != MFS_OK:
+        _check(None, rc)
+
+
+def mfs_sample_rows(logits, uniforms, tokens, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> None:
+    """Draw tokens[r] (int32) from row r of the 2-D CUDA tensor logits (fp32 or bf16, unit column
+    stride) with uniforms[r]: temperature, min-p, top-k and top-p from per-row CUDA tensors, or
+    None (see include/mfs.h); enqueued on `stream` (default: torch's current stream)."""
+    import torch
+    _need(logits.is_cuda and logits.dim() == 2 and (logits.shape[1] <= 1 or logits.stride(1) == 1), "logits: need a 2-D CUDA tensor with unit column stride")
+    (rows, cols), dev, f32, i32 = logits.shape, logits.device, torch.float32, torch.int32
+    _enqueue(dev, stream, "mfs_sample_rows", logits.data_ptr(), _dtype_code(logits), rows, cols,
+             logits.stride(0) if rows > 1 else cols, _array(temperature, "temperature", rows, f32, dev),
+             _array(top_k, "top_k", rows, i32, dev), _array(top_p, "top_p", rows, f32, dev),
+             _array(min_p, "min_p", rows, f32, dev), _array(uniforms, "uniforms", rows, f32, dev),
+             _array(tokens, "tokens", rows, i32, dev))
+
+
+class PagedKV:
+    """One layer's paged key/value cache (mfs_paged_kv): k, v [n_pages, n_kv_heads, page_size,
+    head_dim] CUDA tensors of equal strides with dense rows, table [n_seqs, pages] int32.  Keeps the
+    tensors; what they hold may change between calls."""
+
+    def __init__(self, k, v, table):
+        import torch
+        _need(k.is_cuda and k.dim() == 4 and v.shape == k.shape and v.dtype == k.dtype and v.device == k.device,
+              "cache: need k and v [n_pages, n_kv_heads, page_size, head_dim] of one type on one CUDA device")
+        _need(k.stride(3) == 1 and v.stride(3) == 1 and all(k.shape[i] == 1 or k.stride(i) == v.stride(i) for i in range(3)),
+              "cache: need dense rows, and equal strides in k and v")
+        _need(table.dim() == 2 and table.dtype == torch.int32 and table.device == k.device and
+              (table.shape[1] <= 1 or table.stride(1) == 1), "cache: need an int32 table [n_seqs, pages] with unit column stride on the cache's device")
+        self.k, self.v, self.table = k, v, table
+        self.device = k.device
+        stride = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self.c = mfs_paged_kv(k=k.data_ptr(), v=v.data_ptr(), table=table.data_ptr(), table_width=table.shape[1],
+                              table_stride=table.stride(0) if table.shape[0] > 1 else 0, n_pages=k.shape[0], page_size=k.shape[2],
+                              n_kv_heads=k.shape[1], head_dim=k.shape[3], dtype=_dtype_code(k), page_stride=stride[0],
+                              head_stride=stride[1], row_stride=stride[2])
+
+
+def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=None, rope="interleaved", theta=10000.0,
+                  stream=None) -> None:
+    """Write the tokens' keys (rotated) and values k, v [tokens, n_kv_heads, head_dim] into the cache at
+    their positions, and their rotated queries q [tokens, n_q_heads, head_dim] and keys into q_out and
+    k_out.  cu [n_seqs + 1], kv_len [n_seqs]: int32 CUDA tensors; kv_len counts the new tokens.
+    rope: "interleaved", "half" or None (see include/mfs.h)."""
+    import torch
+    c, dev, i32 = cache.c, cache.device, torch.int32
+    n, n_seqs = k.shape[0], kv_len.shape[0]
+    _need(rope in MFS_ROPE, f"rope: one of {list(MFS_ROPE)}")
+    _need((q is None) == (q_out is None), "q and q_out go together")
+    _need(n_seqs <= cache.table.shape[0], "the cache's table has fewer rows than kv_len")
+    kp, ks = _rows(k, "k", n, c.n_kv_heads, c.head_dim, cache.k)
+    vp, vs = _rows(v, "v", n, c.n_kv_heads, c.head_dim, cache.k)
+    op, os_ = (None, 0) if k_out is None else _rows(k_out, "k_out", n, c.n_kv_heads, c.head_dim, cache.k)
+    qp, qs, hq, xp, xs = None, 0, 0, None, 0
+    if q is not None:
+        hq = q.shape[1]
+        qp, qs = _rows(q, "q", n, hq, c.head_dim, cache.k)
+        xp, xs = _rows(q_out, "q_out", n, hq, c.head_dim, cache.k)
+    _enqueue(dev, stream, "mfs_kv_append", c, n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev),
+             _array(kv_len, "kv_len", n_seqs, i32, dev), qp, qs, hq, xp, xs, kp, ks, op, os_, vp, vs, MFS_ROPE[rope], theta)
+
+
+def mfs_paged_attention_workspace(cache: PagedKV, n_q_heads: int):
+    """A workspace tensor for mfs_paged_attention of this cache (see include/mfs.h on sharing it)."""
+    import torch
+    return torch.empty(_lib.mfs_paged_attention_workspace(cache.c, n_q_heads), dtype=torch.uint8, device=cache.device)
+
+
+def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, workspace=None, stream=None) -> None:
+    """Attention of one new token per sequence, q and out [n_seqs, n_q_heads, head_dim], over the cache's
+    first kv_len[s] positions (the last `window` of them if it is not 0).  scale: default
+    head_dim ** -0.5.  workspace: default one of its own for this call."""
+    import torch
+    c, dev = cache.c, cache.device
+    n, hq = q.shape[0], q.shape[1]
+    _need(n <= cache.table.shape[0], "the cache's table has fewer rows than q")
+    qp, qs = _rows(q, "q", n, hq, c.head_dim, cache.k)
+    op, os_ = _rows(out, "out", n, hq, c.head_dim, cache.k)
+    if workspace is None:
+        if stream is None:
+            workspace = mfs_paged_attention_workspace(cache, hq)
+        else:  # from the pool of the stream that uses it, so that it is not handed out again too early
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+                workspace = mfs_paged_attention_workspace(cache, hq)
+    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: need a contiguous tensor on the cache's device")
+    _enqueue(dev, stream, "mfs_paged_attention", c, n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_,
+             c.head_dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+
+
+def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) -> None:
+    """Causal attention of packed prompts: q, out [tokens, n_q_heads, head_dim], k, v [tokens, n_kv_heads,
+    head_dim] CUDA tensors (fp32 or bf16), sequence s = tokens cu[s] .. cu[s + 1] - 1; the last `window`
+    keys of each row if it is not 0.  scale: default head_dim ** -0.5 (see include/mfs.h)."""
+    import torch
+    _need(q.is_cuda and q.dim() == 3 and k.dim() == 3, "need CUDA tensors [tokens, heads, head_dim]")
+    (n, hq, hd), hkv, n_seqs, dev = q.shape, k.shape[1], cu.shape[0] - 1, q.device
+    qp, qs = _rows(q, "q", n, hq, hd, q)
+    kp, ks = _rows(k, "k", n, hkv, hd, q)
+    vp, vs = _rows(v, "v", n, hkv, hd, q)
+    op, os_ = _rows(out, "out", n, hq, hd, q)
+    _enqueue(dev, stream, "mfs_prompt_attention", _dtype_code(q), n, n_seqs, _array(cu, "cu", n_seqs + 1, torch.int32, dev), qp, qs, hq,
+             kp, ks, vp, vs, hkv, hd, op, os_, hd ** -0.5 if scale is None else scale, window)

@@ -343,6 +343,143 @@ int mfs_rvq_encode(const float* z_sem, const float* z_ac, int T, int D, const fl
 int mfs_argmax_rows_noalloc(const float* logits, int rows, int cols, long long ld, int32_t* out,
                             void* cuda_stream);
 
+/* ---------------------------------------------------------------- sampling rows
+ * Draws one token from each row of logits, from uniforms that the caller gives:
+ * the sampling heads of mfs_step_sampled as a stand-alone call on device memory
+ * (SGLang-Omni cookbook, PersonaPlex, "Stage sampling"), with min-p and top-p
+ * beside temperature and top-k, and settings of its own for every row.
+ *
+ *   logits  device, row r at logits + r * ld (elements); dtype MFS_DTYPE_F32 or
+ *           MFS_DTYPE_BF16; any alignment of an element; read only
+ *   rows    >= 0 (0 returns MFS_OK); cols 1 .. MFS_SAMPLE_MAX_COLS; ld >= cols
+ *   temperature, top_k, top_p, min_p
+ *           device, [rows] each, or NULL: no temperature array means 1 for every
+ *           row, no other array means that filter is off for every row
+ *   uniforms device [rows], in [0, 1)
+ *   tokens   device [rows], out
+ * Row r, with T = temperature[r] and l_i its logits, m their maximum:
+ *   - T <= 0 or NaN: the lowest column of the maximum (mfs_argmax_rows_noalloc's
+ *     rule: NaN never wins, a row of only NaN gives 0).  The same where the
+ *     maximum is -inf.
+ *   - weights w_i = exp((l_i - m) / T) (1 where l_i = m); a NaN logit is never a
+ *     candidate.  Order the columns by logit, largest first, equal logits by
+ *     column.  The candidates are the longest prefix of that order with
+ *     w_i >= min_p[r] (min_p <= 0: every column; above 1 it counts as 1), cut to
+ *     top_k[r] columns (<= 0: not cut), then cut to the shortest prefix whose
+ *     weights sum to at least top_p[r] times the sum of the whole (>= 1: not
+ *     cut; never less than one column).
+ *   - The token is the first candidate, in ascending column order, at which the
+ *     running sum of weights exceeds uniforms[r] times their sum (a uniform below
+ *     0 or NaN acts as 0, one of 1 or more takes the last candidate).
+ * Weights and sums are exact enough that the token is the one that the
+ * definition gives in real numbers, unless a sum lies within 1e-11 of a border
+ * relative to the total.  The same inputs always give the same tokens.
+ * Enqueues on `stream` and returns; no memory is allocated, so it can be captured.
+ * MFS_E_ARG on bad sizes or NULL pointers, before anything is enqueued. */
+#define MFS_SAMPLE_MAX_COLS (1 << 22)
+int mfs_sample_rows(const void* logits, int dtype, int rows, int cols, long long ld, const float* temperature,
+                    const int32_t* top_k, const float* top_p, const float* min_p, const float* uniforms,
+                    int32_t* tokens, void* cuda_stream);
+
+/* ---------------------------------------------------------------- paged cache
+ * Keys and values of many sequences in pages of a shared pool, for callers whose
+ * sessions should hold only the memory of the frames they have seen, instead of
+ * a whole ring each (SGLang-Omni cookbook, PersonaPlex, "Known limitations": the
+ * windowed pool of keys and values).  One descriptor is one layer's cache.
+ *
+ *   k, v     device, dtype MFS_DTYPE_F32 or MFS_DTYPE_BF16; element e of head h
+ *            at row r of page g lies at g * page_stride + h * head_stride +
+ *            r * row_stride + e (strides in elements, of k and v alike, >= 0;
+ *            k, v and every stride a multiple of 16 bytes)
+ *   table    device int32: the page that holds positions j * page_size ..
+ *            (j + 1) * page_size - 1 of sequence s is table[s * table_stride + j],
+ *            j < table_width.
+ *            Entries that a call does not need are not read as pages (they may
+ *            hold anything); sequences may share pages they only read.
+ *   head_dim 64 or 128; page_size 1 .. MFS_MAX_PAGE_SIZE
+ * A needed entry outside [0, n_pages), or a position at or past
+ * table_width * page_size, never touches memory outside the pool: the append
+ * skips that token's row, the attention gives NaN for that sequence. */
+#define MFS_MAX_PAGE_SIZE 65536
+typedef struct {
+    void* k;
+    void* v;
+    const int32_t* table;
+    int table_width;          /* entries of a sequence, >= 1 */
+    long long table_stride;   /* entries from one sequence to the next, >= 0 */
+    int n_pages, page_size, n_kv_heads, head_dim, dtype;
+    long long page_stride, head_stride, row_stride;
+} mfs_paged_kv;
+
+#define MFS_ROPE_NONE 0
+#define MFS_ROPE_INTERLEAVED 1 /* pairs (2 i, 2 i + 1): the frame step's layout */
+#define MFS_ROPE_HALF 2        /* pairs (i, i + head_dim / 2) */
+
+/* Append new tokens' keys and values to the paged cache, rotated by their
+ * positions on the way, and rotate their queries (mobius PR #368, "P2 - Moshi
+ * LM": RoPE at the absolute position, offset by the cached length).
+ *   cu       device [n_seqs + 1]: tokens cu[s] .. cu[s + 1] - 1 belong to sequence
+ *            s (ascending, cu[0] = 0; a sequence may have none; tokens from
+ *            cu[n_seqs] on belong to none and their rows are left as they are)
+ *   kv_len   device [n_seqs]: the sequence's length with the new tokens, so the
+ *            i-th of its c new tokens has position kv_len[s] - c + i (a negative
+ *            position, like a bad page, is rotated but not written to the cache)
+ *   q        [n_tokens][n_q_heads][head_dim] or NULL, out to q_out (may be q)
+ *   k, v     [n_tokens][n_kv_heads][head_dim]; k_out: NULL, or the rotated keys
+ *            (may be k), for mfs_prompt_attention
+ *            *_stride: elements from one token to the next (heads are dense);
+ *            pointers and strides multiples of 16 bytes; the cache's dtype
+ *   theta    RoPE base, > 0: pair i turns by position * theta^(-2 i / head_dim);
+ *            the angle is reduced in 64 bits, the rotation runs in 32 bits and is
+ *            rounded once; ignored with MFS_ROPE_NONE
+ * Outputs overlap inputs only where one is the other's array (same pointer and
+ * stride).  Two tokens that reach the same row of the same page leave either's.
+ * Enqueues and returns; MFS_E_ARG on bad sizes, strides, alignment or NULL. */
+int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len,
+                  const void* q, long long q_stride, int n_q_heads, void* q_out, long long q_out_stride,
+                  const void* k, long long k_stride, void* k_out, long long k_out_stride, const void* v,
+                  long long v_stride, int rope, double theta, void* cuda_stream);
+
+/* Attention of one new token per sequence over the paged cache:
+ *   out[s][h] = sum_j softmax_j(scale * q[s][h] . k_j) v_j,  j in [max(0, L - window), L)
+ * with L = kv_len[s] (the new token is already appended), the keys and values of
+ * kv head h / (n_q_heads / n_kv_heads).  window = 0: every position.  The work is
+ * split over the cache's length into equal shares and joined in a fixed order, so
+ * the same inputs give the same bits.  L <= 0 gives zeros.
+ *   q, out   [n_seqs][n_q_heads][head_dim], the cache's dtype, strides as above
+ *            (out may be q); n_q_heads a multiple of n_kv_heads
+ *   scale    > 0, finite
+ *   workspace device memory of mfs_paged_attention_workspace() bytes, 16-byte
+ *            aligned, its contents need not be kept or set between calls.  Calls whose work
+ *            can overlap on the GPU (other streams, two captured graphs) need one each.
+ * Rows of the cache at or past L, or before the window, are not read.  Sums and
+ * softmax statistics are fp32; with a bf16 cache the softmax weights are rounded
+ * to bf16 for the product with the values.  Enqueues and returns; MFS_E_ARG on
+ * bad sizes, strides, alignment or NULL. */
+size_t mfs_paged_attention_workspace(const mfs_paged_kv* cache, int n_q_heads);
+int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, const void* q,
+                        long long q_stride, int n_q_heads, void* out, long long out_stride, float scale, int window,
+                        void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* Causal attention over whole prompts, packed one behind the other:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,  j in [max(b, t - window + 1), t]
+ * with b the first token of t's sequence (mobius PR #368, "P2 - Moshi LM":
+ * sliding-window causal attention); window = 0: from b on.
+ *   cu       device [n_seqs + 1] as for mfs_kv_append; rows from cu[n_seqs] on
+ *            are left as they are
+ *   q, out   [n_tokens][n_q_heads][head_dim]; k, v [n_tokens][n_kv_heads][head_dim];
+ *            dtype MFS_DTYPE_F32 or MFS_DTYPE_BF16; head_dim 64 or 128; n_q_heads a
+ *            multiple of n_kv_heads; strides as above; out overlaps no input
+ * bf16 runs on the tensor cores (fp32 scores, statistics and sums; the softmax
+ * weights are rounded to bf16 for the product with the values); fp32 runs on the
+ * CUDA cores in fp32.  A key or value outside a row's range (another sequence's,
+ * a later token's) has no influence on it, NaN and infinities included.
+ * Enqueues and returns; MFS_E_ARG on bad sizes, strides, alignment or NULL. */
+int mfs_prompt_attention(int dtype, int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride,
+                         int n_q_heads, const void* k, long long k_stride, const void* v, long long v_stride,
+                         int n_kv_heads, int head_dim, void* out, long long out_stride, float scale, int window,
+                         void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

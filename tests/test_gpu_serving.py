@@ -1,0 +1,570 @@
+"""The serving operators on the GPU (mfs_sample_rows, mfs_kv_append, mfs_paged_attention, mfs_prompt_attention)
+against their 64-bit definitions."""
+import numpy as np
+import pytest
+
+from tests import _serving as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mfs():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from full_duplex_speech_frame_gb300 import mfs as m
+    return m
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _dt(name):
+    return {"bf16": _torch().bfloat16, "f32": _torch().float32}[name]
+
+
+def _normal(rng, *shape, dtype="f32", scale=1.0):
+    return _torch().from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(_dt(dtype)).cuda()
+
+
+def _i32(x):
+    return _torch().tensor(x, dtype=_torch().int32, device="cuda")
+
+
+def _f32(x):
+    return _torch().tensor(x, dtype=_torch().float32, device="cuda")
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------ sampling
+
+SETTINGS = [(0.7, 25, 1.0, 0.0), (0.8, 250, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.3, 0, 1.0, 0.05), (0.9, 40, 0.8, 0.02), (1.0, 0, 1.0, 0.0),
+            (0.0, 0, 1.0, 0.0), (0.5, 1, 0.5, 0.5), (0.05, 100, 0.999, 0.0), (30.0, 0, 0.37, 0.0)]
+
+
+def _sample(mfs, logits, u, t, k, p, m, **kw):
+    out = _torch().full((logits.shape[0],), -7, dtype=_torch().int32, device="cuda")
+    mfs.mfs_sample_rows(logits, _f32(u), out, temperature=_f32(t), top_k=_i32(k), top_p=_f32(p), min_p=_f32(m), **kw)
+    return out.cpu().numpy()
+
+
+@pytest.mark.parametrize("cols", [1, 2, 31, 129, 2048, 4099, 32000, 50001, 131071])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_rows_matches_the_definition(mfs, cols, dtype):
+    """Every setting on normal logits of three widths; rows are strided and start at odd addresses."""
+    rng = np.random.default_rng(cols)
+    rows = 3 * len(SETTINGS)
+    wide = _normal(rng, rows, cols + 5, dtype=dtype)
+    wide *= _torch().linspace(0.3, 6.0, rows, device="cuda")[:, None].to(wide.dtype)
+    x = wide[:, 3:3 + cols]
+    u = rng.random(rows).astype(np.float32)
+    t, k, p, m = (np.array([s[i] for s in SETTINGS] * 3) for i in range(4))
+    got = _sample(mfs, x, u, t, k, p, m)
+    xs = _np(x)
+    want = [S.sample_row(xs[r], u[r], np.float32(t[r]), k[r], np.float32(p[r]), np.float32(m[r])) for r in range(rows)]
+    assert got.tolist() == want
+
+
+@pytest.mark.parametrize("n", [3, 1000, 40000])
+def test_sample_rows_at_the_borders_of_equal_weights(mfs, n):
+    """Equal logits: column floor(u n), for uniforms next to the borders j / n (the nearest fp32 on either side)."""
+    j = np.unique(np.linspace(0, n - 1, 64).astype(np.int64))
+    u = (j / n).astype(np.float32)
+    u = np.concatenate([u, np.nextafter(u, np.float32(0)), np.nextafter(u, np.float32(1))])
+    u = u[(u >= 0) & (u < 1)]
+    x = _f32(np.full((len(u), n), 0.37))
+    one, zero = np.ones(len(u)), np.zeros(len(u))
+    # u is a fraction of powers of two: floor(u n) in whole numbers
+    want = [int(int(float(v) * 2 ** 60) * n >> 60) for v in u]
+    assert _sample(mfs, x, u, one, zero, one, zero).tolist() == want
+    # the first half by top-k, and by top-p (the shortest prefix with sum >= half)
+    h = (n + 1) // 2
+    want = [int(int(float(v) * 2 ** 60) * h >> 60) for v in u]
+    assert _sample(mfs, x, u, one, zero + h, one, zero).tolist() == want
+    assert _sample(mfs, x, u, one, zero, one * 0.5, zero).tolist() == want
+
+
+def test_sample_rows_decides_close_borders(mfs):
+    """Uniforms within a few fp32 steps of a border between unequal weights: fp32 sums would leave them open."""
+    rng = np.random.default_rng(3)
+    n, rows = 700, 256
+    x = rng.standard_normal(n).astype(np.float32)
+    w = np.exp(x.astype(np.float64) - x.max())
+    c = np.cumsum(w) / w.sum()
+    j = rng.integers(0, n - 1, rows)
+    u = c[j].astype(np.float32)
+    for _ in range(2):
+        u = np.where(rng.random(rows) < 0.5, np.nextafter(u, np.float32(1)), np.nextafter(u, np.float32(0)))
+    gap = np.abs(c[None] - u.astype(np.float64)[:, None]).min(1)
+    assert gap.min() > 1e-11  # the definition itself decides
+    logits = _f32(np.tile(x, (rows, 1)))
+    one, zero = np.ones(rows), np.zeros(rows)
+    want = np.searchsorted(c, u.astype(np.float64), side="right")
+    assert _sample(mfs, logits, u, one, zero, one, zero).tolist() == want.tolist()
+    # the same borders as top-p: the cut has to fall on the right column
+    order = np.argsort(-x, kind="stable")
+    cs = np.cumsum(w[order]) / w.sum()
+    p = cs[j].astype(np.float32)
+    last = np.full(rows, np.nextafter(np.float32(1), np.float32(0)))
+    got = _sample(mfs, logits, last, one, zero, p, zero)
+    want = [S.sample_row(x, last[r], 1.0, 0, p[r], 0.0) for r in range(rows)]
+    assert got.tolist() == want
+
+
+def test_sample_rows_special_rows(mfs):
+    inf, nan = np.inf, np.nan
+    cases = [  # logits, u, T, k, p, m
+        ([nan, nan, nan], 0.5, 1, 0, 1, 0), ([nan, -inf, -inf], 0.9, 1, 0, 1, 0), ([-inf, 0, -inf], 0.99, 1, 0, 1, 0),
+        ([0, inf, 1, inf], 0.7, 1, 0, 1, 0), ([0, inf, 1, inf], 0.2, 1, 2, 0.4, 0), ([nan, 2, nan, 2], 0.6, 1, 0, 1, 0),
+        ([1, 2, 3], 0.5, nan, 0, 1, 0), ([1, 2, 3], 0.5, -1, 0, 1, 0), ([3, 2, 3], 0.5, 0, 0, 1, 0), ([1, 2, 3], 0.999, inf, 0, 1, 0),
+        ([1, 2, 3], 0.99, 1e-30, 0, 1, 0), ([1, 2, 3], 0.0, 1, 50, 1, 0), ([1, 2, 3], 0.0, 1, 0, 0, 0), ([1, 2, 3], 0.0, 1, 0, -1, 0),
+        ([1, 2, 3], 0.0, 1, 0, 1, 1), ([1, 3, 3], 0.9, 1, 0, 1, 7), ([1, 2, 3], 1.0, 1, 0, 1, 0), ([1, 2, 3], -0.5, 1, 0, 1, 0),
+        ([1, 2, 3], nan, 1, 0, 1, 0), ([-0.0, 0.0, -0.0], 0.4, 1, 2, 1, 0), ([0, -200, -200], 0.9999999, 1, 0, 1, 0),
+        ([3e38, -3e38, 1], 0.5, 1, 0, 1, 0), ([1, 2, 3], 0.2, 1, 0, nan, nan), ([1e-40, 2e-40, 0], 0.9, 1, 1, 1, 0)]
+    for row, u, t, k, p, m in cases:
+        got = _sample(mfs, _f32([row]), [u], [t], [k], [p], [m])[0]
+        # NaN settings switch their filter off
+        want = S.sample_row(np.array(row, np.float32), 0.0 if u != u else u, t, k, 1.0 if p != p else p, 0.0 if m != m else m)
+        assert got == want, (row, u, t, k, p, m, got, want)
+
+
+def test_sample_rows_defaults_streams_and_capture(mfs):
+    torch = _torch()
+    rng = np.random.default_rng(5)
+    x, u = _normal(rng, 40, 3001), _f32(rng.random(40))
+    out = torch.full((40,), -7, dtype=torch.int32, device="cuda")
+    mfs.mfs_sample_rows(x[:0], u, out)
+    assert (out == -7).all()
+    mfs.mfs_sample_rows(x, u, out)
+    want = [S.sample_row(_np(x)[r], float(u[r])) for r in range(40)]
+    assert out.tolist() == want
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out2 = torch.full((40,), -7, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    mfs.mfs_sample_rows(x, u, out2, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(out, out2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mfs.mfs_sample_rows(x, u, out2)
+    x.copy_(_normal(rng, 40, 3001))
+    g.replay()
+    torch.cuda.synchronize()
+    assert out2.tolist() == [S.sample_row(_np(x)[r], float(u[r])) for r in range(40)]
+
+
+# --------------------------------------------------------------- paged cache
+
+def _pool(rng, pages, heads, page, hd, dtype, layout="head"):
+    """k and v pools: page-major with heads outside ("head") or rows outside ("row"), or one allocation for both ("both")."""
+    if layout == "row":
+        return tuple(_normal(rng, pages, page, heads, hd, dtype=dtype).transpose(1, 2) for _ in range(2))
+    if layout == "both":
+        kv = _normal(rng, pages, 2, heads, page, hd, dtype=dtype)
+        return kv[:, 0], kv[:, 1]
+    return tuple(_normal(rng, pages, heads, page, hd, dtype=dtype) for _ in range(2))
+
+
+def _table(rng, lens, page, spare=2, extra=3):
+    """Shuffled distinct pages; entries past a sequence's length hold rubbish."""
+    need = [-(-max(0, n) // page) for n in lens]
+    order = rng.permutation(sum(need) + spare)
+    t = rng.integers(-2**31, 2**31 - 1, (len(lens), max(need + [0]) + extra)).astype(np.int32)
+    at = 0
+    for s, c in enumerate(need):
+        t[s, :c] = order[at:at + c]
+        at += c
+    return t, sum(need) + spare
+
+
+@pytest.mark.parametrize("hq,hkv,hd,page,dtype,rope,layout", [
+    (4, 4, 64, 16, "f32", "interleaved", "head"), (8, 2, 128, 16, "bf16", "half", "head"), (6, 2, 64, 1, "bf16", "interleaved", "row"),
+    (32, 32, 128, 48, "bf16", "interleaved", "both"), (3, 1, 128, 7, "f32", "half", "row"), (5, 5, 64, 64, "bf16", None, "head")])
+def test_kv_append(mfs, hq, hkv, hd, page, dtype, rope, layout):
+    torch = _torch()
+    rng = np.random.default_rng(hq * 100 + hd + page)
+    new = [3, 0, 1, 17, 40, 1]
+    past = [0, 5, 2999, 16, 7, 1 << 20]
+    total = [a + b for a, b in zip(past, new)]
+    lens = [n if n < 10000 else 40 for n in total]
+    table, pages = _table(rng, lens, page)
+    if page < 1000:  # the far sequence reaches one page only: a table row as wide as its position would be large
+        wide = np.full((len(new), total[-1] // page + 1), -9, np.int32)
+        wide[:, :min(table.shape[1], wide.shape[1])] = table[:, :wide.shape[1]]
+        wide[-1] = -1
+        wide[-1, (total[-1] - 1) // page] = table[-1, 0]
+        table = wide
+    n, tail = sum(new), 4
+    qkv = _normal(rng, n + tail, hq + 2 * hkv, hd, dtype=dtype)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    kc, vc = _pool(rng, pages, hkv, page, hd, dtype, layout)
+    k0, v0 = _np(kc), _np(vc)
+    cache = mfs.PagedKV(kc, vc, torch.from_numpy(table).cuda())
+    q_out = torch.full((n + tail, hq, hd), 7.0, dtype=_dt(dtype), device="cuda")
+    k_out = torch.full((n + tail, hkv, hd), 7.0, dtype=_dt(dtype), device="cuda")
+    mfs.mfs_kv_append(cache, k, v, _i32(np.cumsum([0] + new).tolist()), _i32(total), q=q, q_out=q_out, k_out=k_out, rope=rope, theta=10000.0)
+    qn, kn, vn = _np(q), _np(k), _np(v)
+    t = 0
+    # fp32: the angle in 64 bits is reduced to +-pi and rounded once (2^-24 pi), cosine and sine within 2^-22, two products and a
+    # sum (3 x 2^-24), each relative to |x_a| + |x_b| <= 2 max|x|: 2 * (3.2 + 4 + 3) 2^-24 max|x|; bf16: besides one rounding, 2^-8
+    bound = 2.0 ** -24 * 21 * np.abs(_np(qkv)).max()
+    rel = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    if rope is None:
+        bound = rel = 0.0
+    for s, c in enumerate(new):
+        for p in range(past[s], total[s]):
+            for got, src in ((_np(q_out[t]), qn[t]), (_np(k_out[t]), kn[t])):
+                want = S.rotate(src, p, rope, 10000.0)
+                assert (np.abs(got - want) <= bound + rel * np.abs(want)).all()
+            pg = table[s, p // page]
+            assert np.array_equal(_np(kc[pg, :, p % page]), _np(k_out[t])) and np.array_equal(_np(vc[pg, :, p % page]), vn[t])
+            k0[pg, :, p % page], v0[pg, :, p % page] = _np(k_out[t]), vn[t]
+            t += 1
+    assert np.array_equal(k0, _np(kc)) and np.array_equal(v0, _np(vc))  # no other row changed
+    assert (q_out[n:] == 7).all() and (k_out[n:] == 7).all()          # rows of no sequence
+
+
+def test_kv_append_in_place_and_bad_pages(mfs):
+    """q and k rotated in place; tokens whose page is outside the pool, whose position is outside the table or
+    negative are rotated and not written."""
+    torch = _torch()
+    rng = np.random.default_rng(9)
+    hq, hkv, hd, page = 4, 2, 64, 4
+    kc, vc = _pool(rng, 3, hkv, page, hd, "f32")
+    k0, v0 = kc.clone(), vc.clone()
+    table = _i32([[0, 3], [-1, 1], [2, 2], [0, 1]])  # no two tokens reach the same row
+    new, total = [2, 6, 3, 2], [2, 8, 10, 1]  # 3: no such page; -1; positions 8, 9 past the table; position -1
+    table[0, 0] = 3
+    n = sum(new)
+    q, k, v = (_normal(rng, n, h, hd) for h in (hq, hkv, hkv))
+    qn, kn = _np(q), _np(k)
+    mfs.mfs_kv_append(mfs.PagedKV(kc, vc, table), k, v, _i32(np.cumsum([0] + new).tolist()), _i32(total), q=q, q_out=q, k_out=k, theta=500.0)
+    t, changed = 0, set()
+    for s, c in enumerate(new):
+        for p in range(total[s] - c, total[s]):
+            assert np.abs(_np(q[t]) - S.rotate(qn[t], p, "interleaved", 500.0)).max() < 1e-5
+            assert np.abs(_np(k[t]) - S.rotate(kn[t], p, "interleaved", 500.0)).max() < 1e-5
+            pg = int(table[s, p // page]) if 0 <= p < 8 else -1
+            if 0 <= pg < 3:
+                assert torch.equal(kc[pg, :, p % page], k[t]) and torch.equal(vc[pg, :, p % page], v[t])
+                changed.add((pg, p % page))
+            t += 1
+    for pg in range(3):
+        for r in range(page):
+            if (pg, r) not in changed:
+                assert torch.equal(kc[pg, :, r], k0[pg, :, r]) and torch.equal(vc[pg, :, r], v0[pg, :, r])
+    assert len(changed) == 4 + 1 + 1
+
+
+def _check_decode(mfs, rng, lens, hq, hkv, hd, page, dtype, layout="head", window=0, scale=None, qscale=1.0, check=None):
+    torch = _torch()
+    table, pages = _table(rng, lens, page)
+    kc, vc = _pool(rng, pages, hkv, page, hd, dtype, layout)
+    k, v = _np(kc), _np(vc)
+    # every row that must not be read becomes NaN
+    used = np.zeros((pages, page), bool)
+    for s, n in enumerate(lens):
+        for p in range(max(0, n - window) if window else 0, n):
+            used[table[s, p // page], p % page] = True
+    stale = torch.from_numpy(~used).cuda()
+    for c in (kc, vc):
+        c.masked_fill_(stale[:, None, :, None], float("nan"))
+    n = len(lens)
+    wide = _normal(rng, n, hq + 2, hd, dtype=dtype, scale=qscale)
+    q = wide[:, :hq]
+    out = torch.full((n + 2, hq, hd), 7.0, dtype=_dt(dtype), device="cuda")
+    cache = mfs.PagedKV(kc, vc, torch.from_numpy(table).cuda())
+    kw = {} if scale is None else dict(scale=scale)
+    mfs.mfs_paged_attention(cache, q, _i32(lens), out[:n], window=window, **kw)
+    got, qn = _np(out), _np(q)
+    assert (got[n:] == 7).all()
+    sc, g = hd ** -0.5 if scale is None else scale, hq // hkv
+    for s in (range(n) if check is None else check):
+        lo = max(0, lens[s] - window) if window else 0
+        rows_k, rows_v = S.kv_rows(k, table[s], page, lo, lens[s]), S.kv_rows(v, table[s], page, lo, lens[s])
+        for h in range(hq):
+            ref, weighted, size = S.attend(qn[s, h], rows_k[:, h // g], rows_v[:, h // g], sc)
+            tol = S.attention_tolerance(ref, weighted, size, max(1, lens[s] - lo), hd, dtype == "bf16")
+            assert (np.abs(got[s, h] - ref) <= tol).all(), (s, h, lens[s], np.abs(got[s, h] - ref).max(), tol.min())
+    return cache, q, out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,hd,page,layout", [(4, 4, 64, 16, "head"), (8, 2, 128, 16, "row"), (6, 2, 64, 1, "both"), (3, 1, 128, 7, "head"),
+                                                   (40, 2, 64, 48, "row"), (32, 32, 128, 64, "head"), (34, 1, 128, 33, "both")])
+def test_paged_attention(mfs, hq, hkv, hd, page, layout, dtype):
+    """Lengths 0, 1, around pages and tiles, and some hundred; rows behind each length are NaN."""
+    rng = np.random.default_rng(hq + hd + page)
+    _check_decode(mfs, rng, [0, 1, page, page + 1, 63, 64, 65, 127, 129, 300, -3, 515], hq, hkv, hd, page, dtype, layout)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("window", [1, 2, 64, 100, 4000])
+def test_paged_attention_window(mfs, window, dtype):
+    rng = np.random.default_rng(window)
+    _check_decode(mfs, rng, [0, 1, 63, 64, 100, 101, 165, 700], 8, 2, 64, 16, dtype, window=window)
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,hd", [("bf16", 8, 2, 128), ("f32", 2, 2, 64), ("bf16", 1, 1, 64)])
+def test_paged_attention_long(mfs, dtype, hq, hkv, hd):
+    """One long sequence among short ones: the split over the length, and its join."""
+    rng = np.random.default_rng(17)
+    _check_decode(mfs, rng, [5, 20011, 0, 64], hq, hkv, hd, 32, dtype)
+
+
+def test_paged_attention_many_sequences(mfs):
+    rng = np.random.default_rng(18)
+    lens = (rng.integers(0, 40, 1500)).tolist()
+    _check_decode(mfs, rng, lens, 4, 2, 64, 8, "bf16", check=range(0, 1500, 37))
+
+
+def test_paged_attention_large_scores(mfs):
+    """Scores of some hundreds: one key takes almost all the weight, and the running maximum moves a lot."""
+    rng = np.random.default_rng(19)
+    for dtype in ("f32", "bf16"):
+        _check_decode(mfs, rng, [300, 1000, 77], 4, 1, 64, 16, dtype, qscale=30.0)
+        _check_decode(mfs, rng, [300, 1000, 77], 4, 1, 64, 16, dtype, scale=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_paged_attention_bad_pages_give_nan(mfs, dtype):
+    torch = _torch()
+    rng = np.random.default_rng(20)
+    kc, vc = _pool(rng, 4, 2, 16, 64, dtype)
+    table = _i32([[0, 1], [0, 4], [-1, 1], [2, 3]])
+    q = _normal(rng, 4, 4, 64, dtype=dtype)
+    out = torch.zeros_like(q)
+    mfs.mfs_paged_attention(mfs.PagedKV(kc, vc, table), q, _i32([20, 20, 20, 40]), out)  # 40: past the table
+    o = _np(out)
+    assert np.isfinite(o[0]).all() and np.isnan(o[1:]).all()
+    mfs.mfs_paged_attention(mfs.PagedKV(kc, vc, table), q, _i32([20, 16, 20, 32]), out, window=4)
+    o = _np(out)
+    assert np.isfinite(o).all()  # the bad entries are outside the windows now
+
+
+def test_paged_attention_far_offsets(mfs):
+    """Pages whose offsets pass 32 bits."""
+    torch = _torch()
+    rng = np.random.default_rng(21)
+    pages, hkv, page, hd = 9000, 8, 256, 128  # 2.36e9 elements
+    kc = torch.empty(pages, hkv, page, hd, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    table = _i32([[8999, 0, 8500], [8300, 8998, 1]])
+    n = [600, 513]
+    k, v = _normal(rng, sum(n), hkv, hd, dtype="bf16"), _normal(rng, sum(n), hkv, hd, dtype="bf16")
+    cache = mfs.PagedKV(kc, vc, table)
+    mfs.mfs_kv_append(cache, k, v, _i32([0, n[0], sum(n)]), _i32(n), rope=None)
+    q = _normal(rng, 2, 16, hd, dtype="bf16")
+    out = torch.empty_like(q)
+    mfs.mfs_paged_attention(cache, q, _i32(n), out)
+    at = 0
+    for s in range(2):
+        for h in (0, 7, 15):
+            ref, weighted, size = S.attend(_np(q[s, h]), _np(k[at:at + n[s], h // 2]), _np(v[at:at + n[s], h // 2]), hd ** -0.5)
+            assert (np.abs(_np(out[s, h]) - ref) <= S.attention_tolerance(ref, weighted, size, n[s], hd, True)).all()
+        at += n[s]
+
+
+def test_paged_attention_is_repeatable_and_captured(mfs):
+    torch = _torch()
+    rng = np.random.default_rng(22)
+    lens = [3000, 1, 777, 0, 12000]
+    cache, q, out = _check_decode(mfs, rng, lens, 8, 2, 128, 16, "bf16", check=[0, 1, 3])
+    a = out[:5].clone()
+    ws = mfs.mfs_paged_attention_workspace(cache, 8)
+    kv = _i32(lens)
+    b = torch.empty_like(a)
+    for _ in range(3):
+        ws.fill_(255)  # what a workspace holds before does not matter
+        mfs.mfs_paged_attention(cache, q, kv, b, workspace=ws)
+        assert torch.equal(a, b)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mfs.mfs_paged_attention(cache, q, kv, b, workspace=ws)
+    kv.copy_(_i32([10, 1, 30, 2999, 11]))  # lengths are read when the graph runs
+    cache.table[3, :200] = 0
+    g.replay()
+    want = torch.empty_like(b)
+    mfs.mfs_paged_attention(cache, q, kv, want)
+    assert torch.equal(b, want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b.zero_()
+    torch.cuda.synchronize()
+    mfs.mfs_paged_attention(cache, q, kv, b, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(b, want)
+
+
+# ------------------------------------------------------------------- prompts
+
+def _check_prompt(mfs, rng, lens, hq, hkv, hd, dtype, window=0, scale=None, qscale=1.0, tail=3, rows=None, poison=False):
+    torch = _torch()
+    n = sum(lens) + tail
+    qkv = _normal(rng, n, hq + 2 * hkv, hd, dtype=dtype)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    q *= qscale
+    if tail:
+        qkv[n - tail:] = float("nan")  # rows behind the last sequence
+    qn, kn, vn = _np(q), _np(k), _np(v)
+    out = torch.full((n, hq, hd), 7.0, dtype=_dt(dtype), device="cuda")
+    kw = {} if scale is None else dict(scale=scale)
+    mfs.mfs_prompt_attention(q, k, v, _i32(np.cumsum([0] + lens).tolist()), out, window=window, **kw)
+    got = _np(out)
+    assert (got[n - tail:] == 7).all()
+    sc, g, b = hd ** -0.5 if scale is None else scale, hq // hkv, 0
+    for c in lens:
+        picked = range(c) if rows is None or c <= rows else sorted(set(rng.integers(0, c, rows).tolist() + [0, 1, c - 1, c - 2, c // 2]))
+        for i in picked:
+            lo = max(0, i - window + 1) if window else 0
+            for h in (range(hq) if c < 40 else {0, hq // 2, hq - 1}):
+                ref, weighted, size = S.attend(qn[b + i, h], kn[b + lo:b + i + 1, h // g], vn[b + lo:b + i + 1, h // g], sc)
+                tol = S.attention_tolerance(ref, weighted, size, i + 1 - lo, hd, dtype == "bf16")
+                assert (np.abs(got[b + i, h] - ref) <= tol).all(), (c, i, h, np.abs(got[b + i, h] - ref).max(), tol.min())
+        b += c
+    return q, k, v, out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 4, 64), (8, 2, 128), (6, 2, 64), (3, 1, 128)])
+def test_prompt_attention(mfs, hq, hkv, hd, dtype):
+    rng = np.random.default_rng(hq + hd)
+    _check_prompt(mfs, rng, [1, 0, 2, 33, 127, 0, 128, 129, 1, 257, 64], hq, hkv, hd, dtype, rows=40)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("window", [1, 2, 64, 100, 128, 300, 5000])
+def test_prompt_attention_window(mfs, window, hd, dtype):
+    rng = np.random.default_rng(window + hd)
+    _check_prompt(mfs, rng, [700, 3, 129, 511], 4, 2, hd, dtype, window=window, rows=60)
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_prompt_attention_long(mfs, dtype, hd):
+    rng = np.random.default_rng(31)
+    _check_prompt(mfs, rng, [3001, 10, 2000], 4, 1, hd, dtype, rows=40)
+    _check_prompt(mfs, rng, [2500], 2, 2, hd, dtype, rows=40, tail=0)
+
+
+def test_prompt_attention_large_scores(mfs):
+    rng = np.random.default_rng(32)
+    for dtype in ("f32", "bf16"):
+        _check_prompt(mfs, rng, [500, 260], 2, 1, 64, dtype, qscale=30.0, rows=80)
+        _check_prompt(mfs, rng, [300], 2, 1, 128, dtype, scale=1e-6, rows=80)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_prompt_attention_does_not_see_masked_places(mfs, bad, hd, dtype):
+    """A key and a value that are NaN or infinite change no row before them, outside their window, or of another sequence."""
+    torch = _torch()
+    rng = np.random.default_rng(33)
+    lens, window = [200, 450, 300], 150
+    n = sum(lens)
+    q, k, v = (_normal(rng, n, 2, hd, dtype=dtype) for _ in range(3))
+    cu = _i32(np.cumsum([0] + lens).tolist())
+    for w in (0, window):
+        clean, got = torch.empty_like(q), torch.empty_like(q)
+        mfs.mfs_prompt_attention(q, k, v, cu, clean, window=w)
+        for which in ("v", "k"):
+            at = 200 + 170
+            kk, vv = k.clone(), v.clone()
+            (vv if which == "v" else kk)[at, 1, 5] = bad
+            mfs.mfs_prompt_attention(q, kk, vv, cu, got, window=w)
+            touched = torch.zeros(n, dtype=torch.bool)
+            touched[at:min(650, at + w) if w else 650] = True
+            assert torch.equal(got[:, 0], clean[:, 0])
+            assert torch.equal(got[~touched, 1], clean[~touched, 1])
+            if which == "v":  # and it reaches the rows that do see it, in its own column
+                assert not torch.isfinite(got[touched, 1, 5]).any()
+                same = [c for c in range(hd) if c != 5]
+                far = (got[touched][:, 1][:, same].float() - clean[touched][:, 1][:, same].float()).abs().max()
+                assert float(far) <= 0.05
+
+
+def test_prompt_attention_capture_and_lengths_on_the_device(mfs):
+    torch = _torch()
+    rng = np.random.default_rng(34)
+    q, k, v = (_normal(rng, 600, 4, 128, dtype="bf16") for _ in range(3))
+    cu = _i32([0, 100, 600])
+    out = torch.empty_like(q)
+    mfs.mfs_prompt_attention(q, k, v, cu, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mfs.mfs_prompt_attention(q, k, v, cu, out)
+    cu.copy_(_i32([0, 333, 500]))
+    out.fill_(7)
+    g.replay()
+    want = torch.full_like(out, 7)
+    mfs.mfs_prompt_attention(q, k, v, cu, want)
+    assert torch.equal(out, want) and (out[500:] == 7).all() and (out[:500] != 7).any()
+
+
+# ------------------------------------------------------- a run of them together
+
+@pytest.mark.parametrize("dtype,hd,rope,window", [("bf16", 128, "interleaved", 0), ("f32", 64, "half", 90), ("bf16", 64, "half", 50)])
+def test_prompts_then_tokens_through_the_paged_cache(mfs, dtype, hd, rope, window):
+    """Two prompts enter the cache and are attended to, then tokens follow one by one: every output equals the attention over
+    the sequence's whole history, rotated at its positions; then a token is drawn from logits made of the outputs."""
+    torch = _torch()
+    rng = np.random.default_rng(hd + window)
+    hq, hkv, page, steps, lens = 8, 2, 16, 5, [130, 41]
+    n = sum(lens)
+    table, pages = _table(rng, [x + steps for x in lens], page)
+    kc, vc = _pool(rng, pages, hkv, page, hd, dtype)
+    cache = mfs.PagedKV(kc, vc, torch.from_numpy(table).cuda())
+    hist_k, hist_v = [[], []], [[], []]
+
+    def keep(s, k, v, p):
+        hist_k[s].append(S.rotate(_np(k), p, rope, 10000.0))
+        hist_v[s].append(_np(v))
+
+    def check(s, i, q, got):
+        lo = max(0, i - window + 1) if window else 0
+        k, v = np.stack(hist_k[s])[lo:i + 1], np.stack(hist_v[s])[lo:i + 1]
+        for h in range(hq):
+            qr = S.rotate(_np(q)[h], i, rope, 10000.0)
+            ref, weighted, size = S.attend(qr, k[:, h // 4], v[:, h // 4], hd ** -0.5)
+            tol = S.attention_tolerance(ref, weighted, size, i + 1, hd, dtype == "bf16")
+            # the rotated q and k are rounded to the cache's type: each moves a score by half a step of at most `size`, a weight by as much
+            tol = tol + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22) * 4 * size * weighted
+            assert (np.abs(_np(got)[h] - ref) <= tol).all()
+
+    q, k, v = (_normal(rng, n, h, hd, dtype=dtype) for h in (hq, hkv, hkv))
+    q_out, k_out, out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q)
+    cu = _i32([0, lens[0], n])
+    mfs.mfs_kv_append(cache, k, v, cu, _i32(lens), q=q, q_out=q_out, k_out=k_out, rope=rope)
+    mfs.mfs_prompt_attention(q_out, k_out, v, cu, out, window=window)
+    t = 0
+    for s in range(2):
+        for p in range(lens[s]):
+            keep(s, k[t + p], v[t + p], p)
+        for p in (0, 1, lens[s] // 2, lens[s] - 1):
+            check(s, p, q[t + p], out[t + p])
+        t += lens[s]
+    ws = mfs.mfs_paged_attention_workspace(cache, hq)
+    head = _normal(rng, hq * hd, 501)
+    tokens = torch.empty(2, dtype=torch.int32, device="cuda")
+    for step in range(1, steps + 1):
+        q, k, v = (_normal(rng, 2, h, hd, dtype=dtype) for h in (hq, hkv, hkv))
+        kv_len = _i32([x + step for x in lens])
+        q_out, o = torch.empty_like(q), torch.empty_like(q)
+        mfs.mfs_kv_append(cache, k, v, _i32([0, 1, 2]), kv_len, q=q, q_out=q_out, rope=rope)
+        mfs.mfs_paged_attention(cache, q_out, kv_len, o, window=window, workspace=ws)
+        logits = o.float().reshape(2, -1) @ head
+        u = _f32(rng.random(2))
+        mfs.mfs_sample_rows(logits, u, tokens, temperature=_f32([0.7, 0.9]), top_k=_i32([25, 0]), top_p=_f32([1.0, 0.9]))
+        for s in range(2):
+            keep(s, k[s], v[s], lens[s] + step - 1)
+            check(s, lens[s] + step - 1, q[s], o[s])
+            want = S.sample_row(_np(logits[s]), float(u[s]), *[(np.float32(0.7), 25, 1.0), (np.float32(0.9), 0, np.float32(0.9))][s])
+            assert int(tokens[s]) == want
