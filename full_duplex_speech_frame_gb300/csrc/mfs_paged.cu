@@ -1,5 +1,7 @@
 // Paged key/value cache: mfs_kv_append (rotate and write new tokens) and
 // mfs_paged_attention (one new token per sequence).
+#include <type_traits>
+
 #include "mfs_ops.cuh"
 
 namespace {
@@ -131,49 +133,614 @@ int append(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, const in
 }
 
 // --------------------------------------------------------------- attention
+//
+// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 64 positions
+// and all tiles of the call, laid end to end, into equal shares, one per CTA of a grid that fills
+// the GPU once: a CTA walks through its share whatever sequences it crosses, so ragged lengths and
+// few long sequences load every SM alike.  An item (sequence, head block) that lies in one share is
+// finished there; the pieces of one that crosses shares go to the workspace (at most two per CTA)
+// and a second kernel, whose launch overlaps the first one's run, joins them in share order.
+//
+// Each of the 4 warps takes 16 positions of a tile and keeps its own running maximum, sum and
+// output, so nothing is exchanged until the item ends; it feeds itself through a ring of stages
+// with 16-byte asynchronous copies (rows past the length are filled with zeros and never read),
+// with the page of the next stage's rows looked up a stage ahead.
 
-// One warp per (sequence, query head): a running maximum and sum over the keys, HD / 32 elements per lane.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) paged_attention_kernel(Cache C, int n_seqs, const int32_t* __restrict__ kv_len,
-                                                              const T* q, long long q_stride, int hq, T* out,
-                                                              long long out_stride, float scale, int window)
+constexpr int PA_WARPS = 4;
+constexpr int PA_ROWS = 16;                      // positions per warp and tile
+constexpr int PA_TILE = PA_WARPS * PA_ROWS;
+constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
+
+template <typename T>
+struct PaType;
+template <>
+struct PaType<bf16> {
+    static constexpr int GM = 16;  // query heads per block: the rows of an mma tile
+    static constexpr int STAGES = 3;
+};
+template <>
+struct PaType<float> {
+    static constexpr int GM = 8;
+    static constexpr int STAGES = 2;
+};
+
+__device__ __forceinline__ unsigned su32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void copy16(unsigned dst, const void* src, bool full)
 {
-    constexpr int E = HD / 32;
-    const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (w >= n_seqs * hq) return;
-    const int s = w / hq, h = w % hq, kvh = h / (hq / C.n_kv_heads);
-    const int len = __ldg(kv_len + s);
-    float qf[E], o[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        qf[e] = to_f(q[(long long)s * q_stride + h * HD + lane * E + e]) * scale;
-        o[e] = 0.f;
-    }
-    bool bad = false;
-    for (int p = window > 0 && len > window ? len - window : 0; p < len; ++p) {
-        const long long row = row_offset(C, s, p);
-        if (row < 0) { bad = true; break; }
-        const T* kr = reinterpret_cast<const T*>(C.k) + row + (long long)kvh * C.head_stride + lane * E;
-        const T* vr = reinterpret_cast<const T*>(C.v) + row + (long long)kvh * C.head_stride + lane * E;
-        float a = 0.f;
-        for (int e = 0; e < E; ++e) a = fmaf(qf[e], to_f(kr[e]), a);
-        for (int x = 16; x; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-        const float mn = fmaxf(m, a), c = m == mn ? 1.f : expf(m - mn), pr = a == mn ? 1.f : expf(a - mn);
-        l = l * c + pr;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + pr * to_f(vr[e]);
-        m = mn;
-    }
-    for (int e = 0; e < E; ++e)
-        out[(long long)s * out_stride + h * HD + lane * E + e] = from_f<T>(bad ? NAN : len > 0 ? o[e] / l : 0.f);
+    const int n = full ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldm4(unsigned addr, unsigned (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ void ldm4t(unsigned addr, unsigned (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&v);
+}
+
+struct PaArgs {
+    Cache C;
+    const int32_t* kv_len;
+    const char* q;
+    char* out;
+    long long q_stride, out_stride;
+    int n_seqs, hq, g, nhb, window;
+    float c;          // scale * log2(e)
+    float* part_o;    // [CTA][2][GM][HD]
+    float2* part_ml;  // [CTA][2][GM] running maximum (raw score) and sum
+    int4* rec;        // [CTA] {sequence or -1, head block, last CTA of the item, 0}
+};
+
+// Where a walk through the tiles stands.
+struct PaWalk {
+    int s, hb, tile, ntiles, lo, len;
+};
+
+__device__ __forceinline__ void pa_sequence(const PaArgs& A, PaWalk& w)
+{
+    w.len = __ldg(A.kv_len + w.s);
+    w.lo = A.window > 0 && w.len > A.window ? w.len - A.window : 0;
+    w.ntiles = w.len > w.lo ? (w.len - w.lo + PA_TILE - 1) / PA_TILE : 0;
+}
+
+__device__ __forceinline__ void pa_next(const PaArgs& A, PaWalk& w)
+{
+    if (++w.tile < w.ntiles) return;
+    w.tile = 0;
+    if (++w.hb < A.C.n_kv_heads * A.nhb) return;
+    w.hb = 0;
+    do {
+        ++w.s;
+        if (w.s >= A.n_seqs) return;
+        pa_sequence(A, w);
+    } while (w.ntiles == 0);
+}
+
+// Element offset of this lane's row (lane % 16) of the warp's part of the tile, or -1.
+__device__ __forceinline__ long long pa_offset(const PaArgs& A, const PaWalk& w, int warp, bool& bad)
+{
+    const int p = w.lo + w.tile * PA_TILE + warp * PA_ROWS + (threadIdx.x & 15);
+    if (p >= w.len) return -1;
+    const long long off = row_offset(A.C, w.s, p);
+    if (off < 0) { bad = true; return -1; }
+    return off + (long long)(w.hb / A.nhb) * A.C.head_stride;
 }
 
 template <typename T, int HD>
-int attention(const Cache& C, int n_seqs, const int32_t* kv_len, const void* q, long long q_stride, int hq, void* out,
-              long long out_stride, float scale, int window, cudaStream_t st)
+__device__ __forceinline__ void pa_issue(const PaArgs& A, unsigned stage, long long off)
 {
-    const long long warps = (long long)n_seqs * hq;
-    paged_attention_kernel<T, HD><<<(unsigned)((warps + 3) / 4), 128, 0, st>>>(C, n_seqs, kv_len, (const T*)q, q_stride, hq,
-                                                                             (T*)out, out_stride, scale, window);
-    return mfs::op_launched("paged_attention", cudaGetLastError());
+    constexpr int CH = HD * sizeof(T) / 16;      // 16-byte chunks per row
+    constexpr int RPI = CH >= 32 ? 1 : 32 / CH;  // rows per instruction
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < PA_ROWS / RPI; ++j) {
+        const int row = j * RPI + lane / CH, ch = lane % CH;
+        const long long o = __shfl_sync(0xffffffffu, off, row);
+        const long long byte = (o < 0 ? 0 : o) * (long long)sizeof(T) + ch * 16;
+        const unsigned dst = stage + row * (HD * (int)sizeof(T)) + ((ch ^ (row & 7)) << 4);
+        copy16(dst, A.C.k + byte, o >= 0);
+        copy16(dst + PA_ROWS * HD * (int)sizeof(T), A.C.v + byte, o >= 0);
+    }
+}
+
+// One warp's state for an item: scores by mma for bf16 (16 query heads per tile, the rest zero).
+template <int HD>
+struct PaBf16 {
+    static constexpr int GM = PaType<bf16>::GM;
+    unsigned qf[HD / 16][4];
+    float o[HD / 8][4], m[2], l[2];
+
+    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float*, int)
+    {
+        const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+        const int h0 = (w.hb / A.nhb) * A.g + (w.hb % A.nhb) * GM, nh = min(GM, A.g - (w.hb % A.nhb) * GM);
+        const char* q = A.q + ((long long)w.s * A.q_stride + (long long)h0 * HD) * 2;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int row = r + (x & 1) * 8, e = 16 * k + 2 * t + (x >> 1) * 8;
+                qf[k][x] = row < nh ? __ldg(reinterpret_cast<const unsigned*>(q + (row * HD + e) * 2)) : 0u;
+            }
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[j][x] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    __device__ __forceinline__ void tile(unsigned stage, int valid, float c, float*, const float*, int)
+    {
+        const int lane = threadIdx.x & 31, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+        float s[2][4] = {};
+        {
+            const int key = r8 + (mi >> 1) * 8;
+            const unsigned base = stage + key * HD * 2;
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k) {
+                unsigned b[4];
+                ldm4(base + (((2 * k + (mi & 1)) ^ r8) << 4), b);
+                mma_bf16(s[0], qf[k], b[0], b[1]);
+                mma_bf16(s[1], qf[k], b[2], b[3]);
+            }
+        }
+        if (valid < PA_ROWS) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (8 * n + 2 * t + (x & 1) >= valid) s[n][x] = -INFINITY;
+        }
+        float mn[2], scale[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+            mn[h] = fmaxf(m[h], v);
+            scale[h] = m[h] == mn[h] ? 1.f : exp2f((m[h] - mn[h]) * c);
+        }
+        if (__any_sync(0xffffffffu, scale[0] != 1.f || scale[1] != 1.f)) {
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[j][x] *= scale[x >> 1];
+        }
+        unsigned p[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            m[h] = mn[h];
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = exp2f((s[x >> 1][2 * h + (x & 1)] - mn[h]) * c);
+            l[h] = l[h] * scale[h] + (e[0] + e[1]) + (e[2] + e[3]);
+            p[h] = pack_bf16(e[0], e[1]);
+            p[2 + h] = pack_bf16(e[2], e[3]);
+        }
+        {
+            const int key = r8 + (mi & 1) * 8;
+            const unsigned base = stage + (PA_ROWS + key) * HD * 2;
+#pragma unroll
+            for (int j = 0; j < HD / 8; j += 2) {
+                unsigned b[4];
+                ldm4t(base + (((j + (mi >> 1)) ^ r8) << 4), b);
+                mma_bf16(o[j], p, b[0], b[1]);
+                mma_bf16(o[j + 1], p, b[2], b[3]);
+            }
+        }
+    }
+
+    // whole sums over the quad's keys
+    __device__ __forceinline__ void finish()
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+    }
+
+    template <typename F>
+    __device__ __forceinline__ void each(F f)  // f(row, index of its statistics in this lane, element, value)
+    {
+        const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f(r + (x >> 1) * 8, x >> 1, 8 * j + 2 * t + (x & 1), o[j][x]);
+    }
+    __device__ __forceinline__ int own_row(int h) const { return ((threadIdx.x & 31) >> 2) + 8 * h; }
+    static constexpr int OWN = 2;  // rows a lane holds statistics of
+};
+
+// fp32: a lane scores one position over half of the elements, then owns HD / 32 elements of the output.
+template <int HD>
+struct PaF32 {
+    static constexpr int GM = PaType<float>::GM, E = HD / 32, OWN = GM;
+    float o[GM][E], m[GM], l[GM];
+
+    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float* sq, int warp)
+    {
+        const int lane = threadIdx.x & 31;
+        const int h0 = (w.hb / A.nhb) * A.g + (w.hb % A.nhb) * GM, nh = min(GM, A.g - (w.hb % A.nhb) * GM);
+        const float* q = reinterpret_cast<const float*>(A.q) + (long long)w.s * A.q_stride + (long long)h0 * HD;
+        float* mine = sq + warp * GM * HD;
+        __syncwarp();
+        for (int i = lane; i < GM * HD; i += 32) mine[i] = i < nh * HD ? __ldg(q + i) : 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < GM; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[h][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(unsigned, int valid, float c, float* stage, const float* sq, int nh)
+    {
+        const int lane = threadIdx.x & 31, key = lane & 15, part = lane >> 4;
+        float s[GM];
+#pragma unroll
+        for (int h = 0; h < GM; ++h) s[h] = 0.f;
+        const float4* kr = reinterpret_cast<const float4*>(stage + key * HD);
+        for (int i = 0; i < HD / 8; ++i) {
+            const int ch = part * (HD / 8) + i;
+            const float4 k = kr[ch ^ (key & 7)];
+#pragma unroll
+            for (int h = 0; h < GM; ++h)
+                if (h < nh) {
+                    const float4 x = reinterpret_cast<const float4*>(sq + h * HD)[ch];
+                    s[h] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, s[h]))));
+                }
+        }
+        float p[GM];
+#pragma unroll
+        for (int h = 0; h < GM; ++h)
+            if (h < nh) {
+                s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
+                if (key >= valid) s[h] = -INFINITY;
+                float v = s[h];
+                for (int x = 8; x; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+                const float mn = fmaxf(m[h], v), sc = m[h] == mn ? 1.f : exp2f((m[h] - mn) * c);
+                m[h] = mn;
+                p[h] = exp2f((s[h] - mn) * c);
+                l[h] = l[h] * sc + (part == 0 ? p[h] : 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[h][e] *= sc;
+            }
+        for (int j = 0; j < valid; ++j) {
+            float v[E];
+            const float* vr = stage + (PA_ROWS + j) * HD;
+            if (E == 4) {
+                const float4 x = reinterpret_cast<const float4*>(vr)[lane ^ (j & 7)];
+                v[0] = x.x; v[1] = x.y; v[2 % E] = x.z; v[3 % E] = x.w;
+            } else {
+                const float2 x = reinterpret_cast<const float2*>(vr)[((lane >> 1) ^ (j & 7)) * 2 + (lane & 1)];
+                v[0] = x.x; v[1] = x.y;
+            }
+#pragma unroll
+            for (int h = 0; h < GM; ++h)
+                if (h < nh) {
+                    const float pj = __shfl_sync(0xffffffffu, p[h], j);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[h][e] = fmaf(pj, v[e], o[h][e]);
+                }
+        }
+    }
+
+    __device__ __forceinline__ void finish()
+    {
+#pragma unroll
+        for (int h = 0; h < GM; ++h)
+            for (int x = 16; x; x >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+    }
+
+    template <typename F>
+    __device__ __forceinline__ void each(F f)
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int h = 0; h < GM; ++h)
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(h, h, lane * E + e, o[h][e]);
+    }
+    __device__ __forceinline__ int own_row(int h) const { return h; }
+};
+
+template <typename T, int HD>
+struct PaLayout {
+    static constexpr int GM = PaType<T>::GM;
+    static constexpr int STAGE = PA_ROWS * HD * (int)sizeof(T) * 2;  // keys and values of a warp's rows
+    static constexpr int RING = PA_WARPS * PaType<T>::STAGES * STAGE;
+    static constexpr int Q = sizeof(T) == 4 ? PA_WARPS * GM * HD * 4 : 0;
+    static int bytes(int rows) { return RING + Q + 2 * rows * HD * 4; }
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const __grid_constant__ PaArgs A)
+{
+    using L = PaLayout<T, HD>;
+    using State = typename std::conditional<sizeof(T) == 2, PaBf16<HD>, PaF32<HD>>::type;
+    constexpr int GM = L::GM, S = PaType<T>::STAGES;
+    extern __shared__ __align__(128) char pa_raw[];
+    __shared__ long long sh_sum[PA_WARPS];
+    __shared__ int sh_s;
+    __shared__ long long sh_first;
+    __shared__ float2 sh_ml[2][GM];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int Hx = A.C.n_kv_heads * A.nhb, G = gridDim.x, cta = blockIdx.x;
+    float* sq = reinterpret_cast<float*>(pa_raw + L::RING);
+    float* merge = reinterpret_cast<float*>(pa_raw + L::RING + L::Q);  // [2][min(g, GM)][HD]
+    const int mrows = min(A.g, GM);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // sequences of no length: zeros
+    for (int s = cta; s < A.n_seqs; s += G)
+        if (__ldg(A.kv_len + s) <= 0)
+            for (int i = tid; i < A.hq * HD; i += PA_WARPS * 32)
+                reinterpret_cast<T*>(A.out)[(long long)s * A.out_stride + i] = from_f<T>(0.f);
+
+    // the tiles of the call, and the sequence in which this CTA's share starts
+    auto tiles_of = [&](int s) {
+        PaWalk w;
+        w.s = s;
+        pa_sequence(A, w);
+        return w.ntiles;
+    };
+    long long mine = 0;
+    for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) mine += tiles_of(s);
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sh_sum[warp] = mine;
+    __syncthreads();
+    const long long per_head = (sh_sum[0] + sh_sum[1]) + (sh_sum[2] + sh_sum[3]);
+    const long long total = per_head * Hx;
+    const long long Gu = total < G ? total : G;  // CTAs with a share
+    if (cta >= Gu) {
+        if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    const long long t0 = cta * total / Gu, t1 = (cta + 1) * total / Gu;
+    if (warp == 0) {
+        long long run = 0;
+        for (int b = 0; b < A.n_seqs; b += 32) {
+            const int s = b + lane;
+            const long long v = s < A.n_seqs ? (long long)tiles_of(s) * Hx : 0;
+            long long inc = v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, run + inc > t0);
+            if (hit) {
+                if (lane == __ffs(hit) - 1) { sh_s = s; sh_first = run + inc - v; }
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+    __syncthreads();
+    PaWalk use;
+    use.s = sh_s;
+    pa_sequence(A, use);
+    long long item_first = sh_first;  // first tile of the item
+    {
+        const long long in = t0 - item_first;
+        use.hb = (int)(in / use.ntiles);
+        use.tile = (int)(in - (long long)use.hb * use.ntiles);
+        item_first += (long long)use.hb * use.ntiles;
+    }
+    PaWalk load = use;
+    const unsigned ring = su32(pa_raw) + warp * (S * L::STAGE);
+    char* ring_p = pa_raw + warp * (S * L::STAGE);
+
+    int n_load = (int)(t1 - t0);  // tiles not yet asked for
+    const int n = n_load;
+    // the loads run ahead of the products across items: bad pages are noted by tile
+    unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
+    bool next_bad = false;
+    long long off = pa_offset(A, load, warp, next_bad);
+    auto issue = [&](int stage) {
+        if (n_load > 0) {
+            pa_issue<T, HD>(A, ring + stage * L::STAGE, off);
+            bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
+            next_bad = false;
+            if (--n_load > 0) {
+                pa_next(A, load);
+                off = pa_offset(A, load, warp, next_bad);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S; ++i) issue(i);
+
+    State st;
+    bool fresh = true, bad = false;
+    int stage = 0;
+    bool whole_front = use.tile == 0;  // the item began in this share
+    for (int it = 0; it < n; ++it) {
+        if (fresh) {
+            st.begin(A, use, sq, warp);
+            fresh = false;
+            bad = false;
+            whole_front = use.tile == 0;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        const int valid = min(PA_ROWS, use.len - (use.lo + use.tile * PA_TILE + warp * PA_ROWS));
+        const int nh = min(GM, A.g - (use.hb % A.nhb) * GM);
+        if (valid > 0)
+            st.tile(ring + stage * L::STAGE, valid, A.c, reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq + warp * GM * HD, nh);
+        bad = bad || ((bad_ring >> stage) & 1u);
+        __syncwarp();
+        issue(stage);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        const bool ends = use.tile + 1 == use.ntiles;
+        if (ends || it + 1 == n) {
+            // merge the warps: 2 and 3 into 0 and 1, then 1 into 0
+            st.finish();
+            if (bad) {
+#pragma unroll
+                for (int h = 0; h < State::OWN; ++h) st.l[h] = NAN;
+            }
+#pragma unroll
+            for (int half = 2; half >= 1; half >>= 1) {
+                if (warp >= half && warp < 2 * half) {
+                    float* to = merge + (warp - half) * mrows * HD;
+                    st.each([&](int row, int, int e, float v) {
+                        if (row < mrows) to[row * HD + e] = v;
+                    });
+#pragma unroll
+                    for (int h = 0; h < State::OWN; ++h)
+                        if (sizeof(T) == 2 ? (lane & 3) == 0 : lane == 0) sh_ml[warp - half][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
+                }
+                __syncthreads();
+                if (warp < half) {
+                    const float* from = merge + warp * mrows * HD;
+                    float a[State::OWN], b[State::OWN];
+#pragma unroll
+                    for (int h = 0; h < State::OWN; ++h) {
+                        const float2 ml = sh_ml[warp][st.own_row(h)];
+                        const float mn = fmaxf(st.m[h], ml.x);
+                        a[h] = st.m[h] == mn ? 1.f : exp2f((st.m[h] - mn) * A.c);
+                        b[h] = ml.x == mn ? 1.f : exp2f((ml.x - mn) * A.c);
+                        st.m[h] = mn;
+                        st.l[h] = st.l[h] * a[h] + ml.y * b[h];
+                    }
+                    st.each([&](int row, int h, int e, float& v) {
+                        if (row < mrows) v = v * a[h] + from[row * HD + e] * b[h];
+                    });
+                }
+                __syncthreads();
+            }
+            if (warp == 0) {
+                const int h0 = (use.hb / A.nhb) * A.g + (use.hb % A.nhb) * GM;
+                if (ends && whole_front) {
+                    T* o = reinterpret_cast<T*>(A.out) + (long long)use.s * A.out_stride + (long long)h0 * HD;
+                    float inv[State::OWN];
+#pragma unroll
+                    for (int h = 0; h < State::OWN; ++h) inv[h] = 1.f / st.l[h];
+                    st.each([&](int row, int h, int e, float v) {
+                        if (row < nh) o[row * HD + e] = from_f<T>(v * inv[h]);
+                    });
+                } else {
+                    const long long slot = (long long)cta * 2 + (whole_front ? 1 : 0);
+                    float* o = A.part_o + slot * GM * HD;
+                    st.each([&](int row, int, int e, float v) {
+                        if (row < nh) o[row * HD + e] = v;
+                    });
+#pragma unroll
+                    for (int h = 0; h < State::OWN; ++h)
+                        if (sizeof(T) == 2 ? (lane & 3) == 0 : lane == 0) A.part_ml[slot * GM + st.own_row(h)] = make_float2(st.m[h], st.l[h]);
+                }
+                if (it + 1 == n && lane == 0) {
+                    // an item that began here and goes on: which CTA holds its last tile
+                    int4 r = make_int4(-1, 0, 0, 0);
+                    if (!ends && whole_front) {
+                        const long long last = item_first + use.ntiles - 1;
+                        r = make_int4(use.s, use.hb, (int)(((last + 1) * Gu - 1) / total), 0);
+                    }
+                    A.rec[cta] = r;
+                }
+            }
+            fresh = true;
+        }
+        if (it + 1 < n) {
+            if (ends) item_first += use.ntiles;
+            pa_next(A, use);
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Joins the pieces of the items that cross shares: one block per (CTA that began one, query head).
+template <typename T, int HD>
+__global__ void __launch_bounds__(HD) paged_attention_join(const __grid_constant__ PaArgs A)
+{
+    constexpr int GM = PaType<T>::GM;
+    __shared__ float w[PA_MAX_CTAS], red[HD / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+    const int4 r = A.rec[cta];
+    if (r.x < 0 || row >= A.g - (r.y % A.nhb) * GM) return;
+    const int np = r.z - cta + 1;  // pieces: (cta, 1), then (cta + i, 0)
+    float mx = -INFINITY;
+    for (int i = tid; i < np; i += HD) {
+        const float2 ml = A.part_ml[((long long)(cta + i) * 2 + (i == 0)) * GM + row];
+        w[i] = ml.x;
+        mx = fmaxf(mx, ml.x);
+    }
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((tid & 31) == 0) red[tid >> 5] = mx;
+    __syncthreads();
+    mx = red[0];
+    for (int i = 1; i < HD / 32; ++i) mx = fmaxf(mx, red[i]);
+    for (int i = tid; i < np; i += HD) w[i] = w[i] == mx ? 1.f : exp2f((w[i] - mx) * A.c);
+    __syncthreads();
+    float acc = 0.f, l = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < np; ++i) {
+        const long long slot = ((long long)(cta + i) * 2 + (i == 0)) * GM + row;
+        l = fmaf(A.part_ml[slot].y, w[i], l);
+        acc = fmaf(A.part_o[slot * HD + tid], w[i], acc);
+    }
+    const int h = (r.y / A.nhb) * A.g + (r.y % A.nhb) * GM + row;
+    reinterpret_cast<T*>(A.out)[(long long)r.x * A.out_stride + (long long)h * HD + tid] = from_f<T>(acc / l);
+}
+
+size_t attention_workspace(int dtype, int hd)
+{
+    const size_t gm = dtype == MFS_DTYPE_BF16 ? PaType<bf16>::GM : PaType<float>::GM;
+    return (size_t)PA_MAX_CTAS * (2 * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
+}
+
+template <typename T, int HD>
+int attention(PaArgs A, char* workspace, cudaStream_t st)
+{
+    using L = PaLayout<T, HD>;
+    A.nhb = (A.g + L::GM - 1) / L::GM;
+    A.part_o = reinterpret_cast<float*>(workspace);
+    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * L::GM * HD);
+    A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * L::GM);
+    const int rows = A.g < L::GM ? A.g : L::GM;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(L::GM));
+    if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
+    const int G = 2 * sms < PA_MAX_CTAS ? 2 * sms : PA_MAX_CTAS;
+    paged_attention_kernel<T, HD><<<G, PA_WARPS * 32, L::bytes(rows), st>>>(A);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)G, (unsigned)rows);
+    cfg.blockDim = dim3(HD);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return mfs::op_launched("paged_attention", cudaLaunchKernelEx(&cfg, paged_attention_join<T, HD>, A));
 }
 
 }  // namespace
@@ -213,9 +780,9 @@ extern "C" int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs
 
 extern "C" size_t mfs_paged_attention_workspace(const mfs_paged_kv* cache, int n_q_heads)
 {
-    (void)cache;
-    (void)n_q_heads;
-    return 16;
+    (void)n_q_heads;  // the pieces in flight are bounded by the grid, whatever the heads and lengths
+    if (mfs::paged_kv_problem(cache)) return 0;
+    return attention_workspace(cache->dtype, cache->head_dim);
 }
 
 extern "C" int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, const void* q,
@@ -234,12 +801,20 @@ extern "C" int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const 
         return mfs::op_fail(MFS_E_ARG, op, "pointers and token strides must be multiples of 16 bytes, a stride at least heads x head_dim");
     if (((uintptr_t)workspace & 15u) || workspace_bytes < mfs_paged_attention_workspace(cache, n_q_heads))
         return mfs::op_fail(MFS_E_ARG, op, "workspace too small or not 16-byte aligned");
-    if ((long long)n_seqs * n_q_heads > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many sequences x heads");
-    const Cache C = cache_of(cache);
+    PaArgs A = {};
+    A.C = cache_of(cache);
+    A.kv_len = kv_len;
+    A.q = (const char*)q;
+    A.out = (char*)out;
+    A.q_stride = q_stride;
+    A.out_stride = out_stride;
+    A.n_seqs = n_seqs;
+    A.hq = n_q_heads;
+    A.g = n_q_heads / cache->n_kv_heads;
+    A.window = window;
+    A.c = scale * 1.44269504088896340736f;
     cudaStream_t st = (cudaStream_t)cuda_stream;
-    if (cache->dtype == MFS_DTYPE_BF16)
-        return hd == 128 ? attention<bf16, 128>(C, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, st)
-                         : attention<bf16, 64>(C, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, st);
-    return hd == 128 ? attention<float, 128>(C, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, st)
-                     : attention<float, 64>(C, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, st);
+    char* ws = (char*)workspace;
+    if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? attention<bf16, 128>(A, ws, st) : attention<bf16, 64>(A, ws, st);
+    return hd == 128 ? attention<float, 128>(A, ws, st) : attention<float, 64>(A, ws, st);
 }
