@@ -134,21 +134,20 @@ int append(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, const in
 
 // --------------------------------------------------------------- attention
 //
-// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 64 positions
-// and all tiles of the call, laid end to end, into equal shares, one per CTA of a grid that fills
-// the GPU once: a CTA walks through its share whatever sequences it crosses, so ragged lengths and
+// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 16 positions
+// and all tiles of the call, laid end to end, into equal shares, one per warp of a grid that fills
+// the GPU once: a warp walks through its share whatever sequences it crosses, so ragged lengths and
 // few long sequences load every SM alike.  An item (sequence, head block) that lies in one share is
-// finished there; the pieces of one that crosses shares go to the workspace (at most two per CTA)
-// and a second kernel, whose launch overlaps the first one's run, joins them in share order.
+// finished by its warp.  The pieces of the others meet in shared memory once, when the CTA's warps are
+// done; what still crosses CTAs goes to the workspace (at most two pieces per CTA) and a second
+// kernel, whose launch overlaps the first one's run, joins it in share order.
 //
-// Each of the 4 warps takes 16 positions of a tile and keeps its own running maximum, sum and
-// output, so nothing is exchanged until the item ends; it feeds itself through a ring of stages
-// with 16-byte asynchronous copies (rows past the length are filled with zeros and never read),
-// with the page of the next stage's rows looked up a stage ahead.
+// A warp keeps its own running maximum, sum and output, so no warp waits for another before the end;
+// it feeds itself through a ring of stages with 16-byte asynchronous copies (rows past the length are
+// filled with zeros and never read), with the page of the next stage's rows looked up a stage ahead.
 
 constexpr int PA_WARPS = 4;
-constexpr int PA_ROWS = 16;                      // positions per warp and tile
-constexpr int PA_TILE = PA_WARPS * PA_ROWS;
+constexpr int PA_ROWS = 16;                      // positions per tile
 constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
 
 template <typename T>
@@ -205,6 +204,7 @@ struct PaArgs {
     float c;          // scale * log2(e)
     float* part_o;    // [CTA][2][GM][HD]
     float2* part_ml;  // [CTA][2][GM] running maximum (raw score) and sum
+    float* front_o;   // [warp] an item's end, kept until the CTA's warps are done
     int4* rec;        // [CTA] {sequence or -1, head block, last CTA of the item, 0}
 };
 
@@ -217,7 +217,7 @@ __device__ __forceinline__ void pa_sequence(const PaArgs& A, PaWalk& w)
 {
     w.len = __ldg(A.kv_len + w.s);
     w.lo = A.window > 0 && w.len > A.window ? w.len - A.window : 0;
-    w.ntiles = w.len > w.lo ? (w.len - w.lo + PA_TILE - 1) / PA_TILE : 0;
+    w.ntiles = w.len > w.lo ? (w.len - w.lo + PA_ROWS - 1) / PA_ROWS : 0;
 }
 
 __device__ __forceinline__ void pa_next(const PaArgs& A, PaWalk& w)
@@ -233,10 +233,10 @@ __device__ __forceinline__ void pa_next(const PaArgs& A, PaWalk& w)
     } while (w.ntiles == 0);
 }
 
-// Element offset of this lane's row (lane % 16) of the warp's part of the tile, or -1.
-__device__ __forceinline__ long long pa_offset(const PaArgs& A, const PaWalk& w, int warp, bool& bad)
+// Element offset of this lane's row (lane % 16) of the tile, or -1.
+__device__ __forceinline__ long long pa_offset(const PaArgs& A, const PaWalk& w, bool& bad)
 {
-    const int p = w.lo + w.tile * PA_TILE + warp * PA_ROWS + (threadIdx.x & 15);
+    const int p = w.lo + w.tile * PA_ROWS + (threadIdx.x & 15);
     if (p >= w.len) return -1;
     const long long off = row_offset(A.C, w.s, p);
     if (off < 0) { bad = true; return -1; }
@@ -267,7 +267,7 @@ struct PaBf16 {
     unsigned qf[HD / 16][4];
     float o[HD / 8][4], m[2], l[2];
 
-    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float*, int)
+    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float*)
     {
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
         const int h0 = (w.hb / A.nhb) * A.g + (w.hb % A.nhb) * GM, nh = min(GM, A.g - (w.hb % A.nhb) * GM);
@@ -368,6 +368,7 @@ struct PaBf16 {
             for (int x = 0; x < 4; ++x) f(r + (x >> 1) * 8, x >> 1, 8 * j + 2 * t + (x & 1), o[j][x]);
     }
     __device__ __forceinline__ int own_row(int h) const { return ((threadIdx.x & 31) >> 2) + 8 * h; }
+    __device__ __forceinline__ bool owner() const { return (threadIdx.x & 3) == 0; }
     static constexpr int OWN = 2;  // rows a lane holds statistics of
 };
 
@@ -377,14 +378,13 @@ struct PaF32 {
     static constexpr int GM = PaType<float>::GM, E = HD / 32, OWN = GM;
     float o[GM][E], m[GM], l[GM];
 
-    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float* sq, int warp)
+    __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float* sq)
     {
         const int lane = threadIdx.x & 31;
         const int h0 = (w.hb / A.nhb) * A.g + (w.hb % A.nhb) * GM, nh = min(GM, A.g - (w.hb % A.nhb) * GM);
         const float* q = reinterpret_cast<const float*>(A.q) + (long long)w.s * A.q_stride + (long long)h0 * HD;
-        float* mine = sq + warp * GM * HD;
         __syncwarp();
-        for (int i = lane; i < GM * HD; i += 32) mine[i] = i < nh * HD ? __ldg(q + i) : 0.f;
+        for (int i = lane; i < GM * HD; i += 32) sq[i] = i < nh * HD ? __ldg(q + i) : 0.f;
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < GM; ++h) {
@@ -464,15 +464,23 @@ struct PaF32 {
             for (int e = 0; e < E; ++e) f(h, h, lane * E + e, o[h][e]);
     }
     __device__ __forceinline__ int own_row(int h) const { return h; }
+    __device__ __forceinline__ bool owner() const { return (threadIdx.x & 31) == 0; }
 };
 
 template <typename T, int HD>
 struct PaLayout {
     static constexpr int GM = PaType<T>::GM;
-    static constexpr int STAGE = PA_ROWS * HD * (int)sizeof(T) * 2;  // keys and values of a warp's rows
+    static constexpr int STAGE = PA_ROWS * HD * (int)sizeof(T) * 2;  // keys and values of a tile
     static constexpr int RING = PA_WARPS * PaType<T>::STAGES * STAGE;
     static constexpr int Q = sizeof(T) == 4 ? PA_WARPS * GM * HD * 4 : 0;
-    static int bytes(int rows) { return RING + Q + 2 * rows * HD * 4; }
+    static constexpr int BYTES = RING + Q;
+    static_assert(GM * HD * 4 <= PaType<T>::STAGES * STAGE, "a warp's piece takes its ring's place");
+};
+
+// A piece of an item that a warp could not finish: whether the item's first and last tile were in it, and the
+// CTA that holds the last one.  s = -1: none.
+struct PaPiece {
+    int s, hb, first, last, last_cta;
 };
 
 template <typename T, int HD>
@@ -483,14 +491,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     constexpr int GM = L::GM, S = PaType<T>::STAGES;
     extern __shared__ __align__(128) char pa_raw[];
     __shared__ long long sh_sum[PA_WARPS];
-    __shared__ int sh_s;
-    __shared__ long long sh_first;
-    __shared__ float2 sh_ml[2][GM];
+    __shared__ PaPiece sh_piece[2 * PA_WARPS];
+    __shared__ float2 sh_ml[2 * PA_WARPS][GM];
+    __shared__ float sh_w[2 * PA_WARPS][GM], sh_l[GM], sh_m[GM];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hx = A.C.n_kv_heads * A.nhb, G = gridDim.x, cta = blockIdx.x;
-    float* sq = reinterpret_cast<float*>(pa_raw + L::RING);
-    float* merge = reinterpret_cast<float*>(pa_raw + L::RING + L::Q);  // [2][min(g, GM)][HD]
-    const int mrows = min(A.g, GM);
+    float* sq = reinterpret_cast<float*>(pa_raw + L::RING) + warp * GM * HD;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences of no length: zeros
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             for (int i = tid; i < A.hq * HD; i += PA_WARPS * 32)
                 reinterpret_cast<T*>(A.out)[(long long)s * A.out_stride + i] = from_f<T>(0.f);
 
-    // the tiles of the call, and the sequence in which this CTA's share starts
+    // the tiles of the call
     auto tiles_of = [&](int s) {
         PaWalk w;
         w.s = s;
@@ -510,17 +516,20 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) mine += tiles_of(s);
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) sh_sum[warp] = mine;
+    if (tid < 2 * PA_WARPS) sh_piece[tid].s = -1;
     __syncthreads();
-    const long long per_head = (sh_sum[0] + sh_sum[1]) + (sh_sum[2] + sh_sum[3]);
-    const long long total = per_head * Hx;
-    const long long Gu = total < G ? total : G;  // CTAs with a share
-    if (cta >= Gu) {
+    const long long total = ((sh_sum[0] + sh_sum[1]) + (sh_sum[2] + sh_sum[3])) * Hx;
+    const long long shares = min(total, (long long)G * PA_WARPS);
+    const int share = cta * PA_WARPS + warp;
+    if (cta * PA_WARPS >= shares) {
         if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const long long t0 = cta * total / Gu, t1 = (cta + 1) * total / Gu;
-    if (warp == 0) {
-        long long run = 0;
+    if (share < shares) {
+        const long long t0 = share * total / shares, t1 = (share + 1) * total / shares;
+        // where the share starts
+        PaWalk use;
+        long long item_first = 0;  // the item's first tile
         for (int b = 0; b < A.n_seqs; b += 32) {
             const int s = b + lane;
             const long long v = s < A.n_seqs ? (long long)tiles_of(s) * Hx : 0;
@@ -529,112 +538,71 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                 const long long x = __shfl_up_sync(0xffffffffu, inc, o);
                 if (lane >= o) inc += x;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, run + inc > t0);
+            const unsigned hit = __ballot_sync(0xffffffffu, item_first + inc > t0);
             if (hit) {
-                if (lane == __ffs(hit) - 1) { sh_s = s; sh_first = run + inc - v; }
+                const int l = __ffs(hit) - 1;
+                use.s = b + l;
+                item_first += __shfl_sync(0xffffffffu, inc - v, l);
                 break;
             }
-            run += __shfl_sync(0xffffffffu, inc, 31);
+            item_first += __shfl_sync(0xffffffffu, inc, 31);
         }
-    }
-    __syncthreads();
-    PaWalk use;
-    use.s = sh_s;
-    pa_sequence(A, use);
-    long long item_first = sh_first;  // first tile of the item
-    {
-        const long long in = t0 - item_first;
-        use.hb = (int)(in / use.ntiles);
-        use.tile = (int)(in - (long long)use.hb * use.ntiles);
+        pa_sequence(A, use);
+        use.hb = (int)((t0 - item_first) / use.ntiles);
         item_first += (long long)use.hb * use.ntiles;
-    }
-    PaWalk load = use;
-    const unsigned ring = su32(pa_raw) + warp * (S * L::STAGE);
-    char* ring_p = pa_raw + warp * (S * L::STAGE);
+        use.tile = (int)(t0 - item_first);
+        PaWalk load = use;
+        char* ring_p = pa_raw + warp * (S * L::STAGE);
+        const unsigned ring = su32(ring_p);
 
-    int n_load = (int)(t1 - t0);  // tiles not yet asked for
-    const int n = n_load;
-    // the loads run ahead of the products across items: bad pages are noted by tile
-    unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
-    bool next_bad = false;
-    long long off = pa_offset(A, load, warp, next_bad);
-    auto issue = [&](int stage) {
-        if (n_load > 0) {
-            pa_issue<T, HD>(A, ring + stage * L::STAGE, off);
-            bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
-            next_bad = false;
-            if (--n_load > 0) {
-                pa_next(A, load);
-                off = pa_offset(A, load, warp, next_bad);
+        const int n = (int)(t1 - t0);
+        int n_load = n;         // tiles not yet asked for: the loads run ahead of the products, across items
+        unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
+        bool next_bad = false;
+        long long off = pa_offset(A, load, next_bad);
+        auto issue = [&](int stage) {
+            if (n_load > 0) {
+                pa_issue<T, HD>(A, ring + stage * L::STAGE, off);
+                bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
+                next_bad = false;
+                if (--n_load > 0) {
+                    pa_next(A, load);
+                    off = pa_offset(A, load, next_bad);
+                }
             }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
 #pragma unroll
-    for (int i = 0; i < S; ++i) issue(i);
+        for (int i = 0; i < S; ++i) issue(i);
 
-    State st;
-    bool fresh = true, bad = false;
-    int stage = 0;
-    bool whole_front = use.tile == 0;  // the item began in this share
-    for (int it = 0; it < n; ++it) {
-        if (fresh) {
-            st.begin(A, use, sq, warp);
-            fresh = false;
-            bad = false;
-            whole_front = use.tile == 0;
-        }
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        __syncwarp();
-        const int valid = min(PA_ROWS, use.len - (use.lo + use.tile * PA_TILE + warp * PA_ROWS));
-        const int nh = min(GM, A.g - (use.hb % A.nhb) * GM);
-        if (valid > 0)
-            st.tile(ring + stage * L::STAGE, valid, A.c, reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq + warp * GM * HD, nh);
-        bad = bad || ((bad_ring >> stage) & 1u);
-        __syncwarp();
-        issue(stage);
-        stage = stage + 1 == S ? 0 : stage + 1;
-        const bool ends = use.tile + 1 == use.ntiles;
-        if (ends || it + 1 == n) {
-            // merge the warps: 2 and 3 into 0 and 1, then 1 into 0
-            st.finish();
-            if (bad) {
-#pragma unroll
-                for (int h = 0; h < State::OWN; ++h) st.l[h] = NAN;
+        State st;
+        bool fresh = true, bad = false, front = false;
+        int stage = 0;
+        for (int it = 0; it < n; ++it) {
+            if (fresh) {
+                st.begin(A, use, sq);
+                fresh = false;
+                bad = false;
+                front = use.tile == 0;  // the item begins in this share
             }
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+            __syncwarp();
+            const int nh = min(GM, A.g - (use.hb % A.nhb) * GM);
+            st.tile(ring + stage * L::STAGE, min(PA_ROWS, use.len - (use.lo + use.tile * PA_ROWS)), A.c,
+                    reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq, nh);
+            bad = bad || ((bad_ring >> stage) & 1u);
+            __syncwarp();
+            issue(stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
+            const bool ends = use.tile + 1 == use.ntiles;
+            if (ends || it + 1 == n) {
+                st.finish();
+                if (bad) {
 #pragma unroll
-            for (int half = 2; half >= 1; half >>= 1) {
-                if (warp >= half && warp < 2 * half) {
-                    float* to = merge + (warp - half) * mrows * HD;
-                    st.each([&](int row, int, int e, float v) {
-                        if (row < mrows) to[row * HD + e] = v;
-                    });
-#pragma unroll
-                    for (int h = 0; h < State::OWN; ++h)
-                        if (sizeof(T) == 2 ? (lane & 3) == 0 : lane == 0) sh_ml[warp - half][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
+                    for (int h = 0; h < State::OWN; ++h) st.l[h] = NAN;
                 }
-                __syncthreads();
-                if (warp < half) {
-                    const float* from = merge + warp * mrows * HD;
-                    float a[State::OWN], b[State::OWN];
-#pragma unroll
-                    for (int h = 0; h < State::OWN; ++h) {
-                        const float2 ml = sh_ml[warp][st.own_row(h)];
-                        const float mn = fmaxf(st.m[h], ml.x);
-                        a[h] = st.m[h] == mn ? 1.f : exp2f((st.m[h] - mn) * A.c);
-                        b[h] = ml.x == mn ? 1.f : exp2f((ml.x - mn) * A.c);
-                        st.m[h] = mn;
-                        st.l[h] = st.l[h] * a[h] + ml.y * b[h];
-                    }
-                    st.each([&](int row, int h, int e, float& v) {
-                        if (row < mrows) v = v * a[h] + from[row * HD + e] * b[h];
-                    });
-                }
-                __syncthreads();
-            }
-            if (warp == 0) {
-                const int h0 = (use.hb / A.nhb) * A.g + (use.hb % A.nhb) * GM;
-                if (ends && whole_front) {
+                if (ends && front) {
+                    const int h0 = (use.hb / A.nhb) * A.g + (use.hb % A.nhb) * GM;
                     T* o = reinterpret_cast<T*>(A.out) + (long long)use.s * A.out_stride + (long long)h0 * HD;
                     float inv[State::OWN];
 #pragma unroll
@@ -643,33 +611,81 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                         if (row < nh) o[row * HD + e] = from_f<T>(v * inv[h]);
                     });
                 } else {
-                    const long long slot = (long long)cta * 2 + (whole_front ? 1 : 0);
-                    float* o = A.part_o + slot * GM * HD;
+                    // into the place of the warp's ring if that has nothing more to come, else (the end of an item
+                    // begun before the share: once per warp at most) into the workspace until the CTA's end
+                    const bool end = it + 1 == n;
+                    const int slot = 2 * warp + end;
+                    if (end) {
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        __syncwarp();
+                    }
+                    float* o = end ? reinterpret_cast<float*>(ring_p) : A.front_o + (long long)share * GM * HD;
                     st.each([&](int row, int, int e, float v) {
                         if (row < nh) o[row * HD + e] = v;
                     });
+                    if (st.owner()) {
 #pragma unroll
-                    for (int h = 0; h < State::OWN; ++h)
-                        if (sizeof(T) == 2 ? (lane & 3) == 0 : lane == 0) A.part_ml[slot * GM + st.own_row(h)] = make_float2(st.m[h], st.l[h]);
-                }
-                if (it + 1 == n && lane == 0) {
-                    // an item that began here and goes on: which CTA holds its last tile
-                    int4 r = make_int4(-1, 0, 0, 0);
-                    if (!ends && whole_front) {
-                        const long long last = item_first + use.ntiles - 1;
-                        r = make_int4(use.s, use.hb, (int)(((last + 1) * Gu - 1) / total), 0);
+                        for (int h = 0; h < State::OWN; ++h) sh_ml[slot][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
                     }
-                    A.rec[cta] = r;
+                    if (lane == 0)
+                        sh_piece[slot] = {use.s, use.hb, front, ends, (int)(((item_first + use.ntiles) * shares - 1) / total / PA_WARPS)};
                 }
+                fresh = true;
             }
-            fresh = true;
-        }
-        if (it + 1 < n) {
-            if (ends) item_first += use.ntiles;
-            pa_next(A, use);
+            if (it + 1 < n) {
+                if (ends) item_first += use.ntiles;
+                pa_next(A, use);
+            }
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // the pieces of each item, in order
+    if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
+    for (int i = 0; i < 2 * PA_WARPS; ++i) {
+        if (sh_piece[i].s < 0) continue;
+        int j = i;  // the item's last piece here
+        for (int k = i; k < 2 * PA_WARPS && !sh_piece[j].last; ++k)
+            if (sh_piece[k].s >= 0) j = k;
+        const PaPiece p0 = sh_piece[i], p1 = sh_piece[j];
+        const int nh = min(GM, A.g - (p0.hb % A.nhb) * GM);
+        if (tid < nh) {
+            float mx = -INFINITY, l = 0.f;
+            for (int k = i; k <= j; ++k)
+                if (sh_piece[k].s >= 0) mx = fmaxf(mx, sh_ml[k][tid].x);
+            for (int k = i; k <= j; ++k)
+                if (sh_piece[k].s >= 0) {
+                    const float2 ml = sh_ml[k][tid];
+                    const float w = ml.x == mx ? 1.f : exp2f((ml.x - mx) * A.c);
+                    sh_w[k][tid] = w;
+                    l = fmaf(ml.y, w, l);
+                }
+            sh_m[tid] = mx;
+            sh_l[tid] = l;
+        }
+        __syncthreads();
+        const bool whole = p0.first && p1.last;
+        const int h0 = (p0.hb / A.nhb) * A.g + (p0.hb % A.nhb) * GM;
+        T* out = reinterpret_cast<T*>(A.out) + (long long)p0.s * A.out_stride + (long long)h0 * HD;
+        const long long slot = (long long)cta * 2 + (p0.first ? 1 : 0);
+        for (int x = tid; x < nh * HD; x += PA_WARPS * 32) {
+            float acc = 0.f;
+            const int row = x / HD;
+            for (int k = i; k <= j; ++k)
+                if (sh_piece[k].s >= 0) {
+                    const float* o = k & 1 ? reinterpret_cast<const float*>(pa_raw + (k >> 1) * (S * L::STAGE))
+                                           : A.front_o + (long long)(cta * PA_WARPS + (k >> 1)) * GM * HD;
+                    acc = fmaf(o[x], sh_w[k][row], acc);
+                }
+            if (whole) out[x] = from_f<T>(acc / sh_l[row]);
+            else A.part_o[slot * GM * HD + x] = acc;
+        }
+        if (!whole) {
+            if (tid < nh) A.part_ml[slot * GM + tid] = make_float2(sh_m[tid], sh_l[tid]);
+            if (tid == 0 && p0.first) A.rec[cta] = make_int4(p0.s, p0.hb, p1.last_cta, 0);
+        }
+        __syncthreads();
+        i = j;
+    }
 }
 
 // Joins the pieces of the items that cross shares: one block per (CTA that began one, query head).
@@ -710,7 +726,7 @@ __global__ void __launch_bounds__(HD) paged_attention_join(const __grid_constant
 size_t attention_workspace(int dtype, int hd)
 {
     const size_t gm = dtype == MFS_DTYPE_BF16 ? PaType<bf16>::GM : PaType<float>::GM;
-    return (size_t)PA_MAX_CTAS * (2 * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
+    return (size_t)PA_MAX_CTAS * ((2 + PA_WARPS) * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
 }
 
 template <typename T, int HD>
@@ -719,16 +735,17 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     using L = PaLayout<T, HD>;
     A.nhb = (A.g + L::GM - 1) / L::GM;
     A.part_o = reinterpret_cast<float*>(workspace);
-    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * L::GM * HD);
+    A.front_o = A.part_o + (size_t)PA_MAX_CTAS * 2 * L::GM * HD;
+    A.part_ml = reinterpret_cast<float2*>(A.front_o + (size_t)PA_MAX_CTAS * PA_WARPS * L::GM * HD);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * L::GM);
     const int rows = A.g < L::GM ? A.g : L::GM;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(L::GM));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     const int G = 2 * sms < PA_MAX_CTAS ? 2 * sms : PA_MAX_CTAS;
-    paged_attention_kernel<T, HD><<<G, PA_WARPS * 32, L::bytes(rows), st>>>(A);
+    paged_attention_kernel<T, HD><<<G, PA_WARPS * 32, L::BYTES, st>>>(A);
     e = cudaGetLastError();
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     cudaLaunchConfig_t cfg = {};
