@@ -155,7 +155,7 @@ struct PaType;
 template <>
 struct PaType<bf16> {
     static constexpr int GM = 16;  // query heads per block: the rows of an mma tile
-    static constexpr int STAGES = 3;
+    static constexpr int STAGES = 2;
 };
 template <>
 struct PaType<float> {
