@@ -354,6 +354,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
     const uint32_t tm = B.tmem;  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
     const int ntile = t_end - a0;
 
+    // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
         if (lane == 0) {
             auto load = [&](const CUtensorMap* m, char* dst, int head, int row, uint64_t* bar) {
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             commit(&B.drained);
             bar_drain(&B.drained, 0);
         }
-    } else if (warp >= 10) {
+    } else {
         // V of the tiles that some row does not see whole: non-finite values become 0
         const int th = tid - 10 * 32;
         bool ok = true;
@@ -465,7 +468,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             bar_arrive(&B.v_ready[n % 8]);
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int x = warp >> 2, row = tid & (PT_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * PT_M, to = tm + lanes + 2 * PT_M + x * HD;
