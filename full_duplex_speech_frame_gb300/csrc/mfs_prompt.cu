@@ -200,6 +200,12 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ uint64_t pair(float a, float b)
 {
     uint64_t r;
@@ -356,7 +362,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
 
     // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 9) {
         if (lane == 0) {
             auto load = [&](const CUtensorMap* m, char* dst, int head, int row, uint64_t* bar) {
@@ -368,14 +374,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             bar_expect(&B.q_full, (two ? 2 : 1) * S::TILE);
             load(&mq, sq, h, b + r0, &B.q_full);
             if (two) load(&mq, sq + S::TILE, h, b + r0 + PT_M, &B.q_full);
-            int i = 0;
+            int i = 0, slot = 0;
+            unsigned par = 1;
             bool ok = true;
             for (int t = a0; t < t_end && ok; ++t)
                 for (int kv = 0; kv < 2; ++kv, ++i) {
-                    const int slot = i % S::STAGES;
-                    if (!bar_wait(&B.kv_empty[slot], ((i / S::STAGES) & 1) ^ 1, &B.abort)) { ok = false; break; }
+                    if (!bar_wait(&B.kv_empty[slot], par, &B.abort)) { ok = false; break; }
                     bar_expect(&B.kv_full[slot], S::TILE);
                     load(kv ? &mv : &mk, ring + slot * S::TILE, h / A.g, b + t * PT_M, &B.kv_full[slot]);
+                    if (++slot == S::STAGES) { slot = 0; par ^= 1; }
                 }
             if (!ok) {  // the copies in flight
                 bar_drain(&B.q_full, 0);
@@ -386,23 +393,30 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         if (lane == 0) {
             constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((PT_M >> 3) << 17) | ((PT_M >> 4) << 24);
             constexpr uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((PT_M >> 4) << 24);
-            auto full = [&](int i) { return bar_wait(&B.kv_full[i % S::STAGES], (i / S::STAGES) & 1, &B.abort); };
-            auto scores = [&](int x, int i) {
-                const unsigned qa = su32(sq + x * S::TILE), ka = su32(ring + (i % S::STAGES) * S::TILE);
+            // one thread issues everything: descriptors are built once and stepped, ring positions counted
+            const uint64_t dq = desc(su32(sq), 16), dk = desc(su32(ring), 16), dv = desc(su32(ring), S::BOX);
+            auto scores = [&](int x, int slot) {
+                const uint64_t qa = dq + (uint64_t)(x * (S::TILE >> 4)), ka = dk + (uint64_t)(slot * (S::TILE >> 4));
+                const uint32_t d = tm + x * PT_M;
 #pragma unroll
                 for (int k = 0; k < HD / 16; ++k) {
-                    const unsigned at = (k / 4) * S::BOX + (k % 4) * 32;
-                    mma_ss(tm + x * PT_M, desc(qa + at, 16), desc(ka + at, 16), id_s, k > 0);
+                    const uint64_t at = (k / 4) * (S::BOX >> 4) + (k % 4) * 2;
+                    mma_ss(d, qa + at, ka + at, id_s, k > 0);
                 }
             };
-            auto outputs = [&](int x, int i, bool first) {
-                const unsigned va = su32(ring + (i % S::STAGES) * S::TILE);
+            auto outputs = [&](int x, int slot, bool first) {
+                const uint64_t va = dv + (uint64_t)(slot * (S::TILE >> 4));
+                const uint32_t d = tm + 2 * PT_M + x * HD, pa = tm + x * PT_M;
+                mma_ts(d, pa, va, id_o, !first);
 #pragma unroll
-                for (int k = 0; k < PT_M / 16; ++k)
-                    mma_ts(tm + 2 * PT_M + x * HD, tm + x * PT_M + 8 * k, desc(va + k * 16 * 128, S::BOX), id_o, !(first && k == 0));
+                for (int k = 1; k < PT_M / 16; ++k) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
             };
-            unsigned p_par[2] = {0, 0};
-            bool ok = bar_wait(&B.q_full, 0, &B.abort) && full(0);
+            int slot = 0;  // of the next tile of the ring
+            unsigned par = 0, v_par = 0, p_par[2] = {0, 0};
+            auto step = [&]() {
+                if (++slot == S::STAGES) { slot = 0; par ^= 1; }
+            };
+            bool ok = bar_wait(&B.q_full, 0, &B.abort) && bar_wait(&B.kv_full[0], 0, &B.abort);
             if (ok) {
                 fence_after();
                 scores(0, 0);
@@ -412,31 +426,39 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     commit(&B.s_full[1]);
                 }
                 commit(&B.kv_empty[0]);
+                step();
             }
             for (int n = 0; n < ntile && ok; ++n) {
-                const int t = a0 + n, iv = 2 * n + 1, ik = 2 * n + 2;
+                const int t = a0 + n;
                 const bool next = n + 1 < ntile;
-                ok = full(iv) && (!next || full(ik));
-                if (ok) ok = bar_wait(&B.v_ready[n % 8], (n / 8) & 1, &B.abort);
+                const int vs = slot;
+                ok = bar_wait(&B.kv_full[vs], par, &B.abort) && bar_wait(&B.v_ready[n & 7], v_par, &B.abort);
+                if ((n & 7) == 7) v_par ^= 1;
+                step();
+                const int ks = slot;
+                if (ok && next) ok = bar_wait(&B.kv_full[ks], par, &B.abort);
+                if (next) step();
                 if (!ok) break;
-                fence_after();
-                for (int x = 0; x < 2 && ok; ++x) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
                     const bool now = active(x, t), then = next && active(x, t + 1);
                     if (now) {
-                        if (!bar_wait(&B.p_full[x], p_par[x], &B.abort)) { ok = false; break; }
+                        ok = bar_wait(&B.p_full[x], p_par[x], &B.abort);
+                        if (!ok) break;
                         p_par[x] ^= 1;
                         fence_after();
-                        outputs(x, iv, t == (x ? b0 : a0));
+                        outputs(x, vs, t == (x ? b0 : a0));
                     }
                     if (then) {
-                        scores(x, ik);
+                        scores(x, ks);
                         commit(&B.s_full[x]);
                     } else if (now) {
                         commit(&B.o_full[x]);
                     }
                 }
-                commit(&B.kv_empty[iv % S::STAGES]);
-                if (next) commit(&B.kv_empty[ik % S::STAGES]);
+                if (!ok) break;
+                commit(&B.kv_empty[vs]);
+                if (next) commit(&B.kv_empty[ks]);
             }
             commit(&B.drained);
             bar_drain(&B.drained, 0);
@@ -470,45 +492,51 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int x = warp >> 2, row = tid & (PT_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * PT_M, to = tm + lanes + 2 * PT_M + x * HD;
         const int first = x ? b0 : a0, last = x ? b1 : a1;
         const float c = A.c;
         float m = -INFINITY;     // the maximum in use (raw scores), exact up to 2^8 in the weights
-        uint64_t l2 = 0;         // the sum, in two halves
+        uint64_t l2[2] = {0, 0};  // the sum, in four parts
         bool ok = true;
         const int rr = r0 + x * PT_M + row;  // the row in its sequence
         for (int t = first; t < last; ++t) {
             if (!bar_wait(&B.s_full[x], (t - first) & 1, &B.abort)) { ok = false; break; }
             fence_after();
             uint32_t s[PT_M];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tld32(ts + 32 * i, s + 32 * i);
+            tld32(ts, s);
+            tld32(ts + 32, s + 32);
             tld_wait();
-            if (masked(x, t)) {
-                const int hi = rr - PT_M * t, lo = W > 0 ? hi - W + 1 : 0;
+            tld32(ts + 64, s + 64);  // on its way while the first half's maximum is taken
+            tld32(ts + 96, s + 96);
+            const bool some = masked(x, t);
+            const int hi = rr - PT_M * t, lo = W > 0 ? hi - W + 1 : 0;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < PT_M; ++i)
-                    if (i > hi || i < lo) s[i] = 0xff800000u;
-            }
-            float mx0 = __uint_as_float(s[0]), mx1 = __uint_as_float(s[1]);
+            for (int half = 0; half < 2; ++half) {
+                if (half) tld_wait();
+                if (some) {
 #pragma unroll
-            for (int i = 2; i < PT_M; i += 2) {
-                mx0 = fmaxf(mx0, __uint_as_float(s[i]));
-                mx1 = fmaxf(mx1, __uint_as_float(s[i + 1]));
+                    for (int i = 64 * half; i < 64 * half + 64; ++i)
+                        if (i > hi || i < lo) s[i] = 0xff800000u;
+                }
+#pragma unroll
+                for (int i = 64 * half; i < 64 * half + 64; i += 8)
+#pragma unroll
+                    for (int y2 = 0; y2 < 4; ++y2) mx[y2] = max3(mx[y2], __uint_as_float(s[i + y2]), __uint_as_float(s[i + 4 + y2]));
             }
-            const float mx = fmaxf(mx0, mx1);
+            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             if (t == first) {
-                m = mx;
+                m = mt;
             } else {
-                const bool up = mx > m && !((mx - m) * c <= 8.f);
+                const bool up = mt > m && !((mt - m) * c <= 8.f);
                 if (__any_sync(0xffffffffu, up)) {
-                    const float a = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - mx) * c);
-                    if (up) m = mx;
-                    const uint64_t aa = pair(a, a);
-                    l2 = mul2(l2, aa);
+                    const float a = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - mt) * c);
+                    if (up) m = mt;
+                    l2[0] = mul2(l2[0], pair(a, a));
+                    l2[1] = mul2(l2[1], pair(a, a));
 #pragma unroll
                     for (int i = 0; i < HD; i += 32) {
                         uint32_t o[32];
@@ -522,7 +550,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             }
             const float base_ = m == -INFINITY ? 0.f : -m * c;
             const uint64_t cc = pair(c, c), bb = pair(base_, base_);
-            uint64_t acc[2] = {0, 0};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t p[32];
@@ -533,12 +560,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, bb), u, w);
                     u = ex2(u);
                     w = ex2(w);
-                    acc[i & 1] = add2(acc[i & 1], pair(u, w));
+                    l2[i & 1] = add2(l2[i & 1], pair(u, w));
                     p[i] = pack_bf16(u, w);
                 }
                 tst32(ts + 32 * half, p);
             }
-            l2 = add2(l2, add2(acc[0], acc[1]));
             tst_wait();
             fence_before();
             bar_arrive(&B.p_full[x]);
@@ -548,7 +574,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             __syncwarp();
             fence_after();
             float l0, l1;
-            unpair(l2, l0, l1);
+            unpair(add2(l2[0], l2[1]), l0, l1);
             const float inv = ok ? 1.f / (l0 + l1) : NAN;
             bf16* o = A.out + (long long)(b + rr) * A.out_stride + h * HD;
 #pragma unroll
