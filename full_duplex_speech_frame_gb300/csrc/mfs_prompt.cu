@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tm = B.tmem;  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
+    const uint32_t tm = __shfl_sync(0xffffffffu, B.tmem, 0);  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
     const int ntile = t_end - a0;
 
     // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
@@ -390,7 +390,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             }
         }
     } else if (warp == 8) {
-        if (lane == 0) {
+        {
+            unsigned leader;
+            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
             constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((PT_M >> 3) << 17) | ((PT_M >> 4) << 24);
             constexpr uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((PT_M >> 4) << 24);
             // one thread issues everything: descriptors are built once and stepped, ring positions counted
@@ -401,15 +403,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < HD / 16; ++k) {
                     const uint64_t at = (k / 4) * (S::BOX >> 4) + (k % 4) * 2;
-                    mma_ss(d, qa + at, ka + at, id_s, k > 0);
+                    if (leader) mma_ss(d, qa + at, ka + at, id_s, k > 0);
                 }
             };
             auto outputs = [&](int x, int slot, bool first) {
                 const uint64_t va = dv + (uint64_t)(slot * (S::TILE >> 4));
                 const uint32_t d = tm + 2 * PT_M + x * HD, pa = tm + x * PT_M;
-                mma_ts(d, pa, va, id_o, !first);
+                if (leader) mma_ts(d, pa, va, id_o, !first);
 #pragma unroll
-                for (int k = 1; k < PT_M / 16; ++k) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
+                for (int k = 1; k < PT_M / 16; ++k) if (leader) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
             };
             int slot = 0;  // of the next tile of the ring
             unsigned par = 0, v_par = 0, p_par[2] = {0, 0};
@@ -420,12 +422,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             if (ok) {
                 fence_after();
                 scores(0, 0);
-                commit(&B.s_full[0]);
+                if (leader) commit(&B.s_full[0]);
                 if (active(1, a0)) {
                     scores(1, 0);
-                    commit(&B.s_full[1]);
+                    if (leader) commit(&B.s_full[1]);
                 }
-                commit(&B.kv_empty[0]);
+                if (leader) commit(&B.kv_empty[0]);
                 step();
             }
             for (int n = 0; n < ntile && ok; ++n) {
@@ -451,17 +453,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     }
                     if (then) {
                         scores(x, ks);
-                        commit(&B.s_full[x]);
+                        if (leader) commit(&B.s_full[x]);
                     } else if (now) {
-                        commit(&B.o_full[x]);
+                        if (leader) commit(&B.o_full[x]);
                     }
                 }
                 if (!ok) break;
-                commit(&B.kv_empty[vs]);
-                if (next) commit(&B.kv_empty[ks]);
+                if (leader) commit(&B.kv_empty[vs]);
+                if (next) if (leader) commit(&B.kv_empty[ks]);
             }
-            commit(&B.drained);
-            bar_drain(&B.drained, 0);
+            if (leader) commit(&B.drained);
+            if (leader) bar_drain(&B.drained, 0);
         }
     } else {
         // V of the tiles that some row does not see whole: non-finite values become 0
