@@ -1,18 +1,23 @@
 // mfs_prompt_attention: causal attention over packed prompts.
 //
-// bf16: a CTA takes 256 query rows of one sequence and head as two 128-row tiles and walks over the
-// keys they may see in tiles of 128.  Scores S = Q K^T and outputs O += P V are tcgen05 MMAs with
-// accumulators in tensor memory (S 2 x 128 columns, O 2 x head_dim); K and V tiles arrive by TMA
-// through a ring.  Each 128-row tile has four warps with one row per thread: they read a row of
-// scores into registers, take its maximum without any exchange between threads, and write the
-// weights back over the scores as bf16, where the second product reads them as its A operand.  The
-// two tiles alternate: while one is in its softmax, the tensor cores work for the other.  O is
-// rescaled only when a row's maximum grew by more than 2^8 (in the exponent's base 2) since the
-// value in use; until then weights above 1 do no harm, the sum uses the same scale.
+// bf16: one CTA per SM takes blocks of 256 query rows of one sequence and head, as two 128-row tiles,
+// and walks over the keys they may see in tiles of 128.  Scores S = Q K^T and outputs O += P V are
+// tcgen05 MMAs with accumulators in tensor memory (S 2 x 128 columns, O 2 x head_dim); Q, K and V
+// tiles arrive by TMA, K and V through a ring.  Each 128-row tile has four warps with one row per
+// thread: they read a row of scores into registers, take its maximum without any exchange between
+// threads, and write the weights back over the scores as bf16, where the second product reads them as
+// its A operand.  The two tiles alternate: while one is in its softmax, the tensor cores work for the
+// other.  The weights of a tile are taken against the maximum in use so far, while the tile's own is
+// found; only where that is more than 2^8 larger (in the exponent's base 2) is O rescaled and the tile
+// weighted again.  Until then weights above 1 do no harm: the sum uses the same scale.
+//
+// The blocks of a call, those with the most keys first, are dealt out to the CTAs back and forth, so
+// that each gets about the same work; a CTA loads and multiplies for its next block while the last
+// rows of the one before are written.
 //
 // Masked places: scores outside a row's range are replaced, not added to, so a NaN there is gone.  A
 // masked weight is 0, but 0 x NaN is not, so where a tile of keys is masked for some rows (the
-// diagonal, the end of a sequence, a window's edge), two warps clear the non-finite values of V in
+// diagonal, the end of a sequence, a window's edge), a warp clears the non-finite values of V in
 // shared memory before the product; rows that do see one of them (it lies in their range) are
 // computed again at the end by a plain pass in fp32.
 #include <cuda.h>
@@ -81,7 +86,7 @@ int run(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_
 
 constexpr int PT_M = 128;                    // query rows per tile, keys per tile
 constexpr int PT_BLOCK = 2 * PT_M;           // query rows per CTA
-constexpr int PT_THREADS = 384;              // warps 0-3, 4-7: softmax of the two tiles; 8: MMA; 9: TMA; 10, 11: V of masked tiles
+constexpr int PT_THREADS = 384;              // warps 0-3, 4-7: softmax of the two tiles; 8: MMA; 9: TMA; 10, 11: V of masked tiles (11 also the next block)
 constexpr unsigned long long PT_WAIT_NS = 2000000000ull;
 
 template <int HD>
@@ -92,13 +97,19 @@ struct PtShape {
     static constexpr int BYTES = 1024 + 2 * TILE + STAGES * TILE;
 };
 
-struct PtBars {
-    uint64_t q_full, kv_full[8], kv_empty[8], v_ready[8], s_full[2], p_full[2], o_full[2], drained;
-    uint32_t tmem;
-    int abort, cleared;        // a wait gave up; a non-finite value of V was cleared
-    int seq, blk, b, len;      // the CTA's work
-    int scan[PT_THREADS / 32];
+// A block of rows: tokens b + r0 .. of the sequence of len tokens from token b, of head h; h < 0: no more.
+struct __align__(16) PtWork {
+    int b, len, r0, h;
 };
+
+struct PtBars {
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], v_ready[8], s_full[2], p_full[2], o_full[2], work_full[4], work_empty[4], drained;
+    uint32_t tmem;
+    int abort;          // a wait gave up
+    int cleared[4];     // a non-finite value of V was cleared
+    PtWork work[4];     // block i in place i mod 4
+};
+constexpr int PT_READERS = PT_THREADS / 32;  // warps that read the work
 
 __device__ __forceinline__ unsigned su32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
 
@@ -186,10 +197,14 @@ __device__ __forceinline__ void tld32(uint32_t t, uint32_t* r)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
                  "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];" : PT_R16(r, 0), PT_R16(r, 16) : "r"(t));
 }
-__device__ __forceinline__ void tst32(uint32_t t, const uint32_t* r)
+__device__ __forceinline__ void tld16(uint32_t t, uint32_t* r)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-                 "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t), PT_I16(r, 0), PT_I16(r, 16) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" : PT_R16(r, 0) : "r"(t));
+}
+__device__ __forceinline__ void tst16(uint32_t t, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t), PT_I16(r, 0)
+                 : "memory");
 }
 __device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -274,6 +289,129 @@ __device__ __noinline__ void plain_row(const PtArgs& A, int t, int h, int lo)
 
 __device__ __forceinline__ bool not_finite2(uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; }
 
+// The tiles of keys of a block.
+struct PtItem {
+    int b, len, r0, h, W;
+    int first[2], last[2];  // of each row tile
+    int t0, t1;             // of both
+
+    __device__ __forceinline__ bool two() const { return last[1] > first[1]; }
+    // does some row of tile x not see some key of tile t?
+    __device__ __forceinline__ bool masked(int x, int t) const { return t == last[x] - 1 || (W > 0 && PT_M * t < r0 + PT_M * (x + 1) - W); }
+    __device__ __forceinline__ bool active(int x, int t) const { return t >= first[x] && t < last[x]; }
+    __device__ __forceinline__ bool edge(int t) const { return (active(0, t) && masked(0, t)) || (active(1, t) && masked(1, t)); }
+};
+
+// Block i of this CTA, for a whole warp; false: no more (or the wait gave up).
+__device__ __forceinline__ bool next_item(PtBars& B, int i, int W, PtItem& I)
+{
+    if (!bar_wait(&B.work_full[i & 3], (i >> 2) & 1, &B.abort)) return false;
+    const PtWork w = B.work[i & 3];
+    if (w.h < 0) return false;
+    I.b = w.b;
+    I.len = w.len;
+    I.r0 = w.r0;
+    I.h = w.h;
+    I.W = W;
+    for (int x = 0; x < 2; ++x) {
+        const int r = w.r0 + PT_M * x;
+        I.first[x] = W > 0 ? max(0, r - W + 1) / PT_M : 0;
+        I.last[x] = r < w.len ? r / PT_M + 1 : I.first[x];
+    }
+    I.t0 = I.first[0];
+    I.t1 = max(I.last[0], I.last[1]);
+    if (!I.two()) I.t1 = I.last[0];
+    return true;
+}
+
+__device__ __forceinline__ void done_with_item(PtBars& B, int i)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(&B.work_empty[i & 3]);
+}
+
+// Deals out the call's blocks.  Pairs (row block, sequence) are ordered by block number, largest first (about the
+// number of their keys), then by sequence; an item is a pair and a head, heads innermost, so that neighbouring CTAs
+// share keys; round r of G items goes to the CTAs in ascending order for even r, descending for odd r.
+struct PtDealer {
+    const PtArgs& A;
+    int level, above, upto;  // the current block number; pairs of larger numbers; those and its own
+
+    __device__ __forceinline__ int blocks(int s, int& b, int& len) const
+    {
+        b = min(max(__ldg(A.cu + s), 0), A.n_tokens);
+        len = max(min(__ldg(A.cu + s + 1), A.n_tokens) - b, 0);
+        return (len + PT_BLOCK - 1) / PT_BLOCK;
+    }
+    __device__ int pairs_from(int lv) const
+    {
+        int n = 0, b, len;
+        for (int s = threadIdx.x & 31; s < A.n_seqs; s += 32) n += max(0, blocks(s, b, len) - lv);
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+    __device__ __forceinline__ PtDealer(const PtArgs& a) : A(a), level(0), above(0), upto(0) {}
+    __device__ void start()
+    {
+        int n = 0, b, len;
+        for (int s = threadIdx.x & 31; s < A.n_seqs; s += 32) n = max(n, blocks(s, b, len));
+        level = __reduce_max_sync(0xffffffffu, n);
+    }
+    // item r of this CTA, false: there is none
+    __device__ bool get(int r, PtWork& w)
+    {
+        const long long G = gridDim.x, it = r * G + (r & 1 ? G - 1 - blockIdx.x : blockIdx.x);
+        const long long pair = it / A.hq;
+        while (pair >= upto) {
+            if (level == 0) return false;
+            --level;
+            above = upto;
+            upto = pairs_from(level);
+        }
+        int k = (int)(pair - above);  // the k-th sequence with such a block
+        const int lane = threadIdx.x & 31;
+        for (int s0 = 0; s0 < A.n_seqs; s0 += 32) {
+            int b = 0, len = 0;
+            const bool has = s0 + lane < A.n_seqs && blocks(s0 + lane, b, len) > level;
+            unsigned m = __ballot_sync(0xffffffffu, has);
+            if (k >= __popc(m)) { k -= __popc(m); continue; }
+            while (k--) m &= m - 1;
+            const int l = __ffs(m) - 1;
+            w.b = __shfl_sync(0xffffffffu, b, l);
+            w.len = __shfl_sync(0xffffffffu, len, l);
+            w.r0 = level * PT_BLOCK;
+            w.h = (int)(it % A.hq);
+            return true;
+        }
+        return false;
+    }
+};
+
+// A warp's 32 rows of block i, tile x: those that see a value that was cleared are computed again.
+template <int HD>
+__device__ __noinline__ void again(const PtArgs& A, PtBars& B, int i, int x, int quarter)
+{
+    PtItem I;
+    const int W = A.window, lane = threadIdx.x & 31;
+    if (!next_item(B, i, W, I)) return;  // published long ago
+    const int r1 = I.r0 + x * PT_M + 32 * quarter;
+    for (int r = r1; r < min(I.len, r1 + 32); ++r) {
+        const int lo = W > 0 ? max(0, r - W + 1) : 0;
+        bool sees = false;
+        for (int t = max(I.t0, lo / PT_M); t <= r / PT_M && !sees; ++t) {
+            if (!I.edge(t)) continue;
+            for (int j = max(lo, t * PT_M); j <= min(r, t * PT_M + PT_M - 1); ++j) {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(A.v + (long long)(I.b + j) * A.v_stride + I.h / A.g * HD);
+                for (int e = lane; e < HD / 2; e += 32) sees = sees || not_finite2(__ldg(p + e));
+            }
+            sees = __any_sync(0xffffffffu, sees);
+        }
+        if (sees) plain_row<HD>(A, I.b + r, I.h, I.b + lo);
+    }
+}
+
+// The top bit of each half is set if that half's exponent is all ones (a bf16 infinity or NaN).
+__device__ __forceinline__ uint32_t ones_exponent(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
+
 template <int HD>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_constant__ CUtensorMap mq,
                                                                    const __grid_constant__ CUtensorMap mk,
@@ -287,115 +425,92 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
     char* sq = base;
     char* ring = base + 2 * S::TILE;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % A.hq, y = blockIdx.x / A.hq;
-
-    // this CTA's sequence and block of rows, the last block of a sequence first
-    {
-        const int per = (A.n_seqs + PT_THREADS - 1) / PT_THREADS;
-        auto length = [&](int s, int& b) {
-            b = min(max(__ldg(A.cu + s), 0), A.n_tokens);
-            return max(min(__ldg(A.cu + s + 1), A.n_tokens) - b, 0);
-        };
-        int mine = 0, b;
-        for (int s = tid * per; s < min(A.n_seqs, (tid + 1) * per); ++s) mine += (length(s, b) + PT_BLOCK - 1) / PT_BLOCK;
-        int inc = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
+    if (tid == 0) {
+        B.abort = 0;
+        for (int i = 0; i < S::STAGES; ++i) {
+            bar_init(&B.kv_full[i], 1);
+            bar_init(&B.kv_empty[i], 1);
         }
-        if (lane == 31) B.scan[warp] = inc;
-        if (tid == 0) {
-            B.seq = -1;
-            B.abort = B.cleared = 0;
-            bar_init(&B.q_full, 1);
-            for (int i = 0; i < S::STAGES; ++i) {
-                bar_init(&B.kv_full[i], 1);
-                bar_init(&B.kv_empty[i], 1);
-            }
-            for (int i = 0; i < 8; ++i) bar_init(&B.v_ready[i], 64);
-            for (int i = 0; i < 2; ++i) {
-                bar_init(&B.s_full[i], 1);
-                bar_init(&B.p_full[i], PT_M);
-                bar_init(&B.o_full[i], 1);
-            }
-            bar_init(&B.drained, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < 8; ++i) bar_init(&B.v_ready[i], 2);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&B.q_full[i], 1);
+            bar_init(&B.q_empty[i], 1);
+            bar_init(&B.s_full[i], 1);
+            bar_init(&B.p_full[i], PT_M);
+            bar_init(&B.o_full[i], 1);
         }
-        __syncthreads();
-        int run = inc - mine;
-        for (int w = 0; w < warp; ++w) run += B.scan[w];
-        if (y >= run && y < run + mine)
-            for (int s = tid * per; s < A.n_seqs; ++s) {
-                const int len = length(s, b), nb = (len + PT_BLOCK - 1) / PT_BLOCK;
-                if (y < run + nb) {
-                    B.seq = s;
-                    B.blk = nb - 1 - (y - run);
-                    B.b = b;
-                    B.len = len;
-                    break;
-                }
-                run += nb;
-            }
-        __syncthreads();
-        if (B.seq < 0) return;
+        for (int i = 0; i < 4; ++i) {
+            bar_init(&B.work_full[i], 1);
+            bar_init(&B.work_empty[i], PT_READERS);
+        }
+        bar_init(&B.drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const int b = B.b, len = B.len, r0 = B.blk * PT_BLOCK, W = A.window;
-    // tiles of keys: [a0, a1) for the first row tile, [b0, b1) for the second
-    const int a0 = W > 0 ? max(0, r0 - W + 1) / PT_M : 0, a1 = r0 / PT_M + 1;
-    const bool two = len > r0 + PT_M;
-    const int b0 = W > 0 ? max(0, r0 + PT_M - W + 1) / PT_M : 0, b1 = two ? a1 + 1 : 0;
-    const int t_end = two ? b1 : a1;
-    // does some row of tile x (0, 1) not see some key of tile t?
-    auto masked = [&](int x, int t) { return t == (x ? b1 : a1) - 1 || (W > 0 && PT_M * t < r0 + PT_M * (x + 1) - W); };
-    auto active = [&](int x, int t) { return x ? t >= b0 && t < b1 : t < a1; };
-    auto edge = [&](int t) { return (active(0, t) && masked(0, t)) || (active(1, t) && masked(1, t)); };
-
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&B.tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    PtDealer deal(A);
+    if (warp == 11) deal.start();
+    if (tid == 9 * 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&mk) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&mv) : "memory");
     }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, B.tmem, 0);  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
-    const int ntile = t_end - a0;
+    const int W = A.window;
 
     // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 9) {
-        if (lane == 0) {
+        if (warp == 9) {
             auto load = [&](const CUtensorMap* m, char* dst, int head, int row, uint64_t* bar) {
+                bar_expect(bar, S::TILE);
 #pragma unroll
                 for (int x = 0; x < HD / 64; ++x)
                     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                                  ::"r"(su32(dst + x * S::BOX)), "l"(m), "r"(64 * x), "r"(head), "r"(row), "r"(su32(bar)) : "memory");
             };
-            bar_expect(&B.q_full, (two ? 2 : 1) * S::TILE);
-            load(&mq, sq, h, b + r0, &B.q_full);
-            if (two) load(&mq, sq + S::TILE, h, b + r0 + PT_M, &B.q_full);
-            int i = 0, slot = 0;
-            unsigned par = 1;
-            bool ok = true;
-            for (int t = a0; t < t_end && ok; ++t)
-                for (int kv = 0; kv < 2; ++kv, ++i) {
-                    if (!bar_wait(&B.kv_empty[slot], par, &B.abort)) { ok = false; break; }
-                    bar_expect(&B.kv_full[slot], S::TILE);
-                    load(kv ? &mv : &mk, ring + slot * S::TILE, h / A.g, b + t * PT_M, &B.kv_full[slot]);
-                    if (++slot == S::STAGES) { slot = 0; par ^= 1; }
-                }
-            if (!ok) {  // the copies in flight
-                bar_drain(&B.q_full, 0);
-                for (int k = max(0, i - S::STAGES); k < i; ++k) bar_drain(&B.kv_full[k % S::STAGES], (k / S::STAGES) & 1);
+            PtItem I;
+            int n = 0, slot = 0;               // tiles asked for
+            unsigned par = 1, q_par[2] = {1, 1};
+            bool ok = true, q_used[2] = {false, false};
+            for (int i = 0; ok && next_item(B, i, W, I); ++i) {
+                auto query = [&](int x) {
+                    if (!bar_wait(&B.q_empty[x], q_par[x], &B.abort)) return false;
+                    if (lane == 0) load(&mq, sq + x * S::TILE, I.h, I.b + I.r0 + PT_M * x, &B.q_full[x]);
+                    q_par[x] ^= 1;
+                    q_used[x] = true;
+                    return true;
+                };
+                ok = query(0);
+                for (int t = I.t0; t < I.t1 && ok; ++t)
+                    for (int kv = 0; kv < 2 && ok; ++kv) {
+                        ok = bar_wait(&B.kv_empty[slot], par, &B.abort);
+                        if (!ok) break;
+                        if (lane == 0) load(kv ? &mv : &mk, ring + slot * S::TILE, I.h / A.g, I.b + t * PT_M, &B.kv_full[slot]);
+                        __syncwarp();
+                        ++n;
+                        if (++slot == S::STAGES) { slot = 0; par ^= 1; }
+                        if (t == I.t0 && kv == 0 && I.two()) ok = query(1);
+                    }
+                done_with_item(B, i);
             }
-        }
-    } else if (warp == 8) {
-        {
-            unsigned leader;
-            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+            if (*(volatile int*)&B.abort && lane == 0) {  // the copies in flight
+                for (int x = 0; x < 2; ++x)
+                    if (q_used[x]) bar_drain(&B.q_full[x], q_par[x]);
+                for (int k = max(0, n - S::STAGES); k < n; ++k) bar_drain(&B.kv_full[k % S::STAGES], (k / S::STAGES) & 1);
+            }
+        } else if (warp == 8) {
+            // the whole warp runs the loop and an elected lane issues: the operands' descriptors stay in uniform
+            // registers (a single thread's loop took 70-80 cycles an MMA to move them there, an MMA takes 64)
             constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((PT_M >> 3) << 17) | ((PT_M >> 4) << 24);
             constexpr uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((HD >> 3) << 17) | ((PT_M >> 4) << 24);
-            // one thread issues everything: descriptors are built once and stepped, ring positions counted
+            unsigned leader;
+            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
             const uint64_t dq = desc(su32(sq), 16), dk = desc(su32(ring), 16), dv = desc(su32(ring), S::BOX);
             auto scores = [&](int x, int slot) {
                 const uint64_t qa = dq + (uint64_t)(x * (S::TILE >> 4)), ka = dk + (uint64_t)(slot * (S::TILE >> 4));
@@ -411,191 +526,263 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 const uint32_t d = tm + 2 * PT_M + x * HD, pa = tm + x * PT_M;
                 if (leader) mma_ts(d, pa, va, id_o, !first);
 #pragma unroll
-                for (int k = 1; k < PT_M / 16; ++k) if (leader) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
+                for (int k = 1; k < PT_M / 16; ++k)
+                    if (leader) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
+            };
+            auto signal = [&](uint64_t* bar) {
+                if (leader) commit(bar);
             };
             int slot = 0;  // of the next tile of the ring
-            unsigned par = 0, v_par = 0, p_par[2] = {0, 0};
+            unsigned par = 0, v_at = 0, p_par[2] = {0, 0}, q_par[2] = {0, 0};
             auto step = [&]() {
                 if (++slot == S::STAGES) { slot = 0; par ^= 1; }
             };
-            bool ok = bar_wait(&B.q_full, 0, &B.abort) && bar_wait(&B.kv_full[0], 0, &B.abort);
-            if (ok) {
-                fence_after();
-                scores(0, 0);
-                if (leader) commit(&B.s_full[0]);
-                if (active(1, a0)) {
-                    scores(1, 0);
-                    if (leader) commit(&B.s_full[1]);
-                }
-                if (leader) commit(&B.kv_empty[0]);
-                step();
-            }
-            for (int n = 0; n < ntile && ok; ++n) {
-                const int t = a0 + n;
-                const bool next = n + 1 < ntile;
-                const int vs = slot;
-                ok = bar_wait(&B.kv_full[vs], par, &B.abort) && bar_wait(&B.v_ready[n & 7], v_par, &B.abort);
-                if ((n & 7) == 7) v_par ^= 1;
-                step();
-                const int ks = slot;
-                if (ok && next) ok = bar_wait(&B.kv_full[ks], par, &B.abort);
-                if (next) step();
-                if (!ok) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const bool now = active(x, t), then = next && active(x, t + 1);
-                    if (now) {
-                        ok = bar_wait(&B.p_full[x], p_par[x], &B.abort);
-                        if (!ok) break;
-                        p_par[x] ^= 1;
+            bool ok = true;
+            PtItem I;
+            for (int i = 0; ok && next_item(B, i, W, I); ++i) {
+                // scores of row tile x for tile t of keys, in the ring at ks; the block's Q is free after its last
+                auto score_tile = [&](int x, int t, int ks) {
+                    if (t == I.first[x]) {
+                        if (!bar_wait(&B.q_full[x], q_par[x], &B.abort)) return false;
+                        q_par[x] ^= 1;
                         fence_after();
-                        outputs(x, vs, t == (x ? b0 : a0));
                     }
-                    if (then) {
-                        scores(x, ks);
-                        if (leader) commit(&B.s_full[x]);
-                    } else if (now) {
-                        if (leader) commit(&B.o_full[x]);
-                    }
+                    scores(x, ks);
+                    signal(&B.s_full[x]);
+                    if (t == I.last[x] - 1) signal(&B.q_empty[x]);
+                    return true;
+                };
+                ok = bar_wait(&B.kv_full[slot], par, &B.abort);
+                if (ok) {
+                    fence_after();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (ok && I.active(x, I.t0)) ok = score_tile(x, I.t0, slot);
+                    signal(&B.kv_empty[slot]);
+                    step();
                 }
-                if (!ok) break;
-                if (leader) commit(&B.kv_empty[vs]);
-                if (next) if (leader) commit(&B.kv_empty[ks]);
+                for (int t = I.t0; t < I.t1 && ok; ++t) {
+                    const bool next = t + 1 < I.t1;
+                    const int vs = slot;
+                    ok = bar_wait(&B.v_ready[v_at & 7], (v_at >> 3) & 1, &B.abort);  // loaded, and cleared where masked
+                    ++v_at;
+                    step();
+                    const int ks = slot;
+                    if (next) {
+                        ok = ok && bar_wait(&B.kv_full[ks], par, &B.abort);
+                        step();
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (!ok) break;
+                        if (I.active(x, t)) {
+                            ok = bar_wait(&B.p_full[x], p_par[x], &B.abort);
+                            if (!ok) break;
+                            p_par[x] ^= 1;
+                            fence_after();
+                            outputs(x, vs, t == I.first[x]);
+                            if (t == I.last[x] - 1) signal(&B.o_full[x]);
+                        }
+                        if (next && I.active(x, t + 1)) ok = score_tile(x, t + 1, ks);
+                    }
+                    signal(&B.kv_empty[vs]);
+                    if (next) signal(&B.kv_empty[ks]);
+                }
+                done_with_item(B, i);
             }
-            if (leader) commit(&B.drained);
+            signal(&B.drained);
             if (leader) bar_drain(&B.drained, 0);
-        }
-    } else {
-        // V of the tiles that some row does not see whole: non-finite values become 0
-        const int th = tid - 10 * 32;
-        bool ok = true;
-        for (int n = 0; n < ntile && ok; ++n) {
-            const int t = a0 + n, i = 2 * n + 1, slot = i % S::STAGES;
-            // every tile is waited for and passed on, so that these warps stay in step with the ring
-            ok = bar_wait(&B.kv_full[slot], (i / S::STAGES) & 1, &B.abort);
-            if (!ok) break;
-            bool wrote = false;
-            for (int c = edge(t) ? th : S::TILE; c < S::TILE / 16; c += 64) {
-                uint4* p = reinterpret_cast<uint4*>(ring + slot * S::TILE) + c;
-                const uint4 x = *p;
-                if (not_finite2(x.x) || not_finite2(x.y) || not_finite2(x.z) || not_finite2(x.w)) {
-                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    for (int e = 0; e < 4; ++e) {
-                        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-                        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
-                    }
-                    *p = make_uint4(w[0], w[1], w[2], w[3]);
-                    wrote = true;
-                    if (t * PT_M + (c * 16 % S::BOX) / 128 < len) *(volatile int*)&B.cleared = 1;
+        } else {
+            // Warp 11 deals out the blocks, one ahead; both look through V of the tiles that some row does not see whole,
+            // half a tile each: non-finite values become 0.  Every tile is waited for and passed on.
+            PtItem I;
+            PtWork w;
+            int slot = 1 % S::STAGES;
+            unsigned par = 0, v_at = 0;
+            bool ok = true, more = warp == 11;
+            auto publish = [&](int i) {  // block i
+                if (!more) return true;
+                more = deal.get(i, w);
+                if (!bar_wait(&B.work_empty[i & 3], ((i >> 2) & 1) ^ 1, &B.abort)) return false;
+                if (lane == 0) {
+                    if (!more) w.h = -1;
+                    B.work[i & 3] = w;
+                    B.cleared[i & 3] = 0;
+                    bar_arrive(&B.work_full[i & 3]);
                 }
+                __syncwarp();
+                return true;
+            };
+            int i = 0;
+            ok = publish(0);
+            for (; ok && next_item(B, i, W, I); ++i) {
+                ok = publish(i + 1);
+                for (int t = I.t0; t < I.t1 && ok; ++t) {
+                    ok = bar_wait(&B.kv_full[slot], par, &B.abort);
+                    if (!ok) break;
+                    if (I.edge(t)) {
+                        bool wrote = false;
+                        const int from = (warp - 10) * (S::TILE / 32);
+                        uint4* tile = reinterpret_cast<uint4*>(ring + slot * S::TILE) + from + lane;
+                        for (int c0 = 0; c0 < S::TILE / 32; c0 += 8 * 32) {
+                            uint4 x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = tile[c0 + 32 * e];
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                any |= ones_exponent(x[e].x) | ones_exponent(x[e].y) | ones_exponent(x[e].z) | ones_exponent(x[e].w);
+                            if (!(any & 0x80008000u)) continue;
+                            for (int e = 0; e < 8; ++e) {
+                                const int c = from + c0 + 32 * e + lane;
+                                const uint4 y = tile[c0 + 32 * e];
+                                uint32_t v[4] = {y.x, y.y, y.z, y.w};
+                                bool here = false;
+                                for (int k = 0; k < 4; ++k) {
+                                    here = here || not_finite2(v[k]);
+                                    if ((v[k] & 0x7f80u) == 0x7f80u) v[k] &= 0xffff0000u;
+                                    if ((v[k] & 0x7f800000u) == 0x7f800000u) v[k] &= 0xffffu;
+                                }
+                                if (!here) continue;
+                                tile[c0 + 32 * e] = make_uint4(v[0], v[1], v[2], v[3]);
+                                wrote = true;
+                                if (t * PT_M + (c * 16 % S::BOX) / 128 < I.len) *(volatile int*)&B.cleared[i & 3] = 1;
+                            }
+                        }
+                        if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&B.v_ready[v_at & 7]);
+                    ++v_at;
+                    slot += 2;
+                    if (slot >= S::STAGES) { slot -= S::STAGES; par ^= 1; }
+                }
+                done_with_item(B, i);
             }
-            if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive(&B.v_ready[n % 8]);
+            if (*(volatile int*)&B.abort)
+                // given up: NaN for the blocks that nobody will compute
+                for (++i; more; ++i) {
+                    for (int r = w.r0; r < min(w.len, w.r0 + PT_BLOCK); ++r)
+                        for (int e = lane; e < HD; e += 32) A.out[(long long)(w.b + r) * A.out_stride + w.h * HD + e] = __float2bfloat16_rn(NAN);
+                    more = deal.get(i + 1, w);
+                }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int x = warp >> 2, row = tid & (PT_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * PT_M, to = tm + lanes + 2 * PT_M + x * HD;
-        const int first = x ? b0 : a0, last = x ? b1 : a1;
         const float c = A.c;
-        float m = -INFINITY;     // the maximum in use (raw scores), exact up to 2^8 in the weights
-        uint64_t l2[2] = {0, 0};  // the sum, in four parts
+        unsigned s_par = 0, o_par = 0;
         bool ok = true;
-        const int rr = r0 + x * PT_M + row;  // the row in its sequence
-        for (int t = first; t < last; ++t) {
-            if (!bar_wait(&B.s_full[x], (t - first) & 1, &B.abort)) { ok = false; break; }
-            fence_after();
-            uint32_t s[PT_M];
-            tld32(ts, s);
-            tld32(ts + 32, s + 32);
-            tld_wait();
-            tld32(ts + 64, s + 64);  // on its way while the first half's maximum is taken
-            tld32(ts + 96, s + 96);
-            const bool some = masked(x, t);
-            const int hi = rr - PT_M * t, lo = W > 0 ? hi - W + 1 : 0;
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (half) tld_wait();
-                if (some) {
-#pragma unroll
-                    for (int i = 64 * half; i < 64 * half + 64; ++i)
-                        if (i > hi || i < lo) s[i] = 0xff800000u;
-                }
-#pragma unroll
-                for (int i = 64 * half; i < 64 * half + 64; i += 8)
-#pragma unroll
-                    for (int y2 = 0; y2 < 4; ++y2) mx[y2] = max3(mx[y2], __uint_as_float(s[i + y2]), __uint_as_float(s[i + 4 + y2]));
+        for (int i = 0;; ++i) {
+            int first, last, rr;  // rr: the row in its sequence
+            {
+                PtItem I;
+                if (!next_item(B, i, W, I)) break;
+                first = x ? I.first[1] : I.first[0];
+                last = x ? I.last[1] : I.last[0];
+                rr = I.r0 + x * PT_M + row;
             }
-            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-            if (t == first) {
-                m = mt;
-            } else {
-                const bool up = mt > m && !((mt - m) * c <= 8.f);
-                if (__any_sync(0xffffffffu, up)) {
-                    const float a = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - mt) * c);
-                    if (up) m = mt;
-                    l2[0] = mul2(l2[0], pair(a, a));
-                    l2[1] = mul2(l2[1], pair(a, a));
+            float m = -INFINITY;       // the maximum in use (raw scores), exact up to 2^8 in the weights
+            uint64_t l2[2] = {0, 0};   // the sum, in four parts
+            for (int t = first; t < last && ok; ++t) {
+                ok = bar_wait(&B.s_full[x], s_par, &B.abort);
+                if (!ok) break;
+                s_par ^= 1;
+                __syncwarp();
+                fence_after();
+                uint32_t s[PT_M];
 #pragma unroll
-                    for (int i = 0; i < HD; i += 32) {
-                        uint32_t o[32];
-                        tld32(to + i, o);
-                        tld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tst32(to + i, o);
-                    }
-                }
-            }
-            const float base_ = m == -INFINITY ? 0.f : -m * c;
-            const uint64_t cc = pair(c, c), bb = pair(base_, base_);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = 64 * half + 2 * i;
-                    float u, w;
-                    unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, bb), u, w);
-                    u = ex2(u);
-                    w = ex2(w);
-                    l2[i & 1] = add2(l2[i & 1], pair(u, w));
-                    p[i] = pack_bf16(u, w);
-                }
-                tst32(ts + 32 * half, p);
-            }
-            tst_wait();
-            fence_before();
-            bar_arrive(&B.p_full[x]);
-        }
-        if (last > first) {
-            if (ok) ok = bar_wait(&B.o_full[x], 0, &B.abort);
-            __syncwarp();
-            fence_after();
-            float l0, l1;
-            unpair(add2(l2[0], l2[1]), l0, l1);
-            const float inv = ok ? 1.f / (l0 + l1) : NAN;
-            bf16* o = A.out + (long long)(b + rr) * A.out_stride + h * HD;
-#pragma unroll
-            for (int i = 0; i < HD; i += 32) {
-                uint32_t r[32];
-                tld32(to + i, r);
+                for (int k = 0; k < 4; ++k) tld32(ts + 32 * k, s + 32 * k);
                 tld_wait();
-                if (rr < len) {
+                if (t == last - 1 || (W > 0 && PT_M * t < rr - row + PT_M - W)) {  // masked for some row
+                    const int hi = rr - PT_M * t, lo = W > 0 ? hi - W + 1 : 0;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = pack_bf16(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv);
-                        w.y = pack_bf16(__uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
-                        w.z = pack_bf16(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv);
-                        w.w = pack_bf16(__uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
-                        *reinterpret_cast<uint4*>(o + i + e) = w;
+                    for (int k = 0; k < PT_M; ++k)
+                        if (k > hi || k < lo) s[k] = 0xff800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < PT_M; k += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[k + e]), __uint_as_float(s[k + 4 + e]));
+                const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                if (t == first) {
+                    m = mt;
+                } else {
+                    const bool up = mt > m && !((mt - m) * A.c <= 8.f);
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float a = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - mt) * A.c);
+                        if (up) m = mt;
+                        l2[0] = mul2(l2[0], pair(a, a));
+                        l2[1] = mul2(l2[1], pair(a, a));
+#pragma unroll
+                        for (int k = 0; k < HD; k += 16) {
+                            uint32_t o[16];
+                            tld16(to + k, o);
+                            tld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tst16(to + k, o);
+                        }
                     }
                 }
+                const float base_ = m == -INFINITY ? 0.f : -m * A.c;
+                const uint64_t cc = pair(A.c, A.c), bb = pair(base_, base_);
+#pragma unroll
+                for (int quarter = 0; quarter < 4; ++quarter) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const int e = 32 * quarter + 2 * k;
+                        float u, w;
+                        unpair(fma2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, bb), u, w);
+                        u = ex2(u);
+                        w = ex2(w);
+                        l2[k & 1] = add2(l2[k & 1], pair(u, w));
+                        p[k] = pack_bf16(u, w);
+                    }
+                    tst16(ts + 16 * quarter, p);
+                }
+                tst_wait();
+                fence_before();
+                bar_arrive(&B.p_full[x]);
             }
+            if (last > first) {
+                if (ok) ok = bar_wait(&B.o_full[x], o_par, &B.abort);
+                o_par ^= 1;
+                __syncwarp();
+                fence_after();
+                float l0, l1;
+                unpair(add2(l2[0], l2[1]), l0, l1);
+                const float inv = ok ? 1.f / (l0 + l1) : NAN;
+                const PtWork w = B.work[i & 3];
+                bf16* o = A.out + (long long)(w.b + rr) * A.out_stride + w.h * HD;
+#pragma unroll
+                for (int k = 0; k < HD; k += 32) {
+                    uint32_t r[32];
+                    tld32(to + k, r);
+                    tld_wait();
+                    if (rr < w.len) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 y;
+                            y.x = pack_bf16(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv);
+                            y.y = pack_bf16(__uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
+                            y.z = pack_bf16(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv);
+                            y.w = pack_bf16(__uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(o + k + e) = y;
+                        }
+                    }
+                }
+                fence_before();
+                if (*(volatile int*)&B.cleared[i & 3] && ok) {
+                    __syncwarp();
+                    again<HD>(A, B, i, x, warp & 3);
+                }
+            }
+            done_with_item(B, i);
         }
     }
     fence_before();
@@ -604,23 +791,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         __syncwarp();
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512u));
-    }
-    if (B.cleared) {
-        // rows that see a value that was cleared are computed again
-        const int kv = h / A.g;
-        for (int rr = r0 + warp; rr < min(len, r0 + PT_BLOCK); rr += PT_THREADS / 32) {
-            const int lo = W > 0 ? max(0, rr - W + 1) : 0;
-            bool sees = false;
-            for (int t = max(a0, lo / PT_M); t <= rr / PT_M && !sees; ++t) {
-                if (!edge(t)) continue;
-                for (int j = max(lo, t * PT_M); j <= min(rr, t * PT_M + PT_M - 1); ++j) {
-                    const uint32_t* p = reinterpret_cast<const uint32_t*>(A.v + (long long)(b + j) * A.v_stride + kv * HD);
-                    for (int e = lane; e < HD / 2; e += 32) sees = sees || not_finite2(__ldg(p + e));
-                }
-                sees = __any_sync(0xffffffffu, sees);
-            }
-            if (sees) plain_row<HD>(A, b + rr, h, b + lo);
-        }
     }
 }
 
@@ -652,11 +822,13 @@ int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
     }
     PtArgs A = {cu, (const bf16*)q, (const bf16*)k, (const bf16*)v, (bf16*)out, q_stride, k_stride, v_stride, out_stride,
                 n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
-    const long long blocks = ((long long)n_tokens / PT_BLOCK + n_seqs) * hq;  // at least as many as there are
-    if (blocks > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many tokens and sequences");
-    cudaError_t e = cudaFuncSetAttribute(prompt_mma_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_mma_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e == cudaSuccess) {
-        prompt_mma_kernel<HD><<<(unsigned)blocks, PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);
+        const long long most = ((long long)n_tokens / PT_BLOCK + n_seqs) * hq;  // blocks there can be
+        prompt_mma_kernel<HD><<<(unsigned)(most < sms ? most : sms), PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);
         e = cudaGetLastError();
     }
     return mfs::op_launched(op, e);
