@@ -3,11 +3,18 @@
 //
 // All three filters keep a prefix of the columns ordered by (logit descending,
 // column ascending), so the candidates are {key > tau} and the columns up to
-// `tie` among {key == tau}, and nothing has to be sorted: a boundary is found by
-// histograms of counts and of weights, the first one linear in the distance to
-// the maximum (so that the weights spread over the bins), the next ones over the
-// key range of the bin that holds the boundary.  The token is then found by
-// sums over 128-column segments in column order.
+// `tie` among {key == tau}, and the row is never sorted: a histogram, linear in
+// the distance to the maximum in octaves of the weight, finds the bin that holds
+// a filter's border; only that bin's columns (a few dozen as a rule) are listed
+// and sorted.  The token is then found by sums in column order, first per warp's
+// part of the row, then per piece of that part.
+//
+// A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
+// part of the row in shared memory beside another CTA's, and to use the SMs when
+// there are few rows; the CTAs exchange maxima, histograms, the border's columns
+// and sums through distributed shared memory.  The logits are read from memory
+// once; what bounds the call is the passes over shared memory and the latency of
+// the exchanges.
 //
 // Weights are unsigned fixed point (2^-36 of the maximum's weight), so sums are
 // exact whatever order the atomics take, and the row's token is the same on
@@ -15,32 +22,50 @@
 // sums is made with a bound on that error, and a row in which one falls inside
 // the bound is done again with exponentials of about 2^-40 relative error
 // (pairs of fp32), which decides it.
+#include <cooperative_groups.h>
+
 #include "mfs_ops.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int SR_NT = 512;            // threads per row
+using u64 = unsigned long long;
+using bf16 = __nv_bfloat16;
+
+constexpr int SR_NT = 512;            // threads per CTA
 constexpr int SR_NW = SR_NT / 32;
 constexpr int SR_NB = 1024;           // histogram bins
-constexpr int SR_NSEG = 1024;         // column segments at most
-constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no boundary and no draw
-constexpr int SR_STAGE_COLS = 48 * 1024;  // rows of at most this many columns are kept in shared memory
-using u64 = unsigned long long;
+constexpr int SR_BPT = SR_NB / SR_NT;
+constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
+constexpr int SR_LIST = 1024;         // columns of a border's bin that are sorted at once
+constexpr int SR_MAX_C = 8;           // CTAs per row
+constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
 
-struct SrShared {
-    u64 mass[SR_NB];
-    unsigned count[SR_NB];
-    u64 seg[SR_NSEG];
-    u64 su[SR_NW];
-    float sv[SR_NW];
-    int si[SR_NW];
-    // results of the serial steps
-    int bin, tie, token;
-    unsigned cnt_before, klo, khi;
-    u64 mass_before, mass_upto, total;
-    double err;
+// A pair of fp32 whose sum is the value (error-free sums and products by Dekker and Knuth).
+struct F2 {
+    float h, l;
+};
+
+struct __align__(16) SrShared {
+    unsigned count[SR_NB], lo[SR_NB], hi[SR_NB];  // this CTA's histogram: columns, sums of weights in two words
+    u64 sum[SR_NB];                               // the row's sums of weights
+    unsigned num[SR_NB];                          // and columns
+    u64 list[SR_LIST];                            // key << 32 | ~column of the border's bin
+    u64 ws[SR_NW];
+    float wf[SR_NW];
+    int wi[SR_NW];
+    // one entry per CTA of the row, written by that CTA in every CTA's copy
+    float r_max[SR_MAX_C], r_spread[SR_MAX_C];
+    int r_idx[SR_MAX_C];
+    unsigned r_klo[SR_MAX_C], r_khi[SR_MAX_C];
+    u64 r_sum[SR_MAX_C];
+    // results of a search
+    int where, token, unsure;
+    unsigned listed;
+    u64 before, inside;
     float lmin;
-    int unsure;
+    F2 c;
 };
 
 // larger logit = larger key (NaN columns are never asked for theirs); -0 and +0 are the same logit
@@ -52,10 +77,6 @@ __device__ __forceinline__ unsigned order_key(float x)
 
 __device__ __forceinline__ float key_value(unsigned k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
 
-// A pair of fp32 whose sum is the value (error-free sums and products by Dekker and Knuth).
-struct F2 {
-    float h, l;
-};
 __device__ __forceinline__ F2 two_sum(float a, float b)
 {
     const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
@@ -77,32 +98,26 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
     F2 s = two_sum(a.h, b.h);
     return quick_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
-__device__ __forceinline__ F2 split2(double x)
-{
-    const float h = (float)x;
-    return {h, (float)(x - (double)h)};
-}
+__device__ __forceinline__ constexpr F2 split2(double x) { return {(float)x, (float)(x - (double)(float)x)}; }
 
 struct Weigher {
-    float mx, c;  // maximum; log2(e) / T
-    F2 c2;        // the same as a pair
-    F2 ln2;
-    F2 inv_fact[7];  // 1 / k!
+    float mx;  // the row's maximum
+    F2 c;      // log2(e) / T
 
     // octaves below the maximum's weight
-    __device__ __forceinline__ float octaves(float x) const { return x == mx ? 0.f : (mx - x) * c; }
+    __device__ __forceinline__ float octaves(float x) const { return x == mx ? 0.f : (mx - x) * c.h; }
 
     // weight in units of 2^-36 (fast) or 2^-40 (precise) of the maximum's
     template <bool PRECISE>
-    __device__ __forceinline__ u64 operator()(float x) const
+    __device__ __forceinline__ u64 weight(float x) const
     {
         if (x == mx) return PRECISE ? (1ull << 40) : (1ull << 36);
-        if (!PRECISE) return (u64)__float2ull_rn(exp2f(-(mx - x) * c) * 68719476736.f);
+        if (!PRECISE) return (u64)__float2ull_rn(exp2f(-(mx - x) * c.h) * 68719476736.f);
         // y = (mx - x) * c as a pair, n its nearest integer, 2^-(y - n) by the series of exp
         const F2 d = two_sum(mx, -x);
-        const F2 y = mul2(d, c2);
+        const F2 y = mul2(d, c);
         const float n = rintf(y.h);
-        F2 z = mul2(quick_sum(__fsub_rn(y.h, n), y.l), ln2);  // |z| <= 0.35
+        F2 z = mul2(quick_sum(__fsub_rn(y.h, n), y.l), split2(0.69314718055994530942));  // |z| <= 0.35
         z.h = -z.h;
         z.l = -z.l;
         // terms 7 .. 12 of the series need 24 bits only (the 7th is below 2^-22), the lower ones pairs
@@ -113,25 +128,36 @@ struct Weigher {
         t = fmaf(t, z.h, 1.f / 40320.f);
         t = fmaf(t, z.h, 1.f / 5040.f);
         F2 s = {t, 0.f};
-#pragma unroll
-        for (int k = 6; k >= 0; --k) s = add2(mul2(s, z), inv_fact[k]);
+        s = add2(mul2(s, z), split2(1.0 / 720.0));
+        s = add2(mul2(s, z), split2(1.0 / 120.0));
+        s = add2(mul2(s, z), split2(1.0 / 24.0));
+        s = add2(mul2(s, z), split2(1.0 / 6.0));
+        s = add2(mul2(s, z), split2(0.5));
+        s = add2(mul2(s, z), split2(1.0));
+        s = add2(mul2(s, z), split2(1.0));
         const float up = exp2f(40.f - n);  // an exact power of two
         return (u64)((long long)__float2ull_rn(s.h * up) + __float2ll_rn(s.l * up));
     }
 };
 
-template <typename T>
-struct SrRow {
-    const T* g;
-    const float* staged;  // or nullptr
-    int n;
-    __device__ __forceinline__ float at(int i) const
-    {
-        if (staged) return staged[i];
-        if constexpr (sizeof(T) == 4) return __ldg(g + i);
-        else return __uint_as_float((unsigned)__ldg(reinterpret_cast<const unsigned short*>(g) + i) << 16);
+// f x s for f in [0, 1), rounded down or up, exactly (64-bit floating point is slow here: two products a cycle and SM)
+__device__ __forceinline__ u64 fraction(float f, u64 s, bool up)
+{
+    if (!(f > 0.f)) return 0;
+    const unsigned b = __float_as_uint(f), ex = max(b >> 23, 1u);
+    const u64 m = b >> 23 ? (b & 0x7fffffu) | 0x800000u : b;
+    const unsigned sh = 150 - ex;  // f = m 2^-sh, sh >= 24
+    const u64 lo = m * s, hi = __umul64hi(m, s);
+    u64 r, rest;
+    if (sh < 64) {
+        r = (hi << (64 - sh)) | (lo >> sh);
+        rest = lo << (64 - sh);
+    } else {
+        r = sh < 128 ? hi >> (sh - 64) : 0;
+        rest = lo | (sh < 128 ? hi & ((1ull << (sh - 64)) - 1) : hi);
     }
-};
+    return r + (up && rest);
+}
 
 __device__ __forceinline__ u64 warp_sum(u64 v)
 {
@@ -149,270 +175,279 @@ __device__ __forceinline__ u64 warp_inclusive(u64 v)
     return v;
 }
 
-// Warp 0: the first entry of a[0..m) at which the running sum exceeds `target`, and the sum
-// before it (or m).
+// A CTA's part of a row, in 16-byte vectors of VE elements.  Vector v holds columns c0 + v * VE ..; those outside
+// the part (at the ends, where the row is not 16-byte aligned) read as NaN.
+template <typename T>
+struct Part {
+    static constexpr int VE = 16 / sizeof(T);
+    const T* g;         // column 0 of the row
+    const uint4* kept;  // the vectors in shared memory, or nullptr
+    int lo, hi, c0;     // columns [lo, hi)
+    int nvec, per;      // vectors, and vectors per warp
+
+    __device__ __forceinline__ uint4 fetch(int v) const
+    {
+        const int c = c0 + v * VE;
+        if (c >= lo && c + VE <= hi) return __ldg(reinterpret_cast<const uint4*>(g + c));
+        uint4 r;
+        T e[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            if constexpr (sizeof(T) == 4) e[i] = c + i >= lo && c + i < hi ? __ldg(g + c + i) : __uint_as_float(0x7fc00000u);
+            else e[i] = c + i >= lo && c + i < hi ? g[c + i] : __ushort_as_bfloat16(0x7fc0);
+        }
+        memcpy(&r, e, 16);
+        return r;
+    }
+    __device__ __forceinline__ uint4 vec(int v) const { return kept ? kept[v] : fetch(v); }
+    static __device__ __forceinline__ float elem(const uint4& r, int i)
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w);
+        const unsigned w = (i >> 1) == 0 ? r.x : (i >> 1) == 1 ? r.y : (i >> 1) == 2 ? r.z : r.w;
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+    }
+    // f(column, logit) for the columns of this thread (a warp's vectors are consecutive, and ascend)
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        const int w0 = (threadIdx.x >> 5) * per, w1 = min(nvec, w0 + per);
+        for (int v = w0 + (threadIdx.x & 31); v < w1; v += 32) {
+            const uint4 r = vec(v);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) f(c0 + v * VE + i, elem(r, i));
+        }
+    }
+};
+
+// What the functions below share.
+template <typename T>
+struct Row {
+    Part<T> p;
+    Weigher W;
+    float lmin;  // columns below it are no candidates
+    int C, rank;
+    SrShared* S;
+
+    __device__ __forceinline__ void sync() const
+    {
+        if (C > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    }
+    __device__ __forceinline__ SrShared* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
+    __device__ __forceinline__ int bin(float x) const { return min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1); }
+};
+
+// The first of 1024 values a (in shared memory) at which the running sum, starting at `start`, exceeds target;
+// S->where = its place (or -1), S->before = the sum before it.
 template <typename U>
-__device__ __forceinline__ int warp_find(const U* a, int m, u64 target, u64& before)
-{
-    const int lane = threadIdx.x & 31;
-    u64 run = 0;
-    for (int b0 = 0; b0 < m; b0 += 32) {
-        const u64 v = b0 + lane < m ? (u64)a[b0 + lane] : 0;
-        const u64 inc = warp_inclusive(v);
-        const unsigned hit = __ballot_sync(0xffffffffu, b0 + lane < m && run + inc > target);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            before = run + __shfl_sync(0xffffffffu, inc - v, l);
-            return b0 + l;
-        }
-        run += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    before = run;
-    return m;
-}
-
-// The boundary of the shortest prefix of the candidates' order that holds `target` columns
-// (BY_MASS = false) or weights summing to at least `target`.  On return S->khi is the boundary's key, S->tie the
-// last column taken among those with that key, S->mass_upto the sum up to the boundary and
-// S->unsure is set if the error bound `band` leaves the choice open.  The linear histogram is in
-// S->count / S->mass; it is overwritten.  Every thread calls it.
-template <typename T, bool PRECISE, bool BY_MASS>
-__device__ void find_boundary(const SrRow<T>& row, const Weigher& W, float lmin, u64 target, u64 band, SrShared* S)
+__device__ void block_find(SrShared* S, const U* a, u64 start, u64 target)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto pick_bin = [&]() {  // warp 0
-        u64 before;
-        if (BY_MASS) {
-            const int b = min(warp_find(S->mass, SR_NB, target - 1 - S->mass_before, before), SR_NB - 1);
-            u64 c = 0;
-            for (int i = lane; i < b; i += 32) c += S->count[i];
-            c = warp_sum(c);
-            if (lane == 0) { S->bin = b; S->mass_before += before; S->cnt_before += (unsigned)c; }
-        } else {
-            const int b = min(warp_find(S->count, SR_NB, target - 1 - S->cnt_before, before), SR_NB - 1);
-            u64 c = 0;
-            for (int i = lane; i < b; i += 32) c += S->mass[i];
-            c = warp_sum(c);
-            if (lane == 0) { S->bin = b; S->cnt_before += (unsigned)before; S->mass_before += c; }
-        }
-    };
-    if (tid == 0) { S->cnt_before = 0; S->mass_before = 0; S->klo = 0xffffffffu; S->khi = 0; }
-    __syncthreads();
-    if (warp == 0) pick_bin();
-    __syncthreads();
-    const int bin0 = S->bin;
-    {  // the key range of the bin's columns
-        unsigned lo = 0xffffffffu, hi = 0;
-        for (int i = tid; i < row.n; i += SR_NT) {
-            const float x = row.at(i);
-            if (x >= lmin && min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1) == bin0) {
-                const unsigned k = order_key(x);
-                lo = min(lo, k);
-                hi = max(hi, k);
-            }
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) { atomicMin(&S->klo, lo); atomicMax(&S->khi, hi); }
+    u64 v[SR_BPT], mine = 0;
+#pragma unroll
+    for (int i = 0; i < SR_BPT; ++i) {
+        v[i] = (u64)a[tid * SR_BPT + i];
+        mine += v[i];
     }
+    const u64 inc = warp_inclusive(mine);
+    if (lane == 31) S->ws[warp] = inc;
+    if (tid == 0) S->where = -1;
     __syncthreads();
-    for (;;) {
-        const unsigned klo = S->klo, khi = S->khi;
-        const int bits = 32 - __clz(khi - klo);
-        const int sh = bits > 10 ? bits - 10 : 0;
-        for (int i = tid; i < SR_NB; i += SR_NT) { S->mass[i] = 0; S->count[i] = 0; }
-        __syncthreads();
-        for (int i = tid; i < row.n; i += SR_NT) {
-            const float x = row.at(i);
-            if (!(x >= lmin)) continue;
-            const unsigned k = order_key(x);
-            if (k >= klo && k <= khi) {
-                const unsigned b = (khi - k) >> sh;
-                atomicAdd(&S->count[b], 1u);
-                atomicAdd(&S->mass[b], W.template operator()<PRECISE>(x));
-            }
-        }
-        __syncthreads();
-        if (warp == 0) pick_bin();
-        __syncthreads();
-        if (tid == 0) {
-            const unsigned top = khi - ((unsigned)S->bin << sh);
-            S->khi = top;
-            S->klo = sh == 0 ? top : max(klo, top - ((1u << sh) - 1u));
-        }
-        __syncthreads();
-        if (sh == 0) break;
-    }
-    const unsigned tau = S->khi;
-    const unsigned have = S->count[S->bin];
-    const u64 w = W.template operator()<PRECISE>(key_value(tau));
-    unsigned take;  // columns taken among those with the boundary's key
-    if (BY_MASS) {
-        const u64 r = w ? (target - S->mass_before + w - 1) / w : have;
-        take = (unsigned)min((u64)have, max((u64)1, r));
-    } else {
-        take = min(have, max(1u, (unsigned)(target - S->cnt_before)));
-    }
-    const u64 upto = S->mass_before + (u64)take * w;
-    __syncthreads();
-    if (tid == 0) {
-        S->mass_upto = upto;
-        S->tie = 0x7fffffff;
-        if (BY_MASS && (upto < target + band || (upto > w && upto - w + band >= target))) S->unsure = 1;
-    }
-    if (take < have) {  // the take-th column with that key: counts per segment, in column order
-        const int per = ((row.n + 127) / 128 + SR_NSEG - 1) / SR_NSEG * 128, nseg = (row.n + per - 1) / per;
-        for (int s = warp; s < nseg; s += SR_NW) {
-            unsigned c = 0;
-            const int end = min(row.n, (s + 1) * per);
-            for (int i = s * per + lane; i < end; i += 32) {
-                const float x = row.at(i);
-                c += x >= lmin && order_key(x) == tau;
-            }
-            c = __reduce_add_sync(0xffffffffu, c);
-            if (lane == 0) S->seg[s] = c;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            u64 before;
-            const int s = warp_find(S->seg, nseg, take - 1, before);
-            unsigned left = take - (unsigned)before;
-            const int end = min(row.n, (s + 1) * per);
-            for (int i0 = s * per; i0 < end; i0 += 32) {
-                const int i = i0 + lane;
-                float x = 0.f;
-                if (i < end) x = row.at(i);
-                unsigned m = __ballot_sync(0xffffffffu, i < end && x >= lmin && order_key(x) == tau);
-                const unsigned here = __popc(m);
-                if (here >= left) {
-                    while (--left) m &= m - 1;
-                    if (lane == 0) S->tie = i0 + __ffs(m) - 1;
-                    break;
-                }
-                left -= here;
-            }
+    u64 run = start + inc - mine;
+    for (int w = 0; w < warp; ++w) run += S->ws[w];
+    if (run <= target && run + mine > target) {
+#pragma unroll
+        for (int i = 0; i < SR_BPT; ++i) {
+            if (run <= target && run + v[i] > target) { S->where = tid * SR_BPT + i; S->before = run; }
+            run += v[i];
         }
     }
     __syncthreads();
 }
 
-// One row.  Returns false if an error bound left a choice open (never with PRECISE).
-template <typename T, bool PRECISE>
-__device__ bool sample_row(const SrRow<T>& row, const Weigher& W, float lmin, int top_k, float top_p, float u, SrShared* S)
+// Sums of the first `n` of 1024 values, for all threads.
+template <typename U>
+__device__ u64 block_sum(SrShared* S, const U* a, int n)
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = row.n;
-    unsigned tau = 0;
-    int tie = 0x7fffffff;
-    if (tid == 0) S->unsure = 0;
-    const bool cut_k = top_k > 0 && top_k < n, cut_p = top_p < 1.f;
-    if (cut_k || cut_p) {
-        auto histogram = [&]() {
-            for (int i = tid; i < SR_NB; i += SR_NT) { S->mass[i] = 0; S->count[i] = 0; }
-            __syncthreads();
-            for (int i = tid; i < n; i += SR_NT) {
-                const float x = row.at(i);
-                if (x >= lmin) {
-                    const unsigned k = order_key(x);
-                    if (k > tau || (k == tau && i <= tie)) {
-                        const int b = min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1);
-                        atomicAdd(&S->count[b], 1u);
-                        atomicAdd(&S->mass[b], W.template operator()<PRECISE>(x));
-                    }
-                }
-            }
-            __syncthreads();
-            if (warp == 0) {  // totals, and a bound on the error of any sum of these weights
-                u64 c = 0, m = 0;
-                double e = 0.0;
-                for (int i = lane; i < SR_NB; i += 32) {
-                    c += S->count[i];
-                    m += S->mass[i];
-                    e += (double)S->mass[i] * (double)(i + 1);
-                }
-                c = warp_sum(c);
-                m = warp_sum(m);
-                for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
-                if (lane == 0) { S->cnt_before = (unsigned)c; S->total = m; S->err = e * (SR_REACH / SR_NB); }
-            }
-            __syncthreads();
-        };
-        histogram();
-        u64 total = S->total;
-        if (cut_k && (unsigned)top_k < S->cnt_before) {
-            find_boundary<T, PRECISE, false>(row, W, lmin, (u64)top_k, 0, S);
-            tau = S->khi;
-            tie = S->tie;
-            total = S->mass_upto;
-            __syncthreads();
-            if (cut_p) histogram();
-        }
-        if (cut_p) {
-            const double goal = fmax(0.0, (double)top_p) * (double)total;
-            const u64 band = PRECISE ? 0 : (u64)(2.0 * (1.3e-7 * S->err + 2.5e-7 * (double)total + 0.5 * n)) + 2;
-            const u64 target = max((u64)1, (u64)ceil(goal));
-            __syncthreads();
-            find_boundary<T, PRECISE, true>(row, W, lmin, target, band, S);
-            // the boundary among those of top-k: a tie of its own only if it is the same key
-            const int t2 = S->khi == tau ? min(tie, S->tie) : S->tie;
-            tau = S->khi;
-            tie = t2;
-            __syncthreads();
-        }
-    }
-    // sums of 128-column segments, in column order
-    const int per = ((n + 127) / 128 + SR_NSEG - 1) / SR_NSEG * 128, nseg = (n + per - 1) / per;
-    float spread = 0.f;  // sum of weight x octaves: how exact the weights are
-    for (int s = warp; s < nseg; s += SR_NW) {
-        u64 sum = 0;
-        const int end = min(n, (s + 1) * per);
-        for (int i = s * per + lane; i < end; i += 32) {
-            const float x = row.at(i);
-            if (x >= lmin) {
-                const unsigned k = order_key(x);
-                if (k > tau || (k == tau && i <= tie)) {
-                    const u64 w = W.template operator()<PRECISE>(x);
-                    sum += w;
-                    spread += (float)w * W.octaves(x);
-                }
-            }
-        }
-        sum = warp_sum(sum);
-        if (lane == 0) S->seg[s] = sum;
-    }
-    for (int o = 16; o; o >>= 1) spread += __shfl_xor_sync(0xffffffffu, spread, o);
-    if (lane == 0) S->sv[warp] = spread;
+    const int tid = threadIdx.x;
+    u64 mine = 0;
+#pragma unroll
+    for (int i = 0; i < SR_BPT; ++i)
+        if (tid * SR_BPT + i < n) mine += (u64)a[tid * SR_BPT + i];
+    mine = warp_sum(mine);
     __syncthreads();
+    if ((tid & 31) == 0) S->ws[tid >> 5] = mine;
+    __syncthreads();
+    u64 t = 0;
+    for (int w = 0; w < SR_NW; ++w) t += S->ws[w];
+    __syncthreads();
+    return t;
+}
+
+// Histogram of the columns that `put(column, x, bin)` names a bin for (-1: none), over all CTAs of the row, into S->num
+// and S->sum.
+template <bool PRECISE, typename T, typename F>
+__device__ void histogram(const Row<T>& R, bool counts, bool sums, F put)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < SR_NB; i += SR_NT) S->count[i] = S->lo[i] = S->hi[i] = 0;
+    __syncthreads();
+    R.p.each([&](int col, float x) {
+        if (!(x >= R.lmin)) return;
+        const int b = put(col, x);
+        if (b < 0) return;
+        if (counts) atomicAdd(&S->count[b], 1u);
+        if (sums) {
+            const u64 w = R.W.template weight<PRECISE>(x);
+            const unsigned wl = (unsigned)w;
+            if (w) {
+                const unsigned old = atomicAdd(&S->lo[b], wl);
+                const unsigned wh = (unsigned)(w >> 32) + (old + wl < old);
+                if (wh) atomicAdd(&S->hi[b], wh);
+            }
+        }
+    });
+    R.sync();
+    for (int i = tid; i < SR_NB; i += SR_NT) {
+        u64 m = 0;
+        unsigned n = 0;
+        for (int r = 0; r < R.C; ++r) {
+            const SrShared* o = R.of(r);
+            if (counts) n += o->count[i];
+            if (sums) m += ((u64)o->hi[i] << 32) + o->lo[i];
+        }
+        S->num[i] = n;
+        S->sum[i] = m;
+    }
+    R.sync();  // the others' histograms have been read
+}
+
+// The columns that `take(x)` names, of all CTAs, into S->list in the candidates' order; their number (more than
+// SR_LIST: the list is not complete).
+template <typename T, typename F>
+__device__ unsigned list_sorted(const Row<T>& R, F take)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x;
+    if (tid == 0) S->listed = 0;
+    R.sync();
+    R.p.each([&](int col, float x) {
+        if (!(x >= R.lmin) || !take(x)) return;
+        const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
+        for (int r = 0; r < R.C; ++r) {
+            SrShared* o = R.of(r);
+            const unsigned at = atomicAdd(&o->listed, 1u);
+            if (at < SR_LIST) o->list[at] = e;
+        }
+    });
+    R.sync();
+    const unsigned n = S->listed;
+    if (n > SR_LIST || n <= 1) return n;
+    if (n <= 256) {  // each entry's place is the number of larger ones
+        u64 mine = 0;
+        unsigned at = 0;
+        if (tid < n) {
+            mine = S->list[tid];
+            for (unsigned i = 0; i < n; ++i) at += S->list[i] > mine;
+        }
+        __syncthreads();
+        if (tid < n) S->list[at] = mine;
+        __syncthreads();
+        return n;
+    }
+    unsigned full = 512;
+    while (full < n) full *= 2;
+    for (unsigned i = n + tid; i < full; i += SR_NT) S->list[i] = 0;
+    __syncthreads();
+    for (unsigned k = 2; k <= full; k *= 2)
+        for (unsigned j = k / 2; j; j /= 2) {
+            for (unsigned i = tid; i < full / 2; i += SR_NT) {
+                const unsigned a = 2 * i - (i & (j - 1)), b = a + j;
+                const u64 x = S->list[a], y = S->list[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    S->list[a] = y;
+                    S->list[b] = x;
+                }
+            }
+            __syncthreads();
+        }
+    return n;
+}
+
+// The first column, in ascending order over the whole row, at which the running sum of wt(column, x) exceeds
+// goal(total): only the CTA that holds it returns true, with S->where = the column, S->before = the sum before it and
+// S->inside = its weight.
+template <typename T, typename F, typename G>
+__device__ bool find_in_order(const Row<T>& R, F wt, G goal)
+{
+    SrShared* S = R.S;
+    const Part<T>& P = R.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    u64 mine = 0;
+    P.each([&](int col, float x) { mine += wt(col, x); });
+    mine = warp_sum(mine);
+    __syncthreads();
+    if (lane == 0) S->ws[warp] = mine;
+    __syncthreads();
+    u64 here = 0;
+    for (int w = 0; w < SR_NW; ++w) here += S->ws[w];
+    if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
+    R.sync();
+    u64 run = 0, total = 0;
+    for (int r = 0; r < R.C; ++r) {
+        if (r < R.rank) run += S->r_sum[r];
+        total += S->r_sum[r];
+    }
+    const u64 target = goal(total);
+    if (!(run <= target && run + here > target)) return false;
+    int w = 0;
+    while (run + S->ws[w] <= target) run += S->ws[w++];
+    // the warp's vectors again, in pieces, one per warp
+    const int v0 = w * P.per, v1 = min(P.nvec, v0 + P.per), piece = (P.per + SR_NW - 1) / SR_NW;
+    mine = 0;
+    for (int v = v0 + warp * piece + lane; v < min(v1, v0 + (warp + 1) * piece); v += 32) {
+        const uint4 r = P.vec(v);
+#pragma unroll
+        for (int i = 0; i < P.VE; ++i) mine += wt(P.c0 + v * P.VE + i, P.elem(r, i));
+    }
+    mine = warp_sum(mine);
+    __syncthreads();
+    if (lane == 0) S->ws[warp] = mine;
+    __syncthreads();
+    w = 0;
+    while (run + S->ws[w] <= target) run += S->ws[w++];
     if (warp == 0) {
-        u64 total = 0;
-        for (int s = lane; s < nseg; s += 32) total += S->seg[s];
-        total = warp_sum(total);
-        spread = 0.f;
-        for (int w = 0; w < SR_NW; ++w) spread += S->sv[w];
-        const double goal = fmax(0.0, (double)u) * (double)total;
-        const u64 target = goal < (double)total ? min((u64)goal, total - 1) : total - 1;
-        const u64 band = PRECISE ? 0 : (u64)(2.0 * (1.4e-7 * (double)spread + 2.5e-7 * (double)total + 0.5 * n)) + 2;
-        u64 run;
-        const int s = warp_find(S->seg, nseg, target, run);
-        const int end = min(n, (s + 1) * per);
-        for (int i0 = s * per; i0 < end; i0 += 32) {
-            const int i = i0 + lane;
-            u64 w = 0;
-            if (i < end) {
-                const float x = row.at(i);
-                if (x >= lmin) {
-                    const unsigned k = order_key(x);
-                    if (k > tau || (k == tau && i <= tie)) w = W.template operator()<PRECISE>(x);
+        const int p0 = v0 + w * piece, p1 = min(v1, p0 + piece);
+        for (int b = p0; b < p1; b += 32) {
+            const int v = b + lane;
+            u64 e[P.VE], sum = 0;
+#pragma unroll
+            for (int i = 0; i < P.VE; ++i) e[i] = 0;
+            if (v < p1) {
+                const uint4 r = P.vec(v);
+#pragma unroll
+                for (int i = 0; i < P.VE; ++i) {
+                    e[i] = wt(P.c0 + v * P.VE + i, P.elem(r, i));
+                    sum += e[i];
                 }
             }
-            const u64 inc = warp_inclusive(w);
+            const u64 inc = warp_inclusive(sum);
             const unsigned hit = __ballot_sync(0xffffffffu, run + inc > target);
             if (hit) {
-                const int l = __ffs(hit) - 1;
-                if (lane == l) {
-                    S->token = i;
-                    // the chosen column's weight spans [run + inc - w, run + inc)
-                    if (run + inc <= target + band || (run + inc - w > 0 && run + inc - w + band > target)) S->unsure = 1;
+                if (lane == __ffs(hit) - 1) {
+                    u64 at = run + inc - sum;
+                    bool found = false;
+#pragma unroll
+                    for (int i = 0; i < P.VE; ++i) {
+                        if (!found && at + e[i] > target) {
+                            found = true;
+                            S->where = P.c0 + v * P.VE + i;
+                            S->before = at;
+                            S->inside = e[i];
+                        }
+                        at += e[i];
+                    }
                 }
                 break;
             }
@@ -420,57 +455,311 @@ __device__ bool sample_row(const SrRow<T>& row, const Weigher& W, float lmin, in
         }
     }
     __syncthreads();
-    return PRECISE || S->unsure == 0;
+    return true;
+}
+
+// How far a comparison of two sums of fast weights may be off: `spread` = sum of weight x octaves (an exponent's error
+// is 3 x 2^-24 of it, in octaves), 2 ulp of the exponential, half a unit per column; twice that for the two sides.
+template <typename T>
+__device__ __forceinline__ u64 error_band(float spread, u64 total, const Row<T>& R)
+{
+    return (u64)(2.f * (1.4e-7f * spread + 2.6e-7f * (float)total + 0.51f * (float)(R.p.hi - R.p.lo) * (float)R.C)) + 2;
+}
+
+struct Border {
+    unsigned tau;  // the candidates: keys above tau, and those equal to it up to column tie
+    int tie;
+    u64 mass;      // their sum of weights (if the histogram has sums)
+};
+
+// The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`;
+// S->num / S->sum hold the linear histogram and keep it unless the border's bin is too full to list.
+template <bool PRECISE, bool BY_MASS, typename T>
+__device__ Border find_border(const Row<T>& R, u64 target, u64 band)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x;
+    if (BY_MASS) block_find(S, S->sum, 0, target - 1);
+    else block_find(S, S->num, 0, target - 1);
+    int b = S->where;
+    u64 before = S->before;                                  // of what is counted
+    u64 mass = BY_MASS ? before : block_sum(S, S->sum, b);   // weights before the bin
+    u64 count = BY_MASS ? 0 : before;
+    unsigned klo = 0, khi = 0xffffffffu;
+    bool keyed = false;
+    unsigned n = list_sorted(R, [&](float x) { return R.bin(x) == b; });
+    while (n > SR_LIST) {
+        // too many: split the bin's range of keys, down to one key
+        if (!keyed) {
+            unsigned lo = 0xffffffffu, hi = 0;
+            R.p.each([&](int, float x) {
+                if (x >= R.lmin && R.bin(x) == b) {
+                    const unsigned k = order_key(x);
+                    lo = min(lo, k);
+                    hi = max(hi, k);
+                }
+            });
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (tid == 0) { S->r_klo[R.rank] = 0xffffffffu; S->r_khi[R.rank] = 0; }
+            __syncthreads();
+            if ((tid & 31) == 0) { atomicMin(&S->r_klo[R.rank], lo); atomicMax(&S->r_khi[R.rank], hi); }
+            __syncthreads();
+            if (tid < R.C) {
+                R.of(tid)->r_klo[R.rank] = S->r_klo[R.rank];
+                R.of(tid)->r_khi[R.rank] = S->r_khi[R.rank];
+            }
+            R.sync();
+            klo = 0xffffffffu;
+            khi = 0;
+            for (int r = 0; r < R.C; ++r) {
+                klo = min(klo, S->r_klo[r]);
+                khi = max(khi, S->r_khi[r]);
+            }
+            keyed = true;
+        }
+        if (klo == khi) break;
+        const int bits = 32 - __clz(khi - klo), sh = bits > 10 ? bits - 10 : 0;
+        histogram<PRECISE>(R, true, true, [&](int, float x) {
+            const unsigned k = order_key(x);
+            return k >= klo && k <= khi ? (int)((khi - k) >> sh) : -1;
+        });
+        if (BY_MASS) block_find(S, S->sum, mass, target - 1);
+        else block_find(S, S->num, count, target - 1);
+        const int sub = S->where;
+        const u64 counted = S->before;
+        n = S->num[sub];
+        if (BY_MASS) {
+            mass = counted;
+        } else {
+            count = counted;
+            mass += block_sum(S, S->sum, sub);
+        }
+        const unsigned top = khi - ((unsigned)sub << sh);
+        klo = max(klo, sh ? top - ((1u << sh) - 1u) : top);
+        khi = top;
+        __syncthreads();
+        if (n <= SR_LIST) n = list_sorted(R, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
+    }
+    Border B;
+    u64 w = 0;  // the border column's own weight
+    if (n <= SR_LIST) {
+        u64 v[SR_BPT], mine = 0;
+#pragma unroll
+        for (int i = 0; i < SR_BPT; ++i) {
+            const int at = tid * SR_BPT + i;
+            v[i] = at < (int)n ? R.W.template weight<PRECISE>(key_value((unsigned)(S->list[at] >> 32))) : 0;
+            mine += v[i];
+        }
+        const u64 inc = warp_inclusive(mine);
+        if ((tid & 31) == 31) S->ws[tid >> 5] = inc;
+        if (tid == 0) S->where = 0;
+        __syncthreads();
+        u64 run = mass + inc - mine;
+        for (int q = 0; q < (tid >> 5); ++q) run += S->ws[q];
+#pragma unroll
+        for (int i = 0; i < SR_BPT; ++i) {
+            const int at = tid * SR_BPT + i;
+            const bool last = BY_MASS ? run < target && run + v[i] >= target : (u64)at == target - 1 - count;
+            if (last && at < (int)n) { S->where = at; S->before = run; S->inside = v[i]; }
+            run += v[i];
+        }
+        __syncthreads();
+        const u64 e = S->list[S->where];
+        B.tau = (unsigned)(e >> 32);
+        B.tie = (int)~(unsigned)e;
+        w = S->inside;
+        B.mass = S->before + w;
+    } else {
+        // one key, many columns: the last of them taken, in column order
+        w = R.W.template weight<PRECISE>(key_value(klo));
+        u64 take;
+        if (BY_MASS) take = w ? min((u64)n, max((u64)1, (target - mass + w - 1) / w)) : n;
+        else take = target - count;
+        B.tau = klo;
+        B.mass = mass + take * w;
+        const bool mine = find_in_order(R, [&](int, float x) { return (u64)(x >= R.lmin && order_key(x) == klo); },
+                                        [&](u64) { return take - 1; });
+        const int at = mine ? S->where : -1;
+        R.sync();
+        if (mine && tid < R.C) R.of(tid)->token = at;
+        R.sync();
+        B.tie = S->token;
+    }
+    // the border is certain if no error of the sums can move it
+    if (BY_MASS && (B.mass < target + band || (B.mass > w && B.mass - w + band >= target)) && tid == 0) S->unsure = 1;
+    __syncthreads();
+    return B;
+}
+
+// The token of the row into `token` by the CTA that finds it.  False if an error bound left a choice open (never with PRECISE).
+template <bool PRECISE, typename T>
+__device__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, int32_t* token)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x;
+    unsigned tau = 0;
+    int tie = 0x7fffffff;
+    if (tid == 0) S->unsure = 0;
+    const bool cut_k = top_k > 0, cut_p = top_p < 1.f;
+    if (cut_k || cut_p) {
+        histogram<PRECISE>(R, cut_k, cut_p, [&](int, float x) { return R.bin(x); });
+        u64 total = 0;
+        bool whole = true;  // the histogram still holds the row
+        if (cut_k && block_sum(S, S->num, SR_NB) > (u64)top_k) {
+            const Border B = find_border<PRECISE, false>(R, (u64)top_k, 0);
+            tau = B.tau;
+            tie = B.tie;
+            total = B.mass;
+            whole = false;
+        }
+        if (cut_p) {
+            if (!whole)  // the candidates' own histogram
+                histogram<PRECISE>(R, false, true, [&](int col, float x) {
+                    const unsigned k = order_key(x);
+                    return k > tau || (k == tau && col <= tie) ? R.bin(x) : -1;
+                });
+            total = block_sum(S, S->sum, SR_NB);
+            // a bound on the error of any sum of these weights
+            u64 band = 0;
+            if (!PRECISE) {
+                float f = 0.f, e = 0.f;
+#pragma unroll
+                for (int i = 0; i < SR_BPT; ++i) f += (float)S->sum[tid * SR_BPT + i] * (float)(tid * SR_BPT + i + 1);
+                for (int o = 16; o; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+                if ((tid & 31) == 0) S->wf[tid >> 5] = f;
+                __syncthreads();
+                for (int w = 0; w < SR_NW; ++w) e += S->wf[w];
+                band = error_band(e * (SR_REACH / SR_NB), total, R);
+            }
+            const u64 target = max((u64)1, fraction(top_p, total, true));
+            const Border B = find_border<PRECISE, true>(R, target, band);
+            tie = B.tau == tau ? min(tie, B.tie) : B.tie;
+            tau = B.tau;
+        }
+    }
+    // the draw, in column order
+    float spread = 0.f;  // sum of weight x octaves: how exact the weights are
+    const auto wt = [&](int col, float x) {
+        if (!(x >= R.lmin)) return (u64)0;
+        const unsigned k = order_key(x);
+        if (!(k > tau || (k == tau && col <= tie))) return (u64)0;
+        const u64 w = R.W.template weight<PRECISE>(x);
+        if (!PRECISE) spread += (float)w * R.W.octaves(x);
+        return w;
+    };
+    u64 target = 0, total = 0;
+    const bool mine = find_in_order(R, wt, [&](u64 sum) {
+        total = sum;
+        target = u < 1.f || !(u == u) ? fraction(u, sum, false) : sum - 1;
+        if (!PRECISE) {  // the spread of all CTAs
+            for (int o = 16; o; o >>= 1) spread += __shfl_xor_sync(0xffffffffu, spread, o);
+            if ((tid & 31) == 0) S->wf[tid >> 5] = spread;
+            __syncthreads();
+            float f = 0.f;
+            for (int w = 0; w < SR_NW; ++w) f += S->wf[w];
+            if (tid < R.C) R.of(tid)->r_spread[R.rank] = f;
+        }
+        return target;
+    });
+    R.sync();
+    if (mine && tid == 0) {
+        if (!PRECISE) {
+            float f = 0.f;
+            for (int r = 0; r < R.C; ++r) f += S->r_spread[r];
+            const u64 band = error_band(f, total, R);
+            // the chosen column's weight spans [before, before + inside)
+            if (S->before + S->inside <= target + band || (S->before > 0 && S->before + band > target))
+                for (int r = 0; r < R.C; ++r) R.of(r)->unsure = 1;
+        }
+        *token = S->where;
+    }
+    R.sync();
+    const bool open = S->unsure != 0;
+    __syncthreads();  // read by all before another pass clears it
+    return PRECISE || !open;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(SR_NT) sample_rows_kernel(const T* __restrict__ logits, int cols, long long ld,
-                                                            const float* __restrict__ temperature,
-                                                            const int32_t* __restrict__ top_k,
-                                                            const float* __restrict__ top_p,
-                                                            const float* __restrict__ min_p,
-                                                            const float* __restrict__ uniforms, int32_t* __restrict__ tokens,
-                                                            int stage)
+__global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restrict__ logits, int cols, long long ld,
+                                                               const float* __restrict__ temperature,
+                                                               const int32_t* __restrict__ top_k,
+                                                               const float* __restrict__ top_p,
+                                                               const float* __restrict__ min_p,
+                                                               const float* __restrict__ uniforms, int32_t* __restrict__ tokens,
+                                                               int C, int stage)
 {
     extern __shared__ __align__(16) char sr_raw[];
     SrShared* S = reinterpret_cast<SrShared*>(sr_raw);
-    float* st = reinterpret_cast<float*>(sr_raw + sizeof(SrShared));
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    SrRow<T> row{logits + (long long)r * ld, nullptr, cols};
+    const int r = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float T_ = temperature ? __ldg(temperature + r) : 1.f;
+    const int k = top_k ? __ldg(top_k + r) : 0;
+    const float p = top_p ? __ldg(top_p + r) : 1.f, mp = min_p ? __ldg(min_p + r) : 0.f, u = __ldg(uniforms + r);
+    Row<T> R;
+    constexpr int VE = Part<T>::VE;
+    R.C = C;
+    R.rank = rank;
+    R.S = S;
+    R.p.g = logits + (long long)r * ld;
+    const int each = (cols + C - 1) / C;
+    R.p.lo = min(cols, rank * each);
+    R.p.hi = min(cols, R.p.lo + each);
+    R.p.c0 = R.p.lo - (int)((reinterpret_cast<uintptr_t>(R.p.g + R.p.lo) & 15u) / sizeof(T));
+    R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
+    R.p.per = (R.p.nvec + SR_NW - 1) / SR_NW;
+    R.p.kept = nullptr;
+    uint4* kept = reinterpret_cast<uint4*>(sr_raw + sizeof(SrShared));
+    // the maximum and its lowest column, and the row's part into shared memory
     float v = -INFINITY;
     int idx = 0x7fffffff;
-    for (int i = tid; i < cols; i += SR_NT) {
-        const float x = row.at(i);
-        if (stage) st[i] = x;
-        if (x > v || (x == v && i < idx)) { v = x; idx = i; }
+    {
+        const int w0 = warp * R.p.per, w1 = min(R.p.nvec, w0 + R.p.per);
+        constexpr int DEEP = 8;
+        for (int b = w0 + lane; b < w1; b += 32 * DEEP) {
+            uint4 x[DEEP];
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i)
+                if (b + 32 * i < w1) x[i] = R.p.fetch(b + 32 * i);
+#pragma unroll
+            for (int i = 0; i < DEEP; ++i)
+                if (b + 32 * i < w1) {
+                    if (stage) kept[b + 32 * i] = x[i];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float y = R.p.elem(x[i], e);
+                        const int c = R.p.c0 + (b + 32 * i) * VE + e;
+                        if (y > v || (y == v && c < idx)) { v = y; idx = c; }
+                    }
+                }
+        }
     }
     for (int o = 16; o; o >>= 1) {
         const float ov = __shfl_xor_sync(0xffffffffu, v, o);
         const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
         if (ov > v || (ov == v && oi < idx)) { v = ov; idx = oi; }
     }
-    if (lane == 0) { S->sv[warp] = v; S->si[warp] = idx; }
+    if (lane == 0) { S->wf[warp] = v; S->wi[warp] = idx; }
     __syncthreads();
-    v = S->sv[0];
-    idx = S->si[0];
+    v = S->wf[0];
+    idx = S->wi[0];
     for (int w = 1; w < SR_NW; ++w)
-        if (S->sv[w] > v || (S->sv[w] == v && S->si[w] < idx)) { v = S->sv[w]; idx = S->si[w]; }
-    __syncthreads();
-    if (stage) row.staged = st;
-    const float T_ = temperature ? temperature[r] : 1.f;
-    const int k = top_k ? top_k[r] : 0;
+        if (S->wf[w] > v || (S->wf[w] == v && S->wi[w] < idx)) { v = S->wf[w]; idx = S->wi[w]; }
+    if (C > 1) {
+        cg::this_cluster().sync();  // every CTA of the row has started
+        if (tid < C) { R.of(tid)->r_max[rank] = v; R.of(tid)->r_idx[rank] = idx; }
+        cg::this_cluster().sync();
+        for (int q = 0; q < C; ++q)
+            if (S->r_max[q] > v || (S->r_max[q] == v && S->r_idx[q] < idx)) { v = S->r_max[q]; idx = S->r_idx[q]; }
+    }
+    if (stage) R.p.kept = kept;
     if (!(T_ > 0.f) || v == -INFINITY || k == 1) {
-        if (tid == 0) tokens[r] = idx == 0x7fffffff ? 0 : idx;
+        if (tid == 0 && rank == 0) tokens[r] = idx == 0x7fffffff ? 0 : idx;
         return;
     }
-    const float p = top_p ? top_p[r] : 1.f, mp = min_p ? min_p[r] : 0.f;
-    Weigher W;
-    W.mx = v;
-    const double c = fmin(1.4426950408889634 / (double)T_, 1e30);
-    W.c2 = split2(c);
-    W.c = W.c2.h;
-    if (tid == 0) {
-        float lmin = fmaxf(v - SR_REACH / W.c, -3.402823466e38f);
+    R.W.mx = v;
+    if (tid == 0) {  // the row's 64-bit arithmetic
+        S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
+        float lmin = fmaxf(v - SR_REACH / S->c.h, -3.402823466e38f);
         if (mp > 0.f) {  // the least logit l with exp((l - max) / T) >= min_p
             const double reach = mp >= 1.f ? 0.0 : -(double)T_ * log((double)mp);
             float l = (float)((double)v - reach);
@@ -485,34 +774,44 @@ __global__ void __launch_bounds__(SR_NT) sample_rows_kernel(const T* __restrict_
         S->lmin = v == INFINITY ? INFINITY : lmin;
     }
     __syncthreads();
-    const float lmin = S->lmin, u = uniforms[r];
+    R.lmin = S->lmin;
+    R.W.c = S->c;
     const float pp = p == p ? p : 1.f;
-    if (!sample_row<T, false>(row, W, lmin, k, pp, u, S)) {
-        __syncthreads();
-        W.ln2 = split2(0.69314718055994530942);
-        double f = 1.0;
-        for (int i = 0; i < 7; ++i) {
-            W.inv_fact[i] = split2(1.0 / f);
-            f *= i + 1;
-        }
-        sample_row<T, true>(row, W, lmin, k, pp, u, S);
-    }
-    if (tid == 0) tokens[r] = S->token;
+    if (!sample_row<false>(R, k, pp, u, tokens + r)) sample_row<true>(R, k, pp, u, tokens + r);
 }
 
 template <typename T>
 int launch(const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
            const float* top_p, const float* min_p, const float* uniforms, int32_t* tokens, cudaStream_t st)
 {
-    const bool stage = cols <= SR_STAGE_COLS;
-    const size_t smem = sizeof(SrShared) + (stage ? (size_t)cols * 4 : 0);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
-    }
-    sample_rows_kernel<T><<<rows, SR_NT, smem, st>>>((const T*)logits, cols, ld, temperature, top_k, top_p, min_p, uniforms,
-                                                    tokens, stage);
-    return mfs::op_launched("sample_rows", cudaGetLastError());
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // CTAs per row: parts of at most 64 KB, so that two CTAs share an SM, and more where rows leave SMs empty
+    // and a part keeps at least 4096 columns
+    int C = 1;
+    while (C < SR_MAX_C && ((long long)cols * sizeof(T) / C > 64 * 1024 || ((long long)rows * C * 2 <= sms && cols / C >= 8192))) C *= 2;
+    const long long part = ((long long)cols + C - 1) / C * sizeof(T) + 32;
+    const bool stage = part <= SR_STAGE_BYTES;
+    const size_t smem = sizeof(SrShared) + (stage ? (size_t)part : 0);
+    auto kernel = sample_rows_kernel<T>;
+    if (e == cudaSuccess && smem > 48 * 1024)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(sizeof(SrShared) + SR_STAGE_BYTES));
+    if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
+    if ((long long)rows * C > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, "sample_rows", "too many rows");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(SR_NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return mfs::op_launched("sample_rows", cudaLaunchKernelEx(&cfg, kernel, (const T*)logits, cols, ld, temperature, top_k, top_p, min_p,
+                                                              uniforms, tokens, C, (int)stage));
 }
 
 }  // namespace
@@ -529,7 +828,6 @@ extern "C" int mfs_sample_rows(const void* logits, int dtype, int rows, int cols
     if (!logits || !uniforms || !tokens) return mfs::op_fail(MFS_E_ARG, op, "null logits, uniforms or tokens");
     if ((uintptr_t)logits % (dtype == MFS_DTYPE_BF16 ? 2 : 4)) return mfs::op_fail(MFS_E_ARG, op, "misaligned logits");
     cudaStream_t st = (cudaStream_t)cuda_stream;
-    return dtype == MFS_DTYPE_BF16
-               ? launch<__nv_bfloat16>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st)
-               : launch<float>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
+    return dtype == MFS_DTYPE_BF16 ? launch<bf16>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st)
+                                   : launch<float>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
 }
