@@ -2,26 +2,29 @@
 // after temperature, min-p, top-k and top-p.
 //
 // All three filters keep a prefix of the columns ordered by (logit descending,
-// column ascending), so the candidates are {key > tau} and the columns up to
-// `tie` among {key == tau}, and the row is never sorted: a histogram, linear in
-// the distance to the maximum in octaves of the weight, finds the bin that holds
-// a filter's border; only that bin's columns (a few dozen as a rule) are listed
-// and sorted.  The token is then found by sums in column order, first per warp's
-// part of the row, then per piece of that part.
+// column ascending), so the candidates are {logit > tau} and the columns up to
+// `tie` among {logit == tau}, and the row is never sorted.  Where few columns can
+// be candidates they are listed and sorted: those above the k-th largest of the
+// threads' own maxima (at least k columns reach it, and rarely many more), or above
+// min-p's bound.  Otherwise a histogram, linear in the distance to the maximum in
+// octaves of the weight, finds the bin that holds a filter's border, and only that
+// bin's columns are sorted.  The token is then found by sums in column order, first
+// per warp's part of the row, then per piece of that part.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
 // part of the row in shared memory beside another CTA's, and to use the SMs when
-// there are few rows; the CTAs exchange maxima, histograms, the border's columns
-// and sums through distributed shared memory.  The logits are read from memory
-// once; what bounds the call is the passes over shared memory and the latency of
-// the exchanges.
+// there are few rows; the CTAs exchange maxima, histograms, lists and sums through
+// distributed shared memory.  The logits are read from memory once; what bounds
+// the call is the passes over shared memory and the latency of the exchanges.
 //
-// Weights are unsigned fixed point (2^-36 of the maximum's weight), so sums are
-// exact whatever order the atomics take, and the row's token is the same on
-// every run.  A weight carries the error of its fp32 exponent; each comparison of
-// sums is made with a bound on that error, and a row in which one falls inside
-// the bound is done again with exponentials of about 2^-40 relative error
-// (pairs of fp32), which decides it.
+// Weights are unsigned fixed point (2^scale for the maximum's), so sums are exact
+// whatever order the atomics take, and the row's token is the same on every run.
+// A weight is 2^-y = 2^-n 2^-(i/64) 2^-r with y a pair of fp32, a table for i and
+// three terms for |r| < 1/128: 2^-29 relative.  Each comparison of sums is made
+// with a bound on that error, and a row in which one falls inside the bound is done
+// again with exponentials of about 2^-40 relative error (pairs of fp32), which
+// decides it.  64-bit floating point, two products a cycle and SM here, is kept to
+// one thread per CTA; fractions of sums are taken in 128-bit integers.
 #include <cooperative_groups.h>
 
 #include "mfs_ops.cuh"
@@ -38,7 +41,7 @@ constexpr int SR_NW = SR_NT / 32;
 constexpr int SR_NB = 1024;           // histogram bins
 constexpr int SR_BPT = SR_NB / SR_NT;
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
-constexpr int SR_LIST = 1024;         // columns of a border's bin that are sorted at once
+constexpr int SR_LIST = 1024;         // columns that are sorted at once
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
 
@@ -51,12 +54,13 @@ struct __align__(16) SrShared {
     unsigned count[SR_NB], lo[SR_NB], hi[SR_NB];  // this CTA's histogram: columns, sums of weights in two words
     u64 sum[SR_NB];                               // the row's sums of weights
     unsigned num[SR_NB];                          // and columns
-    u64 list[SR_LIST];                            // key << 32 | ~column of the border's bin
+    u64 list[SR_LIST];                            // key << 32 | ~column
+    uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
     u64 ws[SR_NW];
     float wf[SR_NW];
     int wi[SR_NW];
     // one entry per CTA of the row, written by that CTA in every CTA's copy
-    float r_max[SR_MAX_C], r_spread[SR_MAX_C];
+    float r_max[SR_MAX_C];
     int r_idx[SR_MAX_C];
     unsigned r_klo[SR_MAX_C], r_khi[SR_MAX_C];
     u64 r_sum[SR_MAX_C];
@@ -64,9 +68,26 @@ struct __align__(16) SrShared {
     int where, token, unsure;
     unsigned listed;
     u64 before, inside;
+    // the row's constants
     float lmin;
     F2 c;
 };
+
+struct Table {
+    uint2 at[64];
+};
+constexpr Table make_table()
+{
+    Table t = {};
+    double x = 2147483648.0;
+    for (int i = 0; i < 64; ++i) {
+        t.at[i].x = (unsigned)(x + 0.5);
+        t.at[i].y = 0;
+        x *= 0.989228013193975484129124959065583667774674335384985;  // 2^(-1/64)
+    }
+    return t;
+}
+__constant__ Table sr_table = make_table();
 
 // larger logit = larger key (NaN columns are never asked for theirs); -0 and +0 are the same logit
 __device__ __forceinline__ unsigned order_key(float x)
@@ -100,47 +121,61 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
 }
 __device__ __forceinline__ constexpr F2 split2(double x) { return {(float)x, (float)(x - (double)(float)x)}; }
 
+// 2^(scale - y), y = (mx - x) c, to about 2^-40 of it.
+__device__ __noinline__ u64 precise_weight(float x, float mx, F2 c, int scale)
+{
+    const F2 y = mul2(two_sum(mx, -x), c);
+    const float n = rintf(y.h);
+    F2 z = mul2(quick_sum(__fsub_rn(y.h, n), y.l), split2(0.69314718055994530942));  // |z| <= 0.35
+    z.h = -z.h;
+    z.l = -z.l;
+    // the series of exp: terms 7 .. 12 need 24 bits only (the 7th is below 2^-22), the lower ones pairs
+    float t = 1.f / 479001600.f;
+    t = fmaf(t, z.h, 1.f / 39916800.f);
+    t = fmaf(t, z.h, 1.f / 3628800.f);
+    t = fmaf(t, z.h, 1.f / 362880.f);
+    t = fmaf(t, z.h, 1.f / 40320.f);
+    t = fmaf(t, z.h, 1.f / 5040.f);
+    F2 s = {t, 0.f};
+    s = add2(mul2(s, z), split2(1.0 / 720.0));
+    s = add2(mul2(s, z), split2(1.0 / 120.0));
+    s = add2(mul2(s, z), split2(1.0 / 24.0));
+    s = add2(mul2(s, z), split2(1.0 / 6.0));
+    s = add2(mul2(s, z), split2(0.5));
+    s = add2(mul2(s, z), split2(1.0));
+    s = add2(mul2(s, z), split2(1.0));
+    const float up = exp2f((float)scale - n);  // an exact power of two
+    return (u64)((long long)__float2ull_rn(s.h * up) + __float2ll_rn(s.l * up));
+}
+
 struct Weigher {
-    float mx;  // the row's maximum
-    F2 c;      // log2(e) / T
+    float mx;      // the row's maximum
+    F2 c;          // log2(e) / T
+    int scale;     // the maximum's weight is 2^scale: sums over a row stay below 2^62
+    bool precise;
+    const uint2* table;
 
     // octaves below the maximum's weight
     __device__ __forceinline__ float octaves(float x) const { return x == mx ? 0.f : (mx - x) * c.h; }
 
-    // weight in units of 2^-36 (fast) or 2^-40 (precise) of the maximum's
-    template <bool PRECISE>
-    __device__ __forceinline__ u64 weight(float x) const
+    __device__ __forceinline__ u64 operator()(float x) const
     {
-        if (x == mx) return PRECISE ? (1ull << 40) : (1ull << 36);
-        if (!PRECISE) return (u64)__float2ull_rn(exp2f(-(mx - x) * c.h) * 68719476736.f);
-        // y = (mx - x) * c as a pair, n its nearest integer, 2^-(y - n) by the series of exp
+        if (x == mx) return 1ull << scale;
+        if (precise) return precise_weight(x, mx, c, scale);
         const F2 d = two_sum(mx, -x);
-        const F2 y = mul2(d, c);
-        const float n = rintf(y.h);
-        F2 z = mul2(quick_sum(__fsub_rn(y.h, n), y.l), split2(0.69314718055994530942));  // |z| <= 0.35
-        z.h = -z.h;
-        z.l = -z.l;
-        // terms 7 .. 12 of the series need 24 bits only (the 7th is below 2^-22), the lower ones pairs
-        float t = 1.f / 479001600.f;
-        t = fmaf(t, z.h, 1.f / 39916800.f);
-        t = fmaf(t, z.h, 1.f / 3628800.f);
-        t = fmaf(t, z.h, 1.f / 362880.f);
-        t = fmaf(t, z.h, 1.f / 40320.f);
-        t = fmaf(t, z.h, 1.f / 5040.f);
-        F2 s = {t, 0.f};
-        s = add2(mul2(s, z), split2(1.0 / 720.0));
-        s = add2(mul2(s, z), split2(1.0 / 120.0));
-        s = add2(mul2(s, z), split2(1.0 / 24.0));
-        s = add2(mul2(s, z), split2(1.0 / 6.0));
-        s = add2(mul2(s, z), split2(0.5));
-        s = add2(mul2(s, z), split2(1.0));
-        s = add2(mul2(s, z), split2(1.0));
-        const float up = exp2f(40.f - n);  // an exact power of two
-        return (u64)((long long)__float2ull_rn(s.h * up) + __float2ll_rn(s.l * up));
+        const float h = __fmul_rn(d.h, c.h);
+        const float l = fmaf(d.l, c.h, fmaf(d.h, c.l, fmaf(d.h, c.h, -h)));
+        const float q = fmaf(h, 64.f, 12582912.f);  // 64 h to the nearest integer, in the low bits
+        const int k = __float_as_int(q) - 0x4b400000;
+        const float r = fmaf(q - 12582912.f, -1.f / 64.f, h) + l;
+        const uint2 t = table[k & 63];
+        const float f = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);  // 2^-r - 1
+        const unsigned v = t.x + (unsigned)__float2int_rn(f * __uint_as_float(t.y));
+        return ((u64)v << (scale - 31)) >> min(k >> 6, 63);
     }
 };
 
-// f x s for f in [0, 1), rounded down or up, exactly (64-bit floating point is slow here: two products a cycle and SM)
+// f x s for f in [0, 1), rounded down or up, exactly
 __device__ __forceinline__ u64 fraction(float f, u64 s, bool up)
 {
     if (!(f > 0.f)) return 0;
@@ -176,19 +211,17 @@ __device__ __forceinline__ u64 warp_inclusive(u64 v)
 }
 
 // A CTA's part of a row, in 16-byte vectors of VE elements.  Vector v holds columns c0 + v * VE ..; those outside
-// the part (at the ends, where the row is not 16-byte aligned) read as NaN.
+// the part (at the ends, where the row is not 16-byte aligned) read as NaN.  A warp's vectors are consecutive.
 template <typename T>
 struct Part {
     static constexpr int VE = 16 / sizeof(T);
-    const T* g;         // column 0 of the row
-    const uint4* kept;  // the vectors in shared memory, or nullptr
-    int lo, hi, c0;     // columns [lo, hi)
-    int nvec, per;      // vectors, and vectors per warp
+    const T* g;      // column 0 of the row
+    unsigned kept;   // the vectors' address in shared memory, 0: they are read from memory
+    int lo, hi, c0;  // columns [lo, hi)
+    int nvec, per;   // vectors, and vectors per warp
 
-    __device__ __forceinline__ uint4 fetch(int v) const
+    __device__ __noinline__ static uint4 ragged(const T* g, int c, int lo, int hi)
     {
-        const int c = c0 + v * VE;
-        if (c >= lo && c + VE <= hi) return __ldg(reinterpret_cast<const uint4*>(g + c));
         uint4 r;
         T e[VE];
 #pragma unroll
@@ -199,22 +232,48 @@ struct Part {
         memcpy(&r, e, 16);
         return r;
     }
-    __device__ __forceinline__ uint4 vec(int v) const { return kept ? kept[v] : fetch(v); }
+    __device__ __forceinline__ uint4 fetch(int v) const
+    {
+        const int c = c0 + v * VE;
+        if (c >= lo && c + VE <= hi) return __ldg(reinterpret_cast<const uint4*>(g + c));
+        return ragged(g, c, lo, hi);
+    }
+    __device__ __forceinline__ uint4 vec(int v) const
+    {
+        if (!kept) return fetch(v);
+        uint4 r;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(kept + 16 * v));
+        return r;
+    }
     static __device__ __forceinline__ float elem(const uint4& r, int i)
     {
         if constexpr (sizeof(T) == 4) return __uint_as_float(i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w);
         const unsigned w = (i >> 1) == 0 ? r.x : (i >> 1) == 1 ? r.y : (i >> 1) == 2 ? r.z : r.w;
         return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
-    // f(column, logit) for the columns of this thread (a warp's vectors are consecutive, and ascend)
+    // the largest element (NaN: only if all are)
+    static __device__ __forceinline__ float largest(const uint4& r)
+    {
+        if constexpr (sizeof(T) == 4) {
+            return fmaxf(fmaxf(elem(r, 0), elem(r, 1)), fmaxf(elem(r, 2), elem(r, 3)));
+        } else {
+            __nv_bfloat162 b[4];
+            memcpy(b, &r, 16);
+            const __nv_bfloat162 m = __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3]));
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+    }
+    // f(column, logit) for this thread's columns of at least `least`, in ascending order
     template <typename F>
-    __device__ __forceinline__ void each(F f) const
+    __device__ __forceinline__ void each(float least, F f) const
     {
         const int w0 = (threadIdx.x >> 5) * per, w1 = min(nvec, w0 + per);
         for (int v = w0 + (threadIdx.x & 31); v < w1; v += 32) {
             const uint4 r = vec(v);
+            if (!(largest(r) >= least)) continue;
 #pragma unroll
-            for (int i = 0; i < VE; ++i) f(c0 + v * VE + i, elem(r, i));
+            for (int i = 0; i < VE; ++i)
+                if (elem(r, i) >= least) f(c0 + v * VE + i, elem(r, i));
         }
     }
 };
@@ -225,7 +284,8 @@ struct Row {
     Part<T> p;
     Weigher W;
     float lmin;  // columns below it are no candidates
-    int C, rank;
+    float mine;  // the largest logit among this thread's columns
+    int C, rank, cols;
     SrShared* S;
 
     __device__ __forceinline__ void sync() const
@@ -235,6 +295,8 @@ struct Row {
     }
     __device__ __forceinline__ SrShared* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
     __device__ __forceinline__ int bin(float x) const { return min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1); }
+    // how far a comparison of two sums of fast weights may be off: 2^-29 of each, a unit per column
+    __device__ __forceinline__ u64 band(u64 total) const { return W.precise ? 0 : (total >> 28) + 2ull * cols + 2; }
 };
 
 // The first of 1024 values a (in shared memory) at which the running sum, starting at `start`, exceeds target;
@@ -284,32 +346,13 @@ __device__ u64 block_sum(SrShared* S, const U* a, int n)
     return t;
 }
 
-// Histogram of the columns that `put(column, x, bin)` names a bin for (-1: none), over all CTAs of the row, into S->num
-// and S->sum.
-template <bool PRECISE, typename T, typename F>
-__device__ void histogram(const Row<T>& R, bool counts, bool sums, F put)
+// Adds this CTA's histogram to the others' into S->num and S->sum.
+template <typename T>
+__device__ void gather_histogram(const Row<T>& R, bool counts, bool sums)
 {
     SrShared* S = R.S;
-    const int tid = threadIdx.x;
-    for (int i = tid; i < SR_NB; i += SR_NT) S->count[i] = S->lo[i] = S->hi[i] = 0;
-    __syncthreads();
-    R.p.each([&](int col, float x) {
-        if (!(x >= R.lmin)) return;
-        const int b = put(col, x);
-        if (b < 0) return;
-        if (counts) atomicAdd(&S->count[b], 1u);
-        if (sums) {
-            const u64 w = R.W.template weight<PRECISE>(x);
-            const unsigned wl = (unsigned)w;
-            if (w) {
-                const unsigned old = atomicAdd(&S->lo[b], wl);
-                const unsigned wh = (unsigned)(w >> 32) + (old + wl < old);
-                if (wh) atomicAdd(&S->hi[b], wh);
-            }
-        }
-    });
     R.sync();
-    for (int i = tid; i < SR_NB; i += SR_NT) {
+    for (int i = threadIdx.x; i < SR_NB; i += SR_NT) {
         u64 m = 0;
         unsigned n = 0;
         for (int r = 0; r < R.C; ++r) {
@@ -323,17 +366,46 @@ __device__ void histogram(const Row<T>& R, bool counts, bool sums, F put)
     R.sync();  // the others' histograms have been read
 }
 
-// The columns that `take(x)` names, of all CTAs, into S->list in the candidates' order; their number (more than
-// SR_LIST: the list is not complete).
+__device__ __forceinline__ void clear_histogram(SrShared* S)
+{
+    for (int i = threadIdx.x; i < SR_NB; i += SR_NT) S->count[i] = S->lo[i] = S->hi[i] = 0;
+    __syncthreads();
+}
+
+__device__ __forceinline__ void add_weight(SrShared* S, int b, u64 w)
+{
+    if (!w) return;
+    const unsigned wl = (unsigned)w, old = atomicAdd(&S->lo[b], wl);
+    const unsigned wh = (unsigned)(w >> 32) + (old + wl < old);
+    if (wh) atomicAdd(&S->hi[b], wh);
+}
+
+// Histogram of the columns of at least `least` by put(column, x) (-1: in none), over all CTAs of the row.
 template <typename T, typename F>
-__device__ unsigned list_sorted(const Row<T>& R, F take)
+__device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, F put)
+{
+    SrShared* S = R.S;
+    clear_histogram(S);
+    R.p.each(least, [&](int col, float x) {
+        const int b = put(col, x);
+        if (b < 0) return;
+        if (counts) atomicAdd(&S->count[b], 1u);
+        if (sums) add_weight(S, b, R.W(x));
+    });
+    gather_histogram(R, counts, sums);
+}
+
+// The columns of at least `least` that take(x) names, of all CTAs, into S->list in the candidates' order; their number
+// (more than SR_LIST: the list is not complete).
+template <typename T, typename F>
+__device__ unsigned list_sorted(const Row<T>& R, float least, F take)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
     if (tid == 0) S->listed = 0;
     R.sync();
-    R.p.each([&](int col, float x) {
-        if (!(x >= R.lmin) || !take(x)) return;
+    R.p.each(least, [&](int col, float x) {
+        if (!take(x) || *(volatile unsigned*)&S->listed > SR_LIST) return;
         const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
         for (int r = 0; r < R.C; ++r) {
             SrShared* o = R.of(r);
@@ -375,29 +447,32 @@ __device__ unsigned list_sorted(const Row<T>& R, F take)
     return n;
 }
 
-// The first column, in ascending order over the whole row, at which the running sum of wt(column, x) exceeds
-// goal(total): only the CTA that holds it returns true, with S->where = the column, S->before = the sum before it and
-// S->inside = its weight.
+// The first column, in ascending order over the whole row, at which the running sum of wt(column, x) over the columns of
+// at least `least` exceeds goal(total): only the CTA that holds it returns true, with S->where = the column,
+// S->before = the sum before it and S->inside = its weight.
 template <typename T, typename F, typename G>
-__device__ bool find_in_order(const Row<T>& R, F wt, G goal)
+__device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
 {
     SrShared* S = R.S;
     const Part<T>& P = R.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     u64 mine = 0;
-    P.each([&](int col, float x) { mine += wt(col, x); });
+    P.each(least, [&](int col, float x) { mine += wt(col, x); });
     mine = warp_sum(mine);
     __syncthreads();
     if (lane == 0) S->ws[warp] = mine;
     __syncthreads();
     u64 here = 0;
     for (int w = 0; w < SR_NW; ++w) here += S->ws[w];
-    if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
-    R.sync();
-    u64 run = 0, total = 0;
-    for (int r = 0; r < R.C; ++r) {
-        if (r < R.rank) run += S->r_sum[r];
-        total += S->r_sum[r];
+    u64 run = 0, total = here;
+    if (R.C > 1) {
+        if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
+        R.sync();
+        total = 0;
+        for (int r = 0; r < R.C; ++r) {
+            if (r < R.rank) run += S->r_sum[r];
+            total += S->r_sum[r];
+        }
     }
     const u64 target = goal(total);
     if (!(run <= target && run + here > target)) return false;
@@ -408,8 +483,11 @@ __device__ bool find_in_order(const Row<T>& R, F wt, G goal)
     mine = 0;
     for (int v = v0 + warp * piece + lane; v < min(v1, v0 + (warp + 1) * piece); v += 32) {
         const uint4 r = P.vec(v);
-#pragma unroll
-        for (int i = 0; i < P.VE; ++i) mine += wt(P.c0 + v * P.VE + i, P.elem(r, i));
+#pragma unroll 1
+        for (int i = 0; i < P.VE; ++i) {
+            const float x = P.elem(r, i);
+            if (x >= least) mine += wt(P.c0 + v * P.VE + i, x);
+        }
     }
     mine = warp_sum(mine);
     __syncthreads();
@@ -421,15 +499,14 @@ __device__ bool find_in_order(const Row<T>& R, F wt, G goal)
         const int p0 = v0 + w * piece, p1 = min(v1, p0 + piece);
         for (int b = p0; b < p1; b += 32) {
             const int v = b + lane;
-            u64 e[P.VE], sum = 0;
-#pragma unroll
-            for (int i = 0; i < P.VE; ++i) e[i] = 0;
+            u64 sum = 0;
+            uint4 r = make_uint4(0, 0, 0, 0);
             if (v < p1) {
-                const uint4 r = P.vec(v);
-#pragma unroll
+                r = P.vec(v);
+#pragma unroll 1
                 for (int i = 0; i < P.VE; ++i) {
-                    e[i] = wt(P.c0 + v * P.VE + i, P.elem(r, i));
-                    sum += e[i];
+                    const float x = P.elem(r, i);
+                    if (x >= least) sum += wt(P.c0 + v * P.VE + i, x);
                 }
             }
             const u64 inc = warp_inclusive(sum);
@@ -437,16 +514,17 @@ __device__ bool find_in_order(const Row<T>& R, F wt, G goal)
             if (hit) {
                 if (lane == __ffs(hit) - 1) {
                     u64 at = run + inc - sum;
-                    bool found = false;
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < P.VE; ++i) {
-                        if (!found && at + e[i] > target) {
-                            found = true;
+                        const float x = P.elem(r, i);
+                        const u64 e = x >= least ? wt(P.c0 + v * P.VE + i, x) : 0;
+                        if (at + e > target) {
                             S->where = P.c0 + v * P.VE + i;
                             S->before = at;
-                            S->inside = e[i];
+                            S->inside = e;
+                            break;
                         }
-                        at += e[i];
+                        at += e;
                     }
                 }
                 break;
@@ -458,42 +536,69 @@ __device__ bool find_in_order(const Row<T>& R, F wt, G goal)
     return true;
 }
 
-// How far a comparison of two sums of fast weights may be off: `spread` = sum of weight x octaves (an exponent's error
-// is 3 x 2^-24 of it, in octaves), 2 ulp of the exponential, half a unit per column; twice that for the two sides.
-template <typename T>
-__device__ __forceinline__ u64 error_band(float spread, u64 total, const Row<T>& R)
-{
-    return (u64)(2.f * (1.4e-7f * spread + 2.6e-7f * (float)total + 0.51f * (float)(R.p.hi - R.p.lo) * (float)R.C)) + 2;
-}
-
+// The candidates: logits above tau, and those equal to it up to column tie.
 struct Border {
-    unsigned tau;  // the candidates: keys above tau, and those equal to it up to column tie
+    float tau;
     int tie;
-    u64 mass;      // their sum of weights (if the histogram has sums)
 };
 
-// The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`;
-// S->num / S->sum hold the linear histogram and keep it unless the border's bin is too full to list.
-template <bool PRECISE, bool BY_MASS, typename T>
-__device__ Border find_border(const Row<T>& R, u64 target, u64 band)
+// The last entry of the shortest prefix of the n listed columns that, after sums of `mass` and `count` before the list,
+// reaches `target` (weights if BY_MASS, columns if not); at most the first `most` entries.
+template <bool BY_MASS, typename T>
+__device__ Border border_in_list(const Row<T>& R, unsigned n, u64 mass, u64 count, u64 target, u64 band)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x;
+    if (!BY_MASS) {
+        const u64 e = S->list[target - 1 - count];
+        return {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
+    }
+    u64 v[SR_BPT], mine = 0;
+#pragma unroll
+    for (int i = 0; i < SR_BPT; ++i) {
+        const unsigned at = tid * SR_BPT + i;
+        v[i] = at < n ? R.W(key_value((unsigned)(S->list[at] >> 32))) : 0;
+        mine += v[i];
+    }
+    const u64 inc = warp_inclusive(mine);
+    if ((tid & 31) == 31) S->ws[tid >> 5] = inc;
+    if (tid == 0) { S->where = n - 1; S->before = ~0ull; }
+    __syncthreads();
+    u64 run = mass + inc - mine;
+    for (int q = 0; q < (tid >> 5); ++q) run += S->ws[q];
+#pragma unroll
+    for (int i = 0; i < SR_BPT; ++i) {
+        if (run < target && run + v[i] >= target) { S->where = tid * SR_BPT + i; S->before = run; S->inside = v[i]; }
+        run += v[i];
+    }
+    __syncthreads();
+    const u64 e = S->list[S->where], before = S->before, upto = before + S->inside;
+    // the border is certain if no error of the sums can move it
+    if (before != ~0ull && (upto < target + band || (before > 0 && before + band >= target)) && tid == 0) S->unsure = 1;
+    __syncthreads();
+    return {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
+}
+
+// The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`
+// (less than `band` off), from the linear histogram in S->num / S->sum.
+template <bool BY_MASS, typename T>
+__device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
     if (BY_MASS) block_find(S, S->sum, 0, target - 1);
     else block_find(S, S->num, 0, target - 1);
-    int b = S->where;
-    u64 before = S->before;                                  // of what is counted
-    u64 mass = BY_MASS ? before : block_sum(S, S->sum, b);   // weights before the bin
-    u64 count = BY_MASS ? 0 : before;
+    const int b = S->where;
+    u64 mass = BY_MASS ? S->before : 0, count = BY_MASS ? 0 : S->before;  // before the bin
     unsigned klo = 0, khi = 0xffffffffu;
     bool keyed = false;
-    unsigned n = list_sorted(R, [&](float x) { return R.bin(x) == b; });
+    unsigned n = list_sorted(R, least, [&](float x) { return R.bin(x) == b; });
     while (n > SR_LIST) {
         // too many: split the bin's range of keys, down to one key
         if (!keyed) {
             unsigned lo = 0xffffffffu, hi = 0;
-            R.p.each([&](int, float x) {
-                if (x >= R.lmin && R.bin(x) == b) {
+            R.p.each(least, [&](int, float x) {
+                if (R.bin(x) == b) {
                     const unsigned k = order_key(x);
                     lo = min(lo, k);
                     hi = max(hi, k);
@@ -520,164 +625,151 @@ __device__ Border find_border(const Row<T>& R, u64 target, u64 band)
         }
         if (klo == khi) break;
         const int bits = 32 - __clz(khi - klo), sh = bits > 10 ? bits - 10 : 0;
-        histogram<PRECISE>(R, true, true, [&](int, float x) {
+        histogram(R, least, true, BY_MASS, [&](int, float x) {
             const unsigned k = order_key(x);
             return k >= klo && k <= khi ? (int)((khi - k) >> sh) : -1;
         });
         if (BY_MASS) block_find(S, S->sum, mass, target - 1);
         else block_find(S, S->num, count, target - 1);
         const int sub = S->where;
-        const u64 counted = S->before;
         n = S->num[sub];
-        if (BY_MASS) {
-            mass = counted;
-        } else {
-            count = counted;
-            mass += block_sum(S, S->sum, sub);
-        }
+        if (BY_MASS) mass = S->before;
+        else count = S->before;
         const unsigned top = khi - ((unsigned)sub << sh);
         klo = max(klo, sh ? top - ((1u << sh) - 1u) : top);
         khi = top;
         __syncthreads();
-        if (n <= SR_LIST) n = list_sorted(R, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
+        if (n <= SR_LIST) n = list_sorted(R, least, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
     }
-    Border B;
-    u64 w = 0;  // the border column's own weight
-    if (n <= SR_LIST) {
-        u64 v[SR_BPT], mine = 0;
-#pragma unroll
-        for (int i = 0; i < SR_BPT; ++i) {
-            const int at = tid * SR_BPT + i;
-            v[i] = at < (int)n ? R.W.template weight<PRECISE>(key_value((unsigned)(S->list[at] >> 32))) : 0;
-            mine += v[i];
-        }
-        const u64 inc = warp_inclusive(mine);
-        if ((tid & 31) == 31) S->ws[tid >> 5] = inc;
-        if (tid == 0) S->where = 0;
-        __syncthreads();
-        u64 run = mass + inc - mine;
-        for (int q = 0; q < (tid >> 5); ++q) run += S->ws[q];
-#pragma unroll
-        for (int i = 0; i < SR_BPT; ++i) {
-            const int at = tid * SR_BPT + i;
-            const bool last = BY_MASS ? run < target && run + v[i] >= target : (u64)at == target - 1 - count;
-            if (last && at < (int)n) { S->where = at; S->before = run; S->inside = v[i]; }
-            run += v[i];
-        }
-        __syncthreads();
-        const u64 e = S->list[S->where];
-        B.tau = (unsigned)(e >> 32);
-        B.tie = (int)~(unsigned)e;
-        w = S->inside;
-        B.mass = S->before + w;
-    } else {
-        // one key, many columns: the last of them taken, in column order
-        w = R.W.template weight<PRECISE>(key_value(klo));
-        u64 take;
-        if (BY_MASS) take = w ? min((u64)n, max((u64)1, (target - mass + w - 1) / w)) : n;
-        else take = target - count;
-        B.tau = klo;
-        B.mass = mass + take * w;
-        const bool mine = find_in_order(R, [&](int, float x) { return (u64)(x >= R.lmin && order_key(x) == klo); },
-                                        [&](u64) { return take - 1; });
-        const int at = mine ? S->where : -1;
-        R.sync();
-        if (mine && tid < R.C) R.of(tid)->token = at;
-        R.sync();
-        B.tie = S->token;
+    if (n <= SR_LIST) return border_in_list<BY_MASS>(R, n, mass, count, target, band);
+    // one key, many columns: the last of them taken, in column order
+    const u64 w = R.W(key_value(klo));
+    u64 take = target - count;
+    if (BY_MASS) {
+        take = w ? max((u64)1, (target - mass + w - 1) / w) : 1;
+        const u64 upto = mass + take * w;
+        if ((upto < target + band || (upto > w && upto - w + band >= target)) && tid == 0) S->unsure = 1;
     }
-    // the border is certain if no error of the sums can move it
-    if (BY_MASS && (B.mass < target + band || (B.mass > w && B.mass - w + band >= target)) && tid == 0) S->unsure = 1;
+    const bool mine = find_in_order(R, least, [&](int, float x) { return (u64)(order_key(x) == klo); }, [&](u64) { return take - 1; });
+    const int at = mine ? S->where : -1;
+    R.sync();
+    if (mine && tid < R.C) R.of(tid)->token = at;
+    R.sync();
+    const Border B = {key_value(klo), S->token};
     __syncthreads();
     return B;
 }
 
-// The token of the row into `token` by the CTA that finds it.  False if an error bound left a choice open (never with PRECISE).
-template <bool PRECISE, typename T>
-__device__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, int32_t* token)
+// The token of the row into `token` by the CTA that finds it.  False if an error bound left a choice open (never with
+// precise weights).
+template <typename T>
+__device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, bool few, int32_t* token)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
-    unsigned tau = 0;
-    int tie = 0x7fffffff;
+    Border B = {R.lmin, 0x7fffffff};
     if (tid == 0) S->unsure = 0;
-    const bool cut_k = top_k > 0, cut_p = top_p < 1.f;
+    const bool cut_k = top_k > 0 && top_k < R.cols, cut_p = top_p < 1.f;
     if (cut_k || cut_p) {
-        histogram<PRECISE>(R, cut_k, cut_p, [&](int, float x) { return R.bin(x); });
-        u64 total = 0;
-        bool whole = true;  // the histogram still holds the row
-        if (cut_k && block_sum(S, S->num, SR_NB) > (u64)top_k) {
-            const Border B = find_border<PRECISE, false>(R, (u64)top_k, 0);
-            tau = B.tau;
-            tie = B.tie;
-            total = B.mass;
-            whole = false;
-        }
-        if (cut_p) {
-            if (!whole)  // the candidates' own histogram
-                histogram<PRECISE>(R, false, true, [&](int col, float x) {
-                    const unsigned k = order_key(x);
-                    return k > tau || (k == tau && col <= tie) ? R.bin(x) : -1;
-                });
-            total = block_sum(S, S->sum, SR_NB);
-            // a bound on the error of any sum of these weights
-            u64 band = 0;
-            if (!PRECISE) {
-                float f = 0.f, e = 0.f;
-#pragma unroll
-                for (int i = 0; i < SR_BPT; ++i) f += (float)S->sum[tid * SR_BPT + i] * (float)(tid * SR_BPT + i + 1);
-                for (int o = 16; o; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-                if ((tid & 31) == 0) S->wf[tid >> 5] = f;
+        bool listed = false;
+        unsigned n = 0;
+        if (cut_k || few) {
+            float least = R.lmin;
+            bool bounded = few;
+            if (cut_k && top_k <= SR_NT * R.C) {
+                // the bin that the k-th largest of the threads' maxima lies in: at least k columns reach it
+                clear_histogram(S);
+                if (R.mine >= R.lmin) atomicAdd(&S->count[R.bin(R.mine)], 1u);
+                gather_histogram(R, true, false);
+                block_find(S, S->num, 0, (u64)top_k - 1);
+                if (S->where >= 0) {  // its lower edge, less what the bin's arithmetic may be off
+                    const float edge = R.W.mx - (float)(S->where + 1) * (SR_REACH / SR_NB) * 1.00001f / R.W.c.h;
+                    if (edge > least) least = edge;
+                    bounded = true;
+                }
                 __syncthreads();
-                for (int w = 0; w < SR_NW; ++w) e += S->wf[w];
-                band = error_band(e * (SR_REACH / SR_NB), total, R);
             }
-            const u64 target = max((u64)1, fraction(top_p, total, true));
-            const Border B = find_border<PRECISE, true>(R, target, band);
-            tie = B.tau == tau ? min(tie, B.tie) : B.tie;
-            tau = B.tau;
+            if (bounded) {
+                n = list_sorted(R, least, [](float) { return true; });
+                listed = n <= SR_LIST;
+            }
+        }
+        if (listed) {
+            if (cut_k && n > (unsigned)top_k) n = top_k;
+            const u64 e = S->list[n - 1];
+            B = {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
+            if (cut_p) {
+                u64 mine = 0;
+#pragma unroll
+                for (int i = 0; i < SR_BPT; ++i) {
+                    const unsigned at = tid * SR_BPT + i;
+                    if (at < n) mine += R.W(key_value((unsigned)(S->list[at] >> 32)));
+                }
+                mine = warp_sum(mine);
+                if ((tid & 31) == 0) S->ws[tid >> 5] = mine;
+                __syncthreads();
+                u64 total = 0;
+                for (int w = 0; w < SR_NW; ++w) total += S->ws[w];
+                __syncthreads();
+                B = border_in_list<true>(R, n, 0, 0, max((u64)1, fraction(top_p, total, true)), R.band(total));
+            }
+            __syncthreads();
+        } else {
+            if (cut_k) {
+                histogram(R, R.lmin, true, false, [&](int, float x) { return R.bin(x); });
+                if (block_sum(S, S->num, SR_NB) > (u64)top_k) B = find_border<false>(R, R.lmin, (u64)top_k, 0);
+            }
+            if (cut_p) {
+                // Columns of less than (1 - p) / cols of the maximum's weight hold at most 1 - p of the total: the border
+                // lies above them, and only their sum is needed.
+                const float deep = log2f((float)R.cols / (1.f - fmaxf(top_p, 0.f))) + 1.f;
+                const float shallow = fmaxf(B.tau, R.W.mx - deep / R.W.c.h);
+                clear_histogram(S);
+                u64 rest = 0;
+                R.p.each(B.tau, [&](int col, float x) {
+                    if (x == B.tau && col > B.tie) return;
+                    const u64 w = R.W(x);
+                    if (x >= shallow) add_weight(S, R.bin(x), w);
+                    else rest += w;
+                });
+                rest = warp_sum(rest);
+                if ((tid & 31) == 0) S->ws[tid >> 5] = rest;
+                __syncthreads();
+                rest = 0;
+                for (int w = 0; w < SR_NW; ++w) rest += S->ws[w];
+                if (R.C > 1 && tid < R.C) R.of(tid)->r_sum[R.rank] = rest;
+                gather_histogram(R, false, true);
+                if (R.C > 1) {
+                    rest = 0;
+                    for (int r = 0; r < R.C; ++r) rest += S->r_sum[r];
+                }
+                const u64 total = block_sum(S, S->sum, SR_NB) + rest;
+                const Border Q = find_border<true>(R, shallow, max((u64)1, fraction(top_p, total, true)), R.band(total));
+                if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
+            }
         }
     }
     // the draw, in column order
-    float spread = 0.f;  // sum of weight x octaves: how exact the weights are
-    const auto wt = [&](int col, float x) {
-        if (!(x >= R.lmin)) return (u64)0;
-        const unsigned k = order_key(x);
-        if (!(k > tau || (k == tau && col <= tie))) return (u64)0;
-        const u64 w = R.W.template weight<PRECISE>(x);
-        if (!PRECISE) spread += (float)w * R.W.octaves(x);
-        return w;
-    };
     u64 target = 0, total = 0;
-    const bool mine = find_in_order(R, wt, [&](u64 sum) {
-        total = sum;
-        target = u < 1.f || !(u == u) ? fraction(u, sum, false) : sum - 1;
-        if (!PRECISE) {  // the spread of all CTAs
-            for (int o = 16; o; o >>= 1) spread += __shfl_xor_sync(0xffffffffu, spread, o);
-            if ((tid & 31) == 0) S->wf[tid >> 5] = spread;
-            __syncthreads();
-            float f = 0.f;
-            for (int w = 0; w < SR_NW; ++w) f += S->wf[w];
-            if (tid < R.C) R.of(tid)->r_spread[R.rank] = f;
-        }
-        return target;
-    });
-    R.sync();
+    const bool mine = find_in_order(
+        R, B.tau, [&](int col, float x) { return x == B.tau && col > B.tie ? (u64)0 : R.W(x); },
+        [&](u64 sum) {
+            total = sum;
+            target = u < 1.f || !(u == u) ? fraction(u, sum, false) : sum - 1;
+            return target;
+        });
+    if (R.C > 1) R.sync();
     if (mine && tid == 0) {
-        if (!PRECISE) {
-            float f = 0.f;
-            for (int r = 0; r < R.C; ++r) f += S->r_spread[r];
-            const u64 band = error_band(f, total, R);
-            // the chosen column's weight spans [before, before + inside)
-            if (S->before + S->inside <= target + band || (S->before > 0 && S->before + band > target))
-                for (int r = 0; r < R.C; ++r) R.of(r)->unsure = 1;
-        }
+        const u64 band = R.band(total);
+        // the chosen column's weight spans [before, before + inside)
+        if (!R.W.precise && (S->before + S->inside <= target + band || (S->before > 0 && S->before + band > target)))
+            for (int r = 0; r < R.C; ++r) R.of(r)->unsure = 1;
         *token = S->where;
     }
     R.sync();
     const bool open = S->unsure != 0;
     __syncthreads();  // read by all before another pass clears it
-    return PRECISE || !open;
+    return R.W.precise || !open;
 }
 
 template <typename T>
@@ -695,10 +787,15 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     const float T_ = temperature ? __ldg(temperature + r) : 1.f;
     const int k = top_k ? __ldg(top_k + r) : 0;
     const float p = top_p ? __ldg(top_p + r) : 1.f, mp = min_p ? __ldg(min_p + r) : 0.f, u = __ldg(uniforms + r);
+    if (tid < 64) {
+        const unsigned t = sr_table.at[tid].x;
+        S->table[tid] = make_uint2(t, __float_as_uint((float)t));
+    }
     Row<T> R;
     constexpr int VE = Part<T>::VE;
     R.C = C;
     R.rank = rank;
+    R.cols = cols;
     R.S = S;
     R.p.g = logits + (long long)r * ld;
     const int each = (cols + C - 1) / C;
@@ -707,8 +804,8 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     R.p.c0 = R.p.lo - (int)((reinterpret_cast<uintptr_t>(R.p.g + R.p.lo) & 15u) / sizeof(T));
     R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
     R.p.per = (R.p.nvec + SR_NW - 1) / SR_NW;
-    R.p.kept = nullptr;
-    uint4* kept = reinterpret_cast<uint4*>(sr_raw + sizeof(SrShared));
+    R.p.kept = 0;
+    const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared));
     // the maximum and its lowest column, and the row's part into shared memory
     float v = -INFINITY;
     int idx = 0x7fffffff;
@@ -723,16 +820,20 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
 #pragma unroll
             for (int i = 0; i < DEEP; ++i)
                 if (b + 32 * i < w1) {
-                    if (stage) kept[b + 32 * i] = x[i];
+                    if (stage)
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kept + 16 * (b + 32 * i)), "r"(x[i].x), "r"(x[i].y),
+                                     "r"(x[i].z), "r"(x[i].w) : "memory");
+                    const float m = R.p.largest(x[i]);
+                    if (m > v || (m == v && idx == 0x7fffffff)) {  // columns ascend: an equal one later never wins
+                        v = m;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float y = R.p.elem(x[i], e);
-                        const int c = R.p.c0 + (b + 32 * i) * VE + e;
-                        if (y > v || (y == v && c < idx)) { v = y; idx = c; }
+                        for (int e = VE - 1; e >= 0; --e)
+                            if (R.p.elem(x[i], e) == m) idx = R.p.c0 + (b + 32 * i) * VE + e;
                     }
                 }
         }
     }
+    R.mine = v;
     for (int o = 16; o; o >>= 1) {
         const float ov = __shfl_xor_sync(0xffffffffu, v, o);
         const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
@@ -751,12 +852,11 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
         for (int q = 0; q < C; ++q)
             if (S->r_max[q] > v || (S->r_max[q] == v && S->r_idx[q] < idx)) { v = S->r_max[q]; idx = S->r_idx[q]; }
     }
-    if (stage) R.p.kept = kept;
     if (!(T_ > 0.f) || v == -INFINITY || k == 1) {
         if (tid == 0 && rank == 0) tokens[r] = idx == 0x7fffffff ? 0 : idx;
         return;
     }
-    R.W.mx = v;
+    if (stage) R.p.kept = kept;
     if (tid == 0) {  // the row's 64-bit arithmetic
         S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
         float lmin = fmaxf(v - SR_REACH / S->c.h, -3.402823466e38f);
@@ -775,9 +875,16 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     }
     __syncthreads();
     R.lmin = S->lmin;
+    R.W.mx = v;
     R.W.c = S->c;
+    R.W.table = S->table;
+    R.W.scale = 62 - (32 - __clz(cols));
     const float pp = p == p ? p : 1.f;
-    if (!sample_row<false>(R, k, pp, u, tokens + r)) sample_row<true>(R, k, pp, u, tokens + r);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        R.W.precise = pass != 0;
+        if (sample_row(R, k, pp, u, mp > 0.f, tokens + r)) break;
+    }
 }
 
 template <typename T>
