@@ -4,12 +4,13 @@
 // All three filters keep a prefix of the columns ordered by (logit descending,
 // column ascending), so the candidates are {logit > tau} and the columns up to
 // `tie` among {logit == tau}, and the row is never sorted.  Where few columns can
-// be candidates they are listed and sorted: those above the k-th largest of the
-// threads' own maxima (at least k columns reach it, and rarely many more), or above
-// min-p's bound.  Otherwise a histogram, linear in the distance to the maximum in
-// octaves of the weight, finds the bin that holds a filter's border, and only that
-// bin's columns are sorted.  The token is then found by sums in column order, first
-// per warp's part of the row, then per piece of that part.
+// be candidates they are listed: those above the k-th largest of the threads' own
+// maxima (at least k columns reach it, and rarely many more), or above min-p's
+// bound.  One CTA then sorts the list, cuts it, sorts what is left by column and
+// finds the token.  Otherwise a histogram, linear in the distance to the
+// maximum in octaves of the weight, finds the bin that holds a filter's border, only
+// that bin's columns are listed, and the token is found by sums in column order, per
+// CTA, per thread, and within that thread's columns.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
 // part of the row in shared memory beside another CTA's, and to use the SMs when
@@ -41,7 +42,7 @@ constexpr int SR_NW = SR_NT / 32;
 constexpr int SR_NB = 1024;           // histogram bins
 constexpr int SR_BPT = SR_NB / SR_NT;
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
-constexpr int SR_LIST = 1024;         // columns that are sorted at once
+constexpr int SR_LIST = SR_NT;        // columns that are listed at most
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
 
@@ -55,12 +56,14 @@ struct __align__(16) SrShared {
     u64 sum[SR_NB];                               // the row's sums of weights
     unsigned num[SR_NB];                          // and columns
     u64 list[SR_LIST];                            // key << 32 | ~column
+    u64 other[SR_LIST];                           // the sort's exchanges between warps
+    unsigned base[SR_NW][SR_MAX_C];               // where a warp's listed columns go, in each CTA's list
     uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
     u64 ws[SR_NW];
     float wf[SR_NW];
     int wi[SR_NW];
     // one entry per CTA of the row, written by that CTA in every CTA's copy
-    float r_max[SR_MAX_C];
+    float r_max[SR_MAX_C], r_edge[SR_MAX_C];
     int r_idx[SR_MAX_C];
     unsigned r_klo[SR_MAX_C], r_khi[SR_MAX_C];
     u64 r_sum[SR_MAX_C];
@@ -71,6 +74,7 @@ struct __align__(16) SrShared {
     // the row's constants
     float lmin;
     F2 c;
+    double reach;
 };
 
 struct Table {
@@ -211,14 +215,14 @@ __device__ __forceinline__ u64 warp_inclusive(u64 v)
 }
 
 // A CTA's part of a row, in 16-byte vectors of VE elements.  Vector v holds columns c0 + v * VE ..; those outside
-// the part (at the ends, where the row is not 16-byte aligned) read as NaN.  A warp's vectors are consecutive.
+// the part (at the ends, where the row is not 16-byte aligned) read as NaN.  Thread t has vectors t * per .. (t + 1) * per - 1.
 template <typename T>
 struct Part {
     static constexpr int VE = 16 / sizeof(T);
     const T* g;      // column 0 of the row
     unsigned kept;   // the vectors' address in shared memory, 0: they are read from memory
     int lo, hi, c0;  // columns [lo, hi)
-    int nvec, per;   // vectors, and vectors per warp
+    int nvec, per;   // vectors, and vectors per thread (odd: threads' vectors lie in different banks)
 
     __device__ __noinline__ static uint4 ragged(const T* g, int c, int lo, int hi)
     {
@@ -267,8 +271,8 @@ struct Part {
     template <typename F>
     __device__ __forceinline__ void each(float least, F f) const
     {
-        const int w0 = (threadIdx.x >> 5) * per, w1 = min(nvec, w0 + per);
-        for (int v = w0 + (threadIdx.x & 31); v < w1; v += 32) {
+        const int v1 = min(nvec, (int)(threadIdx.x + 1) * per);
+        for (int v = threadIdx.x * per; v < v1; ++v) {
             const uint4 r = vec(v);
             if (!(largest(r) >= least)) continue;
 #pragma unroll
@@ -395,56 +399,98 @@ __device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, 
     gather_histogram(R, counts, sums);
 }
 
-// The columns of at least `least` that take(x) names, of all CTAs, into S->list in the candidates' order; their number
-// (more than SR_LIST: the list is not complete).
+// The columns of at least `least` that take(x) names, of all CTAs, into the S->list (unordered, S->listed set to 0 before)
+// of the row's first CTA, or of all; their number (more than SR_LIST: the list is not complete).
 template <typename T, typename F>
-__device__ unsigned list_sorted(const Row<T>& R, float least, F take)
+__device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
 {
     SrShared* S = R.S;
-    const int tid = threadIdx.x;
-    if (tid == 0) S->listed = 0;
-    R.sync();
-    R.p.each(least, [&](int col, float x) {
-        if (!take(x) || *(volatile unsigned*)&S->listed > SR_LIST) return;
-        const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
-        for (int r = 0; r < R.C; ++r) {
-            SrShared* o = R.of(r);
-            const unsigned at = atomicAdd(&o->listed, 1u);
-            if (at < SR_LIST) o->list[at] = e;
-        }
-    });
-    R.sync();
-    const unsigned n = S->listed;
-    if (n > SR_LIST || n <= 1) return n;
-    if (n <= 256) {  // each entry's place is the number of larger ones
-        u64 mine = 0;
-        unsigned at = 0;
-        if (tid < n) {
-            mine = S->list[tid];
-            for (unsigned i = 0; i < n; ++i) at += S->list[i] > mine;
-        }
-        __syncthreads();
-        if (tid < n) S->list[at] = mine;
-        __syncthreads();
-        return n;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, dests = all ? R.C : 1;
+    unsigned n = 0;
+    R.p.each(least, [&](int, float x) { n += take(x); });
+    unsigned inc = n;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
     }
-    unsigned full = 512;
-    while (full < n) full *= 2;
-    for (unsigned i = n + tid; i < full; i += SR_NT) S->list[i] = 0;
+    const unsigned whole = __shfl_sync(0xffffffffu, inc, 31);
+    if (whole) {
+        if (lane < dests) S->base[warp][lane] = atomicAdd(&R.of(lane)->listed, whole);
+        __syncwarp();
+        if (n) {
+            unsigned at = inc - n;
+            R.p.each(least, [&](int col, float x) {
+                if (!take(x)) return;
+                const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
+                for (int r = 0; r < dests; ++r)
+                    if (S->base[warp][r] + at < SR_LIST) R.of(r)->list[S->base[warp][r] + at] = e;
+                ++at;
+            });
+        }
+    }
+    if (R.C == 1 || all) {
+        R.sync();
+        return *(volatile unsigned*)&S->listed;
+    }
+    // the first CTA's list: the others learn how long it is from the counts
+    if (lane == 0) S->ws[warp] = whole;
     __syncthreads();
+    u64 here = 0;
+    for (int w = 0; w < SR_NW; ++w) here += S->ws[w];
+    if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
+    R.sync();
+    u64 total = 0;
+    for (int r = 0; r < R.C; ++r) total += S->r_sum[r];
+    return (unsigned)total;
+}
+
+// Sorts e, one value per thread, over the first `full` threads (a power of two from 32), largest first.  All of them call it.
+__device__ __forceinline__ u64 sort_descending(SrShared* S, u64 e, unsigned full)
+{
+    const unsigned tid = threadIdx.x;
     for (unsigned k = 2; k <= full; k *= 2)
         for (unsigned j = k / 2; j; j /= 2) {
-            for (unsigned i = tid; i < full / 2; i += SR_NT) {
-                const unsigned a = 2 * i - (i & (j - 1)), b = a + j;
-                const u64 x = S->list[a], y = S->list[b];
-                if ((x < y) == ((a & k) == 0)) {
-                    S->list[a] = y;
-                    S->list[b] = x;
-                }
+            u64 y;
+            if (j >= 32) {
+                S->other[tid] = e;
+                asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
+                y = S->other[tid ^ j];
+                asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
+            } else {
+                y = __shfl_xor_sync(0xffffffffu, e, j);
             }
-            __syncthreads();
+            const bool larger = ((tid & k) == 0) == ((tid & j) == 0);
+            e = (e > y) == larger ? e : y;
         }
-    return n;
+    return e;
+}
+
+// Inclusive sums of v over the first `full` threads (see sort_descending), and their total.
+__device__ __forceinline__ u64 scan_threads(SrShared* S, u64 v, unsigned full, u64& total)
+{
+    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const u64 inc = warp_inclusive(v);
+    if (full == 32) {
+        total = __shfl_sync(0xffffffffu, inc, 31);
+        return inc;
+    }
+    asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
+    if (lane == 31) S->ws[warp] = inc;
+    asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
+    u64 before = 0;
+    total = 0;
+    for (unsigned w = 0; w < full / 32; ++w) {
+        if (w == warp) before = total;
+        total += S->ws[w];
+    }
+    return before + inc;
+}
+
+__device__ __forceinline__ unsigned sort_width(unsigned n)
+{
+    unsigned full = 32;
+    while (full < n) full *= 2;
+    return full;
 }
 
 // The first column, in ascending order over the whole row, at which the running sum of wt(column, x) over the columns of
@@ -458,82 +504,58 @@ __device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     u64 mine = 0;
     P.each(least, [&](int col, float x) { mine += wt(col, x); });
-    mine = warp_sum(mine);
+    const u64 inc = warp_inclusive(mine);
     __syncthreads();
-    if (lane == 0) S->ws[warp] = mine;
+    if (lane == 31) S->ws[warp] = inc;
     __syncthreads();
-    u64 here = 0;
-    for (int w = 0; w < SR_NW; ++w) here += S->ws[w];
-    u64 run = 0, total = here;
+    u64 here = 0, run = inc - mine;
+#pragma unroll
+    for (int w = 0; w < SR_NW; ++w) {
+        if (w == warp) run += here;
+        here += S->ws[w];
+    }
+    u64 before = 0, total = here;
     if (R.C > 1) {
         if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
         R.sync();
         total = 0;
         for (int r = 0; r < R.C; ++r) {
-            if (r < R.rank) run += S->r_sum[r];
+            if (r < R.rank) before += S->r_sum[r];
             total += S->r_sum[r];
         }
     }
     const u64 target = goal(total);
-    if (!(run <= target && run + here > target)) return false;
-    int w = 0;
-    while (run + S->ws[w] <= target) run += S->ws[w++];
-    // the warp's vectors again, in pieces, one per warp
-    const int v0 = w * P.per, v1 = min(P.nvec, v0 + P.per), piece = (P.per + SR_NW - 1) / SR_NW;
-    mine = 0;
-    for (int v = v0 + warp * piece + lane; v < min(v1, v0 + (warp + 1) * piece); v += 32) {
-        const uint4 r = P.vec(v);
-#pragma unroll 1
-        for (int i = 0; i < P.VE; ++i) {
-            const float x = P.elem(r, i);
-            if (x >= least) mine += wt(P.c0 + v * P.VE + i, x);
-        }
-    }
-    mine = warp_sum(mine);
-    __syncthreads();
-    if (lane == 0) S->ws[warp] = mine;
-    __syncthreads();
-    w = 0;
-    while (run + S->ws[w] <= target) run += S->ws[w++];
-    if (warp == 0) {
-        const int p0 = v0 + w * piece, p1 = min(v1, p0 + piece);
-        for (int b = p0; b < p1; b += 32) {
-            const int v = b + lane;
-            u64 sum = 0;
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (v < p1) {
-                r = P.vec(v);
-#pragma unroll 1
-                for (int i = 0; i < P.VE; ++i) {
-                    const float x = P.elem(r, i);
-                    if (x >= least) sum += wt(P.c0 + v * P.VE + i, x);
-                }
+    run += before;
+    // the thread whose columns hold it, and its warp: that thread's columns, one per lane
+    const unsigned hit = __ballot_sync(0xffffffffu, run <= target && run + mine > target);
+    if (hit) {
+        const int l = __ffs(hit) - 1, v0 = (warp * 32 + l) * P.per, n = (min(P.nvec, v0 + P.per) - v0) * P.VE;
+        run = __shfl_sync(0xffffffffu, run, l);
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            u64 w = 0;
+            int col = 0;
+            if (i < n) {
+                const uint4 r = P.vec(v0 + i / P.VE);
+                const float x = P.elem(r, i % P.VE);
+                col = P.c0 + (v0 + i / P.VE) * P.VE + i % P.VE;
+                if (x >= least) w = wt(col, x);
             }
-            const u64 inc = warp_inclusive(sum);
-            const unsigned hit = __ballot_sync(0xffffffffu, run + inc > target);
-            if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    u64 at = run + inc - sum;
-#pragma unroll 1
-                    for (int i = 0; i < P.VE; ++i) {
-                        const float x = P.elem(r, i);
-                        const u64 e = x >= least ? wt(P.c0 + v * P.VE + i, x) : 0;
-                        if (at + e > target) {
-                            S->where = P.c0 + v * P.VE + i;
-                            S->before = at;
-                            S->inside = e;
-                            break;
-                        }
-                        at += e;
-                    }
+            const u64 sum = warp_inclusive(w);
+            const unsigned found = __ballot_sync(0xffffffffu, run + sum > target);
+            if (found) {
+                if (lane == __ffs(found) - 1) {
+                    S->where = col;
+                    S->before = run + sum - w;
+                    S->inside = w;
                 }
                 break;
             }
-            run += __shfl_sync(0xffffffffu, inc, 31);
+            run += __shfl_sync(0xffffffffu, sum, 31);
         }
     }
     __syncthreads();
-    return true;
+    return before <= target && before + here > target;
 }
 
 // The candidates: logits above tau, and those equal to it up to column tie.
@@ -542,41 +564,72 @@ struct Border {
     int tie;
 };
 
-// The last entry of the shortest prefix of the n listed columns that, after sums of `mass` and `count` before the list,
-// reaches `target` (weights if BY_MASS, columns if not); at most the first `most` entries.
+// The last of the shortest prefix, in the candidates' order, of the n listed columns that, after sums of `mass` and
+// `count` before the list, reaches `target` (weights if BY_MASS, less than `band` off; columns if not).
 template <bool BY_MASS, typename T>
 __device__ Border border_in_list(const Row<T>& R, unsigned n, u64 mass, u64 count, u64 target, u64 band)
 {
     SrShared* S = R.S;
-    const int tid = threadIdx.x;
-    if (!BY_MASS) {
-        const u64 e = S->list[target - 1 - count];
-        return {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
-    }
-    u64 v[SR_BPT], mine = 0;
-#pragma unroll
-    for (int i = 0; i < SR_BPT; ++i) {
-        const unsigned at = tid * SR_BPT + i;
-        v[i] = at < n ? R.W(key_value((unsigned)(S->list[at] >> 32))) : 0;
-        mine += v[i];
-    }
-    const u64 inc = warp_inclusive(mine);
-    if ((tid & 31) == 31) S->ws[tid >> 5] = inc;
-    if (tid == 0) { S->where = n - 1; S->before = ~0ull; }
-    __syncthreads();
-    u64 run = mass + inc - mine;
-    for (int q = 0; q < (tid >> 5); ++q) run += S->ws[q];
-#pragma unroll
-    for (int i = 0; i < SR_BPT; ++i) {
-        if (run < target && run + v[i] >= target) { S->where = tid * SR_BPT + i; S->before = run; S->inside = v[i]; }
-        run += v[i];
+    const unsigned tid = threadIdx.x, full = sort_width(n);
+    if (tid < full) {
+        const u64 e = sort_descending(S, tid < n ? S->list[tid] : 0, full);
+        if (BY_MASS) {
+            const u64 w = tid < n ? R.W(key_value((unsigned)(e >> 32))) : 0;
+            u64 total;
+            const u64 upto = mass + scan_threads(S, w, full, total);
+            if (tid < n && upto - w < target && (upto >= target || tid + 1 == n)) {
+                S->inside = e;
+                // the border is certain if no error of the sums can move it
+                if (upto < target + band || (upto > w && upto - w + band >= target)) S->unsure = 1;
+            }
+        } else if (tid == target - 1 - count) {
+            S->inside = e;
+        }
     }
     __syncthreads();
-    const u64 e = S->list[S->where], before = S->before, upto = before + S->inside;
-    // the border is certain if no error of the sums can move it
-    if (before != ~0ull && (upto < target + band || (before > 0 && before + band >= target)) && tid == 0) S->unsure = 1;
+    const u64 b = S->inside;
     __syncthreads();
-    return {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
+    return {key_value((unsigned)(b >> 32)), (int)~(unsigned)b};
+}
+
+// The token of a row whose candidates are all among the n listed columns.  False if an error bound left a choice open.
+template <typename T>
+__device__ __forceinline__ bool sample_list(const Row<T>& R, unsigned n, int top_k, float top_p, float u, int32_t* token)
+{
+    SrShared* S = R.S;
+    const unsigned tid = threadIdx.x, full = sort_width(n);
+    if (tid == 0) S->unsure = 0;
+    __syncthreads();
+    if (tid < full) {
+        u64 e = tid < n ? S->list[tid] : 0;
+        bool in = tid < n;
+        if (top_k > 0 || top_p < 1.f) {
+            e = sort_descending(S, e, full);
+            in = in && (top_k <= 0 || tid < (unsigned)top_k);
+            if (top_p < 1.f) {
+                const u64 w = in ? R.W(key_value((unsigned)(e >> 32))) : 0;
+                u64 total;
+                const u64 upto = scan_threads(S, w, full, total), target = max((u64)1, fraction(top_p, total, true)), band = R.band(total);
+                if (in && upto - w < target && upto >= target && (upto < target + band || (upto > w && upto - w + band >= target)))
+                    S->unsure = 1;
+                in = in && upto - w < target;
+            }
+        }
+        // what is left, by column
+        e = sort_descending(S, in ? e << 32 | e >> 32 : 0, full);
+        const u64 w = e ? R.W(key_value((unsigned)e)) : 0;
+        u64 total;
+        const u64 upto = scan_threads(S, w, full, total);
+        const u64 target = u < 1.f || !(u == u) ? fraction(u, total, false) : total - 1, band = R.band(total);
+        if (w && upto > target && upto - w <= target) {
+            *token = (int)~(unsigned)(e >> 32);
+            if (upto <= target + band || (upto > w && upto - w + band > target)) S->unsure = 1;
+        }
+    }
+    __syncthreads();
+    const bool open = S->unsure != 0;
+    __syncthreads();
+    return R.W.precise || !open;
 }
 
 // The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`
@@ -592,7 +645,9 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
     u64 mass = BY_MASS ? S->before : 0, count = BY_MASS ? 0 : S->before;  // before the bin
     unsigned klo = 0, khi = 0xffffffffu;
     bool keyed = false;
-    unsigned n = list_sorted(R, least, [&](float x) { return R.bin(x) == b; });
+    if (tid == 0) S->listed = 0;
+    R.sync();
+    unsigned n = list_columns(R, least, true, [&](float x) { return R.bin(x) == b; });
     while (n > SR_LIST) {
         // too many: split the bin's range of keys, down to one key
         if (!keyed) {
@@ -638,8 +693,9 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
         const unsigned top = khi - ((unsigned)sub << sh);
         klo = max(klo, sh ? top - ((1u << sh) - 1u) : top);
         khi = top;
-        __syncthreads();
-        if (n <= SR_LIST) n = list_sorted(R, least, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
+        if (tid == 0) S->listed = 0;
+        R.sync();
+        if (n <= SR_LIST) n = list_columns(R, least, true, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
     }
     if (n <= SR_LIST) return border_in_list<BY_MASS>(R, n, mass, count, target, band);
     // one key, many columns: the last of them taken, in column order
@@ -660,94 +716,46 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
     return B;
 }
 
-// The token of the row into `token` by the CTA that finds it.  False if an error bound left a choice open (never with
-// precise weights).
+// The token of the row into `token` by the CTA that finds it, for rows whose candidates are not listed.  False if an
+// error bound left a choice open (never with precise weights).
 template <typename T>
-__device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, bool few, int32_t* token)
+__device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, int32_t* token)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
     Border B = {R.lmin, 0x7fffffff};
     if (tid == 0) S->unsure = 0;
-    const bool cut_k = top_k > 0 && top_k < R.cols, cut_p = top_p < 1.f;
-    if (cut_k || cut_p) {
-        bool listed = false;
-        unsigned n = 0;
-        if (cut_k || few) {
-            float least = R.lmin;
-            bool bounded = few;
-            if (cut_k && top_k <= SR_NT * R.C) {
-                // the bin that the k-th largest of the threads' maxima lies in: at least k columns reach it
-                clear_histogram(S);
-                if (R.mine >= R.lmin) atomicAdd(&S->count[R.bin(R.mine)], 1u);
-                gather_histogram(R, true, false);
-                block_find(S, S->num, 0, (u64)top_k - 1);
-                if (S->where >= 0) {  // its lower edge, less what the bin's arithmetic may be off
-                    const float edge = R.W.mx - (float)(S->where + 1) * (SR_REACH / SR_NB) * 1.00001f / R.W.c.h;
-                    if (edge > least) least = edge;
-                    bounded = true;
-                }
-                __syncthreads();
-            }
-            if (bounded) {
-                n = list_sorted(R, least, [](float) { return true; });
-                listed = n <= SR_LIST;
-            }
+    if (top_k > 0 && top_k < R.cols) {
+        histogram(R, R.lmin, true, false, [&](int, float x) { return R.bin(x); });
+        if (block_sum(S, S->num, SR_NB) > (u64)top_k) B = find_border<false>(R, R.lmin, (u64)top_k, 0);
+    }
+    if (top_p < 1.f) {
+        // Columns of less than (1 - p) / cols of the maximum's weight hold at most 1 - p of the total: the border
+        // lies above them, and only their sum is needed.
+        const float deep = log2f((float)R.cols / (1.f - fmaxf(top_p, 0.f))) + 1.f;
+        const float shallow = fmaxf(B.tau, R.W.mx - deep / R.W.c.h);
+        clear_histogram(S);
+        u64 rest = 0;
+        R.p.each(B.tau, [&](int col, float x) {
+            if (x == B.tau && col > B.tie) return;
+            const u64 w = R.W(x);
+            if (x >= shallow) add_weight(S, R.bin(x), w);
+            else rest += w;
+        });
+        rest = warp_sum(rest);
+        if ((tid & 31) == 0) S->ws[tid >> 5] = rest;
+        __syncthreads();
+        rest = 0;
+        for (int w = 0; w < SR_NW; ++w) rest += S->ws[w];
+        if (R.C > 1 && tid < R.C) R.of(tid)->r_sum[R.rank] = rest;
+        gather_histogram(R, false, true);
+        if (R.C > 1) {
+            rest = 0;
+            for (int r = 0; r < R.C; ++r) rest += S->r_sum[r];
         }
-        if (listed) {
-            if (cut_k && n > (unsigned)top_k) n = top_k;
-            const u64 e = S->list[n - 1];
-            B = {key_value((unsigned)(e >> 32)), (int)~(unsigned)e};
-            if (cut_p) {
-                u64 mine = 0;
-#pragma unroll
-                for (int i = 0; i < SR_BPT; ++i) {
-                    const unsigned at = tid * SR_BPT + i;
-                    if (at < n) mine += R.W(key_value((unsigned)(S->list[at] >> 32)));
-                }
-                mine = warp_sum(mine);
-                if ((tid & 31) == 0) S->ws[tid >> 5] = mine;
-                __syncthreads();
-                u64 total = 0;
-                for (int w = 0; w < SR_NW; ++w) total += S->ws[w];
-                __syncthreads();
-                B = border_in_list<true>(R, n, 0, 0, max((u64)1, fraction(top_p, total, true)), R.band(total));
-            }
-            __syncthreads();
-        } else {
-            if (cut_k) {
-                histogram(R, R.lmin, true, false, [&](int, float x) { return R.bin(x); });
-                if (block_sum(S, S->num, SR_NB) > (u64)top_k) B = find_border<false>(R, R.lmin, (u64)top_k, 0);
-            }
-            if (cut_p) {
-                // Columns of less than (1 - p) / cols of the maximum's weight hold at most 1 - p of the total: the border
-                // lies above them, and only their sum is needed.
-                const float deep = log2f((float)R.cols / (1.f - fmaxf(top_p, 0.f))) + 1.f;
-                const float shallow = fmaxf(B.tau, R.W.mx - deep / R.W.c.h);
-                clear_histogram(S);
-                u64 rest = 0;
-                R.p.each(B.tau, [&](int col, float x) {
-                    if (x == B.tau && col > B.tie) return;
-                    const u64 w = R.W(x);
-                    if (x >= shallow) add_weight(S, R.bin(x), w);
-                    else rest += w;
-                });
-                rest = warp_sum(rest);
-                if ((tid & 31) == 0) S->ws[tid >> 5] = rest;
-                __syncthreads();
-                rest = 0;
-                for (int w = 0; w < SR_NW; ++w) rest += S->ws[w];
-                if (R.C > 1 && tid < R.C) R.of(tid)->r_sum[R.rank] = rest;
-                gather_histogram(R, false, true);
-                if (R.C > 1) {
-                    rest = 0;
-                    for (int r = 0; r < R.C; ++r) rest += S->r_sum[r];
-                }
-                const u64 total = block_sum(S, S->sum, SR_NB) + rest;
-                const Border Q = find_border<true>(R, shallow, max((u64)1, fraction(top_p, total, true)), R.band(total));
-                if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
-            }
-        }
+        const u64 total = block_sum(S, S->sum, SR_NB) + rest;
+        const Border Q = find_border<true>(R, shallow, max((u64)1, fraction(top_p, total, true)), R.band(total));
+        if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
     }
     // the draw, in column order
     u64 target = 0, total = 0;
@@ -758,7 +766,6 @@ __device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top
             target = u < 1.f || !(u == u) ? fraction(u, sum, false) : sum - 1;
             return target;
         });
-    if (R.C > 1) R.sync();
     if (mine && tid == 0) {
         const u64 band = R.band(total);
         // the chosen column's weight spans [before, before + inside)
@@ -803,35 +810,38 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     R.p.hi = min(cols, R.p.lo + each);
     R.p.c0 = R.p.lo - (int)((reinterpret_cast<uintptr_t>(R.p.g + R.p.lo) & 15u) / sizeof(T));
     R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
-    R.p.per = (R.p.nvec + SR_NW - 1) / SR_NW;
+    R.p.per = ((R.p.nvec + SR_NT - 1) / SR_NT) | 1;
     R.p.kept = 0;
     const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared));
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (tid == SR_NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
+        S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
+        S->reach = mp >= 1.f ? 0.0 : mp > 0.f ? -(double)T_ * log((double)mp) : 0.0;
+    }
+    if (tid == 0) S->listed = 0;
     // the maximum and its lowest column, and the row's part into shared memory
     float v = -INFINITY;
     int idx = 0x7fffffff;
-    {
-        const int w0 = warp * R.p.per, w1 = min(R.p.nvec, w0 + R.p.per);
-        constexpr int DEEP = 8;
-        for (int b = w0 + lane; b < w1; b += 32 * DEEP) {
-            uint4 x[DEEP];
+    constexpr int DEEP = 8;
+    for (int b = tid; b < R.p.nvec; b += SR_NT * DEEP) {
+        uint4 x[DEEP];
 #pragma unroll
-            for (int i = 0; i < DEEP; ++i)
-                if (b + 32 * i < w1) x[i] = R.p.fetch(b + 32 * i);
+        for (int i = 0; i < DEEP; ++i)
+            if (b + SR_NT * i < R.p.nvec) x[i] = R.p.fetch(b + SR_NT * i);
 #pragma unroll
-            for (int i = 0; i < DEEP; ++i)
-                if (b + 32 * i < w1) {
-                    if (stage)
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kept + 16 * (b + 32 * i)), "r"(x[i].x), "r"(x[i].y),
-                                     "r"(x[i].z), "r"(x[i].w) : "memory");
-                    const float m = R.p.largest(x[i]);
-                    if (m > v || (m == v && idx == 0x7fffffff)) {  // columns ascend: an equal one later never wins
-                        v = m;
+        for (int i = 0; i < DEEP; ++i)
+            if (b + SR_NT * i < R.p.nvec) {
+                if (stage)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kept + 16 * (b + SR_NT * i)), "r"(x[i].x), "r"(x[i].y),
+                                 "r"(x[i].z), "r"(x[i].w) : "memory");
+                const float m = R.p.largest(x[i]);
+                if (m > v || (m == v && idx == 0x7fffffff)) {  // columns ascend: an equal one later never wins
+                    v = m;
 #pragma unroll
-                        for (int e = VE - 1; e >= 0; --e)
-                            if (R.p.elem(x[i], e) == m) idx = R.p.c0 + (b + 32 * i) * VE + e;
-                    }
+                    for (int e = VE - 1; e >= 0; --e)
+                        if (R.p.elem(x[i], e) == m) idx = R.p.c0 + (b + SR_NT * i) * VE + e;
                 }
-        }
+            }
     }
     R.mine = v;
     for (int o = 16; o; o >>= 1) {
@@ -846,7 +856,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     for (int w = 1; w < SR_NW; ++w)
         if (S->wf[w] > v || (S->wf[w] == v && S->wi[w] < idx)) { v = S->wf[w]; idx = S->wi[w]; }
     if (C > 1) {
-        cg::this_cluster().sync();  // every CTA of the row has started
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the row has started
         if (tid < C) { R.of(tid)->r_max[rank] = v; R.of(tid)->r_idx[rank] = idx; }
         cg::this_cluster().sync();
         for (int q = 0; q < C; ++q)
@@ -857,11 +867,15 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
         return;
     }
     if (stage) R.p.kept = kept;
-    if (tid == 0) {  // the row's 64-bit arithmetic
-        S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
-        float lmin = fmaxf(v - SR_REACH / S->c.h, -3.402823466e38f);
-        if (mp > 0.f) {  // the least logit l with exp((l - max) / T) >= min_p
-            const double reach = mp >= 1.f ? 0.0 : -(double)T_ * log((double)mp);
+    R.W.c = S->c;
+    R.W.mx = v;
+    R.W.table = S->table;
+    R.W.scale = 62 - (32 - __clz(cols));
+    R.W.precise = false;
+    R.lmin = fmaxf(v - SR_REACH / R.W.c.h, -3.402823466e38f);
+    if (mp > 0.f) {
+        if (tid == 0) {  // the least logit l with exp((l - max) / T) >= min_p
+            const double reach = S->reach;
             float l = (float)((double)v - reach);
             for (int t = 0; t < 4 && (double)v - (double)l > reach; ++t) l = nextafterf(l, INFINITY);
             for (int t = 0; t < 4; ++t) {
@@ -869,21 +883,52 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
                 if ((double)v - (double)below > reach) break;
                 l = below;
             }
-            lmin = fmaxf(lmin, l);
+            S->lmin = l;
         }
-        S->lmin = v == INFINITY ? INFINITY : lmin;
+        __syncthreads();
+        R.lmin = fmaxf(R.lmin, S->lmin);
     }
-    __syncthreads();
-    R.lmin = S->lmin;
-    R.W.mx = v;
-    R.W.c = S->c;
-    R.W.table = S->table;
-    R.W.scale = 62 - (32 - __clz(cols));
+    if (v == INFINITY) R.lmin = INFINITY;
     const float pp = p == p ? p : 1.f;
+    // few candidates: all of them listed by one CTA
+    float least = R.lmin;
+    bool few = mp > 0.f;
+    if (k > 0 && k <= SR_NT) {
+        // the bin that the k-th largest of the threads' maxima lies in: at least k columns reach it
+        clear_histogram(S);
+        if (R.mine >= R.lmin) atomicAdd(&S->count[R.bin(R.mine)], 1u);
+        __syncthreads();
+        block_find(S, S->count, 0, (u64)k - 1);
+        float edge = -INFINITY;  // its lower edge, less what the bin's arithmetic may be off
+        if (S->where >= 0) edge = v - (float)(S->where + 1) * (SR_REACH / SR_NB) * 1.00001f / R.W.c.h;
+        if (C > 1) {  // the best bound of the row's CTAs
+            if (tid < C) R.of(tid)->r_edge[rank] = edge;
+            R.sync();
+            for (int q = 0; q < C; ++q) edge = fmaxf(edge, S->r_edge[q]);
+        }
+        if (edge > -INFINITY) {
+            least = fmaxf(least, edge);
+            few = true;
+        }
+    }
+    if (few) {
+        const unsigned n = list_columns(R, least, false, [](float) { return true; });
+        if (n <= SR_LIST) {
+            if (rank == 0) {
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    R.W.precise = pass != 0;
+                    if (sample_list(R, n, k, pp, u, tokens + r)) break;
+                }
+            }
+            return;
+        }
+        R.sync();  // counts have been read
+    }
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         R.W.precise = pass != 0;
-        if (sample_row(R, k, pp, u, mp > 0.f, tokens + r)) break;
+        if (sample_row(R, k, pp, u, tokens + r)) break;
     }
 }
 
