@@ -10,7 +10,9 @@
 // finds the token.  Otherwise a histogram, linear in the distance to the
 // maximum in octaves of the weight, finds the bin that holds a filter's border, only
 // that bin's columns are listed, and the token is found by sums in column order, per
-// CTA, per thread, and within that thread's columns.
+// CTA, per thread, and within that thread's columns.  Where a filter leaves few
+// columns, their places are gathered first, so that a warp's lanes weigh columns
+// together and not one by one.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
 // part of the row in shared memory beside another CTA's, and to use the SMs when
@@ -43,6 +45,7 @@ constexpr int SR_NB = 1024;           // histogram bins
 constexpr int SR_BPT = SR_NB / SR_NT;
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
 constexpr int SR_LIST = SR_NT;        // columns that are listed at most
+constexpr int SR_IDX = 4096;           // columns of a CTA's part that are gathered at most
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
 
@@ -58,6 +61,7 @@ struct __align__(16) SrShared {
     u64 list[SR_LIST];                            // key << 32 | ~column
     u64 other[SR_LIST];                           // the sort's exchanges between warps
     unsigned base[SR_NW][SR_MAX_C];               // where a warp's listed columns go, in each CTA's list
+    unsigned short idx[SR_IDX];                   // gathered columns, ascending, as places in the part
     uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
     u64 ws[SR_NW];
     float wf[SR_NW];
@@ -267,6 +271,20 @@ struct Part {
             return fmaxf(__low2float(m), __high2float(m));
         }
     }
+    __device__ __forceinline__ float value(int i) const  // column c0 + i
+    {
+        if constexpr (sizeof(T) == 4) {
+            if (!kept) return __ldg(g + c0 + i);
+            float x;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(kept + 4 * i));
+            return x;
+        } else {
+            unsigned short x;
+            if (!kept) x = __ldg(reinterpret_cast<const unsigned short*>(g) + c0 + i);
+            else asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(kept + 2 * i));
+            return __uint_as_float((unsigned)x << 16);
+        }
+    }
     // f(column, logit) for this thread's columns of at least `least`, in ascending order
     template <typename F>
     __device__ __forceinline__ void each(float least, F f) const
@@ -290,6 +308,7 @@ struct Row {
     float lmin;  // columns below it are no candidates
     float mine;  // the largest logit among this thread's columns
     int C, rank, cols;
+    int gathered;  // columns in S->idx, or -1: the part itself is gone through
     SrShared* S;
 
     __device__ __forceinline__ void sync() const
@@ -299,6 +318,20 @@ struct Row {
     }
     __device__ __forceinline__ SrShared* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
     __device__ __forceinline__ int bin(float x) const { return min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1); }
+    // this thread's gathered columns
+    __device__ __forceinline__ int share() const { return (gathered + SR_NT - 1) / SR_NT; }
+    // f(column, logit) for this thread's columns of at least `least`, in ascending order
+    template <typename F>
+    __device__ __forceinline__ void each(float least, F f) const
+    {
+        if (gathered < 0) return p.each(least, f);
+        const int q = share(), e = min(gathered, (int)(threadIdx.x + 1) * q);
+        for (int i = threadIdx.x * q; i < e; ++i) {
+            const int c = S->idx[i];
+            const float x = p.value(c);
+            if (x >= least) f(p.c0 + c, x);
+        }
+    }
     // how far a comparison of two sums of fast weights may be off: 2^-29 of each, a unit per column
     __device__ __forceinline__ u64 band(u64 total) const { return W.precise ? 0 : (total >> 28) + 2ull * cols + 2; }
 };
@@ -390,13 +423,45 @@ __device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, 
 {
     SrShared* S = R.S;
     clear_histogram(S);
-    R.p.each(least, [&](int col, float x) {
+    R.each(least, [&](int col, float x) {
         const int b = put(col, x);
         if (b < 0) return;
         if (counts) atomicAdd(&S->count[b], 1u);
         if (sums) add_weight(S, b, R.W(x));
     });
     gather_histogram(R, counts, sums);
+}
+
+// Gathers this CTA's columns above tau, and those equal to it up to column tie, if there are few.
+template <typename T>
+__device__ void gather_columns(Row<T>& R, float tau, int tie)
+{
+    SrShared* S = R.S;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (R.gathered >= 0 || R.p.nvec * R.p.VE > 65536) return;
+    unsigned n = 0;
+    R.p.each(tau, [&](int col, float x) { n += x > tau || col <= tie; });
+    unsigned inc = n;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+    }
+    __syncthreads();
+    if (lane == 31) S->wi[warp] = inc;
+    __syncthreads();
+    unsigned at = inc - n, all = 0;
+#pragma unroll
+    for (int w = 0; w < SR_NW; ++w) {
+        if (w == warp) at += all;
+        all += S->wi[w];
+    }
+    if (all > SR_IDX) return;
+    if (n)
+        R.p.each(tau, [&](int col, float x) {
+            if (x > tau || col <= tie) S->idx[at++] = (unsigned short)(col - R.p.c0);
+        });
+    R.gathered = all;
+    __syncthreads();
 }
 
 // The columns of at least `least` that take(x) names, of all CTAs, into the S->list (unordered, S->listed set to 0 before)
@@ -407,7 +472,7 @@ __device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
     SrShared* S = R.S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, dests = all ? R.C : 1;
     unsigned n = 0;
-    R.p.each(least, [&](int, float x) { n += take(x); });
+    R.each(least, [&](int, float x) { n += take(x); });
     unsigned inc = n;
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
@@ -419,7 +484,7 @@ __device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
         __syncwarp();
         if (n) {
             unsigned at = inc - n;
-            R.p.each(least, [&](int col, float x) {
+            R.each(least, [&](int col, float x) {
                 if (!take(x)) return;
                 const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
                 for (int r = 0; r < dests; ++r)
@@ -503,7 +568,7 @@ __device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
     const Part<T>& P = R.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     u64 mine = 0;
-    P.each(least, [&](int col, float x) { mine += wt(col, x); });
+    R.each(least, [&](int col, float x) { mine += wt(col, x); });
     const u64 inc = warp_inclusive(mine);
     __syncthreads();
     if (lane == 31) S->ws[warp] = inc;
@@ -529,17 +594,20 @@ __device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
     // the thread whose columns hold it, and its warp: that thread's columns, one per lane
     const unsigned hit = __ballot_sync(0xffffffffu, run <= target && run + mine > target);
     if (hit) {
-        const int l = __ffs(hit) - 1, v0 = (warp * 32 + l) * P.per, n = (min(P.nvec, v0 + P.per) - v0) * P.VE;
-        run = __shfl_sync(0xffffffffu, run, l);
+        const int t = warp * 32 + __ffs(hit) - 1, q = R.gathered < 0 ? P.per * P.VE : R.share();
+        const int first = t * q, n = min(R.gathered < 0 ? P.nvec * P.VE : R.gathered, first + q) - first;
+        run = __shfl_sync(0xffffffffu, run, t & 31);
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + lane;
             u64 w = 0;
             int col = 0;
             if (i < n) {
-                const uint4 r = P.vec(v0 + i / P.VE);
-                const float x = P.elem(r, i % P.VE);
-                col = P.c0 + (v0 + i / P.VE) * P.VE + i % P.VE;
-                if (x >= least) w = wt(col, x);
+                const int c = R.gathered < 0 ? first + i : S->idx[first + i];
+                col = P.c0 + c;
+                if (R.gathered >= 0 || (col >= P.lo && col < P.hi)) {
+                    const float x = P.value(c);
+                    if (x >= least) w = wt(col, x);
+                }
             }
             const u64 sum = warp_inclusive(w);
             const unsigned found = __ballot_sync(0xffffffffu, run + sum > target);
@@ -647,12 +715,19 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
     bool keyed = false;
     if (tid == 0) S->listed = 0;
     R.sync();
-    unsigned n = list_columns(R, least, true, [&](float x) { return R.bin(x) == b; });
+    // the bin's edges, widened by more than its arithmetic may be off, spare most columns the arithmetic
+    float upper = INFINITY, from = least;
+    if (R.W.c.h > 0.f) {
+        const float step = SR_REACH / SR_NB / R.W.c.h;
+        upper = R.W.mx - (float)b * step * 0.99999f;
+        if (b < SR_NB - 1) from = fmaxf(least, R.W.mx - (float)(b + 1) * step * 1.00001f);
+    }
+    unsigned n = list_columns(R, from, true, [&](float x) { return x <= upper && R.bin(x) == b; });
     while (n > SR_LIST) {
         // too many: split the bin's range of keys, down to one key
         if (!keyed) {
             unsigned lo = 0xffffffffu, hi = 0;
-            R.p.each(least, [&](int, float x) {
+            R.each(least, [&](int, float x) {
                 if (R.bin(x) == b) {
                     const unsigned k = order_key(x);
                     lo = min(lo, k);
@@ -719,7 +794,7 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
 // The token of the row into `token` by the CTA that finds it, for rows whose candidates are not listed.  False if an
 // error bound left a choice open (never with precise weights).
 template <typename T>
-__device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top_p, float u, int32_t* token)
+__device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, float u, int32_t* token)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
@@ -736,7 +811,7 @@ __device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top
         const float shallow = fmaxf(B.tau, R.W.mx - deep / R.W.c.h);
         clear_histogram(S);
         u64 rest = 0;
-        R.p.each(B.tau, [&](int col, float x) {
+        R.each(B.tau, [&](int col, float x) {
             if (x == B.tau && col > B.tie) return;
             const u64 w = R.W(x);
             if (x >= shallow) add_weight(S, R.bin(x), w);
@@ -758,6 +833,7 @@ __device__ __forceinline__ bool sample_row(const Row<T>& R, int top_k, float top
         if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
     }
     // the draw, in column order
+    if (top_k > 0 || top_p < 1.f) gather_columns(R, B.tau, B.tie);
     u64 target = 0, total = 0;
     const bool mine = find_in_order(
         R, B.tau, [&](int col, float x) { return x == B.tau && col > B.tie ? (u64)0 : R.W(x); },
@@ -812,6 +888,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
     R.p.per = ((R.p.nvec + SR_NT - 1) / SR_NT) | 1;
     R.p.kept = 0;
+    R.gathered = -1;
     const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared));
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (tid == SR_NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
@@ -924,11 +1001,15 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
             return;
         }
         R.sync();  // counts have been read
+        R.lmin = least;
+        gather_columns(R, least, 0x7fffffff);
     }
+    const int gathered = R.gathered;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         R.W.precise = pass != 0;
         if (sample_row(R, k, pp, u, tokens + r)) break;
+        R.gathered = gathered;  // not those of the first pass's border
     }
 }
 
