@@ -1,5 +1,6 @@
 // Paged key/value cache: mfs_kv_append (rotate and write new tokens) and
 // mfs_paged_attention (one new token per sequence).
+#include <string.h>
 #include <type_traits>
 
 #include "mfs_ops.cuh"
@@ -51,85 +52,158 @@ __device__ __forceinline__ float from_f(float x) { return x; }
 template <>
 __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x); }
 
+// A block takes a few tokens: one warp per token finds its sequence, position and row in the cache, and the cosines and
+// sines of its angles; the block's threads then move items of two 16-byte vectors that hold whole pairs (neighbours for
+// interleaved pairs, half a head apart for split ones), with the first of them on its way while the angles are found.
+// What bounds it is memory: each input is read and each output written once.
 constexpr int AP_THREADS = 256;
+constexpr int AP_TOKENS = 4;   // tokens per block; 1 where that leaves SMs without a block
+constexpr int AP_AHEAD = 3;    // items a thread has on their way
 
-// One block per token: its position's cosines and sines once, then a pair of elements per thread and step.
 template <typename T>
-__global__ void __launch_bounds__(AP_THREADS) append_kernel(Cache C, int n_seqs, int n_tokens, const int32_t* __restrict__ cu,
-                                                            const int32_t* __restrict__ kv_len, const T* q, long long q_stride,
-                                                            int hq, T* q_out, long long q_out_stride, const T* k,
-                                                            long long k_stride, T* k_out, long long k_out_stride, const T* v,
-                                                            long long v_stride, int hd, int rope,
-                                                            const __grid_constant__ Turns turns)
+struct ApArgs {
+    Cache C;
+    const int32_t *cu, *kv_len;
+    const T *q, *k, *v;
+    T *q_out, *k_out;
+    long long q_stride, q_out_stride, k_stride, k_out_stride, v_stride;
+    int n_tokens, n_seqs, hq, rope;
+    Turns turns;
+};
+
+template <typename T>
+struct Vec2 {
+    uint4 a, b;
+};
+
+template <typename T, int HD, int TT>
+__global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constant__ ApArgs<T> A)
 {
-    __shared__ float sc[64], ss[64];
-    __shared__ long long s_row;
-    const int t = blockIdx.x, half = hd / 2;
-    // the sequence: the last s with cu[s] <= t
-    int lo = 0, hi = n_seqs;
-    while (hi - lo > 1) {
-        const int m = (lo + hi) / 2;
-        if (__ldg(cu + m) <= t) lo = m; else hi = m;
+    constexpr int VE = 16 / sizeof(T);        // elements per vector
+    constexpr int IPH = HD / (2 * VE);        // items per head
+    constexpr int HALF = HD / 2;
+    __shared__ float2 cs[TT][HALF];
+    __shared__ long long row[TT];             // element offset of the token's row (head 0) in the cache; -1: none; -2: no token
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int t0 = blockIdx.x * TT, nt = min(TT, A.n_tokens - t0);
+    const int hkv = A.C.n_kv_heads, heads = A.hq + 2 * hkv, items = nt * heads * IPH;
+    const bool split = A.rope == MFS_ROPE_HALF;
+
+    // item i: token, head (queries, keys, values), place within the head
+    auto where = [&](int i, int& t, int& h, int& e) {
+        const int hh = i / IPH;
+        e = i % IPH;
+        t = TT == 1 ? 0 : hh / heads;
+        h = TT == 1 ? hh : hh - t * heads;
+    };
+    auto source = [&](int i) {
+        int t, h, e;
+        where(i, t, h, e);
+        const long long tok = t0 + t;
+        const T* p = h < A.hq ? A.q + tok * A.q_stride + h * HD : h < A.hq + hkv ? A.k + tok * A.k_stride + (h - A.hq) * HD
+                                                                              : A.v + tok * A.v_stride + (h - A.hq - hkv) * HD;
+        const int first = split ? e * VE : 2 * e * VE, second = split ? first + HALF : first + VE;
+        // plain loads: the queries and keys may be their own outputs
+        return Vec2<T>{*reinterpret_cast<const uint4*>(p + first), *reinterpret_cast<const uint4*>(p + second)};
+    };
+    Vec2<T> x[AP_AHEAD];
+#pragma unroll
+    for (int j = 0; j < AP_AHEAD; ++j)
+        if (tid + j * AP_THREADS < items) x[j] = source(tid + j * AP_THREADS);
+
+    if (warp < nt) {
+        // the sequence: the last s with cu[s] <= token, 32 places at a time
+        const int t = t0 + warp;
+        int lo = 0, size = A.n_seqs;
+        while (size > 1) {
+            const int step = (size + 31) / 32, at = lane * step;
+            const unsigned m = __ballot_sync(0xffffffffu, at < size && __ldg(A.cu + lo + at) <= t);
+            const int c = max(0, 31 - __clz(m));  // the last probe that is not past the token
+            lo += c * step;
+            size = min(step, size - c * step);
+        }
+        const int begin = __ldg(A.cu + lo), end = __ldg(A.cu + lo + 1);
+        const long long pos = (long long)__ldg(A.kv_len + lo) - end + t;
+        if (lane == 0) row[warp] = t < begin || t >= end ? -2 : pos < 0 || pos > 0x7fffffff ? -1 : row_offset(A.C, lo, (int)pos);
+        if (A.rope)
+            for (int i = lane; i < HALF; i += 32) {
+                const double a = (double)pos * A.turns.f[i];
+                float s, c;
+                sincospif(2.f * (float)(a - rint(a)), &s, &c);
+                cs[warp][i] = make_float2(c, s);
+            }
     }
-    const int end = __ldg(cu + lo + 1);
-    if (t < __ldg(cu) || t >= end) return;  // a row of no sequence
-    const long long pos = (long long)__ldg(kv_len + lo) - end + t;
-    if (threadIdx.x < half) {
-        const double a = (double)pos * turns.f[threadIdx.x];
-        float s = 0.f, c = 1.f;
-        if (rope) sincospif(2.f * (float)(a - rint(a)), &s, &c);
-        sc[threadIdx.x] = c;
-        ss[threadIdx.x] = s;
-    }
-    if (threadIdx.x == AP_THREADS - 1) s_row = pos < 0 || pos > 0x7fffffff ? -1 : row_offset(C, lo, (int)pos);
     __syncthreads();
-    const long long row = s_row;
-    T* kc = reinterpret_cast<T*>(C.k);
-    T* vc = reinterpret_cast<T*>(C.v);
-    const int hkv = C.n_kv_heads;
-    for (int i = threadIdx.x; i < (hq + hkv) * half; i += AP_THREADS) {
-        const int h = i / half, e = i % half;
-        const int e0 = rope == MFS_ROPE_HALF ? e : 2 * e, e1 = rope == MFS_ROPE_HALF ? e + half : 2 * e + 1;
-        const bool is_q = h < hq;
-        const int hh = is_q ? h : h - hq;
-        const T* src = (is_q ? q + (long long)t * q_stride : k + (long long)t * k_stride) + hh * hd;
-        const float a = to_f(src[e0]), b = to_f(src[e1]);
-        T x = src[e0], y = src[e1];
-        if (rope) {
-            x = from_f<T>(a * sc[e] - b * ss[e]);
-            y = from_f<T>(a * ss[e] + b * sc[e]);
-        }
-        if (is_q) {
-            T* dst = q_out + (long long)t * q_out_stride + hh * hd;
-            dst[e0] = x;
-            dst[e1] = y;
-        } else {
-            if (k_out) {
-                T* dst = k_out + (long long)t * k_out_stride + hh * hd;
-                dst[e0] = x;
-                dst[e1] = y;
+
+    auto finish = [&](int i, Vec2<T> y) {
+        int t, h, e;
+        where(i, t, h, e);
+        const long long r = row[t];
+        if (r == -2) return;
+        const long long tok = t0 + t;
+        const int first = split ? e * VE : 2 * e * VE, second = split ? first + HALF : first + VE;
+        if (h < A.hq + hkv && A.rope) {
+            T in[2 * VE], out[2 * VE];
+            memcpy(in, &y, 32);
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+                // pair j of the item: elements (j, j + VE) of the two vectors for split pairs, (2 j, 2 j + 1) for neighbours
+                const float2 c = cs[t][e * VE + j];
+                const float u = to_f(split ? in[j] : in[2 * j]), w = to_f(split ? in[j + VE] : in[2 * j + 1]);
+                const T a = from_f<T>(u * c.x - w * c.y), b = from_f<T>(u * c.y + w * c.x);
+                if (split) { out[j] = a; out[j + VE] = b; }
+                else { out[2 * j] = a; out[2 * j + 1] = b; }
             }
-            if (row >= 0) {
-                T* dst = kc + row + (long long)hh * C.head_stride;
-                dst[e0] = x;
-                dst[e1] = y;
-            }
+            memcpy(&y, out, 32);
         }
+        auto put = [&](T* p) {
+            *reinterpret_cast<uint4*>(p + first) = y.a;
+            *reinterpret_cast<uint4*>(p + second) = y.b;
+        };
+        if (h < A.hq) {
+            put(A.q_out + tok * A.q_out_stride + h * HD);
+        } else if (h < A.hq + hkv) {
+            if (A.k_out) put(A.k_out + tok * A.k_out_stride + (h - A.hq) * HD);
+            if (r >= 0) put(reinterpret_cast<T*>(A.C.k) + r + (long long)(h - A.hq) * A.C.head_stride);
+        } else if (r >= 0) {
+            put(reinterpret_cast<T*>(A.C.v) + r + (long long)(h - A.hq - hkv) * A.C.head_stride);
+        }
+    };
+    for (int i = tid; i < items; i += AP_AHEAD * AP_THREADS) {
+        Vec2<T> y[AP_AHEAD];
+#pragma unroll
+        for (int j = 0; j < AP_AHEAD; ++j) y[j] = x[j];
+#pragma unroll
+        for (int j = 0; j < AP_AHEAD; ++j)
+            if (i + (AP_AHEAD + j) * AP_THREADS < items) x[j] = source(i + (AP_AHEAD + j) * AP_THREADS);
+#pragma unroll
+        for (int j = 0; j < AP_AHEAD; ++j)
+            if (i + j * AP_THREADS < items) finish(i + j * AP_THREADS, y[j]);
     }
-    if (row < 0) return;
-    for (int i = threadIdx.x; i < hkv * hd; i += AP_THREADS)
-        vc[row + (long long)(i / hd) * C.head_stride + i % hd] = v[(long long)t * v_stride + i];
+}
+
+template <typename T, int HD>
+int append(const ApArgs<T>& A, cudaStream_t st)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) {
+        if (A.n_tokens < 2 * AP_TOKENS * sms) append_kernel<T, HD, 1><<<A.n_tokens, AP_THREADS, 0, st>>>(A);
+        else append_kernel<T, HD, AP_TOKENS><<<(A.n_tokens + AP_TOKENS - 1) / AP_TOKENS, AP_THREADS, 0, st>>>(A);
+        e = cudaGetLastError();
+    }
+    return mfs::op_launched("kv_append", e);
 }
 
 template <typename T>
-int append(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len, const void* q, long long q_stride,
-           int hq, void* q_out, long long q_out_stride, const void* k, long long k_stride, void* k_out, long long k_out_stride,
-           const void* v, long long v_stride, int hd, int rope, const Turns& turns, cudaStream_t st)
+int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len, const void* q, long long q_stride,
+                 int hq, void* q_out, long long q_out_stride, const void* k, long long k_stride, void* k_out,
+                 long long k_out_stride, const void* v, long long v_stride, int hd, int rope, const Turns& turns, cudaStream_t st)
 {
-    append_kernel<T><<<n_tokens, AP_THREADS, 0, st>>>(C, n_seqs, n_tokens, cu, kv_len, (const T*)q, q_stride, hq, (T*)q_out,
-                                                     q_out_stride, (const T*)k, k_stride, (T*)k_out, k_out_stride,
-                                                     (const T*)v, v_stride, hd, rope, turns);
-    return mfs::op_launched("kv_append", cudaGetLastError());
+    const ApArgs<T> A = {C, cu, kv_len, (const T*)q, (const T*)k, (const T*)v, (T*)q_out, (T*)k_out, q_stride, q_out_stride, k_stride,
+                         k_out_stride, v_stride, n_tokens, n_seqs, hq, rope, turns};
+    return hd == 128 ? append<T, 128>(A, st) : append<T, 64>(A, st);
 }
 
 // --------------------------------------------------------------- attention
@@ -789,9 +863,9 @@ extern "C" int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs
     const int hq = q ? n_q_heads : 0;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     return cache->dtype == MFS_DTYPE_BF16
-               ? append<bf16>(C, n_tokens, n_seqs, cu, kv_len, q, q_stride, hq, q_out, q_out_stride, k, k_stride, k_out,
+               ? append_typed<bf16>(C, n_tokens, n_seqs, cu, kv_len, q, q_stride, hq, q_out, q_out_stride, k, k_stride, k_out,
                               k_out_stride, v, v_stride, hd, rope, turns, st)
-               : append<float>(C, n_tokens, n_seqs, cu, kv_len, q, q_stride, hq, q_out, q_out_stride, k, k_stride, k_out,
+               : append_typed<float>(C, n_tokens, n_seqs, cu, kv_len, q, q_stride, hq, q_out, q_out_stride, k, k_stride, k_out,
                                k_out_stride, v, v_stride, hd, rope, turns, st);
 }
 
