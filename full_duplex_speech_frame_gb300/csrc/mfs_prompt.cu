@@ -22,65 +22,15 @@
 // computed again at the end by a plain pass in fp32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 #include "mfs_ops.cuh"
 
 namespace {
 
 using bf16 = __nv_bfloat16;
-__device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(bf16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-// One warp per (token, query head): a running maximum and sum over the row's keys, HD / 32 elements per lane.
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(int n_tokens, int n_seqs, const int32_t* __restrict__ cu,
-                                                          const T* __restrict__ q, long long q_stride, int hq,
-                                                          const T* __restrict__ k, long long k_stride, const T* __restrict__ v,
-                                                          long long v_stride, int hkv, T* out, long long out_stride, float scale,
-                                                          int window)
-{
-    constexpr int E = HD / 32;
-    const int t = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (h >= hq) return;
-    int lo = 0, hi = n_seqs;
-    while (hi - lo > 1) {
-        const int m = (lo + hi) / 2;
-        if (__ldg(cu + m) <= t) lo = m; else hi = m;
-    }
-    int b = max(0, __ldg(cu + lo));
-    if (t < b || t >= __ldg(cu + lo + 1)) return;
-    if (window > 0) b = max(b, t - window + 1);
-    const int kvh = h / (hq / hkv);
-    float qf[E], o[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        qf[e] = to_f(q[(long long)t * q_stride + h * HD + lane * E + e]) * scale;
-        o[e] = 0.f;
-    }
-    for (int j = b; j <= t; ++j) {
-        const T* kr = k + (long long)j * k_stride + kvh * HD + lane * E;
-        const T* vr = v + (long long)j * v_stride + kvh * HD + lane * E;
-        float a = 0.f;
-        for (int e = 0; e < E; ++e) a = fmaf(qf[e], to_f(kr[e]), a);
-        for (int x = 16; x; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-        const float mn = fmaxf(m, a), c = m == mn ? 1.f : expf(m - mn), p = a == mn ? 1.f : expf(a - mn);
-        l = l * c + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * to_f(vr[e]);
-        m = mn;
-    }
-    for (int e = 0; e < E; ++e) put(out + (long long)t * out_stride + h * HD + lane * E + e, o[e] / l);
-}
-
-template <typename T, int HD>
-int run(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride, int hq, const void* k, long long k_stride,
-        const void* v, long long v_stride, int hkv, void* out, long long out_stride, float scale, int window, cudaStream_t st)
-{
-    prompt_rows_kernel<T, HD><<<dim3((unsigned)n_tokens, (unsigned)((hq + 3) / 4)), 128, 0, st>>>(
-        n_tokens, n_seqs, cu, (const T*)q, q_stride, hq, (const T*)k, k_stride, (const T*)v, v_stride, hkv, (T*)out, out_stride,
-        scale, window);
-    return mfs::op_launched("prompt_attention", cudaGetLastError());
-}
 
 // ------------------------------------------------------------- tensor cores
 
@@ -330,37 +280,42 @@ __device__ __forceinline__ void done_with_item(PtBars& B, int i)
     if ((threadIdx.x & 31) == 0) bar_arrive(&B.work_empty[i & 3]);
 }
 
-// Deals out the call's blocks.  Pairs (row block, sequence) are ordered by block number, largest first (about the
+// Deals out the call's blocks of ROWS rows.  Pairs (row block, sequence) are ordered by block number, largest first (about the
 // number of their keys), then by sequence; an item is a pair and a head, heads innermost, so that neighbouring CTAs
 // share keys; round r of G items goes to the CTAs in ascending order for even r, descending for odd r.
+template <int ROWS>
 struct PtDealer {
-    const PtArgs& A;
+    const int32_t* cu;
+    int n_tokens, n_seqs, hq;
     int level, above, upto;  // the current block number; pairs of larger numbers; those and its own
 
     __device__ __forceinline__ int blocks(int s, int& b, int& len) const
     {
-        b = min(max(__ldg(A.cu + s), 0), A.n_tokens);
-        len = max(min(__ldg(A.cu + s + 1), A.n_tokens) - b, 0);
-        return (len + PT_BLOCK - 1) / PT_BLOCK;
+        b = min(max(__ldg(cu + s), 0), n_tokens);
+        len = max(min(__ldg(cu + s + 1), n_tokens) - b, 0);
+        return (len + ROWS - 1) / ROWS;
     }
     __device__ int pairs_from(int lv) const
     {
         int n = 0, b, len;
-        for (int s = threadIdx.x & 31; s < A.n_seqs; s += 32) n += max(0, blocks(s, b, len) - lv);
+        for (int s = threadIdx.x & 31; s < n_seqs; s += 32) n += max(0, blocks(s, b, len) - lv);
         return __reduce_add_sync(0xffffffffu, n);
     }
-    __device__ __forceinline__ PtDealer(const PtArgs& a) : A(a), level(0), above(0), upto(0) {}
+    __device__ __forceinline__ PtDealer(const int32_t* cu_, int n_tokens_, int n_seqs_, int hq_)
+        : cu(cu_), n_tokens(n_tokens_), n_seqs(n_seqs_), hq(hq_), level(0), above(0), upto(0)
+    {
+    }
     __device__ void start()
     {
         int n = 0, b, len;
-        for (int s = threadIdx.x & 31; s < A.n_seqs; s += 32) n = max(n, blocks(s, b, len));
+        for (int s = threadIdx.x & 31; s < n_seqs; s += 32) n = max(n, blocks(s, b, len));
         level = __reduce_max_sync(0xffffffffu, n);
     }
     // item r of this CTA, false: there is none
     __device__ bool get(int r, PtWork& w)
     {
         const long long G = gridDim.x, it = r * G + (r & 1 ? G - 1 - blockIdx.x : blockIdx.x);
-        const long long pair = it / A.hq;
+        const long long pair = it / hq;
         while (pair >= upto) {
             if (level == 0) return false;
             --level;
@@ -369,17 +324,17 @@ struct PtDealer {
         }
         int k = (int)(pair - above);  // the k-th sequence with such a block
         const int lane = threadIdx.x & 31;
-        for (int s0 = 0; s0 < A.n_seqs; s0 += 32) {
+        for (int s0 = 0; s0 < n_seqs; s0 += 32) {
             int b = 0, len = 0;
-            const bool has = s0 + lane < A.n_seqs && blocks(s0 + lane, b, len) > level;
+            const bool has = s0 + lane < n_seqs && blocks(s0 + lane, b, len) > level;
             unsigned m = __ballot_sync(0xffffffffu, has);
             if (k >= __popc(m)) { k -= __popc(m); continue; }
             while (k--) m &= m - 1;
             const int l = __ffs(m) - 1;
             w.b = __shfl_sync(0xffffffffu, b, l);
             w.len = __shfl_sync(0xffffffffu, len, l);
-            w.r0 = level * PT_BLOCK;
-            w.h = (int)(it % A.hq);
+            w.r0 = level * ROWS;
+            w.h = (int)(it % hq);
             return true;
         }
         return false;
@@ -450,7 +405,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&B.tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    PtDealer deal(A);
+    PtDealer<PT_BLOCK> deal(A.cu, A.n_tokens, A.n_seqs, A.hq);
     if (warp == 11) deal.start();
     if (tid == 9 * 32) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
@@ -672,7 +627,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         const int x = warp >> 2, row = tid & (PT_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * PT_M, to = tm + lanes + 2 * PT_M + x * HD;
-        const float c = A.c;
         unsigned s_par = 0, o_par = 0;
         bool ok = true;
         for (int i = 0;; ++i) {
@@ -794,6 +748,209 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
     }
 }
 
+// --------------------------------------------------------------------- fp32
+//
+// On the CUDA cores: a CTA of 256 threads takes 128 query rows of one sequence and head and walks over
+// tiles of 64 keys in shared memory.  A thread has 8 rows x 4 keys of the scores and 8 rows x HD / 16
+// elements of the output in registers (rows and keys 16 apart, so that a warp's 16-byte loads meet no
+// bank twice), with paired fp32 products; a row's maximum and sum go over half a warp.  Keys of the next
+// tile are copied while the values of this one are summed, and the other way round.  What bounds it is
+// the fp32 rate.  In tiles that some row does not see whole, unseen products are left out, not
+// multiplied by zero.
+
+constexpr int PF_ROWS = 128, PF_KEYS = 64, PF_THREADS = 256;
+
+template <int HD>
+struct PfShape {
+    static constexpr int LD = HD + 4, LP = PF_KEYS + 4;  // row strides in shared memory
+    static constexpr int BYTES = 4 * ((PF_ROWS + 2 * PF_KEYS) * LD + PF_ROWS * LP);
+};
+
+struct PfArgs {
+    const int32_t* cu;
+    const float *q, *k, *v;
+    float* out;
+    long long q_stride, k_stride, v_stride, out_stride;
+    int n_tokens, n_seqs, hq, g, window;
+    float c;  // scale * log2(e)
+};
+
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool full)
+{
+    const int n = full ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst)), "l"(src), "r"(n) : "memory");
+}
+
+template <int HD>
+__global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_constant__ PfArgs A)
+{
+    using S = PfShape<HD>;
+    constexpr int LD = S::LD, LP = S::LP, OC = HD / 16;
+    extern __shared__ __align__(16) float pf_raw[];
+    float *sq = pf_raw, *sk = sq + PF_ROWS * LD, *sv = sk + PF_KEYS * LD, *sp = sv + PF_KEYS * LD;
+    __shared__ PtWork work;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    if (tid < 32) {
+        PtDealer<PF_ROWS> deal(A.cu, A.n_tokens, A.n_seqs, A.hq);
+        deal.start();
+        PtWork w;
+        if (!deal.get(0, w)) w.h = -1;
+        if (tid == 0) work = w;
+    }
+    __syncthreads();
+    const PtWork w = work;
+    if (w.h < 0) return;
+    const int rows = min(PF_ROWS, w.len - w.r0), W = A.window;
+    const float* kg = A.k + (long long)w.b * A.k_stride + w.h / A.g * HD;
+    const float* vg = A.v + (long long)w.b * A.v_stride + w.h / A.g * HD;
+    auto copy_tile = [&](float* dst, const float* src, long long stride, int r0, int n, int limit) {
+        for (int i = tid; i < n * (HD / 4); i += PF_THREADS) {
+            const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+            const bool in = r0 + r < limit;
+            copy16(dst + r * LD + c, src + (in ? (long long)(r0 + r) * stride + c : 0), in);
+        }
+    };
+    const int t0 = (W > 0 ? max(0, w.r0 - W + 1) : 0) / PF_KEYS, t1 = (w.r0 + rows - 1) / PF_KEYS + 1;
+    copy_tile(sq, A.q + (long long)(w.b + w.r0) * A.q_stride + w.h * HD, A.q_stride, 0, PF_ROWS, rows);
+    copy_tile(sk, kg, A.k_stride, t0 * PF_KEYS, PF_KEYS, w.len);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    copy_tile(sv, vg, A.v_stride, t0 * PF_KEYS, PF_KEYS, w.len);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+
+    float o[8][OC], m[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < OC; ++e) o[i][e] = 0.f;
+    }
+    for (int t = t0; t < t1; ++t) {
+        const int k0 = t * PF_KEYS;
+        // some row does not see some key
+        const bool edge = k0 + PF_KEYS - 1 > w.r0 || (W > 0 && k0 <= w.r0 + rows - 1 - W);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys
+        __syncthreads();
+        uint64_t acc[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll 4
+        for (int e = 0; e < HD; e += 4) {
+            ulonglong2 k4[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * LD + e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(sq + (ty + 16 * i) * LD + e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fma2(q4.y, k4[j].y, fma2(q4.x, k4[j].x, acc[i][j]));
+            }
+        }
+        __syncthreads();  // all have read the keys
+        if (t + 1 < t1) copy_tile(sk, kg, A.k_stride, k0 + PF_KEYS, PF_KEYS, w.len);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = w.r0 + ty + 16 * i;
+            float s[4], mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float a, b;
+                unpair(acc[i][j], a, b);
+                s[j] = a + b;
+                const int key = k0 + tx + 16 * j;
+                if (edge && (key > row || (W > 0 && key <= row - W))) s[j] = -INFINITY;
+                mx = fmaxf(mx, s[j]);
+            }
+            for (int x = 8; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mn = fmaxf(m[i], mx), a = m[i] == mn ? 1.f : exp2f((m[i] - mn) * A.c);
+            const float sub = mn == -INFINITY ? 0.f : mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f((s[j] - sub) * A.c);
+                sum += p;
+                sp[(ty + 16 * i) * LP + tx + 16 * j] = p;
+            }
+            m[i] = mn;
+            l[i] = l[i] * a + sum;
+#pragma unroll
+            for (int e = 0; e < OC; ++e) o[i][e] *= a;
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // the values
+        __syncthreads();
+        auto product = [&](auto part) {  // part: some keys are left out
+#pragma unroll 2
+            for (int j = 0; j < PF_KEYS; j += 4) {
+                float4 p4[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint64_t v2[OC / 2];
+#pragma unroll
+                    for (int e = 0; e < OC / 4; ++e) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sv + (j + x) * LD + 4 * tx + 64 * e);
+                        v2[2 * e] = y.x;
+                        v2[2 * e + 1] = y.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p = x == 0 ? p4[i].x : x == 1 ? p4[i].y : x == 2 ? p4[i].z : p4[i].w;
+                        if (decltype(part)::value) {
+                            const int row = w.r0 + ty + 16 * i, key = k0 + j + x;
+                            if (key > row || (W > 0 && key <= row - W)) continue;
+                        }
+                        const uint64_t pp = pair(p, p);
+#pragma unroll
+                        for (int e = 0; e < OC / 2; ++e) {
+                            const uint64_t r = fma2(pp, v2[e], pair(o[i][2 * e], o[i][2 * e + 1]));
+                            unpair(r, o[i][2 * e], o[i][2 * e + 1]);
+                        }
+                    }
+                }
+            }
+        };
+        if (edge) product(std::true_type());
+        else product(std::false_type());
+        __syncthreads();  // all have read the values
+        if (t + 1 < t1) copy_tile(sv, vg, A.v_stride, k0 + PF_KEYS, PF_KEYS, w.len);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float sum = l[i];
+        for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int r = ty + 16 * i;
+        if (r >= rows) continue;
+        float* p = A.out + (long long)(w.b + w.r0 + r) * A.out_stride + w.h * HD;
+#pragma unroll
+        for (int e = 0; e < OC / 4; ++e)
+            *reinterpret_cast<float4*>(p + 4 * tx + 64 * e) =
+                make_float4(o[i][4 * e] / sum, o[i][4 * e + 1] / sum, o[i][4 * e + 2] / sum, o[i][4 * e + 3] / sum);
+    }
+}
+
+template <int HD>
+int run_f32(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride, int hq, const void* k, long long k_stride,
+            const void* v, long long v_stride, int hkv, void* out, long long out_stride, float scale, int window, cudaStream_t st)
+{
+    const char* op = "prompt_attention";
+    const PfArgs A = {cu, (const float*)q, (const float*)k, (const float*)v, (float*)out, q_stride, k_stride, v_stride, out_stride,
+                      n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
+    const long long blocks = ((long long)n_tokens / PF_ROWS + n_seqs) * hq;  // blocks there can be
+    if (blocks > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many tokens and sequences");
+    cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<HD>::BYTES);
+    if (e == cudaSuccess) {
+        prompt_f32_kernel<HD><<<(unsigned)blocks, PF_THREADS, PfShape<HD>::BYTES, st>>>(A);
+        e = cudaGetLastError();
+    }
+    return mfs::op_launched(op, e);
+}
+
 template <int HD>
 int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride, int hq, const void* k, long long k_stride,
             const void* v, long long v_stride, int hkv, void* out, long long out_stride, float scale, int window, cudaStream_t st)
@@ -856,6 +1013,6 @@ extern "C" int mfs_prompt_attention(int dtype, int n_tokens, int n_seqs, const i
         return mfs::op_fail(MFS_E_ARG, op, "pointers and token strides must be multiples of 16 bytes, a stride at least heads x head_dim");
     cudaStream_t st = (cudaStream_t)cuda_stream;
     auto fn = dtype == MFS_DTYPE_BF16 ? (head_dim == 128 ? run_mma<128> : run_mma<64>)
-                                      : (head_dim == 128 ? run<float, 128> : run<float, 64>);
+                                      : (head_dim == 128 ? run_f32<128> : run_f32<64>);
     return fn(n_tokens, n_seqs, cu, q, q_stride, n_q_heads, k, k_stride, v, v_stride, n_kv_heads, out, out_stride, scale, window, st);
 }
