@@ -378,47 +378,50 @@ def mfs_rvq_encode(z_sem, z_ac, codebooks, codes, stream=None) -> None:
 
 
 # ------------------------------------------------- operators on device tensors
+# These calls take microseconds on the GPU, so their checks build nothing that is not needed.
 
-def _need(ok: bool, message: str) -> None:
-    if not ok:
-        raise MfsError(-1, message)
+def _refuse(message: str):
+    raise MfsError(-1, message)
 
 
 def _dtype_code(t) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MFS_DTYPE_BF16
-    _need(t.dtype == torch.float32, f"dtype {t.dtype}: need float32 or bfloat16")
+    if t.dtype is not torch.float32:
+        _refuse(f"dtype {t.dtype}: need float32 or bfloat16")
     return MFS_DTYPE_F32
 
 
-def _array(t, what: str, n: int, dtype, device):
-    """Data pointer of a contiguous 1-D CUDA tensor of at least n elements (None: null)."""
+def _array(t, what: str, n: int, dtype, dev: int):
+    """Data pointer of a contiguous 1-D tensor of at least n elements on CUDA device `dev` (None: null)."""
     if t is None:
         return None
-    _need(t.dtype == dtype and t.dim() == 1 and t.shape[0] >= n and t.device == device and (n <= 1 or t.stride(0) == 1),
-          f"{what}: need a contiguous {dtype} tensor of {n} elements on {device}")
+    if t.dtype is not dtype or t.dim() != 1 or t.size(0) < n or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        _refuse(f"{what}: need a contiguous {dtype} tensor of {n} elements on cuda:{dev}")
     return t.data_ptr()
 
 
-def _rows(t, what: str, n: int, heads: int, head_dim: int, like):
+def _rows(t, what: str, n: int, heads: int, head_dim: int, dtype, dev: int):
     """(data pointer, token stride) of a [tokens, heads, head_dim] tensor whose heads are dense."""
-    _need(t.dim() == 3 and t.dtype == like.dtype and t.device == like.device and t.shape[0] == n and t.shape[1] == heads and
-          t.shape[2] == head_dim and t.stride(2) == 1 and (heads == 1 or t.stride(1) == head_dim),
-          f"{what}: need {like.dtype} [{n}, {heads}, {head_dim}] with dense heads on {like.device}")
-    return t.data_ptr(), t.stride(0) if n > 1 else heads * head_dim
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (n, heads, head_dim):
+        _refuse(f"{what}: need {dtype} [{n}, {heads}, {head_dim}] on cuda:{dev}")
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+        _refuse(f"{what}: need dense heads")
+    return t.data_ptr(), stride[0] if n > 1 else heads * head_dim
 
 
-def _enqueue(device, stream, name: str, *args) -> None:
-    """Call a library function (its last argument: the stream) with `device` current."""
+def _enqueue(dev: int, stream, fn, *args) -> None:
+    """Call a library function (its last argument: the stream) with CUDA device `dev` current."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = getattr(_lib, name)(*args, stream)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            rc = getattr(_lib, name)(*args, stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
     if rc != MFS_OK:
         _check(None, rc)
 
@@ -428,9 +431,13 @@ def mfs_sample_rows(logits, uniforms, tokens, temperature=None, top_k=None, top_
     stride) with uniforms[r]: temperature, min-p, top-k and top-p from per-row CUDA tensors, or
     None (see include/mfs.h); enqueued on `stream` (default: torch's current stream)."""
     import torch
-    _need(logits.is_cuda and logits.dim() == 2 and (logits.shape[1] <= 1 or logits.stride(1) == 1), "logits: need a 2-D CUDA tensor with unit column stride")
-    (rows, cols), dev, f32, i32 = logits.shape, logits.device, torch.float32, torch.int32
-    _enqueue(dev, stream, "mfs_sample_rows", logits.data_ptr(), _dtype_code(logits), rows, cols,
+    if not logits.is_cuda or logits.dim() != 2:
+        _refuse("logits: need a 2-D CUDA tensor")
+    rows, cols = logits.shape
+    if cols > 1 and logits.stride(1) != 1:
+        _refuse("logits: need unit column stride")
+    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
+    _enqueue(dev, stream, _lib.mfs_sample_rows, logits.data_ptr(), _dtype_code(logits), rows, cols,
              logits.stride(0) if rows > 1 else cols, _array(temperature, "temperature", rows, f32, dev),
              _array(top_k, "top_k", rows, i32, dev), _array(top_p, "top_p", rows, f32, dev),
              _array(min_p, "min_p", rows, f32, dev), _array(uniforms, "uniforms", rows, f32, dev),
@@ -444,19 +451,21 @@ class PagedKV:
 
     def __init__(self, k, v, table):
         import torch
-        _need(k.is_cuda and k.dim() == 4 and v.shape == k.shape and v.dtype == k.dtype and v.device == k.device,
-              "cache: need k and v [n_pages, n_kv_heads, page_size, head_dim] of one type on one CUDA device")
-        _need(k.stride(3) == 1 and v.stride(3) == 1 and all(k.shape[i] == 1 or k.stride(i) == v.stride(i) for i in range(3)),
-              "cache: need dense rows, and equal strides in k and v")
-        _need(table.dim() == 2 and table.dtype == torch.int32 and table.device == k.device and
-              (table.shape[1] <= 1 or table.stride(1) == 1), "cache: need an int32 table [n_seqs, pages] with unit column stride on the cache's device")
+        if not k.is_cuda or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+            _refuse("cache: need k and v [n_pages, n_kv_heads, page_size, head_dim] of one type on one CUDA device")
+        if k.stride(3) != 1 or v.stride(3) != 1 or any(k.shape[i] > 1 and k.stride(i) != v.stride(i) for i in range(3)):
+            _refuse("cache: need dense rows, and equal strides in k and v")
+        if table.dim() != 2 or table.dtype != torch.int32 or table.device != k.device or (table.shape[1] > 1 and table.stride(1) != 1):
+            _refuse("cache: need an int32 table [n_seqs, pages] with unit column stride on the cache's device")
         self.k, self.v, self.table = k, v, table
-        self.device = k.device
+        self.device, self.n_seqs = k.device, table.shape[0]
         stride = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
         self.c = mfs_paged_kv(k=k.data_ptr(), v=v.data_ptr(), table=table.data_ptr(), table_width=table.shape[1],
                               table_stride=table.stride(0) if table.shape[0] > 1 else 0, n_pages=k.shape[0], page_size=k.shape[2],
                               n_kv_heads=k.shape[1], head_dim=k.shape[3], dtype=_dtype_code(k), page_stride=stride[0],
                               head_stride=stride[1], row_stride=stride[2])
+        # what each call compares its tensors with
+        self._is = (k.get_device(), k.dtype, k.shape[1], k.shape[3])
 
 
 def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=None, rope="interleaved", theta=10000.0,
@@ -466,20 +475,23 @@ def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=No
     k_out.  cu [n_seqs + 1], kv_len [n_seqs]: int32 CUDA tensors; kv_len counts the new tokens.
     rope: "interleaved", "half" or None (see include/mfs.h)."""
     import torch
-    c, dev, i32 = cache.c, cache.device, torch.int32
-    n, n_seqs = k.shape[0], kv_len.shape[0]
-    _need(rope in MFS_ROPE, f"rope: one of {list(MFS_ROPE)}")
-    _need((q is None) == (q_out is None), "q and q_out go together")
-    _need(n_seqs <= cache.table.shape[0], "the cache's table has fewer rows than kv_len")
-    kp, ks = _rows(k, "k", n, c.n_kv_heads, c.head_dim, cache.k)
-    vp, vs = _rows(v, "v", n, c.n_kv_heads, c.head_dim, cache.k)
-    op, os_ = (None, 0) if k_out is None else _rows(k_out, "k_out", n, c.n_kv_heads, c.head_dim, cache.k)
+    dev, dtype, hkv, hd = cache._is
+    n, n_seqs, i32 = k.size(0), kv_len.size(0), torch.int32
+    if rope not in MFS_ROPE:
+        _refuse(f"rope: one of {list(MFS_ROPE)}")
+    if (q is None) != (q_out is None):
+        _refuse("q and q_out go together")
+    if n_seqs > cache.n_seqs:
+        _refuse("the cache's table has fewer rows than kv_len")
+    kp, ks = _rows(k, "k", n, hkv, hd, dtype, dev)
+    vp, vs = _rows(v, "v", n, hkv, hd, dtype, dev)
+    op, os_ = (None, 0) if k_out is None else _rows(k_out, "k_out", n, hkv, hd, dtype, dev)
     qp, qs, hq, xp, xs = None, 0, 0, None, 0
     if q is not None:
-        hq = q.shape[1]
-        qp, qs = _rows(q, "q", n, hq, c.head_dim, cache.k)
-        xp, xs = _rows(q_out, "q_out", n, hq, c.head_dim, cache.k)
-    _enqueue(dev, stream, "mfs_kv_append", c, n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev),
+        hq = q.size(1)
+        qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
+        xp, xs = _rows(q_out, "q_out", n, hq, hd, dtype, dev)
+    _enqueue(dev, stream, _lib.mfs_kv_append, cache.c, n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev),
              _array(kv_len, "kv_len", n_seqs, i32, dev), qp, qs, hq, xp, xs, kp, ks, op, os_, vp, vs, MFS_ROPE[rope], theta)
 
 
@@ -494,21 +506,22 @@ def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, wo
     first kv_len[s] positions (the last `window` of them if it is not 0).  scale: default
     head_dim ** -0.5.  workspace: default one of its own for this call."""
     import torch
-    c, dev = cache.c, cache.device
-    n, hq = q.shape[0], q.shape[1]
-    _need(n <= cache.table.shape[0], "the cache's table has fewer rows than q")
-    qp, qs = _rows(q, "q", n, hq, c.head_dim, cache.k)
-    op, os_ = _rows(out, "out", n, hq, c.head_dim, cache.k)
+    dev, dtype, _, hd = cache._is
+    n, hq = q.size(0), q.size(1)
+    if n > cache.n_seqs:
+        _refuse("the cache's table has fewer rows than q")
+    qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
+    op, os_ = _rows(out, "out", n, hq, hd, dtype, dev)
     if workspace is None:
         if stream is None:
             workspace = mfs_paged_attention_workspace(cache, hq)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=cache.device)):
                 workspace = mfs_paged_attention_workspace(cache, hq)
-    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: need a contiguous tensor on the cache's device")
-    _enqueue(dev, stream, "mfs_paged_attention", c, n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_,
-             c.head_dim ** -0.5 if scale is None else scale, window, workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("workspace: need a contiguous tensor on the cache's device")
+    _enqueue(dev, stream, _lib.mfs_paged_attention, cache.c, n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_,
+             hd ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.nbytes)
 
 
 def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) -> None:
@@ -516,11 +529,12 @@ def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) ->
     head_dim] CUDA tensors (fp32 or bf16), sequence s = tokens cu[s] .. cu[s + 1] - 1; the last `window`
     keys of each row if it is not 0.  scale: default head_dim ** -0.5 (see include/mfs.h)."""
     import torch
-    _need(q.is_cuda and q.dim() == 3 and k.dim() == 3, "need CUDA tensors [tokens, heads, head_dim]")
-    (n, hq, hd), hkv, n_seqs, dev = q.shape, k.shape[1], cu.shape[0] - 1, q.device
-    qp, qs = _rows(q, "q", n, hq, hd, q)
-    kp, ks = _rows(k, "k", n, hkv, hd, q)
-    vp, vs = _rows(v, "v", n, hkv, hd, q)
-    op, os_ = _rows(out, "out", n, hq, hd, q)
-    _enqueue(dev, stream, "mfs_prompt_attention", _dtype_code(q), n, n_seqs, _array(cu, "cu", n_seqs + 1, torch.int32, dev), qp, qs, hq,
+    if not q.is_cuda or q.dim() != 3 or k.dim() != 3 or cu.dim() != 1 or cu.size(0) < 1:
+        _refuse("need CUDA tensors [tokens, heads, head_dim] and cu [n_seqs + 1]")
+    (n, hq, hd), hkv, n_seqs, dev, dtype = q.shape, k.size(1), cu.size(0) - 1, q.get_device(), q.dtype
+    qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
+    kp, ks = _rows(k, "k", n, hkv, hd, dtype, dev)
+    vp, vs = _rows(v, "v", n, hkv, hd, dtype, dev)
+    op, os_ = _rows(out, "out", n, hq, hd, dtype, dev)
+    _enqueue(dev, stream, _lib.mfs_prompt_attention, _dtype_code(q), n, n_seqs, _array(cu, "cu", n_seqs + 1, torch.int32, dev), qp, qs, hq,
              kp, ks, vp, vs, hkv, hd, op, os_, hd ** -0.5 if scale is None else scale, window)

@@ -568,3 +568,53 @@ def test_prompts_then_tokens_through_the_paged_cache(mfs, dtype, hd, rope, windo
             check(s, lens[s] + step - 1, q[s], o[s])
             want = S.sample_row(_np(logits[s]), float(u[s]), *[(np.float32(0.7), 25, 1.0), (np.float32(0.9), 0, np.float32(0.9))][s])
             assert int(tokens[s]) == want
+
+
+# ------------------------------------------------------- refusals of the binding
+
+def test_binding_refuses_tensors_that_do_not_fit(mfs):
+    torch = _torch()
+    f = dict(device="cuda", dtype=torch.bfloat16)
+    kc, table, kv, cu = torch.zeros(4, 2, 16, 64, **f), torch.zeros(2, 2, dtype=torch.int32, device="cuda"), _i32([1, 1]), _i32([0, 1, 2])
+    cache = mfs.PagedKV(kc, kc.clone(), table)
+    q, k = torch.zeros(2, 4, 64, **f), torch.zeros(2, 2, 64, **f)
+
+    def refused(call, *a, **kw):
+        with pytest.raises(mfs.MfsError) as e:
+            call(*a, **kw)
+        assert e.value.status == "MFS_E_ARG"
+
+    refused(mfs.PagedKV, kc, kc.float(), table)
+    refused(mfs.PagedKV, kc, kc[:3], table)
+    refused(mfs.PagedKV, kc, kc.transpose(1, 2).contiguous().transpose(1, 2), table)
+    refused(mfs.PagedKV, kc, kc, table.long())
+    refused(mfs.PagedKV, kc, kc, table.t()[:, :2].contiguous().t())
+    refused(mfs.PagedKV, kc.half(), kc.half(), table)
+    append, attend, prompt, sample = mfs.mfs_kv_append, mfs.mfs_paged_attention, mfs.mfs_prompt_attention, mfs.mfs_sample_rows
+    refused(append, cache, k, k[:1], cu, kv)
+    refused(append, cache, k.float(), k.float(), cu, kv)
+    refused(append, cache, k, k, cu[:2], kv)
+    refused(append, cache, k, k, cu, _i32([1, 1, 1]))
+    refused(append, cache, k, k, cu, kv, q=q)
+    refused(append, cache, k, k, cu, kv, q=q, q_out=q[:, :2])
+    refused(append, cache, k, k, cu.cpu(), kv)
+    refused(append, cache, k, k, cu, kv, rope="both")
+    refused(append, cache, k, k, cu, kv, theta=0.0)
+    refused(append, cache, torch.zeros(2, 64, 2, **f).transpose(1, 2), k, cu, kv)
+    refused(attend, cache, q, kv[:1], q)
+    refused(attend, cache, torch.zeros(3, 4, 64, **f), _i32([1, 1, 1]), torch.zeros(3, 4, 64, **f))
+    refused(attend, cache, q[:, :3], kv, q[:, :3])
+    refused(attend, cache, q, kv, q, window=-1)
+    refused(attend, cache, q, kv, q, scale=0.0)
+    refused(attend, cache, q, kv, q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(prompt, q, k, k.float(), cu, q)
+    refused(prompt, q, k, k, cu.float(), q)
+    refused(prompt, q[:, :3], k, k, cu, torch.empty_like(q[:, :3]))
+    refused(prompt, torch.zeros(2, 4, 32, **f), torch.zeros(2, 2, 32, **f), torch.zeros(2, 2, 32, **f), cu, torch.zeros(2, 4, 32, **f))
+    x, u, out = torch.zeros(2, 8, device="cuda"), _f32([0, 0]), _i32([0, 0])
+    refused(sample, x.half(), u, out)
+    refused(sample, x, u[:1], out)
+    refused(sample, x, u, out.long())
+    refused(sample, x, u, out, top_k=_f32([1, 1]))
+    refused(sample, x.t(), u, out)
+    refused(sample, x[:, :0], u, out)
