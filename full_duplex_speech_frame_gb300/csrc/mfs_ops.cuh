@@ -6,6 +6,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "../../include/mfs.h"
 
 namespace mfs {
@@ -22,6 +24,24 @@ inline int op_fail(int code, const char* op, const char* msg)
 inline int op_launched(const char* op, cudaError_t e)
 {
     return e == cudaSuccess ? MFS_OK : op_fail(MFS_E_CUDA, op, cudaGetErrorString(e));
+}
+
+// What a kernel's launches need to know of each device: its SMs, and that its shared memory limit has been raised there.
+struct PerDevice {
+    std::atomic<int> sms[64];
+};
+
+// SMs of the current device; on the first call there, `kernel` (if any) is allowed `smem` bytes of dynamic shared memory.
+inline cudaError_t op_device(PerDevice& known, const void* kernel, int smem, int* sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (*sms = known.sms[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && kernel) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) known.sms[dev].store(*sms, std::memory_order_release);
+    return e;
 }
 
 // Pointer and token stride of a [tokens][heads][head_dim] array: 16-byte steps, heads dense.

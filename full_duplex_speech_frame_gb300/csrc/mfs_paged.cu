@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
 template <typename T, int HD>
 int append(const ApArgs<T>& A, cudaStream_t st)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, nullptr, 0, &sms);
     if (e == cudaSuccess) {
         if (A.n_tokens < 2 * AP_TOKENS * sms) append_kernel<T, HD, 1><<<A.n_tokens, AP_THREADS, 0, st>>>(A);
         else append_kernel<T, HD, AP_TOKENS><<<(A.n_tokens + AP_TOKENS - 1) / AP_TOKENS, AP_THREADS, 0, st>>>(A);
@@ -534,6 +534,13 @@ struct PaF32 {
     __device__ __forceinline__ bool owner() const { return (threadIdx.x & 31) == 0; }
 };
 
+// x y / z for x <= PA_WARPS * PA_MAX_CTAS or so; 32 bits where they suffice (a 64-bit division takes about 100 instructions)
+__device__ __forceinline__ long long muldiv(long long x, long long y, long long z)
+{
+    if (y < (1ll << 20) && x < 4096) return (unsigned)x * (unsigned)y / (unsigned)z;
+    return x * y / z;
+}
+
 template <typename T, int HD>
 struct PaLayout {
     static constexpr int GM = PaType<T>::GM;
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         return;
     }
     if (share < shares) {
-        const long long t0 = share * total / shares, t1 = (share + 1) * total / shares;
+        const long long t0 = muldiv(share, total, shares), t1 = muldiv(share + 1, total, shares);
         // where the share starts
         PaWalk use;
         long long item_first = 0;  // the item's first tile
@@ -615,13 +622,18 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             item_first += __shfl_sync(0xffffffffu, inc, 31);
         }
         pa_sequence(A, use);
-        use.hb = (int)((t0 - item_first) / use.ntiles);
+        use.hb = (int)((unsigned long long)(t0 - item_first) >> 32 ? (t0 - item_first) / use.ntiles : (unsigned)(t0 - item_first) / (unsigned)use.ntiles);
         item_first += (long long)use.hb * use.ntiles;
         use.tile = (int)(t0 - item_first);
         PaWalk load = use;
         char* ring_p = pa_raw + warp * (S * L::STAGE);
         const unsigned ring = su32(ring_p);
 
+        // the CTA whose share ends with or holds the tile before `end`: the last share with muldiv(share, total, shares) < end
+        auto owner = [&](long long end) {
+            const long long x = end * shares - 1;
+            return (int)((x >> 32 ? x / total : (unsigned)x / (unsigned)total) / PA_WARPS);
+        };
         const int n = (int)(t1 - t0);
         int n_load = n;         // tiles not yet asked for: the loads run ahead of the products, across items
         unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
@@ -695,7 +707,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                         for (int h = 0; h < State::OWN; ++h) sh_ml[slot][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
                     }
                     if (lane == 0)
-                        sh_piece[slot] = {use.s, use.hb, front, ends, (int)(((item_first + use.ntiles) * shares - 1) / total / PA_WARPS)};
+                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + use.ntiles)};
                 }
                 fresh = true;
             }
@@ -755,39 +767,66 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     }
 }
 
-// Joins the pieces of the items that cross shares: one block per (CTA that began one, query head).
+// Joins the pieces of the items that cross CTAs: one block per (CTA that began one, query head), PJ_GROUPS groups of HD
+// threads that take eight pieces at a time, all on their way together.
+constexpr int PJ_GROUPS = 4;
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(HD) paged_attention_join(const __grid_constant__ PaArgs A)
+__global__ void __launch_bounds__(HD * PJ_GROUPS) paged_attention_join(const __grid_constant__ PaArgs A)
 {
     constexpr int GM = PaType<T>::GM;
-    __shared__ float w[PA_MAX_CTAS], red[HD / 32];
+    __shared__ float s_acc[PJ_GROUPS][HD], s_mx[PJ_GROUPS], s_l[PJ_GROUPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
+    const int cta = blockIdx.x, row = blockIdx.y, e = threadIdx.x % HD, group = threadIdx.x / HD;
     const int4 r = A.rec[cta];
     if (r.x < 0 || row >= A.g - (r.y % A.nhb) * GM) return;
     const int np = r.z - cta + 1;  // pieces: (cta, 1), then (cta + i, 0)
-    float mx = -INFINITY;
-    for (int i = tid; i < np; i += HD) {
-        const float2 ml = A.part_ml[((long long)(cta + i) * 2 + (i == 0)) * GM + row];
-        w[i] = ml.x;
-        mx = fmaxf(mx, ml.x);
+    float mx = -INFINITY, acc = 0.f, l = 0.f;
+    for (int i0 = 8 * group; i0 < np; i0 += 8 * PJ_GROUPS) {
+        float2 ml[8];
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const long long slot = ((long long)(cta + i0 + i) * 2 + (i0 + i == 0)) * GM + row;
+            ml[i] = i0 + i < np ? A.part_ml[slot] : make_float2(-INFINITY, 0.f);
+            o[i] = i0 + i < np ? A.part_o[slot * HD + e] : 0.f;
+        }
+        float mn = mx;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
+        const float a = mx == mn ? 1.f : exp2f((mx - mn) * A.c);
+        mx = mn;
+        acc *= a;
+        l *= a;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float w = ml[i].x == mx ? 1.f : exp2f((ml[i].x - mx) * A.c);
+            l = fmaf(ml[i].y, w, l);
+            acc = fmaf(o[i], w, acc);
+        }
     }
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    mx = red[0];
-    for (int i = 1; i < HD / 32; ++i) mx = fmaxf(mx, red[i]);
-    for (int i = tid; i < np; i += HD) w[i] = w[i] == mx ? 1.f : exp2f((w[i] - mx) * A.c);
-    __syncthreads();
-    float acc = 0.f, l = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < np; ++i) {
-        const long long slot = ((long long)(cta + i) * 2 + (i == 0)) * GM + row;
-        l = fmaf(A.part_ml[slot].y, w[i], l);
-        acc = fmaf(A.part_o[slot * HD + tid], w[i], acc);
+    if (np > 8) {  // the groups, in order
+        s_acc[group][e] = acc;
+        if (e == 0) { s_mx[group] = mx; s_l[group] = l; }
+        __syncthreads();
+        if (group) return;
+        float mn = mx;
+#pragma unroll
+        for (int k = 1; k < PJ_GROUPS; ++k) mn = fmaxf(mn, s_mx[k]);
+        float sum = 0.f, all = 0.f;
+#pragma unroll
+        for (int k = 0; k < PJ_GROUPS; ++k) {
+            const float w = s_mx[k] == mn ? 1.f : exp2f((s_mx[k] - mn) * A.c);
+            sum = fmaf(s_l[k], w, sum);
+            all = fmaf(s_acc[k][e], w, all);
+        }
+        l = sum;
+        acc = all;
+    } else if (group) {
+        return;
     }
     const int h = (r.y / A.nhb) * A.g + (r.y % A.nhb) * GM + row;
-    reinterpret_cast<T*>(A.out)[(long long)r.x * A.out_stride + (long long)h * HD + tid] = from_f<T>(acc / l);
+    reinterpret_cast<T*>(A.out)[(long long)r.x * A.out_stride + (long long)h * HD + e] = from_f<T>(acc / l);
 }
 
 size_t attention_workspace(int dtype, int hd)
@@ -806,10 +845,9 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     A.part_ml = reinterpret_cast<float2*>(A.front_o + (size_t)PA_MAX_CTAS * PA_WARPS * L::GM * HD);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * L::GM);
     const int rows = A.g < L::GM ? A.g : L::GM;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<T, HD>, L::BYTES, &sms);
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     const int G = 2 * sms < PA_MAX_CTAS ? 2 * sms : PA_MAX_CTAS;
     paged_attention_kernel<T, HD><<<G, PA_WARPS * 32, L::BYTES, st>>>(A);
@@ -817,7 +855,7 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)G, (unsigned)rows);
-    cfg.blockDim = dim3(HD);
+    cfg.blockDim = dim3(HD * PJ_GROUPS);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

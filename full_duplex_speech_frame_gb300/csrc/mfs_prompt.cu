@@ -943,7 +943,9 @@ int run_f32(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
                       n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
     const long long blocks = ((long long)n_tokens / PF_ROWS + n_seqs) * hq;  // blocks there can be
     if (blocks > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many tokens and sequences");
-    cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfShape<HD>::BYTES);
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, (const void*)prompt_f32_kernel<HD>, PfShape<HD>::BYTES, &sms);
     if (e == cudaSuccess) {
         prompt_f32_kernel<HD><<<(unsigned)blocks, PF_THREADS, PfShape<HD>::BYTES, st>>>(A);
         e = cudaGetLastError();
@@ -957,13 +959,14 @@ int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
 {
     using S = PtShape<HD>;
     const char* op = "prompt_attention";
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 encode = known.load();
     if (!encode) {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult r;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) != cudaSuccess || !fn)
             return mfs::op_fail(MFS_E_CUDA, op, "cuTensorMapEncodeTiled is not available");
-        encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+        known.store(encode = (PFN_cuTensorMapEncodeTiled_v12000)fn);
     }
     CUtensorMap maps[3];
     const void* p[3] = {q, k, v};
@@ -979,10 +982,9 @@ int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
     }
     PtArgs A = {cu, (const bf16*)q, (const bf16*)k, (const bf16*)v, (bf16*)out, q_stride, k_stride, v_stride, out_stride,
                 n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_mma_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, (const void*)prompt_mma_kernel<HD>, S::BYTES, &sms);
     if (e == cudaSuccess) {
         const long long most = ((long long)n_tokens / PT_BLOCK + n_seqs) * hq;  // blocks there can be
         prompt_mma_kernel<HD><<<(unsigned)(most < sms ? most : sms), PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);

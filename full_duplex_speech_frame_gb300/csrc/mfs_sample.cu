@@ -1017,9 +1017,11 @@ template <typename T>
 int launch(const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
            const float* top_p, const float* min_p, const float* uniforms, int32_t* tokens, cudaStream_t st)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    auto kernel = sample_rows_kernel<T>;
+    int sms = 0;
+    static mfs::PerDevice ready;
+    const cudaError_t e = mfs::op_device(ready, (const void*)kernel, (int)(sizeof(SrShared) + SR_STAGE_BYTES), &sms);
+    if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
     // CTAs per row: parts of at most 64 KB, so that two CTAs share an SM, and more where rows leave SMs empty
     // and a part keeps at least 4096 columns
     int C = 1;
@@ -1027,10 +1029,6 @@ int launch(const void* logits, int rows, int cols, long long ld, const float* te
     const long long part = ((long long)cols + C - 1) / C * sizeof(T) + 32;
     const bool stage = part <= SR_STAGE_BYTES;
     const size_t smem = sizeof(SrShared) + (stage ? (size_t)part : 0);
-    auto kernel = sample_rows_kernel<T>;
-    if (e == cudaSuccess && smem > 48 * 1024)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(sizeof(SrShared) + SR_STAGE_BYTES));
-    if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
     if ((long long)rows * C > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, "sample_rows", "too many rows");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
