@@ -6,13 +6,13 @@
 // `tie` among {logit == tau}, and the row is never sorted.  Where few columns can
 // be candidates they are listed: those above the k-th largest of the threads' own
 // maxima (at least k columns reach it, and rarely many more), or above min-p's
-// bound.  One CTA then sorts the list, cuts it, sorts what is left by column and
-// finds the token.  Otherwise a histogram, linear in the distance to the
+// bound, in column order.  One CTA then finds each one's rank by comparing all with
+// all, cuts the list and finds the token.  Otherwise a histogram, linear in the distance to the
 // maximum in octaves of the weight, finds the bin that holds a filter's border, only
 // that bin's columns are listed, and the token is found by sums in column order, per
 // CTA, per thread, and within that thread's columns.  Where a filter leaves few
-// columns, their places are gathered first, so that a warp's lanes weigh columns
-// together and not one by one.
+// columns, each thread notes the places of its own first, so that a warp's lanes
+// weigh columns together and not one by one.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
 // part of the row in shared memory beside another CTA's, and to use the SMs when
@@ -41,11 +41,11 @@ using bf16 = __nv_bfloat16;
 
 constexpr int SR_NT = 512;            // threads per CTA
 constexpr int SR_NW = SR_NT / 32;
-constexpr int SR_NB = 1024;           // histogram bins
+constexpr int SR_NB = 1024;           // histogram bins, of 1 / 16 octave
 constexpr int SR_BPT = SR_NB / SR_NT;
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
 constexpr int SR_LIST = SR_NT;        // columns that are listed at most
-constexpr int SR_IDX = 4096;           // columns of a CTA's part that are gathered at most
+constexpr int SR_SLOTS = 8;           // columns that a thread notes at most
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
 
@@ -58,10 +58,11 @@ struct __align__(16) SrShared {
     unsigned count[SR_NB], lo[SR_NB], hi[SR_NB];  // this CTA's histogram: columns, sums of weights in two words
     u64 sum[SR_NB];                               // the row's sums of weights
     unsigned num[SR_NB];                          // and columns
-    u64 list[SR_LIST];                            // key << 32 | ~column
-    u64 other[SR_LIST];                           // the sort's exchanges between warps
-    unsigned base[SR_NW][SR_MAX_C];               // where a warp's listed columns go, in each CTA's list
-    unsigned short idx[SR_IDX];                   // gathered columns, ascending, as places in the part
+    u64 list[SR_LIST];                            // listed columns, ascending: key << 32 | ~column
+    u64 ranked[SR_LIST];                          // their weights or keys by rank
+    unsigned keys[SR_LIST];                       // the list's keys
+    unsigned short rank[SR_LIST];
+    unsigned short idx[SR_NT][SR_SLOTS];          // noted columns, ascending, as places in the part
     uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
     u64 ws[SR_NW];
     float wf[SR_NW];
@@ -69,11 +70,10 @@ struct __align__(16) SrShared {
     // one entry per CTA of the row, written by that CTA in every CTA's copy
     float r_max[SR_MAX_C], r_edge[SR_MAX_C];
     int r_idx[SR_MAX_C];
-    unsigned r_klo[SR_MAX_C], r_khi[SR_MAX_C];
+    unsigned r_klo[SR_MAX_C], r_khi[SR_MAX_C], r_n[SR_MAX_C];
     u64 r_sum[SR_MAX_C];
     // results of a search
     int where, token, unsure;
-    unsigned listed;
     u64 before, inside;
     // the row's constants
     float lmin;
@@ -163,18 +163,25 @@ struct Weigher {
     bool precise;
     const uint2* table;
 
-    // octaves below the maximum's weight
-    __device__ __forceinline__ float octaves(float x) const { return x == mx ? 0.f : (mx - x) * c.h; }
-
+    // The 64ths of an octave, to the nearest, that x's weight lies below the maximum's (one answer for one x, and
+    // never less for a smaller x); q: the same as a float, plus 1.5 2^23.
+    __device__ __forceinline__ int steps(float x, float& q) const
+    {
+        q = fmaf(x == mx ? 0.f : __fmul_rn(mx - x, c.h), 64.f, 12582912.f);  // the integer is in the low bits
+        return __float_as_int(q) - 0x4b400000;
+    }
     __device__ __forceinline__ u64 operator()(float x) const
+    {
+        float q;
+        return weight(x, steps(x, q), q);
+    }
+    __device__ __forceinline__ u64 weight(float x, int k, float q) const
     {
         if (x == mx) return 1ull << scale;
         if (precise) return precise_weight(x, mx, c, scale);
         const F2 d = two_sum(mx, -x);
         const float h = __fmul_rn(d.h, c.h);
         const float l = fmaf(d.l, c.h, fmaf(d.h, c.l, fmaf(d.h, c.h, -h)));
-        const float q = fmaf(h, 64.f, 12582912.f);  // 64 h to the nearest integer, in the low bits
-        const int k = __float_as_int(q) - 0x4b400000;
         const float r = fmaf(q - 12582912.f, -1.f / 64.f, h) + l;
         const uint2 t = table[k & 63];
         const float f = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);  // 2^-r - 1
@@ -308,7 +315,7 @@ struct Row {
     float lmin;  // columns below it are no candidates
     float mine;  // the largest logit among this thread's columns
     int C, rank, cols;
-    int gathered;  // columns in S->idx, or -1: the part itself is gone through
+    int noted;  // columns of this thread in S->idx, or -1: its part of the row is gone through
     SrShared* S;
 
     __device__ __forceinline__ void sync() const
@@ -317,17 +324,19 @@ struct Row {
         else __syncthreads();
     }
     __device__ __forceinline__ SrShared* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
-    __device__ __forceinline__ int bin(float x) const { return min((int)(W.octaves(x) * (SR_NB / SR_REACH)), SR_NB - 1); }
-    // this thread's gathered columns
-    __device__ __forceinline__ int share() const { return (gathered + SR_NT - 1) / SR_NT; }
+    static __device__ __forceinline__ int bin_of(int steps) { return min(steps >> 2, SR_NB - 1); }
+    __device__ __forceinline__ int bin(float x) const
+    {
+        float q;
+        return bin_of(W.steps(x, q));
+    }
     // f(column, logit) for this thread's columns of at least `least`, in ascending order
     template <typename F>
     __device__ __forceinline__ void each(float least, F f) const
     {
-        if (gathered < 0) return p.each(least, f);
-        const int q = share(), e = min(gathered, (int)(threadIdx.x + 1) * q);
-        for (int i = threadIdx.x * q; i < e; ++i) {
-            const int c = S->idx[i];
+        if (noted < 0) return p.each(least, f);
+        for (int i = 0; i < noted; ++i) {
+            const int c = S->idx[threadIdx.x][i];
             const float x = p.value(c);
             if (x >= least) f(p.c0 + c, x);
         }
@@ -432,15 +441,10 @@ __device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, 
     gather_histogram(R, counts, sums);
 }
 
-// Gathers this CTA's columns above tau, and those equal to it up to column tie, if there are few.
-template <typename T>
-__device__ void gather_columns(Row<T>& R, float tau, int tie)
+// Exclusive sums of n over the CTA's threads, and their total.
+__device__ __forceinline__ unsigned scan_counts(SrShared* S, unsigned n, unsigned& total)
 {
-    SrShared* S = R.S;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (R.gathered >= 0 || R.p.nvec * R.p.VE > 65536) return;
-    unsigned n = 0;
-    R.p.each(tau, [&](int col, float x) { n += x > tau || col <= tie; });
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned inc = n;
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
@@ -452,110 +456,104 @@ __device__ void gather_columns(Row<T>& R, float tau, int tie)
     unsigned at = inc - n, all = 0;
 #pragma unroll
     for (int w = 0; w < SR_NW; ++w) {
-        if (w == warp) at += all;
-        all += S->wi[w];
+        const unsigned x = S->wi[w];
+        if (w < warp) at += x;
+        all += x;
     }
-    if (all > SR_IDX) return;
-    if (n)
-        R.p.each(tau, [&](int col, float x) {
-            if (x > tau || col <= tie) S->idx[at++] = (unsigned short)(col - R.p.c0);
-        });
-    R.gathered = all;
-    __syncthreads();
+    total = all;
+    return at;
 }
 
-// The columns of at least `least` that take(x) names, of all CTAs, into the S->list (unordered, S->listed set to 0 before)
-// of the row's first CTA, or of all; their number (more than SR_LIST: the list is not complete).
+// Each thread notes its columns of at least `least`, if no thread of the CTA has too many.
+template <typename T>
+__device__ __forceinline__ void note_columns(Row<T>& R, float least)
+{
+    SrShared* S = R.S;
+    if (R.noted >= 0 || R.p.nvec * R.p.VE > 65536) return;
+    int n = 0;
+    R.p.each(least, [&](int col, float) {
+        if (n < SR_SLOTS) S->idx[threadIdx.x][n] = (unsigned short)(col - R.p.c0);
+        ++n;
+    });
+    if (!__syncthreads_or(n > SR_SLOTS)) R.noted = n;
+}
+
+// The columns of at least `least` that take(x) names, of all CTAs and in ascending order, into the S->list of the row's
+// first CTA, or of all; their number (more than SR_LIST: the list is not complete).
 template <typename T, typename F>
 __device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
 {
     SrShared* S = R.S;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, dests = all ? R.C : 1;
-    unsigned n = 0;
+    unsigned n = 0, here;
     R.each(least, [&](int, float x) { n += take(x); });
-    unsigned inc = n;
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
-    }
-    const unsigned whole = __shfl_sync(0xffffffffu, inc, 31);
-    if (whole) {
-        if (lane < dests) S->base[warp][lane] = atomicAdd(&R.of(lane)->listed, whole);
-        __syncwarp();
-        if (n) {
-            unsigned at = inc - n;
-            R.each(least, [&](int col, float x) {
-                if (!take(x)) return;
-                const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
-                for (int r = 0; r < dests; ++r)
-                    if (S->base[warp][r] + at < SR_LIST) R.of(r)->list[S->base[warp][r] + at] = e;
-                ++at;
-            });
+    unsigned at = scan_counts(S, n, here), total = here;
+    if (R.C > 1) {
+        if (threadIdx.x < R.C) R.of(threadIdx.x)->r_n[R.rank] = here;
+        R.sync();
+        total = 0;
+        for (int r = 0; r < R.C; ++r) {
+            if (r < R.rank) at += S->r_n[r];
+            total += S->r_n[r];
         }
     }
-    if (R.C == 1 || all) {
-        R.sync();
-        return *(volatile unsigned*)&S->listed;
-    }
-    // the first CTA's list: the others learn how long it is from the counts
-    if (lane == 0) S->ws[warp] = whole;
-    __syncthreads();
-    u64 here = 0;
-    for (int w = 0; w < SR_NW; ++w) here += S->ws[w];
-    if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
+    if (n && total <= SR_LIST)
+        R.each(least, [&](int col, float x) {
+            if (!take(x)) return;
+            const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
+            if (all)
+                for (int r = 0; r < R.C; ++r) R.of(r)->list[at] = e;
+            else
+                R.of(0)->list[at] = e;
+            ++at;
+        });
     R.sync();
-    u64 total = 0;
-    for (int r = 0; r < R.C; ++r) total += S->r_sum[r];
-    return (unsigned)total;
+    return total;
 }
 
-// Sorts e, one value per thread, over the first `full` threads (a power of two from 32), largest first.  All of them call it.
-__device__ __forceinline__ u64 sort_descending(SrShared* S, u64 e, unsigned full)
+// The ranks of the n listed columns among the candidates, into S->rank: each entry's keys are compared with all, by as
+// many threads as there are for it.  A lower entry of the same key comes first.
+__device__ __forceinline__ void rank_list(SrShared* S, unsigned n)
 {
     const unsigned tid = threadIdx.x;
-    for (unsigned k = 2; k <= full; k *= 2)
-        for (unsigned j = k / 2; j; j /= 2) {
-            u64 y;
-            if (j >= 32) {
-                S->other[tid] = e;
-                asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
-                y = S->other[tid ^ j];
-                asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
-            } else {
-                y = __shfl_xor_sync(0xffffffffu, e, j);
-            }
-            const bool larger = ((tid & k) == 0) == ((tid & j) == 0);
-            e = (e > y) == larger ? e : y;
+    S->keys[tid] = tid < n ? (unsigned)(S->list[tid] >> 32) : 0;
+    __syncthreads();
+    int g = 1;
+    while (g < 32 && n * (2 * g) <= SR_NT) g *= 2;
+    const unsigned me = tid / g;
+    if (me < n || g > 1) {
+        const unsigned k = S->keys[me < n ? me : 0];
+        unsigned rank = 0;
+        const uint4* keys = reinterpret_cast<const uint4*>(S->keys);
+        for (unsigned c = tid & (g - 1); c < (n + 3) / 4; c += g) {
+            const uint4 x = keys[c];
+            const unsigned t = c < me / 4 ? k - 1 : k;  // keys are above 0
+            rank += (x.x > t) + (x.y > t) + (x.z > t) + (x.w > t);
         }
-    return e;
+        if ((tid & (g - 1)) == 0)
+            for (unsigned i = me & ~3u; i < me && i < n; ++i) rank += S->keys[i] == k;
+        for (int o = g / 2; o; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+        if (me < n && (tid & (g - 1)) == 0) S->rank[me] = (unsigned short)rank;
+    }
+    __syncthreads();
 }
 
-// Inclusive sums of v over the first `full` threads (see sort_descending), and their total.
-__device__ __forceinline__ u64 scan_threads(SrShared* S, u64 v, unsigned full, u64& total)
+// Inclusive sums of v over the CTA's threads, and their total.
+__device__ __forceinline__ u64 scan_weights(SrShared* S, u64 v, u64& total)
 {
-    const unsigned warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const u64 inc = warp_inclusive(v);
-    if (full == 32) {
-        total = __shfl_sync(0xffffffffu, inc, 31);
-        return inc;
-    }
-    asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
+    __syncthreads();
     if (lane == 31) S->ws[warp] = inc;
-    asm volatile("bar.sync 1, %0;" ::"r"(full) : "memory");
-    u64 before = 0;
-    total = 0;
-    for (unsigned w = 0; w < full / 32; ++w) {
-        if (w == warp) before = total;
-        total += S->ws[w];
+    __syncthreads();
+    u64 before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < SR_NW; ++w) {
+        const u64 x = S->ws[w];
+        if (w < warp) before += x;
+        all += x;
     }
+    total = all;
     return before + inc;
-}
-
-__device__ __forceinline__ unsigned sort_width(unsigned n)
-{
-    unsigned full = 32;
-    while (full < n) full *= 2;
-    return full;
 }
 
 // The first column, in ascending order over the whole row, at which the running sum of wt(column, x) over the columns of
@@ -566,19 +564,11 @@ __device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
 {
     SrShared* S = R.S;
     const Part<T>& P = R.p;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     u64 mine = 0;
     R.each(least, [&](int col, float x) { mine += wt(col, x); });
-    const u64 inc = warp_inclusive(mine);
-    __syncthreads();
-    if (lane == 31) S->ws[warp] = inc;
-    __syncthreads();
-    u64 here = 0, run = inc - mine;
-#pragma unroll
-    for (int w = 0; w < SR_NW; ++w) {
-        if (w == warp) run += here;
-        here += S->ws[w];
-    }
+    u64 here;
+    u64 run = scan_weights(S, mine, here) - mine;
     u64 before = 0, total = here;
     if (R.C > 1) {
         if (tid < R.C) R.of(tid)->r_sum[R.rank] = here;
@@ -594,17 +584,17 @@ __device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
     // the thread whose columns hold it, and its warp: that thread's columns, one per lane
     const unsigned hit = __ballot_sync(0xffffffffu, run <= target && run + mine > target);
     if (hit) {
-        const int t = warp * 32 + __ffs(hit) - 1, q = R.gathered < 0 ? P.per * P.VE : R.share();
-        const int first = t * q, n = min(R.gathered < 0 ? P.nvec * P.VE : R.gathered, first + q) - first;
-        run = __shfl_sync(0xffffffffu, run, t & 31);
+        const int l = __ffs(hit) - 1, t = warp * 32 + l, first = t * P.per * P.VE;
+        const int n = R.noted < 0 ? min(P.nvec, (t + 1) * P.per) * P.VE - first : __shfl_sync(0xffffffffu, R.noted, l);
+        run = __shfl_sync(0xffffffffu, run, l);
         for (int i0 = 0; i0 < n; i0 += 32) {
             const int i = i0 + lane;
             u64 w = 0;
             int col = 0;
             if (i < n) {
-                const int c = R.gathered < 0 ? first + i : S->idx[first + i];
+                const int c = R.noted < 0 ? first + i : S->idx[t][i];
                 col = P.c0 + c;
-                if (R.gathered >= 0 || (col >= P.lo && col < P.hi)) {
+                if (col >= P.lo && col < P.hi) {
                     const float x = P.value(c);
                     if (x >= least) w = wt(col, x);
                 }
@@ -638,23 +628,25 @@ template <bool BY_MASS, typename T>
 __device__ Border border_in_list(const Row<T>& R, unsigned n, u64 mass, u64 count, u64 target, u64 band)
 {
     SrShared* S = R.S;
-    const unsigned tid = threadIdx.x, full = sort_width(n);
-    if (tid < full) {
-        const u64 e = sort_descending(S, tid < n ? S->list[tid] : 0, full);
-        if (BY_MASS) {
-            const u64 w = tid < n ? R.W(key_value((unsigned)(e >> 32))) : 0;
-            u64 total;
-            const u64 upto = mass + scan_threads(S, w, full, total);
-            if (tid < n && upto - w < target && (upto >= target || tid + 1 == n)) {
-                S->inside = e;
-                // the border is certain if no error of the sums can move it
-                if (upto < target + band || (upto > w && upto - w + band >= target)) S->unsure = 1;
-            }
-        } else if (tid == target - 1 - count) {
-            S->inside = e;
-        }
+    const int tid = threadIdx.x;
+    rank_list(S, n);
+    if (tid < n) {
+        const unsigned rank = S->rank[tid];
+        if (BY_MASS) S->ranked[rank] = S->list[tid];
+        else if (rank == target - 1 - count) S->inside = S->list[tid];
     }
     __syncthreads();
+    if (BY_MASS) {
+        const u64 f = tid < n ? S->ranked[tid] : 0, w = tid < n ? R.W(key_value((unsigned)(f >> 32))) : 0;
+        u64 total;
+        const u64 upto = mass + scan_weights(S, w, total);
+        if (tid < n && upto - w < target && (upto >= target || tid + 1 == n)) {
+            S->inside = f;
+            // the border is certain if no error of the sums can move it
+            if (upto < target + band || (upto > w && upto - w + band >= target)) S->unsure = 1;
+        }
+        __syncthreads();
+    }
     const u64 b = S->inside;
     __syncthreads();
     return {key_value((unsigned)(b >> 32)), (int)~(unsigned)b};
@@ -665,34 +657,35 @@ template <typename T>
 __device__ __forceinline__ bool sample_list(const Row<T>& R, unsigned n, int top_k, float top_p, float u, int32_t* token)
 {
     SrShared* S = R.S;
-    const unsigned tid = threadIdx.x, full = sort_width(n);
+    const int tid = threadIdx.x;
+    const u64 e = tid < n ? S->list[tid] : 0;
+    const u64 w = tid < n ? R.W(key_value((unsigned)(e >> 32))) : 0;
+    u64 total;
     if (tid == 0) S->unsure = 0;
-    __syncthreads();
-    if (tid < full) {
-        u64 e = tid < n ? S->list[tid] : 0;
-        bool in = tid < n;
-        if (top_k > 0 || top_p < 1.f) {
-            e = sort_descending(S, e, full);
-            in = in && (top_k <= 0 || tid < (unsigned)top_k);
-            if (top_p < 1.f) {
-                const u64 w = in ? R.W(key_value((unsigned)(e >> 32))) : 0;
-                u64 total;
-                const u64 upto = scan_threads(S, w, full, total), target = max((u64)1, fraction(top_p, total, true)), band = R.band(total);
-                if (in && upto - w < target && upto >= target && (upto < target + band || (upto > w && upto - w + band >= target)))
-                    S->unsure = 1;
-                in = in && upto - w < target;
+    unsigned keep = top_k > 0 ? min(n, (unsigned)top_k) : n, rank = 0;  // columns kept, of the largest
+    if (keep < n || top_p < 1.f) {
+        rank_list(S, n);
+        rank = tid < n ? S->rank[tid] : n;
+        if (top_p < 1.f) {
+            if (tid < n) S->ranked[rank] = w;
+            __syncthreads();
+            const u64 v = tid < keep ? S->ranked[tid] : 0;
+            const u64 upto = scan_weights(S, v, total), target = max((u64)1, fraction(top_p, total, true)), band = R.band(total);
+            if (tid < keep && upto - v < target && upto >= target) {
+                S->where = tid + 1;
+                if (upto < target + band || (upto > v && upto - v + band >= target)) S->unsure = 1;
             }
+            __syncthreads();
+            keep = S->where;
         }
-        // what is left, by column
-        e = sort_descending(S, in ? e << 32 | e >> 32 : 0, full);
-        const u64 w = e ? R.W(key_value((unsigned)e)) : 0;
-        u64 total;
-        const u64 upto = scan_threads(S, w, full, total);
-        const u64 target = u < 1.f || !(u == u) ? fraction(u, total, false) : total - 1, band = R.band(total);
-        if (w && upto > target && upto - w <= target) {
-            *token = (int)~(unsigned)(e >> 32);
-            if (upto <= target + band || (upto > w && upto - w + band > target)) S->unsure = 1;
-        }
+    }
+    // the draw, in column order
+    const u64 mine = tid < n && rank < keep ? w : 0;
+    const u64 upto = scan_weights(S, mine, total);
+    const u64 target = u < 1.f || !(u == u) ? fraction(u, total, false) : total - 1, band = R.band(total);
+    if (mine && upto > target && upto - mine <= target) {
+        *token = (int)~(unsigned)e;
+        if (upto <= target + band || (upto > mine && upto - mine + band > target)) S->unsure = 1;
     }
     __syncthreads();
     const bool open = S->unsure != 0;
@@ -703,7 +696,7 @@ __device__ __forceinline__ bool sample_list(const Row<T>& R, unsigned n, int top
 // The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`
 // (less than `band` off), from the linear histogram in S->num / S->sum.
 template <bool BY_MASS, typename T>
-__device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band)
+__device__ Border find_border(Row<T>& R, float least, u64 target, u64 band)
 {
     SrShared* S = R.S;
     const int tid = threadIdx.x;
@@ -713,15 +706,14 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
     u64 mass = BY_MASS ? S->before : 0, count = BY_MASS ? 0 : S->before;  // before the bin
     unsigned klo = 0, khi = 0xffffffffu;
     bool keyed = false;
-    if (tid == 0) S->listed = 0;
-    R.sync();
     // the bin's edges, widened by more than its arithmetic may be off, spare most columns the arithmetic
     float upper = INFINITY, from = least;
     if (R.W.c.h > 0.f) {
         const float step = SR_REACH / SR_NB / R.W.c.h;
-        upper = R.W.mx - (float)b * step * 0.99999f;
+        upper = R.W.mx - ((float)b - 0.2f) * step * 0.99999f;
         if (b < SR_NB - 1) from = fmaxf(least, R.W.mx - (float)(b + 1) * step * 1.00001f);
     }
+    note_columns(R, from);
     unsigned n = list_columns(R, from, true, [&](float x) { return x <= upper && R.bin(x) == b; });
     while (n > SR_LIST) {
         // too many: split the bin's range of keys, down to one key
@@ -768,8 +760,6 @@ __device__ Border find_border(const Row<T>& R, float least, u64 target, u64 band
         const unsigned top = khi - ((unsigned)sub << sh);
         klo = max(klo, sh ? top - ((1u << sh) - 1u) : top);
         khi = top;
-        if (tid == 0) S->listed = 0;
-        R.sync();
         if (n <= SR_LIST) n = list_columns(R, least, true, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
     }
     if (n <= SR_LIST) return border_in_list<BY_MASS>(R, n, mass, count, target, band);
@@ -813,8 +803,10 @@ __device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, fl
         u64 rest = 0;
         R.each(B.tau, [&](int col, float x) {
             if (x == B.tau && col > B.tie) return;
-            const u64 w = R.W(x);
-            if (x >= shallow) add_weight(S, R.bin(x), w);
+            float q;
+            const int steps = R.W.steps(x, q);
+            const u64 w = R.W.weight(x, steps, q);
+            if (x >= shallow) add_weight(S, R.bin_of(steps), w);
             else rest += w;
         });
         rest = warp_sum(rest);
@@ -833,7 +825,7 @@ __device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, fl
         if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
     }
     // the draw, in column order
-    if (top_k > 0 || top_p < 1.f) gather_columns(R, B.tau, B.tie);
+    if (top_k > 0 || top_p < 1.f) note_columns(R, B.tau);
     u64 target = 0, total = 0;
     const bool mine = find_in_order(
         R, B.tau, [&](int col, float x) { return x == B.tau && col > B.tie ? (u64)0 : R.W(x); },
@@ -888,14 +880,13 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
     R.p.per = ((R.p.nvec + SR_NT - 1) / SR_NT) | 1;
     R.p.kept = 0;
-    R.gathered = -1;
+    R.noted = -1;
     const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared));
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (tid == SR_NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
         S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
         S->reach = mp >= 1.f ? 0.0 : mp > 0.f ? -(double)T_ * log((double)mp) : 0.0;
     }
-    if (tid == 0) S->listed = 0;
     // the maximum and its lowest column, and the row's part into shared memory
     float v = -INFINITY;
     int idx = 0x7fffffff;
@@ -928,10 +919,13 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     }
     if (lane == 0) { S->wf[warp] = v; S->wi[warp] = idx; }
     __syncthreads();
-    v = S->wf[0];
-    idx = S->wi[0];
-    for (int w = 1; w < SR_NW; ++w)
-        if (S->wf[w] > v || (S->wf[w] == v && S->wi[w] < idx)) { v = S->wf[w]; idx = S->wi[w]; }
+    v = S->wf[lane & (SR_NW - 1)];
+    idx = S->wi[lane & (SR_NW - 1)];
+    for (int o = SR_NW / 2; o; o >>= 1) {
+        const float ov = __shfl_xor_sync(0xffffffffu, v, o);
+        const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
+        if (ov > v || (ov == v && oi < idx)) { v = ov; idx = oi; }
+    }
     if (C > 1) {
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the row has started
         if (tid < C) { R.of(tid)->r_max[rank] = v; R.of(tid)->r_idx[rank] = idx; }
@@ -989,6 +983,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
         }
     }
     if (few) {
+        note_columns(R, least);
         const unsigned n = list_columns(R, least, false, [](float) { return true; });
         if (n <= SR_LIST) {
             if (rank == 0) {
@@ -1000,16 +995,14 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
             }
             return;
         }
-        R.sync();  // counts have been read
         R.lmin = least;
-        gather_columns(R, least, 0x7fffffff);
     }
-    const int gathered = R.gathered;
+    const int noted = R.noted;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         R.W.precise = pass != 0;
         if (sample_row(R, k, pp, u, tokens + r)) break;
-        R.gathered = gathered;  // not those of the first pass's border
+        R.noted = noted;  // not those of the first pass's border
     }
 }
 
