@@ -39,34 +39,33 @@ namespace {
 using u64 = unsigned long long;
 using bf16 = __nv_bfloat16;
 
-constexpr int SR_NT = 512;            // threads per CTA
-constexpr int SR_NW = SR_NT / 32;
 constexpr int SR_NB = 1024;           // histogram bins, of 1 / 16 octave
-constexpr int SR_BPT = SR_NB / SR_NT;
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
-constexpr int SR_LIST = SR_NT;        // columns that are listed at most
-constexpr int SR_SLOTS = 8;           // columns that a thread notes at most
+constexpr int SR_SLOTS = 12;          // columns that a thread notes at most
 constexpr int SR_MAX_C = 8;           // CTAs per row
-constexpr int SR_STAGE_BYTES = 180 * 1024;  // a CTA's part of the row in shared memory at most
+constexpr int SR_STAGE_BYTES = 168 * 1024;  // a CTA's part of the row in shared memory at most
+constexpr int SR_WIDE_BYTES = 140 * 1024;   // the same for CTAs of 1024 threads
 
 // A pair of fp32 whose sum is the value (error-free sums and products by Dekker and Knuth).
 struct F2 {
     float h, l;
 };
 
+// Of a CTA of NT threads; at most NT columns are listed.
+template <int NT>
 struct __align__(16) SrShared {
     unsigned count[SR_NB], lo[SR_NB], hi[SR_NB];  // this CTA's histogram: columns, sums of weights in two words
     u64 sum[SR_NB];                               // the row's sums of weights
     unsigned num[SR_NB];                          // and columns
-    u64 list[SR_LIST];                            // listed columns, ascending: key << 32 | ~column
-    u64 ranked[SR_LIST];                          // their weights or keys by rank
-    unsigned keys[SR_LIST];                       // the list's keys
-    unsigned short rank[SR_LIST];
-    unsigned short idx[SR_NT][SR_SLOTS];          // noted columns, ascending, as places in the part
+    u64 list[NT];                            // listed columns, ascending: key << 32 | ~column
+    u64 ranked[NT];                          // their weights or keys by rank
+    unsigned keys[NT];                       // the list's keys
+    unsigned short rank[NT];
+    unsigned short idx[NT][SR_SLOTS];          // noted columns, ascending, as places in the part
     uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
-    u64 ws[SR_NW];
-    float wf[SR_NW];
-    int wi[SR_NW];
+    u64 ws[(NT / 32)];
+    float wf[(NT / 32)];
+    int wi[(NT / 32)];
     // one entry per CTA of the row, written by that CTA in every CTA's copy
     float r_max[SR_MAX_C], r_edge[SR_MAX_C];
     int r_idx[SR_MAX_C];
@@ -308,7 +307,7 @@ struct Part {
 };
 
 // What the functions below share.
-template <typename T>
+template <typename T, int NT>
 struct Row {
     Part<T> p;
     Weigher W;
@@ -316,14 +315,14 @@ struct Row {
     float mine;  // the largest logit among this thread's columns
     int C, rank, cols;
     int noted;  // columns of this thread in S->idx, or -1: its part of the row is gone through
-    SrShared* S;
+    SrShared<NT>* S;
 
     __device__ __forceinline__ void sync() const
     {
         if (C > 1) cg::this_cluster().sync();
         else __syncthreads();
     }
-    __device__ __forceinline__ SrShared* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
+    __device__ __forceinline__ SrShared<NT>* of(int r) const { return C > 1 ? cg::this_cluster().map_shared_rank(S, r) : S; }
     static __device__ __forceinline__ int bin_of(int steps) { return min(steps >> 2, SR_NB - 1); }
     __device__ __forceinline__ int bin(float x) const
     {
@@ -345,28 +344,52 @@ struct Row {
     __device__ __forceinline__ u64 band(u64 total) const { return W.precise ? 0 : (total >> 28) + 2ull * cols + 2; }
 };
 
+// Inclusive sums of v over the CTA's threads, and their total.
+template <int NT>
+__device__ __forceinline__ u64 scan_weights(SrShared<NT>* S, u64 v, u64& total)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const u64 inc = warp_inclusive(v);
+    __syncthreads();
+    if (lane == 31) S->ws[warp] = inc;
+    __syncthreads();
+    const u64 all = warp_inclusive(lane < NT / 32 ? S->ws[lane] : 0);  // every warp scans the warps' sums
+    total = __shfl_sync(0xffffffffu, all, 31);
+    const u64 before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+    return inc + (warp ? before : 0);
+}
+
+// The sum of v over the CTA's threads, for all of them.
+template <int NT>
+__device__ __forceinline__ u64 all_sum(SrShared<NT>* S, u64 v)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) S->ws[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < NT / 32 ? S->ws[lane] : 0);
+}
+
 // The first of 1024 values a (in shared memory) at which the running sum, starting at `start`, exceeds target;
 // S->where = its place (or -1), S->before = the sum before it.
-template <typename U>
-__device__ void block_find(SrShared* S, const U* a, u64 start, u64 target)
+template <int NT, typename U>
+__device__ void block_find(SrShared<NT>* S, const U* a, u64 start, u64 target)
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    u64 v[SR_BPT], mine = 0;
+    const int tid = threadIdx.x;
+    u64 v[(SR_NB / NT)], mine = 0;
 #pragma unroll
-    for (int i = 0; i < SR_BPT; ++i) {
-        v[i] = (u64)a[tid * SR_BPT + i];
+    for (int i = 0; i < (SR_NB / NT); ++i) {
+        v[i] = (u64)a[tid * (SR_NB / NT) + i];
         mine += v[i];
     }
-    const u64 inc = warp_inclusive(mine);
-    if (lane == 31) S->ws[warp] = inc;
     if (tid == 0) S->where = -1;
-    __syncthreads();
-    u64 run = start + inc - mine;
-    for (int w = 0; w < warp; ++w) run += S->ws[w];
+    u64 total;
+    u64 run = start + scan_weights(S, mine, total) - mine;
     if (run <= target && run + mine > target) {
 #pragma unroll
-        for (int i = 0; i < SR_BPT; ++i) {
-            if (run <= target && run + v[i] > target) { S->where = tid * SR_BPT + i; S->before = run; }
+        for (int i = 0; i < (SR_NB / NT); ++i) {
+            if (run <= target && run + v[i] > target) { S->where = tid * (SR_NB / NT) + i; S->before = run; }
             run += v[i];
         }
     }
@@ -374,35 +397,28 @@ __device__ void block_find(SrShared* S, const U* a, u64 start, u64 target)
 }
 
 // Sums of the first `n` of 1024 values, for all threads.
-template <typename U>
-__device__ u64 block_sum(SrShared* S, const U* a, int n)
+template <int NT, typename U>
+__device__ u64 block_sum(SrShared<NT>* S, const U* a, int n)
 {
     const int tid = threadIdx.x;
     u64 mine = 0;
 #pragma unroll
-    for (int i = 0; i < SR_BPT; ++i)
-        if (tid * SR_BPT + i < n) mine += (u64)a[tid * SR_BPT + i];
-    mine = warp_sum(mine);
-    __syncthreads();
-    if ((tid & 31) == 0) S->ws[tid >> 5] = mine;
-    __syncthreads();
-    u64 t = 0;
-    for (int w = 0; w < SR_NW; ++w) t += S->ws[w];
-    __syncthreads();
-    return t;
+    for (int i = 0; i < (SR_NB / NT); ++i)
+        if (tid * (SR_NB / NT) + i < n) mine += (u64)a[tid * (SR_NB / NT) + i];
+    return all_sum(S, mine);
 }
 
 // Adds this CTA's histogram to the others' into S->num and S->sum.
-template <typename T>
-__device__ void gather_histogram(const Row<T>& R, bool counts, bool sums)
+template <int NT, typename T>
+__device__ void gather_histogram(const Row<T, NT>& R, bool counts, bool sums)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     R.sync();
-    for (int i = threadIdx.x; i < SR_NB; i += SR_NT) {
+    for (int i = threadIdx.x; i < SR_NB; i += NT) {
         u64 m = 0;
         unsigned n = 0;
         for (int r = 0; r < R.C; ++r) {
-            const SrShared* o = R.of(r);
+            const SrShared<NT>* o = R.of(r);
             if (counts) n += o->count[i];
             if (sums) m += ((u64)o->hi[i] << 32) + o->lo[i];
         }
@@ -412,13 +428,15 @@ __device__ void gather_histogram(const Row<T>& R, bool counts, bool sums)
     R.sync();  // the others' histograms have been read
 }
 
-__device__ __forceinline__ void clear_histogram(SrShared* S)
+template <int NT>
+__device__ __forceinline__ void clear_histogram(SrShared<NT>* S)
 {
-    for (int i = threadIdx.x; i < SR_NB; i += SR_NT) S->count[i] = S->lo[i] = S->hi[i] = 0;
+    for (int i = threadIdx.x; i < SR_NB; i += NT) S->count[i] = S->lo[i] = S->hi[i] = 0;
     __syncthreads();
 }
 
-__device__ __forceinline__ void add_weight(SrShared* S, int b, u64 w)
+template <int NT>
+__device__ __forceinline__ void add_weight(SrShared<NT>* S, int b, u64 w)
 {
     if (!w) return;
     const unsigned wl = (unsigned)w, old = atomicAdd(&S->lo[b], wl);
@@ -427,10 +445,10 @@ __device__ __forceinline__ void add_weight(SrShared* S, int b, u64 w)
 }
 
 // Histogram of the columns of at least `least` by put(column, x) (-1: in none), over all CTAs of the row.
-template <typename T, typename F>
-__device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, F put)
+template <int NT, typename T, typename F>
+__device__ void histogram(const Row<T, NT>& R, float least, bool counts, bool sums, F put)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     clear_histogram(S);
     R.each(least, [&](int col, float x) {
         const int b = put(col, x);
@@ -442,7 +460,8 @@ __device__ void histogram(const Row<T>& R, float least, bool counts, bool sums, 
 }
 
 // Exclusive sums of n over the CTA's threads, and their total.
-__device__ __forceinline__ unsigned scan_counts(SrShared* S, unsigned n, unsigned& total)
+template <int NT>
+__device__ __forceinline__ unsigned scan_counts(SrShared<NT>* S, unsigned n, unsigned& total)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned inc = n;
@@ -453,22 +472,22 @@ __device__ __forceinline__ unsigned scan_counts(SrShared* S, unsigned n, unsigne
     __syncthreads();
     if (lane == 31) S->wi[warp] = inc;
     __syncthreads();
-    unsigned at = inc - n, all = 0;
-#pragma unroll
-    for (int w = 0; w < SR_NW; ++w) {
-        const unsigned x = S->wi[w];
-        if (w < warp) at += x;
-        all += x;
+    // every warp scans the warps' sums
+    unsigned all = lane < NT / 32 ? S->wi[lane] : 0;
+    for (int o = 1; o < NT / 32; o <<= 1) {
+        const unsigned t = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += t;
     }
-    total = all;
-    return at;
+    total = __shfl_sync(0xffffffffu, all, NT / 32 - 1);
+    const unsigned before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+    return inc - n + (warp ? before : 0);
 }
 
 // Each thread notes its columns of at least `least`, if no thread of the CTA has too many.
-template <typename T>
-__device__ __forceinline__ void note_columns(Row<T>& R, float least)
+template <int NT, typename T>
+__device__ __forceinline__ void note_columns(Row<T, NT>& R, float least)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     if (R.noted >= 0 || R.p.nvec * R.p.VE > 65536) return;
     int n = 0;
     R.p.each(least, [&](int col, float) {
@@ -479,11 +498,11 @@ __device__ __forceinline__ void note_columns(Row<T>& R, float least)
 }
 
 // The columns of at least `least` that take(x) names, of all CTAs and in ascending order, into the S->list of the row's
-// first CTA, or of all; their number (more than SR_LIST: the list is not complete).
-template <typename T, typename F>
-__device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
+// first CTA, or of all; their number (more than NT: the list is not complete).
+template <int NT, typename T, typename F>
+__device__ unsigned list_columns(const Row<T, NT>& R, float least, bool all, F take)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     unsigned n = 0, here;
     R.each(least, [&](int, float x) { n += take(x); });
     unsigned at = scan_counts(S, n, here), total = here;
@@ -496,7 +515,7 @@ __device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
             total += S->r_n[r];
         }
     }
-    if (n && total <= SR_LIST)
+    if (n && total <= NT)
         R.each(least, [&](int col, float x) {
             if (!take(x)) return;
             const u64 e = ((u64)order_key(x) << 32) | (unsigned)~col;
@@ -512,13 +531,14 @@ __device__ unsigned list_columns(const Row<T>& R, float least, bool all, F take)
 
 // The ranks of the n listed columns among the candidates, into S->rank: each entry's keys are compared with all, by as
 // many threads as there are for it.  A lower entry of the same key comes first.
-__device__ __forceinline__ void rank_list(SrShared* S, unsigned n)
+template <int NT>
+__device__ __forceinline__ void rank_list(SrShared<NT>* S, unsigned n)
 {
     const unsigned tid = threadIdx.x;
     S->keys[tid] = tid < n ? (unsigned)(S->list[tid] >> 32) : 0;
     __syncthreads();
     int g = 1;
-    while (g < 32 && n * (2 * g) <= SR_NT) g *= 2;
+    while (g < 32 && n * (2 * g) <= NT) g *= 2;
     const unsigned me = tid / g;
     if (me < n || g > 1) {
         const unsigned k = S->keys[me < n ? me : 0];
@@ -537,32 +557,13 @@ __device__ __forceinline__ void rank_list(SrShared* S, unsigned n)
     __syncthreads();
 }
 
-// Inclusive sums of v over the CTA's threads, and their total.
-__device__ __forceinline__ u64 scan_weights(SrShared* S, u64 v, u64& total)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const u64 inc = warp_inclusive(v);
-    __syncthreads();
-    if (lane == 31) S->ws[warp] = inc;
-    __syncthreads();
-    u64 before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < SR_NW; ++w) {
-        const u64 x = S->ws[w];
-        if (w < warp) before += x;
-        all += x;
-    }
-    total = all;
-    return before + inc;
-}
-
 // The first column, in ascending order over the whole row, at which the running sum of wt(column, x) over the columns of
 // at least `least` exceeds goal(total): only the CTA that holds it returns true, with S->where = the column,
 // S->before = the sum before it and S->inside = its weight.
-template <typename T, typename F, typename G>
-__device__ bool find_in_order(const Row<T>& R, float least, F wt, G goal)
+template <int NT, typename T, typename F, typename G>
+__device__ bool find_in_order(const Row<T, NT>& R, float least, F wt, G goal)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     const Part<T>& P = R.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     u64 mine = 0;
@@ -624,10 +625,10 @@ struct Border {
 
 // The last of the shortest prefix, in the candidates' order, of the n listed columns that, after sums of `mass` and
 // `count` before the list, reaches `target` (weights if BY_MASS, less than `band` off; columns if not).
-template <bool BY_MASS, typename T>
-__device__ Border border_in_list(const Row<T>& R, unsigned n, u64 mass, u64 count, u64 target, u64 band)
+template <bool BY_MASS, int NT, typename T>
+__device__ Border border_in_list(const Row<T, NT>& R, unsigned n, u64 mass, u64 count, u64 target, u64 band)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     const int tid = threadIdx.x;
     rank_list(S, n);
     if (tid < n) {
@@ -653,10 +654,10 @@ __device__ Border border_in_list(const Row<T>& R, unsigned n, u64 mass, u64 coun
 }
 
 // The token of a row whose candidates are all among the n listed columns.  False if an error bound left a choice open.
-template <typename T>
-__device__ __forceinline__ bool sample_list(const Row<T>& R, unsigned n, int top_k, float top_p, float u, int32_t* token)
+template <int NT, typename T>
+__device__ __forceinline__ bool sample_list(const Row<T, NT>& R, unsigned n, int top_k, float top_p, float u, int32_t* token)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     const int tid = threadIdx.x;
     const u64 e = tid < n ? S->list[tid] : 0;
     const u64 w = tid < n ? R.W(key_value((unsigned)(e >> 32))) : 0;
@@ -695,10 +696,10 @@ __device__ __forceinline__ bool sample_list(const Row<T>& R, unsigned n, int top
 
 // The border of the shortest prefix that holds `target` columns (BY_MASS = false) or weights summing to at least `target`
 // (less than `band` off), from the linear histogram in S->num / S->sum.
-template <bool BY_MASS, typename T>
-__device__ Border find_border(Row<T>& R, float least, u64 target, u64 band)
+template <bool BY_MASS, int NT, typename T>
+__device__ Border find_border(Row<T, NT>& R, float least, u64 target, u64 band)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     const int tid = threadIdx.x;
     if (BY_MASS) block_find(S, S->sum, 0, target - 1);
     else block_find(S, S->num, 0, target - 1);
@@ -715,7 +716,7 @@ __device__ Border find_border(Row<T>& R, float least, u64 target, u64 band)
     }
     note_columns(R, from);
     unsigned n = list_columns(R, from, true, [&](float x) { return x <= upper && R.bin(x) == b; });
-    while (n > SR_LIST) {
+    while (n > NT) {
         // too many: split the bin's range of keys, down to one key
         if (!keyed) {
             unsigned lo = 0xffffffffu, hi = 0;
@@ -760,9 +761,9 @@ __device__ Border find_border(Row<T>& R, float least, u64 target, u64 band)
         const unsigned top = khi - ((unsigned)sub << sh);
         klo = max(klo, sh ? top - ((1u << sh) - 1u) : top);
         khi = top;
-        if (n <= SR_LIST) n = list_columns(R, least, true, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
+        if (n <= NT) n = list_columns(R, least, true, [&](float x) { const unsigned k = order_key(x); return k >= klo && k <= khi; });
     }
-    if (n <= SR_LIST) return border_in_list<BY_MASS>(R, n, mass, count, target, band);
+    if (n <= NT) return border_in_list<BY_MASS>(R, n, mass, count, target, band);
     // one key, many columns: the last of them taken, in column order
     const u64 w = R.W(key_value(klo));
     u64 take = target - count;
@@ -783,10 +784,10 @@ __device__ Border find_border(Row<T>& R, float least, u64 target, u64 band)
 
 // The token of the row into `token` by the CTA that finds it, for rows whose candidates are not listed.  False if an
 // error bound left a choice open (never with precise weights).
-template <typename T>
-__device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, float u, int32_t* token)
+template <int NT, typename T>
+__device__ __forceinline__ bool sample_row(Row<T, NT>& R, int top_k, float top_p, float u, int32_t* token)
 {
-    SrShared* S = R.S;
+    SrShared<NT>* S = R.S;
     const int tid = threadIdx.x;
     Border B = {R.lmin, 0x7fffffff};
     if (tid == 0) S->unsure = 0;
@@ -809,11 +810,7 @@ __device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, fl
             if (x >= shallow) add_weight(S, R.bin_of(steps), w);
             else rest += w;
         });
-        rest = warp_sum(rest);
-        if ((tid & 31) == 0) S->ws[tid >> 5] = rest;
-        __syncthreads();
-        rest = 0;
-        for (int w = 0; w < SR_NW; ++w) rest += S->ws[w];
+        rest = all_sum(S, rest);
         if (R.C > 1 && tid < R.C) R.of(tid)->r_sum[R.rank] = rest;
         gather_histogram(R, false, true);
         if (R.C > 1) {
@@ -847,8 +844,8 @@ __device__ __forceinline__ bool sample_row(Row<T>& R, int top_k, float top_p, fl
     return R.W.precise || !open;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restrict__ logits, int cols, long long ld,
+template <int NT, typename T>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const T* __restrict__ logits, int cols, long long ld,
                                                                const float* __restrict__ temperature,
                                                                const int32_t* __restrict__ top_k,
                                                                const float* __restrict__ top_p,
@@ -857,7 +854,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
                                                                int C, int stage)
 {
     extern __shared__ __align__(16) char sr_raw[];
-    SrShared* S = reinterpret_cast<SrShared*>(sr_raw);
+    SrShared<NT>* S = reinterpret_cast<SrShared<NT>*>(sr_raw);
     const int r = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float T_ = temperature ? __ldg(temperature + r) : 1.f;
     const int k = top_k ? __ldg(top_k + r) : 0;
@@ -866,7 +863,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
         const unsigned t = sr_table.at[tid].x;
         S->table[tid] = make_uint2(t, __float_as_uint((float)t));
     }
-    Row<T> R;
+    Row<T, NT> R;
     constexpr int VE = Part<T>::VE;
     R.C = C;
     R.rank = rank;
@@ -878,12 +875,12 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     R.p.hi = min(cols, R.p.lo + each);
     R.p.c0 = R.p.lo - (int)((reinterpret_cast<uintptr_t>(R.p.g + R.p.lo) & 15u) / sizeof(T));
     R.p.nvec = R.p.hi > R.p.lo ? (R.p.hi - R.p.c0 + VE - 1) / VE : 0;
-    R.p.per = ((R.p.nvec + SR_NT - 1) / SR_NT) | 1;
+    R.p.per = ((R.p.nvec + NT - 1) / NT) | 1;
     R.p.kept = 0;
     R.noted = -1;
-    const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared));
+    const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared<NT>));
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (tid == SR_NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
+    if (tid == NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
         S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
         S->reach = mp >= 1.f ? 0.0 : mp > 0.f ? -(double)T_ * log((double)mp) : 0.0;
     }
@@ -891,23 +888,23 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     float v = -INFINITY;
     int idx = 0x7fffffff;
     constexpr int DEEP = 8;
-    for (int b = tid; b < R.p.nvec; b += SR_NT * DEEP) {
+    for (int b = tid; b < R.p.nvec; b += NT * DEEP) {
         uint4 x[DEEP];
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
-            if (b + SR_NT * i < R.p.nvec) x[i] = R.p.fetch(b + SR_NT * i);
+            if (b + NT * i < R.p.nvec) x[i] = R.p.fetch(b + NT * i);
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
-            if (b + SR_NT * i < R.p.nvec) {
+            if (b + NT * i < R.p.nvec) {
                 if (stage)
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kept + 16 * (b + SR_NT * i)), "r"(x[i].x), "r"(x[i].y),
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(kept + 16 * (b + NT * i)), "r"(x[i].x), "r"(x[i].y),
                                  "r"(x[i].z), "r"(x[i].w) : "memory");
                 const float m = R.p.largest(x[i]);
                 if (m > v || (m == v && idx == 0x7fffffff)) {  // columns ascend: an equal one later never wins
                     v = m;
 #pragma unroll
                     for (int e = VE - 1; e >= 0; --e)
-                        if (R.p.elem(x[i], e) == m) idx = R.p.c0 + (b + SR_NT * i) * VE + e;
+                        if (R.p.elem(x[i], e) == m) idx = R.p.c0 + (b + NT * i) * VE + e;
                 }
             }
     }
@@ -919,9 +916,9 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     }
     if (lane == 0) { S->wf[warp] = v; S->wi[warp] = idx; }
     __syncthreads();
-    v = S->wf[lane & (SR_NW - 1)];
-    idx = S->wi[lane & (SR_NW - 1)];
-    for (int o = SR_NW / 2; o; o >>= 1) {
+    v = S->wf[lane & ((NT / 32) - 1)];
+    idx = S->wi[lane & ((NT / 32) - 1)];
+    for (int o = (NT / 32) / 2; o; o >>= 1) {
         const float ov = __shfl_xor_sync(0xffffffffu, v, o);
         const int oi = __shfl_xor_sync(0xffffffffu, idx, o);
         if (ov > v || (ov == v && oi < idx)) { v = ov; idx = oi; }
@@ -964,7 +961,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     // few candidates: all of them listed by one CTA
     float least = R.lmin;
     bool few = mp > 0.f;
-    if (k > 0 && k <= SR_NT) {
+    if (k > 0 && k <= NT) {
         // the bin that the k-th largest of the threads' maxima lies in: at least k columns reach it
         clear_histogram(S);
         if (R.mine >= R.lmin) atomicAdd(&S->count[R.bin(R.mine)], 1u);
@@ -985,7 +982,7 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     if (few) {
         note_columns(R, least);
         const unsigned n = list_columns(R, least, false, [](float) { return true; });
-        if (n <= SR_LIST) {
+        if (n <= NT) {
             if (rank == 0) {
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
@@ -1006,26 +1003,24 @@ __global__ void __launch_bounds__(SR_NT, 2) sample_rows_kernel(const T* __restri
     }
 }
 
-template <typename T>
-int launch(const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
+template <typename T, int NT>
+int launch(int C, const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
            const float* top_p, const float* min_p, const float* uniforms, int32_t* tokens, cudaStream_t st)
 {
-    auto kernel = sample_rows_kernel<T>;
+    constexpr int STAGE = NT == 512 ? SR_STAGE_BYTES : SR_WIDE_BYTES + 4096;
+    static_assert(sizeof(SrShared<NT>) + STAGE <= 227 * 1024, "shared memory");
+    auto kernel = sample_rows_kernel<NT, T>;
     int sms = 0;
     static mfs::PerDevice ready;
-    const cudaError_t e = mfs::op_device(ready, (const void*)kernel, (int)(sizeof(SrShared) + SR_STAGE_BYTES), &sms);
+    const cudaError_t e = mfs::op_device(ready, (const void*)kernel, (int)(sizeof(SrShared<NT>) + STAGE), &sms);
     if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
-    // CTAs per row: parts of at most 64 KB, so that two CTAs share an SM, and more where rows leave SMs empty
-    // and a part keeps at least 4096 columns
-    int C = 1;
-    while (C < SR_MAX_C && ((long long)cols * sizeof(T) / C > 64 * 1024 || ((long long)rows * C * 2 <= sms && cols / C >= 8192))) C *= 2;
     const long long part = ((long long)cols + C - 1) / C * sizeof(T) + 32;
-    const bool stage = part <= SR_STAGE_BYTES;
-    const size_t smem = sizeof(SrShared) + (stage ? (size_t)part : 0);
+    const bool stage = part <= STAGE;
+    const size_t smem = sizeof(SrShared<NT>) + (stage ? (size_t)part : 0);
     if ((long long)rows * C > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, "sample_rows", "too many rows");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
-    cfg.blockDim = dim3(SR_NT);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
@@ -1036,6 +1031,26 @@ int launch(const void* logits, int rows, int cols, long long ld, const float* te
     cfg.numAttrs = C > 1 ? 1 : 0;
     return mfs::op_launched("sample_rows", cudaLaunchKernelEx(&cfg, kernel, (const T*)logits, cols, ld, temperature, top_k, top_p, min_p,
                                                               uniforms, tokens, C, (int)stage));
+}
+
+// CTAs of 512 threads, two on an SM: as many per row as keep its parts within 64 KB, and more where rows leave SMs empty
+// and a part keeps at least 4096 columns.  Where that makes clusters of rows that would fill the SMs with fewer CTAs of
+// 1024 threads, one on an SM, those are taken: an exchange between the CTAs of a row costs over 1 us.
+template <typename T>
+int choose(const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
+           const float* top_p, const float* min_p, const float* uniforms, int32_t* tokens, cudaStream_t st)
+{
+    int sms = 0;
+    static mfs::PerDevice known;
+    const cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
+    if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
+    const long long bytes = (long long)cols * sizeof(T);
+    int C = 1, wide = 1;
+    while (C < SR_MAX_C && (bytes / C > 64 * 1024 || ((long long)rows * C * 2 <= sms && cols / C >= 8192))) C *= 2;
+    while (wide < C && bytes / wide > SR_WIDE_BYTES) wide *= 2;
+    if (wide < C && (long long)rows * wide >= sms)
+        return launch<T, 1024>(wide, logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
+    return launch<T, 512>(C, logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
 }
 
 }  // namespace
@@ -1052,6 +1067,6 @@ extern "C" int mfs_sample_rows(const void* logits, int dtype, int rows, int cols
     if (!logits || !uniforms || !tokens) return mfs::op_fail(MFS_E_ARG, op, "null logits, uniforms or tokens");
     if ((uintptr_t)logits % (dtype == MFS_DTYPE_BF16 ? 2 : 4)) return mfs::op_fail(MFS_E_ARG, op, "misaligned logits");
     cudaStream_t st = (cudaStream_t)cuda_stream;
-    return dtype == MFS_DTYPE_BF16 ? launch<bf16>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st)
-                                   : launch<float>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
+    return dtype == MFS_DTYPE_BF16 ? choose<bf16>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st)
+                                   : choose<float>(logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
 }
