@@ -653,6 +653,52 @@ __device__ Border border_in_list(const Row<T, NT>& R, unsigned n, u64 mass, u64 
     return {key_value((unsigned)(b >> 32)), (int)~(unsigned)b};
 }
 
+// The same among the CTA's threads, one entry e of weight w each where `in` is set: the entry that is the last of the
+// shortest prefix, in descending order of the entries, that reaches `target` (weights if BY_MASS, entries if not), by a
+// histogram and a comparison of all with all in the border's bin.
+template <bool BY_MASS, int NT, typename T>
+__device__ u64 border_among(const Row<T, NT>& R, u64 e, u64 w, bool in, u64 target, u64 band)
+{
+    SrShared<NT>* S = R.S;
+    const int tid = threadIdx.x, b = in ? R.bin(key_value((unsigned)(e >> 32))) : -1;
+    clear_histogram(S);
+    if (in) {
+        if (BY_MASS) add_weight(S, b, w);
+        else atomicAdd(&S->count[b], 1u);
+    }
+    __syncthreads();
+    if (BY_MASS) {
+        for (int i = tid; i < SR_NB; i += NT) S->sum[i] = ((u64)S->hi[i] << 32) + S->lo[i];
+        __syncthreads();
+        block_find(S, S->sum, 0, target - 1);
+    } else {
+        block_find(S, S->count, 0, target - 1);
+    }
+    const bool here = in && b == S->where;
+    u64 above = S->before;
+    unsigned m;
+    const unsigned at = scan_counts(S, here, m);
+    u64* weight = S->sum;
+    if (here) {
+        S->ranked[at] = e;
+        weight[at] = w;
+    }
+    __syncthreads();
+    if (here) {
+        for (unsigned i = 0; i < m; ++i)
+            if (S->ranked[i] > e) above += BY_MASS ? weight[i] : 1;
+        const u64 upto = above + (BY_MASS ? w : 1);
+        if (above < target && upto >= target) {
+            S->inside = e;
+            if (BY_MASS && (upto < target + band || (above > 0 && above + band >= target))) S->unsure = 1;
+        }
+    }
+    __syncthreads();
+    const u64 border = S->inside;
+    __syncthreads();
+    return border;
+}
+
 // The token of a row whose candidates are all among the n listed columns.  False if an error bound left a choice open.
 template <int NT, typename T>
 __device__ __forceinline__ bool sample_list(const Row<T, NT>& R, unsigned n, int top_k, float top_p, float u, int32_t* token)
@@ -663,10 +709,22 @@ __device__ __forceinline__ bool sample_list(const Row<T, NT>& R, unsigned n, int
     const u64 w = tid < n ? R.W(key_value((unsigned)(e >> 32))) : 0;
     u64 total;
     if (tid == 0) S->unsure = 0;
-    unsigned keep = top_k > 0 ? min(n, (unsigned)top_k) : n, rank = 0;  // columns kept, of the largest
-    if (keep < n || top_p < 1.f) {
+    __syncthreads();
+    unsigned keep = top_k > 0 ? min(n, (unsigned)top_k) : n;  // columns kept, of the largest
+    bool in = tid < n;
+    if (n > 256) {
+        if (keep < n) {  // all threads take part
+            const u64 border = border_among<false>(R, e, w, in, keep, 0);
+            in = in && e >= border;
+        }
+        if (top_p < 1.f) {
+            total = all_sum(S, in ? w : 0);
+            const u64 border = border_among<true>(R, e, w, in, max((u64)1, fraction(top_p, total, true)), R.band(total));
+            in = in && e >= border;
+        }
+    } else if (keep < n || top_p < 1.f) {
         rank_list(S, n);
-        rank = tid < n ? S->rank[tid] : n;
+        const unsigned rank = tid < n ? S->rank[tid] : n;
         if (top_p < 1.f) {
             if (tid < n) S->ranked[rank] = w;
             __syncthreads();
@@ -679,9 +737,10 @@ __device__ __forceinline__ bool sample_list(const Row<T, NT>& R, unsigned n, int
             __syncthreads();
             keep = S->where;
         }
+        in = rank < keep;
     }
     // the draw, in column order
-    const u64 mine = tid < n && rank < keep ? w : 0;
+    const u64 mine = in ? w : 0;
     const u64 upto = scan_weights(S, mine, total);
     const u64 target = u < 1.f || !(u == u) ? fraction(u, total, false) : total - 1, band = R.band(total);
     if (mine && upto > target && upto - mine <= target) {
