@@ -1,7 +1,9 @@
 // mfs_prompt_attention: causal attention over packed prompts.
 //
-// bf16: one CTA per SM takes blocks of 256 query rows of one sequence and head, as two 128-row tiles,
-// and walks over the keys they may see in tiles of 128.  Scores S = Q K^T and outputs O += P V are
+// bf16: one CTA per SM takes blocks of two 128-row tiles of queries and walks over the keys they may
+// see in tiles of 128.  The two tiles are the same rows of two heads that share keys, or, where the heads
+// of a group are odd in number, 256 rows of one head (whose second tile sees one tile of keys more, so
+// that the first one's warps wait at the end).  Scores S = Q K^T and outputs O += P V are
 // tcgen05 MMAs with accumulators in tensor memory (S 2 x 128 columns, O 2 x head_dim); Q, K and V
 // tiles arrive by TMA, K and V through a ring.  Each 128-row tile has four warps with one row per
 // thread: they read a row of scores into registers, take its maximum without any exchange between
@@ -35,7 +37,6 @@ __device__ __forceinline__ void put(bf16* p, float x) { *p = __float2bfloat16_rn
 // ------------------------------------------------------------- tensor cores
 
 constexpr int PT_M = 128;                    // query rows per tile, keys per tile
-constexpr int PT_BLOCK = 2 * PT_M;           // query rows per CTA
 constexpr int PT_THREADS = 384;              // warps 0-3, 4-7: softmax of the two tiles; 8: MMA; 9: TMA; 10, 11: V of masked tiles (11 also the next block)
 constexpr unsigned long long PT_WAIT_NS = 2000000000ull;
 
@@ -47,7 +48,7 @@ struct PtShape {
     static constexpr int BYTES = 1024 + 2 * TILE + STAGES * TILE;
 };
 
-// A block of rows: tokens b + r0 .. of the sequence of len tokens from token b, of head h; h < 0: no more.
+// A block: rows r0 .. of the sequence of len tokens from token b, of head h; h < 0: no more.
 struct __align__(16) PtWork {
     int b, len, r0, h;
 };
@@ -209,7 +210,8 @@ struct PtArgs {
     bf16* out;
     long long q_stride, k_stride, v_stride, out_stride;
     int n_tokens, n_seqs, hq, g, window;
-    float c;  // scale * log2(e)
+    int down, across;  // rows and heads from a block's first tile to its second: 0 and 1, or 128 and 0
+    float c;           // scale * log2(e)
 };
 
 // Row t (token) of head h again, by the warp: the running maximum and sum over keys lo .. t.
@@ -241,19 +243,19 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) { return (x & 0x7f80u) =
 
 // The tiles of keys of a block.
 struct PtItem {
-    int b, len, r0, h, W;
+    int b, len, r0, h, W, down;
     int first[2], last[2];  // of each row tile
     int t0, t1;             // of both
 
     __device__ __forceinline__ bool two() const { return last[1] > first[1]; }
     // does some row of tile x not see some key of tile t?
-    __device__ __forceinline__ bool masked(int x, int t) const { return t == last[x] - 1 || (W > 0 && PT_M * t < r0 + PT_M * (x + 1) - W); }
+    __device__ __forceinline__ bool masked(int x, int t) const { return t == last[x] - 1 || (W > 0 && PT_M * t < r0 + down * x + PT_M - W); }
     __device__ __forceinline__ bool active(int x, int t) const { return t >= first[x] && t < last[x]; }
     __device__ __forceinline__ bool edge(int t) const { return (active(0, t) && masked(0, t)) || (active(1, t) && masked(1, t)); }
 };
 
 // Block i of this CTA, for a whole warp; false: no more (or the wait gave up).
-__device__ __forceinline__ bool next_item(PtBars& B, int i, int W, PtItem& I)
+__device__ __forceinline__ bool next_item(PtBars& B, int i, const PtArgs& A, PtItem& I)
 {
     if (!bar_wait(&B.work_full[i & 3], (i >> 2) & 1, &B.abort)) return false;
     const PtWork w = B.work[i & 3];
@@ -262,9 +264,11 @@ __device__ __forceinline__ bool next_item(PtBars& B, int i, int W, PtItem& I)
     I.len = w.len;
     I.r0 = w.r0;
     I.h = w.h;
+    const int W = A.window;
     I.W = W;
+    I.down = A.down;
     for (int x = 0; x < 2; ++x) {
-        const int r = w.r0 + PT_M * x;
+        const int r = w.r0 + A.down * x;
         I.first[x] = W > 0 ? max(0, r - W + 1) / PT_M : 0;
         I.last[x] = r < w.len ? r / PT_M + 1 : I.first[x];
     }
@@ -280,20 +284,19 @@ __device__ __forceinline__ void done_with_item(PtBars& B, int i)
     if ((threadIdx.x & 31) == 0) bar_arrive(&B.work_empty[i & 3]);
 }
 
-// Deals out the call's blocks of ROWS rows.  Pairs (row block, sequence) are ordered by block number, largest first (about the
+// Deals out the call's blocks, of `rows` rows and one of `hq` heads or pairs of heads.  Pairs (row block, sequence) are ordered by block number, largest first (about the
 // number of their keys), then by sequence; an item is a pair and a head, heads innermost, so that neighbouring CTAs
 // share keys; round r of G items goes to the CTAs in ascending order for even r, descending for odd r.
-template <int ROWS>
 struct PtDealer {
     const int32_t* cu;
-    int n_tokens, n_seqs, hq;
+    int n_tokens, n_seqs, hq, rows;
     int level, above, upto;  // the current block number; pairs of larger numbers; those and its own
 
     __device__ __forceinline__ int blocks(int s, int& b, int& len) const
     {
         b = min(max(__ldg(cu + s), 0), n_tokens);
         len = max(min(__ldg(cu + s + 1), n_tokens) - b, 0);
-        return (len + ROWS - 1) / ROWS;
+        return (len + rows - 1) / rows;
     }
     __device__ int pairs_from(int lv) const
     {
@@ -301,8 +304,8 @@ struct PtDealer {
         for (int s = threadIdx.x & 31; s < n_seqs; s += 32) n += max(0, blocks(s, b, len) - lv);
         return __reduce_add_sync(0xffffffffu, n);
     }
-    __device__ __forceinline__ PtDealer(const int32_t* cu_, int n_tokens_, int n_seqs_, int hq_)
-        : cu(cu_), n_tokens(n_tokens_), n_seqs(n_seqs_), hq(hq_), level(0), above(0), upto(0)
+    __device__ __forceinline__ PtDealer(const int32_t* cu_, int n_tokens_, int n_seqs_, int hq_, int rows_)
+        : cu(cu_), n_tokens(n_tokens_), n_seqs(n_seqs_), hq(hq_), rows(rows_), level(0), above(0), upto(0)
     {
     }
     __device__ void start()
@@ -333,7 +336,7 @@ struct PtDealer {
             const int l = __ffs(m) - 1;
             w.b = __shfl_sync(0xffffffffu, b, l);
             w.len = __shfl_sync(0xffffffffu, len, l);
-            w.r0 = level * ROWS;
+            w.r0 = level * rows;
             w.h = (int)(it % hq);
             return true;
         }
@@ -347,20 +350,20 @@ __device__ __noinline__ void again(const PtArgs& A, PtBars& B, int i, int x, int
 {
     PtItem I;
     const int W = A.window, lane = threadIdx.x & 31;
-    if (!next_item(B, i, W, I)) return;  // published long ago
-    const int r1 = I.r0 + x * PT_M + 32 * quarter;
+    if (!next_item(B, i, A, I)) return;  // published long ago
+    const int r1 = I.r0 + x * A.down + 32 * quarter, h = I.h + x * A.across;
     for (int r = r1; r < min(I.len, r1 + 32); ++r) {
         const int lo = W > 0 ? max(0, r - W + 1) : 0;
         bool sees = false;
         for (int t = max(I.t0, lo / PT_M); t <= r / PT_M && !sees; ++t) {
             if (!I.edge(t)) continue;
             for (int j = max(lo, t * PT_M); j <= min(r, t * PT_M + PT_M - 1); ++j) {
-                const uint32_t* p = reinterpret_cast<const uint32_t*>(A.v + (long long)(I.b + j) * A.v_stride + I.h / A.g * HD);
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(A.v + (long long)(I.b + j) * A.v_stride + h / A.g * HD);
                 for (int e = lane; e < HD / 2; e += 32) sees = sees || not_finite2(__ldg(p + e));
             }
             sees = __any_sync(0xffffffffu, sees);
         }
-        if (sees) plain_row<HD>(A, I.b + r, I.h, I.b + lo);
+        if (sees) plain_row<HD>(A, I.b + r, h, I.b + lo);
     }
 }
 
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&B.tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    PtDealer<PT_BLOCK> deal(A.cu, A.n_tokens, A.n_seqs, A.hq);
+    PtDealer deal(A.cu, A.n_tokens, A.n_seqs, A.hq >> A.across, PT_M + A.down);
     if (warp == 11) deal.start();
     if (tid == 9 * 32) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&mq) : "memory");
@@ -433,10 +436,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             int n = 0, slot = 0;               // tiles asked for
             unsigned par = 1, q_par[2] = {1, 1};
             bool ok = true, q_used[2] = {false, false};
-            for (int i = 0; ok && next_item(B, i, W, I); ++i) {
+            for (int i = 0; ok && next_item(B, i, A, I); ++i) {
                 auto query = [&](int x) {
                     if (!bar_wait(&B.q_empty[x], q_par[x], &B.abort)) return false;
-                    if (lane == 0) load(&mq, sq + x * S::TILE, I.h, I.b + I.r0 + PT_M * x, &B.q_full[x]);
+                    if (lane == 0) load(&mq, sq + x * S::TILE, I.h + A.across * x, I.b + I.r0 + A.down * x, &B.q_full[x]);
                     q_par[x] ^= 1;
                     q_used[x] = true;
                     return true;
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             };
             bool ok = true;
             PtItem I;
-            for (int i = 0; ok && next_item(B, i, W, I); ++i) {
+            for (int i = 0; ok && next_item(B, i, A, I); ++i) {
                 // scores of row tile x for tile t of keys, in the ring at ks; the block's Q is free after its last
                 auto score_tile = [&](int x, int t, int ks) {
                     if (t == I.first[x]) {
@@ -558,6 +561,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             auto publish = [&](int i) {  // block i
                 if (!more) return true;
                 more = deal.get(i, w);
+                w.h <<= A.across;
                 if (!bar_wait(&B.work_empty[i & 3], ((i >> 2) & 1) ^ 1, &B.abort)) return false;
                 if (lane == 0) {
                     if (!more) w.h = -1;
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             };
             int i = 0;
             ok = publish(0);
-            for (; ok && next_item(B, i, W, I); ++i) {
+            for (; ok && next_item(B, i, A, I); ++i) {
                 ok = publish(i + 1);
                 for (int t = I.t0; t < I.t1 && ok; ++t) {
                     ok = bar_wait(&B.kv_full[slot], par, &B.abort);
@@ -617,9 +621,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             if (*(volatile int*)&B.abort)
                 // given up: NaN for the blocks that nobody will compute
                 for (++i; more; ++i) {
-                    for (int r = w.r0; r < min(w.len, w.r0 + PT_BLOCK); ++r)
-                        for (int e = lane; e < HD; e += 32) A.out[(long long)(w.b + r) * A.out_stride + w.h * HD + e] = __float2bfloat16_rn(NAN);
+                    for (int r = w.r0; r < min(w.len, w.r0 + PT_M + A.down); ++r)
+                        for (int e = lane; e < HD << A.across; e += 32)
+                            A.out[(long long)(w.b + r) * A.out_stride + w.h * HD + e] = __float2bfloat16_rn(NAN);
                     more = deal.get(i + 1, w);
+                    w.h <<= A.across;
                 }
         }
     } else {
@@ -633,10 +639,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             int first, last, rr;  // rr: the row in its sequence
             {
                 PtItem I;
-                if (!next_item(B, i, W, I)) break;
+                if (!next_item(B, i, A, I)) break;
                 first = x ? I.first[1] : I.first[0];
                 last = x ? I.last[1] : I.last[0];
-                rr = I.r0 + x * PT_M + row;
+                rr = I.r0 + x * A.down + row;
             }
             float m = -INFINITY;       // the maximum in use (raw scores), exact up to 2^8 in the weights
             uint64_t l2[2] = {0, 0};   // the sum, in four parts
@@ -712,7 +718,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 unpair(add2(l2[0], l2[1]), l0, l1);
                 const float inv = ok ? 1.f / (l0 + l1) : NAN;
                 const PtWork w = B.work[i & 3];
-                bf16* o = A.out + (long long)(w.b + rr) * A.out_stride + w.h * HD;
+                bf16* o = A.out + (long long)(w.b + rr) * A.out_stride + (w.h + x * A.across) * HD;
 #pragma unroll
                 for (int k = 0; k < HD; k += 32) {
                     uint32_t r[32];
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
     __shared__ PtWork work;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     if (tid < 32) {
-        PtDealer<PF_ROWS> deal(A.cu, A.n_tokens, A.n_seqs, A.hq);
+        PtDealer deal(A.cu, A.n_tokens, A.n_seqs, A.hq, PF_ROWS);
         deal.start();
         PtWork w;
         if (!deal.get(0, w)) w.h = -1;
@@ -981,12 +987,16 @@ int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
             return mfs::op_fail(MFS_E_ARG, op, "the tensor is too large for a tensor map");
     }
     PtArgs A = {cu, (const bf16*)q, (const bf16*)k, (const bf16*)v, (bf16*)out, q_stride, k_stride, v_stride, out_stride,
-                n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
+                n_tokens, n_seqs, hq, hq / hkv, window, PT_M, 0, scale * 1.44269504088896340736f};
+    if (A.g % 2 == 0) {
+        A.down = 0;
+        A.across = 1;
+    }
     int sms = 0;
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, (const void*)prompt_mma_kernel<HD>, S::BYTES, &sms);
     if (e == cudaSuccess) {
-        const long long most = ((long long)n_tokens / PT_BLOCK + n_seqs) * hq;  // blocks there can be
+        const long long most = ((long long)n_tokens / (PT_M + A.down) + n_seqs) * (hq >> A.across);  // blocks there can be
         prompt_mma_kernel<HD><<<(unsigned)(most < sms ? most : sms), PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);
         e = cudaGetLastError();
     }

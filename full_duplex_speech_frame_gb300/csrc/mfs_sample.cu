@@ -23,7 +23,9 @@
 // Weights are unsigned fixed point (2^scale for the maximum's), so sums are exact
 // whatever order the atomics take, and the row's token is the same on every run.
 // A weight is 2^-y = 2^-n 2^-(i/64) 2^-r with y a pair of fp32, a table for i and
-// three terms for |r| < 1/128: 2^-29 relative.  Each comparison of sums is made
+// three terms for |r| < 1/128: off by less than 2^-28 of itself (2^-30.2 from the
+// terms' own rounding, 2^-31 each from the table's and the result's, 2^-31.5 each from
+// r's, the table's in fp32 and the product's, 2^-34.7 from the terms left out).  Each comparison of sums is made
 // with a bound on that error, and a row in which one falls inside the bound is done
 // again with exponentials of about 2^-40 relative error (pairs of fp32), which
 // decides it.  64-bit floating point, two products a cycle and SM here, is kept to
@@ -340,8 +342,8 @@ struct Row {
             if (x >= least) f(p.c0 + c, x);
         }
     }
-    // how far a comparison of two sums of fast weights may be off: 2^-29 of each, a unit per column
-    __device__ __forceinline__ u64 band(u64 total) const { return W.precise ? 0 : (total >> 28) + 2ull * cols + 2; }
+    // how far a comparison of two sums of fast weights may be off: less than 2^-28 of each, a unit per column
+    __device__ __forceinline__ u64 band(u64 total) const { return W.precise ? 0 : (total >> 27) + 2ull * cols + 2; }
 };
 
 // Inclusive sums of v over the CTA's threads, and their total.

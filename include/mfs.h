@@ -372,8 +372,8 @@ int mfs_argmax_rows_noalloc(const float* logits, int rows, int cols, long long l
  *     running sum of weights exceeds uniforms[r] times their sum (a uniform below
  *     0 or NaN acts as 0, one of 1 or more takes the last candidate).
  * Weights and sums are exact enough that the token is the one that the
- * definition gives in real numbers, unless a sum lies within 1e-11 of a border
- * relative to the total.  The same inputs always give the same tokens.
+ * definition gives in real numbers, unless a sum lies within 2^-40 + cols^2 2^-63
+ * of the total from a border.  The same inputs always give the same tokens.
  * Enqueues on `stream` and returns; no memory is allocated, so it can be captured.
  * MFS_E_ARG on bad sizes or NULL pointers, before anything is enqueued. */
 #define MFS_SAMPLE_MAX_COLS (1 << 22)
@@ -473,7 +473,9 @@ int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv
  * bf16 runs on the tensor cores (fp32 scores, statistics and sums; the softmax
  * weights are rounded to bf16 for the product with the values); fp32 runs on the
  * CUDA cores in fp32.  A key or value outside a row's range (another sequence's,
- * a later token's) has no influence on it, NaN and infinities included.
+ * a later token's) has no influence on it, NaN and infinities included.  If one
+ * of the bf16 kernel's internal waits gives up (about 2 s: a stalled device), the
+ * rows that it had still to write are NaN.
  * Enqueues and returns; MFS_E_ARG on bad sizes, strides, alignment or NULL. */
 int mfs_prompt_attention(int dtype, int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride,
                          int n_q_heads, const void* k, long long k_stride, const void* v, long long v_stride,

@@ -618,3 +618,97 @@ def test_binding_refuses_tensors_that_do_not_fit(mfs):
     refused(sample, x, u, out, top_k=_f32([1, 1]))
     refused(sample, x.t(), u, out)
     refused(sample, x[:, :0], u, out)
+
+
+# ------------------------------------------------------------- calls at the edges
+
+def test_sample_rows_of_extreme_shapes(mfs):
+    """Many short rows; one row of the most columns; a row too wide for shared memory with each filter."""
+    rng = np.random.default_rng(41)
+    x = _normal(rng, 5000, 50, scale=2.0)
+    u = rng.random(5000).astype(np.float32)
+    t, k, p, m = np.full(5000, 0.9), rng.integers(0, 60, 5000), rng.random(5000).astype(np.float32) * 1.2, rng.random(5000).astype(np.float32) * 0.2
+    xs = _np(x)
+    assert _sample(mfs, x, u, t, k, p, m).tolist() == [S.sample_row(xs[r], u[r], np.float32(0.9), k[r], p[r], m[r]) for r in range(5000)]
+    for cols, dtype in ((1 << 22, "bf16"), (500_001, "f32")):
+        x = _normal(rng, 1, cols, dtype=dtype, scale=3.0)
+        xs = _np(x)[0]
+        for t, k, p, m in ((1.0, 0, 1.0, 0.0), (0.8, 40, 0.9, 0.0), (1.0, 0, 0.8, 0.0), (1.2, 3000, 1.0, 0.0), (1.0, 0, 1.0, 0.01)):
+            assert _sample(mfs, x, [0.37], [t], [k], [p], [m])[0] == S.sample_row(xs, np.float32(0.37), np.float32(t), k, np.float32(p), np.float32(m))
+
+
+@pytest.mark.parametrize("cols", [700, 40000])
+def test_sample_rows_of_ties_and_flat_rows(mfs, cols):
+    """Few distinct logits, so that borders fall among equal ones; temperatures from almost 0 to infinity."""
+    rng = np.random.default_rng(cols)
+    rows = 60
+    x = _torch().from_numpy(rng.integers(-3, 3, (rows, cols)).astype(np.float32)).cuda()
+    u = rng.random(rows).astype(np.float32)
+    t = np.array([1e-20, 0.01, 0.5, 1.0, 40.0, np.inf] * 10)
+    k = np.array([0, 1, 7, 300, 600, cols // 3, cols, cols + 5, 0, 0] * 6)
+    p = np.array([1.0, 0.5, 0.99, 0.2] * 15).astype(np.float32)
+    m = np.array([0.0, 0.0, 0.1] * 20).astype(np.float32)
+    xs = _np(x)
+    want = [S.sample_row(xs[r], u[r], np.float32(t[r]), k[r], p[r], m[r]) for r in range(rows)]
+    assert _sample(mfs, x, u, t, k, p, m).tolist() == want
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_paged_attention_over_its_own_queries(mfs, dtype):
+    """out may be q; the table may be shared by all sequences (stride 0) and the pages too."""
+    torch = _torch()
+    rng = np.random.default_rng(43)
+    kc, vc = _pool(rng, 64, 2, 16, 128, dtype)
+    table = torch.randperm(64, device="cuda").to(torch.int32)[None].expand(5, 64)
+    cache = mfs.PagedKV(kc, vc, table)
+    q = _normal(rng, 5, 8, 128, dtype=dtype)
+    kv = _i32([1000, 3, 517, 0, 1024])
+    want = torch.empty_like(q)
+    mfs.mfs_paged_attention(cache, q, kv, want)
+    k = _np(kc)[table[0].cpu().numpy()].transpose(0, 2, 1, 3).reshape(-1, 2, 128)
+    v = _np(vc)[table[0].cpu().numpy()].transpose(0, 2, 1, 3).reshape(-1, 2, 128)
+    for s, n in ((0, 1000), (4, 1024)):
+        ref, weighted, size = S.attend(_np(q[s, 5]), k[:n, 1], v[:n, 1], 128 ** -0.5)
+        assert (np.abs(_np(want[s, 5]) - ref) <= S.attention_tolerance(ref, weighted, size, n, 128, dtype == "bf16")).all()
+    mfs.mfs_paged_attention(cache, q, kv, q)
+    assert torch.equal(q, want)
+
+
+def test_calls_on_two_streams_at_once(mfs):
+    """Prompts, tokens and sampling on two streams, each with outputs and a workspace of its own, repeated."""
+    torch = _torch()
+    rng = np.random.default_rng(44)
+    kc, vc = _pool(rng, 300, 4, 16, 128, "bf16")
+    cache = mfs.PagedKV(kc, vc, torch.arange(300, dtype=torch.int32, device="cuda").reshape(3, 100))
+    q, kv = _normal(rng, 3, 16, 128, dtype="bf16"), _i32([1600, 100, 900])
+    pq, pk, pv, cu = _normal(rng, 1500, 16, 128, dtype="bf16"), _normal(rng, 1500, 4, 128, dtype="bf16"), _normal(rng, 1500, 4, 128, dtype="bf16"), _i32([0, 400, 1500])
+    x, u = _normal(rng, 200, 33000, scale=3.0), _f32(rng.random(200))
+    p = torch.full((200,), 0.9, device="cuda")
+
+    def run(stream):
+        a, b, c = torch.empty_like(q), torch.empty_like(pq), torch.empty(200, dtype=torch.int32, device="cuda")
+        ws = mfs.mfs_paged_attention_workspace(cache, 16)
+        torch.cuda.synchronize()
+        return a, b, c, lambda: (mfs.mfs_paged_attention(cache, q, kv, a, workspace=ws, stream=stream), mfs.mfs_prompt_attention(pq, pk, pv, cu, b, stream=stream),
+                                 mfs.mfs_sample_rows(x, u, c, top_p=p, stream=stream))
+
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    one, two = run(s1.cuda_stream), run(s2.cuda_stream)
+    one[3]()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in one[:3]]
+    for _ in range(10):
+        one[3]()
+        two[3]()
+    torch.cuda.synchronize()
+    for t in (one, two):
+        assert all(torch.equal(a, b) for a, b in zip(t[:3], want))
+
+
+def test_prompt_attention_many_short_sequences(mfs):
+    """Padded batches: far more entries in cu than sequences with tokens, and hundreds of short ones."""
+    rng = np.random.default_rng(45)
+    lens = np.zeros(700, int)
+    lens[::3] = rng.integers(1, 9, len(lens[::3]))
+    for dtype in ("bf16", "f32"):
+        _check_prompt(mfs, rng, lens.tolist(), 4, 2, 64, dtype)
