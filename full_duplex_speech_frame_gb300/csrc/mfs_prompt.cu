@@ -370,7 +370,7 @@ __device__ __noinline__ void again(const PtArgs& A, PtBars& B, int i, int x, int
 // The top bit of each half is set if that half's exponent is all ones (a bf16 infinity or NaN).
 __device__ __forceinline__ uint32_t ones_exponent(uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; }
 
-template <int HD>
+template <int HD, bool PAIRED>
 __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_constant__ CUtensorMap mq,
                                                                    const __grid_constant__ CUtensorMap mk,
                                                                    const __grid_constant__ CUtensorMap mv,
@@ -497,6 +497,64 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             };
             bool ok = true;
             PtItem I;
+            if constexpr (PAIRED) {
+                // Both row tiles see the same tiles of keys.  The steps of all blocks follow each other: the scores of the
+                // next step, of the next block after the last tile, go behind each outputs.
+                bool have = next_item(B, 0, A, I), fresh = true;  // fresh: the step is its block's first
+                int i = 0, t = I.t0, t1 = I.t1;
+                auto score_tile = [&](int x, int ks, bool first, bool last) {
+                    if (first) {
+                        if (!bar_wait(&B.q_full[x], q_par[x], &B.abort)) return false;
+                        q_par[x] ^= 1;
+                        fence_after();
+                    }
+                    scores(x, ks);
+                    signal(&B.s_full[x]);
+                    if (last) signal(&B.q_empty[x]);
+                    return true;
+                };
+                if (have) {
+                    ok = bar_wait(&B.kv_full[slot], par, &B.abort);
+                    fence_after();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) ok = ok && score_tile(x, slot, true, t + 1 == t1);
+                    signal(&B.kv_empty[slot]);
+                    step();
+                }
+                while (ok && have) {
+                    const bool ends = t + 1 == t1, was_fresh = fresh;
+                    if (ends) {
+                        have = next_item(B, i + 1, A, I);
+                        t = I.t0;
+                        t1 = I.t1;
+                    } else {
+                        ++t;
+                    }
+                    fresh = ends;
+                    const int vs = slot;
+                    ok = bar_wait(&B.v_ready[v_at & 7], (v_at >> 3) & 1, &B.abort);  // loaded, and cleared where masked
+                    ++v_at;
+                    step();
+                    const int ks = slot;
+                    if (have) {
+                        ok = ok && bar_wait(&B.kv_full[ks], par, &B.abort);
+                        step();
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        ok = ok && bar_wait(&B.p_full[x], p_par[x], &B.abort);
+                        if (!ok) break;
+                        p_par[x] ^= 1;
+                        fence_after();
+                        outputs(x, vs, was_fresh);
+                        if (ends) signal(&B.o_full[x]);
+                        if (have) ok = score_tile(x, ks, fresh, t + 1 == t1);
+                    }
+                    signal(&B.kv_empty[vs]);
+                    if (have) signal(&B.kv_empty[ks]);
+                    if (ends) done_with_item(B, i++);
+                }
+            } else
             for (int i = 0; ok && next_item(B, i, A, I); ++i) {
                 // scores of row tile x for tile t of keys, in the ring at ks; the block's Q is free after its last
                 auto score_tile = [&](int x, int t, int ks) {
@@ -992,12 +1050,13 @@ int run_mma(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long lon
         A.down = 0;
         A.across = 1;
     }
+    auto kernel = A.across ? prompt_mma_kernel<HD, true> : prompt_mma_kernel<HD, false>;
     int sms = 0;
-    static mfs::PerDevice ready;
-    cudaError_t e = mfs::op_device(ready, (const void*)prompt_mma_kernel<HD>, S::BYTES, &sms);
+    static mfs::PerDevice ready[2];
+    cudaError_t e = mfs::op_device(ready[A.across], (const void*)kernel, S::BYTES, &sms);
     if (e == cudaSuccess) {
         const long long most = ((long long)n_tokens / (PT_M + A.down) + n_seqs) * (hq >> A.across);  // blocks there can be
-        prompt_mma_kernel<HD><<<(unsigned)(most < sms ? most : sms), PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);
+        kernel<<<(unsigned)(most < sms ? most : sms), PT_THREADS, S::BYTES, st>>>(maps[0], maps[1], maps[2], A);
         e = cudaGetLastError();
     }
     return mfs::op_launched(op, e);
