@@ -776,23 +776,38 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 unpair(add2(l2[0], l2[1]), l0, l1);
                 const float inv = ok ? 1.f / (l0 + l1) : NAN;
                 const PtWork w = B.work[i & 3];
-                bf16* o = A.out + (long long)(w.b + rr) * A.out_stride + (w.h + x * A.across) * HD;
+                // 64 elements of a row at a time: the eight lanes of eight rows exchange 16-byte units so that a store
+                // writes 128 bytes of each of four rows (a lane per row would touch 32 lines with each)
+                const int j = lane & 7;
+                bf16* o = A.out + (long long)(w.b + rr - j) * A.out_stride + (w.h + x * A.across) * HD + 8 * j;
 #pragma unroll
-                for (int k = 0; k < HD; k += 32) {
-                    uint32_t r[32];
-                    tld32(to + k, r);
-                    tld_wait();
-                    if (rr < w.len) {
+                for (int k = 0; k < HD; k += 64) {
+                    uint32_t u[8][4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 y;
-                            y.x = pack_bf16(__uint_as_float(r[e]) * inv, __uint_as_float(r[e + 1]) * inv);
-                            y.y = pack_bf16(__uint_as_float(r[e + 2]) * inv, __uint_as_float(r[e + 3]) * inv);
-                            y.z = pack_bf16(__uint_as_float(r[e + 4]) * inv, __uint_as_float(r[e + 5]) * inv);
-                            y.w = pack_bf16(__uint_as_float(r[e + 6]) * inv, __uint_as_float(r[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(o + k + e) = y;
-                        }
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t r[32];
+                        tld32(to + k + 32 * half, r);
+                        tld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[4 * half + e / 4][e % 4] = pack_bf16(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
                     }
+#pragma unroll
+                    for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            if (!(y & d)) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, j & d ? u[y][e] : u[y | d][e], d);
+                                    if (j & d) u[y][e] = got;
+                                    else u[y | d][e] = got;
+                                }
+                            }
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        if (rr - j + y < w.len)
+                            *reinterpret_cast<uint4*>(o + y * A.out_stride + k) = make_uint4(u[y][0], u[y][1], u[y][2], u[y][3]);
                 }
                 fence_before();
                 if (*(volatile int*)&B.cleared[i & 3] && ok) {
