@@ -201,7 +201,7 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 
 // --------------------------------------------------------------- attention
 //
-// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 16 positions
+// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 8 KB of keys and values (16 positions of 128 bf16)
 // and all tiles of the call, laid end to end, into equal shares, one per warp of a grid that fills
 // the GPU once: a warp walks through its share whatever sequences it crosses, so ragged lengths and
 // few long sequences load every SM alike.  An item (sequence, head block) that lies in one share is
@@ -214,21 +214,13 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 // filled with zeros and never read), with the page of the next stage's rows looked up a stage ahead.
 
 constexpr int PA_WARPS = 4;
-constexpr int PA_ROWS = 16;                      // positions per tile
 constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
+constexpr int PA_STAGES = 2;                     // 16 KB per warp, 128 KB per SM: 3 stages measured 5 % slower on long contexts
 
+// Query heads per block, by group size: the 16 rows of an mma tile for bf16; for fp32, where every head costs
+// products, as many as there are, in three widths.
 template <typename T>
-struct PaType;
-template <>
-struct PaType<bf16> {
-    static constexpr int GM = 16;  // query heads per block: the rows of an mma tile
-    static constexpr int STAGES = 2;
-};
-template <>
-struct PaType<float> {
-    static constexpr int GM = 8;
-    static constexpr int STAGES = 2;
-};
+constexpr int PA_GM_MAX = sizeof(T) == 2 ? 16 : 8;
 
 __device__ __forceinline__ unsigned su32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
 
@@ -261,6 +253,9 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
     return *reinterpret_cast<const unsigned*>(&v);
 }
 
+template <typename T, int HD>
+constexpr int PA_ROWS = 4096 / (HD * (int)sizeof(T));  // positions per tile: 4 KB of keys, 4 KB of values
+
 struct PaArgs {
     Cache C;
     const int32_t* kv_len;
@@ -280,13 +275,15 @@ struct PaWalk {
     int s, hb, tile, ntiles, lo, len;
 };
 
+template <int ROWS>
 __device__ __forceinline__ void pa_sequence(const PaArgs& A, PaWalk& w)
 {
     w.len = __ldg(A.kv_len + w.s);
     w.lo = A.window > 0 && w.len > A.window ? w.len - A.window : 0;
-    w.ntiles = w.len > w.lo ? (w.len - w.lo + PA_ROWS - 1) / PA_ROWS : 0;
+    w.ntiles = w.len > w.lo ? (int)(((long long)w.len - w.lo + ROWS - 1) / ROWS) : 0;
 }
 
+template <int ROWS>
 __device__ __forceinline__ void pa_next(const PaArgs& A, PaWalk& w)
 {
     if (++w.tile < w.ntiles) return;
@@ -296,14 +293,15 @@ __device__ __forceinline__ void pa_next(const PaArgs& A, PaWalk& w)
     do {
         ++w.s;
         if (w.s >= A.n_seqs) return;
-        pa_sequence(A, w);
+        pa_sequence<ROWS>(A, w);
     } while (w.ntiles == 0);
 }
 
-// Element offset of this lane's row (lane % 16) of the tile, or -1.
+// Element offset of this lane's row (lane mod ROWS) of the tile, or -1.
+template <int ROWS>
 __device__ __forceinline__ long long pa_offset(const PaArgs& A, const PaWalk& w, bool& bad)
 {
-    const int p = w.lo + w.tile * PA_ROWS + (threadIdx.x & 15);
+    const int p = w.lo + w.tile * ROWS + (threadIdx.x & (ROWS - 1));
     if (p >= w.len) return -1;
     const long long off = row_offset(A.C, w.s, p);
     if (off < 0) { bad = true; return -1; }
@@ -315,22 +313,23 @@ __device__ __forceinline__ void pa_issue(const PaArgs& A, unsigned stage, long l
 {
     constexpr int CH = HD * sizeof(T) / 16;      // 16-byte chunks per row
     constexpr int RPI = CH >= 32 ? 1 : 32 / CH;  // rows per instruction
+    constexpr int ROWS = PA_ROWS<T, HD>;
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int j = 0; j < PA_ROWS / RPI; ++j) {
+    for (int j = 0; j < ROWS / RPI; ++j) {
         const int row = j * RPI + lane / CH, ch = lane % CH;
         const long long o = __shfl_sync(0xffffffffu, off, row);
         const long long byte = (o < 0 ? 0 : o) * (long long)sizeof(T) + ch * 16;
         const unsigned dst = stage + row * (HD * (int)sizeof(T)) + ((ch ^ (row & 7)) << 4);
         copy16(dst, A.C.k + byte, o >= 0);
-        copy16(dst + PA_ROWS * HD * (int)sizeof(T), A.C.v + byte, o >= 0);
+        copy16(dst + ROWS * HD * (int)sizeof(T), A.C.v + byte, o >= 0);
     }
 }
 
 // One warp's state for an item: scores by mma for bf16 (16 query heads per tile, the rest zero).
 template <int HD>
 struct PaBf16 {
-    static constexpr int GM = PaType<bf16>::GM;
+    static constexpr int GM = 16, ROWS = PA_ROWS<bf16, HD>, NK = ROWS / 8;  // key octets
     unsigned qf[HD / 16][4];
     float o[HD / 8][4], m[2], l[2];
 
@@ -354,24 +353,24 @@ struct PaBf16 {
         l[0] = l[1] = 0.f;
     }
 
-    __device__ __forceinline__ void tile(unsigned stage, int valid, float c, float*, const float*, int)
+    __device__ __forceinline__ void tile(unsigned stage, int valid, float c, float*, const float*)
     {
         const int lane = threadIdx.x & 31, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
-        float s[2][4] = {};
-        {
-            const int key = r8 + (mi >> 1) * 8;
-            const unsigned base = stage + key * HD * 2;
+        float s[NK][4] = {};
+#pragma unroll
+        for (int n = 0; n < NK; n += 2) {
+            const unsigned base = stage + (8 * n + r8 + (mi >> 1) * 8) * HD * 2;
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
                 unsigned b[4];
                 ldm4(base + (((2 * k + (mi & 1)) ^ r8) << 4), b);
-                mma_bf16(s[0], qf[k], b[0], b[1]);
-                mma_bf16(s[1], qf[k], b[2], b[3]);
+                mma_bf16(s[n], qf[k], b[0], b[1]);
+                mma_bf16(s[n + 1], qf[k], b[2], b[3]);
             }
         }
-        if (valid < PA_ROWS) {
+        if (valid < ROWS) {
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NK; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     if (8 * n + 2 * t + (x & 1) >= valid) s[n][x] = -INFINITY;
@@ -379,7 +378,9 @@ struct PaBf16 {
         float mn[2], scale[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float v = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            float v = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+            for (int n = 1; n < NK; ++n) v = fmaxf(v, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
             mn[h] = fmaxf(m[h], v);
@@ -391,26 +392,28 @@ struct PaBf16 {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) o[j][x] *= scale[x >> 1];
         }
-        unsigned p[4];
+        unsigned p[NK / 2][4];  // the weights, rounded to bf16 for the product with the values; the sums take them unrounded
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             m[h] = mn[h];
-            float e[4];
+            float sum = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) e[x] = exp2f((s[x >> 1][2 * h + (x & 1)] - mn[h]) * c);
-            l[h] = l[h] * scale[h] + (e[0] + e[1]) + (e[2] + e[3]);
-            p[h] = pack_bf16(e[0], e[1]);
-            p[2 + h] = pack_bf16(e[2], e[3]);
+            for (int n = 0; n < NK; ++n) {
+                const float a = exp2f((s[n][2 * h] - mn[h]) * c), b = exp2f((s[n][2 * h + 1] - mn[h]) * c);
+                sum += a + b;
+                p[n / 2][2 * (n & 1) + h] = pack_bf16(a, b);
+            }
+            l[h] = l[h] * scale[h] + sum;
         }
-        {
-            const int key = r8 + (mi & 1) * 8;
-            const unsigned base = stage + (PA_ROWS + key) * HD * 2;
+#pragma unroll
+        for (int n = 0; n < NK / 2; ++n) {
+            const unsigned base = stage + (ROWS + 16 * n + r8 + (mi & 1) * 8) * HD * 2;
 #pragma unroll
             for (int j = 0; j < HD / 8; j += 2) {
                 unsigned b[4];
                 ldm4t(base + (((j + (mi >> 1)) ^ r8) << 4), b);
-                mma_bf16(o[j], p, b[0], b[1]);
-                mma_bf16(o[j + 1], p, b[2], b[3]);
+                mma_bf16(o[j], p[n], b[0], b[1]);
+                mma_bf16(o[j + 1], p[n], b[2], b[3]);
             }
         }
     }
@@ -439,10 +442,10 @@ struct PaBf16 {
     static constexpr int OWN = 2;  // rows a lane holds statistics of
 };
 
-// fp32: a lane scores one position over half of the elements, then owns HD / 32 elements of the output.
-template <int HD>
+// fp32: a lane scores one position over 1 / PARTS of the elements, then owns HD / 32 elements of the output.
+template <int HD, int GM>
 struct PaF32 {
-    static constexpr int GM = PaType<float>::GM, E = HD / 32, OWN = GM;
+    static constexpr int E = HD / 32, OWN = GM, ROWS = PA_ROWS<float, HD>, PARTS = 32 / ROWS;
     float o[GM][E], m[GM], l[GM];
 
     __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float* sq)
@@ -462,41 +465,40 @@ struct PaF32 {
         }
     }
 
-    __device__ __forceinline__ void tile(unsigned, int valid, float c, float* stage, const float* sq, int nh)
+    __device__ __forceinline__ void tile(unsigned, int valid, float c, float* stage, const float* sq)
     {
-        const int lane = threadIdx.x & 31, key = lane & 15, part = lane >> 4;
+        const int lane = threadIdx.x & 31, key = lane & (ROWS - 1), part = lane / ROWS;
         float s[GM];
 #pragma unroll
         for (int h = 0; h < GM; ++h) s[h] = 0.f;
         const float4* kr = reinterpret_cast<const float4*>(stage + key * HD);
-        for (int i = 0; i < HD / 8; ++i) {
-            const int ch = part * (HD / 8) + i;
+#pragma unroll 4
+        for (int i = 0; i < HD / 4 / PARTS; ++i) {
+            const int ch = part * (HD / 4 / PARTS) + i;
             const float4 k = kr[ch ^ (key & 7)];
 #pragma unroll
-            for (int h = 0; h < GM; ++h)
-                if (h < nh) {
-                    const float4 x = reinterpret_cast<const float4*>(sq + h * HD)[ch];
-                    s[h] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, s[h]))));
-                }
+            for (int h = 0; h < GM; ++h) {
+                const float4 x = reinterpret_cast<const float4*>(sq + h * HD)[ch];
+                s[h] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, s[h]))));
+            }
         }
         float p[GM];
 #pragma unroll
-        for (int h = 0; h < GM; ++h)
-            if (h < nh) {
-                s[h] += __shfl_xor_sync(0xffffffffu, s[h], 16);
-                if (key >= valid) s[h] = -INFINITY;
-                float v = s[h];
-                for (int x = 8; x; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                const float mn = fmaxf(m[h], v), sc = m[h] == mn ? 1.f : exp2f((m[h] - mn) * c);
-                m[h] = mn;
-                p[h] = exp2f((s[h] - mn) * c);
-                l[h] = l[h] * sc + (part == 0 ? p[h] : 0.f);
+        for (int h = 0; h < GM; ++h) {
+            for (int x = ROWS; x < 32; x *= 2) s[h] += __shfl_xor_sync(0xffffffffu, s[h], x);
+            if (key >= valid) s[h] = -INFINITY;
+            float v = s[h];
+            for (int x = ROWS / 2; x; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+            const float mn = fmaxf(m[h], v), sc = m[h] == mn ? 1.f : exp2f((m[h] - mn) * c);
+            m[h] = mn;
+            p[h] = exp2f((s[h] - mn) * c);
+            l[h] = l[h] * sc + (part == 0 ? p[h] : 0.f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[h][e] *= sc;
-            }
+            for (int e = 0; e < E; ++e) o[h][e] *= sc;
+        }
         for (int j = 0; j < valid; ++j) {
             float v[E];
-            const float* vr = stage + (PA_ROWS + j) * HD;
+            const float* vr = stage + (ROWS + j) * HD;
             if (E == 4) {
                 const float4 x = reinterpret_cast<const float4*>(vr)[lane ^ (j & 7)];
                 v[0] = x.x; v[1] = x.y; v[2 % E] = x.z; v[3 % E] = x.w;
@@ -505,12 +507,11 @@ struct PaF32 {
                 v[0] = x.x; v[1] = x.y;
             }
 #pragma unroll
-            for (int h = 0; h < GM; ++h)
-                if (h < nh) {
-                    const float pj = __shfl_sync(0xffffffffu, p[h], j);
+            for (int h = 0; h < GM; ++h) {
+                const float pj = __shfl_sync(0xffffffffu, p[h], j);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[h][e] = fmaf(pj, v[e], o[h][e]);
-                }
+                for (int e = 0; e < E; ++e) o[h][e] = fmaf(pj, v[e], o[h][e]);
+            }
         }
     }
 
@@ -541,14 +542,13 @@ __device__ __forceinline__ long long muldiv(long long x, long long y, long long 
     return x * y / z;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int GM>
 struct PaLayout {
-    static constexpr int GM = PaType<T>::GM;
-    static constexpr int STAGE = PA_ROWS * HD * (int)sizeof(T) * 2;  // keys and values of a tile
-    static constexpr int RING = PA_WARPS * PaType<T>::STAGES * STAGE;
+    static constexpr int STAGE = PA_ROWS<T, HD> * HD * (int)sizeof(T) * 2;  // keys and values of a tile
+    static constexpr int RING = PA_WARPS * PA_STAGES * STAGE;
     static constexpr int Q = sizeof(T) == 4 ? PA_WARPS * GM * HD * 4 : 0;
     static constexpr int BYTES = RING + Q;
-    static_assert(GM * HD * 4 <= PaType<T>::STAGES * STAGE, "a warp's piece takes its ring's place");
+    static_assert(GM * HD * 4 <= PA_STAGES * STAGE, "a warp's piece takes its ring's place");
 };
 
 // A piece of an item that a warp could not finish: whether the item's first and last tile were in it, and the
@@ -557,12 +557,12 @@ struct PaPiece {
     int s, hb, first, last, last_cta;
 };
 
-template <typename T, int HD>
+template <typename T, int HD, int GM>
 __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const __grid_constant__ PaArgs A)
 {
-    using L = PaLayout<T, HD>;
-    using State = typename std::conditional<sizeof(T) == 2, PaBf16<HD>, PaF32<HD>>::type;
-    constexpr int GM = L::GM, S = PaType<T>::STAGES;
+    using L = PaLayout<T, HD, GM>;
+    using State = typename std::conditional<sizeof(T) == 2, PaBf16<HD>, PaF32<HD, GM>>::type;
+    constexpr int S = PA_STAGES, ROWS = PA_ROWS<T, HD>;
     extern __shared__ __align__(128) char pa_raw[];
     __shared__ long long sh_sum[PA_WARPS];
     __shared__ PaPiece sh_piece[2 * PA_WARPS];
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     auto tiles_of = [&](int s) {
         PaWalk w;
         w.s = s;
-        pa_sequence(A, w);
+        pa_sequence<ROWS>(A, w);
         return w.ntiles;
     };
     long long mine = 0;
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             }
             item_first += __shfl_sync(0xffffffffu, inc, 31);
         }
-        pa_sequence(A, use);
+        pa_sequence<ROWS>(A, use);
         use.hb = (int)((unsigned long long)(t0 - item_first) >> 32 ? (t0 - item_first) / use.ntiles : (unsigned)(t0 - item_first) / (unsigned)use.ntiles);
         item_first += (long long)use.hb * use.ntiles;
         use.tile = (int)(t0 - item_first);
@@ -638,15 +638,15 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         int n_load = n;         // tiles not yet asked for: the loads run ahead of the products, across items
         unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
         bool next_bad = false;
-        long long off = pa_offset(A, load, next_bad);
+        long long off = pa_offset<ROWS>(A, load, next_bad);
         auto issue = [&](int stage) {
             if (n_load > 0) {
                 pa_issue<T, HD>(A, ring + stage * L::STAGE, off);
                 bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
                 next_bad = false;
                 if (--n_load > 0) {
-                    pa_next(A, load);
-                    off = pa_offset(A, load, next_bad);
+                    pa_next<ROWS>(A, load);
+                    off = pa_offset<ROWS>(A, load, next_bad);
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -667,8 +667,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();
             const int nh = min(GM, A.g - (use.hb % A.nhb) * GM);
-            st.tile(ring + stage * L::STAGE, min(PA_ROWS, use.len - (use.lo + use.tile * PA_ROWS)), A.c,
-                    reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq, nh);
+            st.tile(ring + stage * L::STAGE, min(ROWS, use.len - (use.lo + use.tile * ROWS)), A.c,
+                    reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq);
             bad = bad || ((bad_ring >> stage) & 1u);
             __syncwarp();
             issue(stage);
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             }
             if (it + 1 < n) {
                 if (ends) item_first += use.ntiles;
-                pa_next(A, use);
+                pa_next<ROWS>(A, use);
             }
         }
     }
@@ -771,10 +771,9 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
 // threads that take eight pieces at a time, all on their way together.
 constexpr int PJ_GROUPS = 4;
 
-template <typename T, int HD>
+template <typename T, int HD, int GM>
 __global__ void __launch_bounds__(HD * PJ_GROUPS) paged_attention_join(const __grid_constant__ PaArgs A)
 {
-    constexpr int GM = PaType<T>::GM;
     __shared__ float s_acc[PJ_GROUPS][HD], s_mx[PJ_GROUPS], s_l[PJ_GROUPS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cta = blockIdx.x, row = blockIdx.y, e = threadIdx.x % HD, group = threadIdx.x / HD;
@@ -831,26 +830,26 @@ __global__ void __launch_bounds__(HD * PJ_GROUPS) paged_attention_join(const __g
 
 size_t attention_workspace(int dtype, int hd)
 {
-    const size_t gm = dtype == MFS_DTYPE_BF16 ? PaType<bf16>::GM : PaType<float>::GM;
+    const size_t gm = dtype == MFS_DTYPE_BF16 ? PA_GM_MAX<bf16> : PA_GM_MAX<float>;
     return (size_t)PA_MAX_CTAS * ((2 + PA_WARPS) * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int GM>
 int attention(PaArgs A, char* workspace, cudaStream_t st)
 {
-    using L = PaLayout<T, HD>;
-    A.nhb = (A.g + L::GM - 1) / L::GM;
+    using L = PaLayout<T, HD, GM>;
+    A.nhb = (A.g + GM - 1) / GM;
     A.part_o = reinterpret_cast<float*>(workspace);
-    A.front_o = A.part_o + (size_t)PA_MAX_CTAS * 2 * L::GM * HD;
-    A.part_ml = reinterpret_cast<float2*>(A.front_o + (size_t)PA_MAX_CTAS * PA_WARPS * L::GM * HD);
-    A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * L::GM);
-    const int rows = A.g < L::GM ? A.g : L::GM;
+    A.front_o = A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD;
+    A.part_ml = reinterpret_cast<float2*>(A.front_o + (size_t)PA_MAX_CTAS * PA_WARPS * GM * HD);
+    A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * GM);
+    const int rows = A.g < GM ? A.g : GM;
     int sms = 0;
     static mfs::PerDevice ready;
-    cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<T, HD>, L::BYTES, &sms);
+    cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<T, HD, GM>, L::BYTES, &sms);
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     const int G = 2 * sms < PA_MAX_CTAS ? 2 * sms : PA_MAX_CTAS;
-    paged_attention_kernel<T, HD><<<G, PA_WARPS * 32, L::BYTES, st>>>(A);
+    paged_attention_kernel<T, HD, GM><<<G, PA_WARPS * 32, L::BYTES, st>>>(A);
     e = cudaGetLastError();
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     cudaLaunchConfig_t cfg = {};
@@ -862,7 +861,7 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return mfs::op_launched("paged_attention", cudaLaunchKernelEx(&cfg, paged_attention_join<T, HD>, A));
+    return mfs::op_launched("paged_attention", cudaLaunchKernelEx(&cfg, paged_attention_join<T, HD, GM>, A));
 }
 
 }  // namespace
@@ -937,6 +936,8 @@ extern "C" int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const 
     A.c = scale * 1.44269504088896340736f;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
-    if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? attention<bf16, 128>(A, ws, st) : attention<bf16, 64>(A, ws, st);
-    return hd == 128 ? attention<float, 128>(A, ws, st) : attention<float, 64>(A, ws, st);
+    if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? attention<bf16, 128, 16>(A, ws, st) : attention<bf16, 64, 16>(A, ws, st);
+    auto fn = hd == 128 ? (A.g == 1 ? attention<float, 128, 1> : A.g <= 4 ? attention<float, 128, 4> : attention<float, 128, 8>)
+                        : (A.g == 1 ? attention<float, 64, 1> : A.g <= 4 ? attention<float, 64, 4> : attention<float, 64, 8>);
+    return fn(A, ws, st);
 }
