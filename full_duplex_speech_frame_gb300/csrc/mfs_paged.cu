@@ -59,7 +59,9 @@ __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x);
 // heads of 128 bf16: 39 us, 0.83 of the measured copy rate; blocks of 256 threads and 4 tokens 40 us, three items on
 // their way per thread (fewer blocks on an SM) 45 us, 8 tokens 45 us.
 constexpr int AP_THREADS = 128;
-constexpr int AP_TOKENS = 2;   // tokens per block; 1 where that leaves SMs without a block
+// Tokens per block; 1 up to 8 blocks per SM (4 tokens of 16 heads: 3.9 us, 5.5 us by twos; 1200 of 32 + 8 heads 8.7 and
+// 9.3; 1800 14.2 and 13.1; 8192 40.3 and 38.5).
+constexpr int AP_TOKENS = 2;
 
 template <typename T>
 struct ApArgs {
@@ -182,7 +184,7 @@ int append(const ApArgs<T>& A, cudaStream_t st)
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, nullptr, 0, &sms);
     if (e == cudaSuccess) {
-        if (A.n_tokens < 2 * AP_TOKENS * sms) append_kernel<T, HD, 1><<<A.n_tokens, AP_THREADS, 0, st>>>(A);
+        if (A.n_tokens <= 8 * sms) append_kernel<T, HD, 1><<<A.n_tokens, AP_THREADS, 0, st>>>(A);
         else append_kernel<T, HD, AP_TOKENS><<<(A.n_tokens + AP_TOKENS - 1) / AP_TOKENS, AP_THREADS, 0, st>>>(A);
         e = cudaGetLastError();
     }
@@ -201,24 +203,32 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 
 // --------------------------------------------------------------- attention
 //
-// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 8 KB of keys and values (16 positions of 128 bf16)
-// and all tiles of the call, laid end to end, into equal shares, one per warp of a grid that fills
-// the GPU once: a warp walks through its share whatever sequences it crosses, so ragged lengths and
-// few long sequences load every SM alike.  An item (sequence, head block) that lies in one share is
-// finished by its warp.  The pieces of the others meet in shared memory once, when the CTA's warps are
-// done; what still crosses CTAs goes to the workspace (at most two pieces per CTA) and a second
-// kernel, whose launch overlaps the first one's run, joins it in share order.
+// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 8 KB of keys and
+// values (16 positions of 128 bf16), and all tiles of the call, laid end to end, into equal shares, one
+// per warp of a grid that fills the GPU once: a warp walks through its share whatever sequences it
+// crosses, so ragged lengths and few long sequences load every SM alike.  An item (sequence, head block)
+// that lies in one share is finished by its warp.  The pieces of the others meet in shared memory once,
+// when the CTA's warps are done; what still crosses CTAs goes to the workspace (at most two pieces per
+// CTA) and a second kernel, whose launch overlaps the first one's run, joins it in share order.
 //
 // A warp keeps its own running maximum, sum and output, so no warp waits for another before the end;
 // it feeds itself through a ring of stages with 16-byte asynchronous copies (rows past the length are
 // filled with zeros and never read), with the page of the next stage's rows looked up a stage ahead.
+//
+// What bounds it is memory: each key and value is read once.  bf16, 8 kv heads of 128: 4 sequences of up
+// to 131072, 64 query heads, 209 us = 6.4 TB/s, 0.95 of the measured copy rate; 32 of up to 8192, 32
+// query heads, pages of 16, 98 us = 5.65 TB/s; the rest is the start, the join and two launches, which
+// is most of one sequence of 3000 positions and 32 kv heads: 18 us, 7.3 us of it memory.  The matrix
+// instructions (a tile's 16 rows are the group's query heads, zero rows for those it lacks) keep the
+// tensor pipe 17 % busy there, so the wide forms of them would gain nothing.
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
 constexpr int PA_STAGES = 2;                     // 16 KB per warp, 128 KB per SM: 3 stages measured 5 % slower on long contexts
 
-// Query heads per block, by group size: the 16 rows of an mma tile for bf16; for fp32, where every head costs
-// products, as many as there are, in three widths.
+// Query heads per block: the 16 rows of an mma tile for bf16.  fp32, on the CUDA cores, pays for every head of the
+// block, so it has three widths, 1, 4 and 8: 8 sequences of 8192, 8 kv heads of 128, groups of 1, 2, 4 and 8 take 88,
+// 111, 114 and 167 us, with 8 alone 158, 159, 162 and 166 us (537 MB: 79 us at the measured copy rate).
 template <typename T>
 constexpr int PA_GM_MAX = sizeof(T) == 2 ? 16 : 8;
 

@@ -7,29 +7,36 @@
 // be candidates they are listed: those above the k-th largest of the threads' own
 // maxima (at least k columns reach it, and rarely many more), or above min-p's
 // bound, in column order.  One CTA then finds each one's rank by comparing all with
-// all, cuts the list and finds the token.  Otherwise a histogram, linear in the distance to the
-// maximum in octaves of the weight, finds the bin that holds a filter's border, only
-// that bin's columns are listed, and the token is found by sums in column order, per
-// CTA, per thread, and within that thread's columns.  Where a filter leaves few
-// columns, each thread notes the places of its own first, so that a warp's lanes
-// weigh columns together and not one by one.
+// all, cuts the list and finds the token.  Otherwise a histogram, linear in the
+// distance to the maximum in octaves of the weight, finds the bin that holds a
+// filter's border, only that bin's columns are listed, and the token is found by
+// sums in column order, per CTA, per thread, and within that thread's columns.
+// Where a filter leaves few columns, each thread notes the places of its own first,
+// so that a warp's lanes weigh columns together and not one by one.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, as many as it takes to keep its
 // part of the row in shared memory beside another CTA's, and to use the SMs when
 // there are few rows; the CTAs exchange maxima, histograms, lists and sums through
 // distributed shared memory.  The logits are read from memory once; what bounds
-// the call is the passes over shared memory and the latency of the exchanges.
+// the call is the passes over shared memory, the weighing (about 80 instructions a
+// column with the loop around it) and the latency of the exchanges; with many long
+// rows also the second wave, as a row takes most of an SM's shared memory.  Top-k of
+// 16 rows of 2048 fp32: 8 us, of 32 rows of 32000: 10 us; top-p with min-p of 256 rows
+// of 32000: 46 us; 128 rows of 131072 bf16: top-k 30 us, no filter 83 us, top-p alone,
+// which weighs all columns, 133 us.  Rows left in memory instead, read again from L2
+// by every pass, need no second wave but took 108 us and 215 us for the last two.
 //
 // Weights are unsigned fixed point (2^scale for the maximum's), so sums are exact
 // whatever order the atomics take, and the row's token is the same on every run.
 // A weight is 2^-y = 2^-n 2^-(i/64) 2^-r with y a pair of fp32, a table for i and
 // three terms for |r| < 1/128: off by less than 2^-28 of itself (2^-30.2 from the
-// terms' own rounding, 2^-31 each from the table's and the result's, 2^-31.5 each from
-// r's, the table's in fp32 and the product's, 2^-34.7 from the terms left out).  Each comparison of sums is made
-// with a bound on that error, and a row in which one falls inside the bound is done
-// again with exponentials of about 2^-40 relative error (pairs of fp32), which
-// decides it.  64-bit floating point, two products a cycle and SM here, is kept to
-// one thread per CTA; fractions of sums are taken in 128-bit integers.
+// terms' own rounding, 2^-31 each from the table's and the result's, 2^-31.5 each
+// from r's, the table's in fp32 and the product's, 2^-34.7 from the terms left out).
+// Each comparison of sums is made with a bound on that error, and a row in which one
+// falls inside the bound is done again with exponentials of about 2^-40 relative
+// error (pairs of fp32), which decides it.  64-bit floating point, two products a
+// cycle and SM here, is kept to one thread per CTA; fractions of sums are taken in
+// 128-bit integers.
 #include <cooperative_groups.h>
 
 #include "mfs_ops.cuh"
@@ -59,11 +66,11 @@ struct __align__(16) SrShared {
     unsigned count[SR_NB], lo[SR_NB], hi[SR_NB];  // this CTA's histogram: columns, sums of weights in two words
     u64 sum[SR_NB];                               // the row's sums of weights
     unsigned num[SR_NB];                          // and columns
-    u64 list[NT];                            // listed columns, ascending: key << 32 | ~column
-    u64 ranked[NT];                          // their weights or keys by rank
-    unsigned keys[NT];                       // the list's keys
+    u64 list[NT];                                 // listed columns, ascending: key << 32 | ~column
+    u64 ranked[NT];                               // their weights or keys by rank
+    unsigned keys[NT];                            // the list's keys
     unsigned short rank[NT];
-    unsigned short idx[NT][SR_SLOTS];          // noted columns, ascending, as places in the part
+    unsigned short idx[NT][SR_SLOTS];             // noted columns, ascending, as places in the part
     uint2 table[64];                              // 2^(31 - i / 64), as an integer and as fp32
     u64 ws[(NT / 32)];
     float wf[(NT / 32)];
@@ -1094,9 +1101,13 @@ int launch(int C, const void* logits, int rows, int cols, long long ld, const fl
                                                               uniforms, tokens, C, (int)stage));
 }
 
-// CTAs of 512 threads, two on an SM: as many per row as keep its parts within 64 KB, and more where rows leave SMs empty
-// and a part keeps at least 4096 columns.  Where that makes clusters of rows that would fill the SMs with fewer CTAs of
-// 1024 threads, one on an SM, those are taken: an exchange between the CTAs of a row costs over 1 us.
+// CTAs of 512 threads, two on an SM: as many per row as keep its parts within 64 KB, and more where rows leave SMs
+// empty.  An exchange between the CTAs of a row costs over 1 us, so a row is cut in two for that from 16384 columns on
+// (16 rows of 8192: 7.8 us whole, 9.6 us in two, with top-p 17.7 and 20.3 us; of 16384: 8.5 and 9.9, 19.8 and 20.6,
+// without a filter 12.0 and 9.6), further while a part keeps 8192 (16 rows of 20000 bf16, top-p: 21.6 us in two, 20.4 us
+// in four).  Where many rows would each need a cluster but fit one CTA of 1024 threads, alone on an SM, they get it:
+// 128 rows of 32000 fp32, top-k 10.7 us (12.9 us as pairs), top-p 25.7 (29.1), 256 rows 20.5 (23.8) and 46.5 (52.5); 16
+// rows, that leave SMs empty, 12.6 us without a filter (10.0 us as clusters of four).
 template <typename T>
 int choose(const void* logits, int rows, int cols, long long ld, const float* temperature, const int32_t* top_k,
            const float* top_p, const float* min_p, const float* uniforms, int32_t* tokens, cudaStream_t st)
@@ -1106,11 +1117,10 @@ int choose(const void* logits, int rows, int cols, long long ld, const float* te
     const cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
     if (e != cudaSuccess) return mfs::op_launched("sample_rows", e);
     const long long bytes = (long long)cols * sizeof(T);
-    int C = 1, wide = 1;
-    while (C < SR_MAX_C && (bytes / C > 64 * 1024 || ((long long)rows * C * 2 <= sms && cols / C >= 8192))) C *= 2;
-    while (wide < C && bytes / wide > SR_WIDE_BYTES) wide *= 2;
-    if (wide < C && (long long)rows * wide >= sms)
-        return launch<T, 1024>(wide, logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
+    int C = 1;
+    while (C < SR_MAX_C && (bytes / C > 64 * 1024 || ((long long)rows * C * 2 <= sms && cols / C >= (C == 1 ? 16384 : 8192)))) C *= 2;
+    if (C > 1 && bytes <= SR_WIDE_BYTES && 2LL * rows > sms)
+        return launch<T, 1024>(1, logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
     return launch<T, 512>(C, logits, rows, cols, ld, temperature, top_k, top_p, min_p, uniforms, tokens, st);
 }
 
