@@ -59,6 +59,7 @@ inline const char* paged_kv_problem(const mfs_paged_kv* c)
     if (c->head_dim != 64 && c->head_dim != 128) return "head_dim must be 64 or 128";
     if (c->n_pages < 1 || c->n_kv_heads < 1 || c->table_width < 1 || c->table_stride < 0)
         return "need n_pages, n_kv_heads and table_width >= 1, table_stride >= 0";
+    if (c->n_kv_heads > MFS_MAX_HEADS) return "more than 65535 kv heads";
     if (c->page_size < 1 || c->page_size > MFS_MAX_PAGE_SIZE) return "page_size outside [1, 65536]";
     const int elem = c->dtype == MFS_DTYPE_BF16 ? 2 : 4;
     if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < 0) return "negative cache stride";

@@ -312,7 +312,7 @@ template <int ROWS>
 __device__ __forceinline__ long long pa_offset(const PaArgs& A, const PaWalk& w, bool& bad)
 {
     const int p = w.lo + w.tile * ROWS + (threadIdx.x & (ROWS - 1));
-    if (p >= w.len) return -1;
+    if ((unsigned)p >= (unsigned)w.len) return -1;  // a last tile may reach past 2^31 - 1
     const long long off = row_offset(A.C, w.s, p);
     if (off < 0) { bad = true; return -1; }
     return off + (long long)(w.hb / A.nhb) * A.C.head_stride;
@@ -891,7 +891,7 @@ extern "C" int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs
     const int hd = cache->head_dim, elem = cache->dtype == MFS_DTYPE_BF16 ? 2 : 4;
     if (!cu || !kv_len || !k || !v) return mfs::op_fail(MFS_E_ARG, op, "null cu, kv_len, k or v");
     if ((q != nullptr) != (q_out != nullptr)) return mfs::op_fail(MFS_E_ARG, op, "q and q_out go together");
-    if (q && n_q_heads < 1) return mfs::op_fail(MFS_E_ARG, op, "need n_q_heads >= 1");
+    if (q && (n_q_heads < 1 || n_q_heads > MFS_MAX_HEADS)) return mfs::op_fail(MFS_E_ARG, op, "n_q_heads outside [1, 65535]");
     if (!mfs::rows_ok(k, k_stride, cache->n_kv_heads, hd, elem) || !mfs::rows_ok(v, v_stride, cache->n_kv_heads, hd, elem) ||
         (k_out && !mfs::rows_ok(k_out, k_out_stride, cache->n_kv_heads, hd, elem)) ||
         (q && (!mfs::rows_ok(q, q_stride, n_q_heads, hd, elem) || !mfs::rows_ok(q_out, q_out_stride, n_q_heads, hd, elem))))
@@ -923,7 +923,8 @@ extern "C" int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const 
     const char* op = "paged_attention";
     if (const char* why = mfs::paged_kv_problem(cache)) return mfs::op_fail(MFS_E_ARG, op, why);
     if (n_seqs < 0 || window < 0) return mfs::op_fail(MFS_E_ARG, op, "need n_seqs >= 0 and window >= 0");
-    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads) return mfs::op_fail(MFS_E_ARG, op, "n_q_heads must be a multiple of n_kv_heads");
+    if (n_q_heads < 1 || n_q_heads % cache->n_kv_heads || n_q_heads > MFS_MAX_HEADS)
+        return mfs::op_fail(MFS_E_ARG, op, "n_q_heads must be a multiple of n_kv_heads, at most 65535");
     if (!(scale > 0.f && scale <= 1e30f)) return mfs::op_fail(MFS_E_ARG, op, "scale must be positive and finite");
     if (n_seqs == 0) return MFS_OK;
     if (!kv_len || !q || !out || !workspace) return mfs::op_fail(MFS_E_ARG, op, "null kv_len, q, out or workspace");

@@ -1095,7 +1095,7 @@ extern "C" int mfs_prompt_attention(int dtype, int n_tokens, int n_seqs, const i
     if (dtype != MFS_DTYPE_F32 && dtype != MFS_DTYPE_BF16) return mfs::op_fail(MFS_E_ARG, op, "dtype must be fp32 or bf16");
     if (head_dim != 64 && head_dim != 128) return mfs::op_fail(MFS_E_ARG, op, "head_dim must be 64 or 128");
     if (n_tokens < 0 || n_seqs < 0 || window < 0) return mfs::op_fail(MFS_E_ARG, op, "need n_tokens, n_seqs and window >= 0");
-    if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads > 65535)
+    if (n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads > MFS_MAX_HEADS)
         return mfs::op_fail(MFS_E_ARG, op, "n_q_heads must be a multiple of n_kv_heads, at most 65535");
     if (!(scale > 0.f && scale <= 1e30f)) return mfs::op_fail(MFS_E_ARG, op, "scale must be positive and finite");
     if (n_tokens == 0 || n_seqs == 0) return MFS_OK;

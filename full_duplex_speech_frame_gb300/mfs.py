@@ -384,6 +384,12 @@ def _refuse(message: str):
     raise MfsError(-1, message)
 
 
+def _window(w: int) -> int:
+    if not 0 <= w <= 0x7fffffff:
+        _refuse(f"window {w} outside [0, 2^31)")
+    return w
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype is torch.bfloat16:
@@ -436,6 +442,8 @@ def mfs_sample_rows(logits, uniforms, tokens, temperature=None, top_k=None, top_
     rows, cols = logits.shape
     if cols > 1 and logits.stride(1) != 1:
         _refuse("logits: need unit column stride")
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        _refuse("logits: too many rows or columns")
     dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
     _enqueue(dev, stream, _lib.mfs_sample_rows, logits.data_ptr(), _dtype_code(logits), rows, cols,
              logits.stride(0) if rows > 1 else cols, _array(temperature, "temperature", rows, f32, dev),
@@ -457,6 +465,8 @@ class PagedKV:
             _refuse("cache: need dense rows, and equal strides in k and v")
         if table.dim() != 2 or table.dtype != torch.int32 or table.device != k.device or (table.shape[1] > 1 and table.stride(1) != 1):
             _refuse("cache: need an int32 table [n_seqs, pages] with unit column stride on the cache's device")
+        if max(*k.shape, *table.shape) > 0x7fffffff:
+            _refuse("cache: too many pages")
         self.k, self.v, self.table = k, v, table
         self.device, self.n_seqs = k.device, table.shape[0]
         stride = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
@@ -521,7 +531,7 @@ def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, wo
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse("workspace: need a contiguous tensor on the cache's device")
     _enqueue(dev, stream, _lib.mfs_paged_attention, cache.c, n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_,
-             hd ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.nbytes)
+             hd ** -0.5 if scale is None else scale, _window(window), workspace.data_ptr(), workspace.nbytes)
 
 
 def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) -> None:
@@ -537,4 +547,4 @@ def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) ->
     vp, vs = _rows(v, "v", n, hkv, hd, dtype, dev)
     op, os_ = _rows(out, "out", n, hq, hd, dtype, dev)
     _enqueue(dev, stream, _lib.mfs_prompt_attention, _dtype_code(q), n, n_seqs, _array(cu, "cu", n_seqs + 1, torch.int32, dev), qp, qs, hq,
-             kp, ks, vp, vs, hkv, hd, op, os_, hd ** -0.5 if scale is None else scale, window)
+             kp, ks, vp, vs, hkv, hd, op, os_, hd ** -0.5 if scale is None else scale, _window(window))

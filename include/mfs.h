@@ -396,11 +396,13 @@ int mfs_sample_rows(const void* logits, int dtype, int rows, int cols, long long
  *            j < table_width.
  *            Entries that a call does not need are not read as pages (they may
  *            hold anything); sequences may share pages they only read.
- *   head_dim 64 or 128; page_size 1 .. MFS_MAX_PAGE_SIZE
+ *   head_dim 64 or 128; page_size 1 .. MFS_MAX_PAGE_SIZE; at most MFS_MAX_HEADS heads, of
+ *            queries in the calls below too
  * A needed entry outside [0, n_pages), or a position at or past
  * table_width * page_size, never touches memory outside the pool: the append
  * skips that token's row, the attention gives NaN for that sequence. */
 #define MFS_MAX_PAGE_SIZE 65536
+#define MFS_MAX_HEADS 65535
 typedef struct {
     void* k;
     void* v;
@@ -469,7 +471,8 @@ int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv
  *            are left as they are
  *   q, out   [n_tokens][n_q_heads][head_dim]; k, v [n_tokens][n_kv_heads][head_dim];
  *            dtype MFS_DTYPE_F32 or MFS_DTYPE_BF16; head_dim 64 or 128; n_q_heads a
- *            multiple of n_kv_heads; strides as above; out overlaps no input
+ *            multiple of n_kv_heads, at most MFS_MAX_HEADS; strides as above; out overlaps no
+ *            input
  * bf16 runs on the tensor cores (fp32 scores, statistics and sums; the softmax
  * weights are rounded to bf16 for the product with the values); fp32 runs on the
  * CUDA cores in fp32.  A key or value outside a row's range (another sequence's,

@@ -712,3 +712,39 @@ def test_prompt_attention_many_short_sequences(mfs):
     lens[::3] = rng.integers(1, 9, len(lens[::3]))
     for dtype in ("bf16", "f32"):
         _check_prompt(mfs, rng, lens.tolist(), 4, 2, 64, dtype)
+
+
+@pytest.mark.parametrize("hd,dtype", [(64, "bf16"), (128, "f32")])
+def test_paged_attention_at_the_largest_length(mfs, hd, dtype):
+    """2^31 - 1 positions, a window of the last 1001: the last tile ends past the largest int.  Every
+    page of the sequence is the same one, so the window's rows are its rows 64534 .. 65534."""
+    torch, rng = _torch(), np.random.RandomState(3)
+    k, v = _normal(rng, 1, 1, 65536, hd, dtype=dtype), _normal(rng, 1, 1, 65536, hd, dtype=dtype)
+    k[:, :, 65535] = v[:, :, 65535] = float("nan")
+    q = _normal(rng, 1, 4, hd, dtype=dtype)
+    out = torch.full_like(q, -7.0)
+    table = torch.zeros(1, 32768, dtype=torch.int32, device="cuda")
+    mfs.mfs_paged_attention(mfs.PagedKV(k, v, table), q, _i32([2**31 - 1]), out, window=1001)
+    keys, vals, qs = _np(k)[0, 0, 64534:65535], _np(v)[0, 0, 64534:65535], _np(q)[0]
+    scores = qs @ keys.T * hd ** -0.5
+    w = np.exp(scores - scores.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    ref = w @ vals
+    size = (np.abs(qs) @ np.abs(keys).T * hd ** -0.5).max()
+    assert (np.abs(_np(out)[0] - ref) <= S.attention_tolerance(ref, w @ np.abs(vals), size, 1001, hd, dtype == "bf16")).all()
+
+
+def test_numbers_past_an_int_are_refused(mfs):
+    import torch
+    q = torch.zeros(1, 2, 64, device="cuda")
+    c = mfs.PagedKV(torch.zeros(1, 2, 16, 64, device="cuda"), torch.zeros(1, 2, 16, 64, device="cuda"),
+                    torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    for window in (-1, 2**31, 2**32 + 5):
+        with pytest.raises(mfs.MfsError, match="window"):
+            mfs.mfs_paged_attention(c, q, n[:1], torch.empty_like(q), window=window)
+        with pytest.raises(mfs.MfsError, match="window"):
+            mfs.mfs_prompt_attention(q, q, q, n, torch.empty_like(q), window=window)
+    one = torch.zeros(1, device="cuda")
+    with pytest.raises(mfs.MfsError, match="too many"):
+        mfs.mfs_sample_rows(one[:, None].expand(2**32 + 1, 1), one, torch.zeros(1, dtype=torch.int32, device="cuda"))

@@ -99,6 +99,17 @@ def test_prompt_attention_refusals(mfs, bad):
     assert mfs.mfs_last_error(None).startswith("prompt_attention: ")
 
 
+def test_heads_past_the_limit_are_refused(mfs):
+    n = 65536
+    c = _cache(mfs, n_kv_heads=n, head_stride=64, row_stride=64 * n, page_stride=64 * n * 16)
+    assert _append(mfs, c, ks=64 * n, vs=64 * n, k_out=None) == -1 and "heads" in mfs.mfs_last_error(None)
+    assert _attend(mfs, c, hq=n, qs=64 * n, os=64 * n) == -1 and "heads" in mfs.mfs_last_error(None)
+    c = _cache(mfs)
+    assert _append(mfs, c, hq=n, qs=64 * n, qos=64 * n) == -1 and "heads" in mfs.mfs_last_error(None)
+    assert _attend(mfs, c, hq=n, qs=64 * n, os=64 * n) == -1 and "heads" in mfs.mfs_last_error(None)
+    assert _prompt(mfs, hq=n, qs=64 * n, os=64 * n) == -1 and "heads" in mfs.mfs_last_error(None)
+
+
 def test_nothing_to_do_is_ok(mfs):
     assert _append(mfs, n=0) == 0 and _append(mfs, n_seqs=0) == 0
     assert _attend(mfs, n=0) == 0
