@@ -897,8 +897,16 @@ extern "C" int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs
         (q && (!mfs::rows_ok(q, q_stride, n_q_heads, hd, elem) || !mfs::rows_ok(q_out, q_out_stride, n_q_heads, hd, elem))))
         return mfs::op_fail(MFS_E_ARG, op, "pointers and token strides must be multiples of 16 bytes, a stride at least heads x head_dim");
     Turns turns = {};
-    if (rope)
-        for (int i = 0; i < hd / 2; ++i) turns.f[i] = pow(theta, -2.0 * i / hd) / 6.283185307179586476925;
+    if (rope) {
+        // powers of the first ratio, each the product of two before it: at most 7 roundings of 2^-53, where 64 calls of
+        // pow cost the caller 2 us
+        turns.f[0] = 1.0;
+        for (int b = 1; b < hd / 2; b *= 2) {
+            turns.f[b] = pow(theta, -2.0 * b / hd);
+            for (int i = 1; i < b; ++i) turns.f[b + i] = turns.f[b] * turns.f[i];
+        }
+        for (int i = 0; i < hd / 2; ++i) turns.f[i] /= 6.283185307179586476925;
+    }
     const Cache C = cache_of(cache);
     const int hq = q ? n_q_heads : 0;
     cudaStream_t st = (cudaStream_t)cuda_stream;

@@ -403,7 +403,7 @@ def _array(t, what: str, n: int, dtype, dev: int):
     """Data pointer of a contiguous 1-D tensor of at least n elements on CUDA device `dev` (None: null)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.dim() != 1 or t.size(0) < n or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() < n or t.get_device() != dev or not (t.is_contiguous() or n <= 1):
         _refuse(f"{what}: need a contiguous {dtype} tensor of {n} elements on cuda:{dev}")
     return t.data_ptr()
 
