@@ -836,20 +836,21 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
 
 // --------------------------------------------------------------------- fp32
 //
-// On the CUDA cores: a CTA of 256 threads takes 128 query rows of one sequence and head and walks over
-// tiles of 64 keys in shared memory.  A thread has 8 rows x 4 keys of the scores and 8 rows x HD / 16
-// elements of the output in registers (rows and keys 16 apart, so that a warp's 16-byte loads meet no
-// bank twice), with paired fp32 products; a row's maximum and sum go over half a warp.  Keys of the next
-// tile are copied while the values of this one are summed, and the other way round.  What bounds it is
-// the fp32 rate: 4096 tokens, 32 + 8 heads of 128, take 3.0 ms = 46 TFLOP/s.  In tiles that some
-// row does not see whole, unseen products are left out, not multiplied by zero.
+// On the CUDA cores: a CTA of 256 threads takes 16 RT query rows of one sequence and head (RT 8, 4 or 2)
+// and walks over tiles of 64 keys in shared memory.  A thread has RT rows x 4 keys of the scores and
+// RT rows x HD / 16 elements of the output in registers (rows and keys 16 apart, so that a warp's 16-byte
+// loads meet no bank twice), with paired fp32 products; a row's maximum and sum go over half a warp.
+// Keys of the next tile are copied while the values of this one are summed, and the other way round.
+// What bounds it is the fp32 rate: 4096 tokens, 32 + 8 heads of 128, take 3.0 ms = 46 TFLOP/s.  In tiles
+// that some row does not see whole, unseen products are left out, not multiplied by zero.
 
-constexpr int PF_ROWS = 128, PF_KEYS = 64, PF_THREADS = 256;
+constexpr int PF_KEYS = 64, PF_THREADS = 256;
 
-template <int HD>
+template <int HD, int RT>
 struct PfShape {
+    static constexpr int ROWS = 16 * RT;                 // query rows of a CTA
     static constexpr int LD = HD + 4, LP = PF_KEYS + 4;  // row strides in shared memory
-    static constexpr int BYTES = 4 * ((PF_ROWS + 2 * PF_KEYS) * LD + PF_ROWS * LP);
+    static constexpr int BYTES = 4 * ((ROWS + 2 * PF_KEYS) * LD + ROWS * LP);
 };
 
 struct PfArgs {
@@ -867,17 +868,17 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool full)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(dst)), "l"(src), "r"(n) : "memory");
 }
 
-template <int HD>
-__global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_constant__ PfArgs A)
+template <int HD, int RT>
+__global__ void __launch_bounds__(PF_THREADS, RT == 2 ? 2 : 1) prompt_f32_kernel(const __grid_constant__ PfArgs A)
 {
-    using S = PfShape<HD>;
-    constexpr int LD = S::LD, LP = S::LP, OC = HD / 16;
+    using S = PfShape<HD, RT>;
+    constexpr int ROWS = S::ROWS, LD = S::LD, LP = S::LP, OC = HD / 16;
     extern __shared__ __align__(16) float pf_raw[];
-    float *sq = pf_raw, *sk = sq + PF_ROWS * LD, *sv = sk + PF_KEYS * LD, *sp = sv + PF_KEYS * LD;
+    float *sq = pf_raw, *sk = sq + ROWS * LD, *sv = sk + PF_KEYS * LD, *sp = sv + PF_KEYS * LD;
     __shared__ PtWork work;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     if (tid < 32) {
-        PtDealer deal(A.cu, A.n_tokens, A.n_seqs, A.hq, PF_ROWS);
+        PtDealer deal(A.cu, A.n_tokens, A.n_seqs, A.hq, ROWS);
         deal.start();
         PtWork w;
         if (!deal.get(0, w)) w.h = -1;
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
     __syncthreads();
     const PtWork w = work;
     if (w.h < 0) return;
-    const int rows = min(PF_ROWS, w.len - w.r0), W = A.window;
+    const int rows = min(ROWS, w.len - w.r0), W = A.window;
     const float* kg = A.k + (long long)w.b * A.k_stride + w.h / A.g * HD;
     const float* vg = A.v + (long long)w.b * A.v_stride + w.h / A.g * HD;
     auto copy_tile = [&](float* dst, const float* src, long long stride, int r0, int n, int limit) {
@@ -897,15 +898,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
         }
     };
     const int t0 = (W > 0 ? max(0, w.r0 - W + 1) : 0) / PF_KEYS, t1 = (w.r0 + rows - 1) / PF_KEYS + 1;
-    copy_tile(sq, A.q + (long long)(w.b + w.r0) * A.q_stride + w.h * HD, A.q_stride, 0, PF_ROWS, rows);
+    copy_tile(sq, A.q + (long long)(w.b + w.r0) * A.q_stride + w.h * HD, A.q_stride, 0, ROWS, rows);
     copy_tile(sk, kg, A.k_stride, t0 * PF_KEYS, PF_KEYS, w.len);
     asm volatile("cp.async.commit_group;" ::: "memory");
     copy_tile(sv, vg, A.v_stride, t0 * PF_KEYS, PF_KEYS, w.len);
     asm volatile("cp.async.commit_group;" ::: "memory");
 
-    float o[8][OC], m[8], l[8];
+    float o[RT][OC], m[RT], l[RT];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -917,9 +918,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
         const bool edge = k0 + PF_KEYS - 1 > w.r0 || (W > 0 && k0 <= w.r0 + rows - 1 - W);
         asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys
         __syncthreads();
-        uint64_t acc[8][4];
+        uint64_t acc[RT][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = 0;
 #pragma unroll 4
@@ -928,7 +929,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
 #pragma unroll
             for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * LD + e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(sq + (ty + 16 * i) * LD + e);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = fma2(q4.y, k4[j].y, fma2(q4.x, k4[j].x, acc[i][j]));
@@ -938,7 +939,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
         if (t + 1 < t1) copy_tile(sk, kg, A.k_stride, k0 + PF_KEYS, PF_KEYS, w.len);
         asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < RT; ++i) {
             const int row = w.r0 + ty + 16 * i;
             float s[4], mx = -INFINITY;
 #pragma unroll
@@ -970,9 +971,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
         auto product = [&](auto part) {  // part: some keys are left out
 #pragma unroll 2
             for (int j = 0; j < PF_KEYS; j += 4) {
-                float4 p4[8];
+                float4 p4[RT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
+                for (int i = 0; i < RT; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     uint64_t v2[OC / 2];
@@ -983,7 +984,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
                         v2[2 * e + 1] = y.y;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < RT; ++i) {
                         const float p = x == 0 ? p4[i].x : x == 1 ? p4[i].y : x == 2 ? p4[i].z : p4[i].w;
                         if (decltype(part)::value) {
                             const int row = w.r0 + ty + 16 * i, key = k0 + j + x;
@@ -1007,7 +1008,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
         float sum = l[i];
         for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
         const int r = ty + 16 * i;
@@ -1020,23 +1021,40 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prompt_f32_kernel(const __grid_
     }
 }
 
+template <int HD, int RT>
+int launch_f32(const PfArgs& A, cudaStream_t st)
+{
+    const char* op = "prompt_attention";
+    using S = PfShape<HD, RT>;
+    const long long blocks = ((long long)A.n_tokens / S::ROWS + A.n_seqs) * A.hq;  // blocks there can be
+    if (blocks > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many tokens and sequences");
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, (const void*)prompt_f32_kernel<HD, RT>, S::BYTES, &sms);
+    if (e == cudaSuccess) {
+        prompt_f32_kernel<HD, RT><<<(unsigned)blocks, PF_THREADS, S::BYTES, st>>>(A);
+        e = cudaGetLastError();
+    }
+    return mfs::op_launched(op, e);
+}
+
+// Row tiles of 128; of 64 or 32 where they would be fewer than one and a half per SM, or longer than the sequences on
+// average.  With 128, 64 and 32 rows, heads of 128: 4096 tokens, 32 heads 3010, 3481 and 4706 us; 1000 tokens 227, 246, 322;
+// 512 tokens 114, 72, 99; 8 heads 115, 67, 52; 137 tokens, 32 heads 46, 28, 26; 100 sequences of 20 408, 254, 152; 50 of
+// 40 208, 134, 116; 25 of 80 168, 130, 129.
 template <int HD>
 int run_f32(int n_tokens, int n_seqs, const int32_t* cu, const void* q, long long q_stride, int hq, const void* k, long long k_stride,
             const void* v, long long v_stride, int hkv, void* out, long long out_stride, float scale, int window, cudaStream_t st)
 {
-    const char* op = "prompt_attention";
     const PfArgs A = {cu, (const float*)q, (const float*)k, (const float*)v, (float*)out, q_stride, k_stride, v_stride, out_stride,
                       n_tokens, n_seqs, hq, hq / hkv, window, scale * 1.44269504088896340736f};
-    const long long blocks = ((long long)n_tokens / PF_ROWS + n_seqs) * hq;  // blocks there can be
-    if (blocks > 0x7fffffffLL) return mfs::op_fail(MFS_E_ARG, op, "too many tokens and sequences");
     int sms = 0;
-    static mfs::PerDevice ready;
-    cudaError_t e = mfs::op_device(ready, (const void*)prompt_f32_kernel<HD>, PfShape<HD>::BYTES, &sms);
-    if (e == cudaSuccess) {
-        prompt_f32_kernel<HD><<<(unsigned)blocks, PF_THREADS, PfShape<HD>::BYTES, st>>>(A);
-        e = cudaGetLastError();
-    }
-    return mfs::op_launched(op, e);
+    static mfs::PerDevice known;
+    const cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
+    if (e != cudaSuccess) return mfs::op_launched("prompt_attention", e);
+    int rt = 8;
+    while (rt > 2 && (((long long)n_tokens / (16 * rt) + n_seqs) * hq * 2 < 3 * sms || n_tokens <= 16LL * rt * n_seqs)) rt /= 2;
+    return rt == 8 ? launch_f32<HD, 8>(A, st) : rt == 4 ? launch_f32<HD, 4>(A, st) : launch_f32<HD, 2>(A, st);
 }
 
 template <int HD>

@@ -748,3 +748,11 @@ def test_numbers_past_an_int_are_refused(mfs):
     one = torch.zeros(1, device="cuda")
     with pytest.raises(mfs.MfsError, match="too many"):
         mfs.mfs_sample_rows(one[:, None].expand(2**32 + 1, 1), one, torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("hq,hkv,hd,lens", [(1, 1, 128, [333]), (8, 8, 64, [300]), (4, 2, 128, [150] * 12), (32, 8, 64, [300, 1, 299]),
+                                            (3, 1, 64, [33] * 70), (32, 8, 128, [700, 600])])
+def test_prompt_attention_fp32_row_tiles(mfs, hq, hkv, hd, lens):
+    """Few rows, many short sequences and many rows, so that row tiles of every size are chosen."""
+    _check_prompt(mfs, np.random.default_rng(71), lens, hq, hkv, hd, "f32", rows=12)
+    _check_prompt(mfs, np.random.default_rng(72), lens, hq, hkv, hd, "f32", window=37, rows=12)
