@@ -266,6 +266,19 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi)
 template <typename T, int HD>
 constexpr int PA_ROWS = 4096 / (HD * (int)sizeof(T));  // positions per tile: 4 KB of keys, 4 KB of values
 
+// Where element x (row x / HD) of a piece lies: 8 rows of a store meet different banks.
+template <int HD>
+__device__ __forceinline__ int pa_at(int x) { return x ^ (((x / HD) & 7) << 3); }
+
+__device__ __forceinline__ void put4(float* p, float4 v, float by)
+{
+    *reinterpret_cast<float4*>(p) = make_float4(v.x * by, v.y * by, v.z * by, v.w * by);
+}
+__device__ __forceinline__ void put4(bf16* p, float4 v, float by)
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x * by, v.y * by), pack_bf16(v.z * by, v.w * by));
+}
+
 struct PaArgs {
     Cache C;
     const int32_t* kv_len;
@@ -438,14 +451,14 @@ struct PaBf16 {
         }
     }
 
-    template <typename F>
-    __device__ __forceinline__ void each(F f)  // f(row, index of its statistics in this lane, element, value)
+    __device__ __forceinline__ void write(float* piece)
     {
         const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) f(r + (x >> 1) * 8, x >> 1, 8 * j + 2 * t + (x & 1), o[j][x]);
+            for (int x = 0; x < 4; x += 2)
+                *reinterpret_cast<float2*>(piece + pa_at<HD>((r + 4 * x) * HD + 8 * j + 2 * t)) = make_float2(o[j][x], o[j][x + 1]);
     }
     __device__ __forceinline__ int own_row(int h) const { return ((threadIdx.x & 31) >> 2) + 8 * h; }
     __device__ __forceinline__ bool owner() const { return (threadIdx.x & 3) == 0; }
@@ -532,14 +545,14 @@ struct PaF32 {
             for (int x = 16; x; x >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
     }
 
-    template <typename F>
-    __device__ __forceinline__ void each(F f)
+    __device__ __forceinline__ void write(float* piece)
     {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int h = 0; h < GM; ++h)
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(h, h, lane * E + e, o[h][e]);
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<float2*>(piece + pa_at<HD>(h * HD + lane * E + e)) = make_float2(o[h][e], o[h][e + 1]);
     }
     __device__ __forceinline__ int own_row(int h) const { return h; }
     __device__ __forceinline__ bool owner() const { return (threadIdx.x & 31) == 0; }
@@ -558,13 +571,13 @@ struct PaLayout {
     static constexpr int RING = PA_WARPS * PA_STAGES * STAGE;
     static constexpr int Q = sizeof(T) == 4 ? PA_WARPS * GM * HD * 4 : 0;
     static constexpr int BYTES = RING + Q;
-    static_assert(GM * HD * 4 <= PA_STAGES * STAGE, "a warp's piece takes its ring's place");
+    static_assert(GM * HD * 4 <= STAGE, "a warp's piece takes a stage's place");
 };
 
 // A piece of an item that a warp could not finish: whether the item's first and last tile were in it, and the
 // CTA that holds the last one.  s = -1: none.
 struct PaPiece {
-    int s, hb, first, last, last_cta;
+    int s, hb, first, last, last_cta, stage;  // stage: of the warp's ring, where the piece lies
 };
 
 template <typename T, int HD, int GM>
@@ -681,46 +694,47 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                     reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq);
             bad = bad || ((bad_ring >> stage) & 1u);
             __syncwarp();
-            issue(stage);
-            stage = stage + 1 == S ? 0 : stage + 1;
-            const bool ends = use.tile + 1 == use.ntiles;
-            if (ends || it + 1 == n) {
+            const bool ends = use.tile + 1 == use.ntiles, end = it + 1 == n;
+            if (ends || end) {
+                // the item's output, through the stage just read: one place in the code writes the accumulators, which
+                // matters where a call is mostly fetching instructions
                 st.finish();
                 if (bad) {
 #pragma unroll
                     for (int h = 0; h < State::OWN; ++h) st.l[h] = NAN;
                 }
+                float* piece = reinterpret_cast<float*>(ring_p + stage * L::STAGE);
+                const int slot = 2 * warp + (end || (ends && front));
+                st.write(piece);
+                if (st.owner()) {
+#pragma unroll
+                    for (int h = 0; h < State::OWN; ++h) sh_ml[slot][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
+                }
+                __syncwarp();
                 if (ends && front) {
                     const int h0 = (use.hb / A.nhb) * A.g + (use.hb % A.nhb) * GM;
                     T* o = reinterpret_cast<T*>(A.out) + (long long)use.s * A.out_stride + (long long)h0 * HD;
-                    float inv[State::OWN];
-#pragma unroll
-                    for (int h = 0; h < State::OWN; ++h) inv[h] = 1.f / st.l[h];
-                    st.each([&](int row, int h, int e, float v) {
-                        if (row < nh) o[row * HD + e] = from_f<T>(v * inv[h]);
-                    });
+                    for (int x = 4 * lane; x < nh * HD; x += 128) {
+                        const float4 v = *reinterpret_cast<const float4*>(piece + pa_at<HD>(x));
+                        put4(o + x, v, 1.f / sh_ml[slot][x / HD].y);
+                    }
+                    __syncwarp();
                 } else {
-                    // into the place of the warp's ring if that has nothing more to come, else (the end of an item
-                    // begun before the share: once per warp at most) into the workspace until the CTA's end
-                    const bool end = it + 1 == n;
-                    const int slot = 2 * warp + end;
-                    if (end) {
-                        asm volatile("cp.async.wait_all;" ::: "memory");
+                    // stays in the ring if that has nothing more to come; else (the end of an item begun before the share:
+                    // once per warp at most) into the workspace until the CTA's end
+                    if (!end) {
+                        float* o = A.front_o + (long long)share * GM * HD;
+                        for (int x = 4 * lane; x < nh * HD; x += 128)
+                            *reinterpret_cast<float4*>(o + pa_at<HD>(x)) = *reinterpret_cast<const float4*>(piece + pa_at<HD>(x));
                         __syncwarp();
                     }
-                    float* o = end ? reinterpret_cast<float*>(ring_p) : A.front_o + (long long)share * GM * HD;
-                    st.each([&](int row, int, int e, float v) {
-                        if (row < nh) o[row * HD + e] = v;
-                    });
-                    if (st.owner()) {
-#pragma unroll
-                        for (int h = 0; h < State::OWN; ++h) sh_ml[slot][st.own_row(h)] = make_float2(st.m[h], st.l[h]);
-                    }
                     if (lane == 0)
-                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + use.ntiles)};
+                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + use.ntiles), stage};
                 }
                 fresh = true;
             }
+            issue(stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
             if (it + 1 < n) {
                 if (ends) item_first += use.ntiles;
                 pa_next<ROWS>(A, use);
@@ -756,17 +770,19 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         const int h0 = (p0.hb / A.nhb) * A.g + (p0.hb % A.nhb) * GM;
         T* out = reinterpret_cast<T*>(A.out) + (long long)p0.s * A.out_stride + (long long)h0 * HD;
         const long long slot = (long long)cta * 2 + (p0.first ? 1 : 0);
-        for (int x = tid; x < nh * HD; x += PA_WARPS * 32) {
-            float acc = 0.f;
+        for (int x = 4 * tid; x < nh * HD; x += PA_WARPS * 128) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             const int row = x / HD;
             for (int k = i; k <= j; ++k)
                 if (sh_piece[k].s >= 0) {
-                    const float* o = k & 1 ? reinterpret_cast<const float*>(pa_raw + (k >> 1) * (S * L::STAGE))
+                    const float* o = k & 1 ? reinterpret_cast<const float*>(pa_raw + ((k >> 1) * S + sh_piece[k].stage) * L::STAGE)
                                            : A.front_o + (long long)(cta * PA_WARPS + (k >> 1)) * GM * HD;
-                    acc = fmaf(o[x], sh_w[k][row], acc);
+                    const float4 v = *reinterpret_cast<const float4*>(o + pa_at<HD>(x));
+                    const float w = sh_w[k][row];
+                    acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
                 }
-            if (whole) out[x] = from_f<T>(acc / sh_l[row]);
-            else A.part_o[slot * GM * HD + x] = acc;
+            if (whole) put4(out + x, acc, 1.f / sh_l[row]);
+            else *reinterpret_cast<float4*>(A.part_o + slot * GM * HD + x) = acc;
         }
         if (!whole) {
             if (tid < nh) A.part_ml[slot * GM + tid] = make_float2(sh_m[tid], sh_l[tid]);
