@@ -224,6 +224,10 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
+// What an item costs beside its tiles (its start, its end, its queries), in tiles: shares are cut over both.  64 ragged
+// sequences of up to 1000, 24 + 8 heads of 128: 44.3 us with 0, 35.7 with 1, 35.9 with 2, 35.6 with 4; 256 of up to 300,
+// 32 + 8 heads: 53.9, 44.0, 43.0, 44.3, fp32 139, 85, 81, 82; 64 of up to 100, 8 + 8 heads: 13.7, 12.7, 13.0, 14.1.
+constexpr int PA_ITEM = 2;
 constexpr int PA_STAGES = 2;                     // 16 KB per warp, 128 KB per SM: 3 stages measured 5 % slower on long contexts
 
 // Query heads per block: the 16 rows of an mma tile for bf16.  fp32, on the CUDA cores, pays for every head of the
@@ -289,7 +293,6 @@ struct PaArgs {
     float c;          // scale * log2(e)
     float* part_o;    // [CTA][2][GM][HD]
     float2* part_ml;  // [CTA][2][GM] running maximum (raw score) and sum
-    float* front_o;   // [warp] an item's end, kept until the CTA's warps are done
     int4* rec;        // [CTA] {sequence or -1, head block, last CTA of the item, 0}
 };
 
@@ -570,7 +573,8 @@ struct PaLayout {
     static constexpr int STAGE = PA_ROWS<T, HD> * HD * (int)sizeof(T) * 2;  // keys and values of a tile
     static constexpr int RING = PA_WARPS * PA_STAGES * STAGE;
     static constexpr int Q = sizeof(T) == 4 ? PA_WARPS * GM * HD * 4 : 0;
-    static constexpr int BYTES = RING + Q;
+    static constexpr int FRONTS = PA_WARPS * GM * HD * 4;  // an item's end per warp, kept until the CTA's warps are done
+    static constexpr int BYTES = RING + FRONTS + Q;
     static_assert(GM * HD * 4 <= STAGE, "a warp's piece takes a stage's place");
 };
 
@@ -587,13 +591,15 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     using State = typename std::conditional<sizeof(T) == 2, PaBf16<HD>, PaF32<HD, GM>>::type;
     constexpr int S = PA_STAGES, ROWS = PA_ROWS<T, HD>;
     extern __shared__ __align__(128) char pa_raw[];
-    __shared__ long long sh_sum[PA_WARPS];
+    __shared__ long long sh_tiles[PA_WARPS];
     __shared__ PaPiece sh_piece[2 * PA_WARPS];
     __shared__ float2 sh_ml[2 * PA_WARPS][GM];
-    __shared__ float sh_w[2 * PA_WARPS][GM], sh_l[GM], sh_m[GM];
+    __shared__ float sh_w[2 * PA_WARPS][GM];
+    __shared__ float2 sh_sum[2 * PA_WARPS][GM];  // maximum and sum of the pieces of an item, at its first
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hx = A.C.n_kv_heads * A.nhb, G = gridDim.x, cta = blockIdx.x;
-    float* sq = reinterpret_cast<float*>(pa_raw + L::RING) + warp * GM * HD;
+    float* fronts = reinterpret_cast<float*>(pa_raw + L::RING);
+    float* sq = fronts + (PA_WARPS + warp) * GM * HD;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences of no length: zeros
@@ -607,15 +613,15 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         PaWalk w;
         w.s = s;
         pa_sequence<ROWS>(A, w);
-        return w.ntiles;
+        return w.ntiles ? w.ntiles + PA_ITEM : 0;
     };
     long long mine = 0;
     for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) mine += tiles_of(s);
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sh_sum[warp] = mine;
+    if (lane == 0) sh_tiles[warp] = mine;
     if (tid < 2 * PA_WARPS) sh_piece[tid].s = -1;
     __syncthreads();
-    const long long total = ((sh_sum[0] + sh_sum[1]) + (sh_sum[2] + sh_sum[3])) * Hx;
+    const long long total = ((sh_tiles[0] + sh_tiles[1]) + (sh_tiles[2] + sh_tiles[3])) * Hx;
     const long long shares = min(total, (long long)G * PA_WARPS);
     const int share = cta * PA_WARPS + warp;
     if (cta * PA_WARPS >= shares) {
@@ -645,9 +651,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             item_first += __shfl_sync(0xffffffffu, inc, 31);
         }
         pa_sequence<ROWS>(A, use);
-        use.hb = (int)((unsigned long long)(t0 - item_first) >> 32 ? (t0 - item_first) / use.ntiles : (unsigned)(t0 - item_first) / (unsigned)use.ntiles);
-        item_first += (long long)use.hb * use.ntiles;
-        use.tile = (int)(t0 - item_first);
+        const long long in = t0 - item_first;
+        use.hb = (int)(in >> 32 ? in / (use.ntiles + PA_ITEM) : (unsigned)in / (unsigned)(use.ntiles + PA_ITEM));
+        item_first += (long long)use.hb * (use.ntiles + PA_ITEM);
+        use.tile = max(0, (int)(t0 - item_first) - PA_ITEM);
+        long long at = item_first + PA_ITEM + use.tile;  // where the tile of `use` lies
         PaWalk load = use;
         char* ring_p = pa_raw + warp * (S * L::STAGE);
         const unsigned ring = su32(ring_p);
@@ -657,17 +665,17 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             const long long x = end * shares - 1;
             return (int)((x >> 32 ? x / total : (unsigned)x / (unsigned)total) / PA_WARPS);
         };
-        const int n = (int)(t1 - t0);
-        int n_load = n;         // tiles not yet asked for: the loads run ahead of the products, across items
+        long long at_load = at;  // of `load`: the loads run ahead of the products, across items
         unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
         bool next_bad = false;
-        long long off = pa_offset<ROWS>(A, load, next_bad);
+        long long off = at < t1 ? pa_offset<ROWS>(A, load, next_bad) : -1;
         auto issue = [&](int stage) {
-            if (n_load > 0) {
+            if (at_load < t1) {
                 pa_issue<T, HD>(A, ring + stage * L::STAGE, off);
                 bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
                 next_bad = false;
-                if (--n_load > 0) {
+                at_load += load.tile + 1 < load.ntiles ? 1 : 1 + PA_ITEM;
+                if (at_load < t1) {
                     pa_next<ROWS>(A, load);
                     off = pa_offset<ROWS>(A, load, next_bad);
                 }
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         State st;
         bool fresh = true, bad = false, front = false;
         int stage = 0;
-        for (int it = 0; it < n; ++it) {
+        while (at < t1) {
             if (fresh) {
                 st.begin(A, use, sq);
                 fresh = false;
@@ -694,7 +702,9 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                     reinterpret_cast<float*>(ring_p + stage * L::STAGE), sq);
             bad = bad || ((bad_ring >> stage) & 1u);
             __syncwarp();
-            const bool ends = use.tile + 1 == use.ntiles, end = it + 1 == n;
+            const bool ends = use.tile + 1 == use.ntiles;
+            at += ends ? 1 + PA_ITEM : 1;
+            const bool end = at >= t1;
             if (ends || end) {
                 // the item's output, through the stage just read: one place in the code writes the accumulators, which
                 // matters where a call is mostly fetching instructions
@@ -721,51 +731,57 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                     __syncwarp();
                 } else {
                     // stays in the ring if that has nothing more to come; else (the end of an item begun before the share:
-                    // once per warp at most) into the workspace until the CTA's end
+                    // once per warp at most) into a place of its own
                     if (!end) {
-                        float* o = A.front_o + (long long)share * GM * HD;
+                        float* o = fronts + warp * GM * HD;
                         for (int x = 4 * lane; x < nh * HD; x += 128)
                             *reinterpret_cast<float4*>(o + pa_at<HD>(x)) = *reinterpret_cast<const float4*>(piece + pa_at<HD>(x));
                         __syncwarp();
                     }
                     if (lane == 0)
-                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + use.ntiles), stage};
+                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + PA_ITEM + use.ntiles), stage};
                 }
                 fresh = true;
             }
             issue(stage);
             stage = stage + 1 == S ? 0 : stage + 1;
-            if (it + 1 < n) {
-                if (ends) item_first += use.ntiles;
+            if (!end) {
+                if (ends) item_first += use.ntiles + PA_ITEM;
                 pa_next<ROWS>(A, use);
             }
         }
     }
     __syncthreads();
-    // the pieces of each item, in order
+    // the pieces of each item, in order; `held`, `ended`: bit i: there is a piece i, and it is its item's last
+    const bool is = lane < 2 * PA_WARPS && sh_piece[lane].s >= 0;
+    const unsigned held = __ballot_sync(0xffffffffu, is), ended = __ballot_sync(0xffffffffu, is && sh_piece[lane].last);
+    auto last_of = [&](int i) { return ended >> i ? i + __ffs(ended >> i) - 1 : 31 - __clz(held); };
+    // weights first, a thread per row and piece that is its item's first here
+    if (tid / GM < 2 * PA_WARPS) {
+        const int i = tid / GM, row = tid % GM;
+        const unsigned below = held & ((1u << i) - 1);
+        if ((held >> i & 1) && (!below || (ended >> (31 - __clz(below)) & 1)) && row < A.g - (sh_piece[i].hb % A.nhb) * GM) {
+            const unsigned item = held & ((2u << last_of(i)) - (1u << i));
+            float mx = -INFINITY, l = 0.f;
+            for (unsigned r = item; r; r &= r - 1) mx = fmaxf(mx, sh_ml[__ffs(r) - 1][row].x);
+            for (unsigned r = item; r; r &= r - 1) {
+                const int k = __ffs(r) - 1;
+                const float2 ml = sh_ml[k][row];
+                const float w = ml.x == mx ? 1.f : exp2f((ml.x - mx) * A.c);
+                sh_w[k][row] = w;
+                l = fmaf(ml.y, w, l);
+            }
+            sh_sum[i][row] = make_float2(mx, l);
+        }
+    }
+    __syncthreads();
     if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
-    for (int i = 0; i < 2 * PA_WARPS; ++i) {
-        if (sh_piece[i].s < 0) continue;
-        int j = i;  // the item's last piece here
-        for (int k = i; k < 2 * PA_WARPS && !sh_piece[j].last; ++k)
-            if (sh_piece[k].s >= 0) j = k;
+    for (int i = 0, j; held >> i; i = j + 1) {
+        i += __ffs(held >> i) - 1;
+        j = last_of(i);
+        const unsigned item = held & ((2u << j) - (1u << i));
         const PaPiece p0 = sh_piece[i], p1 = sh_piece[j];
         const int nh = min(GM, A.g - (p0.hb % A.nhb) * GM);
-        if (tid < nh) {
-            float mx = -INFINITY, l = 0.f;
-            for (int k = i; k <= j; ++k)
-                if (sh_piece[k].s >= 0) mx = fmaxf(mx, sh_ml[k][tid].x);
-            for (int k = i; k <= j; ++k)
-                if (sh_piece[k].s >= 0) {
-                    const float2 ml = sh_ml[k][tid];
-                    const float w = ml.x == mx ? 1.f : exp2f((ml.x - mx) * A.c);
-                    sh_w[k][tid] = w;
-                    l = fmaf(ml.y, w, l);
-                }
-            sh_m[tid] = mx;
-            sh_l[tid] = l;
-        }
-        __syncthreads();
         const bool whole = p0.first && p1.last;
         const int h0 = (p0.hb / A.nhb) * A.g + (p0.hb % A.nhb) * GM;
         T* out = reinterpret_cast<T*>(A.out) + (long long)p0.s * A.out_stride + (long long)h0 * HD;
@@ -773,23 +789,21 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         for (int x = 4 * tid; x < nh * HD; x += PA_WARPS * 128) {
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             const int row = x / HD;
-            for (int k = i; k <= j; ++k)
-                if (sh_piece[k].s >= 0) {
-                    const float* o = k & 1 ? reinterpret_cast<const float*>(pa_raw + ((k >> 1) * S + sh_piece[k].stage) * L::STAGE)
-                                           : A.front_o + (long long)(cta * PA_WARPS + (k >> 1)) * GM * HD;
-                    const float4 v = *reinterpret_cast<const float4*>(o + pa_at<HD>(x));
-                    const float w = sh_w[k][row];
-                    acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
-                }
-            if (whole) put4(out + x, acc, 1.f / sh_l[row]);
+            for (unsigned r = item; r; r &= r - 1) {
+                const int k = __ffs(r) - 1;
+                const float* o = k & 1 ? reinterpret_cast<const float*>(pa_raw + ((k >> 1) * S + sh_piece[k].stage) * L::STAGE)
+                                       : fronts + (k >> 1) * GM * HD;
+                const float4 v = *reinterpret_cast<const float4*>(o + pa_at<HD>(x));
+                const float w = sh_w[k][row];
+                acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+            }
+            if (whole) put4(out + x, acc, 1.f / sh_sum[i][row].y);
             else *reinterpret_cast<float4*>(A.part_o + slot * GM * HD + x) = acc;
         }
         if (!whole) {
-            if (tid < nh) A.part_ml[slot * GM + tid] = make_float2(sh_m[tid], sh_l[tid]);
+            if (tid < nh) A.part_ml[slot * GM + tid] = sh_sum[i][tid];
             if (tid == 0 && p0.first) A.rec[cta] = make_int4(p0.s, p0.hb, p1.last_cta, 0);
         }
-        __syncthreads();
-        i = j;
     }
 }
 
@@ -857,7 +871,7 @@ __global__ void __launch_bounds__(HD * PJ_GROUPS) paged_attention_join(const __g
 size_t attention_workspace(int dtype, int hd)
 {
     const size_t gm = dtype == MFS_DTYPE_BF16 ? PA_GM_MAX<bf16> : PA_GM_MAX<float>;
-    return (size_t)PA_MAX_CTAS * ((2 + PA_WARPS) * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
+    return (size_t)PA_MAX_CTAS * (2 * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
 }
 
 template <typename T, int HD, int GM>
@@ -866,8 +880,7 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     using L = PaLayout<T, HD, GM>;
     A.nhb = (A.g + GM - 1) / GM;
     A.part_o = reinterpret_cast<float*>(workspace);
-    A.front_o = A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD;
-    A.part_ml = reinterpret_cast<float2*>(A.front_o + (size_t)PA_MAX_CTAS * PA_WARPS * GM * HD);
+    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * GM);
     const int rows = A.g < GM ? A.g : GM;
     int sms = 0;
