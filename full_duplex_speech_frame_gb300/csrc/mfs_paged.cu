@@ -216,9 +216,9 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 // filled with zeros and never read), with the page of the next stage's rows looked up a stage ahead.
 //
 // What bounds it is memory: each key and value is read once.  bf16, 8 kv heads of 128: 4 sequences of up
-// to 131072, 64 query heads, 209 us = 6.4 TB/s, 0.95 of the measured copy rate; 32 of up to 8192, 32
-// query heads, pages of 16, 98 us = 5.65 TB/s; the rest is the start, the join and two launches, which
-// is most of one sequence of 3000 positions and 32 kv heads: 18 us, 7.3 us of it memory.  The matrix
+// to 131072, 64 query heads, 202 us = 6.6 TB/s, 0.98 of the measured copy rate; 32 of up to 8192, 32
+// query heads, pages of 16, 91 us = 6.1 TB/s; the rest is the start, the join and two launches, which
+// is most of one sequence of 3000 positions and 32 kv heads: 17.3 us, 7.3 us of it memory.  The matrix
 // instructions (a tile's 16 rows are the group's query heads, zero rows for those it lacks) keep the
 // tensor pipe 17 % busy there, so the wide forms of them would gain nothing.
 
@@ -293,6 +293,7 @@ struct PaArgs {
     float c;          // scale * log2(e)
     float* part_o;    // [CTA][2][GM][HD]
     float2* part_ml;  // [CTA][2][GM] running maximum (raw score) and sum
+    int join_rows;    // log2 of the query heads per block of the join: 0 or 1
     int4* rec;        // [CTA] {sequence or -1, head block, last CTA of the item, 0}
 };
 
@@ -807,65 +808,71 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     }
 }
 
-// Joins the pieces of the items that cross CTAs: one block per (CTA that began one, query head), PJ_GROUPS groups of HD
-// threads that take eight pieces at a time, all on their way together.
-constexpr int PJ_GROUPS = 4;
+// Joins the pieces of the items that cross CTAs: a block per CTA that began one and one or two query heads, HD / 2
+// threads for each head and group of pieces, of which a group takes eight at a time, all on their way together.  Small
+// blocks, as they start while the last CTAs of the first kernel still hold their registers: 4 ragged contexts of up to
+// 1000, 32 + 8 heads of 128: 10.9 us (11.6 us by blocks of 512, 12.1 us by one block of 512 per head); one context of
+// 100000, 8 heads on one kv head, 34 us (31 us by blocks of 512).
+constexpr int PJ_THREADS = 256;
 
 template <typename T, int HD, int GM>
-__global__ void __launch_bounds__(HD * PJ_GROUPS) paged_attention_join(const __grid_constant__ PaArgs A)
+__global__ void __launch_bounds__(PJ_THREADS) paged_attention_join(const __grid_constant__ PaArgs A)
 {
-    __shared__ float s_acc[PJ_GROUPS][HD], s_mx[PJ_GROUPS], s_l[PJ_GROUPS];
+    constexpr int LANES = HD / 2, SLOTS = PJ_THREADS / LANES;
+    const int groups = SLOTS >> A.join_rows;
+    __shared__ float2 s_acc[SLOTS][LANES], s_ml[SLOTS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int cta = blockIdx.x, row = blockIdx.y, e = threadIdx.x % HD, group = threadIdx.x / HD;
+    const int cta = blockIdx.x, e = threadIdx.x % LANES, slot = threadIdx.x / LANES, group = slot >> A.join_rows;
     const int4 r = A.rec[cta];
-    if (r.x < 0 || row >= A.g - (r.y % A.nhb) * GM) return;
-    const int np = r.z - cta + 1;  // pieces: (cta, 1), then (cta + i, 0)
-    float mx = -INFINITY, acc = 0.f, l = 0.f;
-    for (int i0 = 8 * group; i0 < np; i0 += 8 * PJ_GROUPS) {
-        float2 ml[8];
-        float o[8];
+    if (r.x < 0) return;
+    const int row = (blockIdx.y << A.join_rows) + (slot & ((1 << A.join_rows) - 1)), nh = min(GM, A.g - (r.y % A.nhb) * GM);
+    const int np = row < nh ? r.z - cta + 1 : 0;  // pieces: (cta, 1), then (cta + i, 0)
+    float mx = -INFINITY, l = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int i0 = 8 * group; i0 < np; i0 += 8 * groups) {
+        float2 ml[8], o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const long long slot = ((long long)(cta + i0 + i) * 2 + (i0 + i == 0)) * GM + row;
-            ml[i] = i0 + i < np ? A.part_ml[slot] : make_float2(-INFINITY, 0.f);
-            o[i] = i0 + i < np ? A.part_o[slot * HD + e] : 0.f;
+            const long long at = ((long long)(cta + i0 + i) * 2 + (i0 + i == 0)) * GM + row;
+            ml[i] = i0 + i < np ? A.part_ml[at] : make_float2(-INFINITY, 0.f);
+            o[i] = i0 + i < np ? reinterpret_cast<const float2*>(A.part_o + at * HD)[e] : make_float2(0.f, 0.f);
         }
         float mn = mx;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mn = fmaxf(mn, ml[i].x);
         const float a = mx == mn ? 1.f : exp2f((mx - mn) * A.c);
         mx = mn;
-        acc *= a;
+        acc = make_float2(acc.x * a, acc.y * a);
         l *= a;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float w = ml[i].x == mx ? 1.f : exp2f((ml[i].x - mx) * A.c);
             l = fmaf(ml[i].y, w, l);
-            acc = fmaf(o[i], w, acc);
+            acc = make_float2(fmaf(o[i].x, w, acc.x), fmaf(o[i].y, w, acc.y));
         }
     }
-    if (np > 8) {  // the groups, in order
-        s_acc[group][e] = acc;
-        if (e == 0) { s_mx[group] = mx; s_l[group] = l; }
+    if (r.z - cta >= 8) {  // the groups, in order
+        s_acc[slot][e] = acc;
+        if (e == 0) s_ml[slot] = make_float2(mx, l);
         __syncthreads();
-        if (group) return;
-        float mn = mx;
-#pragma unroll
-        for (int k = 1; k < PJ_GROUPS; ++k) mn = fmaxf(mn, s_mx[k]);
-        float sum = 0.f, all = 0.f;
-#pragma unroll
-        for (int k = 0; k < PJ_GROUPS; ++k) {
-            const float w = s_mx[k] == mn ? 1.f : exp2f((s_mx[k] - mn) * A.c);
-            sum = fmaf(s_l[k], w, sum);
-            all = fmaf(s_acc[k][e], w, all);
+        if (group == 0) {
+            const int ng = min(groups, (np + 7) / 8);
+            for (int k = 1; k < ng; ++k) mx = fmaxf(mx, s_ml[slot + (k << A.join_rows)].x);
+            l = 0.f;
+            acc = make_float2(0.f, 0.f);
+            for (int k = 0; k < ng; ++k) {
+                const float2 ml = s_ml[slot + (k << A.join_rows)], o = s_acc[slot + (k << A.join_rows)][e];
+                const float w = ml.x == mx ? 1.f : exp2f((ml.x - mx) * A.c);
+                l = fmaf(ml.y, w, l);
+                acc = make_float2(fmaf(o.x, w, acc.x), fmaf(o.y, w, acc.y));
+            }
         }
-        l = sum;
-        acc = all;
-    } else if (group) {
-        return;
     }
+    if (group || !np) return;
     const int h = (r.y / A.nhb) * A.g + (r.y % A.nhb) * GM + row;
-    reinterpret_cast<T*>(A.out)[(long long)r.x * A.out_stride + (long long)h * HD + e] = from_f<T>(acc / l);
+    T* out = reinterpret_cast<T*>(A.out) + (long long)r.x * A.out_stride + (long long)h * HD + 2 * e;
+    out[0] = from_f<T>(acc.x / l);
+    out[1] = from_f<T>(acc.y / l);
 }
 
 size_t attention_workspace(int dtype, int hd)
@@ -883,6 +890,7 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * GM);
     const int rows = A.g < GM ? A.g : GM;
+    A.join_rows = rows > 1 ? 1 : 0;
     int sms = 0;
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<T, HD, GM>, L::BYTES, &sms);
@@ -892,8 +900,8 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     e = cudaGetLastError();
     if (e != cudaSuccess) return mfs::op_launched("paged_attention", e);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)G, (unsigned)rows);
-    cfg.blockDim = dim3(HD * PJ_GROUPS);
+    cfg.gridDim = dim3((unsigned)G, (unsigned)((rows - 1) >> A.join_rows) + 1);
+    cfg.blockDim = dim3(PJ_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
