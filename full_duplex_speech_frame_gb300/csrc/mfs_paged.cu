@@ -203,13 +203,14 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 
 // --------------------------------------------------------------- attention
 //
-// The keys of every (sequence, kv head, block of GM query heads) are cut into tiles of 8 KB of keys and
-// values (16 positions of 128 bf16), and all tiles of the call, laid end to end, into equal shares, one
-// per warp of a grid that fills the GPU once: a warp walks through its share whatever sequences it
-// crosses, so ragged lengths and few long sequences load every SM alike.  An item (sequence, head block)
-// that lies in one share is finished by its warp.  The pieces of the others meet in shared memory once,
-// when the CTA's warps are done; what still crosses CTAs goes to the workspace (at most two pieces per
-// CTA) and a second kernel, whose launch overlaps the first one's run, joins it in share order.
+// The keys of every (sequence, kv head, block of GM query heads), an item, are cut into tiles of 8 KB of
+// keys and values (16 positions of 128 bf16).  All tiles of the call, laid end to end with a little room
+// at each item's start for what it costs beside them, are cut into equal shares, one per warp of a grid
+// that fills the GPU once: a warp walks through its share whatever sequences it crosses, so ragged lengths
+// and few long sequences load every SM alike.  An item that lies in one share is finished by its warp.
+// The pieces of the others meet in shared memory once, when the CTA's warps are done; what still crosses
+// CTAs goes to the workspace (at most two pieces per CTA) and a second kernel, whose launch overlaps the
+// first one's run, joins it in share order.
 //
 // A warp keeps its own running maximum, sum and output, so no warp waits for another before the end;
 // it feeds itself through a ring of stages with 16-byte asynchronous copies (rows past the length are
@@ -223,12 +224,12 @@ int append_typed(const Cache& C, int n_tokens, int n_seqs, const int32_t* cu, co
 // tensor pipe 17 % busy there, so the wide forms of them would gain nothing.
 
 constexpr int PA_WARPS = 4;
-constexpr int PA_MAX_CTAS = 304;                 // 2 per SM
+constexpr int PA_MAX_CTAS = 304;  // 2 per SM
 // What an item costs beside its tiles (its start, its end, its queries), in tiles: shares are cut over both.  64 ragged
 // sequences of up to 1000, 24 + 8 heads of 128: 44.3 us with 0, 35.7 with 1, 35.9 with 2, 35.6 with 4; 256 of up to 300,
 // 32 + 8 heads: 53.9, 44.0, 43.0, 44.3, fp32 139, 85, 81, 82; 64 of up to 100, 8 + 8 heads: 13.7, 12.7, 13.0, 14.1.
 constexpr int PA_ITEM = 2;
-constexpr int PA_STAGES = 2;                     // 16 KB per warp, 128 KB per SM: 3 stages measured 5 % slower on long contexts
+constexpr int PA_STAGES = 2;      // 16 KB per warp; 3 stages measured 5 % slower on long contexts
 
 // Query heads per block: the 16 rows of an mma tile for bf16.  fp32, on the CUDA cores, pays for every head of the
 // block, so it has three widths, 1, 4 and 8: 8 sequences of 8192, 8 kv heads of 128, groups of 1, 2, 4 and 8 take 88,
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             for (int i = tid; i < A.hq * HD; i += PA_WARPS * 32)
                 reinterpret_cast<T*>(A.out)[(long long)s * A.out_stride + i] = from_f<T>(0.f);
 
-    // the tiles of the call
+    // the tiles of the call, PA_ITEM more for each item
     auto tiles_of = [&](int s) {
         PaWalk w;
         w.s = s;
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         const long long t0 = muldiv(share, total, shares), t1 = muldiv(share + 1, total, shares);
         // where the share starts
         PaWalk use;
-        long long item_first = 0;  // the item's first tile
+        long long item_first = 0;  // where the item begins: PA_ITEM empty places, then its tiles
         for (int b = 0; b < A.n_seqs; b += 32) {
             const int s = b + lane;
             const long long v = s < A.n_seqs ? (long long)tiles_of(s) * Hx : 0;
@@ -666,8 +667,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             const long long x = end * shares - 1;
             return (int)((x >> 32 ? x / total : (unsigned)x / (unsigned)total) / PA_WARPS);
         };
-        long long at_load = at;  // of `load`: the loads run ahead of the products, across items
-        unsigned bad_ring = 0;  // bit i: the tile in stage i has a row without a valid page
+        long long at_load = at;  // the same of `load`: the loads run ahead of the products, across items
+        unsigned bad_ring = 0;   // bit i: the tile in stage i has a row without a valid page
         bool next_bad = false;
         long long off = at < t1 ? pa_offset<ROWS>(A, load, next_bad) : -1;
         auto issue = [&](int stage) {
