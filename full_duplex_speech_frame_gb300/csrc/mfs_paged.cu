@@ -232,8 +232,8 @@ constexpr int PA_ITEM = 2;
 constexpr int PA_STAGES = 2;      // 16 KB per warp; 3 stages measured 5 % slower on long contexts
 
 // Query heads per block: the 16 rows of an mma tile for bf16.  fp32, on the CUDA cores, pays for every head of the
-// block, so it has three widths, 1, 4 and 8: 8 sequences of 8192, 8 kv heads of 128, groups of 1, 2, 4 and 8 take 88,
-// 111, 114 and 167 us, with 8 alone 158, 159, 162 and 166 us (537 MB: 79 us at the measured copy rate).
+// block, so it has three widths, 1, 4 and 8: 8 sequences of 8192, 8 kv heads of 128, groups of 1, 2, 4 and 8 take 87,
+// 111, 113 and 167 us, with 8 alone 164, 164, 166 and 167 us (537 MB: 79 us at the measured copy rate).
 template <typename T>
 constexpr int PA_GM_MAX = sizeof(T) == 2 ? 16 : 8;
 
