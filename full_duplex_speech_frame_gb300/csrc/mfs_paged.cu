@@ -812,8 +812,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
 // Joins the pieces of the items that cross CTAs: a block per CTA that began one and one or two query heads, HD / 2
 // threads for each head and group of pieces, of which a group takes eight at a time, all on their way together.  Small
 // blocks, as they start while the last CTAs of the first kernel still hold their registers: 4 ragged contexts of up to
-// 1000, 32 + 8 heads of 128: 10.9 us (11.6 us by blocks of 512, 12.1 us by one block of 512 per head); one context of
-// 100000, 8 heads on one kv head, 34 us (31 us by blocks of 512).
+// 1000, 32 + 8 heads of 128: 10.9 us (11.6 us by blocks of 512).
 constexpr int PJ_THREADS = 256;
 
 template <typename T, int HD, int GM>
@@ -891,7 +890,10 @@ int attention(PaArgs A, char* workspace, cudaStream_t st)
     A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * GM);
     const int rows = A.g < GM ? A.g : GM;
-    A.join_rows = rows > 1 ? 1 : 0;
+    // two heads per block of the join, or one where the items are so few that each has over a dozen pieces: one context of
+    // 100000, 8 heads on one kv head: 28 us (34 us by two), one of 20000, 32 + 8 heads: 24.3 us (25.4 us); but 4 of up to
+    // 1000, 32 + 8 heads: 11.2 us (10.8 us by two)
+    A.join_rows = rows > 1 && (long long)A.n_seqs * A.C.n_kv_heads * A.nhb > 16 ? 1 : 0;
     int sms = 0;
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<T, HD, GM>, L::BYTES, &sms);

@@ -756,3 +756,31 @@ def test_prompt_attention_fp32_row_tiles(mfs, hq, hkv, hd, lens):
     """Few rows, many short sequences and many rows, so that row tiles of every size are chosen."""
     _check_prompt(mfs, np.random.default_rng(71), lens, hq, hkv, hd, "f32", rows=12)
     _check_prompt(mfs, np.random.default_rng(72), lens, hq, hkv, hd, "f32", window=37, rows=12)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,hd", [(2, 2, 128), (10, 2, 64), (24, 2, 128)])
+def test_paged_attention_of_tiny_and_long_sequences_together(mfs, hq, hkv, hd, dtype):
+    """Hundreds of sequences of one to three positions around a few long ones: shares that hold many items, one,
+    a part of one, or nothing."""
+    rng = np.random.default_rng(hq + hd)
+    lens = [1] * 400 + [0, 3001, 2, 0] + [3] * 300 + [700, 1, 0, 650]
+    check = [0, 1, 399, 400, 401, 402, 403, 404, 405, 555, 700, 703, 704, 705, 706, 707]
+    _check_decode(mfs, rng, lens, hq, hkv, hd, 16, dtype, check=check)
+    _check_decode(mfs, rng, [40] * 61 + [1], hq, hkv, hd, 16, dtype, window=33)
+
+
+@pytest.mark.parametrize("cols,dtype", [(16384, "f32"), (32000, "f32"), (40003, "bf16")])
+def test_sample_rows_many_long_rows(mfs, cols, dtype):
+    """More rows than half the SMs, each too long for half an SM's shared memory: one CTA to a row."""
+    rng = np.random.default_rng(cols + 1)
+    rows = 9 * len(SETTINGS)
+    x = _normal(rng, rows, cols + 1, dtype=dtype, scale=2.5)[:, 1:]
+    u = rng.random(rows).astype(np.float32)
+    t, k, p, m = (np.array([s[i] for s in SETTINGS] * 9) for i in range(4))
+    got = _sample(mfs, x, u, t, k, p, m)
+    xs = _np(x)
+    assert got.tolist() == [S.sample_row(xs[r], u[r], np.float32(t[r]), k[r], np.float32(p[r]), np.float32(m[r])) for r in range(rows)]
+    flat = _torch().from_numpy(rng.integers(-2, 2, (rows, cols)).astype(np.float32)).to(_dt(dtype)).cuda()
+    got, fs = _sample(mfs, flat, u, t, k, p, m), _np(flat)
+    assert got.tolist() == [S.sample_row(fs[r], u[r], np.float32(t[r]), k[r], np.float32(p[r]), np.float32(m[r])) for r in range(rows)]
