@@ -21,6 +21,9 @@
 // beside the tensor pipe, which is 70 % busy.  8192 tokens, 32 + 8 heads of 128:
 // 340 us = 1616 TFLOP/s, 0.85 of the measured matrix rate (353 us with two row tiles of one head); 12
 // packed prompts of the same total 75 us (95 us): short ones are bounded by the blocks' starts and ends.
+// Heads of 64 halve the products but not the softmax: 8192 tokens 269 us = 1023 TFLOP/s.  Their O leaves
+// columns to keep the weights apart from the scores, so that the next scores are made while the softmax of
+// these runs (294 us with the weights over the scores; 12 packed prompts 61 us against 60 us).
 //
 // Masked places: scores outside a row's range are replaced, not added to, so a NaN there is gone.  A
 // masked weight is 0, but 0 x NaN is not, so where a tile of keys is masked for some rows (the
@@ -60,7 +63,7 @@ struct __align__(16) PtWork {
 };
 
 struct PtBars {
-    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], v_ready[8], s_full[2], p_full[2], o_full[2], work_full[4], work_empty[4], drained;
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], v_ready[8], s_full[2], s_read[2], p_full[2], o_full[2], work_full[4], work_empty[4], drained;
     uint32_t tmem;
     int abort;          // a wait gave up
     int cleared[4];     // a non-finite value of V was cleared
@@ -384,6 +387,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                                                                    const __grid_constant__ PtArgs A)
 {
     using S = PtShape<HD>;
+    // heads of 64 leave columns for the weights beside the scores, which are then replaced while their softmax runs
+    constexpr bool APART = HD == 64 && PAIRED;
     extern __shared__ char pt_raw[];
     __shared__ PtBars B;
     char* base = (char*)(((uintptr_t)pt_raw + 1023) & ~(uintptr_t)1023);
@@ -401,6 +406,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             bar_init(&B.q_full[i], 1);
             bar_init(&B.q_empty[i], 1);
             bar_init(&B.s_full[i], 1);
+            bar_init(&B.s_read[i], PT_M);
             bar_init(&B.p_full[i], PT_M);
             bar_init(&B.o_full[i], 1);
         }
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, B.tmem, 0);  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
+    const uint32_t tm = __shfl_sync(0xffffffffu, B.tmem, 0);  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1, APART: P of each
     const int W = A.window;
 
     // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             };
             auto outputs = [&](int x, int slot, bool first) {
                 const uint64_t va = dv + (uint64_t)(slot * (S::TILE >> 4));
-                const uint32_t d = tm + 2 * PT_M + x * HD, pa = tm + x * PT_M;
+                const uint32_t d = tm + 2 * PT_M + x * HD, pa = tm + (APART ? 2 * (PT_M + HD) + x * (PT_M / 2) : x * PT_M);
                 if (leader) mma_ts(d, pa, va, id_o, !first);
 #pragma unroll
                 for (int k = 1; k < PT_M / 16; ++k)
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 if (leader) commit(bar);
             };
             int slot = 0;  // of the next tile of the ring
-            unsigned par = 0, v_at = 0, p_par[2] = {0, 0}, q_par[2] = {0, 0};
+            unsigned par = 0, v_at = 0, p_par[2] = {0, 0}, q_par[2] = {0, 0}, r_par = 0;
             auto step = [&]() {
                 if (++slot == S::STAGES) { slot = 0; par ^= 1; }
             };
@@ -539,14 +545,27 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     }
                     fresh = ends;
                     const int vs = slot;
-                    ok = bar_wait(&B.v_ready[v_at & 7], (v_at >> 3) & 1, &B.abort);  // loaded, and cleared where masked
-                    ++v_at;
                     step();
                     const int ks = slot;
                     if (have) {
-                        ok = ok && bar_wait(&B.kv_full[ks], par, &B.abort);
+                        ok = bar_wait(&B.kv_full[ks], par, &B.abort);
                         step();
                     }
+                    if constexpr (APART)
+                        if (have) {
+                            // the next scores as soon as these are in registers
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                ok = ok && bar_wait(&B.s_read[x], r_par, &B.abort);
+                                if (!ok) break;
+                                fence_after();
+                                ok = score_tile(x, ks, fresh, t + 1 == t1);
+                            }
+                            r_par ^= 1;
+                            signal(&B.kv_empty[ks]);
+                        }
+                    ok = ok && bar_wait(&B.v_ready[v_at & 7], (v_at >> 3) & 1, &B.abort);  // loaded, and cleared where masked
+                    ++v_at;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         ok = ok && bar_wait(&B.p_full[x], p_par[x], &B.abort);
@@ -554,11 +573,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                         p_par[x] ^= 1;
                         fence_after();
                         outputs(x, vs, was_fresh);
-                        if (ends) signal(&B.o_full[x]);
-                        if (have) ok = score_tile(x, ks, fresh, t + 1 == t1);
+                        if (ends || APART) signal(&B.o_full[x]);
+                        if (have && !APART) ok = score_tile(x, ks, fresh, t + 1 == t1);
                     }
                     signal(&B.kv_empty[vs]);
-                    if (have) signal(&B.kv_empty[ks]);
+                    if (have && !APART) signal(&B.kv_empty[ks]);
                     if (ends) done_with_item(B, i++);
                 }
             } else
@@ -698,8 +717,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
         const int x = warp >> 2, row = tid & (PT_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * PT_M, to = tm + lanes + 2 * PT_M + x * HD;
+        const uint32_t tp = APART ? tm + lanes + 2 * (PT_M + HD) + x * (PT_M / 2) : ts;
         unsigned s_par = 0, o_par = 0;
-        bool ok = true;
+        bool ok = true, summing = false;  // summing: APART, the last weights' product may still run
         for (int i = 0;; ++i) {
             int first, last, rr;  // rr: the row in its sequence
             {
@@ -721,12 +741,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) tld32(ts + 32 * k, s + 32 * k);
                 tld_wait();
+                if constexpr (APART) {
+                    fence_before();
+                    bar_arrive(&B.s_read[x]);
+                }
                 if (t == last - 1 || (W > 0 && PT_M * t < rr - row + PT_M - W)) {  // masked for some row
                     const int hi = rr - PT_M * t, lo = W > 0 ? hi - W + 1 : 0;
 #pragma unroll
                     for (int k = 0; k < PT_M; ++k)
                         if (k > hi || k < lo) s[k] = 0xff800000u;
                 }
+                auto summed = [&]() {  // O and the weights' place are free
+                    if (APART && summing) {
+                        ok = bar_wait(&B.o_full[x], o_par, &B.abort);
+                        o_par ^= 1;
+                        summing = false;
+                        __syncwarp();
+                        fence_after();
+                    }
+                    return ok;
+                };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < PT_M; k += 8)
@@ -738,6 +772,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 } else {
                     const bool up = mt > m && !((mt - m) * A.c <= 8.f);
                     if (__any_sync(0xffffffffu, up)) {
+                        if (!summed()) break;
                         const float a = !up ? 1.f : m == -INFINITY ? 0.f : ex2((m - mt) * A.c);
                         if (up) m = mt;
                         l2[0] = mul2(l2[0], pair(a, a));
@@ -768,8 +803,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                         l2[k & 1] = add2(l2[k & 1], pair(u, w));
                         p[k] = pack_bf16(u, w);
                     }
-                    tst16(ts + 16 * quarter, p);
+                    if (quarter == 0 && !summed()) break;
+                    tst16(tp + 16 * quarter, p);
                 }
+                if (!ok) break;
+                summing = APART;
                 tst_wait();
                 fence_before();
                 bar_arrive(&B.p_full[x]);
@@ -777,6 +815,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             if (last > first) {
                 if (ok) ok = bar_wait(&B.o_full[x], o_par, &B.abort);
                 o_par ^= 1;
+                summing = false;
                 __syncwarp();
                 fence_after();
                 float l0, l1;
