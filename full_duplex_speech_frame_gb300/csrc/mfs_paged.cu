@@ -424,10 +424,11 @@ struct PaBf16 {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             m[h] = mn[h];
+            const float sub = mn[h] == -INFINITY ? 0.f : mn[h];  // scores of -infinity alone so far: weights 0, not NaN
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < NK; ++n) {
-                const float a = exp2f((s[n][2 * h] - mn[h]) * c), b = exp2f((s[n][2 * h + 1] - mn[h]) * c);
+                const float a = exp2f((s[n][2 * h] - sub) * c), b = exp2f((s[n][2 * h + 1] - sub) * c);
                 sum += a + b;
                 p[n / 2][2 * (n & 1) + h] = pack_bf16(a, b);
             }
@@ -519,7 +520,7 @@ struct PaF32 {
             for (int x = ROWS / 2; x; x >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
             const float mn = fmaxf(m[h], v), sc = m[h] == mn ? 1.f : exp2f((m[h] - mn) * c);
             m[h] = mn;
-            p[h] = exp2f((s[h] - mn) * c);
+            p[h] = exp2f((s[h] - (mn == -INFINITY ? 0.f : mn)) * c);  // scores of -infinity alone so far: weights 0, not NaN
             l[h] = l[h] * sc + (part == 0 ? p[h] : 0.f);
 #pragma unroll
             for (int e = 0; e < E; ++e) o[h][e] *= sc;

@@ -454,6 +454,7 @@ int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int
  *   workspace device memory of mfs_paged_attention_workspace() bytes, 16-byte
  *            aligned, its contents need not be kept or set between calls.  Calls whose work
  *            can overlap on the GPU (other streams, two captured graphs) need one each.
+ * A score of -infinity is a weight of 0; a sequence that has no other gives NaN.
  * Rows of the cache at or past L, or before the window, are not read.  Sums and
  * softmax statistics are fp32; with a bf16 cache the softmax weights are rounded
  * to bf16 for the product with the values.  Enqueues and returns; MFS_E_ARG on

@@ -784,3 +784,43 @@ def test_sample_rows_many_long_rows(mfs, cols, dtype):
     flat = _torch().from_numpy(rng.integers(-2, 2, (rows, cols)).astype(np.float32)).to(_dt(dtype)).cuda()
     got, fs = _sample(mfs, flat, u, t, k, p, m), _np(flat)
     assert got.tolist() == [S.sample_row(fs[r], u[r], np.float32(t[r]), k[r], np.float32(p[r]), np.float32(m[r])) for r in range(rows)]
+
+
+@pytest.mark.parametrize("how", ["infinite", "overflowing"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 4, 64), (8, 2, 128), (6, 2, 64), (3, 1, 128), (40, 2, 64)])
+def test_paged_attention_scores_of_minus_infinity(mfs, hq, hkv, hd, dtype, how):
+    """Keys whose score is -infinity (an infinite element, or products past the largest fp32) weigh nothing, wherever they
+    lie in their tile, share or sequence; a sequence that has no other keys gives NaN.  The same alone and in a batch."""
+    torch = _torch()
+    rng = np.random.default_rng(51 + hq + hd)
+    page, big = 16, 1e20
+    where = [(1, [0]), (17, [16]), (33, [32]), (40, range(32)), (65, range(64)), (300, range(299)), (300, range(1, 300)), (50, range(50)),
+             (3001, range(2990)), (3001, range(100, 3001)), (3001, [0, 1500, 3000]), (3001, range(3001)), (20, [])]
+    lens = [n for n, _ in where]
+    table, pages = _table(rng, lens, page)
+    kc, vc = _pool(rng, pages, hkv, page, hd, dtype)
+    q = _normal(rng, len(lens), hq, hd, dtype=dtype)
+    q[:, :, 5] = big if how == "overflowing" else q[:, :, 5].abs() + 0.125
+    if how == "overflowing":
+        kc[:, :, :, 5] = 0
+    for s, (_, gone) in enumerate(where):
+        for p in gone:
+            kc[table[s, p // page], :, p % page, 5] = -big if how == "overflowing" else -np.inf
+    cache = mfs.PagedKV(kc, vc, torch.from_numpy(table).cuda())
+    out, k, v, qn = torch.empty_like(q), _np(kc), _np(vc), _np(q)
+    mfs.mfs_paged_attention(cache, q, _i32(lens), out)
+    alone = torch.empty_like(q)
+    for s, n in enumerate(lens):
+        mfs.mfs_paged_attention(mfs.PagedKV(kc, vc, cache.table[s:s + 1]), q[s:s + 1], _i32([n]), alone[s:s + 1])
+    for s, (n, gone) in enumerate(where):
+        seen = sorted(set(range(n)) - set(gone))
+        rows_k, rows_v = S.kv_rows(k, table[s], page, 0, n)[seen], S.kv_rows(v, table[s], page, 0, n)[seen]
+        for got in (_np(out[s]), _np(alone[s])):
+            if not seen:
+                assert np.isnan(got).all(), (s, n)
+                continue
+            for h in range(hq):
+                ref, weighted, size = S.attend(qn[s, h], rows_k[:, h * hkv // hq], rows_v[:, h * hkv // hq], hd ** -0.5)
+                tol = S.attention_tolerance(ref, weighted, size, n, hd, dtype == "bf16")
+                assert (np.abs(got[h] - ref) <= tol).all(), (s, n, h)
