@@ -526,7 +526,9 @@ def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, wo
         if stream is None:
             workspace = mfs_paged_attention_workspace(cache, hq)
         else:  # from the pool of the stream that uses it, so that it is not handed out again too early
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=cache.device)):
+            # (ExternalStream takes the null stream's handle for none given)
+            own = torch.cuda.ExternalStream(stream, device=cache.device) if stream else torch.cuda.default_stream(cache.device)
+            with torch.cuda.stream(own):
                 workspace = mfs_paged_attention_workspace(cache, hq)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse("workspace: need a contiguous tensor on the cache's device")

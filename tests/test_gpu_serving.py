@@ -824,3 +824,23 @@ def test_paged_attention_scores_of_minus_infinity(mfs, hq, hkv, hd, dtype, how):
                 ref, weighted, size = S.attend(qn[s, h], rows_k[:, h * hkv // hq], rows_v[:, h * hkv // hq], hd ** -0.5)
                 tol = S.attention_tolerance(ref, weighted, size, n, hd, dtype == "bf16")
                 assert (np.abs(got[h] - ref) <= tol).all(), (s, n, h)
+
+
+def test_default_workspace_on_the_null_stream(mfs):
+    """stream=0 with no workspace, beside other streams that allocate and write: each call has its own results."""
+    torch = _torch()
+    rng = np.random.default_rng(52)
+    cache = mfs.PagedKV(*_pool(rng, 300, 2, 16, 128, "bf16"), torch.arange(300, dtype=torch.int32, device="cuda")[None])
+    q, kv = _normal(rng, 1, 8, 128, dtype="bf16"), _i32([4800])
+    want, others = torch.empty_like(q), [torch.cuda.Stream() for _ in range(33)]
+    mfs.mfs_paged_attention(cache, q, kv, want)
+    size = mfs.mfs_paged_attention_workspace(cache, 8).numel()
+    torch.cuda.synchronize()
+    outs = [torch.zeros_like(q) for _ in others]
+    torch.cuda.synchronize()
+    for out, side in zip(outs, others):
+        mfs.mfs_paged_attention(cache, q, kv, out, stream=0)
+        with torch.cuda.stream(side):
+            torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)

@@ -158,3 +158,35 @@ def test_sampling_definition_by_hand():
     assert S.sample_row(x, 0.0, t, min_p=0.6) == 2 and S.sample_row(x, 0.0, t, min_p=0.4) == 0
     assert S.sample_row([np.nan, np.nan], 0.3) == 0 and S.sample_row([np.nan, -np.inf], 0.3) == 1
     assert S.sample_row([0.0, np.inf, np.inf], 0.6) == 2
+
+
+@pytest.mark.parametrize("stream,owner", [(None, "current"), (0, "default of dev"), (77, "external 77 on dev")])
+def test_default_workspace_is_of_the_stream_that_runs(mfs, monkeypatch, stream, owner):
+    """A workspace made for a call comes from the pool of the call's stream, the null stream's among them: torch takes a
+    null handle given to ExternalStream for none and hands out another stream."""
+    import contextlib
+    import types
+
+    import torch
+    now, made, ran = ["current"], [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"external {handle} on {device}")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: f"default of {device}")
+
+    def workspace(cache, heads):
+        made.append(now[-1])
+        return torch.empty(16, dtype=torch.uint8)
+
+    monkeypatch.setattr(mfs, "mfs_paged_attention_workspace", workspace)
+    monkeypatch.setattr(mfs, "_enqueue", lambda dev, stream, fn, *args: ran.append(stream))
+    cache = types.SimpleNamespace(_is=(-1, torch.float32, 2, 64), n_seqs=3, device="dev", c=None)
+    q = torch.zeros(3, 4, 64)
+    mfs.mfs_paged_attention(cache, q, torch.ones(3, dtype=torch.int32), torch.empty_like(q), stream=stream)
+    assert made == [owner] and ran == [stream] and now == ["current"]
