@@ -844,3 +844,41 @@ def test_default_workspace_on_the_null_stream(mfs):
             torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255)
     torch.cuda.synchronize()
     assert all(torch.equal(out, want) for out in outs)
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (8, 2), (6, 2), (10, 2)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_prompt_attention_bad_values_among_grouped_heads(mfs, bad, hd, hq, hkv):
+    """A NaN or infinite value reaches exactly the rows of its kv head's query heads that see it, in its own column, and
+    as itself; every other element is what it is without it."""
+    torch = _torch()
+    rng = np.random.default_rng(35)
+    lens, g = [200, 450, 300], hq // hkv
+    n = sum(lens)
+    q, k, v = (_normal(rng, n, h, hd, dtype="bf16") for h in (hq, hkv, hkv))
+    cu = _i32(np.cumsum([0] + lens).tolist())
+    qn, kn, vn = _np(q), _np(k), _np(v)
+    for w in (0, 150):
+        clean, got, again = (torch.empty_like(q) for _ in range(3))
+        mfs.mfs_prompt_attention(q, k, v, cu, clean, window=w)
+        for at in (200 + 170, 200 + 3, 200 + 449):  # inside the second sequence, near its start, its last token
+            vv = v.clone()
+            vv[at, 1, 5] = bad
+            mfs.mfs_prompt_attention(q, k, vv, cu, got, window=w)
+            mfs.mfs_prompt_attention(q, k, vv, cu, again, window=w)
+            assert torch.equal(got.view(torch.int16), again.view(torch.int16))
+            end = min(650, at + w) if w else 650
+            touched = torch.zeros(n, dtype=torch.bool)
+            touched[at:end] = True
+            assert torch.equal(got[:, :g], clean[:, :g]) and torch.equal(got[~touched], clean[~touched])
+            column = _np(got[at:end, g:, 5])
+            assert np.isnan(column).all() if bad != bad else (column == bad).all()
+            for i in {at, at + 1, (at + end) // 2, end - 1} - {650}:
+                lo = max(200, i - w + 1) if w else 200
+                for h in range(g, hq):
+                    ref, weighted, size = S.attend(qn[i, h], kn[lo:i + 1, 1], vn[lo:i + 1, 1], hd ** -0.5)
+                    tol = S.attention_tolerance(ref, weighted, size, i + 1 - lo, hd, True)
+                    off = np.abs(_np(got[i, h]) - ref) <= tol
+                    off[5] = True
+                    assert off.all(), (at, i, h)
