@@ -28,8 +28,8 @@
 // Masked places: scores outside a row's range are replaced, not added to, so a NaN there is gone.  A
 // masked weight is 0, but 0 x NaN is not, so where a tile of keys is masked for some rows (the
 // diagonal, the end of a sequence, a window's edge), a warp clears the non-finite values of V in
-// shared memory before the product; rows that do see one of them (it lies in their range) are
-// computed again at the end by a plain pass in fp32.
+// shared memory before the product; the rows that do see one of them (it lies in their range) get it
+// added to their outputs at the end.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -223,29 +223,10 @@ struct PtArgs {
     float c;           // scale * log2(e)
 };
 
-// Row t (token) of head h again, by the warp: the running maximum and sum over keys lo .. t.
-template <int HD>
-__device__ __noinline__ void plain_row(const PtArgs& A, int t, int h, int lo)
+// s plus the products of two pairs of bf16
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s)
 {
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    float qf[E], o[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        qf[e] = to_f(A.q[(long long)t * A.q_stride + h * HD + lane * E + e]);
-        o[e] = 0.f;
-    }
-    for (int j = lo; j <= t; ++j) {
-        const bf16* kr = A.k + (long long)j * A.k_stride + (h / A.g) * HD + lane * E;
-        const bf16* vr = A.v + (long long)j * A.v_stride + (h / A.g) * HD + lane * E;
-        float a = 0.f;
-        for (int e = 0; e < E; ++e) a = fmaf(qf[e], to_f(kr[e]), a);
-        for (int x = 16; x; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-        const float mn = fmaxf(m, a), cc = m == mn ? 1.f : exp2f((m - mn) * A.c), p = a == mn ? 1.f : exp2f((a - mn) * A.c);
-        l = l * cc + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * cc + p * to_f(vr[e]);
-        m = mn;
-    }
-    for (int e = 0; e < E; ++e) put(A.out + (long long)t * A.out_stride + h * HD + lane * E + e, o[e] / l);
+    return fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), fmaf(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), s));
 }
 
 __device__ __forceinline__ bool not_finite2(uint32_t x) { return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u; }
@@ -354,26 +335,53 @@ struct PtDealer {
     }
 };
 
-// A warp's 32 rows of block i, tile x: those that see a value that was cleared are computed again.
+// A warp's 32 rows of block i, tile x, one per lane, whose outputs are written: adds the non-finite values that were cleared
+// to the rows that see them, each in its own column, or NaN where the key's weight is 0.  m: the row's maximum in use.  Only
+// tiles of keys that some row does not see whole were cleared (the last ones, and the window's first), so this takes the same
+// time however long the prompt is: some microseconds for each key with such a value.
 template <int HD>
-__device__ __noinline__ void again(const PtArgs& A, PtBars& B, int i, int x, int quarter)
+__device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int x, int quarter, float m)
 {
     PtItem I;
     const int W = A.window, lane = threadIdx.x & 31;
     if (!next_item(B, i, A, I)) return;  // published long ago
-    const int r1 = I.r0 + x * A.down + 32 * quarter, h = I.h + x * A.across;
-    for (int r = r1; r < min(I.len, r1 + 32); ++r) {
-        const int lo = W > 0 ? max(0, r - W + 1) : 0;
-        bool sees = false;
-        for (int t = max(I.t0, lo / PT_M); t <= r / PT_M && !sees; ++t) {
-            if (!I.edge(t)) continue;
-            for (int j = max(lo, t * PT_M); j <= min(r, t * PT_M + PT_M - 1); ++j) {
-                const uint32_t* p = reinterpret_cast<const uint32_t*>(A.v + (long long)(I.b + j) * A.v_stride + h / A.g * HD);
-                for (int e = lane; e < HD / 2; e += 32) sees = sees || not_finite2(__ldg(p + e));
+    const int r1 = I.r0 + x * A.down + 32 * quarter, r = r1 + lane, h = I.h + x * A.across;
+    if (r1 >= I.len) return;
+    const bool row = r < I.len;
+    const int lo = W > 0 ? max(0, r - W + 1) : 0;
+    const int from = W > 0 ? max(0, r1 - W + 1) : 0, upto = min(I.len, r1 + 32) - 1;  // the keys that the warp's rows see
+    const float base_ = m == -INFINITY ? 0.f : -m * A.c;
+    const uint4* q = reinterpret_cast<const uint4*>(A.q + (long long)(I.b + (row ? r : r1)) * A.q_stride + h * HD);
+    bf16* o = A.out + (long long)(I.b + (row ? r : r1)) * A.out_stride + h * HD;
+    for (int t = from / PT_M; t <= upto / PT_M; ++t) {
+        if (!I.edge(t)) continue;
+        for (int j = max(from, t * PT_M); j <= min(upto, t * PT_M + PT_M - 1); ++j) {
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(A.v + (long long)(I.b + j) * A.v_stride + h / A.g * HD);
+            uint32_t y[HD / 64], bad[HD / 64], any = 0;
+#pragma unroll
+            for (int e = 0; e < HD / 64; ++e) {
+                y[e] = __ldg(v + 32 * e + lane);
+                bad[e] = __ballot_sync(0xffffffffu, not_finite2(y[e]));
+                any |= bad[e];
             }
-            sees = __any_sync(0xffffffffu, sees);
+            if (!any) continue;
+            const uint4* k = reinterpret_cast<const uint4*>(A.k + (long long)(I.b + j) * A.k_stride + h / A.g * HD);
+            float s = 0.f;
+            for (int e = 0; e < HD / 8; ++e) {
+                const uint4 a = __ldg(q + e), b = __ldg(k + e);
+                s = dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, s))));
+            }
+            const bool sees = row && j >= lo && j <= r, weighs = ex2(fmaf(s, A.c, base_)) > 0.f;
+#pragma unroll
+            for (int e = 0; e < HD / 64; ++e)
+                for (unsigned u = bad[e]; u; u &= u - 1) {
+                    const int at = __ffs(u) - 1;
+                    const uint32_t z = __shfl_sync(0xffffffffu, y[e], at);
+                    bf16* p = o + 2 * (32 * e + at);
+                    if (sees && (z & 0x7f80u) == 0x7f80u) put(p, to_f(*p) + (weighs ? __uint_as_float(z << 16) : NAN));
+                    if (sees && (z & 0x7f800000u) == 0x7f800000u) put(p + 1, to_f(p[1]) + (weighs ? __uint_as_float(z & 0xffff0000u) : NAN));
+                }
         }
-        if (sees) plain_row<HD>(A, I.b + r, h, I.b + lo);
     }
 }
 
@@ -858,7 +866,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 fence_before();
                 if (*(volatile int*)&B.cleared[i & 3] && ok) {
                     __syncwarp();
-                    again<HD>(A, B, i, x, warp & 3);
+                    put_cleared<HD>(A, B, i, x, warp & 3, m);
                 }
             }
             done_with_item(B, i);

@@ -882,3 +882,65 @@ def test_prompt_attention_bad_values_among_grouped_heads(mfs, bad, hd, hq, hkv):
                     off = np.abs(_np(got[i, h]) - ref) <= tol
                     off[5] = True
                     assert off.all(), (at, i, h)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,dtype", [(2, 2, 64, "bf16"), (2, 2, 128, "bf16"), (4, 2, 128, "bf16"), (8, 2, 64, "bf16"), (3, 1, 64, "f32")])
+def test_prompt_attention_infinite_scores_beside_bad_values(mfs, hq, hkv, hd, dtype):
+    """An infinite key next to an infinite value: rows whose score is +infinity there are NaN, rows whose score is
+    -infinity do not see that key, and have the infinity in the value's column."""
+    torch = _torch()
+    rng = np.random.default_rng(36)
+    n, at, g, b = 330, 140, hq // hkv, hkv - 1
+    q, k, v = (_normal(rng, n, h, hd, dtype=dtype) for h in (hq, hkv, hkv))
+    k[at + 3, b, 5] = float("inf")
+    v[at, b, 7] = float("inf")
+    k[0, b, 9] = float("-inf")  # and a first key that some rows do not see
+    out = torch.empty_like(q)
+    mfs.mfs_prompt_attention(q, k, v, _i32([0, n]), out)
+    qn, kn, vn, got = _np(q), _np(k), _np(v), _np(out)
+    vn[at, b, 7] = 0
+    for i in (at - 1, at, at + 2, at + 3, at + 4, at + 20, 255, 256, n - 1):
+        for h in range(b * g, hq):
+            plus = qn[i, h, 9] < 0 or (i >= at + 3 and qn[i, h, 5] > 0)
+            if plus:
+                assert np.isnan(got[i, h]).all(), (i, h)
+                continue
+            keys = [j for j in range(1, i + 1) if j != at + 3]
+            ref, weighted, size = S.attend(qn[i, h], kn[keys, b], vn[keys, b], hd ** -0.5)
+            off = np.abs(got[i, h] - ref) <= S.attention_tolerance(ref, weighted, size, i + 1, hd, dtype == "bf16")
+            if i >= at:
+                assert got[i, h, 7] == np.inf
+                off[7] = True
+            assert off.all(), (i, h)
+    # rows that see nothing but keys of score -infinity
+    q, k = torch.ones_like(q), torch.ones_like(k)
+    k[:129, :, 3] = float("-inf")
+    mfs.mfs_prompt_attention(q, k, v, _i32([0, n]), out)
+    got = _np(out)
+    assert np.isnan(got[:129]).all() and np.isfinite(got[129:, 0, 8]).all() and (got[at:, hq - 1, 7] == np.inf).all()
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(2, 1, 64), (1, 1, 128)])
+def test_prompt_attention_bad_values_cost_no_pass_over_the_prompt(mfs, hq, hkv, hd):
+    """What rows that see a bad value take besides does not grow with the prompt."""
+    torch = _torch()
+    rng = np.random.default_rng(37)
+    n = 16384
+    q, k, v = (_normal(rng, n, h, hd, dtype="bf16") for h in (hq, hkv, hkv))
+    cu, clean, got = _i32([0, n]), torch.empty_like(q), torch.empty_like(q)
+
+    def milliseconds(values, out):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        mfs.mfs_prompt_attention(q, k, values, cu, out)
+        a.record()
+        mfs.mfs_prompt_attention(q, k, values, cu, out)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    fast = milliseconds(v, clean)
+    v[n - 120, 0, 3] = float("nan")
+    slow = milliseconds(v, got)
+    assert torch.equal(got[:n - 120], clean[:n - 120]) and torch.isnan(got[n - 120:, :, 3]).all()
+    # keys of the last 128-row tile by 32 rows a warp, some microseconds each: a millisecond; 32 passes over all keys take a hundred
+    assert slow <= 2 * fast + 10, (fast, slow)
