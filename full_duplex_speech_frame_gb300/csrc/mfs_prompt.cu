@@ -47,7 +47,15 @@ __device__ __forceinline__ void put(bf16* p, float x) { *p = __float2bfloat16_rn
 constexpr int PT_M = 128;                    // query rows per tile, keys per tile
 // warps 0-3, 4-7: softmax of the two tiles; 8: MMA; 9: TMA; 10, 11: V of masked tiles (11 also the next block)
 constexpr int PT_THREADS = 384;
-constexpr unsigned long long PT_WAIT_NS = 2000000000ull;
+// A test build may shorten the waits' limit, and have every CTA lose one tile of its ring (never ask for it), so that they
+// run out.
+#ifndef MFS_PROMPT_WAIT_NS
+#define MFS_PROMPT_WAIT_NS 2000000000ull
+#endif
+#ifndef MFS_PROMPT_LOST_TILE
+#define MFS_PROMPT_LOST_TILE -1
+#endif
+constexpr unsigned long long PT_WAIT_NS = MFS_PROMPT_WAIT_NS;
 
 template <int HD>
 struct PtShape {
@@ -98,23 +106,25 @@ __device__ __forceinline__ unsigned long long gtime()
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Waits for the phase of parity `par`; false if it took too long or another wait of the CTA gave up.
+// Waits, for a whole warp, for the phase of parity `par`; false if it took too long or another wait of the CTA gave up.
+// The lanes leave together, with the same answer: what follows exchanges registers and uses tensor memory.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned par, int* abort)
 {
     unsigned long long t0 = 0;
     for (unsigned n = 1;; ++n) {
-        if (bar_try(b, par)) return true;
+        if (__all_sync(0xffffffffu, bar_try(b, par))) return true;
         if (n & 63u) continue;
-        if (*(volatile int*)abort) return false;
         const unsigned long long t = gtime();
-        if (t0 == 0) {
-            t0 = t;
-        } else if (t - t0 > PT_WAIT_NS) {
+        if (t0 == 0) t0 = t;
+        if (__any_sync(0xffffffffu, *(volatile int*)abort || t - t0 > PT_WAIT_NS)) {
             *(volatile int*)abort = 1;
+            __threadfence_block();
             return false;
         }
     }
 }
+// Has a wait of the CTA given up?  For a whole warp.
+__device__ __forceinline__ bool gave_up(PtBars& B) { return __any_sync(0xffffffffu, *(volatile int*)&B.abort); }
 __device__ __forceinline__ void bar_drain(uint64_t* b, unsigned par)
 {
     const unsigned long long t0 = gtime();
@@ -457,9 +467,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             int n = 0, slot = 0;               // tiles asked for
             unsigned par = 1, q_par[2] = {1, 1};
             bool ok = true, q_used[2] = {false, false};
+            // After a wait that gave up nothing more is asked for: the issuing warp may then free a place of the ring whose tile
+            // is still on its way (a test for that there, where it would be made first, takes 5 % of a long prompt's time).
             for (int i = 0; ok && next_item(B, i, A, I); ++i) {
                 auto query = [&](int x) {
-                    if (!bar_wait(&B.q_empty[x], q_par[x], &B.abort)) return false;
+                    if (!bar_wait(&B.q_empty[x], q_par[x], &B.abort) || gave_up(B)) return false;
                     if (lane == 0) load(&mq, sq + x * S::TILE, I.h + A.across * x, I.b + I.r0 + A.down * x, &B.q_full[x]);
                     q_par[x] ^= 1;
                     q_used[x] = true;
@@ -468,9 +480,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 ok = query(0);
                 for (int t = I.t0; t < I.t1 && ok; ++t)
                     for (int kv = 0; kv < 2 && ok; ++kv) {
-                        ok = bar_wait(&B.kv_empty[slot], par, &B.abort);
+                        ok = bar_wait(&B.kv_empty[slot], par, &B.abort) && !gave_up(B);
                         if (!ok) break;
-                        if (lane == 0) load(kv ? &mv : &mk, ring + slot * S::TILE, I.h / A.g, I.b + t * PT_M, &B.kv_full[slot]);
+                        if (lane == 0 && n != MFS_PROMPT_LOST_TILE) load(kv ? &mv : &mk, ring + slot * S::TILE, I.h / A.g, I.b + t * PT_M, &B.kv_full[slot]);
                         __syncwarp();
                         ++n;
                         if (++slot == S::STAGES) { slot = 0; par ^= 1; }
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     }
                 done_with_item(B, i);
             }
-            if (*(volatile int*)&B.abort && lane == 0) {  // the copies in flight
+            if (lane == 0) {  // no copy is in flight when the CTA ends, whichever warp gave up
                 for (int x = 0; x < 2; ++x)
                     if (q_used[x]) bar_drain(&B.q_full[x], q_par[x]);
                 for (int k = max(0, n - S::STAGES); k < n; ++k) bar_drain(&B.kv_full[k % S::STAGES], (k / S::STAGES) & 1);
