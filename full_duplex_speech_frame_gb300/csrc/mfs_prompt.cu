@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
             // half a tile each: non-finite values become 0.  Every tile is waited for and passed on.
             PtItem I;
             PtWork w;
+            int next = 0;  // blocks published
             int slot = 1 % S::STAGES;
             unsigned par = 0, v_at = 0;
             bool ok = true, more = warp == 11;
@@ -674,6 +675,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                     bar_arrive(&B.work_full[i & 3]);
                 }
                 __syncwarp();
+                next = i + 1;
                 return true;
             };
             int i = 0;
@@ -722,15 +724,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
                 }
                 done_with_item(B, i);
             }
-            if (*(volatile int*)&B.abort)
-                // given up: NaN for the blocks that nobody will compute
-                for (++i; more; ++i) {
+            if (!ok && warp == 11)
+                // given up: NaN for the blocks that nobody will compute; those published are the softmax warps' to write
+                for (; deal.get(next, w); ++next)
                     for (int r = w.r0; r < min(w.len, w.r0 + PT_M + A.down); ++r)
                         for (int e = lane; e < HD << A.across; e += 32)
-                            A.out[(long long)(w.b + r) * A.out_stride + w.h * HD + e] = __float2bfloat16_rn(NAN);
-                    more = deal.get(i + 1, w);
-                    w.h <<= A.across;
-                }
+                            A.out[(long long)(w.b + r) * A.out_stride + (w.h << A.across) * HD + e] = __float2bfloat16_rn(NAN);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");

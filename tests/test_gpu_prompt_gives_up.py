@@ -71,3 +71,16 @@ def test_rows_that_miss_a_tile_are_nan(mfs, losing, lost, hq, hkv, hd):  # noqa:
                 assert right, (r0, h)
             else:
                 assert nan or right, (r0, h)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,lens", [(32, 16, 64, [300] * 20), (64, 32, 128, [130, 1, 260] * 8), (27, 9, 128, [300, 520] * 9), (16, 16, 64, [40] * 300)])
+@pytest.mark.parametrize("lost", [0, 3, 10])
+def test_no_row_is_left_as_it_was(mfs, losing, lost, hq, hkv, hd, lens):  # noqa: F811
+    """Several blocks to a CTA, waiting, dealt out or not yet: each row and head is right or NaN, and with the first tile lost
+    every one is NaN."""
+    torch = _torch()
+    out, want = _run(mfs, losing, lost, lens, hq, hkv, hd)
+    nan, right = torch.isnan(out).all(-1), (out == want).all(-1)
+    assert (nan | right).all() and nan.any()
+    if lost == 0:
+        assert nan.all()
