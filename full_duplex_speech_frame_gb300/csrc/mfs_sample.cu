@@ -34,7 +34,8 @@
 // from r's, the table's in fp32 and the product's, 2^-34.7 from the terms left out).
 // Each comparison of sums is made with a bound on that error, and a row in which one
 // falls inside the bound is done again with exponentials of about 2^-40 relative
-// error (pairs of fp32), which decides it.  64-bit floating point, two products a
+// error (pairs of fp32), in units fitted to the row's sum, 2^-61 of it or less (a
+// list's: fitted to its length), which decides it.  64-bit floating point, two products a
 // cycle and SM here, is kept to one thread per CTA; fractions of sums are taken in
 // 128-bit integers.
 #include <cooperative_groups.h>
@@ -850,10 +851,10 @@ __device__ Border find_border(Row<T, NT>& R, float least, u64 target, u64 band)
     return B;
 }
 
-// The token of the row into `token` by the CTA that finds it, for rows whose candidates are not listed.  False if an
-// error bound left a choice open (never with precise weights).
+// The token of the row into `token` by the CTA that finds it, for rows whose candidates are not listed; all: the sum of
+// their weights before top-p.  False if an error bound left a choice open (never with precise weights).
 template <int NT, typename T>
-__device__ __forceinline__ bool sample_row(Row<T, NT>& R, int top_k, float top_p, float u, int32_t* token)
+__device__ __forceinline__ bool sample_row(Row<T, NT>& R, int top_k, float top_p, float u, int32_t* token, u64& all)
 {
     SrShared<NT>* S = R.S;
     const int tid = threadIdx.x;
@@ -886,6 +887,7 @@ __device__ __forceinline__ bool sample_row(Row<T, NT>& R, int top_k, float top_p
             for (int r = 0; r < R.C; ++r) rest += S->r_sum[r];
         }
         const u64 total = block_sum(S, S->sum, SR_NB) + rest;
+        all = total;
         const Border Q = find_border<true>(R, shallow, max((u64)1, fraction(top_p, total, true)), R.band(total));
         if (!(Q.tau == B.tau && Q.tie > B.tie)) B = Q;
     }
@@ -906,6 +908,7 @@ __device__ __forceinline__ bool sample_row(Row<T, NT>& R, int top_k, float top_p
             for (int r = 0; r < R.C; ++r) R.of(r)->unsure = 1;
         *token = S->where;
     }
+    if (!(top_p < 1.f)) all = total;
     R.sync();
     const bool open = S->unsure != 0;
     __syncthreads();  // read by all before another pass clears it
@@ -1055,6 +1058,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const T* __r
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
                     R.W.precise = pass != 0;
+                    if (pass) R.W.scale = 62 - (32 - __clz(n));
                     if (sample_list(R, n, k, pp, u, tokens + r)) break;
                 }
             }
@@ -1063,11 +1067,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const T* __r
         R.lmin = least;
     }
     const int noted = R.noted;
+    u64 all = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         R.W.precise = pass != 0;
-        if (sample_row(R, k, pp, u, tokens + r)) break;
+        if (sample_row(R, k, pp, u, tokens + r, all)) break;
         R.noted = noted;  // not those of the first pass's border
+        // as many bits more as the sum (and what it may be off) leaves below 2^62, so that a unit is at most 2^-61 of it
+        R.W.scale += __clzll(all + (all >> 26) + 2ull * cols + 2) - 2;
     }
 }
 

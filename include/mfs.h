@@ -372,7 +372,7 @@ int mfs_argmax_rows_noalloc(const float* logits, int rows, int cols, long long l
  *     running sum of weights exceeds uniforms[r] times their sum (a uniform below
  *     0 or NaN acts as 0, one of 1 or more takes the last candidate).
  * Weights and sums are exact enough that the token is the one that the
- * definition gives in real numbers, unless a sum lies within 2^-40 + cols^2 2^-63
+ * definition gives in real numbers, unless a sum lies within 2^-40 + cols 2^-60
  * of the total from a border.  The same inputs always give the same tokens.
  * Enqueues on `stream` and returns; no memory is allocated, so it can be captured.
  * MFS_E_ARG on bad sizes or NULL pointers, before anything is enqueued. */

@@ -944,3 +944,30 @@ def test_prompt_attention_bad_values_cost_no_pass_over_the_prompt(mfs, hq, hkv, 
     assert torch.equal(got[:n - 120], clean[:n - 120]) and torch.isnan(got[n - 120:, :, 3]).all()
     # keys of the last 128-row tile by 32 rows a warp, some microseconds each: a millisecond; 32 passes over all keys take a hundred
     assert slow <= 2 * fast + 10, (fast, slow)
+
+
+def test_sample_rows_of_the_most_columns_with_a_light_tail(mfs):
+    """One column outweighs 4194303 others of 0.49 2^-39 of it each, 3.7e-6 of the total together: the draw and the border of
+    top-p fall into the tail at the place that the definition gives, to the stated distance in weight."""
+    import math
+    from fractions import Fraction as F
+    cols = 1 << 22
+    tail = np.float32(math.log(0.49) - 39 * math.log(2))
+    w, n = F(math.exp(float(tail))), cols - 1
+    far = [1.0 - j * 2.0 ** -24 for j in (1, 7, 20, 30, 41, 55, 60)]  # fp32 numbers; 62 of these steps are the tail
+    x = np.full(cols, tail, np.float32)
+    x[0] = 0
+    # a border may be missed by (2^-40 + cols 2^-60) of the total; each column weighs w, and a rounding of the place down
+    miss = (2.0 ** -40 + cols * 2.0 ** -60) / float(w) + 1
+
+    def column(u, kept):  # the first one at which 1 + c w exceeds u (1 + kept w)
+        return math.floor((F(u) * (1 + kept * w) - 1) / w) + 1
+
+    rows = _f32(np.tile(x, (len(far), 1)))
+    one, zero = np.ones(len(far)), np.zeros(len(far))
+    got = _sample(mfs, rows, np.array(far, np.float32), one, zero, one, zero)
+    assert (np.abs(got - np.array([column(u, n) for u in far])) <= miss).all(), got
+    last = 1.0 - 2.0 ** -24
+    got = _sample(mfs, rows, np.full(len(far), last, np.float32), one, zero, np.array(far, np.float32), zero)
+    kept = [math.ceil((F(p) * (1 + n * w) - 1) / w) for p in far]  # the shortest prefix of at least p
+    assert (np.abs(got - np.array([max(0, column(last, m)) for m in kept])) <= 2 * miss).all(), got
