@@ -435,7 +435,9 @@ typedef struct {
  *            the angle is reduced in 64 bits, the rotation runs in 32 bits and is
  *            rounded once; ignored with MFS_ROPE_NONE
  * Outputs overlap inputs only where one is the other's array (same pointer and
- * stride).  Two tokens that reach the same row of the same page leave either's.
+ * stride).  Where two tokens of a call reach the same row of the same page, that
+ * row is left with parts of both, its key and value not of one token; no other
+ * row is touched.
  * Enqueues and returns; MFS_E_ARG on bad sizes, strides, alignment or NULL. */
 int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len,
                   const void* q, long long q_stride, int n_q_heads, void* q_out, long long q_out_stride,

@@ -971,3 +971,19 @@ def test_sample_rows_of_the_most_columns_with_a_light_tail(mfs):
     got = _sample(mfs, rows, np.full(len(far), last, np.float32), one, zero, np.array(far, np.float32), zero)
     kept = [math.ceil((F(p) * (1 + n * w) - 1) / w) for p in far]  # the shortest prefix of at least p
     assert (np.abs(got - np.array([max(0, column(last, m)) for m in kept])) <= 2 * miss).all(), got
+
+
+def test_kv_append_of_two_tokens_on_one_row(mfs):
+    """Two sequences whose tables share a page and reach the same row of it: every 16 bytes of that row are one of the two
+    tokens', and no other row changes."""
+    torch = _torch()
+    rng = np.random.default_rng(53)
+    kc, vc = _pool(rng, 3, 2, 16, 128, "bf16")
+    k0, v0 = kc.clone(), vc.clone()
+    k, v = _normal(rng, 2, 2, 128, dtype="bf16"), _normal(rng, 2, 2, 128, dtype="bf16")
+    mfs.mfs_kv_append(mfs.PagedKV(kc, vc, _i32([[1], [1]])), k, v, _i32([0, 1, 2]), _i32([6, 6]), rope=None)
+    for pool, old, new in ((kc, k0, k), (vc, v0, v)):
+        parts, either = pool[1, :, 5].reshape(2, 16, 8), new.reshape(2, 2, 16, 8)
+        assert ((parts == either[0]).all(-1) | (parts == either[1]).all(-1)).all()
+        pool[1, :, 5] = old[1, :, 5]
+        assert torch.equal(pool, old)
