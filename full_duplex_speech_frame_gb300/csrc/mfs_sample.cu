@@ -51,6 +51,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int SR_NB = 1024;           // histogram bins, of 1 / 16 octave
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
+constexpr float SR_LEAST_T = 1.5e-30f;  // lower temperatures count as this: weights stay pairs of normal fp32 numbers
 constexpr int SR_SLOTS = 12;          // columns that a thread notes at most
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 168 * 1024;  // a CTA's part of the row in shared memory at most
@@ -138,10 +139,12 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b)
 }
 __device__ __forceinline__ constexpr F2 split2(double x) { return {(float)x, (float)(x - (double)(float)x)}; }
 
-// 2^(scale - y), y = (mx - x) c, to about 2^-40 of it.
+// 2^(scale - y), y = (mx - x) c, to about 2^-40 of it; 0 where the difference is past the largest fp32 number, as the fast
+// weight has it.
 __device__ __noinline__ u64 precise_weight(float x, float mx, F2 c, int scale)
 {
     const F2 y = mul2(two_sum(mx, -x), c);
+    if (!(y.h < 128.f)) return 0;
     const float n = rintf(y.h);
     F2 z = mul2(quick_sum(__fsub_rn(y.h, n), y.l), split2(0.69314718055994530942));  // |z| <= 0.35
     z.h = -z.h;
@@ -781,6 +784,7 @@ __device__ Border find_border(Row<T, NT>& R, float least, u64 target, u64 band)
     if (R.W.c.h > 0.f) {
         const float step = SR_REACH / SR_NB / R.W.c.h;
         upper = R.W.mx - ((float)b - 0.2f) * step * 0.99999f;
+        if (upper == -INFINITY) upper = INFINITY;  // past the largest fp32 number
         if (b < SR_NB - 1) from = fmaxf(least, R.W.mx - (float)(b + 1) * step * 1.00001f);
     }
     note_columns(R, from);
@@ -927,7 +931,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const T* __r
     extern __shared__ __align__(16) char sr_raw[];
     SrShared<NT>* S = reinterpret_cast<SrShared<NT>*>(sr_raw);
     const int r = blockIdx.x / C, rank = blockIdx.x % C, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const float T_ = temperature ? __ldg(temperature + r) : 1.f;
+    float T_ = temperature ? __ldg(temperature + r) : 1.f;
+    if (T_ > 0.f) T_ = fmaxf(T_, SR_LEAST_T);
     const int k = top_k ? __ldg(top_k + r) : 0;
     const float p = top_p ? __ldg(top_p + r) : 1.f, mp = min_p ? __ldg(min_p + r) : 0.f, u = __ldg(uniforms + r);
     if (tid < 64) {
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const T* __r
     const unsigned kept = (unsigned)__cvta_generic_to_shared(sr_raw + sizeof(SrShared<NT>));
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (tid == NT - 1) {  // the row's 64-bit arithmetic, while the logits are on their way
-        S->c = split2(fmin(1.4426950408889634 / (double)T_, 1e30));
+        S->c = split2(1.4426950408889634 / (double)T_);
         S->reach = mp >= 1.f ? 0.0 : mp > 0.f ? -(double)T_ * log((double)mp) : 0.0;
     }
     // the maximum and its lowest column, and the row's part into shared memory

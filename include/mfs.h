@@ -361,8 +361,9 @@ int mfs_argmax_rows_noalloc(const float* logits, int rows, int cols, long long l
  *   - T <= 0 or NaN: the lowest column of the maximum (mfs_argmax_rows_noalloc's
  *     rule: NaN never wins, a row of only NaN gives 0).  The same where the
  *     maximum is -inf.
- *   - weights w_i = exp((l_i - m) / T) (1 where l_i = m); a NaN logit is never a
- *     candidate.  Order the columns by logit, largest first, equal logits by
+ *   - weights w_i = exp((l_i - m) / T) (1 where l_i = m; a T below 1.5e-30 counts as
+ *     that, a difference past the largest fp32 number as infinite); a NaN logit is
+ *     never a candidate.  Order the columns by logit, largest first, equal logits by
  *     column.  The candidates are the longest prefix of that order with
  *     w_i >= min_p[r] (min_p <= 0: every column; above 1 it counts as 1), cut to
  *     top_k[r] columns (<= 0: not cut), then cut to the shortest prefix whose

@@ -987,3 +987,34 @@ def test_kv_append_of_two_tokens_on_one_row(mfs):
         assert ((parts == either[0]).all(-1) | (parts == either[1]).all(-1)).all()
         pool[1, :, 5] = old[1, :, 5]
         assert torch.equal(pool, old)
+
+
+def test_sample_rows_at_the_ends_of_temperature(mfs):
+    """Temperatures next to 0 (below 1.5e-30 they count as that) with logits as small; temperatures near the largest fp32
+    number with logits whose difference is past it (which counts as infinite), in short rows and long ones."""
+    u = np.linspace(0, 0.999, 23).astype(np.float32)
+    one = np.ones(len(u))
+    x = np.array([0, 1e-30, 2e-30, -1e-30, -4e-31], np.float32)
+    for t in (1e-45, 1e-38, 1.4e-30, 1.6e-30, 1e-29):
+        for k, p, m in ((0, 1.0, 0.0), (3, 1.0, 0.0), (0, 0.6, 0.0), (0, 1.0, 0.3)):
+            got = _sample(mfs, _f32(np.tile(x, (len(u), 1))), u, one * t, one * k, one * p, one * m)
+            want = [S.sample_row(x, v, max(np.float32(t), np.float32(1.5e-30)), k, np.float32(p), np.float32(m)) for v in u]
+            assert got.tolist() == want, (t, k, p, m)
+    rng = np.random.default_rng(54)
+    big = np.float32(3e38)
+    for x in (np.array([big, -big, 1, 2.9e38], np.float32), rng.choice(np.array([big, -big, 0, 1e38, -2e37], np.float32), 5000),
+              rng.choice(np.array([big, -big, 1e38], np.float32), 40000)):
+        seen = np.where(x == -big, -np.inf, x)
+        n = len(x)
+        for k, p, m in ((0, 1.0, 0.0), (2, 1.0, 0.0), (n - 1, 1.0, 0.0), (n * 9 // 10, 0.99, 0.0), (0, 0.7, 0.0), (0, 1.0, 0.4)):
+            got = _sample(mfs, _f32(np.tile(x, (len(u), 1))), u, one * big, one * k, one * p, one * m)
+            assert got.tolist() == [S.sample_row(seen, v, big, k, np.float32(p), np.float32(m)) for v in u], (n, k, p, m)
+    # equal weights besides, so that the draws next to their borders are decided by the second pass
+    x = np.where(rng.random(3000) < 0.4, big, -big)
+    heavy = np.nonzero(x > 0)[0]
+    n = len(heavy)
+    v = (rng.integers(0, n, 60) / n).astype(np.float32)
+    v = np.concatenate([v, np.nextafter(v, np.float32(0)), np.nextafter(v, np.float32(1))])
+    v = v[(v >= 0) & (v < 1)]
+    got = _sample(mfs, _f32(np.tile(x, (len(v), 1))), v, np.full(len(v), big), np.zeros(len(v)), np.ones(len(v)), np.zeros(len(v)))
+    assert got.tolist() == [int(heavy[int(float(a) * 2 ** 60) * n >> 60]) for a in v]
