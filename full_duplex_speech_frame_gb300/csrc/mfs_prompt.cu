@@ -363,6 +363,7 @@ __device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int 
     const float base_ = m == -INFINITY ? 0.f : -m * A.c;
     const uint4* q = reinterpret_cast<const uint4*>(A.q + (long long)(I.b + (row ? r : r1)) * A.q_stride + h * HD);
     bf16* o = A.out + (long long)(I.b + (row ? r : r1)) * A.out_stride + h * HD;
+    uint32_t done[HD / 64] = {};  // words that are NaN in all of the warp's rows: a prompt of NaN values takes each once
     for (int t = from / PT_M; t <= upto / PT_M; ++t) {
         if (!I.edge(t)) continue;
         for (int j = max(from, t * PT_M); j <= min(upto, t * PT_M + PT_M - 1); ++j) {
@@ -371,7 +372,7 @@ __device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int 
 #pragma unroll
             for (int e = 0; e < HD / 64; ++e) {
                 y[e] = __ldg(v + 32 * e + lane);
-                bad[e] = __ballot_sync(0xffffffffu, not_finite2(y[e]));
+                bad[e] = __ballot_sync(0xffffffffu, not_finite2(y[e])) & ~done[e];
                 any |= bad[e];
             }
             if (!any) continue;
@@ -382,8 +383,9 @@ __device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int 
                 s = dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, s))));
             }
             const bool sees = row && j >= lo && j <= r, weighs = ex2(fmaf(s, A.c, base_)) > 0.f;
+            const bool all = __all_sync(0xffffffffu, sees || !row);
 #pragma unroll
-            for (int e = 0; e < HD / 64; ++e)
+            for (int e = 0; e < HD / 64; ++e) {
                 for (unsigned u = bad[e]; u; u &= u - 1) {
                     const int at = __ffs(u) - 1;
                     const uint32_t z = __shfl_sync(0xffffffffu, y[e], at);
@@ -391,6 +393,9 @@ __device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int 
                     if (sees && (z & 0x7f80u) == 0x7f80u) put(p, to_f(*p) + (weighs ? __uint_as_float(z << 16) : NAN));
                     if (sees && (z & 0x7f800000u) == 0x7f800000u) put(p + 1, to_f(p[1]) + (weighs ? __uint_as_float(z & 0xffff0000u) : NAN));
                 }
+                const uint32_t nan = __ballot_sync(0xffffffffu, (y[e] & 0x7fffu) > 0x7f80u && (y[e] & 0x7fffffffu) > 0x7f80ffffu);
+                if (all) done[e] |= nan;
+            }
         }
     }
 }

@@ -1018,3 +1018,29 @@ def test_sample_rows_at_the_ends_of_temperature(mfs):
     v = v[(v >= 0) & (v < 1)]
     got = _sample(mfs, _f32(np.tile(x, (len(v), 1))), v, np.full(len(v), big), np.zeros(len(v)), np.ones(len(v)), np.zeros(len(v)))
     assert got.tolist() == [int(heavy[int(float(a) * 2 ** 60) * n >> 60]) for a in v]
+
+
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 2, 64), (4, 2, 128), (3, 1, 128), (2, 2, 64)])
+@pytest.mark.parametrize("window", [0, 3, 40, 200])
+def test_prompt_attention_many_bad_values(mfs, window, hq, hkv, hd):
+    """NaN in every value from a token on, and NaN, infinities of either sign and both in neighbouring columns of some tokens:
+    each element is what the values that its row sees make it."""
+    torch = _torch()
+    rng = np.random.default_rng(38)
+    n, inf, nan = 420, float("inf"), float("nan")
+    q, k, v = (_normal(rng, n, h, hd, dtype="bf16") for h in (hq, hkv, hkv))
+    cu, clean, got = _i32([0, n]), torch.empty_like(q), torch.empty_like(q)
+    mfs.mfs_prompt_attention(q, k, v, cu, clean, window=window)
+    for bad in ([(130, 4, nan), (131, 5, inf), (140, 4, inf), (150, 5, -inf), (131, 20, -inf), (290, 20, -inf), (291, 21, nan), (292, 20, nan),
+                 (3, 9, inf), (3, 8, -inf), (260, 9, inf), (255, hd - 1, inf), (256, hd - 2, nan), (256, hd - 1, nan), (257, hd - 1, -inf)],
+                [(t, slice(None), nan) for t in range(200, n)], [(t, slice(None), nan) for t in range(37)], [(t, slice(None), inf) for t in range(260, 275)]):
+        vv = v.clone()
+        for t, c, x in bad:
+            vv[t, hkv - 1, c] = x
+        mfs.mfs_prompt_attention(q, k, vv, cu, got, window=window)
+        add = torch.zeros(n, hd)  # what the bad values that a row sees add to it
+        for t, c, x in bad:
+            add[t:min(n, t + window) if window else n, c] += x
+        want, g = clean.cpu().float(), hq // hkv
+        want[:, -g:] += add[:, None]
+        assert torch.equal(torch.nan_to_num(got.cpu().float(), nan=7e7), torch.nan_to_num(want, nan=7e7))
