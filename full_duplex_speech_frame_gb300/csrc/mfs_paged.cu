@@ -57,7 +57,7 @@ __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x);
 // interleaved pairs, half a head apart for split ones), the next one on its way while one is rotated, the first while
 // the angles are found.  What bounds it is memory: each input is read and each output written once.  8192 tokens of 32 + 8
 // heads of 128 bf16: 39 us, 0.83 of the measured copy rate; blocks of 256 threads and 4 tokens 40 us, three items on
-// their way per thread (fewer blocks on an SM) 45 us, 8 tokens 45 us.
+// their way per thread (fewer blocks on an SM) 45 us, 8 tokens 45 us.  The same in fp32: 77 us, 0.84.
 constexpr int AP_THREADS = 128;
 // Tokens per block; 1 up to 8 blocks per SM (4 tokens of 16 heads: 3.9 us, 5.5 us by twos; 1200 of 32 + 8 heads 8.7 and
 // 9.3; 1800 14.2 and 13.1; 8192 40.3 and 38.5).
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
         if (lane == 0) row[warp] = t < begin || t >= end ? -2 : pos < 0 || pos > 0x7fffffff ? -1 : row_offset(A.C, lo, (int)pos);
         if (A.rope)
             for (int i = lane; i < HALF; i += 32) {
+                // turns in 64 bits; what is left of one, up to half, in fp32: off by 2^-26 of a turn, 1e-7 in the cosine
                 const double a = (double)pos * A.turns.f[i];
                 float s, c;
                 sincospif(2.f * (float)(a - rint(a)), &s, &c);
@@ -233,7 +234,9 @@ constexpr int PA_STAGES = 2;      // 16 KB per warp; 3 stages measured 5 % slowe
 
 // Query heads per block: the 16 rows of an mma tile for bf16.  fp32, on the CUDA cores, pays for every head of the
 // block, so it has three widths, 1, 4 and 8: 8 sequences of 8192, 8 kv heads of 128, groups of 1, 2, 4 and 8 take 87,
-// 111, 113 and 167 us, with 8 alone 164, 164, 166 and 167 us (537 MB: 79 us at the measured copy rate).
+// 111, 113 and 167 us, with 8 alone 164, 164, 166 and 167 us (537 MB: 79 us at the measured copy rate).  What bounds the
+// wider ones is not the products (9.5 TFLOP/s) but shared memory and the two warps per scheduler: every product's operands
+// and a shuffle per key and head go through its data path, 49 % busy for groups of 4 and 56 % for 8; issue 44 and 47 %.
 template <typename T>
 constexpr int PA_GM_MAX = sizeof(T) == 2 ? 16 : 8;
 
@@ -420,7 +423,10 @@ struct PaBf16 {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) o[j][x] *= scale[x >> 1];
         }
-        unsigned p[NK / 2][4];  // the weights, rounded to bf16 for the product with the values; the sums take them unrounded
+        // The weights, rounded to bf16 (2^-8 of each at most), since the matrix instruction takes both operands in one type and
+        // the values are bf16; the sums take them unrounded.  Outputs are off by 2.1 - 2.3e-3 of their size against 64 bits
+        // (1.7e-3 with fp32 weights: the outputs' own rounding).
+        unsigned p[NK / 2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             m[h] = mn[h];

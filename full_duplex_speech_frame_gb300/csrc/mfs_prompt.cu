@@ -18,12 +18,20 @@
 // rows of the one before are written.
 //
 // What bounds it is the softmax's instructions on each score (maximum, exponential, sum, conversion)
-// beside the tensor pipe, which is 70 % busy.  8192 tokens, 32 + 8 heads of 128:
-// 340 us = 1616 TFLOP/s, 0.85 of the measured matrix rate (353 us with two row tiles of one head); 12
-// packed prompts of the same total 75 us (95 us): short ones are bounded by the blocks' starts and ends.
-// Heads of 64 halve the products but not the softmax: 8192 tokens 269 us = 1023 TFLOP/s.  Their O leaves
-// columns to keep the weights apart from the scores, so that the next scores are made while the softmax of
-// these runs (294 us with the weights over the scores; 12 packed prompts 61 us against 60 us).
+// beside the tensor pipe, which is 70 % busy.  8192 tokens, 32 + 8 heads of 128: 341 us = 1610 TFLOP/s in
+// replays of a graph, 0.84 of the measured matrix rate, 364 us by calls one behind the other, where the
+// power limit holds the clock lower (with two row tiles of one head 353 us in replays; 32 + 32 heads, which
+// have no other form, 380 us); 12 packed prompts of the same total 74 us (95 us): short ones are bounded by
+// the blocks' starts and ends, where both row tiles end together and the softmax warps write.
+// Heads of 64 halve the products but not the softmax: 8192 tokens 269 us = 1023 TFLOP/s, tensor pipe 44 %
+// busy, exponentials 44 %, issue 47 %: the chain of one row per thread, with three warps per scheduler.  Their
+// O leaves columns to keep the weights apart from the scores, so that the next scores are made while the softmax
+// of these runs (294 us with the weights over the scores; 12 packed prompts 61 us against 60 us).
+//
+// The weights are rounded to bf16, since the tensor cores take both operands of a product in one type and the
+// values are bf16; a weight is then off by at most half a step, 2^-8 of itself, as the output is when it is
+// rounded.  Against 64 bits the outputs are off by 1.9 - 2.1e-3 of their size (1.6e-3 with the weights in fp32:
+// the outputs' own rounding).  The sums take the weights unrounded; the exponential is the hardware's, 2^-22.
 //
 // Masked places: scores outside a row's range are replaced, not added to, so a NaN there is gone.  A
 // masked weight is 0, but 0 x NaN is not, so where a tile of keys is masked for some rows (the
@@ -348,7 +356,8 @@ struct PtDealer {
 // A warp's 32 rows of block i, tile x, one per lane, whose outputs are written: adds the non-finite values that were cleared
 // to the rows that see them, each in its own column, or NaN where the key's weight is 0.  m: the row's maximum in use.  Only
 // tiles of keys that some row does not see whole were cleared (the last ones, and the window's first), so this takes the same
-// time however long the prompt is: some microseconds for each key with such a value.
+// time however long the prompt is: to 0.35 ms of 8192 tokens, 32 + 8 heads of 128, one such value adds 0.07 ms,
+// one in every 64th token and head 0.5 ms, NaN in all values 0.9 ms.
 template <int HD>
 __device__ __noinline__ void put_cleared(const PtArgs& A, PtBars& B, int i, int x, int quarter, float m)
 {
@@ -904,7 +913,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prompt_mma_kernel(const __grid_
 // RT rows x HD / 16 elements of the output in registers (rows and keys 16 apart, so that a warp's 16-byte
 // loads meet no bank twice), with paired fp32 products; a row's maximum and sum go over half a warp.
 // Keys of the next tile are copied while the values of this one are summed, and the other way round.
-// What bounds it is the fp32 rate: 4096 tokens, 32 + 8 heads of 128, take 3.0 ms = 46 TFLOP/s.  In tiles
+// 4096 tokens, 32 + 8 heads of 128, take 3.0 ms = 46 TFLOP/s, about 0.6 of the CUDA cores' rate; the data path of
+// shared memory, which feeds them, is 55 % busy, and two warps per scheduler issue 45 % of the time.  In tiles
 // that some row does not see whole, unseen products are left out, not multiplied by zero.
 
 constexpr int PF_KEYS = 64, PF_THREADS = 256;

@@ -22,9 +22,10 @@
 // column with the loop around it) and the latency of the exchanges; with many long
 // rows also the second wave, as a row takes most of an SM's shared memory.  Top-k of
 // 16 rows of 2048 fp32: 8 us, of 32 rows of 32000: 10 us; top-p with min-p of 256 rows
-// of 32000: 46 us; 128 rows of 131072 bf16: top-k 30 us, no filter 83 us, top-p alone,
-// which weighs all columns, 133 us.  Rows left in memory instead, read again from L2
-// by every pass, need no second wave but took 108 us and 215 us for the last two.
+// of 32000: 46 us; 128 rows of 131072 bf16: top-k 35 us, no filter 61 to 72 us (by how many
+// rows are done again), top-p alone, which weighs all columns, 130 us.  Rows left in memory
+// instead, read again from L2 by every pass, need no second wave but took 1.3 to 1.6 times as
+// long in the last two.  The bf16 forms spill about 44 bytes a thread at 64 registers.
 //
 // Weights are unsigned fixed point (2^scale for the maximum's), so sums are exact
 // whatever order the atomics take, and the row's token is the same on every run.
@@ -52,7 +53,10 @@ using bf16 = __nv_bfloat16;
 constexpr int SR_NB = 1024;           // histogram bins, of 1 / 16 octave
 constexpr float SR_REACH = 64.f;      // columns below 2^-64 of the maximum's weight can hold no border and no draw
 constexpr float SR_LEAST_T = 1.5e-30f;  // lower temperatures count as this: weights stay pairs of normal fp32 numbers
-constexpr int SR_SLOTS = 12;          // columns that a thread notes at most
+// Columns that a thread notes at most.  With 6, 12 and 16: top-p and min-p of 256 rows of 32000 36.9, 34.6 and 34.7 us
+// (temperature 0.8), top-k 400 of 16 rows of 8192 18.0, 15.1 and 15.2 us; top-k 50 of 128 rows of 131072 bf16 33.4, 33.4
+// and 46.6 us, as 16 take the shared memory of a second block.
+constexpr int SR_SLOTS = 12;
 constexpr int SR_MAX_C = 8;           // CTAs per row
 constexpr int SR_STAGE_BYTES = 168 * 1024;  // a CTA's part of the row in shared memory at most
 constexpr int SR_WIDE_BYTES = 140 * 1024;   // the same for CTAs of 1024 threads
@@ -725,6 +729,9 @@ __device__ __forceinline__ bool sample_list(const Row<T, NT>& R, unsigned n, int
     __syncthreads();
     unsigned keep = top_k > 0 ? min(n, (unsigned)top_k) : n;  // columns kept, of the largest
     bool in = tid < n;
+    // Up to 256 columns all are ranked against all, longer lists go through a histogram.  Lists of about 130 (16 rows of 2048,
+    // top-k 100 and top-p): ranked 7.7 us, by histogram 8.8; of about 316 (top-k 250): 10.8 and 7.6; 256 rows of 32000, top-k
+    // 100 and top-p: 23.5 and 26.4, top-k 400: 39.0 and 25.0.
     if (n > 256) {
         if (keep < n) {  // all threads take part
             const u64 border = border_among<false>(R, e, w, in, keep, 0);
