@@ -1044,3 +1044,32 @@ def test_prompt_attention_many_bad_values(mfs, window, hq, hkv, hd):
         want, g = clean.cpu().float(), hq // hkv
         want[:, -g:] += add[:, None]
         assert torch.equal(torch.nan_to_num(got.cpu().float(), nan=7e7), torch.nan_to_num(want, nan=7e7))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("hq,hkv,hd", [(4, 2, 64), (8, 1, 128), (2, 2, 128)])
+def test_paged_attention_bad_keys_and_values_stay_with_their_rows(mfs, hq, hkv, hd, bad, dtype):
+    """A NaN key, or one whose score is +infinity, makes its sequence's heads of that kv head NaN; a NaN or infinite value
+    reaches its own column of them; every other output is what it is without them."""
+    torch = _torch()
+    rng = np.random.default_rng(55)
+    page, lens = 16, [5, 700, 33, 3001, 64]
+    table, pages = _table(rng, lens, page)
+    kc, vc = _pool(rng, pages, hkv, page, hd, dtype)
+    q, g = _normal(rng, 5, hq, hd, dtype=dtype), hq // hkv
+    q[:, :, 5] = q[:, :, 5].abs() + 0.125
+    cache, kv = mfs.PagedKV(kc, vc, torch.from_numpy(table).cuda()), _i32(lens)
+    clean, got = torch.empty_like(q), torch.empty_like(q)
+    mfs.mfs_paged_attention(cache, q, kv, clean)
+    for s, p in ((1, 0), (1, 333), (2, 32), (3, 1700), (4, 63)):
+        at = (int(table[s, p // page]), hkv - 1, p % page, 5)
+        for pool, columns in ((kc, slice(None)), (vc, slice(5, 6))):
+            was = pool[at].item()
+            pool[at] = bad
+            mfs.mfs_paged_attention(cache, q, kv, got)
+            pool[at] = was
+            hit = torch.zeros_like(got, dtype=torch.bool)
+            hit[s, hq - g:, columns] = True
+            assert torch.equal(got[~hit], clean[~hit])
+            assert torch.isnan(got[hit]).all() if pool is kc or bad != bad else (got[hit] == bad).all()
