@@ -42,6 +42,7 @@
 #include <cudaTypedefs.h>
 #include <type_traits>
 
+#include "mfs_mma.cuh"
 #include "mfs_ops.cuh"
 
 namespace {
@@ -57,13 +58,9 @@ constexpr int PT_M = 128;                    // query rows per tile, keys per ti
 constexpr int PT_THREADS = 384;
 // A test build may shorten the waits' limit, and have every CTA lose one tile of its ring (never ask for it), so that they
 // run out.
-#ifndef MFS_PROMPT_WAIT_NS
-#define MFS_PROMPT_WAIT_NS 2000000000ull
-#endif
 #ifndef MFS_PROMPT_LOST_TILE
 #define MFS_PROMPT_LOST_TILE -1
 #endif
-constexpr unsigned long long PT_WAIT_NS = MFS_PROMPT_WAIT_NS;
 
 template <int HD>
 struct PtShape {
@@ -87,150 +84,8 @@ struct PtBars {
 };
 constexpr int PT_READERS = PT_THREADS / 32;  // warps that read the work
 
-__device__ __forceinline__ unsigned su32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void bar_init(uint64_t* b, unsigned n)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* b, unsigned bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* b)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t* b, unsigned par)
-{
-    unsigned ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(su32(b)), "r"(par) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long gtime()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Waits, for a whole warp, for the phase of parity `par`; false if it took too long or another wait of the CTA gave up.
-// The lanes leave together, with the same answer: what follows exchanges registers and uses tensor memory.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned par, int* abort)
-{
-    unsigned long long t0 = 0;
-    for (unsigned n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, bar_try(b, par))) return true;
-        if (n & 63u) continue;
-        const unsigned long long t = gtime();
-        if (t0 == 0) t0 = t;
-        if (__any_sync(0xffffffffu, *(volatile int*)abort || t - t0 > PT_WAIT_NS)) {
-            *(volatile int*)abort = 1;
-            __threadfence_block();
-            return false;
-        }
-    }
-}
 // Has a wait of the CTA given up?  For a whole warp.
 __device__ __forceinline__ bool gave_up(PtBars& B) { return __any_sync(0xffffffffu, *(volatile int*)&B.abort); }
-__device__ __forceinline__ void bar_drain(uint64_t* b, unsigned par)
-{
-    const unsigned long long t0 = gtime();
-    while (!bar_try(b, par) && gtime() - t0 <= PT_WAIT_NS) {
-    }
-}
-
-// Shared-memory operand, 128-byte swizzle, groups of 8 rows 1024 bytes apart; `lead`: bytes between
-// 64-element blocks of the contiguous dimension where that is the MMA's M or N (V), else unused.
-__device__ __forceinline__ uint64_t desc(unsigned saddr, unsigned lead)
-{
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* b)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-#define PT_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
-#define PT_R16(r, i) PT_R4(r, i), PT_R4(r, i + 4), PT_R4(r, i + 8), PT_R4(r, i + 12)
-#define PT_I4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
-#define PT_I16(r, i) PT_I4(r, i), PT_I4(r, i + 4), PT_I4(r, i + 8), PT_I4(r, i + 12)
-
-// 32 columns of this thread's row (no wait)
-__device__ __forceinline__ void tld32(uint32_t t, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-                 "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];" : PT_R16(r, 0), PT_R16(r, 16) : "r"(t));
-}
-__device__ __forceinline__ void tld16(uint32_t t, uint32_t* r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];" : PT_R16(r, 0) : "r"(t));
-}
-__device__ __forceinline__ void tst16(uint32_t t, const uint32_t* r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t), PT_I16(r, 0)
-                 : "memory");
-}
-__device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 struct PtArgs {
     const int32_t* cu;
     const bf16 *q, *k, *v;

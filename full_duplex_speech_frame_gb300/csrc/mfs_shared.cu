@@ -1,0 +1,472 @@
+// mfs_shared_attention: one new token per sequence, for groups of sequences whose first positions are the same.
+//
+// A prefix's keys and values meet all rows of its group at once: a row is a query head of one of the group's sequences,
+// n sequences with g query heads to a kv head make n g rows.  Items (group, block of rows, kv head) are cut into tiles of
+// positions, all laid end to end with a little room at each item's start, and dealt in equal shares to the CTAs, one each,
+// which walk through them with a running maximum, sum and output for each row.  An item that lies in one share leaves its
+// rows' results; the pieces of others are left for each CTA, two at most.  What follows the prefix is each sequence's own:
+// paged_attention_kernel takes it, with the same split over its length.  The last kernel joins, for each sequence and head,
+// its own part and the prefix's pieces.
+#include "mfs_shared.cuh"
+
+namespace {
+
+// ------------------------------------------------------------- CUDA cores
+//
+// 256 threads take 16 RT rows (RT 8, 4 or 2) and walk over tiles of 64 positions in shared memory, in fp32 whatever the cache
+// holds; a thread has RT rows x 4 positions of the scores and RT rows x HD / 16 elements of the output in registers (rows and
+// positions 16 apart), with paired products; a row's maximum and sum go over half a warp.  The next tile's keys come while
+// the values of this one are summed, and the other way round.
+
+constexpr int SF_KEYS = 64, SF_THREADS = 256;
+
+template <int HD, int RT>
+struct SfShape {
+    static constexpr int ROWS = 16 * RT, LD = HD + 4, LP = SF_KEYS + 4;
+    static constexpr int BYTES = 4 * ((ROWS + 2 * SF_KEYS) * LD + ROWS * LP);
+};
+
+__device__ __forceinline__ float4 codes_f32(unsigned w, float by)
+{
+    unsigned lo, hi;
+    e4m3_f16(w, lo, hi);
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(x.x * by, x.y * by, y.x * by, y.y * by);
+}
+
+template <typename T, int HD, int RT, bool QUANT>
+__global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_constant__ ShArgs A)
+{
+    using S = SfShape<HD, RT>;
+    constexpr int ROWS = S::ROWS, LD = S::LD, LP = S::LP, OC = HD / 16;
+    extern __shared__ __align__(16) float sf_raw[];
+    float *sq = sf_raw, *sk = sq + ROWS * LD, *sv = sk + SF_KEYS * LD, *sp = sv + SF_KEYS * LD;
+    __shared__ ShPart sh_part;
+    __shared__ int sh_more, sh_bad;
+    __shared__ long long sh_off[2][SF_KEYS], sh_x[QUANT ? 2 : 1][SF_KEYS];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    ShParts parts;
+    bool more = false;
+    if (tid < 32) more = parts.start(A, blockIdx.x);
+    for (;;) {
+        if (tid < 32) {
+            ShPart p;
+            more = more && parts.next(A, p);
+            if (tid == 0) {
+                sh_more = more;
+                sh_bad = 0;
+                if (more) sh_part = p;
+            }
+        }
+        __syncthreads();
+        if (!sh_more) break;
+        const ShPart P = sh_part;
+        const int r0 = P.w.rb * ROWS, rows = min(ROWS, P.w.ns * A.g - r0);
+
+        // where a tile's rows lie: -1 for those past the prefix, -2 for a bad page
+        auto look_up = [&](int t) {
+            if (t >= P.upto || tid >= SF_KEYS) return;
+            const int p = t * SF_KEYS + tid;
+            long long off = -1, x = 0;
+            int page, row;
+            if (p < P.w.p) {
+                if (row_place(A.C, P.reader, p, page, row)) {
+                    off = (long long)page * A.C.page_stride + (long long)row * A.C.row_stride + (long long)P.w.h * A.C.head_stride;
+                    x = (long long)page * A.x_page + (long long)row * A.x_row + (long long)P.w.h * A.x_head;
+                } else {
+                    sh_bad = 1;
+                }
+            }
+            sh_off[t & 1][tid] = off;
+            if (QUANT) sh_x[t & 1][tid] = x;
+        };
+        auto fetch = [&](float* dst, bool key, int t) {
+            const char* base = key ? A.C.k : A.C.v;
+            if constexpr (!QUANT && sizeof(T) == 4) {
+                for (int i = tid; i < SF_KEYS * (HD / 4); i += SF_THREADS) {
+                    const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+                    const long long off = sh_off[t & 1][r];
+                    copy16(su32(dst + r * LD + c), base + (off < 0 ? 0 : (off + c) * 4), off >= 0);
+                }
+            } else if constexpr (QUANT) {
+                for (int i = tid; i < SF_KEYS * (HD / 16); i += SF_THREADS) {
+                    const int r = i / (HD / 16), c = i % (HD / 16) * 16;
+                    const long long off = sh_off[t & 1][r];
+                    const uint4 w = off < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + off + c));
+                    const float by = off < 0 ? 0.f : pow2_of(__ldg((key ? A.kx : A.vx) + sh_x[t & 1][r]));
+                    float4* d = reinterpret_cast<float4*>(dst + r * LD + c);
+                    d[0] = codes_f32(w.x, by); d[1] = codes_f32(w.y, by); d[2] = codes_f32(w.z, by); d[3] = codes_f32(w.w, by);
+                }
+            } else {
+                for (int i = tid; i < SF_KEYS * (HD / 8); i += SF_THREADS) {
+                    const int r = i / (HD / 8), c = i % (HD / 8) * 8;
+                    const long long off = sh_off[t & 1][r];
+                    const uint4 w = off < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + (off + c) * 2));
+                    float4* d = reinterpret_cast<float4*>(dst + r * LD + c);
+                    d[0] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+                    d[1] = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u), __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u));
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        look_up(P.from);
+        for (int i = tid; i < ROWS * (HD / 4); i += SF_THREADS) {
+            const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const int s = P.w.s0 + (r0 + r) / A.g, h = P.w.h * A.g + (r0 + r) % A.g;
+                const T* x = reinterpret_cast<const T*>(A.q) + (long long)s * A.q_stride + (long long)h * HD + c;
+                v = make_float4(to_f(x[0]), to_f(x[1]), to_f(x[2]), to_f(x[3]));
+            }
+            *reinterpret_cast<float4*>(sq + r * LD + c) = v;
+        }
+        __syncthreads();
+        if (P.upto > P.from) {
+            fetch(sk, true, P.from);
+            fetch(sv, false, P.from);
+        }
+        float o[RT][OC], m[RT], l[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < OC; ++e) o[i][e] = 0.f;
+        }
+        for (int t = P.from; t < P.upto; ++t) {
+            const int valid = P.w.p - t * SF_KEYS;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // the keys
+            look_up(t + 1);
+            __syncthreads();
+            uint64_t acc[RT][4];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll 4
+            for (int e = 0; e < HD; e += 4) {
+                ulonglong2 k4[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * LD + e);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const ulonglong2 q4 = *reinterpret_cast<const ulonglong2*>(sq + (ty + 16 * i) * LD + e);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fma2(q4.y, k4[j].y, fma2(q4.x, k4[j].x, acc[i][j]));
+                }
+            }
+            __syncthreads();  // all have read the keys
+            if (t + 1 < P.upto) fetch(sk, true, t + 1);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                float s[4], mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float a, b;
+                    unpair(acc[i][j], a, b);
+                    s[j] = a + b;
+                    if (tx + 16 * j >= valid) s[j] = -INFINITY;
+                    mx = fmaxf(mx, s[j]);
+                }
+                for (int x = 8; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                const float mn = fmaxf(m[i], mx), a = m[i] == mn ? 1.f : exp2f((m[i] - mn) * A.c);
+                const float sub = mn == -INFINITY ? 0.f : mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f((s[j] - sub) * A.c);
+                    sum += p;
+                    sp[(ty + 16 * i) * LP + tx + 16 * j] = p;
+                }
+                m[i] = mn;
+                l[i] = l[i] * a + sum;
+#pragma unroll
+                for (int e = 0; e < OC; ++e) o[i][e] *= a;
+            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // the values
+            __syncthreads();
+            // (places past the prefix: weights of 0 and values of 0)
+#pragma unroll 2
+            for (int j = 0; j < SF_KEYS; j += 4) {
+                float4 p4[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) p4[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * LP + j);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint64_t v2[OC / 2];
+#pragma unroll
+                    for (int e = 0; e < OC / 4; ++e) {
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sv + (j + x) * LD + 4 * tx + 64 * e);
+                        v2[2 * e] = y.x;
+                        v2[2 * e + 1] = y.y;
+                    }
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        const float p = x == 0 ? p4[i].x : x == 1 ? p4[i].y : x == 2 ? p4[i].z : p4[i].w;
+                        const uint64_t pp = pair(p, p);
+#pragma unroll
+                        for (int e = 0; e < OC / 2; ++e) {
+                            const uint64_t r = fma2(pp, v2[e], pair(o[i][2 * e], o[i][2 * e + 1]));
+                            unpair(r, o[i][2 * e], o[i][2 * e + 1]);
+                        }
+                    }
+                }
+            }
+            __syncthreads();  // all have read the values
+            if (t + 1 < P.upto) fetch(sv, false, t + 1);
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float sum = l[i];
+            for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            const int r = ty + 16 * i;
+            if (r >= rows) continue;
+            if (sh_bad) sum = NAN;
+            long long at = ((long long)blockIdx.x * 2 + P.slot) * ROWS + r;
+            if (P.slot == 2) at = (long long)(P.w.s0 + (r0 + r) / A.g) * A.hq + P.w.h * A.g + (r0 + r) % A.g;
+            float* po = (P.slot == 2 ? A.row_o : A.part_o) + at * HD;
+            if (tx == 0) (P.slot == 2 ? A.row_ml : A.part_ml)[at] = make_float2(m[i], sum);
+#pragma unroll
+            for (int e = 0; e < OC / 4; ++e)
+                *reinterpret_cast<float4*>(po + 4 * tx + 64 * e) = make_float4(o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]);
+        }
+        __syncthreads();  // before the next part's place is written
+    }
+}
+
+// -------------------------------------------------------------------- join
+//
+// HD / 4 threads for each sequence and head: its own part, then the prefix's pieces in order.
+
+constexpr int SJ_THREADS = 256;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant__ ShArgs A)
+{
+    constexpr int LANES = HD / 4, HEADS = SJ_THREADS / LANES;
+    __shared__ long long sh_first, sh_total_places;
+    __shared__ ShWalk sh_w;
+    __shared__ int sh_p;
+    const int s = blockIdx.x, tid = threadIdx.x, e = tid % LANES;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int len = __ldg(A.kv_len + s);
+    if (tid < 32) {
+        const int lo = A.window > 0 && len > A.window ? len - A.window : 0;
+        const int p = shared_part(A.groups, A.n_groups, A.prefix_len, A.n_seqs, s, lo, len);
+        long long total = 0, first = 0;
+        ShWalk w = {};
+        if (p > 0) {  // the same for all lanes
+            total = sh_total(A);
+            w.i = group_of(A.groups, A.n_groups, s);
+            ShWalk x;
+            for (x.i = tid; x.i < w.i; x.i += 32) {
+                sh_group(A, x);
+                first += sh_places(A, x);
+            }
+            for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+            sh_group(A, w);
+        }
+        if (tid == 0) {
+            sh_first = first;
+            sh_total_places = total;
+            sh_w = w;
+            sh_p = p;
+        }
+    }
+    __syncthreads();
+    const ShWalk w = sh_w;
+    const int p = sh_p, lo = A.window > 0 && len > A.window ? len - A.window : 0;
+    const bool own = len > lo + p;
+    for (int h = blockIdx.y * HEADS + tid / LANES; h < A.hq; h += gridDim.y * HEADS) {
+        const long long at = (long long)s * A.hq + h;
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto take = [&](const float* o, float2 ml) {
+            const float4 v = *reinterpret_cast<const float4*>(o + 4 * e);
+            const float mn = fmaxf(m, ml.x), a = m == mn ? 1.f : exp2f((m - mn) * A.c), b = ml.x == mn ? 1.f : exp2f((ml.x - mn) * A.c);
+            m = mn;
+            l = l * a + ml.y * b;
+            acc = make_float4(acc.x * a + v.x * b, acc.y * a + v.y * b, acc.z * a + v.z * b, acc.w * a + v.w * b);
+        };
+        if (own) take(A.own_o + at * HD, A.own_ml[at]);
+        if (p > 0) {
+            const long long total = sh_total_places, shares = sh_shares(A, total);
+            const int r = (s - w.s0) * A.g + h % A.g, rb = r / A.rows, per = w.ntiles + SH_ITEM;
+            const long long begin = sh_first + ((long long)rb * A.C.n_kv_heads + h / A.g) * per;
+            // the last share that begins at or before a place
+            auto share_of = [&](long long x) { return (int)(((x + 1) * shares - 1) / total); };
+            const int c0 = share_of(begin), c1 = share_of(begin + per - 1);
+            if (c0 == c1) take(A.row_o + at * HD, A.row_ml[at]);
+            else
+                for (int c = c0; c <= c1; ++c) {
+                    const long long k = ((long long)c * 2 + (c == c0)) * A.rows + r % A.rows;
+                    take(A.part_o + k * HD, A.part_ml[k]);
+                }
+        }
+        T* o = reinterpret_cast<T*>(A.out) + (long long)s * A.out_stride + (long long)h * HD + 4 * e;
+        if (len <= 0) put4(o, make_float4(0.f, 0.f, 0.f, 0.f), 1.f);
+        else put4(o, acc, 1.f / l);
+    }
+}
+
+// -------------------------------------------------------------------- host
+
+constexpr int SH_MAX_CTAS = 304;
+
+// Rows of the prefix kernel's blocks: 128, or 64 or 32 where groups have so few on average.
+int f32_rows(long long rows, int n_groups)
+{
+    const long long each = rows / (n_groups > 0 ? n_groups : 1);
+    return each > 64 ? 128 : each > 32 ? 64 : 32;
+}
+
+struct ShSpace {
+    size_t own, part_o, part_ml, row_o, row_ml, own_o, own_ml, bytes;
+};
+
+ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
+{
+    ShSpace s;
+    const size_t rows = (size_t)n_seqs * hq, most = 256;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t x = at;
+        at += (n + 255) & ~(size_t)255;
+        return x;
+    };
+    s.own = take(pa_workspace(16, hd));
+    s.part_o = take((size_t)SH_MAX_CTAS / 2 * 2 * most * hd * 4);
+    s.part_ml = take((size_t)SH_MAX_CTAS / 2 * 2 * most * 8);
+    s.row_o = take(rows * hd * 4);
+    s.row_ml = take(rows * 8);
+    s.own_o = take(rows * hd * 4);
+    s.own_ml = take(rows * 8);
+    s.bytes = at;
+    return s;
+}
+
+template <typename T, int HD, int RT, bool QUANT>
+cudaError_t prefix_f32(const ShArgs& A, cudaStream_t st)
+{
+    using S = SfShape<HD, RT>;
+    int sms = 0;
+    static mfs::PerDevice ready;
+    cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_f32<T, HD, RT, QUANT>, S::BYTES, &sms);
+    if (e != cudaSuccess) return e;
+    shared_prefix_f32<T, HD, RT, QUANT><<<A.ctas, SF_THREADS, S::BYTES, st>>>(A);
+    return cudaGetLastError();
+}
+
+template <typename K, bool QUANT>
+int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
+{
+    using T = typename K::T;
+    constexpr int HD = K::HD;
+    const char* op = "shared_attention";
+    const ShSpace sp = sh_space(0, HD, A.hq, A.n_seqs);
+    A.part_o = (float*)(ws + sp.part_o);
+    A.part_ml = (float2*)(ws + sp.part_ml);
+    A.row_o = (float*)(ws + sp.row_o);
+    A.row_ml = (float2*)(ws + sp.row_ml);
+    A.own_o = P.own_o = (float*)(ws + sp.own_o);
+    A.own_ml = P.own_ml = (float2*)(ws + sp.own_ml);
+    int sms = 0;
+    static mfs::PerDevice known;
+    cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
+    if (e != cudaSuccess) return mfs::op_launched(op, e);
+    A.ctas = sms < SH_MAX_CTAS / 2 ? sms : SH_MAX_CTAS / 2;
+    {
+        A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
+        A.tile = SF_KEYS;
+        e = A.rows == 128 ? prefix_f32<T, HD, 8, QUANT>(A, st) : A.rows == 64 ? prefix_f32<T, HD, 4, QUANT>(A, st) : prefix_f32<T, HD, 2, QUANT>(A, st);
+    }
+    if (e != cudaSuccess) return mfs::op_launched(op, e);
+    if (const int rc = attention<K>(P, ws + sp.own, st, op)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)A.n_seqs, (unsigned)((A.hq - 1) / (SJ_THREADS / (HD / 4)) + 1));
+    cfg.blockDim = dim3(SJ_THREADS);
+    cfg.stream = st;
+    shared_join<T, HD><<<cfg.gridDim, cfg.blockDim, 0, st>>>(A);
+    return mfs::op_launched(op, cudaGetLastError());
+}
+
+// 0: go on, 1: nothing to do, else an error's code
+int shared_checked(const char* op, PaArgs& P, ShArgs& A, int n_groups, const int32_t* groups, const int32_t* prefix_len)
+{
+    if (!groups || (n_groups && !prefix_len)) return mfs::op_fail(MFS_E_ARG, op, "null groups or prefix_len");
+    P.groups = groups;
+    P.prefix_len = prefix_len;
+    P.n_groups = n_groups;
+    A.C = P.C;
+    A.kv_len = P.kv_len; A.groups = groups; A.prefix_len = prefix_len;
+    A.q = P.q; A.out = P.out;
+    A.q_stride = P.q_stride; A.out_stride = P.out_stride;
+    A.n_seqs = P.n_seqs; A.n_groups = n_groups; A.hq = P.hq; A.g = P.g; A.window = P.window;
+    A.c = P.c;
+    A.kx = P.kx; A.vx = P.vx;
+    A.x_page = P.x_page; A.x_head = P.x_head; A.x_row = P.x_row;
+    return 0;
+}
+
+}  // namespace
+
+extern "C" size_t mfs_shared_attention_workspace(const mfs_paged_kv* cache, int n_q_heads, int n_seqs)
+{
+    if (mfs::paged_kv_problem(cache) || n_q_heads < 1 || n_q_heads > MFS_MAX_HEADS || n_seqs < 0) return 0;
+    return sh_space(cache->dtype, cache->head_dim, n_q_heads, n_seqs).bytes;
+}
+
+extern "C" size_t mfs_quant_shared_attention_workspace(const mfs_quant_kv* cache, int dtype, int n_q_heads, int n_seqs)
+{
+    if (mfs::quant_kv_problem(cache) || (dtype != MFS_DTYPE_F32 && dtype != MFS_DTYPE_BF16) || n_q_heads < 1 || n_q_heads > MFS_MAX_HEADS || n_seqs < 0)
+        return 0;
+    return sh_space(dtype, cache->kv.head_dim, n_q_heads, n_seqs).bytes;
+}
+
+extern "C" int mfs_shared_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, int n_groups, const int32_t* groups,
+                                    const int32_t* prefix_len, const void* q, long long q_stride, int n_q_heads, void* out,
+                                    long long out_stride, float scale, int window, void* workspace, size_t workspace_bytes, void* cuda_stream)
+{
+    const char* op = "shared_attention";
+    if (const char* why = mfs::paged_kv_problem(cache)) return mfs::op_fail(MFS_E_ARG, op, why);
+    if (n_groups < 0) return mfs::op_fail(MFS_E_ARG, op, "need n_groups >= 0");
+    PaArgs P = {};
+    ShArgs A = {};
+    P.C = cache_of(cache);
+    const int hd = cache->head_dim;
+    int rc = pa_checked(op, P, cache->dtype, hd, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, workspace, workspace_bytes,
+                        mfs_shared_attention_workspace(cache, n_q_heads, n_seqs));
+    if (!rc) rc = shared_checked(op, P, A, n_groups, groups, prefix_len);
+    if (rc) return rc < 0 ? rc : MFS_OK;
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    char* ws = (char*)workspace;
+    if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? shared<PaKindBf16<128, true>, false>(P, A, ws, st) : shared<PaKindBf16<64, true>, false>(P, A, ws, st);
+    auto fn = hd == 128 ? (P.g == 1 ? shared<PaKindF32<128, 1, true>, false> : P.g <= 4 ? shared<PaKindF32<128, 4, true>, false> : shared<PaKindF32<128, 8, true>, false>)
+                        : (P.g == 1 ? shared<PaKindF32<64, 1, true>, false> : P.g <= 4 ? shared<PaKindF32<64, 4, true>, false> : shared<PaKindF32<64, 8, true>, false>);
+    return fn(P, A, ws, st);
+}
+
+extern "C" int mfs_quant_shared_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const int32_t* kv_len, int n_groups,
+                                          const int32_t* groups, const int32_t* prefix_len, const void* q, long long q_stride, int n_q_heads,
+                                          void* out, long long out_stride, float scale, int window, void* workspace, size_t workspace_bytes,
+                                          void* cuda_stream)
+{
+    const char* op = "shared_attention";
+    if (const char* why = mfs::quant_kv_problem(cache)) return mfs::op_fail(MFS_E_ARG, op, why);
+    if (n_groups < 0) return mfs::op_fail(MFS_E_ARG, op, "need n_groups >= 0");
+    PaArgs P = quant_args(cache);
+    ShArgs A = {};
+    const int hd = cache->kv.head_dim;
+    int rc = pa_checked(op, P, dtype, hd, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, workspace, workspace_bytes,
+                        mfs_quant_shared_attention_workspace(cache, dtype, n_q_heads, n_seqs));
+    if (!rc) rc = shared_checked(op, P, A, n_groups, groups, prefix_len);
+    if (rc) return rc < 0 ? rc : MFS_OK;
+    cudaStream_t st = (cudaStream_t)cuda_stream;
+    char* ws = (char*)workspace;
+    if (dtype == MFS_DTYPE_BF16) return hd == 128 ? shared<PaKindE4m3<bf16, 128, true>, true>(P, A, ws, st) : shared<PaKindE4m3<bf16, 64, true>, true>(P, A, ws, st);
+    return hd == 128 ? shared<PaKindE4m3<float, 128, true>, true>(P, A, ws, st) : shared<PaKindE4m3<float, 64, true>, true>(P, A, ws, st);
+}

@@ -19,7 +19,7 @@ LIB_PATH = os.environ.get("MFS_LIBRARY") or os.path.join(_HERE, "libmfs.so")
 MFS_OK = 0
 STATUS = {-1: "MFS_E_ARG", -2: "MFS_E_SLOT", -3: "MFS_E_TOKEN", -4: "MFS_E_RANGE", -5: "MFS_E_STATE",
           -6: "MFS_E_CUDA", -7: "MFS_E_DEVICE", -8: "MFS_E_NOMEM"}
-MFS_DTYPE_F32, MFS_DTYPE_BF16 = 0, 1
+MFS_DTYPE_F32, MFS_DTYPE_BF16, MFS_DTYPE_E4M3 = 0, 1, 2
 MFS_MAX_SLOTS = 64
 MFS_ROPE = {None: 0, "interleaved": 1, "half": 2}
 
@@ -46,6 +46,16 @@ class mfs_paged_kv(ctypes.Structure):
                         (n, ctypes.c_longlong) for n in ("page_stride", "head_stride", "row_stride")]
 
 
+class mfs_quant_kv(ctypes.Structure):
+    _fields_ = [("kv", mfs_paged_kv), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("exp_page_stride", "exp_head_stride", "exp_row_stride")]
+
+
+class mfs_rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("dims", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "original", "low", "high", "magnitude")]
+
+
 def _load_library():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -53,7 +63,8 @@ def _load_library():
                           "(or python full_duplex_speech_frame_gb300/build.py)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, ci, i32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
-    ll, pkv = ctypes.c_longlong, ctypes.POINTER(mfs_paged_kv)
+    ll, pkv, qkv, rp = ctypes.c_longlong, ctypes.POINTER(mfs_paged_kv), ctypes.POINTER(mfs_quant_kv), ctypes.POINTER(mfs_rope)
+    sz, cf = ctypes.c_size_t, ctypes.c_float
     sig = {
         "mfs_create": (ci, [ctypes.POINTER(mfs_config), vp, ctypes.POINTER(vp)]),
         "mfs_destroy": (None, [vp]),
@@ -82,6 +93,16 @@ def _load_library():
         "mfs_rvq_encode": (ci, [vp, vp, ci, ci, vp, ci, vp, vp]),
         "mfs_sample_rows": (ci, [vp, ci, ci, ci, ll, vp, vp, vp, vp, vp, vp, vp]),
         "mfs_kv_append": (ci, [pkv, ci, ci, vp, vp, vp, ll, ci, vp, ll, vp, ll, vp, ll, vp, ll, ci, ctypes.c_double, vp]),
+        "mfs_kv_append_rope": (ci, [pkv, ci, ci, vp, vp, vp, ll, ci, vp, ll, vp, ll, vp, ll, vp, ll, rp, vp]),
+        "mfs_quant_append": (ci, [qkv, ci, ci, ci, vp, vp, vp, ll, ci, vp, ll, vp, ll, vp, ll, vp, ll, rp, vp]),
+        "mfs_kv_read": (ci, [pkv, ci, ci, vp, vp, vp, ll, vp, ll, vp]),
+        "mfs_quant_read": (ci, [qkv, ci, ci, ci, vp, vp, vp, ll, vp, ll, vp]),
+        "mfs_quant_attention_workspace": (sz, [qkv, ci, ci]),
+        "mfs_quant_attention": (ci, [qkv, ci, ci, vp, vp, ll, ci, vp, ll, cf, ci, vp, sz, vp]),
+        "mfs_shared_attention_workspace": (sz, [pkv, ci, ci]),
+        "mfs_shared_attention": (ci, [pkv, ci, vp, ci, vp, vp, vp, ll, ci, vp, ll, cf, ci, vp, sz, vp]),
+        "mfs_quant_shared_attention_workspace": (sz, [qkv, ci, ci, ci]),
+        "mfs_quant_shared_attention": (ci, [qkv, ci, ci, vp, ci, vp, vp, vp, ll, ci, vp, ll, cf, ci, vp, sz, vp]),
         "mfs_paged_attention_workspace": (ctypes.c_size_t, [pkv, ci]),
         "mfs_paged_attention": (ci, [pkv, ci, vp, vp, ll, ci, vp, ll, ctypes.c_float, ci, vp, ctypes.c_size_t, vp]),
         "mfs_prompt_attention": (ci, [ci, ci, ci, vp, vp, ll, ci, vp, ll, vp, ll, ci, ci, vp, ll, ctypes.c_float, ci, vp]),
@@ -454,7 +475,7 @@ def mfs_sample_rows(logits, uniforms, tokens, temperature=None, top_k=None, top_
 
 class PagedKV:
     """One layer's paged key/value cache (mfs_paged_kv): k, v [n_pages, n_kv_heads, page_size,
-    head_dim] CUDA tensors of equal strides with dense rows, table [n_seqs, pages] int32.  Keeps the
+    head_dim] CUDA tensors (fp32 or bf16) of equal strides with dense rows, table [n_seqs, pages] int32.  Keeps the
     tensors; what they hold may change between calls."""
 
     def __init__(self, k, v, table):
@@ -472,10 +493,48 @@ class PagedKV:
         stride = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
         self.c = mfs_paged_kv(k=k.data_ptr(), v=v.data_ptr(), table=table.data_ptr(), table_width=table.shape[1],
                               table_stride=table.stride(0) if table.shape[0] > 1 else 0, n_pages=k.shape[0], page_size=k.shape[2],
-                              n_kv_heads=k.shape[1], head_dim=k.shape[3], dtype=_dtype_code(k), page_stride=stride[0],
+                              n_kv_heads=k.shape[1], head_dim=k.shape[3], dtype=self._code(k), page_stride=stride[0],
                               head_stride=stride[1], row_stride=stride[2])
-        # what each call compares its tensors with
-        self._is = (k.get_device(), k.dtype, k.shape[1], k.shape[3])
+        # what each call compares its tensors with (no dtype: theirs may be fp32 or bf16)
+        self._is = (k.get_device(), None if self.c.dtype == MFS_DTYPE_E4M3 else k.dtype, k.shape[1], k.shape[3])
+
+    def _code(self, k) -> int:
+        return _dtype_code(k)
+
+
+class QuantKV(PagedKV):
+    """One layer's 8-bit paged cache (mfs_quant_kv): codes k, v [n_pages, n_kv_heads, page_size, head_dim] (uint8 or
+    float8_e4m3fn) and exponent bytes k_exp, v_exp [n_pages, n_kv_heads, page_size] (uint8), each pair of equal strides, and
+    the table.  The calls take and give fp32 or bf16, whichever their tensors have."""
+
+    def __init__(self, k, v, k_exp, v_exp, table):
+        import torch
+        if k.dtype is not torch.uint8 and k.dtype is not torch.float8_e4m3fn:
+            _refuse(f"dtype {k.dtype}: need codes as uint8 or float8_e4m3fn")
+        super().__init__(k, v, table)
+        for x in (k_exp, v_exp):
+            if x.dtype is not torch.uint8 or x.shape != k.shape[:3] or x.device != k.device:
+                _refuse("cache: need uint8 exponents [n_pages, n_kv_heads, page_size] on the cache's device")
+        if any(k.shape[i] > 1 and k_exp.stride(i) != v_exp.stride(i) for i in range(3)):
+            _refuse("cache: need equal strides in k_exp and v_exp")
+        self.k_exp, self.v_exp = k_exp, v_exp
+        stride = [k_exp.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self.c = mfs_quant_kv(kv=self.c, k_exp=k_exp.data_ptr(), v_exp=v_exp.data_ptr(), exp_page_stride=stride[0],
+                              exp_head_stride=stride[1], exp_row_stride=stride[2])
+
+    def _code(self, k) -> int:
+        return MFS_DTYPE_E4M3
+
+
+class Rope:
+    """A rotation for mfs_kv_append (mfs_rope): the first `dims` elements of each head (0: all), pairs by `layout`
+    ("interleaved" or "half"); pairs that turn less than `high` times over `original` positions are slowed down, by `factor`
+    below `low` turns (original = 0: all of them); the rotated part is multiplied by `magnitude` (see include/mfs.h)."""
+
+    def __init__(self, layout="interleaved", dims=0, theta=10000.0, factor=1.0, original=0.0, low=1.0, high=4.0, magnitude=1.0):
+        if layout not in MFS_ROPE:
+            _refuse(f"rope: one of {list(MFS_ROPE)}")
+        self.c = mfs_rope(MFS_ROPE[layout], dims, theta, factor, original, low, high, magnitude)
 
 
 def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=None, rope="interleaved", theta=10000.0,
@@ -483,12 +542,14 @@ def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=No
     """Write the tokens' keys (rotated) and values k, v [tokens, n_kv_heads, head_dim] into the cache at
     their positions, and their rotated queries q [tokens, n_q_heads, head_dim] and keys into q_out and
     k_out.  cu [n_seqs + 1], kv_len [n_seqs]: int32 CUDA tensors; kv_len counts the new tokens.
-    rope: "interleaved", "half" or None (see include/mfs.h)."""
+    rope: "interleaved", "half" or None, of whole heads with base theta, or a Rope (theta is then its own).
+    A QuantKV gets the keys and values in 8 bits (see include/mfs.h)."""
     import torch
     dev, dtype, hkv, hd = cache._is
+    dtype = dtype or k.dtype
     n, n_seqs, i32 = k.size(0), kv_len.size(0), torch.int32
-    if rope not in MFS_ROPE:
-        _refuse(f"rope: one of {list(MFS_ROPE)}")
+    if not isinstance(rope, Rope) and rope not in MFS_ROPE:
+        _refuse(f"rope: a Rope or one of {list(MFS_ROPE)}")
     if (q is None) != (q_out is None):
         _refuse("q and q_out go together")
     if n_seqs > cache.n_seqs:
@@ -501,14 +562,60 @@ def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=No
         hq = q.size(1)
         qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
         xp, xs = _rows(q_out, "q_out", n, hq, hd, dtype, dev)
-    _enqueue(dev, stream, _lib.mfs_kv_append, cache.c, n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev),
-             _array(kv_len, "kv_len", n_seqs, i32, dev), qp, qs, hq, xp, xs, kp, ks, op, os_, vp, vs, MFS_ROPE[rope], theta)
+    args = (n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev), _array(kv_len, "kv_len", n_seqs, i32, dev), qp, qs, hq, xp, xs, kp, ks,
+            op, os_, vp, vs)
+    if isinstance(cache, QuantKV):
+        r = (rope if isinstance(rope, Rope) else Rope(rope, theta=theta)).c
+        _enqueue(dev, stream, _lib.mfs_quant_append, cache.c, _dtype_code(k), *args, r)
+    elif isinstance(rope, Rope):
+        _enqueue(dev, stream, _lib.mfs_kv_append_rope, cache.c, *args, rope.c)
+    else:
+        _enqueue(dev, stream, _lib.mfs_kv_append, cache.c, *args, MFS_ROPE[rope], theta)
+
+
+def mfs_kv_read(cache: PagedKV, cu, kv_len, k_out, v_out, stream=None) -> None:
+    """Read the last cu[s + 1] - cu[s] rows of each sequence's first kv_len[s] positions back, packed, into k_out and v_out
+    [tokens, n_kv_heads, head_dim]: the cache's dtype, for a QuantKV fp32 or bf16 (see include/mfs.h)."""
+    import torch
+    dev, dtype, hkv, hd = cache._is
+    n, n_seqs, i32 = k_out.size(0), kv_len.size(0), torch.int32
+    if n_seqs > cache.n_seqs:
+        _refuse("the cache's table has fewer rows than kv_len")
+    dtype = dtype or k_out.dtype
+    kp, ks = _rows(k_out, "k_out", n, hkv, hd, dtype, dev)
+    vp, vs = _rows(v_out, "v_out", n, hkv, hd, dtype, dev)
+    args = (n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev), _array(kv_len, "kv_len", n_seqs, i32, dev), kp, ks, vp, vs)
+    if isinstance(cache, QuantKV):
+        _enqueue(dev, stream, _lib.mfs_quant_read, cache.c, _dtype_code(k_out), *args)
+    else:
+        _enqueue(dev, stream, _lib.mfs_kv_read, cache.c, *args)
+
+
+def _own_workspace(cache: PagedKV, stream, make):
+    """make(), from the pool of the stream that will use it, so that it is not handed out again too early."""
+    import torch
+    if stream is None:
+        return make()
+    # (ExternalStream takes the null stream's handle for none given)
+    own = torch.cuda.ExternalStream(stream, device=cache.device) if stream else torch.cuda.default_stream(cache.device)
+    with torch.cuda.stream(own):
+        return make()
+
+
+def _workspace_at(workspace, dev: int):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("workspace: need a contiguous tensor on the cache's device")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def mfs_paged_attention_workspace(cache: PagedKV, n_q_heads: int):
     """A workspace tensor for mfs_paged_attention of this cache (see include/mfs.h on sharing it)."""
     import torch
-    return torch.empty(_lib.mfs_paged_attention_workspace(cache.c, n_q_heads), dtype=torch.uint8, device=cache.device)
+    if isinstance(cache, QuantKV):  # bf16 queries need the more
+        n = _lib.mfs_quant_attention_workspace(cache.c, MFS_DTYPE_BF16, n_q_heads)
+    else:
+        n = _lib.mfs_paged_attention_workspace(cache.c, n_q_heads)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, workspace=None, stream=None) -> None:
@@ -520,20 +627,50 @@ def mfs_paged_attention(cache: PagedKV, q, kv_len, out, scale=None, window=0, wo
     n, hq = q.size(0), q.size(1)
     if n > cache.n_seqs:
         _refuse("the cache's table has fewer rows than q")
+    dtype = dtype or q.dtype
     qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
     op, os_ = _rows(out, "out", n, hq, hd, dtype, dev)
     if workspace is None:
-        if stream is None:
-            workspace = mfs_paged_attention_workspace(cache, hq)
-        else:  # from the pool of the stream that uses it, so that it is not handed out again too early
-            # (ExternalStream takes the null stream's handle for none given)
-            own = torch.cuda.ExternalStream(stream, device=cache.device) if stream else torch.cuda.default_stream(cache.device)
-            with torch.cuda.stream(own):
-                workspace = mfs_paged_attention_workspace(cache, hq)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _refuse("workspace: need a contiguous tensor on the cache's device")
-    _enqueue(dev, stream, _lib.mfs_paged_attention, cache.c, n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_,
-             hd ** -0.5 if scale is None else scale, _window(window), workspace.data_ptr(), workspace.nbytes)
+        workspace = _own_workspace(cache, stream, lambda: mfs_paged_attention_workspace(cache, hq))
+    args = (n, _array(kv_len, "kv_len", n, torch.int32, dev), qp, qs, hq, op, os_, hd ** -0.5 if scale is None else scale, _window(window),
+            *_workspace_at(workspace, dev))
+    if isinstance(cache, QuantKV):
+        _enqueue(dev, stream, _lib.mfs_quant_attention, cache.c, _dtype_code(q), *args)
+    else:
+        _enqueue(dev, stream, _lib.mfs_paged_attention, cache.c, *args)
+
+
+def mfs_shared_attention_workspace(cache: PagedKV, n_q_heads: int, n_seqs: int):
+    """A workspace tensor for mfs_shared_attention of this cache and up to n_seqs sequences (see include/mfs.h on sharing it)."""
+    import torch
+    if isinstance(cache, QuantKV):  # enough for queries of either type
+        n = max(_lib.mfs_quant_shared_attention_workspace(cache.c, t, n_q_heads, n_seqs) for t in (MFS_DTYPE_BF16, MFS_DTYPE_F32))
+    else:
+        n = _lib.mfs_shared_attention_workspace(cache.c, n_q_heads, n_seqs)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def mfs_shared_attention(cache: PagedKV, q, kv_len, groups, prefix_len, out, scale=None, window=0, workspace=None, stream=None) -> None:
+    """mfs_paged_attention for sequences in groups with a common prefix, which is read once for each group: sequences
+    groups[i] .. groups[i + 1] - 1 have their first prefix_len[i] positions in common (groups [n_groups + 1], prefix_len
+    [n_groups]: int32 CUDA tensors; see include/mfs.h)."""
+    import torch
+    dev, dtype, _, hd = cache._is
+    n, hq, n_groups = q.size(0), q.size(1), prefix_len.size(0)
+    if n > cache.n_seqs:
+        _refuse("the cache's table has fewer rows than q")
+    dtype = dtype or q.dtype
+    qp, qs = _rows(q, "q", n, hq, hd, dtype, dev)
+    op, os_ = _rows(out, "out", n, hq, hd, dtype, dev)
+    if workspace is None:
+        workspace = _own_workspace(cache, stream, lambda: mfs_shared_attention_workspace(cache, hq, n))
+    args = (n, _array(kv_len, "kv_len", n, torch.int32, dev), n_groups, _array(groups, "groups", n_groups + 1, torch.int32, dev),
+            _array(prefix_len, "prefix_len", n_groups, torch.int32, dev), qp, qs, hq, op, os_, hd ** -0.5 if scale is None else scale,
+            _window(window), *_workspace_at(workspace, dev))
+    if isinstance(cache, QuantKV):
+        _enqueue(dev, stream, _lib.mfs_quant_shared_attention, cache.c, _dtype_code(q), *args)
+    else:
+        _enqueue(dev, stream, _lib.mfs_shared_attention, cache.c, *args)
 
 
 def mfs_prompt_attention(q, k, v, cu, out, scale=None, window=0, stream=None) -> None:

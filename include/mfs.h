@@ -48,6 +48,7 @@ extern "C" {
 
 #define MFS_DTYPE_F32 0
 #define MFS_DTYPE_BF16 1
+#define MFS_DTYPE_E4M3 2 /* only the codes of mfs_quant_kv */
 
 #define MFS_MAX_SLOTS 64
 #define MFS_N_STREAMS 17
@@ -418,6 +419,24 @@ typedef struct {
 #define MFS_ROPE_INTERLEAVED 1 /* pairs (2 i, 2 i + 1): the frame step's layout */
 #define MFS_ROPE_HALF 2        /* pairs (i, i + head_dim / 2) */
 
+/* A rotation of part of each head, or one slowed down for contexts longer than the model's own:
+ *   layout    MFS_ROPE_*
+ *   dims      elements of each head that are rotated, from its first: pairs (2 i, 2 i + 1) or
+ *             (i, i + dims / 2); a multiple of 16, at most head_dim; 0: all.  The others pass unchanged.
+ *   theta     base, > 0: pair i turns by position * f_i, f_i = theta^(-2 i / dims)
+ *   factor, original, low, high
+ *             f_i becomes f_i (c_i + (1 - c_i) / factor), with c_i the clamp to [0, 1] of
+ *             (r_i - low) / (high - low), r_i = original * f_i / (2 pi) the turns that pair i makes
+ *             over `original` positions: pairs that turn often keep their speed, slow ones are
+ *             interpolated, those between are blended.  original = 0: c_i = 0, every pair is
+ *             slowed by factor.  factor = 1: no change.  factor > 0, original >= 0, and with
+ *             original > 0 0 <= low < high.
+ *   magnitude the rotated elements are multiplied by it, > 0 */
+typedef struct {
+    int layout, dims;
+    double theta, factor, original, low, high, magnitude;
+} mfs_rope;
+
 /* Append new tokens' keys and values to the paged cache, rotated by their
  * positions on the way, and rotate their queries (mobius PR #368, "P2 - Moshi
  * LM": RoPE at the absolute position, offset by the cached length).
@@ -445,6 +464,20 @@ int mfs_kv_append(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int
                   const void* k, long long k_stride, void* k_out, long long k_out_stride, const void* v,
                   long long v_stride, int rope, double theta, void* cuda_stream);
 
+/* mfs_kv_append with a rotation as above (NULL: none). */
+int mfs_kv_append_rope(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len,
+                       const void* q, long long q_stride, int n_q_heads, void* q_out, long long q_out_stride,
+                       const void* k, long long k_stride, void* k_out, long long k_out_stride, const void* v,
+                       long long v_stride, const mfs_rope* rope, void* cuda_stream);
+
+/* Read the last rows of sequences back: row i of the c = cu[s + 1] - cu[s] rows of
+ * sequence s is position kv_len[s] - c + i, as in mfs_kv_append.
+ *   k_out, v_out  [n_tokens][n_kv_heads][head_dim], the cache's dtype, strides as above;
+ *                 rows from cu[n_seqs] on are left as they are
+ * A negative position or one without a valid page gives NaN. */
+int mfs_kv_read(const mfs_paged_kv* cache, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len, void* k_out,
+                long long k_stride, void* v_out, long long v_stride, void* cuda_stream);
+
 /* Attention of one new token per sequence over the paged cache:
  *   out[s][h] = sum_j softmax_j(scale * q[s][h] . k_j) v_j,  j in [max(0, L - window), L)
  * with L = kv_len[s] (the new token is already appended), the keys and values of
@@ -466,6 +499,79 @@ size_t mfs_paged_attention_workspace(const mfs_paged_kv* cache, int n_q_heads);
 int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, const void* q,
                         long long q_stride, int n_q_heads, void* out, long long out_stride, float scale, int window,
                         void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* ---------------------------------------------------------------- 8-bit cache
+ * A paged cache whose rows (one position of one head, of keys or of values) are
+ * held as e4m3 codes with one power of two each: half the memory, and half the
+ * bytes that attention reads, of bf16 (SGLang-Omni cookbook, PersonaPlex, "Known
+ * limitations": the pool's memory bounds the sessions).
+ *
+ *   kv       as above with dtype MFS_DTYPE_E4M3: k and v hold codes, strides in
+ *            elements are bytes (multiples of 16)
+ *   k_exp, v_exp
+ *            device: the exponent byte b of head h at row r of page g lies at
+ *            g * exp_page_stride + h * exp_head_stride + r * exp_row_stride (bytes, >= 0)
+ * Code c of a row with exponent b stands for c * 2^(b - 127), 1 <= b <= 254; b = 0: the
+ * row is zeros.  The append writes the least b that keeps the row's largest value
+ * within 448 (at least 1; 0 for a row of zeros) and rounds to nearest, ties to
+ * even: off by at most 2^-4 of a value, or 2^-17 of the row's largest (a value above
+ * 1.9375 * 2^127 becomes 2^128, which reads as infinite).  A row with an element that
+ * is not finite becomes codes of NaN. */
+typedef struct {
+    mfs_paged_kv kv;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    long long exp_page_stride, exp_head_stride, exp_row_stride;
+} mfs_quant_kv;
+
+/* mfs_kv_append_rope into an 8-bit cache; q, k, v, q_out and k_out have `dtype`
+ * (MFS_DTYPE_F32 or MFS_DTYPE_BF16).  A key is quantised as rotated in 32 bits;
+ * k_out gets it rounded to dtype, not quantised. */
+int mfs_quant_append(const mfs_quant_kv* cache, int dtype, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len,
+                     const void* q, long long q_stride, int n_q_heads, void* q_out, long long q_out_stride,
+                     const void* k, long long k_stride, void* k_out, long long k_out_stride, const void* v,
+                     long long v_stride, const mfs_rope* rope, void* cuda_stream);
+
+/* mfs_kv_read from an 8-bit cache, to `dtype` (fp32 holds every value; bf16 rounds only below 2^-126). */
+int mfs_quant_read(const mfs_quant_kv* cache, int dtype, int n_tokens, int n_seqs, const int32_t* cu, const int32_t* kv_len,
+                   void* k_out, long long k_stride, void* v_out, long long v_stride, void* cuda_stream);
+
+/* mfs_paged_attention over an 8-bit cache; q and out have `dtype`.  Products run on
+ * the codes, scores, statistics and sums in fp32.  With bf16 queries the softmax
+ * weights are rounded to 11 bits for the product with the values, with fp32 queries
+ * queries and weights are held in two such parts.  A code of NaN in a row that is seen gives NaN. */
+size_t mfs_quant_attention_workspace(const mfs_quant_kv* cache, int dtype, int n_q_heads);
+int mfs_quant_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const int32_t* kv_len, const void* q,
+                        long long q_stride, int n_q_heads, void* out, long long out_stride, float scale, int window,
+                        void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* ------------------------------------------------------------ shared prefixes
+ * mfs_paged_attention for a batch in groups of sequences that begin alike (one
+ * persona's or one system prompt's frames): the keys and values of a group's
+ * prefix are read and multiplied once for all its sequences.
+ *   groups     device [n_groups + 1]: sequences groups[i] .. groups[i + 1] - 1 are group
+ *              i (ascending; sequences outside every group are attended to by themselves)
+ *   prefix_len device [n_groups]: positions that the group's sequences have in common.
+ *              Their tables name the pages of all their positions, the shared
+ *              ones among them, and positions count from the prefix's first, as for
+ *              mfs_paged_attention: the result is that call's.  A prefix is
+ *              read by way of the table of one of the group's sequences that see it whole.
+ * A sequence that does not see its whole prefix (kv_len shorter than it, or a window
+ * that begins inside it) is attended to by itself, as is one that is alone in its
+ * group.  A bad page in a prefix gives NaN for those that share it.  bf16 queries: prefix products on the tensor cores,
+ * keys and values in bf16 (an 8-bit cache's values are exact in it), softmax weights
+ * rounded to bf16; fp32: on the CUDA cores in fp32.
+ *   workspace  of mfs_shared_attention_workspace() bytes for n_seqs sequences or more,
+ *              else as for mfs_paged_attention */
+size_t mfs_shared_attention_workspace(const mfs_paged_kv* cache, int n_q_heads, int n_seqs);
+int mfs_shared_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, int n_groups, const int32_t* groups,
+                         const int32_t* prefix_len, const void* q, long long q_stride, int n_q_heads, void* out,
+                         long long out_stride, float scale, int window, void* workspace, size_t workspace_bytes, void* cuda_stream);
+size_t mfs_quant_shared_attention_workspace(const mfs_quant_kv* cache, int dtype, int n_q_heads, int n_seqs);
+int mfs_quant_shared_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const int32_t* kv_len, int n_groups,
+                               const int32_t* groups, const int32_t* prefix_len, const void* q, long long q_stride, int n_q_heads,
+                               void* out, long long out_stride, float scale, int window, void* workspace, size_t workspace_bytes,
+                               void* cuda_stream);
 
 /* Causal attention over whole prompts, packed one behind the other:
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j,  j in [max(b, t - window + 1), t]
