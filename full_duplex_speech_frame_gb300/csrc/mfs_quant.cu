@@ -21,7 +21,9 @@ extern "C" int mfs_quant_attention(const mfs_quant_kv* cache, int dtype, int n_s
         return rc < 0 ? rc : MFS_OK;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
-    auto fn = dtype == MFS_DTYPE_BF16 ? (hd == 128 ? attention<PaKindE4m3<bf16, 128>> : attention<PaKindE4m3<bf16, 64>>)
-                                      : (hd == 128 ? attention<PaKindE4m3<float, 128>> : attention<PaKindE4m3<float, 64>>);
+    // bf16: blocks of eight or sixteen query heads; the second reads the cache once for groups of nine and more
+    auto fn = dtype == MFS_DTYPE_F32 ? (hd == 128 ? attention<PaKindE4m3<float, 128, 1>> : attention<PaKindE4m3<float, 64, 1>>)
+              : A.g <= 8             ? (hd == 128 ? attention<PaKindE4m3<bf16, 128, 1>> : attention<PaKindE4m3<bf16, 64, 1>>)
+                                     : (hd == 128 ? attention<PaKindE4m3<bf16, 128, 2>> : attention<PaKindE4m3<bf16, 64, 2>>);
     return fn(A, ws, st, op);
 }

@@ -7,7 +7,7 @@
 // rows' results; the pieces of others are left for each CTA, two at most.  What follows the prefix is each sequence's own:
 // paged_attention_kernel takes it, with the same split over its length.  The last kernel joins, for each sequence and head,
 // its own part and the prefix's pieces.
-#include "mfs_shared.cuh"
+#include "mfs_shared_mma.cuh"
 
 namespace {
 
@@ -34,7 +34,7 @@ __device__ __forceinline__ float4 codes_f32(unsigned w, float by)
     return make_float4(x.x * by, x.y * by, y.x * by, y.y * by);
 }
 
-template <typename T, int HD, int RT, bool QUANT>
+template <int HD, int RT, bool QUANT>
 __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_constant__ ShArgs A)
 {
     using S = SfShape<HD, RT>;
@@ -83,13 +83,13 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
         };
         auto fetch = [&](float* dst, bool key, int t) {
             const char* base = key ? A.C.k : A.C.v;
-            if constexpr (!QUANT && sizeof(T) == 4) {
+            if constexpr (!QUANT) {
                 for (int i = tid; i < SF_KEYS * (HD / 4); i += SF_THREADS) {
                     const int r = i / (HD / 4), c = i % (HD / 4) * 4;
                     const long long off = sh_off[t & 1][r];
                     copy16(su32(dst + r * LD + c), base + (off < 0 ? 0 : (off + c) * 4), off >= 0);
                 }
-            } else if constexpr (QUANT) {
+            } else {
                 for (int i = tid; i < SF_KEYS * (HD / 16); i += SF_THREADS) {
                     const int r = i / (HD / 16), c = i % (HD / 16) * 16;
                     const long long off = sh_off[t & 1][r];
@@ -97,15 +97,6 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
                     const float by = off < 0 ? 0.f : pow2_of(__ldg((key ? A.kx : A.vx) + sh_x[t & 1][r]));
                     float4* d = reinterpret_cast<float4*>(dst + r * LD + c);
                     d[0] = codes_f32(w.x, by); d[1] = codes_f32(w.y, by); d[2] = codes_f32(w.z, by); d[3] = codes_f32(w.w, by);
-                }
-            } else {
-                for (int i = tid; i < SF_KEYS * (HD / 8); i += SF_THREADS) {
-                    const int r = i / (HD / 8), c = i % (HD / 8) * 8;
-                    const long long off = sh_off[t & 1][r];
-                    const uint4 w = off < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + (off + c) * 2));
-                    float4* d = reinterpret_cast<float4*>(dst + r * LD + c);
-                    d[0] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-                    d[1] = make_float4(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u), __uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u));
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -116,8 +107,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int s = P.w.s0 + (r0 + r) / A.g, h = P.w.h * A.g + (r0 + r) % A.g;
-                const T* x = reinterpret_cast<const T*>(A.q) + (long long)s * A.q_stride + (long long)h * HD + c;
-                v = make_float4(to_f(x[0]), to_f(x[1]), to_f(x[2]), to_f(x[3]));
+                v = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(A.q) + (long long)s * A.q_stride + (long long)h * HD + c));
             }
             *reinterpret_cast<float4*>(sq + r * LD + c) = v;
         }
@@ -349,15 +339,15 @@ ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
     return s;
 }
 
-template <typename T, int HD, int RT, bool QUANT>
+template <int HD, int RT, bool QUANT>
 cudaError_t prefix_f32(const ShArgs& A, cudaStream_t st)
 {
     using S = SfShape<HD, RT>;
     int sms = 0;
     static mfs::PerDevice ready;
-    cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_f32<T, HD, RT, QUANT>, S::BYTES, &sms);
+    cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_f32<HD, RT, QUANT>, S::BYTES, &sms);
     if (e != cudaSuccess) return e;
-    shared_prefix_f32<T, HD, RT, QUANT><<<A.ctas, SF_THREADS, S::BYTES, st>>>(A);
+    shared_prefix_f32<HD, RT, QUANT><<<A.ctas, SF_THREADS, S::BYTES, st>>>(A);
     return cudaGetLastError();
 }
 
@@ -379,10 +369,14 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
     if (e != cudaSuccess) return mfs::op_launched(op, e);
     A.ctas = sms < SH_MAX_CTAS / 2 ? sms : SH_MAX_CTAS / 2;
-    {
+    if constexpr (sizeof(T) == 2) {
+        A.rows = 2 * SM_M;
+        A.tile = SM_M;
+        e = prefix_mma<HD, QUANT>(A, st);
+    } else {
         A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
         A.tile = SF_KEYS;
-        e = A.rows == 128 ? prefix_f32<T, HD, 8, QUANT>(A, st) : A.rows == 64 ? prefix_f32<T, HD, 4, QUANT>(A, st) : prefix_f32<T, HD, 2, QUANT>(A, st);
+        e = A.rows == 128 ? prefix_f32<HD, 8, QUANT>(A, st) : A.rows == 64 ? prefix_f32<HD, 4, QUANT>(A, st) : prefix_f32<HD, 2, QUANT>(A, st);
     }
     if (e != cudaSuccess) return mfs::op_launched(op, e);
     if (const int rc = attention<K>(P, ws + sp.own, st, op)) return rc;
@@ -467,6 +461,8 @@ extern "C" int mfs_quant_shared_attention(const mfs_quant_kv* cache, int dtype, 
     if (rc) return rc < 0 ? rc : MFS_OK;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
-    if (dtype == MFS_DTYPE_BF16) return hd == 128 ? shared<PaKindE4m3<bf16, 128, true>, true>(P, A, ws, st) : shared<PaKindE4m3<bf16, 64, true>, true>(P, A, ws, st);
-    return hd == 128 ? shared<PaKindE4m3<float, 128, true>, true>(P, A, ws, st) : shared<PaKindE4m3<float, 64, true>, true>(P, A, ws, st);
+    auto fn = dtype == MFS_DTYPE_F32 ? (hd == 128 ? shared<PaKindE4m3<float, 128, 1, true>, true> : shared<PaKindE4m3<float, 64, 1, true>, true>)
+              : P.g <= 8             ? (hd == 128 ? shared<PaKindE4m3<bf16, 128, 1, true>, true> : shared<PaKindE4m3<bf16, 64, 1, true>, true>)
+                                     : (hd == 128 ? shared<PaKindE4m3<bf16, 128, 2, true>, true> : shared<PaKindE4m3<bf16, 64, 2, true>, true>);
+    return fn(P, A, ws, st);
 }
