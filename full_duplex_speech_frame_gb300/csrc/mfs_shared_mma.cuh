@@ -18,8 +18,9 @@
 
 namespace {
 
+constexpr int SM_LOADERS = 4;
 constexpr int SM_M = 128;                     // rows of a row tile, positions of a tile
-constexpr int SM_THREADS = 384;               // warps 0-3, 4-7: softmax of the two row tiles; 8: MMA; 9-11: loads (11 also the parts)
+constexpr int SM_THREADS = 512;               // warps 0-3, 4-7: softmax of the two row tiles; 8: MMA; 9-12: loads; 15: the parts
 
 template <int HD>
 struct SmShape {
@@ -35,7 +36,7 @@ struct SmBars {
     int abort;  // a wait gave up
     int more, bad;
     ShPart part;
-    ShParts parts;  // warp 11's, between the parts
+    ShParts parts;  // warp 15's, between the parts
 };
 
 __device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 0, %0;" ::"n"(SM_THREADS) : "memory"); }
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
     if (tid == 0) {
         B.abort = 0;
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(&B.kv_full[i], 32);
+            bar_init(&B.kv_full[i], 32 * SM_LOADERS);
             bar_init(&B.kv_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&B.tmem)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == 11) {
+    if (warp == 15) {
         ShParts parts;
         const bool more = parts.start(A, blockIdx.x);
         if (lane == 0) {
@@ -101,9 +102,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
     fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, B.tmem, 0);  // columns: S of tile 0, S of tile 1, O of tile 0, O of tile 1
 
-    // registers: 384 threads x 168 at launch; the softmax warps take more, the others less
+    // registers: 512 threads x 128 at launch; the softmax warps take more, the others less
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         unsigned done = 0;  // tiles of the ring that earlier parts had
         bool ok = true;
         // MMA
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
             if (leader) commit(bar);
         };
         for (;;) {
-            if (warp == 11) {
+            if (warp == 15) {
                 ShPart p;
                 bool more = B.more;
                 if (more) {
@@ -202,29 +203,36 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
                     signal(&B.kv_empty[vs]);
                     if (next) signal(&B.kv_empty[ks]);
                 }
-            } else {
-                // the tiles' rows, four a lane: where they lie, -1 for those past the prefix
-                long long off[4];
-                unsigned exps = 0;  // of the rows, a byte each
-                auto look_up = [&](int n) {
-                    exps = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const long long p = (long long)(P.from + (n >> 1)) * SM_M + lane + 32 * i;
-                        off[i] = -1;
-                        int page, row;
-                        if (n >= nl || p >= P.w.p) continue;
-                        if (!row_place(A.C, P.reader, (int)p, page, row)) {
-                            *(volatile int*)&B.bad = 1;
-                            continue;
-                        }
-                        off[i] = (long long)page * A.C.page_stride + (long long)row * A.C.row_stride + (long long)P.w.h * A.C.head_stride;
-                        if (QUANT)
-                            exps |= (unsigned)__ldg((n & 1 ? A.vx : A.kx) + (long long)page * A.x_page + (long long)row * A.x_row + (long long)P.w.h * A.x_head) << (8 * i);
-                    }
+            } else if (warp - 9 < SM_LOADERS) {
+                // 32 rows of each tile, one a lane: pages are looked up two tiles ahead, offsets and exponents found one ahead
+                const int row0 = 32 * (warp - 9);
+                int page, in_page;  // page -1: none or a bad one, -2: past the prefix
+                auto look_up = [&](int t) {
+                    const long long p = (long long)(P.from + t) * SM_M + row0 + lane;
+                    const int j = (int)min(p, (long long)P.w.p) / A.C.page_size;
+                    in_page = (int)p - j * A.C.page_size;
+                    page = t >= nt || p >= P.w.p ? -2 : j < A.C.table_width ? __ldg(A.C.table + P.reader * A.C.table_stride + j) : -1;
                 };
-                int n = (int)((unsigned)(warp - 9 + 3) - done % 3u) % 3, slot = (done + n) % STAGES, waiting = -1;
-                unsigned par = (((done + n) / STAGES) & 1) ^ 1;
+                struct Row {
+                    long long off;  // bytes; a row without a page has the cache's first, whatever it is
+                    unsigned xk, xv;
+                };
+                auto resolve = [&]() {
+                    Row R = {0, 0u, 0u};
+                    if (page >= 0 && page < A.C.n_pages) {
+                        R.off = ((long long)page * A.C.page_stride + (long long)in_page * A.C.row_stride + (long long)P.w.h * A.C.head_stride) * (QUANT ? 1 : 2);
+                        if (QUANT) {
+                            const long long x = (long long)page * A.x_page + (long long)in_page * A.x_row + (long long)P.w.h * A.x_head;
+                            R.xk = __ldg(A.kx + x);
+                            R.xv = __ldg(A.vx + x);
+                        }
+                    } else if (page != -2) {
+                        *(volatile int*)&B.bad = 1;
+                    }
+                    return R;
+                };
+                int slot = done % STAGES, waiting = -1;
+                unsigned par = ((done / STAGES) & 1) ^ 1;
                 auto landed = [&](int ahead) {  // the copies before the last `ahead` are there: passed on
                     if (ahead) asm volatile("cp.async.wait_group 1;" ::: "memory");
                     else asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -232,56 +240,82 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
                     bar_arrive(&B.kv_full[waiting]);
                     waiting = -1;
                 };
-                look_up(n);
-                for (; n < nl; n += 3) {
-                    if (waiting >= 0 && !__all_sync(0xffffffffu, bar_try(&B.kv_empty[slot], par))) landed(0);
-                    ok = bar_wait(&B.kv_empty[slot], par, &B.abort);
-                    if (!ok) break;
-                    const char* src = n & 1 ? A.C.v : A.C.k;
-                    char* dst = ring + slot * S::TILE;
-                    if constexpr (!QUANT) {
-                        constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows of an instruction
-                        const int ch = lane % CH;
+                // 16-byte chunks of a row, rows of an instruction, instructions of 32 rows
+                constexpr int CH = QUANT ? HD / 16 : HD / 8, RPI = 32 / CH, NI = 32 / RPI;
+                const int ch = lane % CH, sub = lane / CH;
+                uint4 w[QUANT ? NI : 1];
+                auto load = [&](int j, const char* from, int t) {  // codes of instruction j's rows
+                    const long long left = (long long)P.w.p - (long long)(P.from + t) * SM_M - row0;
+                    const unsigned long long o = __shfl_sync(0xffffffffu, (unsigned long long)from, j * RPI + sub);
+                    w[QUANT ? j : 0] = j * RPI + sub < left ? __ldg(reinterpret_cast<const uint4*>(o) + ch) : make_uint4(0u, 0u, 0u, 0u);
+                };
+                Row now = {0, 0u, 0u}, then = {0, 0u, 0u};
+                if (nt > 0) {
+                    look_up(0);
+                    now = resolve();
+                    look_up(1);
+                    if constexpr (QUANT) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll 8
-                            for (int j = 0; j < 32; j += RPI) {
-                                const int in = j + lane / CH, row = 32 * i + in;
-                                const long long o = __shfl_sync(0xffffffffu, off[i], in);
-                                copy16(su32(dst + (ch / 8) * S::BOX + row * 128 + (((ch % 8) ^ (row & 7)) << 4)), src + (o < 0 ? 0 : (o + 8 * ch) * 2), o >= 0);
-                            }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        if (waiting >= 0) landed(1);
-                        waiting = slot;
-                    } else {
-                        constexpr int CH = HD / 16, RPI = 32 / CH;  // 16-byte chunks of a row's codes
-                        const int ch = lane % CH;
-                        const unsigned x4 = exps;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint4 w[CH];
-#pragma unroll
-                            for (int j = 0; j < CH; ++j) {
-                                const long long o = __shfl_sync(0xffffffffu, off[i], j * RPI + lane / CH);
-                                w[j] = o < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(src + o + 16 * ch));
-                            }
-#pragma unroll
-                            for (int j = 0; j < CH; ++j) {
-                                const int in = j * RPI + lane / CH, row = 32 * i + in;
-                                const float by = pow2_of(__shfl_sync(0xffffffffu, x4, in) >> (8 * i) & 255u);
-                                uint4 a, b;
-                                codes_bf16(w[j], by, a, b);
-                                char* d = dst + (ch / 4) * S::BOX + row * 128;
-                                *reinterpret_cast<uint4*>(d + (((2 * ch % 8) ^ (row & 7)) << 4)) = a;
-                                *reinterpret_cast<uint4*>(d + ((((2 * ch + 1) % 8) ^ (row & 7)) << 4)) = b;
-                            }
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        bar_arrive(&B.kv_full[slot]);
+                        for (int j = 0; j < NI; ++j) load(j, A.C.k + now.off, 0);
                     }
-                    look_up(n + 3);
-                    slot += 3;
-                    if (slot >= STAGES) { slot -= STAGES; par ^= 1; }
+                }
+                for (int t = 0; t < nt && ok; ++t) {
+                    then = resolve();
+                    look_up(t + 2);
+                    const long long left = (long long)P.w.p - (long long)(P.from + t) * SM_M - row0;  // of the warp's rows, those of the prefix
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (waiting >= 0 && !__all_sync(0xffffffffu, bar_try(&B.kv_empty[slot], par))) landed(0);
+                        ok = ok && bar_wait(&B.kv_empty[slot], par, &B.abort);
+                        if (!ok) break;
+                        char* dst = ring + slot * S::TILE + row0 * 128;
+                        if constexpr (!QUANT) {
+                            // (few instructions for each copy: a warp issues them one behind the other)
+                            const unsigned long long src = (unsigned long long)((kv ? A.C.v : A.C.k) + now.off);
+                            const unsigned to = su32(dst + (ch / 8) * S::BOX) + sub * 128;
+                            unsigned at[8 / RPI];  // of eight rows
+#pragma unroll
+                            for (int j = 0; j < 8 / RPI; ++j) at[j] = to + j * RPI * 128 + (((ch % 8) ^ (j * RPI + sub)) << 4);
+                            auto copy = [&](auto whole) {
+#pragma unroll
+                                for (int j0 = 0; j0 < 32; j0 += 8) {
+                                    unsigned long long o[8 / RPI];
+#pragma unroll
+                                    for (int j = 0; j < 8 / RPI; ++j) o[j] = __shfl_sync(0xffffffffu, src, j0 + j * RPI + sub) + 16 * ch;
+#pragma unroll
+                                    for (int j = 0; j < 8 / RPI; ++j) {
+                                        if (decltype(whole)::value)
+                                            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(at[j] + j0 * 128), "l"(o[j]) : "memory");
+                                        else
+                                            copy16(at[j] + j0 * 128, (const void*)o[j], j0 + j * RPI + sub < left);
+                                    }
+                                }
+                            };
+                            if (left >= 32) copy(std::true_type());
+                            else copy(std::false_type());
+                            asm volatile("cp.async.commit_group;" ::: "memory");
+                            if (waiting >= 0) landed(1);
+                            waiting = slot;
+                        } else {
+                            const bool more = kv == 0 || t + 1 < nt;
+                            const char* next = kv ? A.C.k + then.off : A.C.v + now.off;
+#pragma unroll
+                            for (int j = 0; j < NI; ++j) {
+                                const int r = j * RPI + sub;
+                                const float by = pow2_of(__shfl_sync(0xffffffffu, kv ? now.xv : now.xk, r));
+                                uint4 x, y;
+                                codes_bf16(w[j], by, x, y);
+                                char* d = dst + (ch / 4) * S::BOX + r * 128;
+                                *reinterpret_cast<uint4*>(d + (((2 * ch % 8) ^ (r & 7)) << 4)) = x;
+                                *reinterpret_cast<uint4*>(d + ((((2 * ch + 1) % 8) ^ (r & 7)) << 4)) = y;
+                                if (more) load(j, next, t + kv);
+                            }
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            bar_arrive(&B.kv_full[slot]);
+                        }
+                        if (++slot == STAGES) { slot = 0; par ^= 1; }
+                    }
+                    now = then;
                 }
                 if (waiting >= 0) landed(0);
                 asm volatile("cp.async.wait_all;" ::: "memory");
@@ -294,7 +328,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
             if (leader) bar_drain(&B.drained, 0);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int x = warp >> 2, row = tid & (SM_M - 1);
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tm + lanes + x * SM_M, to = tm + lanes + 2 * SM_M + x * HD;
