@@ -75,7 +75,7 @@ __device__ __forceinline__ unsigned to_e4m3(float a, float b, float c, float d)
 // a magnitude.  2: as 1, and the cache has 8 bits: the lanes that share a row find its largest value, and from it the
 // exponent; the key is quantised as rotated in 32 bits, not as rounded for k_out.
 template <typename T, int HD, int TT, int MODE>
-__global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constant__ ApArgs<T> A)
+__global__ void __launch_bounds__(AP_THREADS, MODE == 2 ? 8 : 1) append_kernel(const __grid_constant__ ApArgs<T> A)
 {
     constexpr int VE = 16 / sizeof(T);        // elements per vector
     constexpr int IPH = HD / (2 * VE);        // items per head
@@ -110,8 +110,10 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
         // plain loads: the queries and keys may be their own outputs
         return Vec2<T>{*reinterpret_cast<const uint4*>(p + first), *reinterpret_cast<const uint4*>(p + second)};
     };
+    // MODE 1, 2: few tokens' items are dealt to several blocks each
+    const int begin = MODE ? blockIdx.y * AP_THREADS + tid : tid, every = MODE ? gridDim.y * AP_THREADS : AP_THREADS;
     Vec2<T> x;
-    if (tid < items) x = source(tid);
+    if (begin < items) x = source(begin);
 
     if (warp < nt) {
         int s, page = 0, r = 0;
@@ -212,9 +214,9 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const __grid_constan
             put(reinterpret_cast<T*>(key ? A.C.k : A.C.v) + r + (long long)hk * A.C.head_stride);
         }
     };
-    for (int i = tid; i < items; i += AP_THREADS) {
+    for (int i = begin; i < items; i += every) {
         const Vec2<T> y = x;
-        if (i + AP_THREADS < items) x = source(i + AP_THREADS);
+        if (i + every < items) x = source(i + every);
         finish(i, y);
     }
 }
@@ -226,7 +228,11 @@ int append(const ApArgs<T>& A, cudaStream_t st)
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, nullptr, 0, &sms);
     if (e == cudaSuccess) {
-        if (A.n_tokens <= 8 * sms) append_kernel<T, HD, 1, MODE><<<A.n_tokens, AP_THREADS, 0, st>>>(A);
+        // as many blocks for a token as its items fill, up to eight per SM in all
+        const long long items = (long long)(A.hq + 2 * A.C.n_kv_heads) * (HD * (int)sizeof(T) / 32), most = (items - 1) / AP_THREADS + 1;
+        const long long room = 8LL * sms / (A.n_tokens > 0 ? A.n_tokens : 1);
+        const unsigned each = MODE == 0 || room < 2 ? 1u : (unsigned)(room < most ? room : most);
+        if (A.n_tokens <= 8 * sms) append_kernel<T, HD, 1, MODE><<<dim3(A.n_tokens, each), AP_THREADS, 0, st>>>(A);
         else append_kernel<T, HD, AP_TOKENS, MODE><<<(A.n_tokens + AP_TOKENS - 1) / AP_TOKENS, AP_THREADS, 0, st>>>(A);
         e = cudaGetLastError();
     }
@@ -326,9 +332,10 @@ int append_ropes(const Append& P, const Cache& C, int hd, const mfs_rope* rope, 
 
 // -------------------------------------------------------------------- read
 
-// The last rows of each sequence, packed: a block takes RD_TOKENS tokens, a warp for each to find its place, and the block's
-// threads move the tokens' keys and values by 16 bytes of output, RD_AHEAD of them on their way at once.
-constexpr int RD_THREADS = 256, RD_TOKENS = 8, RD_AHEAD = 4;
+// The last rows of each sequence, packed: a block takes a few tokens (about RD_ROWS rows of keys and values), then others,
+// until there are none.  A warp for each token finds its place, which takes several dependent reads, while the rows of the
+// tokens before are on their way; the block's threads move these by 16 bytes of output, RD_AHEAD of them at once.
+constexpr int RD_THREADS = 256, RD_TOKENS = 8, RD_ROWS = 128, RD_AHEAD = 8, RD_BLOCKS = 4;
 
 struct RdArgs {
     Cache C;
@@ -336,6 +343,8 @@ struct RdArgs {
     char *k, *v;                    // out
     long long k_stride, v_stride;   // bytes
     int n_tokens, n_seqs;
+    int tokens;        // of a block
+    unsigned inverse;  // 2^32 / (2 n_kv_heads), rounded up: exact for the rows of a block, which are fewer than 2^16 where tokens > 1
     const uint8_t *kx, *vx;
     long long x_page, x_head, x_row;
 };
@@ -352,85 +361,101 @@ __device__ __forceinline__ float4 from_e4m3(unsigned w, unsigned b)
 
 // T: of the output; the cache has the same, or 8 bits (QUANT)
 template <typename T, int HD, bool QUANT>
-__global__ void __launch_bounds__(RD_THREADS) read_kernel(const __grid_constant__ RdArgs A)
+__global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __grid_constant__ RdArgs A)
 {
     constexpr int VE = 16 / sizeof(T), IPH = HD / VE;  // elements of an item, items per row
     constexpr int CE = QUANT ? 1 : sizeof(T);
-    __shared__ long long row[RD_TOKENS], xrow[RD_TOKENS];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int t0 = blockIdx.x * RD_TOKENS, nt = min(RD_TOKENS, A.n_tokens - t0), hkv = A.C.n_kv_heads;
-    if (warp < nt) {
+    __shared__ long long places[2][2][RD_TOKENS];  // of this turn's tokens and the next's: row -1: none, -2: no token; exponents
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hkv = A.C.n_kv_heads;
+    auto look_up = [&](int t0, int turn) {
+        if (warp >= A.tokens || t0 + warp >= A.n_tokens) return;
         int s, page = 0, r = 0;
         long long pos;
         const bool is = token_place(A.cu, A.kv_len, A.n_seqs, t0 + warp, s, pos);
         if (lane == 0) {
             const bool has = is && pos >= 0 && pos <= 0x7fffffff && row_place(A.C, s, (int)pos, page, r);
-            row[warp] = !is ? -2 : !has ? -1 : (long long)page * A.C.page_stride + (long long)r * A.C.row_stride;
-            xrow[warp] = (long long)page * A.x_page + (long long)r * A.x_row;
+            places[turn][0][warp] = !is ? -2 : !has ? -1 : (long long)page * A.C.page_stride + (long long)r * A.C.row_stride;
+            places[turn][1][warp] = (long long)page * A.x_page + (long long)r * A.x_row;
         }
-    }
+    };
+    long long t0 = (long long)blockIdx.x * A.tokens;
+    const long long ahead = (long long)gridDim.x * A.tokens;
+    look_up((int)t0, 0);
     __syncthreads();
-    const int items = nt * 2 * hkv * IPH;  // of a token: keys of all heads, then values
-    for (int i0 = tid; i0 < items; i0 += RD_THREADS * RD_AHEAD) {
-        uint4 x[RD_AHEAD];
-        unsigned b[RD_AHEAD];
-#pragma unroll
-        for (int j = 0; j < RD_AHEAD; ++j) {
-            const int i = i0 + j * RD_THREADS;
-            if (i >= items) break;
-            const int hh = i / IPH, e = i % IPH, t = hh / (2 * hkv), h2 = hh - t * 2 * hkv;
-            const bool key = h2 < hkv;
-            const int h = key ? h2 : h2 - hkv;
-            const long long r = row[t];
-            if (r < 0) continue;
-            const char* p = (key ? A.C.k : A.C.v) + (r + (long long)h * A.C.head_stride + e * VE) * CE;
-            if constexpr (!QUANT) {
-                x[j] = __ldg(reinterpret_cast<const uint4*>(p));
-            } else {
-                if constexpr (VE == 8) {
-                    const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
-                    x[j].x = y.x;
-                    x[j].y = y.y;
-                } else {
-                    x[j].x = __ldg(reinterpret_cast<const unsigned*>(p));
+    for (int turn = 0; t0 < A.n_tokens; t0 += ahead, turn ^= 1) {
+        const long long *row = places[turn][0], *xrow = places[turn][1];
+        const int nt = (int)min((long long)A.tokens, A.n_tokens - t0);
+        bool found = t0 + ahead >= A.n_tokens;  // the next tokens' places
+        // rows of a token: keys of all heads, then values; a thread has item e of every RD_THREADS / IPH-th row
+        const int rows = nt * 2 * hkv, e = tid % IPH;
+        for (int r0 = tid / IPH; r0 < rows || !found; r0 += RD_THREADS / IPH * RD_AHEAD) {
+            uint4 x[RD_AHEAD];
+            unsigned b[RD_AHEAD];
+            char* out[RD_AHEAD];  // null: nothing to write
+    #pragma unroll
+            for (int j = 0; j < RD_AHEAD; ++j) {
+                const int i = r0 + j * (RD_THREADS / IPH);
+                out[j] = nullptr;
+                if (i >= rows) continue;
+                const int t = A.tokens == 1 ? 0 : (int)__umulhi((unsigned)i, A.inverse), h2 = i - t * 2 * hkv;
+                const bool key = h2 < hkv;
+                const int h = key ? h2 : h2 - hkv;
+                const long long r = row[t];
+                if (r == -2) continue;
+                out[j] = (key ? A.k + (t0 + t) * A.k_stride : A.v + (t0 + t) * A.v_stride) + (long long)h * HD * sizeof(T) + e * 16;
+                if (r < 0) {  // no page: NaN
+                    const unsigned nan = QUANT ? 0x7f7f7f7fu : sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
+                    x[j] = make_uint4(nan, nan, nan, nan);
+                    b[j] = 127;
+                    continue;
                 }
-                b[j] = __ldg((key ? A.kx : A.vx) + xrow[t] + (long long)h * A.x_head);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < RD_AHEAD; ++j) {
-            const int i = i0 + j * RD_THREADS;
-            if (i >= items) break;
-            const int hh = i / IPH, e = i % IPH, t = hh / (2 * hkv), h2 = hh - t * 2 * hkv;
-            const bool key = h2 < hkv;
-            const int h = key ? h2 : h2 - hkv;
-            const long long r = row[t];
-            if (r == -2) continue;
-            uint4 y;
-            if (r < 0) {
-                const unsigned nan = sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-                y = make_uint4(nan, nan, nan, nan);
-            } else if constexpr (!QUANT) {
-                y = x[j];
-            } else {
-                const float4 f = from_e4m3(x[j].x, b[j]);
-                if constexpr (VE == 8) {
-                    const float4 g = from_e4m3(x[j].y, b[j]);
-                    y = make_uint4(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w), pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
+                const char* p = (key ? A.C.k : A.C.v) + (r + (long long)h * A.C.head_stride + e * VE) * CE;
+                if constexpr (!QUANT) {
+                    x[j] = __ldg(reinterpret_cast<const uint4*>(p));
                 } else {
-                    memcpy(&y, &f, 16);
+                    if constexpr (VE == 8) {
+                        const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
+                        x[j].x = y.x;
+                        x[j].y = y.y;
+                    } else {
+                        x[j].x = __ldg(reinterpret_cast<const unsigned*>(p));
+                    }
+                    b[j] = __ldg((key ? A.kx : A.vx) + xrow[t] + (long long)h * A.x_head);
                 }
             }
-            char* o = key ? A.k + (t0 + t) * A.k_stride : A.v + (t0 + t) * A.v_stride;
-            *reinterpret_cast<uint4*>(o + (long long)h * HD * sizeof(T) + e * 16) = y;
+            if (!found) look_up((int)(t0 + ahead), turn ^ 1);
+            found = true;
+    #pragma unroll
+            for (int j = 0; j < RD_AHEAD; ++j) {
+                if (!out[j]) continue;
+                uint4 y = x[j];
+                if constexpr (QUANT) {
+                    const float4 f = from_e4m3(x[j].x, b[j]);
+                    if constexpr (VE == 8) {
+                        const float4 g = from_e4m3(x[j].y, b[j]);
+                        y = make_uint4(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w), pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
+                    } else {
+                        memcpy(&y, &f, 16);
+                    }
+                }
+                *reinterpret_cast<uint4*>(out[j]) = y;
+            }
         }
+        __syncthreads();
     }
 }
 
 template <typename T, bool QUANT>
-int read_rows(const RdArgs& A, int hd, cudaStream_t st)
+int read_rows(RdArgs A, int hd, cudaStream_t st)
 {
-    const int blocks = (A.n_tokens - 1) / RD_TOKENS + 1;
+    const int rows = 2 * A.C.n_kv_heads;
+    A.tokens = rows >= RD_ROWS ? 1 : RD_ROWS / rows < RD_TOKENS ? RD_ROWS / rows : RD_TOKENS;
+    A.inverse = (unsigned)(((1ull << 32) + rows - 1) / rows);
+    int sms = 0;
+    static mfs::PerDevice known;
+    const cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
+    if (e != cudaSuccess) return mfs::op_launched("kv_read", e);
+    const int turns = (A.n_tokens - 1) / A.tokens + 1, blocks = turns < RD_BLOCKS * sms ? turns : RD_BLOCKS * sms;
     if (hd == 128) read_kernel<T, 128, QUANT><<<blocks, RD_THREADS, 0, st>>>(A);
     else read_kernel<T, 64, QUANT><<<blocks, RD_THREADS, 0, st>>>(A);
     return mfs::op_launched("kv_read", cudaGetLastError());

@@ -17,18 +17,30 @@ struct Cache {
     const int32_t* table;
     int table_width, n_pages, page_size, n_kv_heads;
     long long table_stride, page_stride, head_stride, row_stride;  // elements
+    unsigned by, shift;  // p / page_size = (p by) >> (32 + shift) for 0 <= p < 2^31
 };
 
 Cache cache_of(const mfs_paged_kv* c)
 {
+    // by = 2^(32 + shift) / page_size rounded up with shift the least that 2^(shift + 1) >= page_size: by < 2^32, and its excess
+    // of less than 1 makes (p by) / 2^(32 + shift) too large by less than 2^31 / 2^(32 + shift) <= 1 / page_size
+    unsigned shift = 0;
+    while ((2 << shift) < c->page_size) ++shift;
+    const unsigned by = c->page_size == 1 ? 0xffffffffu : (unsigned)(((1ull << (32 + shift)) + c->page_size - 1) / c->page_size);
     return {(char*)c->k, (char*)c->v, c->table, c->table_width, c->n_pages, c->page_size, c->n_kv_heads,
-            c->table_stride, c->page_stride, c->head_stride, c->row_stride};
+            c->table_stride, c->page_stride, c->head_stride, c->row_stride, by, shift};
+}
+
+// p / page_size for p >= 0
+__device__ __forceinline__ int page_of(const Cache& C, int p)
+{
+    return C.page_size == 1 ? p : (int)(__umulhi((unsigned)p, C.by) >> C.shift);
 }
 
 // Page and row of position p of sequence s; false where the table has no valid page for it.
 __device__ __forceinline__ bool row_place(const Cache& C, int s, int p, int& page, int& row)
 {
-    const int j = p / C.page_size;
+    const int j = page_of(C, p);
     if (p < 0 || j >= C.table_width) return false;
     page = __ldg(C.table + s * C.table_stride + j);
     row = p - j * C.page_size;
@@ -71,7 +83,7 @@ __device__ __forceinline__ bf16 from_f(float x) { return __float2bfloat16_rn(x);
 // tensor pipe 17 % busy there, so the wide forms of them would gain nothing.
 
 constexpr int PA_WARPS = 4;
-constexpr int PA_MAX_CTAS = 304;  // 2 per SM
+constexpr int PA_SMS = 152;
 // What an item costs beside its tiles (its start, its end, its queries), in tiles: shares are cut over both.  64 ragged
 // sequences of up to 1000, 24 + 8 heads of 128: 44.3 us with 0, 35.7 with 1, 35.9 with 2, 35.6 with 4; 256 of up to 300,
 // 32 + 8 heads: 53.9, 44.0, 43.0, 44.3, fp32 139, 85, 81, 82; 64 of up to 100, 8 + 8 heads: 13.7, 12.7, 13.0, 14.1.
@@ -142,6 +154,7 @@ struct PaArgs {
     // 8-bit caches: an exponent per row
     const uint8_t *kx, *vx;
     long long x_page, x_head, x_row;
+    float* fronts;    // [CTA][PA_WARPS][GM][HD]
     // behind a shared prefix: what follows it is attended to, and what comes of it goes to own_o [n_seqs][hq][HD] and own_ml
     // [n_seqs][hq] (maximum, sum)
     const int32_t *groups, *prefix_len;
@@ -242,6 +255,31 @@ __device__ __forceinline__ void pa_issue(const PaArgs& A, unsigned stage, long l
         copy16(dst, A.C.k + byte, o >= 0);
         copy16(dst + ROWS * HD * CE, A.C.v + byte, o >= 0);
     }
+}
+
+// The same for codes, in fewer instructions: a tile takes half the copies' time.  left: positions from the tile's first on.
+template <typename K>
+__device__ __forceinline__ void pa_issue_codes(const PaArgs& A, unsigned stage, long long off, int left)
+{
+    constexpr int HD = K::HD, CH = HD / 16, RPI = 32 / CH, ROWS = K::ROWS, SAME = 8 / RPI;  // instructions until the banks repeat
+    const int lane = threadIdx.x & 31, ch = lane % CH, sub = lane / CH;
+    const unsigned long long first = (unsigned long long)A.C.k, row = first + (off < 0 ? 0 : off);  // without a page: the cache's first, whatever it is
+    const unsigned long long to_v = (unsigned long long)A.C.v - first;
+    unsigned at[SAME];
+#pragma unroll
+    for (int j = 0; j < SAME; ++j) at[j] = stage + (j * RPI + sub) * HD + (pa_chunk<CH>(j * RPI + sub, ch) << 4);
+    auto copy = [&](auto whole) {
+#pragma unroll
+        for (int j = 0; j < ROWS / RPI; ++j) {
+            const unsigned long long src = __shfl_sync(0xffffffffu, row, j * RPI + sub) + 16 * ch;
+            const unsigned dst = at[j % SAME] + j / SAME * (8 * HD);
+            const bool in = decltype(whole)::value || j * RPI + sub < left;
+            copy16(dst, (const void*)src, in);
+            copy16(dst + ROWS * HD, (const void*)(src + to_v), in);
+        }
+    };
+    if (left >= ROWS) copy(std::true_type());
+    else copy(std::false_type());
 }
 
 // One warp's state for an item: scores by mma for bf16 (16 query heads per tile, the rest zero).
@@ -457,7 +495,7 @@ struct PaF32 {
     __device__ __forceinline__ bool owner() const { return (threadIdx.x & 31) == 0; }
 };
 
-// x y / z for x <= PA_WARPS * PA_MAX_CTAS or so; 32 bits where they suffice (a 64-bit division takes about 100 instructions)
+// x y / z for x <= 4096 or so; 32 bits where they suffice (a 64-bit division takes about 100 instructions)
 __device__ __forceinline__ long long muldiv(long long x, long long y, long long z)
 {
     if (y < (1ll << 20) && x < 4096) return (unsigned)x * (unsigned)y / (unsigned)z;
@@ -472,6 +510,7 @@ struct PaKindBf16 {
     using T = bf16;
     using State = PaBf16<HD_>;
     static constexpr int HD = HD_, GM = 16, CE = 2, ROWS = 2048 / HD, STAGES = PA_STAGES, Q = 0;
+    static constexpr int BLOCKS = 2, ITEM = PA_ITEM;  // per SM
     static constexpr bool QUANT = false, SHARED = SHARED_;
 };
 template <int HD_, int GM_, bool SHARED_ = false>
@@ -479,6 +518,7 @@ struct PaKindF32 {
     using T = float;
     using State = PaF32<HD_, GM_>;
     static constexpr int HD = HD_, GM = GM_, CE = 4, ROWS = 1024 / HD, STAGES = PA_STAGES, Q = PA_WARPS * GM * HD * 4;
+    static constexpr int BLOCKS = 2, ITEM = PA_ITEM;  // per SM
     static constexpr bool QUANT = false, SHARED = SHARED_;
 };
 
@@ -487,7 +527,8 @@ struct PaLayout {
     static constexpr int HD = K::HD, GM = K::GM, Q = K::Q;
     static constexpr int STAGE = K::ROWS * HD * K::CE * 2;  // keys and values of a tile
     static constexpr int RING = PA_WARPS * K::STAGES * STAGE;
-    static constexpr int FRONTS = PA_WARPS * GM * HD * 4;  // an item's end per warp, kept until the CTA's warps are done
+    // an item's end per warp, kept until the CTA's warps are done; 8-bit caches: in the workspace, so that a third block fits
+    static constexpr int FRONTS = K::QUANT ? 0 : PA_WARPS * GM * HD * 4;
     static constexpr int BYTES = RING + FRONTS + Q;
     static_assert(GM * HD * 4 <= STAGE, "a warp's piece takes a stage's place");
 };
@@ -499,7 +540,7 @@ struct PaPiece {
 };
 
 template <typename K>
-__global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const __grid_constant__ PaArgs A)
+__global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kernel(const __grid_constant__ PaArgs A)
 {
     using L = PaLayout<K>;
     using T = typename K::T;
@@ -515,8 +556,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
     __shared__ float2 sh_sum[2 * PA_WARPS][GM];  // maximum and sum of the pieces of an item, at its first
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hx = A.C.n_kv_heads * A.nhb, G = gridDim.x, cta = blockIdx.x;
-    float* fronts = reinterpret_cast<float*>(pa_raw + L::RING);
-    float* sq = fronts + (PA_WARPS + warp) * GM * HD;
+    float* fronts = K::QUANT ? A.fronts + (long long)cta * PA_WARPS * GM * HD : reinterpret_cast<float*>(pa_raw + L::RING);
+    float* sq = reinterpret_cast<float*>(pa_raw + L::RING) + (PA_WARPS + warp) * GM * HD;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // sequences of no length: zeros
@@ -525,12 +566,12 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             for (int i = tid; i < A.hq * HD; i += PA_WARPS * 32)
                 reinterpret_cast<T*>(A.out)[(long long)s * A.out_stride + i] = from_f<T>(0.f);
 
-    // the tiles of the call, PA_ITEM more for each item
+    // the tiles of the call, K::ITEM more for each item
     auto tiles_of = [&](int s) {
         PaWalk w;
         w.s = s;
         pa_sequence<K>(A, w);
-        return w.ntiles ? w.ntiles + PA_ITEM : 0;
+        return w.ntiles ? w.ntiles + K::ITEM : 0;
     };
     long long mine = 0;
     for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) mine += tiles_of(s);
@@ -550,7 +591,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         const long long t0 = muldiv(share, total, shares), t1 = muldiv(share + 1, total, shares);
         // where the share starts
         PaWalk use;
-        long long item_first = 0;  // where the item begins: PA_ITEM empty places, then its tiles
+        long long item_first = 0;  // where the item begins: K::ITEM empty places, then its tiles
         for (int b = 0; b < A.n_seqs; b += 32) {
             const int s = b + lane;
             const long long v = s < A.n_seqs ? (long long)tiles_of(s) * Hx : 0;
@@ -570,10 +611,10 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         }
         pa_sequence<K>(A, use);
         const long long in = t0 - item_first;
-        use.hb = (int)(in >> 32 ? in / (use.ntiles + PA_ITEM) : (unsigned)in / (unsigned)(use.ntiles + PA_ITEM));
-        item_first += (long long)use.hb * (use.ntiles + PA_ITEM);
-        use.tile = max(0, (int)(t0 - item_first) - PA_ITEM);
-        long long at = item_first + PA_ITEM + use.tile;  // where the tile of `use` lies
+        use.hb = (int)(in >> 32 ? in / (use.ntiles + K::ITEM) : (unsigned)in / (unsigned)(use.ntiles + K::ITEM));
+        item_first += (long long)use.hb * (use.ntiles + K::ITEM);
+        use.tile = max(0, (int)(t0 - item_first) - K::ITEM);
+        long long at = item_first + K::ITEM + use.tile;  // where the tile of `use` lies
         PaWalk load = use;
         char* ring_p = pa_raw + warp * (S * L::STAGE);
         const unsigned ring = su32(ring_p);
@@ -592,8 +633,8 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
         long long off = at < t1 ? pa_offset<K>(A, load, next_bad, x_at) : -1;
         auto issue = [&](int stage) {
             if constexpr (K::QUANT) {
-                static_assert(ROWS == 32 && S >= 2, "a lane has a row's exponents, and they are there a tile later");
-                if (x_stage >= 0) {
+                static_assert(ROWS <= 32 && S >= 2, "a lane has a row's exponents, and they are there a tile later");
+                if (x_stage >= 0 && lane < ROWS) {
                     sh_x[warp][x_stage][0][lane] = (uint8_t)x_next;
                     sh_x[warp][x_stage][1][lane] = (uint8_t)(x_next >> 8);
                 }
@@ -604,10 +645,11 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                 }
             }
             if (at_load < t1) {
-                pa_issue<K>(A, ring + stage * L::STAGE, off);
+                if constexpr (K::QUANT) pa_issue_codes<K>(A, ring + stage * L::STAGE, off, load.len - (load.lo + load.tile * ROWS));
+                else pa_issue<K>(A, ring + stage * L::STAGE, off);
                 bad_ring = (bad_ring & ~(1u << stage)) | (__any_sync(0xffffffffu, next_bad) ? 1u << stage : 0u);
                 next_bad = false;
-                at_load += load.tile + 1 < load.ntiles ? 1 : 1 + PA_ITEM;
+                at_load += load.tile + 1 < load.ntiles ? 1 : 1 + K::ITEM;
                 if (at_load < t1) {
                     pa_next<K>(A, load);
                     off = pa_offset<K>(A, load, next_bad, x_at);
@@ -636,7 +678,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
             bad = bad || ((bad_ring >> stage) & 1u);
             __syncwarp();
             const bool ends = use.tile + 1 == use.ntiles;
-            at += ends ? 1 + PA_ITEM : 1;
+            at += ends ? 1 + K::ITEM : 1;
             const bool end = at >= t1;
             if (ends || end) {
                 // the item's output, through the stage just read: one place in the code writes the accumulators, which
@@ -679,14 +721,14 @@ __global__ void __launch_bounds__(PA_WARPS * 32, 2) paged_attention_kernel(const
                         __syncwarp();
                     }
                     if (lane == 0)
-                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + PA_ITEM + use.ntiles), stage};
+                        sh_piece[slot] = {use.s, use.hb, front, ends, owner(item_first + K::ITEM + use.ntiles), stage};
                 }
                 fresh = true;
             }
             issue(stage);
             stage = stage + 1 == S ? 0 : stage + 1;
             if (!end) {
-                if (ends) item_first += use.ntiles + PA_ITEM;
+                if (ends) item_first += use.ntiles + K::ITEM;
                 pa_next<K>(A, use);
             }
         }
@@ -766,6 +808,7 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_attention_join(const __grid_
     constexpr int LANES = HD / 2, SLOTS = PJ_THREADS / LANES;
     const int groups = SLOTS >> A.join_rows;
     __shared__ float2 s_acc[SLOTS][LANES], s_ml[SLOTS];
+    if (K::SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cta = blockIdx.x, e = threadIdx.x % LANES, slot = threadIdx.x / LANES, group = slot >> A.join_rows;
     const int4 r = A.rec[cta];
@@ -827,9 +870,10 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_attention_join(const __grid_
 }
 
 // Bytes of the pieces in flight, which the grid bounds, whatever the heads and lengths.
-inline size_t pa_workspace(int gm, int hd)
+inline size_t pa_fronts(int gm, int hd, int blocks) { return (size_t)PA_SMS * blocks * PA_WARPS * gm * hd * sizeof(float); }
+inline size_t pa_workspace(int gm, int hd, int blocks = 2)
 {
-    return (size_t)PA_MAX_CTAS * (2 * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
+    return (size_t)PA_SMS * blocks * (2 * gm * hd * sizeof(float) + 2 * gm * sizeof(float2) + sizeof(int4));
 }
 
 template <typename K>
@@ -839,8 +883,9 @@ int attention(PaArgs A, char* workspace, cudaStream_t st, const char* op = "page
     constexpr int HD = K::HD, GM = K::GM;
     A.nhb = (A.g + GM - 1) / GM;
     A.part_o = reinterpret_cast<float*>(workspace);
-    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_MAX_CTAS * 2 * GM * HD);
-    A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_MAX_CTAS * 2 * GM);
+    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_SMS * K::BLOCKS * 2 * GM * HD);
+    A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_SMS * K::BLOCKS * 2 * GM);
+    if (K::QUANT) A.fronts = reinterpret_cast<float*>(workspace + ((pa_workspace(GM, HD, K::BLOCKS) + 15) & ~(size_t)15));
     const int rows = A.g < GM ? A.g : GM;
     // two heads per block of the join, or one where the items are so few that each has over a dozen pieces: one context of
     // 100000, 8 heads on one kv head: 28 us (34 us by two), one of 20000, 32 + 8 heads: 24.3 us (25.4 us); but 4 of up to
@@ -850,7 +895,7 @@ int attention(PaArgs A, char* workspace, cudaStream_t st, const char* op = "page
     static mfs::PerDevice ready;
     cudaError_t e = mfs::op_device(ready, (const void*)paged_attention_kernel<K>, L::BYTES, &sms);
     if (e != cudaSuccess) return mfs::op_launched(op, e);
-    const int G = 2 * sms < PA_MAX_CTAS ? 2 * sms : PA_MAX_CTAS;
+    const int G = K::BLOCKS * (sms < PA_SMS ? sms : PA_SMS);
     cudaLaunchConfig_t cfg = {};
     cfg.stream = st;
     cudaLaunchAttribute attr;

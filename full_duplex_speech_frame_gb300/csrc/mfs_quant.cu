@@ -5,7 +5,7 @@ extern "C" size_t mfs_quant_attention_workspace(const mfs_quant_kv* cache, int d
 {
     (void)n_q_heads;
     if (mfs::quant_kv_problem(cache) || (dtype != MFS_DTYPE_F32 && dtype != MFS_DTYPE_BF16)) return 0;
-    return pa_workspace(dtype == MFS_DTYPE_BF16 ? 16 : 8, cache->kv.head_dim);
+    return quant_workspace(cache->kv.head_dim);
 }
 
 extern "C" int mfs_quant_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const int32_t* kv_len, const void* q,

@@ -48,8 +48,8 @@ __device__ __forceinline__ float max_of_keys(float v)  // over a warp's eight gr
 // loses nothing above 2^-39 of it.  bf16 queries are then exact; fp32 ones are the sum of two fp16 parts, 22 bits, and take two
 // products.
 //
-// Weights: w_j 2^(e_j) with e_j the value's exponent, under a running maximum Y of log2 of that, times 2^14: so the weights'
-// fp16 has its 11 bits for all that matter down to 2^-28 of the largest part of the output, and 2^-39 is lost, whatever the
+// Weights: w_j 2^(e_j) with e_j the value's exponent, under a running maximum Y of log2 of that, times 2^BASE: so the weights'
+// fp16 has its 11 bits for all that matter down to 2^-25 of the largest part of the output, and 2^-36 is lost, whatever the
 // values' sizes.  fp32 queries: two parts again.  The sum of the weights is apart from this, in fp32 under the maximum of
 // the scores alone.
 //
@@ -58,6 +58,7 @@ template <typename T, int HD, int NB>
 struct PaE4m3 {
     static constexpr bool SPLIT = sizeof(T) == 4;
     static constexpr int GM = 8 * NB, ROWS = 32, MB = ROWS / 16, CH = HD / 16, OWN = 2 * NB, NP = SPLIT ? 2 : 1;
+    static constexpr float BASE = 11.f, TAKE = 4.5f;  // weights stay below 2^15.5, fp16 ends at 2^16
     unsigned qf[CH][NB][NP][2];
     float o[CH][NB][4];
     float m[OWN], l[OWN], y[OWN], inv[OWN];  // of heads 2 t and 2 t + 1 of each block; m: in scores times 1 / inv until finish()
@@ -165,47 +166,63 @@ struct PaE4m3 {
                     s[n][b][2 * u + 1] = key < valid ? s[n][b][2 * u + 1] * by : -INFINITY;
                 }
             }
-        float scale[OWN];
-        bool same = true;
+        // The maxima in use stay while no weight passes 2^8 under them, and no weight times its value's size 2^TAKE: then no lane
+        // asks another.  Else (the first tile of an item, and few behind it; always where a score is NaN) they are found anew.
+        float z[MB][NB][4];
+        bool fits = true;
 #pragma unroll
         for (int h = 0; h < OWN; ++h) {
             const int b = h / 2, e = h % 2;
             const float ch = c * inv[h];
-            float v = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < MB; ++n) v = fmaxf(v, fmaxf(s[n][b][e], s[n][b][e + 2]));
-            const float mn = fmaxf(m[h], max_of_keys(v)), sub = mn == -INFINITY ? 0.f : mn;  // scores of -infinity alone so far: weights 0, not NaN
-            const float down = m[h] == mn ? 0.f : (m[h] - mn) * ch;
-            float sum = 0.f, top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < MB; ++n)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float& z = s[n][b][2 * u + e];
-                    z = (z - sub) * ch;
-                    sum += ex2(z);
-                    z += ve[n][u];
-                    top = fmaxf(top, z);
+                    const float a = (s[n][b][2 * u + e] - m[h]) * ch;
+                    z[n][b][2 * u + e] = a;
+                    fits = fits && a <= 8.f && a + ve[n][u] <= y[h] + TAKE;
                 }
-            const float was = y[h] + down, yn = fmaxf(was, max_of_keys(top));
-            scale[h] = was == yn ? 1.f : ex2(was - yn);
-            same = same && scale[h] == 1.f;
-            l[h] = l[h] * ex2(down) + sum;
-            m[h] = mn;
-            y[h] = yn;
-            const float up = 14.f - (yn == -INFINITY ? 0.f : yn);
+        }
+        if (!__all_sync(0xffffffffu, fits)) {
+#pragma unroll
+            for (int h = 0; h < OWN; ++h) {
+                const int b = h / 2, e = h % 2;
+                const float ch = c * inv[h];
+                float v = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < MB; ++n) v = fmaxf(v, fmaxf(s[n][b][e], s[n][b][e + 2]));
+                const float mn = fmaxf(m[h], max_of_keys(v)), sub = mn == -INFINITY ? 0.f : mn;  // scores of -infinity alone so far: weights 0, not NaN
+                const float down = m[h] == mn ? 0.f : (m[h] - mn) * ch;
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < MB; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        z[n][b][2 * u + e] = (s[n][b][2 * u + e] - sub) * ch;
+                        top = fmaxf(top, z[n][b][2 * u + e] + ve[n][u]);
+                    }
+                const float was = y[h] + down, yn = fmaxf(was, max_of_keys(top)), scale = was == yn ? 1.f : ex2(was - yn);
+                l[h] *= ex2(down);
+                m[h] = mn;
+                y[h] = yn;
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    o[k][b][e] *= scale;
+                    o[k][b][e + 2] *= scale;
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < OWN; ++h) {
+            const int b = h / 2, e = h % 2;
+            const float up = BASE - (y[h] == -INFINITY ? 0.f : y[h]);
 #pragma unroll
             for (int n = 0; n < MB; ++n)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) s[n][b][2 * u + e] = ex2(s[n][b][2 * u + e] + up);
-        }
-        if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-            for (int k = 0; k < CH; ++k)
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[k][b][e] *= scale[2 * b + (e & 1)];
+                for (int u = 0; u < 2; ++u) {
+                    l[h] += ex2(z[n][b][2 * u + e]);
+                    s[n][b][2 * u + e] = ex2(z[n][b][2 * u + e] + (ve[n][u] + up));
+                }
         }
         // the weights as the products' columns: by heads, not by keys
         unsigned p[MB][NB][NP][2];
@@ -262,7 +279,7 @@ struct PaE4m3 {
 #pragma unroll
         for (int h = 0; h < OWN; ++h) {
             const int b = h / 2, e = h % 2;
-            const float by = exp2f(y[h] - 14.f);
+            const float by = exp2f(y[h] - BASE);
 #pragma unroll
             for (int k = 0; k < CH; ++k)
                 *reinterpret_cast<float2*>(piece + pa_at<HD>((8 * b + 2 * t + e) * HD + 16 * k + 2 * r)) = make_float2(o[k][b][e] * by, o[k][b][2 + e] * by);
@@ -272,14 +289,27 @@ struct PaE4m3 {
     __device__ __forceinline__ bool owner() const { return (threadIdx.x & 31) < 4; }
 };
 
-// A warp's ring holds 16 KB as the others' does: two tiles, or four of heads of 64.
+// What bounds the loop is not one unit but the latency of its instructions (conversions, products, the softmax), so as many
+// warps as their registers allow, against 32 rows a tile: 4 sequences of up to 131072, 8 kv heads of 128, 64 query heads 113 us
+// (100 us at the measured copy rate), with two blocks per SM 121, with four and tiles of 16 rows 129; 32 of up to 8192, 32
+// query heads, pages of 16, 58.5 us, 65.8 and 66.3; in fp32 the first 121 us, 133 with two blocks; heads of 64 40 us, 54 with
+// two blocks.
 template <typename T_, int HD_, int NB, bool SHARED_ = false>
 struct PaKindE4m3 {
     using T = T_;
     using State = PaE4m3<T_, HD_, NB>;
-    static constexpr int HD = HD_, GM = State::GM, CE = 1, ROWS = 32, STAGES = 256 / HD, Q = 0;
+    static constexpr int HD = HD_, GM = State::GM, CE = 1, ROWS = State::ROWS, STAGES = 2, Q = 0;
+    static constexpr int BLOCKS = NB == 2 ? 2 : HD == 64 && !State::SPLIT ? 4 : 3;  // per SM
+    static constexpr int ITEM = 1;  // (1, 2 and 4: 64 sequences of up to 1000, 24 + 8 heads of 64 in fp32 19.8, 20.3 and 20.5 us)
     static constexpr bool QUANT = true, SHARED = SHARED_;
 };
+
+// Of any kind above, with the items' ends
+inline size_t quant_workspace(int hd)
+{
+    const size_t a = pa_workspace(8, hd, 4) + pa_fronts(8, hd, 4), b = pa_workspace(16, hd, 2) + pa_fronts(16, hd, 2);
+    return a > b ? a : b;
+}
 
 inline PaArgs quant_args(const mfs_quant_kv* c)
 {

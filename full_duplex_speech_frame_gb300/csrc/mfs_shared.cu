@@ -230,9 +230,10 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
 
 // -------------------------------------------------------------------- join
 //
-// HD / 4 threads for each sequence and head: its own part, then the prefix's pieces in order.
+// HD / 4 threads for each sequence and head: its own part and the prefix's pieces, in order, eight at a time, all on their
+// way together.  Where they lie follows from the lengths alone, and is found while the kernels before still run.
 
-constexpr int SJ_THREADS = 256;
+constexpr int SJ_THREADS = 256, SJ_AHEAD = 8;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant__ ShArgs A)
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
     __shared__ ShWalk sh_w;
     __shared__ int sh_p;
     const int s = blockIdx.x, tid = threadIdx.x, e = tid % LANES;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int len = __ldg(A.kv_len + s);
     if (tid < 32) {
         const int lo = A.window > 0 && len > A.window ? len - A.window : 0;
@@ -271,31 +271,49 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
     const ShWalk w = sh_w;
     const int p = sh_p, lo = A.window > 0 && len > A.window ? len - A.window : 0;
     const bool own = len > lo + p;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int h = blockIdx.y * HEADS + tid / LANES; h < A.hq; h += gridDim.y * HEADS) {
         const long long at = (long long)s * A.hq + h;
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto take = [&](const float* o, float2 ml) {
-            const float4 v = *reinterpret_cast<const float4*>(o + 4 * e);
-            const float mn = fmaxf(m, ml.x), a = m == mn ? 1.f : exp2f((m - mn) * A.c), b = ml.x == mn ? 1.f : exp2f((ml.x - mn) * A.c);
-            m = mn;
-            l = l * a + ml.y * b;
-            acc = make_float4(acc.x * a + v.x * b, acc.y * a + v.y * b, acc.z * a + v.z * b, acc.w * a + v.w * b);
-        };
-        if (own) take(A.own_o + at * HD, A.own_ml[at]);
+        // parts: -1: its own, 0 ...: the prefix's (one: the rows themselves)
+        int c0 = 0, n = 0, row = 0;
         if (p > 0) {
             const long long total = sh_total_places, shares = sh_shares(A, total);
-            const int r = (s - w.s0) * A.g + h % A.g, rb = r / A.rows, per = w.ntiles + SH_ITEM;
-            const long long begin = sh_first + ((long long)rb * A.C.n_kv_heads + h / A.g) * per;
+            const int r = (s - w.s0) * A.g + h % A.g, per = w.ntiles + SH_ITEM;
+            const long long begin = sh_first + ((long long)(r / A.rows) * A.C.n_kv_heads + h / A.g) * per;
             // the last share that begins at or before a place
             auto share_of = [&](long long x) { return (int)(((x + 1) * shares - 1) / total); };
-            const int c0 = share_of(begin), c1 = share_of(begin + per - 1);
-            if (c0 == c1) take(A.row_o + at * HD, A.row_ml[at]);
-            else
-                for (int c = c0; c <= c1; ++c) {
-                    const long long k = ((long long)c * 2 + (c == c0)) * A.rows + r % A.rows;
-                    take(A.part_o + k * HD, A.part_ml[k]);
-                }
+            c0 = share_of(begin);
+            n = share_of(begin + per - 1) - c0 + 1;
+            row = r % A.rows;
+        }
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = own ? -1 : 0; i0 < n; i0 += SJ_AHEAD) {
+            float2 ml[SJ_AHEAD];
+            float4 v[SJ_AHEAD];
+#pragma unroll
+            for (int j = 0; j < SJ_AHEAD; ++j) {
+                const int i = i0 + j;
+                ml[j] = make_float2(-INFINITY, 0.f);
+                v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i >= n) continue;
+                const long long k = i < 0 || n == 1 ? at : ((long long)(c0 + i) * 2 + (i == 0)) * A.rows + row;
+                ml[j] = (i < 0 ? A.own_ml : n == 1 ? A.row_ml : A.part_ml)[k];
+                v[j] = *reinterpret_cast<const float4*>((i < 0 ? A.own_o : n == 1 ? A.row_o : A.part_o) + k * HD + 4 * e);
+            }
+            float mn = m;
+#pragma unroll
+            for (int j = 0; j < SJ_AHEAD; ++j) mn = fmaxf(mn, ml[j].x);
+            const float a = m == mn ? 1.f : exp2f((m - mn) * A.c);
+            m = mn;
+            l *= a;
+            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+            for (int j = 0; j < SJ_AHEAD; ++j) {
+                const float b = ml[j].x == mn ? 1.f : exp2f((ml[j].x - mn) * A.c);
+                l = fmaf(ml[j].y, b, l);
+                acc = make_float4(fmaf(v[j].x, b, acc.x), fmaf(v[j].y, b, acc.y), fmaf(v[j].z, b, acc.z), fmaf(v[j].w, b, acc.w));
+            }
         }
         T* o = reinterpret_cast<T*>(A.out) + (long long)s * A.out_stride + (long long)h * HD + 4 * e;
         if (len <= 0) put4(o, make_float4(0.f, 0.f, 0.f, 0.f), 1.f);
@@ -328,7 +346,7 @@ ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
         at += (n + 255) & ~(size_t)255;
         return x;
     };
-    s.own = take(pa_workspace(16, hd));
+    s.own = take(quant_workspace(hd));
     s.part_o = take((size_t)SH_MAX_CTAS / 2 * 2 * most * hd * 4);
     s.part_ml = take((size_t)SH_MAX_CTAS / 2 * 2 * most * 8);
     s.row_o = take(rows * hd * 4);
@@ -384,8 +402,12 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     cfg.gridDim = dim3((unsigned)A.n_seqs, (unsigned)((A.hq - 1) / (SJ_THREADS / (HD / 4)) + 1));
     cfg.blockDim = dim3(SJ_THREADS);
     cfg.stream = st;
-    shared_join<T, HD><<<cfg.gridDim, cfg.blockDim, 0, st>>>(A);
-    return mfs::op_launched(op, cudaGetLastError());
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return mfs::op_launched(op, cudaLaunchKernelEx(&cfg, shared_join<T, HD>, A));
 }
 
 // 0: go on, 1: nothing to do, else an error's code

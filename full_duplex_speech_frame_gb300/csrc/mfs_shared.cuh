@@ -17,6 +17,7 @@ struct ShArgs {
     long long x_page, x_head, x_row;
     int rows, tile;      // rows of a block, positions of a tile
     int ctas;            // of the prefix kernel
+    int box;             // rows that a TMA copy takes, 0: none
     float* part_o;       // [CTA][2][rows][HD]
     float2* part_ml;     // [CTA][2][rows] running maximum (raw score) and sum
     float *row_o, *own_o;    // [n_seqs][hq][HD] of the prefix, where one CTA has it all; of what follows

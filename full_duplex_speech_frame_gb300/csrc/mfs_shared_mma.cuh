@@ -7,13 +7,17 @@
 // softmax the tensor cores work for the other.  The weights are taken against the maximum in use so far; only where a tile's
 // own is more than 2^8 larger is O rescaled first.
 //
-// Three warps fill the ring of K and V tiles, a tile each in turn, in the layout that the MMA reads, row by row, since pages
-// may have any size: a bf16 cache by asynchronous copies, an 8-bit one by way of registers, where each value becomes the bf16
-// that it is exactly.  Rows past the prefix are zeros, so nothing that lies there is seen.
+// A bf16 cache's K and V tiles come by TMA, a box for each run of rows that lie in one page, where pages are whole groups of
+// eight rows, the layout's unit; else, and where a tile reaches past the prefix, four warps copy them row by row.  An 8-bit
+// cache's tiles go through those warps' registers, where each value becomes the bf16 that it is exactly.  Rows past the
+// prefix are zeros, so nothing that lies there is seen.
 //
 // The weights are rounded to bf16 (2^-8 of each at most), since the MMA takes both operands of a product in one type and the
 // values are bf16; the sums take them unrounded.
 #pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "mfs_shared.cuh"
 
 namespace {
@@ -59,7 +63,8 @@ __device__ __forceinline__ void codes_bf16(uint4 w, float by, uint4& a, uint4& b
 }
 
 template <int HD, bool QUANT>
-__global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_constant__ ShArgs A)
+__global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                                                                  const __grid_constant__ ShArgs A)
 {
     using S = SmShape<HD>;
     constexpr int STAGES = S::STAGES;
@@ -105,7 +110,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
     // registers: 512 threads x 128 at launch; the softmax warps take more, the others less
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        unsigned done = 0;  // tiles of the ring that earlier parts had
+        unsigned done = 0, asked = 0;  // tiles of the ring that earlier parts had; and all that were asked for by TMA or before such
         bool ok = true;
         // MMA
         constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((SM_M >> 3) << 17) | ((SM_M >> 4) << 24);
@@ -204,27 +209,34 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
                     if (next) signal(&B.kv_empty[ks]);
                 }
             } else if (warp - 9 < SM_LOADERS) {
-                // 32 rows of each tile, one a lane: pages are looked up two tiles ahead, offsets and exponents found one ahead
+                // 32 rows of each tile, one a lane: pages are looked up two tiles ahead, offsets and exponents found one ahead.
+                // By TMA: the first warp's lanes have a box each.
                 const int row0 = 32 * (warp - 9);
-                int page, in_page;  // page -1: none or a bad one, -2: past the prefix
+                int page, in_page;  // page -1: none or a bad one, -2: past the prefix, or not this lane's
+                auto boxed = [&](int t) { return !QUANT && A.box > 0 && (long long)P.w.p - (long long)(P.from + t) * SM_M >= SM_M; };
                 auto look_up = [&](int t) {
-                    const long long p = (long long)(P.from + t) * SM_M + row0 + lane;
-                    const int j = (int)min(p, (long long)P.w.p) / A.C.page_size;
+                    const bool box = boxed(t);
+                    const long long p = box && row0 + lane * A.box >= SM_M ? P.w.p : (long long)(P.from + t) * SM_M + row0 + lane * (box ? A.box : 1);
+                    const int j = page_of(A.C, (int)min(p, (long long)P.w.p));
                     in_page = (int)p - j * A.C.page_size;
                     page = t >= nt || p >= P.w.p ? -2 : j < A.C.table_width ? __ldg(A.C.table + P.reader * A.C.table_stride + j) : -1;
                 };
                 struct Row {
                     long long off;  // bytes; a row without a page has the cache's first, whatever it is
-                    unsigned xk, xv;
+                    unsigned xk, xv;  // 8 bits: the row's exponents; a box: its page and its first row there
                 };
                 auto resolve = [&]() {
-                    Row R = {0, 0u, 0u};
+                    Row R = {0, (unsigned)A.C.n_pages, 0u};  // (past the last page a box is zeros)
+                    if (QUANT) R.xk = 0;
                     if (page >= 0 && page < A.C.n_pages) {
                         R.off = ((long long)page * A.C.page_stride + (long long)in_page * A.C.row_stride + (long long)P.w.h * A.C.head_stride) * (QUANT ? 1 : 2);
                         if (QUANT) {
                             const long long x = (long long)page * A.x_page + (long long)in_page * A.x_row + (long long)P.w.h * A.x_head;
                             R.xk = __ldg(A.kx + x);
                             R.xv = __ldg(A.vx + x);
+                        } else {
+                            R.xk = page;
+                            R.xv = in_page;
                         }
                     } else if (page != -2) {
                         *(volatile int*)&B.bad = 1;
@@ -269,7 +281,19 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
                         ok = ok && bar_wait(&B.kv_empty[slot], par, &B.abort);
                         if (!ok) break;
                         char* dst = ring + slot * S::TILE + row0 * 128;
-                        if constexpr (!QUANT) {
+                        if (boxed(t)) {
+                            if (warp == 9 && lane == 0) bar_expect(&B.kv_full[slot], S::TILE);  // its arrival
+                            __syncwarp();
+                            if (warp == 9 && lane * A.box < SM_M) {
+#pragma unroll
+                                for (int x = 0; x < HD / 64; ++x)
+                                    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                                                 ::"r"(su32(dst + x * S::BOX + lane * A.box * 128)), "l"(kv ? &mv : &mk), "r"(64 * x), "r"(now.xv), "r"(P.w.h), "r"(now.xk),
+                                                 "r"(su32(&B.kv_full[slot])) : "memory");
+                            }
+                            if (warp != 9 || lane != 0) bar_arrive(&B.kv_full[slot]);
+                            asked = done + 2 * t + kv + 1;
+                        } else if constexpr (!QUANT) {
                             // (few instructions for each copy: a warp issues them one behind the other)
                             const unsigned long long src = (unsigned long long)((kv ? A.C.v : A.C.k) + now.off);
                             const unsigned to = su32(dst + (ch / 8) * S::BOX) + sub * 128;
@@ -327,6 +351,8 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
             signal(&B.drained);
             if (leader) bar_drain(&B.drained, 0);
         }
+        if (warp == 9 && lane == 0 && !ok)  // no copy is in flight when the CTA ends, whichever wait gave up
+            for (unsigned k = asked > STAGES ? asked - STAGES : 0; k < asked; ++k) bar_drain(&B.kv_full[k % STAGES], (k / STAGES) & 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int x = warp >> 2, row = tid & (SM_M - 1);
@@ -487,15 +513,47 @@ __global__ void __launch_bounds__(SM_THREADS, 1) shared_prefix_mma(const __grid_
     }
 }
 
+// Tensor maps of a bf16 cache, for boxes of A.box rows; 0: it is copied row by row.
+template <int HD>
+void prefix_maps(ShArgs& A, CUtensorMap (&maps)[2])
+{
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    A.box = 0;
+    const Cache& C = A.C;
+    if (C.page_size % 8) return;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = known.load();
+    if (!encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &r) != cudaSuccess || !fn) return;
+        known.store(encode = (PFN_cuTensorMapEncodeTiled_v12000)fn);
+    }
+    const int run = C.page_size & -C.page_size, box = run < SM_M ? run : SM_M;
+    // (the strides of dimensions of one place are not used, but have to be sound)
+    auto stride = [](long long n, long long s) { return (cuuint64_t)(n > 1 ? s : HD) * 2; };
+    const cuuint64_t dim[4] = {(cuuint64_t)HD, (cuuint64_t)C.page_size, (cuuint64_t)C.n_kv_heads, (cuuint64_t)C.n_pages};
+    const cuuint64_t str[3] = {stride(C.page_size, C.row_stride), stride(C.n_kv_heads, C.head_stride), stride(C.n_pages, C.page_stride)};
+    const cuuint32_t size[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i)
+        if (str[i] == 0 || str[i] >= (1ull << 40)) return;
+    for (int i = 0; i < 2; ++i)
+        if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i ? C.v : C.k, dim, str, size, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return;
+    A.box = box;
+}
+
 template <int HD, bool QUANT>
-cudaError_t prefix_mma(const ShArgs& A, cudaStream_t st)
+cudaError_t prefix_mma(ShArgs& A, cudaStream_t st)
 {
     using S = SmShape<HD>;
+    CUtensorMap maps[2] = {};
+    if (!QUANT) prefix_maps<HD>(A, maps);
     int sms = 0;
     static mfs::PerDevice ready;
     const cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_mma<HD, QUANT>, S::BYTES, &sms);
     if (e != cudaSuccess) return e;
-    shared_prefix_mma<HD, QUANT><<<A.ctas, SM_THREADS, S::BYTES, st>>>(A);
+    shared_prefix_mma<HD, QUANT><<<A.ctas, SM_THREADS, S::BYTES, st>>>(maps[0], maps[1], A);
     return cudaGetLastError();
 }
 

@@ -86,14 +86,14 @@ def check_row(codes, b, x, slack):
 
 def lost_weights(q, k, v_codes, v_exps, scale):
     """What the weights' fp16 leaves out below its smallest step: the kernel weighs code values with w_j 2^(e_j), brought to
-    2^14 at most; fp16's steps end at 2^-24, so a rounding is off by 2^-25 at least there, 2^-39 of the largest w_j 2^(e_j),
-    for each position and times its code."""
+    2^11 or more where largest; fp16's steps end at 2^-24, so a rounding is off by 2^-25 at least there, 2^-36 of the largest
+    w_j 2^(e_j), for each position and times its code."""
     if not len(k):
         return 0.0
     s = (k @ q) * scale
     w = np.exp(s - s.max())
     size = np.exp2(np.asarray(v_exps, np.float64) - 127.0)
-    return 2.0 ** -39 * (w * size).max() / w.sum() * np.abs(E4M3[v_codes]).sum(0) * 1.01
+    return 2.0 ** -36 * (w * size).max() / w.sum() * np.abs(E4M3[v_codes]).sum(0) * 1.01
 
 
 def attention_tolerance(ref, weighted, score_size, n, hd, bf16, lost=0.0):
