@@ -161,6 +161,7 @@ struct PaArgs {
     int n_groups;
     float* own_o;
     float2* own_ml;
+    int2* own_at;     // [n_seqs][head blocks] of what follows: {first CTA or -1: it is in own_o, last CTA} of its pieces
 };
 
 // The last group that begins at or before sequence s.
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
     const long long shares = min(total, (long long)G * PA_WARPS);
     const int share = cta * PA_WARPS + warp;
     if (cta * PA_WARPS >= shares) {
-        if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
+        if (!K::SHARED && tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
         if (K::SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
                         for (int x = 4 * lane; x < nh * HD; x += 128)
                             *reinterpret_cast<float4*>(A.own_o + row0 * HD + x) = *reinterpret_cast<const float4*>(piece + pa_at<HD>(x));
                         if (lane < nh) A.own_ml[row0 + lane] = sh_ml[slot][lane];
+                        if (lane == 0) A.own_at[(long long)use.s * Hx + use.hb] = make_int2(-1, 0);
                     } else {
                         T* o = reinterpret_cast<T*>(A.out) + (long long)use.s * A.out_stride + (long long)h0 * HD;
                         for (int x = 4 * lane; x < nh * HD; x += 128) {
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
         }
     }
     __syncthreads();
-    if (tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
+    if (!K::SHARED && tid == 0) A.rec[cta] = make_int4(-1, 0, 0, 0);
     for (int i = 0, j; held >> i; i = j + 1) {
         i += __ffs(held >> i) - 1;
         j = last_of(i);
@@ -785,9 +787,13 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
         }
         if (!whole) {
             if (tid < nh) A.part_ml[slot * GM + tid] = sh_sum[i][tid];
-            if (tid == 0 && p0.first) A.rec[cta] = make_int4(p0.s, p0.hb, p1.last_cta, 0);
+            if (tid == 0 && p0.first) {
+                if (K::SHARED) A.own_at[(long long)p0.s * Hx + p0.hb] = make_int2(cta, p1.last_cta);
+                else A.rec[cta] = make_int4(p0.s, p0.hb, p1.last_cta, 0);
+            }
         } else if (K::SHARED && tid < nh) {
             A.own_ml[(long long)p0.s * A.hq + h0 + tid] = sh_sum[i][tid];
+            if (tid == 0) A.own_at[(long long)p0.s * Hx + p0.hb] = make_int2(-1, 0);
         }
     }
     // behind a shared prefix this kernel runs beside the prefix's, and ends after it: what waits for this one has both
@@ -808,7 +814,6 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_attention_join(const __grid_
     constexpr int LANES = HD / 2, SLOTS = PJ_THREADS / LANES;
     const int groups = SLOTS >> A.join_rows;
     __shared__ float2 s_acc[SLOTS][LANES], s_ml[SLOTS];
-    if (K::SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cta = blockIdx.x, e = threadIdx.x % LANES, slot = threadIdx.x / LANES, group = slot >> A.join_rows;
     const int4 r = A.rec[cta];
@@ -858,12 +863,6 @@ __global__ void __launch_bounds__(PJ_THREADS) paged_attention_join(const __grid_
     }
     if (group || !np) return;
     const int h = (r.y / A.nhb) * A.g + (r.y % A.nhb) * GM + row;
-    if constexpr (K::SHARED) {
-        const long long at = (long long)r.x * A.hq + h;
-        reinterpret_cast<float2*>(A.own_o + at * HD)[e] = acc;
-        if (e == 0) A.own_ml[at] = make_float2(mx, l);
-        return;
-    }
     T* out = reinterpret_cast<T*>(A.out) + (long long)r.x * A.out_stride + (long long)h * HD + 2 * e;
     out[0] = from_f<T>(acc.x / l);
     out[1] = from_f<T>(acc.y / l);
@@ -877,13 +876,16 @@ inline size_t pa_workspace(int gm, int hd, int blocks = 2)
 }
 
 template <typename K>
+float2* pa_part_ml(char* workspace) { return reinterpret_cast<float2*>(reinterpret_cast<float*>(workspace) + (size_t)PA_SMS * K::BLOCKS * 2 * K::GM * K::HD); }
+
+template <typename K>
 int attention(PaArgs A, char* workspace, cudaStream_t st, const char* op = "paged_attention")
 {
     using L = PaLayout<K>;
     constexpr int HD = K::HD, GM = K::GM;
     A.nhb = (A.g + GM - 1) / GM;
     A.part_o = reinterpret_cast<float*>(workspace);
-    A.part_ml = reinterpret_cast<float2*>(A.part_o + (size_t)PA_SMS * K::BLOCKS * 2 * GM * HD);
+    A.part_ml = pa_part_ml<K>(workspace);
     A.rec = reinterpret_cast<int4*>(A.part_ml + (size_t)PA_SMS * K::BLOCKS * 2 * GM);
     if (K::QUANT) A.fronts = reinterpret_cast<float*>(workspace + ((pa_workspace(GM, HD, K::BLOCKS) + 15) & ~(size_t)15));
     const int rows = A.g < GM ? A.g : GM;
@@ -913,10 +915,11 @@ int attention(PaArgs A, char* workspace, cudaStream_t st, const char* op = "page
         paged_attention_kernel<K><<<G, PA_WARPS * 32, L::BYTES, st>>>(A);
         e = cudaGetLastError();
     }
-    if (e != cudaSuccess) return mfs::op_launched(op, e);
+    if (e != cudaSuccess || K::SHARED) return mfs::op_launched(op, e);  // behind a shared prefix one kernel joins all parts
     cfg.gridDim = dim3((unsigned)G, (unsigned)((rows - 1) >> A.join_rows) + 1);
     cfg.blockDim = dim3(PJ_THREADS);
-    return mfs::op_launched(op, cudaLaunchKernelEx(&cfg, paged_attention_join<K>, A));
+    if constexpr (!K::SHARED) e = cudaLaunchKernelEx(&cfg, paged_attention_join<K>, A);
+    return mfs::op_launched(op, e);
 }
 
 // The checks that the attention calls share, and what they fill in; 0: go on, 1: nothing to do, else an error's code.

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
 
 // -------------------------------------------------------------------- join
 //
-// HD / 4 threads for each sequence and head: its own part and the prefix's pieces, in order, eight at a time, all on their
+// HD / 4 threads for each sequence and head: its own pieces and the prefix's, in order, eight at a time, all on their
 // way together.  Where they lie follows from the lengths alone, and is found while the kernels before still run.
 
 constexpr int SJ_THREADS = 256, SJ_AHEAD = 8;
@@ -274,21 +274,28 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int h = blockIdx.y * HEADS + tid / LANES; h < A.hq; h += gridDim.y * HEADS) {
         const long long at = (long long)s * A.hq + h;
-        // parts: -1: its own, 0 ...: the prefix's (one: the rows themselves)
-        int c0 = 0, n = 0, row = 0;
+        // parts: -own_n .. -1: its own, 0 ...: the prefix's (one of either: the row itself)
+        int c0 = 0, n = 0, row = 0, unit = e, own_n = 0, own_c0 = 0;
+        const int in = h % A.g;
+        if (own) {
+            const int2 r = A.own_at[((long long)s * A.C.n_kv_heads + h / A.g) * A.nhb + in / A.gm];
+            own_c0 = r.x;
+            own_n = r.x < 0 ? 1 : r.y - r.x + 1;
+        }
         if (p > 0) {
             const long long total = sh_total_places, shares = sh_shares(A, total);
-            const int r = (s - w.s0) * A.g + h % A.g, per = w.ntiles + SH_ITEM;
+            const int r = (s - w.s0) * A.g + in, per = w.ntiles + SH_ITEM;
             const long long begin = sh_first + ((long long)(r / A.rows) * A.C.n_kv_heads + h / A.g) * per;
             // the last share that begins at or before a place
             auto share_of = [&](long long x) { return (int)(((x + 1) * shares - 1) / total); };
             c0 = share_of(begin);
             n = share_of(begin + per - 1) - c0 + 1;
             row = r % A.rows;
+            unit = e ^ (row & A.turned);
         }
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = own ? -1 : 0; i0 < n; i0 += SJ_AHEAD) {
+        for (int i0 = -own_n; i0 < n; i0 += SJ_AHEAD) {
             float2 ml[SJ_AHEAD];
             float4 v[SJ_AHEAD];
 #pragma unroll
@@ -297,9 +304,20 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
                 ml[j] = make_float2(-INFINITY, 0.f);
                 v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (i >= n) continue;
-                const long long k = i < 0 || n == 1 ? at : ((long long)(c0 + i) * 2 + (i == 0)) * A.rows + row;
-                ml[j] = (i < 0 ? A.own_ml : n == 1 ? A.row_ml : A.part_ml)[k];
-                v[j] = *reinterpret_cast<const float4*>((i < 0 ? A.own_o : n == 1 ? A.row_o : A.part_o) + k * HD + 4 * e);
+                long long k = at;
+                const float* o = i < 0 ? A.own_o : A.row_o;
+                const float2* s_ml = i < 0 ? A.own_ml : A.row_ml;
+                if (i < 0 && own_c0 >= 0) {
+                    k = ((long long)(own_c0 + i + own_n) * 2 + (i == -own_n)) * A.gm + in % A.gm;
+                    o = A.own_part_o;
+                    s_ml = A.own_part_ml;
+                } else if (i >= 0 && n > 1) {
+                    k = ((long long)(c0 + i) * 2 + (i == 0)) * A.rows + row;
+                    o = A.part_o;
+                    s_ml = A.part_ml;
+                }
+                ml[j] = s_ml[k];
+                v[j] = *reinterpret_cast<const float4*>(o + k * HD + 4 * (i < 0 ? e : unit));
             }
             float mn = m;
 #pragma unroll
@@ -324,6 +342,9 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
 // -------------------------------------------------------------------- host
 
 constexpr int SH_MAX_CTAS = 304;
+#ifndef SH_LEAST
+#define SH_LEAST 1
+#endif
 
 // Rows of the prefix kernel's blocks: 128, or 64 or 32 where groups have so few on average.
 int f32_rows(long long rows, int n_groups)
@@ -333,7 +354,7 @@ int f32_rows(long long rows, int n_groups)
 }
 
 struct ShSpace {
-    size_t own, part_o, part_ml, row_o, row_ml, own_o, own_ml, bytes;
+    size_t own, part_o, part_ml, row_o, row_ml, own_o, own_ml, own_at, bytes;
 };
 
 ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
@@ -353,6 +374,7 @@ ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
     s.row_ml = take(rows * 8);
     s.own_o = take(rows * hd * 4);
     s.own_ml = take(rows * 8);
+    s.own_at = take(rows * 8);  // (head blocks are no more than heads)
     s.bytes = at;
     return s;
 }
@@ -382,6 +404,11 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     A.row_ml = (float2*)(ws + sp.row_ml);
     A.own_o = P.own_o = (float*)(ws + sp.own_o);
     A.own_ml = P.own_ml = (float2*)(ws + sp.own_ml);
+    A.own_at = P.own_at = (int2*)(ws + sp.own_at);
+    A.own_part_o = (const float*)(ws + sp.own);
+    A.own_part_ml = pa_part_ml<K>(ws + sp.own);
+    A.gm = K::GM;
+    A.nhb = (A.g + K::GM - 1) / K::GM;
     int sms = 0;
     static mfs::PerDevice known;
     cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
@@ -390,10 +417,13 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     if constexpr (sizeof(T) == 2) {
         A.rows = 2 * SM_M;
         A.tile = SM_M;
+        A.turned = 7;
+        A.least = SH_LEAST;
         e = prefix_mma<HD, QUANT>(A, st);
     } else {
         A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
         A.tile = SF_KEYS;
+        A.least = 1;
         e = A.rows == 128 ? prefix_f32<HD, 8, QUANT>(A, st) : A.rows == 64 ? prefix_f32<HD, 4, QUANT>(A, st) : prefix_f32<HD, 2, QUANT>(A, st);
     }
     if (e != cudaSuccess) return mfs::op_launched(op, e);

@@ -17,11 +17,17 @@ struct ShArgs {
     long long x_page, x_head, x_row;
     int rows, tile;      // rows of a block, positions of a tile
     int ctas;            // of the prefix kernel
+    int least;           // places of a share
     int box;             // rows that a TMA copy takes, 0: none
+    int turned;          // the prefix's results: 16-byte unit c of row r of a block lies at c ^ (r & turned)
     float* part_o;       // [CTA][2][rows][HD]
     float2* part_ml;     // [CTA][2][rows] running maximum (raw score) and sum
     float *row_o, *own_o;    // [n_seqs][hq][HD] of the prefix, where one CTA has it all; of what follows
     float2 *row_ml, *own_ml;
+    const int2* own_at;      // [n_seqs][head blocks] the pieces of what follows, if any
+    const float* own_part_o; // [CTA][2][gm][HD]
+    const float2* own_part_ml;
+    int gm, nhb;             // query heads of a head block there, head blocks of a kv head
 };
 
 // What an item costs beside its tiles, in tiles.
@@ -106,8 +112,8 @@ __device__ __forceinline__ int sh_reader(const ShArgs& A, const ShWalk& w)
     return -1;
 }
 
-// The number of shares.
-__device__ __forceinline__ long long sh_shares(const ShArgs& A, long long total) { return min(total, (long long)A.ctas); }
+// The number of shares: one per CTA, of A.least places at least, since a part costs several tiles' time besides.
+__device__ __forceinline__ long long sh_shares(const ShArgs& A, long long total) { return min(max(total / A.least, min(total, 1ll)), (long long)A.ctas); }
 
 // A CTA's part of an item: tiles from .. upto - 1; whole: all of them.
 struct ShPart {
@@ -125,13 +131,13 @@ struct ShParts {
     {
         const long long total = sh_total(A), shares = sh_shares(A, total);
         if (cta >= shares) return false;
-        at = cta * total / shares;
-        end = (cta + 1) * total / shares;
+        at = muldiv(cta, total, shares);
+        end = muldiv(cta + 1, total, shares);
         const long long first = sh_find(A, at, w), in = at - first;
         const int per = w.ntiles + SH_ITEM;
-        const long long item = in / per;
-        w.h = (int)(item % A.C.n_kv_heads);
-        w.rb = (int)(item / A.C.n_kv_heads);
+        const long long item = in >> 32 ? in / per : (unsigned)in / (unsigned)per;
+        w.rb = (int)(item >> 32 ? item / A.C.n_kv_heads : (unsigned)item / (unsigned)A.C.n_kv_heads);
+        w.h = (int)(item - (long long)w.rb * A.C.n_kv_heads);
         w.tile = (int)(in - item * per) - SH_ITEM;  // -SH_ITEM: at the item's beginning
         return true;
     }
