@@ -13,8 +13,7 @@ namespace {
 
 // ------------------------------------------------------------- CUDA cores
 //
-// 256 threads take 16 RT rows (RT 8, 4 or 2) and walk over tiles of 64 positions in shared memory, in fp32 whatever the cache
-// holds; a thread has RT rows x 4 positions of the scores and RT rows x HD / 16 elements of the output in registers (rows and
+// fp32: 256 threads take 16 RT rows (RT 8, 4 or 2) and walk over tiles of 64 positions in shared memory; a thread has RT rows x 4 positions of the scores and RT rows x HD / 16 elements of the output in registers (rows and
 // positions 16 apart), with paired products; a row's maximum and sum go over half a warp.  The next tile's keys come while
 // the values of this one are summed, and the other way round.
 
@@ -26,15 +25,7 @@ struct SfShape {
     static constexpr int BYTES = 4 * ((ROWS + 2 * SF_KEYS) * LD + ROWS * LP);
 };
 
-__device__ __forceinline__ float4 codes_f32(unsigned w, float by)
-{
-    unsigned lo, hi;
-    e4m3_f16(w, lo, hi);
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo)), y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    return make_float4(x.x * by, x.y * by, y.x * by, y.y * by);
-}
-
-template <int HD, int RT, bool QUANT>
+template <int HD, int RT>
 __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_constant__ ShArgs A)
 {
     using S = SfShape<HD, RT>;
@@ -43,7 +34,7 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
     float *sq = sf_raw, *sk = sq + ROWS * LD, *sv = sk + SF_KEYS * LD, *sp = sv + SF_KEYS * LD;
     __shared__ ShPart sh_part;
     __shared__ int sh_more, sh_bad;
-    __shared__ long long sh_off[2][SF_KEYS], sh_x[QUANT ? 2 : 1][SF_KEYS];
+    __shared__ long long sh_off[2][SF_KEYS];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ShParts parts;
@@ -68,36 +59,23 @@ __global__ void __launch_bounds__(SF_THREADS, 1) shared_prefix_f32(const __grid_
         auto look_up = [&](int t) {
             if (t >= P.upto || tid >= SF_KEYS) return;
             const int p = t * SF_KEYS + tid;
-            long long off = -1, x = 0;
+            long long off = -1;
             int page, row;
             if (p < P.w.p) {
                 if (row_place(A.C, P.reader, p, page, row)) {
                     off = (long long)page * A.C.page_stride + (long long)row * A.C.row_stride + (long long)P.w.h * A.C.head_stride;
-                    x = (long long)page * A.x_page + (long long)row * A.x_row + (long long)P.w.h * A.x_head;
                 } else {
                     sh_bad = 1;
                 }
             }
             sh_off[t & 1][tid] = off;
-            if (QUANT) sh_x[t & 1][tid] = x;
         };
         auto fetch = [&](float* dst, bool key, int t) {
             const char* base = key ? A.C.k : A.C.v;
-            if constexpr (!QUANT) {
-                for (int i = tid; i < SF_KEYS * (HD / 4); i += SF_THREADS) {
-                    const int r = i / (HD / 4), c = i % (HD / 4) * 4;
-                    const long long off = sh_off[t & 1][r];
-                    copy16(su32(dst + r * LD + c), base + (off < 0 ? 0 : (off + c) * 4), off >= 0);
-                }
-            } else {
-                for (int i = tid; i < SF_KEYS * (HD / 16); i += SF_THREADS) {
-                    const int r = i / (HD / 16), c = i % (HD / 16) * 16;
-                    const long long off = sh_off[t & 1][r];
-                    const uint4 w = off < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(base + off + c));
-                    const float by = off < 0 ? 0.f : pow2_of(__ldg((key ? A.kx : A.vx) + sh_x[t & 1][r]));
-                    float4* d = reinterpret_cast<float4*>(dst + r * LD + c);
-                    d[0] = codes_f32(w.x, by); d[1] = codes_f32(w.y, by); d[2] = codes_f32(w.z, by); d[3] = codes_f32(w.w, by);
-                }
+            for (int i = tid; i < SF_KEYS * (HD / 4); i += SF_THREADS) {
+                const int r = i / (HD / 4), c = i % (HD / 4) * 4;
+                const long long off = sh_off[t & 1][r];
+                copy16(su32(dst + r * LD + c), base + (off < 0 ? 0 : (off + c) * 4), off >= 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -353,11 +331,22 @@ int f32_rows(long long rows, int n_groups)
     return each > 64 ? 128 : each > 32 ? 64 : 32;
 }
 
+// Whether sharing could pay: what it saves, at most, is reading the positions that the table has room for once for each
+// sequence but one of a group.  Its three kernels take about 15 us more than the one-token attention's two.  bf16, 8 kv heads
+// of 128, 32 query heads: 4 sequences behind 7000 positions (86 MB saved) 28.1 us, one by one 24.8; 8 (201 MB) 29.7 and 38.4;
+// 64 behind 500 (129 MB) 28.7 and 28.6; fp32, 64 behind 500 (258 MB) 49 and 64; 8 bits, 96 behind 500 to 1000 (190 MB) 35.6 and
+// 31.5, behind 3000 to 6000 (1143 MB) 61 and 119.
+bool sharing_pays(const mfs_paged_kv* c, int n_seqs, int n_groups, double row_bytes)
+{
+    const double saved = ((double)n_seqs - n_groups) * c->table_width * c->page_size * c->n_kv_heads * 2 * row_bytes;
+    return n_groups > 0 && saved > (c->dtype == MFS_DTYPE_E4M3 ? 200e6 : 120e6);
+}
+
 struct ShSpace {
     size_t own, part_o, part_ml, row_o, row_ml, own_o, own_ml, own_at, bytes;
 };
 
-ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
+ShSpace sh_space(int hd, int hq, int n_seqs)
 {
     ShSpace s;
     const size_t rows = (size_t)n_seqs * hq, most = 256;
@@ -379,15 +368,15 @@ ShSpace sh_space(int dtype, int hd, int hq, int n_seqs)
     return s;
 }
 
-template <int HD, int RT, bool QUANT>
+template <int HD, int RT>
 cudaError_t prefix_f32(const ShArgs& A, cudaStream_t st)
 {
     using S = SfShape<HD, RT>;
     int sms = 0;
     static mfs::PerDevice ready;
-    cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_f32<HD, RT, QUANT>, S::BYTES, &sms);
+    cudaError_t e = mfs::op_device(ready, (const void*)shared_prefix_f32<HD, RT>, S::BYTES, &sms);
     if (e != cudaSuccess) return e;
-    shared_prefix_f32<HD, RT, QUANT><<<A.ctas, SF_THREADS, S::BYTES, st>>>(A);
+    shared_prefix_f32<HD, RT><<<A.ctas, SF_THREADS, S::BYTES, st>>>(A);
     return cudaGetLastError();
 }
 
@@ -397,7 +386,7 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     using T = typename K::T;
     constexpr int HD = K::HD;
     const char* op = "shared_attention";
-    const ShSpace sp = sh_space(0, HD, A.hq, A.n_seqs);
+    const ShSpace sp = sh_space(HD, A.hq, A.n_seqs);
     A.part_o = (float*)(ws + sp.part_o);
     A.part_ml = (float2*)(ws + sp.part_ml);
     A.row_o = (float*)(ws + sp.row_o);
@@ -424,7 +413,7 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
         A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
         A.tile = SF_KEYS;
         A.least = 1;
-        e = A.rows == 128 ? prefix_f32<HD, 8, QUANT>(A, st) : A.rows == 64 ? prefix_f32<HD, 4, QUANT>(A, st) : prefix_f32<HD, 2, QUANT>(A, st);
+        e = A.rows == 128 ? prefix_f32<HD, 8>(A, st) : A.rows == 64 ? prefix_f32<HD, 4>(A, st) : prefix_f32<HD, 2>(A, st);
     }
     if (e != cudaSuccess) return mfs::op_launched(op, e);
     if (const int rc = attention<K>(P, ws + sp.own, st, op)) return rc;
@@ -463,14 +452,14 @@ int shared_checked(const char* op, PaArgs& P, ShArgs& A, int n_groups, const int
 extern "C" size_t mfs_shared_attention_workspace(const mfs_paged_kv* cache, int n_q_heads, int n_seqs)
 {
     if (mfs::paged_kv_problem(cache) || n_q_heads < 1 || n_q_heads > MFS_MAX_HEADS || n_seqs < 0) return 0;
-    return sh_space(cache->dtype, cache->head_dim, n_q_heads, n_seqs).bytes;
+    return sh_space(cache->head_dim, n_q_heads, n_seqs).bytes;
 }
 
 extern "C" size_t mfs_quant_shared_attention_workspace(const mfs_quant_kv* cache, int dtype, int n_q_heads, int n_seqs)
 {
     if (mfs::quant_kv_problem(cache) || (dtype != MFS_DTYPE_F32 && dtype != MFS_DTYPE_BF16) || n_q_heads < 1 || n_q_heads > MFS_MAX_HEADS || n_seqs < 0)
         return 0;
-    return sh_space(dtype, cache->kv.head_dim, n_q_heads, n_seqs).bytes;
+    return dtype == MFS_DTYPE_F32 ? quant_workspace(cache->kv.head_dim) : sh_space(cache->kv.head_dim, n_q_heads, n_seqs).bytes;
 }
 
 extern "C" int mfs_shared_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv_len, int n_groups, const int32_t* groups,
@@ -490,6 +479,8 @@ extern "C" int mfs_shared_attention(const mfs_paged_kv* cache, int n_seqs, const
     if (rc) return rc < 0 ? rc : MFS_OK;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
+    if (!sharing_pays(cache, n_seqs, n_groups, hd * (cache->dtype == MFS_DTYPE_BF16 ? 2.0 : 4.0)))
+        return mfs_paged_attention(cache, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, ws, workspace_bytes, cuda_stream);
     if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? shared<PaKindBf16<128, true>, false>(P, A, ws, st) : shared<PaKindBf16<64, true>, false>(P, A, ws, st);
     auto fn = hd == 128 ? (P.g == 1 ? shared<PaKindF32<128, 1, true>, false> : P.g <= 4 ? shared<PaKindF32<128, 4, true>, false> : shared<PaKindF32<128, 8, true>, false>)
                         : (P.g == 1 ? shared<PaKindF32<64, 1, true>, false> : P.g <= 4 ? shared<PaKindF32<64, 4, true>, false> : shared<PaKindF32<64, 8, true>, false>);
@@ -513,8 +504,11 @@ extern "C" int mfs_quant_shared_attention(const mfs_quant_kv* cache, int dtype, 
     if (rc) return rc < 0 ? rc : MFS_OK;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
-    auto fn = dtype == MFS_DTYPE_F32 ? (hd == 128 ? shared<PaKindE4m3<float, 128, 1, true>, true> : shared<PaKindE4m3<float, 64, 1, true>, true>)
-              : P.g <= 8             ? (hd == 128 ? shared<PaKindE4m3<bf16, 128, 1, true>, true> : shared<PaKindE4m3<bf16, 64, 1, true>, true>)
-                                     : (hd == 128 ? shared<PaKindE4m3<bf16, 128, 2, true>, true> : shared<PaKindE4m3<bf16, 64, 2, true>, true>);
+    // fp32 queries: the CUDA cores would take longer for a prefix's products than the one-token attention, whose products of
+    // codes run on the matrix units, takes to read it for each sequence (32 behind 4000, 32 + 8 heads of 128: 98 and 59 us)
+    if (dtype == MFS_DTYPE_F32 || !sharing_pays(&cache->kv, n_seqs, n_groups, hd + 1.0))
+        return mfs_quant_attention(cache, dtype, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, ws, workspace_bytes, cuda_stream);
+    auto fn = P.g <= 8 ? (hd == 128 ? shared<PaKindE4m3<bf16, 128, 1, true>, true> : shared<PaKindE4m3<bf16, 64, 1, true>, true>)
+                       : (hd == 128 ? shared<PaKindE4m3<bf16, 128, 2, true>, true> : shared<PaKindE4m3<bf16, 64, 2, true>, true>);
     return fn(P, A, ws, st);
 }

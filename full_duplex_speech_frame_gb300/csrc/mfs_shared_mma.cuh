@@ -20,6 +20,11 @@
 
 #include "mfs_shared.cuh"
 
+// A test build may have every CTA lose one tile of its ring (never fill it), so that waits run out.
+#ifndef MFS_SHARED_LOST_TILE
+#define MFS_SHARED_LOST_TILE -1
+#endif
+
 namespace {
 
 constexpr int SM_M = 128;                     // rows of a row tile, positions of a tile
@@ -324,6 +329,10 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
                             if (ok && !QUANT && A.box > 0 && !box && lane == 0) bar_arrive(&B.tail[kv]);
                         }
                         if (!ok) break;
+                        if (MFS_SHARED_LOST_TILE >= 0 && done + 2 * t + kv == (unsigned)MFS_SHARED_LOST_TILE) {
+                            if (++slot == STAGES) { slot = 0; par ^= 1; }
+                            continue;
+                        }
                         char* dst = ring + slot * S::TILE + row0 * 128;
                         if (box) {
                             if (lane == 0) {  // its arrival, and the others'

@@ -69,6 +69,13 @@ def _tables(rng, sizes, prefix, lens, page, outside=0):
     return table, len(order), copies
 
 
+def _wide(table, groups, page, hkv, hd, dtype, quant):
+    """The table with room for so many positions that sharing them is tried (it is not where it could not pay)."""
+    row = hd + 1 if quant else hd * (2 if dtype == "bf16" else 4)
+    positions = 260e6 / (max(1, len(table) - groups) * hkv * 2 * row)
+    return np.pad(table, ((0, 0), (0, int(positions / page) + 1)), constant_values=-1)
+
+
 def _cache(mfs, rng, table, pages, copies, hkv, page, hd, dtype, quant):
     torch = _torch()
     if quant:
@@ -123,10 +130,12 @@ def _check(cache, table, q, out, lens, window, dtype, quant, scale=None, heads=N
             assert (far <= tol).all(), (s, h, (far / tol).max(), far.max())
 
 
-def _case(mfs, seed, sizes, prefix, lens, hq, hkv, hd, page, dtype, quant, window=0, outside=0, scale=None, **kw):
+def _case(mfs, seed, sizes, prefix, lens, hq, hkv, hd, page, dtype, quant, window=0, outside=0, scale=None, wide=True, **kw):
     torch = _torch()
     rng = np.random.default_rng(seed)
     table, pages, copies = _tables(rng, sizes, prefix, lens, page, outside)
+    if wide:
+        table = _wide(table, len(sizes), page, hkv, hd, dtype, quant)
     cache = _cache(mfs, rng, table, pages, copies, hkv, page, hd, dtype, quant)
     n = len(lens)
     q = _normal(rng, n, hq + 1, hd, dtype=dtype)[:, :hq]
@@ -205,8 +214,11 @@ def test_the_same_as_one_by_one(mfs, dtype, quant):
     """Where nothing can be shared the bits are mfs_paged_attention's; elsewhere the two agree within both tolerances."""
     torch = _torch()
     lens = [300, 310, 290, 500]
-    cache, table, q, groups, out = _case(mfs, 7, [4], [250], lens, 4, 2, 64, 16, dtype, quant)
+    cache, table, q, groups, out = _case(mfs, 7, [4], [250], lens, 4, 2, 64, 16, dtype, quant, wide=False)
     one = torch.empty_like(out)
+    mfs.mfs_paged_attention(cache, q, _i32(lens), one)
+    assert torch.equal(out, one)  # a table with room for so little is not shared
+    cache, table, q, groups, out = _case(mfs, 7, [4], [250], lens, 4, 2, 64, 16, dtype, quant)
     mfs.mfs_paged_attention(cache, q, _i32(lens), one)
     got = torch.empty_like(out)
     for g, p in (([0, 1, 2, 3, 4], [250] * 4), ([0, 4], [0]), ([0, 0], [250]), ([0, 4], [600])):
@@ -349,6 +361,7 @@ def test_a_session_from_prompt_to_shared_steps(mfs, quant):
     own = -(-frames // page)
     table = np.array([list(range(prompt // page)) + [prompt // page + s * own + j for j in range(own)] for s in range(n)])
     pages = prompt // page + n * own
+    table = _wide(table, 1, page, hkv, hd, "bf16", quant)
     if quant:
         cache = mfs.QuantKV(*(torch.zeros(pages, hkv, page, hd, dtype=torch.uint8, device="cuda") for _ in "kv"),
                             *(torch.zeros(pages, hkv, page, dtype=torch.uint8, device="cuda") for _ in "kv"), _i32(table))
