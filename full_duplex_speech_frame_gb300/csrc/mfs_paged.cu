@@ -75,7 +75,7 @@ __device__ __forceinline__ unsigned to_e4m3(float a, float b, float c, float d)
 // a magnitude.  2: as 1, and the cache has 8 bits: the lanes that share a row find its largest value, and from it the
 // exponent; the key is quantised as rotated in 32 bits, not as rounded for k_out.
 template <typename T, int HD, int TT, int MODE>
-__global__ void __launch_bounds__(AP_THREADS, MODE == 2 ? 8 : 1) append_kernel(const __grid_constant__ ApArgs<T> A)
+__global__ void __launch_bounds__(AP_THREADS, MODE == 2 ? 8 : 10) append_kernel(const __grid_constant__ ApArgs<T> A)
 {
     constexpr int VE = 16 / sizeof(T);        // elements per vector
     constexpr int IPH = HD / (2 * VE);        // items per head
@@ -129,6 +129,16 @@ __global__ void __launch_bounds__(AP_THREADS, MODE == 2 ? 8 : 1) append_kernel(c
                 // turns in 64 bits; what is left of one, up to half, in fp32: off by 2^-26 of a turn, 1e-7 in the cosine
                 const double a = (double)pos * A.turns.f[i];
                 float s, c;
+                if (MODE == 2) {
+                    // what fp32 leaves out of the angle and of the products with the magnitude is added: a key next to a border of
+                    // its codes takes the wrong one less often
+                    const double x = 2.0 * (a - rint(a));
+                    const float hi = (float)x, d = 3.14159265f * (float)(x - hi) * A.magnitude;
+                    sincospif(hi, &s, &c);
+                    const float mc = A.magnitude * c, ms = A.magnitude * s;
+                    cs[warp][i] = make_float2(mc + fmaf(-d, s, fmaf(A.magnitude, c, -mc)), ms + fmaf(d, c, fmaf(A.magnitude, s, -ms)));
+                    continue;
+                }
                 sincospif(2.f * (float)(a - rint(a)), &s, &c);
                 cs[warp][i] = MODE ? make_float2(c * A.magnitude, s * A.magnitude) : make_float2(c, s);
             }

@@ -574,8 +574,15 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
         pa_sequence<K>(A, w);
         return w.ntiles ? w.ntiles + K::ITEM : 0;
     };
+    // behind a shared prefix a sequence's tiles take several dependent reads to find: once, and kept
+    constexpr int KEPT = K::SHARED ? 1024 : 1;
+    __shared__ int sh_kept[KEPT];
     long long mine = 0;
-    for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) mine += tiles_of(s);
+    for (int s = tid; s < A.n_seqs; s += PA_WARPS * 32) {
+        const int v = tiles_of(s);
+        if (K::SHARED && s < KEPT) sh_kept[s] = v;
+        mine += v;
+    }
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) sh_tiles[warp] = mine;
     if (tid < 2 * PA_WARPS) sh_piece[tid].s = -1;
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32, K::BLOCKS) paged_attention_kern
         long long item_first = 0;  // where the item begins: K::ITEM empty places, then its tiles
         for (int b = 0; b < A.n_seqs; b += 32) {
             const int s = b + lane;
-            const long long v = s < A.n_seqs ? (long long)tiles_of(s) * Hx : 0;
+            const long long v = s < A.n_seqs ? (long long)(K::SHARED && s < KEPT ? sh_kept[s] : tiles_of(s)) * Hx : 0;
             long long inc = v;
             for (int o = 1; o < 32; o <<= 1) {
                 const long long x = __shfl_up_sync(0xffffffffu, inc, o);

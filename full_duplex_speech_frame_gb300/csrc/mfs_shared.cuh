@@ -45,7 +45,7 @@ __device__ __forceinline__ void sh_group(const ShArgs& A, ShWalk& w)
     group_span(A.groups, w.i, A.n_seqs, w.s0, w.ns);
     w.p = max(__ldg(A.prefix_len + w.i), 0);
     w.nrb = (int)(((long long)w.ns * A.g + A.rows - 1) / A.rows);
-    w.ntiles = w.ns > 1 ? (w.p + A.tile - 1) / A.tile : 0;
+    w.ntiles = w.ns > 1 ? (int)(((long long)w.p + A.tile - 1) / A.tile) : 0;
     if (w.ntiles == 0) w.nrb = 0;
 }
 

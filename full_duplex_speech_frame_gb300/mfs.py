@@ -545,10 +545,11 @@ def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=No
     rope: "interleaved", "half" or None, of whole heads with base theta, or a Rope (theta is then its own).
     A QuantKV gets the keys and values in 8 bits (see include/mfs.h)."""
     import torch
-    dev, dtype, hkv, hd = cache._is
-    dtype = dtype or k.dtype
+    dev, own_dtype, hkv, hd = cache._is
+    dtype = own_dtype or k.dtype
     n, n_seqs, i32 = k.size(0), kv_len.size(0), torch.int32
-    if not isinstance(rope, Rope) and rope not in MFS_ROPE:
+    own_rope = rope.__class__ is Rope
+    if not own_rope and rope not in MFS_ROPE:
         _refuse(f"rope: a Rope or one of {list(MFS_ROPE)}")
     if (q is None) != (q_out is None):
         _refuse("q and q_out go together")
@@ -564,10 +565,9 @@ def mfs_kv_append(cache: PagedKV, k, v, cu, kv_len, q=None, q_out=None, k_out=No
         xp, xs = _rows(q_out, "q_out", n, hq, hd, dtype, dev)
     args = (n, n_seqs, _array(cu, "cu", n_seqs + 1, i32, dev), _array(kv_len, "kv_len", n_seqs, i32, dev), qp, qs, hq, xp, xs, kp, ks,
             op, os_, vp, vs)
-    if isinstance(cache, QuantKV):
-        r = (rope if isinstance(rope, Rope) else Rope(rope, theta=theta)).c
-        _enqueue(dev, stream, _lib.mfs_quant_append, cache.c, _dtype_code(k), *args, r)
-    elif isinstance(rope, Rope):
+    if own_dtype is None:
+        _enqueue(dev, stream, _lib.mfs_quant_append, cache.c, _dtype_code(k), *args, (rope if own_rope else Rope(rope, theta=theta)).c)
+    elif own_rope:
         _enqueue(dev, stream, _lib.mfs_kv_append_rope, cache.c, *args, rope.c)
     else:
         _enqueue(dev, stream, _lib.mfs_kv_append, cache.c, *args, MFS_ROPE[rope], theta)

@@ -194,6 +194,45 @@ def test_many_rows_and_long_prefixes(mfs, dtype, quant):
 
 
 @pytest.mark.parametrize("dtype,quant", KINDS)
+def test_many_sequences(mfs, dtype, quant):
+    """More sequences than a block keeps numbers of, with own parts of none to two positions."""
+    sizes, prefix = [1400, 100], [150, 90]
+    lens = [prefix[0] + i % 3 for i in range(1400)] + [prefix[1] + i % 2 for i in range(100)]
+    _case(mfs, 15, sizes, prefix, lens, 2, 1, 64, 16, dtype, quant, seqs=[0, 1, 2, 700, 1022, 1023, 1024, 1025, 1399, 1400, 1499])
+
+
+@pytest.mark.parametrize("dtype,quant", KINDS)
+@pytest.mark.parametrize("page", [8, 24, 7])
+def test_strided_pools(mfs, dtype, quant, page):
+    """Pools with the heads innermost and room between rows, in pages that are and are not whole groups of eight rows."""
+    torch = _torch()
+    rng = np.random.default_rng(16)
+    lens, prefix, hkv, hd = [300, 320, 301, 299], 299, 3, 64
+    cache, table, q, groups, out = _case(mfs, 16, [4], [prefix], lens, 6, hkv, hd, page, dtype, quant)
+    room = 16 if quant else 8
+    strided = []
+    for src in (cache.k, cache.v):
+        x = torch.zeros(src.shape[0], page, hkv, hd + room, dtype=src.dtype, device="cuda").permute(0, 2, 1, 3)[..., :hd]
+        x.copy_(src)
+        strided.append(x)
+    if quant:
+        for src in (cache.k_exp, cache.v_exp):
+            x = torch.zeros(src.shape[0], page, hkv + 2, dtype=torch.uint8, device="cuda").permute(0, 2, 1)[:, :hkv]
+            x.copy_(src)
+            strided.append(x)
+        other = mfs.QuantKV(strided[0].view(torch.float8_e4m3fn), strided[1].view(torch.float8_e4m3fn), strided[2], strided[3], cache.table)
+    else:
+        other = mfs.PagedKV(*strided, cache.table)
+    got = torch.empty_like(out)
+    mfs.mfs_shared_attention(other, q, _i32(lens), groups, _i32([prefix]), got)
+    assert torch.equal(got, out)
+    one = torch.empty_like(out)
+    mfs.mfs_paged_attention(other, q, _i32(lens), one)
+    mfs.mfs_paged_attention(cache, q, _i32(lens), got)
+    assert torch.equal(one, got)
+
+
+@pytest.mark.parametrize("dtype,quant", KINDS)
 def test_many_groups(mfs, dtype, quant):
     """More groups than a warp has lanes, pairs and threes, with their own prefixes."""
     rng = np.random.default_rng(5)
