@@ -17,6 +17,8 @@ struct Turns {
 // heads of 128 bf16: 39 us, 0.83 of the measured copy rate; blocks of 256 threads and 4 tokens 40 us, three items on
 // their way per thread (fewer blocks on an SM) 45 us, 8 tokens 45 us.  The same in fp32: 77 us, 0.84.
 constexpr int AP_THREADS = 128;
+// 8-bit caches: 8192 tokens 39 us for 202 MB, 0.76 of the copy rate; the row's maximum is three or four exchanges, and the conversion
+// makes it issue 60 % of the time (64 registers, eight blocks per SM; 48 and ten with spills: 64 us).
 // Tokens per block; 1 up to 8 blocks per SM (4 tokens of 16 heads: 3.9 us, 5.5 us by twos; 1200 of 32 + 8 heads 8.7 and
 // 9.3; 1800 14.2 and 13.1; 8192 40.3 and 38.5).
 constexpr int AP_TOKENS = 2;
@@ -345,11 +347,11 @@ int append_ropes(const Append& P, const Cache& C, int hd, const mfs_rope* rope, 
 
 // The last rows of each sequence, packed: a block takes a few tokens (64 or 256 rows of keys and values), then others,
 // until there are none.  A warp for each token finds its place, which takes several dependent reads, while the rows of the
-// tokens before are on their way; the block's threads move these by 16 bytes of output, RD_AHEAD of them at once.
-constexpr int RD_THREADS = 256, RD_TOKENS = 8, RD_AHEAD = 4, RD_BLOCKS = 6;
-// Rows of a turn: 64 where the call has few, 256 else.  8 tokens of 32 heads (with their append) 8.2 us, 13.0 by 256; 3000 18.5 and
-// 18.4; 131 000 of 8 heads, 554 MB written, 179 and 170 us, 4.9 TB/s in all.  With eight items ahead of a thread, four and three
-// blocks per SM, 174 and 173.
+// tokens before are on their way.
+constexpr int RD_THREADS = 256, RD_TOKENS = 8, RD_BLOCKS = 8;
+// Rows of a turn: 64 where the call has few, 256 else: 3000 tokens of 32 heads of 128 to bf16 18.5 us (20 by 256), 8 tokens with
+// their append 8.9 (13.0); 131 000 of 8 heads 158 us = 5.3 TB/s, two thirds of it written, 0.78 of the measured copy rate (179 by
+// 64).  What bounds it is memory; with items of 16 bytes it was the instructions that find an item's place (issue 70 %, 170 us).
 constexpr int RD_FEW = 64, RD_MANY = 256;
 
 struct RdArgs {
@@ -374,12 +376,14 @@ __device__ __forceinline__ float4 from_e4m3(unsigned w, unsigned b)
     return make_float4(x.x * by, x.y * by, y.x * by, y.y * by);
 }
 
-// T: of the output; the cache has the same, or 8 bits (QUANT)
+// T: of the output; the cache has the same, or 8 bits (QUANT).  An item is 32 bytes of output, and pairs of lanes exchange halves
+// of theirs, so that each store writes whole sectors.
 template <typename T, int HD, bool QUANT>
 __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __grid_constant__ RdArgs A)
 {
-    constexpr int VE = 16 / sizeof(T), IPH = HD / VE;  // elements of an item, items per row
+    constexpr int VE = 32 / sizeof(T), IPH = HD / VE;  // elements of an item, items per row
     constexpr int CE = QUANT ? 1 : sizeof(T);
+    static_assert(IPH >= 2 && IPH % 2 == 0, "a pair of lanes has two items of a row");
     __shared__ long long places[2][2][RD_TOKENS];  // of this turn's tokens and the next's: row -1: none, -2: no token; exponents
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hkv = A.C.n_kv_heads;
     auto look_up = [&](int t0, int turn) {
@@ -403,58 +407,66 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __gri
         bool found = t0 + ahead >= A.n_tokens;  // the next tokens' places
         // rows of a token: keys of all heads, then values; a thread has item e of every RD_THREADS / IPH-th row
         const int rows = nt * 2 * hkv, e = tid % IPH;
-        for (int r0 = tid / IPH; r0 < rows || !found; r0 += RD_THREADS / IPH * RD_AHEAD) {
-            uint4 x[RD_AHEAD];
-            unsigned b[RD_AHEAD];
-            char* out[RD_AHEAD];  // null: nothing to write
-    #pragma unroll
-            for (int j = 0; j < RD_AHEAD; ++j) {
-                const int i = r0 + j * (RD_THREADS / IPH);
-                out[j] = nullptr;
-                if (i >= rows) continue;
+        const bool odd = lane & 1;
+        for (int i = tid / IPH; i < rows || !found; i += RD_THREADS / IPH) {
+            uint4 x[QUANT ? 1 : 2];
+            unsigned b = 127;
+            char* out = nullptr;  // of the pair's two items; null: nothing to write
+            if (i < rows) {
                 const int t = A.tokens == 1 ? 0 : (int)__umulhi((unsigned)i, A.inverse), h2 = i - t * 2 * hkv;
                 const bool key = h2 < hkv;
                 const int h = key ? h2 : h2 - hkv;
                 const long long r = row[t];
-                if (r == -2) continue;
-                out[j] = (key ? A.k + (t0 + t) * A.k_stride : A.v + (t0 + t) * A.v_stride) + (long long)h * HD * sizeof(T) + e * 16;
-                if (r < 0) {  // no page: NaN
+                if (r != -2) out = (key ? A.k + (t0 + t) * A.k_stride : A.v + (t0 + t) * A.v_stride) + (long long)h * HD * sizeof(T) + (e & ~1) * 32;
+                if (r == -1) {  // no page: NaN
                     const unsigned nan = QUANT ? 0x7f7f7f7fu : sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-                    x[j] = make_uint4(nan, nan, nan, nan);
-                    b[j] = 127;
-                    continue;
-                }
-                const char* p = (key ? A.C.k : A.C.v) + (r + (long long)h * A.C.head_stride + e * VE) * CE;
-                if constexpr (!QUANT) {
-                    x[j] = __ldg(reinterpret_cast<const uint4*>(p));
-                } else {
-                    if constexpr (VE == 8) {
-                        const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
-                        x[j].x = y.x;
-                        x[j].y = y.y;
+                    x[0] = x[QUANT ? 0 : 1] = make_uint4(nan, nan, nan, nan);
+                } else if (r >= 0) {
+                    const char* p = (key ? A.C.k : A.C.v) + (r + (long long)h * A.C.head_stride + e * VE) * CE;
+                    if constexpr (!QUANT) {
+                        x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+                        x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
                     } else {
-                        x[j].x = __ldg(reinterpret_cast<const unsigned*>(p));
+                        if constexpr (VE == 16) {
+                            x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+                        } else {
+                            const uint2 y = __ldg(reinterpret_cast<const uint2*>(p));
+                            x[0].x = y.x;
+                            x[0].y = y.y;
+                        }
+                        b = __ldg((key ? A.kx : A.vx) + xrow[t] + (long long)h * A.x_head);
                     }
-                    b[j] = __ldg((key ? A.kx : A.vx) + xrow[t] + (long long)h * A.x_head);
                 }
             }
             if (!found) look_up((int)(t0 + ahead), turn ^ 1);
             found = true;
-    #pragma unroll
-            for (int j = 0; j < RD_AHEAD; ++j) {
-                if (!out[j]) continue;
-                uint4 y = x[j];
-                if constexpr (QUANT) {
-                    const float4 f = from_e4m3(x[j].x, b[j]);
-                    if constexpr (VE == 8) {
-                        const float4 g = from_e4m3(x[j].y, b[j]);
-                        y = make_uint4(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w), pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
-                    } else {
-                        memcpy(&y, &f, 16);
-                    }
+            if (!out) continue;  // (the same in both lanes of a pair)
+            uint4 y[2];
+            if constexpr (!QUANT) {
+                y[0] = x[0];
+                y[1] = x[1];
+            } else {
+                const float4 f = from_e4m3(x[0].x, b), g = from_e4m3(x[0].y, b);
+                if constexpr (VE == 16) {
+                    const float4 u = from_e4m3(x[0].z, b), v = from_e4m3(x[0].w, b);
+                    y[0] = make_uint4(pack_bf16(f.x, f.y), pack_bf16(f.z, f.w), pack_bf16(g.x, g.y), pack_bf16(g.z, g.w));
+                    y[1] = make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                } else {
+                    memcpy(&y[0], &f, 16);
+                    memcpy(&y[1], &g, 16);
                 }
-                *reinterpret_cast<uint4*>(out[j]) = y;
             }
+            // the even lane's second half for the odd one's first
+            const unsigned both = 3u << (lane & ~1);
+            const uint4 give = odd ? y[0] : y[1];
+            uint4 got;
+            got.x = __shfl_xor_sync(both, give.x, 1);
+            got.y = __shfl_xor_sync(both, give.y, 1);
+            got.z = __shfl_xor_sync(both, give.z, 1);
+            got.w = __shfl_xor_sync(both, give.w, 1);
+            uint4* o = reinterpret_cast<uint4*>(out) + odd;
+            o[0] = odd ? got : y[0];
+            o[2] = odd ? y[1] : got;
         }
         __syncthreads();
     }
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __gri
 template <typename T, bool QUANT>
 int read_rows(RdArgs A, int hd, cudaStream_t st)
 {
-    const int rows = 2 * A.C.n_kv_heads, most = (long long)A.n_tokens * rows <= 1024 * RD_FEW ? RD_FEW : RD_MANY;
+    const int rows = 2 * A.C.n_kv_heads, most = (long long)A.n_tokens * rows <= 4096 * RD_FEW ? RD_FEW : RD_MANY;
     A.tokens = rows >= most ? 1 : most / rows < RD_TOKENS ? most / rows : RD_TOKENS;
     A.inverse = (unsigned)(((1ull << 32) + rows - 1) / rows);
     int sms = 0;

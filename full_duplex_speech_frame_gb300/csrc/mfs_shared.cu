@@ -270,7 +270,10 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
             const int r = (s - w.s0) * A.g + in, per = w.ntiles + SH_ITEM;
             const long long begin = sh_first + ((long long)(r / A.rows) * A.C.n_kv_heads + h / A.g) * per;
             // the last share that begins at or before a place
-            auto share_of = [&](long long x) { return (int)(((x + 1) * shares - 1) / total); };
+            auto share_of = [&](long long x) {
+                const long long y = (x + 1) * shares - 1;
+                return (int)(total < (1 << 24) ? (unsigned)y / (unsigned)total : y / total);  // (304 shares at most)
+            };
             c0 = share_of(begin);
             n = share_of(begin + per - 1) - c0 + 1;
             row = r % A.rows;
@@ -423,7 +426,9 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     if (e != cudaSuccess) return mfs::op_launched(op, e);
     if (const int rc = attention<K>(P, ws + sp.own, st, op)) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)A.n_seqs, (unsigned)((A.hq - 1) / (SJ_THREADS / (HD / 4)) + 1));
+    // a block takes eight (sixteen) heads of a sequence at a time, and all of them where the sequences are enough to fill the SMs
+    const int turns = (A.hq - 1) / (SJ_THREADS / (HD / 4)) + 1, most = 4 * sms / A.n_seqs + 1;
+    cfg.gridDim = dim3((unsigned)A.n_seqs, (unsigned)(turns < most ? turns : most));
     cfg.blockDim = dim3(SJ_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute attr;
