@@ -290,9 +290,9 @@ struct PaE4m3 {
 };
 
 // What bounds the loop is not one unit but the latency of its instructions (conversions, products, the softmax), so as many
-// warps as their registers allow, against 32 rows a tile: 4 sequences of up to 131072, 8 kv heads of 128, 64 query heads 113 us
+// warps as their registers allow, against 32 rows a tile: 4 sequences of up to 131072, 8 kv heads of 128, 64 query heads 114 us
 // (100 us at the measured copy rate), with two blocks per SM 121, with four and tiles of 16 rows 129; 32 of up to 8192, 32
-// query heads, pages of 16, 58.5 us, 65.8 and 66.3; in fp32 the first 121 us, 133 with two blocks; heads of 64 40 us, 54 with
+// query heads, pages of 16, 59 us, 65.8 and 66.3; in fp32 the first 120 us, 133 with two blocks; heads of 64 39 us, 54 with
 // two blocks.
 template <typename T_, int HD_, int NB, bool SHARED_ = false>
 struct PaKindE4m3 {

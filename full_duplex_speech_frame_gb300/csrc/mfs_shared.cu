@@ -8,8 +8,8 @@
 // paged_attention_kernel takes it, with the same split over its length.  The last kernel joins, for each sequence and head,
 // its own pieces and the prefix's.
 //
-// bf16, 8 kv heads of 128, 32 query heads: 64 sequences behind 7000 positions, up to 1000 of their own, 59 us (one by one 236 us; 22 us
-// is what its bytes take at the measured copy rate): 18 us the prefix, 28 us the own parts, memory at 70 % of that rate, the
+// bf16, 8 kv heads of 128, 32 query heads: 64 sequences behind 7000 positions, up to 1000 of their own, 58 us (one by one 236 us; 22 us
+// is what its bytes take at the measured copy rate): 17 us the prefix, 28 us the own parts, memory at 70 % of that rate, the
 // rest the join, which reads each CTA's pieces, 20 MB.
 #include "mfs_shared_mma.cuh"
 
@@ -18,7 +18,7 @@ namespace {
 // ------------------------------------------------------------- CUDA cores
 //
 // What bounds it is the data path of shared memory, which feeds the products, as in the prompt attention's fp32 kernel: 64
-// sequences behind 2000 positions, 32 + 8 heads of 128, 89 us (one by one 207 us).  fp32: 256 threads take 16 RT rows (RT 8, 4 or 2) and walk over tiles of 64 positions in shared memory; a thread has RT rows x 4 positions of the scores and RT rows x HD / 16 elements of the output in registers (rows and
+// sequences behind 2000 positions, 32 + 8 heads of 128, 88 us (one by one 207 us).  fp32: 256 threads take 16 RT rows (RT 8, 4 or 2) and walk over tiles of 64 positions in shared memory; a thread has RT rows x 4 positions of the scores and RT rows x HD / 16 elements of the output in registers (rows and
 // positions 16 apart), with paired products; a row's maximum and sum go over half a warp.  The next tile's keys come while
 // the values of this one are summed, and the other way round.
 
