@@ -328,9 +328,9 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
 // -------------------------------------------------------------------- host
 
 constexpr int SH_MAX_CTAS = 304;
-#ifndef SH_LEAST
-#define SH_LEAST 1
-#endif
+// Places of a share at least: with 4, 8 and 16, fewer CTAs and more SMs for the own parts meanwhile, 64 sequences behind 7000
+// positions took 64.5, 74 and 93 us, with 1 65.
+constexpr int SH_LEAST = 1;
 
 // Rows of the prefix kernel's blocks: 128, or 64 or 32 where groups have so few on average.
 int f32_rows(long long rows, int n_groups)
@@ -420,7 +420,7 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     } else {
         A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
         A.tile = SF_KEYS;
-        A.least = 1;
+        A.least = SH_LEAST;
         e = A.rows == 128 ? prefix_f32<HD, 8>(A, st) : A.rows == 64 ? prefix_f32<HD, 4>(A, st) : prefix_f32<HD, 2>(A, st);
     }
     if (e != cudaSuccess) return mfs::op_launched(op, e);

@@ -112,7 +112,7 @@ __device__ __forceinline__ int sh_reader(const ShArgs& A, const ShWalk& w)
     return -1;
 }
 
-// The number of shares: one per CTA, of A.least places at least, since a part costs several tiles' time besides.
+// The number of shares: one per CTA, of A.least places at least.
 __device__ __forceinline__ long long sh_shares(const ShArgs& A, long long total) { return min(max(total / A.least, min(total, 1ll)), (long long)A.ctas); }
 
 // A CTA's part of an item: tiles from .. upto - 1; whole: all of them.
