@@ -424,7 +424,9 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
             signal(&B.drained);
             if (leader) bar_drain(&B.drained, 0);
         }
-        if (warp == 9 && lane == 0 && !ok)  // no copy is in flight when the CTA ends, whichever wait gave up
+        // No copy is in flight when the CTA ends, whichever warp's wait gave up: this one may have asked for all of a last part's
+        // tiles without a wait, and not know.  (All waits of the parts are behind the barrier that ended the last one.)
+        if (warp == 9 && lane == 0 && *(volatile int*)&B.abort)
             for (unsigned k = asked > STAGES ? asked - STAGES : 0; k < asked; ++k) bar_drain(&B.kv_full[k % STAGES], (k / STAGES) & 1);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(QUANT ? 192 : 208));
