@@ -577,6 +577,7 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 const bool pieces = B.part.slot != 2;  // then a warp's rows lie one behind the other
                 const int n = __popc(__ballot_sync(0xffffffffu, at >= 0)) * (HD * 4);
+                __syncwarp();  // the first lane's copy reads what all lanes have written
                 if (pieces && lane == 0)
                     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(po + at * HD), "r"(su32(mine)), "r"(n) : "memory");
                 else if (!pieces && at >= 0)
