@@ -366,7 +366,7 @@ struct RdArgs {
     long long x_page, x_head, x_row;
 };
 
-// Four e4m3 codes under 2^(b - 127) (b = 0: zeros)
+// Four e4m3 codes under 2^(b - 127); b = 0: codes of 0
 __device__ __forceinline__ float4 from_e4m3(unsigned w, unsigned b)
 {
     unsigned lo, hi;
@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __gri
     constexpr int CE = QUANT ? 1 : sizeof(T);
     static_assert(IPH >= 2 && IPH % 2 == 0, "a pair of lanes has two items of a row");
     __shared__ long long places[2][2][RD_TOKENS];  // of this turn's tokens and the next's: row -1: none, -2: no token; exponents
+    __shared__ uint4 zeros;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hkv = A.C.n_kv_heads;
+    if (tid == 0) zeros = make_uint4(0u, 0u, 0u, 0u);
     auto look_up = [&](int t0, int turn) {
         if (warp >= A.tokens || t0 + warp >= A.n_tokens) return;
         int s, page = 0, r = 0;
@@ -456,6 +458,7 @@ __global__ void __launch_bounds__(RD_THREADS, RD_BLOCKS) read_kernel(const __gri
                     memcpy(&y[1], &g, 16);
                 }
             }
+            if (QUANT && b == 0) y[0] = y[1] = zeros;  // a row of zeros, codes of NaN among its too (by loads: two instructions, not eight)
             // the even lane's second half for the odd one's first
             const unsigned both = 3u << (lane & ~1);
             const uint4 give = odd ? y[0] : y[1];

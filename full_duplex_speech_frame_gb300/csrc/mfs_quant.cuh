@@ -58,6 +58,7 @@ template <typename T, int HD, int NB>
 struct PaE4m3 {
     static constexpr bool SPLIT = sizeof(T) == 4;
     static constexpr int GM = 8 * NB, ROWS = 32, MB = ROWS / 16, CH = HD / 16, OWN = 2 * NB, NP = SPLIT ? 2 : 1;
+    static_assert(ROWS == 32, "a lane looks at one row's exponents");
     static constexpr float BASE = 11.f, TAKE = 4.5f;  // weights stay below 2^15.5, fp16 ends at 2^16
     unsigned qf[CH][NB][NP][2];
     float o[CH][NB][4];
@@ -128,9 +129,10 @@ struct PaE4m3 {
     }
 
     // x: exponents of the tile's 32 keys, then of its values
-    __device__ __forceinline__ void tile(unsigned stage, int valid, float c, float*, const float*, const uint8_t* x)
+    __device__ __forceinline__ void tile(unsigned stage, int valid, float c, float* staged, const float*, const uint8_t* x)
     {
         const int lane = threadIdx.x & 31, r = lane >> 2, mi = lane >> 3, r8 = lane & 7;
+        const bool no_key = x[lane] == 0, no_value = x[32 + lane] == 0;  // the row that this lane looks after
         float s[MB][NB][4] = {};  // keys r (0, 1) and r + 8 (2, 3) of heads 2 t (0, 2) and 2 t + 1 (1, 3)
 #pragma unroll
         for (int n = 0; n < MB; ++n) {
@@ -166,6 +168,19 @@ struct PaE4m3 {
                     s[n][b][2 * u + 1] = key < valid ? s[n][b][2 * u + 1] * by : -INFINITY;
                 }
             }
+        // rows of exponent 0 are zeros, codes of NaN among theirs too (0 times NaN would not be)
+        if (__any_sync(0xffffffffu, lane < valid && (no_key || no_value))) {
+            uint4* row = reinterpret_cast<uint4*>(staged) + (ROWS + lane) * CH;
+            for (int i = 0; i < CH && no_value; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < MB; ++n)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (16 * n + 8 * (e >> 1) + r < valid && x[16 * n + 8 * (e >> 1) + r] == 0) s[n][b][e] = 0.f;
+        }
         // The maxima in use stay while no weight passes 2^8 under them, and no weight times its value's size 2^TAKE: then no lane
         // asks another.  Else (the first tile of an item, and few behind it; always where a score is NaN) they are found anew.
         float z[MB][NB][4];

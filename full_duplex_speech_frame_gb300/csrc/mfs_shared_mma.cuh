@@ -381,6 +381,14 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
                         } else {
                             asm volatile("cp.async.wait_group 1;" ::: "memory");
                             __syncwarp();
+                            // rows of exponent 0 are zeros, codes of NaN among theirs too (0 times NaN would not be)
+                            if (__any_sync(0xffffffffu, (kv ? now.xv : now.xk) == 0)) {
+                                uint4* mine = reinterpret_cast<uint4*>(raw + kv * R::RAW + lane * HD);
+                                if ((kv ? now.xv : now.xk) == 0)
+#pragma unroll 1
+                                    for (int i = 0; i < HD / 16; ++i) mine[i] = make_uint4(0u, 0u, 0u, 0u);
+                                __syncwarp();
+                            }
                             const uint4* in = reinterpret_cast<const uint4*>(raw + kv * R::RAW) + lane;
                             const bool odd = ch & 4;  // lanes whose chunks lie in the second box store them in the other order: other banks
 #pragma unroll 1
