@@ -75,7 +75,7 @@ struct PaE4m3 {
             // a lane's elements of a head: 16 k + 4 t ..., the instruction's places 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of step k, as
             // a word of codes has them
             float x[CH][4];
-            unsigned top = 0;
+            unsigned top = 0, most = 0;  // largest finite element; of all, NaN above infinity
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 if constexpr (SPLIT) {
@@ -90,13 +90,16 @@ struct PaE4m3 {
                 for (int e = 0; e < 4; ++e) {
                     const unsigned bits = __float_as_uint(x[k][e]) & 0x7fffffffu;
                     if (bits < 0x7f800000u) top = max(top, bits);
+                    most = max(most, bits);
                 }
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const unsigned f = min(253u, 268u - (top >> 23));  // of 2^(f - 127)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) inv[2 * b + e] = __shfl_sync(0xffffffffu, pow2_of(254u - f), 4 * (2 * t + e));
+            for (int e = 0; e < 2; ++e) inv[2 * b + e] = __shfl_sync(0xffffffffu, most < 0x7f800000u ? pow2_of(254u - f) : NAN, 4 * (2 * t + e));
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 float z[4];
@@ -179,7 +182,7 @@ struct PaE4m3 {
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (16 * n + 8 * (e >> 1) + r < valid && x[16 * n + 8 * (e >> 1) + r] == 0) s[n][b][e] = 0.f;
+                        if (16 * n + 8 * (e >> 1) + r < valid && x[16 * n + 8 * (e >> 1) + r] == 0) s[n][b][e] = 0.f * inv[2 * b + (e & 1)];
         }
         // The maxima in use stay while no weight passes 2^8 under them, and no weight times its value's size 2^TAKE: then no lane
         // asks another.  Else (the first tile of an item, and few behind it; always where a score is NaN) they are found anew.

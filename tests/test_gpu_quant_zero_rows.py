@@ -73,3 +73,22 @@ def test_shared_prefix(mfs, dtype, hd):  # noqa: F811
     mfs.mfs_shared_attention(cache, q, _i32(lens), groups, _i32([prefix]), got)
     mfs.mfs_shared_attention(twin, q, _i32(lens), groups, _i32([prefix]), want)
     assert torch.equal(got, want) and torch.isfinite(got).all() and not torch.equal(got, out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_queries_that_are_not_finite(mfs, dtype, bad):  # noqa: F811
+    """Such a query's products with keys of zeros are NaN, as with any others; the heads beside it are right."""
+    torch = _torch()
+    rng = np.random.default_rng(3)
+    for hq in (4, 12):
+        cache = _quant_pool(mfs, rng, 3, 1, 16, 64, [[0, 1, 2]] * 2)
+        cache.k_exp[:] = 0
+        q = _normal(rng, 2, hq, 64, dtype=dtype)
+        want, got = torch.empty_like(q), torch.empty_like(q)
+        mfs.mfs_paged_attention(cache, q, _i32([40, 3]), want)
+        q[1, 2, 9] = bad
+        mfs.mfs_paged_attention(cache, q, _i32([40, 3]), got)
+        keep = torch.ones(2, hq, dtype=torch.bool)
+        keep[1, 2] = False
+        assert torch.isnan(got[1, 2]).all() and torch.isfinite(want).all() and torch.equal(got[keep], want[keep])
