@@ -45,8 +45,9 @@ __device__ __forceinline__ float max_of_keys(float v)  // over a warp's eight gr
 // eight heads fills it (with heads as rows half of it would be zeros).
 //
 // Queries: q = q' / f with a power of two f for each head that brings its largest element to [2^14, 2^15), so that fp16
-// loses nothing above 2^-39 of it.  bf16 queries are then exact; fp32 ones are the sum of two fp16 parts, 22 bits, and take two
-// products.
+// loses nothing above 2^-39 of it; a score takes f back as its key's power of two meets it, so that scores have their own size,
+// whatever the query's and the key's (kept times f it would end at keys of 2^106).  bf16 queries are then exact;
+// fp32 ones are the sum of two fp16 parts, 22 bits, and take two products.
 //
 // Weights: w_j 2^(e_j) with e_j the value's exponent, under a running maximum Y of log2 of that, times 2^BASE: so the weights'
 // fp16 has its 11 bits for all that matter down to 2^-25 of the largest part of the output, and 2^-36 is lost, whatever the
@@ -62,7 +63,7 @@ struct PaE4m3 {
     static constexpr float BASE = 11.f, TAKE = 4.5f;  // weights stay below 2^15.5, fp16 ends at 2^16
     unsigned qf[CH][NB][NP][2];
     float o[CH][NB][4];
-    float m[OWN], l[OWN], y[OWN], inv[OWN];  // of heads 2 t and 2 t + 1 of each block; m: in scores times 1 / inv until finish()
+    float m[OWN], l[OWN], y[OWN], inv[OWN];  // of heads 2 t and 2 t + 1 of each block; inv: 1 / f, NaN where the query is not finite
 
     __device__ __forceinline__ void begin(const PaArgs& A, const PaWalk& w, float*)
     {
@@ -163,12 +164,15 @@ struct PaE4m3 {
             for (int u = 0; u < 2; ++u) {
                 const int key = 16 * n + 8 * u + r;
                 const float by = pow2_of(x[key]);
+                float to[OWN];  // (finite, so that a score of 0 stays one)
+#pragma unroll
+                for (int h = 0; h < OWN; ++h) to[h] = fminf(by * inv[h], 0x1p127f);
                 const unsigned vb = x[32 + key];
                 ve[n][u] = vb ? (float)((int)vb - 127) : -INFINITY;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    s[n][b][2 * u] = key < valid ? s[n][b][2 * u] * by : -INFINITY;
-                    s[n][b][2 * u + 1] = key < valid ? s[n][b][2 * u + 1] * by : -INFINITY;
+                    s[n][b][2 * u] = key < valid ? s[n][b][2 * u] * to[2 * b] : -INFINITY;
+                    s[n][b][2 * u + 1] = key < valid ? s[n][b][2 * u + 1] * to[2 * b + 1] : -INFINITY;
                 }
             }
         // rows of exponent 0 are zeros, codes of NaN among theirs too (0 times NaN would not be)
@@ -191,12 +195,11 @@ struct PaE4m3 {
 #pragma unroll
         for (int h = 0; h < OWN; ++h) {
             const int b = h / 2, e = h % 2;
-            const float ch = c * inv[h];
 #pragma unroll
             for (int n = 0; n < MB; ++n)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const float a = (s[n][b][2 * u + e] - m[h]) * ch;
+                    const float a = (s[n][b][2 * u + e] - m[h]) * c;
                     z[n][b][2 * u + e] = a;
                     fits = fits && a <= 8.f && a + ve[n][u] <= y[h] + TAKE;
                 }
@@ -205,18 +208,17 @@ struct PaE4m3 {
 #pragma unroll
             for (int h = 0; h < OWN; ++h) {
                 const int b = h / 2, e = h % 2;
-                const float ch = c * inv[h];
                 float v = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < MB; ++n) v = fmaxf(v, fmaxf(s[n][b][e], s[n][b][e + 2]));
                 const float mn = fmaxf(m[h], max_of_keys(v)), sub = mn == -INFINITY ? 0.f : mn;  // scores of -infinity alone so far: weights 0, not NaN
-                const float down = m[h] == mn ? 0.f : (m[h] - mn) * ch;
+                const float down = m[h] == mn ? 0.f : (m[h] - mn) * c;
                 float top = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < MB; ++n)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        z[n][b][2 * u + e] = (s[n][b][2 * u + e] - sub) * ch;
+                        z[n][b][2 * u + e] = (s[n][b][2 * u + e] - sub) * c;
                         top = fmaxf(top, z[n][b][2 * u + e] + ve[n][u]);
                     }
                 const float was = y[h] + down, yn = fmaxf(was, max_of_keys(top)), scale = was == yn ? 1.f : ex2(was - yn);
@@ -281,14 +283,12 @@ struct PaE4m3 {
         }
     }
 
-    // whole sums over the warp's keys, in the scores' own scale
+    // whole sums over the warp's keys
     __device__ __forceinline__ void finish()
     {
 #pragma unroll
-        for (int h = 0; h < OWN; ++h) {
+        for (int h = 0; h < OWN; ++h)
             for (int d = 4; d < 32; d *= 2) l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
-            m[h] *= inv[h];
-        }
     }
 
     __device__ __forceinline__ void write(float* piece)
