@@ -297,10 +297,13 @@ struct PaE4m3 {
 #pragma unroll
         for (int h = 0; h < OWN; ++h) {
             const int b = h / 2, e = h % 2;
-            const float by = exp2f(y[h] - BASE);
+            // 2^(Y - BASE) in two factors: as one it would be subnormal, with few bits, where Y is next to -126
+            const float by = exp2f(y[h]), base = 0x1p-11f;
+            static_assert(BASE == 11.f, "the other factor");
 #pragma unroll
             for (int k = 0; k < CH; ++k)
-                *reinterpret_cast<float2*>(piece + pa_at<HD>((8 * b + 2 * t + e) * HD + 16 * k + 2 * r)) = make_float2(o[k][b][e] * by, o[k][b][2 + e] * by);
+                *reinterpret_cast<float2*>(piece + pa_at<HD>((8 * b + 2 * t + e) * HD + 16 * k + 2 * r)) =
+                    make_float2(o[k][b][e] * base * by, o[k][b][2 + e] * base * by);
         }
     }
     __device__ __forceinline__ int own_row(int h) const { return 8 * (h / 2) + 2 * (threadIdx.x & 3) + h % 2; }

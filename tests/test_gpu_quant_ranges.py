@@ -58,3 +58,27 @@ def test_orthogonal_huge_keys(mfs):  # noqa: F811
         out = torch.empty_like(q)
         mfs.mfs_paged_attention(cache, q, _i32([45]), out)
         _check_attention(_np(out[0]), _np(q[0]), _codes(cache, 0, 0, 45), 0.125, dtype == "bf16", 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [2, 3, 40])
+def test_values_next_to_the_smallest(mfs, dtype, n):  # noqa: F811
+    """Values about 2^-118 (exponents 1 to 4) keep their precision.  The tolerance is attention_tolerance()'s without its floor of
+    1e-30, which is far above them; outputs below 2^-126 are rounded to steps of 2^-149 (bf16: 2^-133)."""
+    torch = _torch()
+    rng = np.random.default_rng(34 + n)
+    cache = _quant_pool(mfs, rng, 6, 1, 8, 64, [[4, 2, 0, 1, 3]] * 8)
+    cache.v_exp.copy_(torch.from_numpy(rng.integers(1, 5, tuple(cache.v_exp.shape)).astype(np.uint8)))
+    cache.k_exp[:] = 115
+    q = _normal(rng, 8, 4, 64, dtype=dtype, scale=0.1)
+    out = torch.empty_like(q)
+    mfs.mfs_paged_attention(cache, q, _i32([n] * 8), out)
+    got, qs = _np(out), _np(q)
+    for s in range(8):
+        kc, kx, vc, vx = _codes(cache, s, 0, n)
+        k, v = Q.values(kc, kx)[:, 0], Q.values(vc, vx)[:, 0]
+        for h in range(4):
+            ref, weighted, size = S.attend(qs[s, h], k, v, 0.125)
+            lost = Q.lost_weights(qs[s, h], k, vc[:, 0], vx[:, 0], 0.125)
+            tol = Q.attention_tolerance(ref, weighted, size, n, 64, dtype == "bf16", lost) - 1e-30 + (2.0 ** -133 if dtype == "bf16" else 2.0 ** -148)
+            assert (np.abs(got[s, h] - ref) <= tol).all(), (s, h, (np.abs(got[s, h] - ref) / tol).max())
