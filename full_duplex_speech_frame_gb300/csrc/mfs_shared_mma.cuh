@@ -19,8 +19,9 @@
 // to the first part (launch, places, the first fetch of the code), 5.7 k until the queries are there, 1.5 k until the first scores,
 // 7 k to write 128 KB of outputs: 64 sequences behind 7000 positions, three steps a CTA, 17 us.
 //
-// The weights are rounded to bf16 (2^-8 of each at most), since the MMA takes both operands of a product in one type and the
-// values are bf16; the sums take them unrounded.
+// Over a bf16 cache the weights are rounded to bf16 (2^-8 of each at most), since the MMA takes both operands of a product in one
+// type and the values are bf16; the sums take them unrounded.  Over codes, whose one-token attention keeps 11 bits of each, they are the
+// sum of two such parts (2^-16): the second lies where the rest of the scores was, and takes products of its own.
 #pragma once
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -197,6 +198,11 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
 #pragma unroll
                     for (int k = 1; k < SM_M / 16; ++k)
                         if (leader) mma_ts(d, pa + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
+                    if constexpr (QUANT) {  // the weights' second parts
+#pragma unroll
+                        for (int k = 0; k < SM_M / 16; ++k)
+                            if (leader) mma_ts(d, pa + SM_M / 2 + 8 * k, va + (uint64_t)(k * 128), id_o, 1);
+                    }
                 };
                 // (the same in all lanes, and known to be: the operands' descriptors then stay in uniform registers, where an MMA
                 // takes them; moving them there takes longer than the MMA)
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
                 const uint64_t cc = pair(A.c, A.c), bb = pair(base_, base_);
 #pragma unroll
                 for (int quarter = 0; quarter < 4; ++quarter) {
-                    uint32_t p[16];
+                    uint32_t p[16], rest[QUANT ? 16 : 1];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const int e = 32 * quarter + 2 * k;
@@ -545,8 +551,13 @@ __global__ void __launch_bounds__(SmWarps<QUANT>::THREADS, 1) shared_prefix_mma(
                         w = ex2(w);
                         l2[k & 1] = add2(l2[k & 1], pair(u, w));
                         p[k] = pack_bf16(u, w);
+                        if constexpr (QUANT) {
+                            unpair(fma2(pair(__uint_as_float(p[k] << 16), __uint_as_float(p[k] & 0xffff0000u)), pair(-1.f, -1.f), pair(u, w)), u, w);
+                            rest[k] = pack_bf16(u, w);
+                        }
                     }
                     tst16(ts + 16 * quarter, p);
+                    if constexpr (QUANT) tst16(ts + SM_M / 2 + 16 * quarter, rest);
                 }
                 tst_wait();
                 fence_before();

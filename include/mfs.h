@@ -562,9 +562,9 @@ int mfs_quant_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const 
  * sharing could save is little by the table's size, or the queries are fp32 over an
  * 8-bit cache, the call is the one-token attention's.  bf16 queries: prefix products
  * on the tensor cores, keys and values in bf16 (an 8-bit cache's values are exact in
- * it), softmax weights rounded to bf16; if one of that kernel's internal waits gives up
- * (about 2 s: a stalled device), what it could not compute is NaN.  fp32: on the
- * CUDA cores in fp32.
+ * it), softmax weights rounded to bf16, over an 8-bit cache held in two such parts (16
+ * bits); if one of that kernel's internal waits gives up (about 2 s: a stalled device),
+ * what it could not compute is NaN.  fp32: on the CUDA cores in fp32.
  *   workspace  of mfs_shared_attention_workspace() bytes for n_seqs sequences or more,
  *              else as for mfs_paged_attention */
 size_t mfs_shared_attention_workspace(const mfs_paged_kv* cache, int n_q_heads, int n_seqs);
