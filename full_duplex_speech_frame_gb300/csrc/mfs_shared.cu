@@ -339,14 +339,15 @@ int f32_rows(long long rows, int n_groups)
     return each > 64 ? 128 : each > 32 ? 64 : 32;
 }
 
-// Whether sharing could pay: what it saves, at most, is reading the positions that the table has room for once for each
-// sequence but one of a group.  Its three kernels take about 15 us more than the one-token attention's two.  bf16, 8 kv heads
+// Whether sharing could pay: what it saves, at most, is reading the positions that the table has room for, or as many of them as a
+// window lets a sequence see that begins at its first, once for each sequence but one of a group.  Its three kernels take about 15 us more than the one-token attention's two.  bf16, 8 kv heads
 // of 128, 32 query heads: 4 sequences behind 7000 positions (86 MB saved) 28.1 us, one by one 24.8; 8 (201 MB) 29.7 and 38.4;
 // 64 behind 500 (129 MB) 28.7 and 28.6; fp32, 64 behind 500 (258 MB) 49 and 64; 8 bits, 96 behind 500 to 1000 (190 MB) 35.6 and
 // 31.5, behind 3000 to 6000 (1143 MB) 61 and 119.
-bool sharing_pays(const mfs_paged_kv* c, int n_seqs, int n_groups, double row_bytes)
+bool sharing_pays(const mfs_paged_kv* c, int n_seqs, int n_groups, int window, double row_bytes)
 {
-    const double saved = ((double)n_seqs - n_groups) * c->table_width * c->page_size * c->n_kv_heads * 2 * row_bytes;
+    const long long room = (long long)c->table_width * c->page_size, most = window > 0 && window < room ? window : room;
+    const double saved = ((double)n_seqs - n_groups) * most * c->n_kv_heads * 2 * row_bytes;
     return n_groups > 0 && saved > (c->dtype == MFS_DTYPE_E4M3 ? 200e6 : 120e6);
 }
 
@@ -489,7 +490,7 @@ extern "C" int mfs_shared_attention(const mfs_paged_kv* cache, int n_seqs, const
     if (rc) return rc < 0 ? rc : MFS_OK;
     cudaStream_t st = (cudaStream_t)cuda_stream;
     char* ws = (char*)workspace;
-    if (!sharing_pays(cache, n_seqs, n_groups, hd * (cache->dtype == MFS_DTYPE_BF16 ? 2.0 : 4.0)))
+    if (!sharing_pays(cache, n_seqs, n_groups, window, hd * (cache->dtype == MFS_DTYPE_BF16 ? 2.0 : 4.0)))
         return mfs_paged_attention(cache, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, ws, workspace_bytes, cuda_stream);
     if (cache->dtype == MFS_DTYPE_BF16) return hd == 128 ? shared<PaKindBf16<128, true>, false>(P, A, ws, st) : shared<PaKindBf16<64, true>, false>(P, A, ws, st);
     auto fn = hd == 128 ? (P.g == 1 ? shared<PaKindF32<128, 1, true>, false> : P.g <= 4 ? shared<PaKindF32<128, 4, true>, false> : shared<PaKindF32<128, 8, true>, false>)
@@ -516,7 +517,7 @@ extern "C" int mfs_quant_shared_attention(const mfs_quant_kv* cache, int dtype, 
     char* ws = (char*)workspace;
     // fp32 queries: the CUDA cores would take longer for a prefix's products than the one-token attention, whose products of
     // codes run on the matrix units, takes to read it for each sequence (32 behind 4000, 32 + 8 heads of 128: 98 and 59 us)
-    if (dtype == MFS_DTYPE_F32 || !sharing_pays(&cache->kv, n_seqs, n_groups, hd + 1.0))
+    if (dtype == MFS_DTYPE_F32 || !sharing_pays(&cache->kv, n_seqs, n_groups, window, hd + 1.0))
         return mfs_quant_attention(cache, dtype, n_seqs, kv_len, q, q_stride, n_q_heads, out, out_stride, scale, window, ws, workspace_bytes, cuda_stream);
     auto fn = P.g <= 8 ? (hd == 128 ? shared<PaKindE4m3<bf16, 128, 1, true>, true> : shared<PaKindE4m3<bf16, 64, 1, true>, true>)
                        : (hd == 128 ? shared<PaKindE4m3<bf16, 128, 2, true>, true> : shared<PaKindE4m3<bf16, 64, 2, true>, true>);

@@ -559,8 +559,9 @@ int mfs_quant_attention(const mfs_quant_kv* cache, int dtype, int n_seqs, const 
  * A sequence that does not see its whole prefix (kv_len shorter than it, or a window
  * that begins inside it) is attended to by itself, as is one that is alone in its
  * group.  A bad page in a prefix gives NaN for those that share it.  Where all that
- * sharing could save is little by the table's size, or the queries are fp32 over an
- * 8-bit cache, the call is the one-token attention's.  bf16 queries: prefix products
+ * sharing could save is little by the table's width and the window (lengths are not
+ * known on the host: give a table no wider than they need, as a view of a wider one),
+ * or the queries are fp32 over an 8-bit cache, the call is the one-token attention's.  bf16 queries: prefix products
  * on the tensor cores, keys and values in bf16 (an 8-bit cache's values are exact in
  * it), softmax weights rounded to bf16, over an 8-bit cache held in two such parts (16
  * bits); if one of that kernel's internal waits gives up (about 2 s: a stalled device),
