@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
             // the last share that begins at or before a place
             auto share_of = [&](long long x) {
                 const long long y = (x + 1) * shares - 1;
-                return (int)(total < (1 << 24) ? (unsigned)y / (unsigned)total : y / total);  // (304 shares at most)
+                static_assert((long long)SH_MAX_CTAS << 24 <= 1ll << 32, "y fits in 32 bits");
+                return (int)(total < (1 << 24) ? (unsigned)y / (unsigned)total : y / total);
             };
             c0 = share_of(begin);
             n = share_of(begin + per - 1) - c0 + 1;
@@ -327,7 +328,6 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
 
 // -------------------------------------------------------------------- host
 
-constexpr int SH_MAX_CTAS = 304;
 // Places of a share at least: with 4, 8 and 16, fewer CTAs and more SMs for the own parts meanwhile, 64 sequences behind 7000
 // positions took 64.5, 74 and 93 us, with 1 65.
 constexpr int SH_LEAST = 1;
@@ -366,8 +366,8 @@ ShSpace sh_space(int hd, int hq, int n_seqs)
         return x;
     };
     s.own = take(quant_workspace(hd));
-    s.part_o = take((size_t)SH_MAX_CTAS / 2 * 2 * most * hd * 4);
-    s.part_ml = take((size_t)SH_MAX_CTAS / 2 * 2 * most * 8);
+    s.part_o = take((size_t)SH_MAX_CTAS * 2 * most * hd * 4);
+    s.part_ml = take((size_t)SH_MAX_CTAS * 2 * most * 8);
     s.row_o = take(rows * hd * 4);
     s.row_ml = take(rows * 8);
     s.own_o = take(rows * hd * 4);
@@ -411,7 +411,7 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
     static mfs::PerDevice known;
     cudaError_t e = mfs::op_device(known, nullptr, 0, &sms);
     if (e != cudaSuccess) return mfs::op_launched(op, e);
-    A.ctas = sms < SH_MAX_CTAS / 2 ? sms : SH_MAX_CTAS / 2;
+    A.ctas = sms < SH_MAX_CTAS ? sms : SH_MAX_CTAS;
     if constexpr (sizeof(T) == 2) {
         A.rows = 2 * SM_M;
         A.tile = SM_M;

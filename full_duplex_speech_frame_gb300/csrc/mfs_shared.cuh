@@ -30,6 +30,8 @@ struct ShArgs {
     int gm, nhb;             // query heads of a head block there, head blocks of a kv head
 };
 
+constexpr int SH_MAX_CTAS = 152;  // of the prefix kernel: one for each SM
+
 // What an item costs beside its tiles, in tiles.
 constexpr int SH_ITEM = 1;
 
