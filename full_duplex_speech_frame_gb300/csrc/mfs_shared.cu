@@ -328,10 +328,6 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join(const __grid_constant_
 
 // -------------------------------------------------------------------- host
 
-// Places of a share at least: with 4, 8 and 16, fewer CTAs and more SMs for the own parts meanwhile, 64 sequences behind 7000
-// positions took 64.5, 74 and 93 us, with 1 65.
-constexpr int SH_LEAST = 1;
-
 // Rows of the prefix kernel's blocks: 128, or 64 or 32 where groups have so few on average.
 int f32_rows(long long rows, int n_groups)
 {
@@ -416,12 +412,10 @@ int shared(PaArgs P, ShArgs A, char* ws, cudaStream_t st)
         A.rows = 2 * SM_M;
         A.tile = SM_M;
         A.turned = 7;
-        A.least = SH_LEAST;
         e = prefix_mma<HD, QUANT>(A, st);
     } else {
         A.rows = f32_rows((long long)A.n_seqs * A.g, A.n_groups);
         A.tile = SF_KEYS;
-        A.least = SH_LEAST;
         e = A.rows == 128 ? prefix_f32<HD, 8>(A, st) : A.rows == 64 ? prefix_f32<HD, 4>(A, st) : prefix_f32<HD, 2>(A, st);
     }
     if (e != cudaSuccess) return mfs::op_launched(op, e);

@@ -17,7 +17,6 @@ struct ShArgs {
     long long x_page, x_head, x_row;
     int rows, tile;      // rows of a block, positions of a tile
     int ctas;            // of the prefix kernel
-    int least;           // places of a share
     int box;             // rows that a TMA copy takes, 0: none
     int turned;          // the prefix's results: 16-byte unit c of row r of a block lies at c ^ (r & turned)
     float* part_o;       // [CTA][2][rows][HD]
@@ -114,8 +113,9 @@ __device__ __forceinline__ int sh_reader(const ShArgs& A, const ShWalk& w)
     return -1;
 }
 
-// The number of shares: one per CTA, of A.least places at least.
-__device__ __forceinline__ long long sh_shares(const ShArgs& A, long long total) { return min(max(total / A.least, min(total, 1ll)), (long long)A.ctas); }
+// The number of shares: one per CTA, of one place at least (of 4, 8 and 16 at least, fewer CTAs and more SMs for the own parts
+// meanwhile, 64 sequences behind 7000 positions took as long, 15 % and 45 % longer).
+__device__ __forceinline__ long long sh_shares(const ShArgs& A, long long total) { return min(total, (long long)A.ctas); }
 
 // A CTA's part of an item: tiles from .. upto - 1; whole: all of them.
 struct ShPart {
