@@ -245,8 +245,9 @@ int append(const ApArgs<T>& A, cudaStream_t st)
         const long long room = 8LL * sms / (A.n_tokens > 0 ? A.n_tokens : 1);
         const unsigned each = MODE == 0 || room < 2 ? 1u : (unsigned)(room < most ? room : most);
         // (8-bit caches: 8192 tokens of 32 + 8 heads and their reading back 54 us by ones, 57 us by twos)
-        if (A.n_tokens <= 8 * sms || MODE == 2) append_kernel<T, HD, 1, MODE><<<dim3(A.n_tokens, each), AP_THREADS, 0, st>>>(A);
-        else append_kernel<T, HD, AP_TOKENS, MODE><<<(A.n_tokens + AP_TOKENS - 1) / AP_TOKENS, AP_THREADS, 0, st>>>(A);
+        constexpr int TOKENS = MODE == 2 ? 1 : AP_TOKENS;
+        if (A.n_tokens <= 8 * sms || TOKENS == 1) append_kernel<T, HD, 1, MODE><<<dim3(A.n_tokens, each), AP_THREADS, 0, st>>>(A);
+        else append_kernel<T, HD, TOKENS, MODE><<<(A.n_tokens + TOKENS - 1) / TOKENS, AP_THREADS, 0, st>>>(A);
         e = cudaGetLastError();
     }
     return mfs::op_launched("kv_append", e);
