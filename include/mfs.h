@@ -514,9 +514,10 @@ int mfs_paged_attention(const mfs_paged_kv* cache, int n_seqs, const int32_t* kv
  * Code c of a row with exponent b stands for c * 2^(b - 127), 1 <= b <= 254; b = 0: the
  * row is zeros, whatever its codes (NaN among them).  The append writes the least b
  * that keeps the row's largest value within 448 (at least 1; 0 for a row of zeros)
- * and rounds to nearest, ties to even: off by at most 2^-4 of a value, or 2^-17 of the row's largest (a value above
- * 1.9375 * 2^127 becomes 2^128, which reads as infinite).  A row with an element that
- * is not finite becomes codes of NaN. */
+ * and rounds to nearest, ties to even: off by at most 2^-4 of a value, or 2^-17 of
+ * the row's largest, or 2^-136 (where b is at its least: rows below 448 * 2^-126) (a
+ * value above 1.9375 * 2^127 becomes 2^128, which reads as infinite).  A row with an
+ * element that is not finite becomes codes of NaN. */
 typedef struct {
     mfs_paged_kv kv;
     uint8_t* k_exp;
