@@ -17,8 +17,9 @@ struct Turns {
 // heads of 128 bf16: 39 us, 0.83 of the measured copy rate; blocks of 256 threads and 4 tokens 40 us, three items on
 // their way per thread (fewer blocks on an SM) 45 us, 8 tokens 45 us.  The same in fp32: 77 us, 0.84.
 constexpr int AP_THREADS = 128;
-// 8-bit caches: 8192 tokens 39 us for 202 MB, 0.76 of the copy rate; the row's maximum is three or four exchanges, and the conversion
-// makes it issue 60 % of the time (64 registers, eight blocks per SM; 48 and ten with spills: 64 us).
+// 8-bit caches: 8192 tokens, half of each head rotated, 41 us for 201 MB, 0.72 of the copy rate (all of it 51 us); the row's maximum is
+// three or four exchanges, and the conversion makes it issue 60 % of the time (64 registers, eight blocks per SM; 48 and ten with
+// spills 25 us more).  In fp32 63 us for 386 MB, 0.91 (all of it 65 us).  A partial rotation into a plain cache: 38 us, 0.84; fp32 71 us, 0.90.
 // Tokens per block; 1 up to 8 blocks per SM (4 tokens of 16 heads: 3.9 us, 5.5 us by twos; 1200 of 32 + 8 heads 8.7 and
 // 9.3; 1800 14.2 and 13.1; 8192 40.3 and 38.5).
 constexpr int AP_TOKENS = 2;
@@ -350,7 +351,7 @@ int append_ropes(const Append& P, const Cache& C, int hd, const mfs_rope* rope, 
 // until there are none.  A warp for each token finds its place, which takes several dependent reads, while the rows of the
 // tokens before are on their way.
 constexpr int RD_THREADS = 256, RD_TOKENS = 8, RD_BLOCKS = 8;
-// Rows of a turn: 64 where the call has few, 256 else: 3000 tokens of 32 heads of 128 to bf16 18.5 us (20 by 256), 8 tokens with
+// Rows of a turn: 64 where the call has few, 256 else: 3000 tokens of 32 heads of 128 to bf16 18 us (20 by 256), 8 tokens with
 // their append 8.9 (13.0); 131 000 of 8 heads 158 us = 5.3 TB/s, two thirds of it written, 0.78 of the measured copy rate (179 by
 // 64).  What bounds it is memory; with items of 16 bytes it was the instructions that find an item's place (issue 70 %, 170 us).
 constexpr int RD_FEW = 64, RD_MANY = 256;

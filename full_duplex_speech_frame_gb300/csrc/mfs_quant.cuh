@@ -311,10 +311,10 @@ struct PaE4m3 {
 };
 
 // What bounds the loop is not one unit but the latency of its instructions (conversions, products, the softmax), so as many
-// warps as their registers allow, against 32 rows a tile: 4 sequences of up to 131072, 8 kv heads of 128, 64 query heads 114 us
-// (100 us at the measured copy rate), with two blocks per SM 121, with four and tiles of 16 rows 129; 32 of up to 8192, 32
-// query heads, pages of 16, 59 us, 65.8 and 66.3; in fp32 the first 120 us, 133 with two blocks; heads of 64 39 us, 54 with
-// two blocks.
+// warps as their registers allow, against 32 rows a tile: 4 sequences of up to 131072, 8 kv heads of 128, 64 query heads 115 us
+// (100 us at the measured copy rate), with two blocks per SM 8 us more, with four and tiles of 16 rows 16 more; 32 of up to 8192, 32
+// query heads, pages of 16, 60 us, 7 more either way; in fp32 the first 122 us, 13 more with two blocks; heads of 64 40.5 us, 15
+// more with two blocks.  The look at the rows of exponent 0 and the scores' own size are 1 us of the 60.
 template <typename T_, int HD_, int NB, bool SHARED_ = false>
 struct PaKindE4m3 {
     using T = T_;

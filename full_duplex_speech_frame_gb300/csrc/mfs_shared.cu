@@ -336,10 +336,11 @@ int f32_rows(long long rows, int n_groups)
 }
 
 // Whether sharing could pay: what it saves, at most, is reading the positions that the table has room for, or as many of them as a
-// window lets a sequence see that begins at its first, once for each sequence but one of a group.  Its three kernels take about 15 us more than the one-token attention's two.  bf16, 8 kv heads
-// of 128, 32 query heads: 4 sequences behind 7000 positions (86 MB saved) 28.1 us, one by one 24.8; 8 (201 MB) 29.7 and 38.4;
-// 64 behind 500 (129 MB) 28.7 and 28.6; fp32, 64 behind 500 (258 MB) 49 and 64; 8 bits, 96 behind 500 to 1000 (190 MB) 35.6 and
-// 31.5, behind 3000 to 6000 (1143 MB) 61 and 119.
+// window lets a sequence see that begins at its first, once for each sequence but one of a group.  (Where lengths
+// are far below the room it is a loss: 16 sequences of 32 + 32 heads behind 250 positions, room for 750, 34 us, one by one 31.)  Its
+// three kernels take about 15 us more than the one-token attention's two.  bf16, 8 kv heads of 128, 32 query heads: 4 sequences behind 7000 positions (86 MB saved) 28.1 us, one by one 24.8; 8 (201 MB) 29.7 and 38.4;
+// 64 behind 500 (129 MB) 28.7 and 28.6; fp32, 64 behind 500 (258 MB) 49 and 64; 8 bits, 96 behind 500 to 1000 (193 MB) 32.1 and
+// 32.0, 64 behind 2000 (262 MB) 31 and 47, 96 behind 3000 to 6000 (1210 MB) 64 and 123.
 bool sharing_pays(const mfs_paged_kv* c, int n_seqs, int n_groups, int window, double row_bytes)
 {
     const long long room = (long long)c->table_width * c->page_size, most = window > 0 && window < room ? window : room;

@@ -14,8 +14,9 @@
 //
 // What bounds it: a step over 128 positions takes 3.3 k cycles, 2.7 k of them the tensor core's turns with 32 MMAs (a score
 // product reads both operands from shared memory at its full rate), the rest the MMA warp's waits between them; 256 sequences
-// of 64 query heads on 8 kv heads of 128 behind 32768 positions about 220 us of the call's 257 us, 1.2 PFLOP/s.  Over codes a step takes
-// 5.8 k cycles: the conversions share the issue slots with the softmax.  A call of few steps is its start and end: 7.5 k cycles
+// of 64 query heads on 8 kv heads of 128 behind 32768 positions about 220 us of the call's 260 us, 1.2 PFLOP/s.  Over codes a step takes
+// 6.5 k cycles: the conversions share the issue slots with the softmax, and the weights' second parts take 16 MMAs more (5.8 k without
+// them).  A call of few steps is its start and end: 7.5 k cycles
 // to the first part (launch, places, the first fetch of the code), 5.7 k until the queries are there, 1.5 k until the first scores,
 // 7 k to write 128 KB of outputs: 64 sequences behind 7000 positions, three steps a CTA, 17 us.
 //
