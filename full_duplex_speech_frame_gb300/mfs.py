@@ -653,7 +653,8 @@ def mfs_shared_attention_workspace(cache: PagedKV, n_q_heads: int, n_seqs: int):
 def mfs_shared_attention(cache: PagedKV, q, kv_len, groups, prefix_len, out, scale=None, window=0, workspace=None, stream=None) -> None:
     """mfs_paged_attention for sequences in groups with a common prefix, which is read once for each group: sequences
     groups[i] .. groups[i + 1] - 1 have their first prefix_len[i] positions in common (groups [n_groups + 1], prefix_len
-    [n_groups]: int32 CUDA tensors; see include/mfs.h)."""
+    [n_groups]: int32 CUDA tensors; see include/mfs.h).  Whether sharing is tried goes by the table's width and the window: make
+    the cache of a view of the table that is as wide as its longest sequence."""
     import torch
     dev, dtype, _, hd = cache._is
     n, hq, n_groups = q.size(0), q.size(1), prefix_len.size(0)
