@@ -25,3 +25,17 @@ def test_a_long_window_is_shared(mfs, dtype, quant):  # noqa: F811
     lens = [2699, 2700, 2701, 2799, 2800, 2801, 2802, 2900, 5499, 5500, 5501, 5600] + [2700 + 2 * i for i in range(28)]
     _, _, _, _, out = H._case(mfs, 51, [40], [2700], lens, 16, 8, 128, 64, dtype, quant, window=2800, heads=[0, 9, 15], seqs=list(range(13)) + [39])
     assert np.isfinite(out.float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_view_of_a_wide_table(mfs, quant):  # noqa: F811
+    """A cache of a view as wide as the longest sequence needs: the choice goes by the view, whatever the table's own width."""
+    torch = _torch()
+    lens = [250, 260, 290, 400]
+    cache, table, q, groups, out = H._case(mfs, 52, [4], [250], lens, 4, 2, 64, 16, "bf16", quant)
+    view = cache.table[:, :25]
+    narrow = mfs.QuantKV(cache.k, cache.v, cache.k_exp, cache.v_exp, view) if quant else mfs.PagedKV(cache.k, cache.v, view)
+    got, one = torch.empty_like(out), torch.empty_like(out)
+    mfs.mfs_shared_attention(narrow, q, _i32(lens), groups, _i32([250]), got)
+    mfs.mfs_paged_attention(cache, q, _i32(lens), one)
+    assert torch.equal(got, one)
